@@ -191,6 +191,173 @@ norm_status_t norm_add_bwd(const void *dy, const void *dh, const void *h,
                            size_t workspace_bytes, norm_stream_t stream);
 
 /*
+ * Element types of the group-normalisation and dropout entry points.
+ */
+typedef enum { NORM_BF16 = 0, NORM_FP16 = 1, NORM_FP32 = 2 } norm_dtype_t;
+
+/*
+ * Dropout.  The mask comes from a counter-based generator and is never
+ * stored: it is a function of (seed, offset, element index), so a backward
+ * pass recomputes the forward's mask, and every entry point below drops the
+ * same elements of a tensor for the same seed and offset.
+ *   Block i of eight consecutive elements of the flattened row-major tensor
+ *   takes the four 32-bit outputs of Philox4x32-10 (Salmon, Moraes, Dror,
+ *   Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011) at the
+ *   128-bit counter (i, offset) under the 64-bit key seed.  Element e of the
+ *   block reads 16-bit half e (the low half of word e / 2 first) and is kept
+ *   when half >= T, T = p * 2^16 rounded to the nearest integer (halves up).
+ *   A kept element is multiplied by 2^16 / (2^16 - T), the inverse of the
+ *   exact probability of being kept; a dropped one becomes +0 whatever its
+ *   value (infinities and NaN included).
+ * Arguments every such entry point takes:
+ *   p           probability of dropping an element, 0 <= p < 1 - 2^-17 (else
+ *               NORM_ERR_ARG); 0 drops nothing;
+ *   seed        the generator's key;
+ *   offset      number of the call: calls that must not share a mask use
+ *               different offsets (consecutive ones will do);
+ *   offset_dev  NULL, or the 8-byte aligned device address of a uint64 that
+ *               is read when the kernel runs and added to offset, so that a
+ *               captured graph draws a new mask at every replay: advance the
+ *               word between replays.  A backward pass must see the value
+ *               that its forward pass saw.
+ *
+ * norm_dropout -- y = dropout(x) of n elements (1 <= n <= 2^40, else
+ * NORM_ERR_SHAPE); x and y 16-byte aligned; y may be x (in place), and must
+ * not overlap it otherwise.  The backward pass is the same call on dy.  One
+ * kernel on `stream`.
+ */
+norm_status_t norm_dropout(const void *x, int64_t n, float p, uint64_t seed,
+                           uint64_t offset, const void *offset_dev,
+                           norm_dtype_t dtype, void *y, norm_stream_t stream);
+
+/*
+ * Dropout + residual add + norm: the residual branch x is dropped out and
+ * added to the residual stream r in the pass that normalises it,
+ *   h = bf16(r + dropout(x))   (sum in fp32, rounded to nearest even)
+ *   y = norm(h)                (as norm_fwd, on the bf16 values of h)
+ * and the backward pass gives the gradients of both branches,
+ *   dr = (norm_bwd's dx at h) + dh,   dx = dropout(dr)   (dr before rounding)
+ * with the forward's mask, recomputed.  dgamma / dbeta as norm_bwd.  With p =
+ * 0 dx equals dr and the forward is norm_add_fwd.
+ *
+ * norm_dropout_add_fwd: x, r bf16 [M, N]; h, y bf16 [M, N] outputs; rstd,
+ *   mean (LAYER) fp32 [M] outputs; gamma, beta, eps, mode as norm_fwd.
+ * norm_dropout_add_bwd: dy, dh, h bf16 [M, N]; rstd, mean from the forward;
+ *   dx, dr bf16 [M, N] outputs; dgamma, dbeta as norm_bwd; workspace of
+ *   norm_dropout_add_bwd_workspace_bytes bytes.
+ * Shapes and alignment as norm_add_fwd / norm_add_bwd (N up to
+ * NORM_MAX_N_FUSED); outputs must not alias inputs or each other.
+ */
+norm_status_t norm_dropout_add_fwd(const void *x, const void *r, const void *gamma,
+                                   const void *beta, int64_t M, int64_t N, float eps,
+                                   norm_mode_t mode, float p, uint64_t seed,
+                                   uint64_t offset, const void *offset_dev, void *h,
+                                   void *y, float *rstd, float *mean,
+                                   norm_stream_t stream);
+
+norm_status_t norm_dropout_add_bwd_workspace_bytes(int64_t M, int64_t N,
+                                                   norm_mode_t mode, size_t *bytes);
+
+norm_status_t norm_dropout_add_bwd(const void *dy, const void *dh, const void *h,
+                                   const void *gamma, const float *rstd,
+                                   const float *mean, int64_t M, int64_t N,
+                                   norm_mode_t mode, float p, uint64_t seed,
+                                   uint64_t offset, const void *offset_dev, void *dx,
+                                   void *dr, float *dgamma, float *dbeta,
+                                   void *workspace, size_t workspace_bytes,
+                                   norm_stream_t stream);
+
+/*
+ * Group normalisation of channels-last tensors, with an activation and
+ * dropout behind it.  x is [B, S, C]: B samples of S positions (the
+ * flattened spatial axes) of C contiguous channels; group g owns the D = C /
+ * groups channels [g D, (g + 1) D) of every position of a sample.
+ *   mean, var   over the S * D values of each (sample, group), population
+ *               variance; rstd = 1 / sqrt(var + eps)
+ *   xhat = (x - mean) * rstd,   z = xhat * gamma_c + beta_c
+ *   y = dropout(act(z))         (fp32 throughout, rounded once)
+ *   act(z) = z (NONE), z / (1 + exp(-z)) (SILU), or GELU in its tanh form,
+ *            z * 0.5 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3)))
+ * Backward, from the saved statistics:
+ *   dz = dropout(dy) * act'(z),  g = dz * gamma_c
+ *   dgamma_c = sum over (b, s) of dz * xhat,  dbeta_c = sum of dz
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)), the means over the S *
+ *        D values of the (sample, group)
+ * Results are bitwise reproducible for a given shape, type and device.
+ *
+ * Arguments:
+ *   x, dy, y, dx  [B, S, C] of `dtype`, contiguous
+ *   gamma, beta   [C] of `dtype`; beta NULL means zero (in the backward pass
+ *                 beta takes part in z: pass the forward's)
+ *   rstd, mean    fp32 [B, groups]: outputs of the forward, inputs of the
+ *                 backward pass
+ *   p, seed, offset, offset_dev  dropout of the activation (see above; the
+ *                 element index is that of the whole [B, S, C] tensor)
+ *   dgamma, dbeta fp32 [C] outputs; dbeta may be NULL
+ *   workspace     norm_group_fwd_workspace_bytes / ..._bwd_... bytes for this
+ *                 shape on the CURRENT device; may be NULL when that is 0.
+ *                 Two calls that overlap in time must not share it.
+ * Requirements: C % 8 == 0, 8 <= C <= NORM_MAX_GROUP_C, groups divides C, 1
+ * <= B <= 2^24, 1 <= S <= 2^30, B * S <= 2^40 (else NORM_ERR_SHAPE); every
+ * pointer 16-byte aligned; outputs must not alias inputs.  Unknown act or
+ * dtype: NORM_ERR_ARG.
+ * One kernel where a cluster of up to 8 CTAs holds the samples' slabs in
+ * shared memory (x, and dy, read once), two where the sample is read twice;
+ * the backward adds a fixed-order reduction of dgamma / dbeta unless a single
+ * partial row is left.
+ */
+#define NORM_MAX_GROUP_C 8192
+
+typedef enum { NORM_ACT_NONE = 0, NORM_ACT_SILU = 1, NORM_ACT_GELU = 2 } norm_act_t;
+
+norm_status_t norm_group_fwd_workspace_bytes(int64_t B, int64_t S, int64_t C,
+                                             int64_t groups, norm_dtype_t dtype,
+                                             size_t *bytes);
+
+norm_status_t norm_group_fwd(const void *x, const void *gamma, const void *beta,
+                             int64_t B, int64_t S, int64_t C, int64_t groups,
+                             float eps, norm_act_t act, norm_dtype_t dtype, float p,
+                             uint64_t seed, uint64_t offset, const void *offset_dev,
+                             void *y, float *rstd, float *mean, void *workspace,
+                             size_t workspace_bytes, norm_stream_t stream);
+
+norm_status_t norm_group_bwd_workspace_bytes(int64_t B, int64_t S, int64_t C,
+                                             int64_t groups, norm_dtype_t dtype,
+                                             size_t *bytes);
+
+norm_status_t norm_group_bwd(const void *dy, const void *x, const void *gamma,
+                             const void *beta, const float *rstd, const float *mean,
+                             int64_t B, int64_t S, int64_t C, int64_t groups,
+                             norm_act_t act, norm_dtype_t dtype, float p,
+                             uint64_t seed, uint64_t offset, const void *offset_dev,
+                             void *dx, float *dgamma, float *dbeta, void *workspace,
+                             size_t workspace_bytes, norm_stream_t stream);
+
+/*
+ * norm_group_plan -- how the library runs norm_group_fwd (backward = 0) or
+ * norm_group_bwd (1) of a shape; sm_count and smem_optin_bytes as norm_plan.
+ */
+typedef struct {
+    int32_t streamed;        /* 0: one kernel, data resident in shared memory;
+                                1: a statistics and an output kernel */
+    int32_t groups_per_slab; /* groups a cluster owns of one sample */
+    int32_t slabs;           /* per sample */
+    int32_t chunk_columns;   /* 16-byte columns per slab (streamed: per CTA) */
+    int32_t cluster;         /* CTAs sharing a slab's rows */
+    int32_t row_lanes;       /* rows a CTA works on side by side */
+    int32_t rows_per_thread; /* resident: rows a thread holds (at most) */
+    int32_t row_splits;      /* streamed: row ranges per sample */
+    int32_t threads;         /* CTA size */
+    int32_t smem_bytes;      /* dynamic shared memory per CTA */
+    int32_t grid;            /* CTAs launched */
+    int64_t workspace_bytes;
+} norm_group_plan_t;
+
+norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
+                              norm_dtype_t dtype, int backward, int sm_count,
+                              int smem_optin_bytes, norm_group_plan_t *out);
+
+/*
  * FP8 output.  The page "Otimizacao de Performance de GPU" (introl.com,
  * December 2025 update) reports FP8 training as production ready on
  * Blackwell; the next consumer of a norm's output is usually a GEMM, which

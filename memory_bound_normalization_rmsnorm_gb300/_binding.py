@@ -58,6 +58,17 @@ class Plan(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class GroupPlan(ctypes.Structure):
+    """Mirror of norm_group_plan_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("streamed", "groups_per_slab", "slabs", "chunk_columns", "cluster", "row_lanes",
+                 "rows_per_thread", "row_splits", "threads", "smem_bytes", "grid")
+                ] + [("workspace_bytes", ctypes.c_int64)]
+
+    def as_dict(self):
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+
 class NormError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -127,6 +138,28 @@ def lib():
             L.norm_gemm_fwd.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_float,
                                         ctypes.c_int, _vp, _vp, _vp, _vp]
             L.norm_gemm_fwd.restype = ctypes.c_int
+            f32, u64, sz, ci = ctypes.c_float, ctypes.c_uint64, ctypes.c_size_t, ctypes.c_int
+            drop = [f32, u64, u64, _vp]  # p, seed, offset, offset_dev
+            L.norm_dropout.argtypes = [_vp, _i64, *drop, ci, _vp, _vp]
+            L.norm_dropout_add_fwd.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, f32, ci, *drop,
+                                               _vp, _vp, _vp, _vp, _vp]
+            L.norm_dropout_add_bwd_workspace_bytes.argtypes = [_i64, _i64, ci,
+                                                               ctypes.POINTER(sz)]
+            L.norm_dropout_add_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, ci,
+                                               *drop, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+            for f in (L.norm_group_fwd_workspace_bytes, L.norm_group_bwd_workspace_bytes):
+                f.argtypes = [_i64, _i64, _i64, _i64, ci, ctypes.POINTER(sz)]
+            L.norm_group_fwd.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, f32, ci, ci, *drop,
+                                         _vp, _vp, _vp, _vp, sz, _vp]
+            L.norm_group_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, ci,
+                                         ci, *drop, _vp, _vp, _vp, _vp, sz, _vp]
+            L.norm_group_plan.argtypes = [_i64, _i64, _i64, _i64, ci, ci, ci, ci,
+                                          ctypes.POINTER(GroupPlan)]
+            for f in (L.norm_dropout, L.norm_dropout_add_fwd,
+                      L.norm_dropout_add_bwd_workspace_bytes, L.norm_dropout_add_bwd,
+                      L.norm_group_fwd_workspace_bytes, L.norm_group_bwd_workspace_bytes,
+                      L.norm_group_fwd, L.norm_group_bwd, L.norm_group_plan):
+                f.restype = ci
             L.norm_plan.argtypes = [_i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                     ctypes.c_int, ctypes.POINTER(Plan)]
             L.norm_plan.restype = ctypes.c_int
@@ -570,3 +603,293 @@ def norm_plan(M, N, mode=RMS, backward=False, sm_count=0, smem_optin=0, residual
 def norm_get_device_error(stream=None, device=None):
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     return lib().norm_get_device_error(_stream(stream, dev))
+
+
+# --------------------------------------------- dropout and group normalisation
+BF16 = 0
+FP16 = 1
+FP32 = 2
+_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
+_ACTS = {"none": ACT_NONE, "silu": ACT_SILU, "gelu": ACT_GELU}
+
+
+def _act(act):
+    if isinstance(act, str):
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+        return _ACTS[act]
+    return int(act)
+
+
+def _dtype_code(x):
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    return code
+
+
+def _check(t, name, dtype, shape, device):
+    """_check_tensor, quick where nothing is wrong."""
+    if (t is None or (t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape
+                      and t.is_contiguous())):
+        return
+    _check_tensor(t, name, dtype, shape, device)
+
+
+def _check_x(x):
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    return x.device
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _u64(v, name):
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise ValueError(f"{name} must be in [0, 2**64)")
+    return v
+
+
+def _offset_dev(t, device):
+    """Address of the device word added to a call's offset (a one-element
+    int64 or uint64 tensor), or None."""
+    if t is None:
+        return None
+    if t.dtype not in (torch.int64, torch.uint64) or t.numel() != 1 or t.device != device:
+        raise ValueError(f"offset_dev must be one int64 or uint64 on {device}")
+    return t.data_ptr()
+
+
+def _call(where, fn, dev, stream, *args):
+    """fn(*args, stream) on device `dev`, whichever device is current."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream, dev))
+    else:
+        st = fn(*args, _stream(stream, dev))
+    if st != 0:
+        raise NormError(st, where)
+
+
+def _scratch(where, query, dev, *shape):
+    """The workspace that `query` asks for, or None when it needs no bytes."""
+    out = ctypes.c_size_t(0)
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = query(*shape, ctypes.byref(out))
+    else:
+        st = query(*shape, ctypes.byref(out))
+    if st != 0:
+        raise NormError(st, where)
+    return torch.empty(out.value, dtype=torch.uint8, device=dev) if out.value else None
+
+
+def norm_dropout(x, p, seed, offset=0, *, offset_dev=None, y=None, stream=None):
+    """y = dropout(x) for a contiguous bf16, fp16 or fp32 tensor of any shape
+    (norm_dropout in gbnorm.h).  The mask depends on (seed, offset, element
+    index) alone and is not stored: the backward pass is the same call on dy.
+    offset_dev: a one-element int64 CUDA tensor whose value, read when the
+    kernel runs, is added to offset (for captured graphs).  y=x drops in
+    place."""
+    dev = _check_x(x)
+    code = _dtype_code(x)
+    if y is None:
+        y = torch.empty_like(x)
+    _check(y, "y", x.dtype, x.shape, dev)
+    _call("norm_dropout", lib().norm_dropout, dev, stream, x.data_ptr(), x.numel(), float(p),
+          _u64(seed, "seed"), _u64(offset, "offset"), _offset_dev(offset_dev, dev), code,
+          y.data_ptr())
+    return y
+
+
+def norm_dropout_add_fwd(x, r, gamma, beta=None, eps=1e-5, mode=RMS, *, p, seed, offset=0,
+                         offset_dev=None, h=None, y=None, rstd=None, mean=None, stream=None):
+    """Dropout + residual add + norm forward: h = bf16(r + dropout(x)), y =
+    norm(h), with the mask of norm_dropout(x, p, seed, offset).  Returns (h,
+    y, rstd, mean)."""
+    mode = int(mode)
+    dev = _check_x(x)
+    M, N = _rows(x)
+    bf, f32 = torch.bfloat16, torch.float32
+    shape, lead = x.shape, x.shape[:-1]
+    h = torch.empty_like(x) if h is None else h
+    y = torch.empty_like(x) if y is None else y
+    if rstd is None:
+        rstd = torch.empty(lead, dtype=f32, device=dev)
+    if mode == LAYER and mean is None:
+        mean = torch.empty(lead, dtype=f32, device=dev)
+    for t, n in ((x, "x"), (r, "r"), (h, "h"), (y, "y")):
+        _check(t, n, bf, shape, dev)
+    _check(gamma, "gamma", bf, (N,), dev)
+    _check(beta, "beta", bf, (N,), dev)
+    _check(rstd, "rstd", f32, lead, dev)
+    _check(mean, "mean", f32, lead, dev)
+    _call("norm_dropout_add_fwd", lib().norm_dropout_add_fwd, dev, stream, x.data_ptr(),
+          r.data_ptr(), gamma.data_ptr(), _addr(beta), M, N, float(eps), mode, float(p),
+          _u64(seed, "seed"), _u64(offset, "offset"), _offset_dev(offset_dev, dev), h.data_ptr(),
+          y.data_ptr(), rstd.data_ptr(), _addr(mean))
+    return h, y, rstd, mean
+
+
+def norm_dropout_add_bwd_workspace_bytes(M, N, mode=RMS) -> int:
+    out = ctypes.c_size_t(0)
+    st = lib().norm_dropout_add_bwd_workspace_bytes(int(M), int(N), int(mode), ctypes.byref(out))
+    if st != 0:
+        raise NormError(st, "norm_dropout_add_bwd_workspace_bytes")
+    return int(out.value)
+
+
+def norm_dropout_add_bwd(dy, dh, h, gamma, rstd, mean=None, mode=RMS, *, p, seed, offset=0,
+                         offset_dev=None, dx=None, dr=None, dgamma=None, dbeta=None,
+                         want_dbeta=True, workspace=None, stream=None):
+    """Backward of norm_dropout_add_fwd: dr = norm backward at h + dh (the
+    gradient of r), dx = dropout(dr) with the forward's mask.  Returns (dx,
+    dr, dgamma, dbeta)."""
+    mode = int(mode)
+    dev = _check_x(h)
+    M, N = _rows(h)
+    bf, f32 = torch.bfloat16, torch.float32
+    shape, lead = h.shape, h.shape[:-1]
+    dx = torch.empty_like(h) if dx is None else dx
+    dr = torch.empty_like(h) if dr is None else dr
+    dgamma = torch.empty(N, dtype=f32, device=dev) if dgamma is None else dgamma
+    if mode == LAYER and want_dbeta and dbeta is None:
+        dbeta = torch.empty(N, dtype=f32, device=dev)
+    for t, n in ((dy, "dy"), (dh, "dh"), (h, "h"), (dx, "dx"), (dr, "dr")):
+        _check(t, n, bf, shape, dev)
+    _check(gamma, "gamma", bf, (N,), dev)
+    _check(rstd, "rstd", f32, lead, dev)
+    _check(mean, "mean", f32, lead, dev)
+    _check(dgamma, "dgamma", f32, (N,), dev)
+    _check(dbeta, "dbeta", f32, (N,), dev)
+    if workspace is None:
+        workspace = _scratch("norm_dropout_add_bwd_workspace_bytes",
+                             lib().norm_dropout_add_bwd_workspace_bytes, dev, M, N, mode)
+    _call("norm_dropout_add_bwd", lib().norm_dropout_add_bwd, dev, stream, dy.data_ptr(),
+          dh.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _addr(mean), M, N, mode,
+          float(p), _u64(seed, "seed"), _u64(offset, "offset"), _offset_dev(offset_dev, dev),
+          dx.data_ptr(), dr.data_ptr(), dgamma.data_ptr(), _addr(dbeta), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return dx, dr, dgamma, dbeta
+
+
+def _group_shape(x):
+    if x.dim() < 2:
+        raise ValueError("x must be [B, ..., C]")
+    B, C = x.shape[0], x.shape[-1]
+    return B, (x.numel() // (B * C) if B and C else 0), C
+
+
+def norm_group_fwd_workspace_bytes(B, S, C, groups, dtype=BF16) -> int:
+    out = ctypes.c_size_t(0)
+    st = lib().norm_group_fwd_workspace_bytes(int(B), int(S), int(C), int(groups), int(dtype),
+                                              ctypes.byref(out))
+    if st != 0:
+        raise NormError(st, "norm_group_fwd_workspace_bytes")
+    return int(out.value)
+
+
+def norm_group_bwd_workspace_bytes(B, S, C, groups, dtype=BF16) -> int:
+    out = ctypes.c_size_t(0)
+    st = lib().norm_group_bwd_workspace_bytes(int(B), int(S), int(C), int(groups), int(dtype),
+                                              ctypes.byref(out))
+    if st != 0:
+        raise NormError(st, "norm_group_bwd_workspace_bytes")
+    return int(out.value)
+
+
+def norm_group_fwd(x, gamma, beta, groups, eps=1e-5, act=ACT_NONE, *, p=0.0, seed=0, offset=0,
+                   offset_dev=None, y=None, rstd=None, mean=None, workspace=None, stream=None):
+    """Group normalisation, activation ("none", "silu", "gelu" or ACT_*) and
+    dropout of a channels-last tensor x [B, ..., C] (contiguous bf16, fp16 or
+    fp32; a torch channels_last [B, C, H, W] tensor is x.permute(0, 2, 3, 1)).
+    gamma, beta: [C] of x's type (beta None: zero).  Returns (y, rstd, mean),
+    rstd and mean fp32 [B, groups]."""
+    dev = _check_x(x)
+    code = _dtype_code(x)
+    act = _act(act)
+    groups = int(groups)
+    B, S, C = _group_shape(x)
+    dt, f32 = x.dtype, torch.float32
+    if y is None:
+        y = torch.empty_like(x)
+    gs = (B, groups)
+    if rstd is None:
+        rstd = torch.empty(gs, dtype=f32, device=dev)
+    if mean is None:
+        mean = torch.empty(gs, dtype=f32, device=dev)
+    _check(y, "y", dt, x.shape, dev)
+    _check(gamma, "gamma", dt, (C,), dev)
+    _check(beta, "beta", dt, (C,), dev)
+    _check(rstd, "rstd", f32, gs, dev)
+    _check(mean, "mean", f32, gs, dev)
+    L = lib()
+    if workspace is None:
+        workspace = _scratch("norm_group_fwd_workspace_bytes", L.norm_group_fwd_workspace_bytes,
+                             dev, B, S, C, groups, code)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call("norm_group_fwd", L.norm_group_fwd, dev, stream, x.data_ptr(), gamma.data_ptr(),
+          _addr(beta), B, S, C, groups, float(eps), act, code, float(p), _u64(seed, "seed"),
+          _u64(offset, "offset"), _offset_dev(offset_dev, dev), y.data_ptr(), rstd.data_ptr(),
+          mean.data_ptr(), _addr(workspace), nbytes)
+    return y, rstd, mean
+
+
+def norm_group_bwd(dy, x, gamma, beta, rstd, mean, groups, act=ACT_NONE, *, p=0.0, seed=0,
+                   offset=0, offset_dev=None, dx=None, dgamma=None, dbeta=None, want_dbeta=True,
+                   workspace=None, stream=None):
+    """Backward of norm_group_fwd from its saved rstd and mean (same beta, act,
+    p, seed and offset).  Returns (dx, dgamma, dbeta), dgamma and dbeta fp32
+    [C] (dbeta None when want_dbeta is False)."""
+    dev = _check_x(x)
+    code = _dtype_code(x)
+    act = _act(act)
+    groups = int(groups)
+    B, S, C = _group_shape(x)
+    dt, f32 = x.dtype, torch.float32
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dgamma is None:
+        dgamma = torch.empty(C, dtype=f32, device=dev)
+    if want_dbeta and dbeta is None:
+        dbeta = torch.empty(C, dtype=f32, device=dev)
+    gs = (B, groups)
+    _check(dy, "dy", dt, x.shape, dev)
+    _check(gamma, "gamma", dt, (C,), dev)
+    _check(beta, "beta", dt, (C,), dev)
+    _check(rstd, "rstd", f32, gs, dev)
+    _check(mean, "mean", f32, gs, dev)
+    _check(dx, "dx", dt, x.shape, dev)
+    _check(dgamma, "dgamma", f32, (C,), dev)
+    _check(dbeta, "dbeta", f32, (C,), dev)
+    L = lib()
+    if workspace is None:
+        workspace = _scratch("norm_group_bwd_workspace_bytes", L.norm_group_bwd_workspace_bytes,
+                             dev, B, S, C, groups, code)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call("norm_group_bwd", L.norm_group_bwd, dev, stream, dy.data_ptr(), x.data_ptr(),
+          gamma.data_ptr(), _addr(beta), rstd.data_ptr(), mean.data_ptr(), B, S, C, groups, act,
+          code, float(p), _u64(seed, "seed"), _u64(offset, "offset"),
+          _offset_dev(offset_dev, dev), dx.data_ptr(), dgamma.data_ptr(), _addr(dbeta),
+          _addr(workspace), nbytes)
+    return dx, dgamma, dbeta
+
+
+def norm_group_plan(B, S, C, groups, dtype=BF16, backward=False, sm_count=0, smem_optin=0) -> dict:
+    """How norm_group_fwd / norm_group_bwd run a shape (norm_group_plan in
+    gbnorm.h); sm_count > 0 plans for a described device without CUDA."""
+    out = GroupPlan()
+    st = lib().norm_group_plan(int(B), int(S), int(C), int(groups), int(dtype), int(bool(backward)),
+                               int(sm_count), int(smem_optin), ctypes.byref(out))
+    if st != 0:
+        raise NormError(st, "norm_group_plan")
+    return out.as_dict()

@@ -1,9 +1,10 @@
 """Builds the CUDA library libgbnorm.so in-tree for sm_103a.
 
-Eleven translation units (bf16- and E4M3-output forward, forward with staged
+Its translation units (bf16- and E4M3-output forward, forward with staged
 parameters, backward, long-row kernels plain, with the fused residual add and
-with E4M3 output, the two-pass path for the longest rows, host ABI,
-host-tensor pipeline, and the normalisation fused into a tcgen05 GEMM) are
+with E4M3 output, the streamed rows, the two-pass path for the longest rows,
+host ABI, host-tensor pipeline, the normalisation fused into a tcgen05 GEMM,
+dropout, dropout + residual add + norm, and group normalisation) are
 compiled in parallel with nvcc and linked into one shared object with the
 CUDA runtime linked statically, so the library needs no CUDA library path at
 load time.  `python -m memory_bound_normalization_rmsnorm_gb300.builder -v`
@@ -25,7 +26,8 @@ OUT_DIR = os.path.join(PKG, "lib")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgbnorm.so")
 SOURCES = ["fwd.cu", "fwd_fp8.cu", "fwd_gsm.cu", "bwd.cu", "long.cu", "long_resid.cu",
-           "long_fp8.cu", "split.cu", "stream.cu", "api.cu", "host.cu", "gemm.cu"]
+           "long_fp8.cu", "split.cu", "stream.cu", "api.cu", "host.cu", "gemm.cu", "dropout.cu",
+           "drop_add.cu", "group_fwd.cu", "group_bwd.cu", "group.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -29,6 +29,7 @@
 
 #include "../../include/gbnorm.h"
 #include "common.cuh"
+#include "host_util.h"
 
 namespace gbn {
 namespace {
@@ -644,6 +645,10 @@ norm_status_t shape_plan(int mode, bool bwd, int64_t M, int N, int smem_optin,
 }
 
 const void *kernel_for(const Plan &p, int mode, bool bwd) {
+  if (p.drop)
+    return (p.gsm || p.stream)
+               ? nullptr
+               : drop_add_kernel_ptr(mode, p.K, p.C > 1, p.exact, bwd, p.long_rows);
   if (p.split) return split_kernel_ptr(mode, p.phase, p.K);
   if (p.stream)
     return bwd ? stream_kernel_ptr(mode, p.piece_kp, p.C > 1, p.resid)
@@ -666,14 +671,16 @@ norm_status_t finish_plan(const DeviceInfo &d, int dev, int mode, bool bwd, cons
 // Full plan on the current device: shape part plus the occupancy-derived
 // grid (persistent: as many CTAs or clusters as can be resident at once).
 // `no_stream`: a backward plan without the streaming kernel (the resident
-// long-row kernel or the two-pass path instead; fewer partial rows).
+// long-row kernel or the two-pass path instead; fewer partial rows).  `drop`:
+// the fused residual add with dropout (which has no streaming kernel).
 norm_status_t make_plan(const DeviceInfo &d, int dev, int mode, bool bwd, int64_t M, int N,
                         Plan *out, bool resid = false, bool fp8 = false,
-                        bool no_stream = false) {
+                        bool no_stream = false, bool drop = false) {
   Override ov = read_override();
   if (no_stream) ov.stream = 0;
   const auto key = std::make_tuple(dev, mode * 2 + (bwd ? 1 : 0), M, N,
-                                   (resid ? 1 : 0) | (fp8 ? 2 : 0) | (no_stream ? 4 : 0));
+                                   (resid ? 1 : 0) | (fp8 ? 2 : 0) | (no_stream ? 4 : 0) |
+                                       (drop ? 16 : 0));
   if (!ov.any) {
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_plans.find(key);
@@ -685,6 +692,8 @@ norm_status_t make_plan(const DeviceInfo &d, int dev, int mode, bool bwd, int64_
   Plan p;
   norm_status_t st = shape_plan(mode, bwd, M, N, d.smem_optin, ov, &p, resid, fp8);
   if (st != NORM_OK) return st;
+  p.drop = drop;
+  if (drop) p.wait_ns = 0;
   st = finish_plan(d, dev, mode, bwd, ov, &p);
   if (st != NORM_OK) return st;
 
@@ -1199,6 +1208,38 @@ norm_status_t device_context(int *dev, int *sms, int *smem_optin, unsigned **err
   return NORM_OK;
 }
 
+norm_status_t function_ready(int dev, const void *fn, int smem_optin) {
+  return prepare_function(dev, fn, smem_optin);
+}
+
+norm_status_t launch_serial(const void *fn, dim3 grid, dim3 block, size_t smem, int cluster,
+                            void **args, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
+  if (cluster > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = cluster;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    cudaGetLastError();
+    return NORM_ERR_CUDA;
+  }
+  return NORM_OK;
+}
+
 }  // namespace gbn
 
 // ---------------------------------------------------------------------------
@@ -1458,6 +1499,112 @@ norm_status_t norm_add_bwd(const void *dy, const void *dh, const void *h, const 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((st = launch(kernel_for(p, mode, true), p, a, s)) != NORM_OK) return st;
   return launch_reduce(static_cast<const float *>(workspace), p.P, static_cast<int>(N), dgamma,
+                       (mode == NORM_LAYER) ? dbeta : nullptr, s);
+}
+
+norm_status_t norm_dropout_add_fwd(const void *x, const void *r, const void *gamma,
+                                   const void *beta, int64_t M, int64_t N, float eps,
+                                   norm_mode_t mode, float p, uint64_t seed, uint64_t offset,
+                                   const void *offset_dev, void *h, void *y, float *rstd,
+                                   float *mean, norm_stream_t stream) {
+  if (!x || !r || !gamma || !h || !y || !rstd) return NORM_ERR_NULL;
+  norm_status_t st = check_common(M, N, mode, NORM_MAX_N_FUSED);
+  if (st != NORM_OK) return st;
+  if (mode == NORM_RMS && (beta || mean)) return NORM_ERR_MODE;
+  if (mode == NORM_LAYER && !mean) return NORM_ERR_MODE;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return NORM_ERR_ARG;
+  DropArgs drop;
+  if ((st = make_drop(p, seed, offset, offset_dev, &drop)) != NORM_OK) return st;
+  if (drop.thr == 0)
+    return norm_add_fwd(x, r, gamma, beta, M, N, eps, mode, h, y, rstd, mean, stream);
+  if (!aligned16(x) || !aligned16(r) || !aligned16(gamma) || !aligned16(h) || !aligned16(y) ||
+      !aligned16(rstd) || (beta && !aligned16(beta)) || (mean && !aligned16(mean)))
+    return NORM_ERR_ALIGN;
+  DeviceInfo d;
+  int dev = 0;
+  if ((st = device_info(&d, &dev)) != NORM_OK) return st;
+  Plan pl;
+  if ((st = make_plan(d, dev, mode, false, M, static_cast<int>(N), &pl, true, false, true, true)) !=
+      NORM_OK)
+    return st;
+  NormArgs a = base_args(pl, M, static_cast<int>(N));
+  a.x = static_cast<const uint16_t *>(x);
+  a.res = static_cast<const uint16_t *>(r);
+  a.gamma = static_cast<const uint16_t *>(gamma);
+  a.beta = static_cast<const uint16_t *>(beta);
+  a.h = static_cast<uint16_t *>(h);
+  a.out = static_cast<uint16_t *>(y);
+  a.rstd = rstd;
+  a.mean = mean;
+  a.err = d.err;
+  a.eps = eps;
+  a.drop = drop;
+  return launch(kernel_for(pl, mode, false), pl, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// p = 0 drops nothing but still writes both gradients: the kernels with the
+// generator keep every element at a threshold of 0 and a factor of 1.
+norm_status_t norm_dropout_add_bwd_workspace_bytes(int64_t M, int64_t N, norm_mode_t mode,
+                                                   size_t *bytes) {
+  if (!bytes) return NORM_ERR_NULL;
+  norm_status_t st = check_common(M, N, mode, NORM_MAX_N_FUSED);
+  if (st != NORM_OK) return st;
+  DeviceInfo d;
+  int dev = 0;
+  if ((st = device_info(&d, &dev)) != NORM_OK) return st;
+  Plan pl;
+  if ((st = make_plan(d, dev, mode, true, M, static_cast<int>(N), &pl, true, false, true, true)) !=
+      NORM_OK)
+    return st;
+  *bytes = static_cast<size_t>(pl.P) * static_cast<size_t>(N) * sizeof(float) *
+           (mode == NORM_LAYER ? 2u : 1u);
+  return NORM_OK;
+}
+
+norm_status_t norm_dropout_add_bwd(const void *dy, const void *dh, const void *h,
+                                   const void *gamma, const float *rstd, const float *mean,
+                                   int64_t M, int64_t N, norm_mode_t mode, float p, uint64_t seed,
+                                   uint64_t offset, const void *offset_dev, void *dx, void *dr,
+                                   float *dgamma, float *dbeta, void *workspace,
+                                   size_t workspace_bytes, norm_stream_t stream) {
+  if (!dy || !dh || !h || !gamma || !rstd || !dx || !dr || !dgamma) return NORM_ERR_NULL;
+  norm_status_t st = check_common(M, N, mode, NORM_MAX_N_FUSED);
+  if (st != NORM_OK) return st;
+  if (mode == NORM_RMS && (mean || dbeta)) return NORM_ERR_MODE;
+  if (mode == NORM_LAYER && !mean) return NORM_ERR_MODE;
+  DropArgs drop;
+  if ((st = make_drop(p, seed, offset, offset_dev, &drop)) != NORM_OK) return st;
+  if (!aligned16(dy) || !aligned16(dh) || !aligned16(h) || !aligned16(gamma) ||
+      !aligned16(rstd) || !aligned16(dx) || !aligned16(dr) || !aligned16(dgamma) ||
+      (mean && !aligned16(mean)) || (dbeta && !aligned16(dbeta)) ||
+      (workspace && !aligned16(workspace)))
+    return NORM_ERR_ALIGN;
+  if (!workspace) return NORM_ERR_WORKSPACE;
+  DeviceInfo d;
+  int dev = 0;
+  if ((st = device_info(&d, &dev)) != NORM_OK) return st;
+  Plan pl;
+  if ((st = make_plan(d, dev, mode, true, M, static_cast<int>(N), &pl, true, false, true, true)) !=
+      NORM_OK)
+    return st;
+  const size_t need = static_cast<size_t>(pl.P) * static_cast<size_t>(N) * sizeof(float) *
+                      (mode == NORM_LAYER ? 2u : 1u);
+  if (workspace_bytes < need) return NORM_ERR_WORKSPACE;
+  NormArgs a = base_args(pl, M, static_cast<int>(N));
+  a.x = static_cast<const uint16_t *>(h);
+  a.dy = static_cast<const uint16_t *>(dy);
+  a.res = static_cast<const uint16_t *>(dh);
+  a.gamma = static_cast<const uint16_t *>(gamma);
+  a.out = static_cast<uint16_t *>(dx);
+  a.out2 = static_cast<uint16_t *>(dr);
+  a.rstd = const_cast<float *>(rstd);
+  a.mean = const_cast<float *>(mean);
+  a.ws = static_cast<float *>(workspace);
+  a.err = d.err;
+  a.drop = drop;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = launch(kernel_for(pl, mode, true), pl, a, s)) != NORM_OK) return st;
+  return launch_reduce(static_cast<const float *>(workspace), pl.P, static_cast<int>(N), dgamma,
                        (mode == NORM_LAYER) ? dbeta : nullptr, s);
 }
 

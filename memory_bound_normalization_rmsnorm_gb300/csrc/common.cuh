@@ -18,6 +18,16 @@ constexpr int kMaxThreads = 512;
 // be pushed before the previous one is consumed).
 constexpr int kXchBuffers = 4;
 
+// Dropout, by value (dropout.cuh).  thr = T << 16, T in [1, 65535] out of 2^16;
+// 0: none.
+struct DropArgs {
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t *offset_dev;  // device word added to offset, or null
+  uint32_t thr;
+  float scale;                 // 2^16 / (2^16 - T)
+};
+
 // Kernel arguments.  A "tile" is RT consecutive rows restricted to the
 // column slice [col0, col0 + NS) that one CTA of a cluster owns (the whole
 // row when the cluster has one CTA).  Each row of a tile is processed by a
@@ -57,6 +67,8 @@ struct NormArgs {
   float eps;
   float invN;
   unsigned wait_ns;  // register-resident forward: suspend hint of its stage waits (0: none)
+  uint16_t *out2;    // dropout + residual backward: dr, bf16 [M, N]
+  DropArgs drop;     // dropout + residual add
 };
 
 // Byte offsets of the dynamic shared memory regions (all 16-byte aligned).
@@ -119,6 +131,7 @@ struct Plan {
   bool exact = false; // slices divide evenly into K chunks x tpr threads, tpr >= 32
   bool long_rows = false; // long-row kernels (row re-read from the stage)
   bool resid = false;     // fused residual add variant
+  bool drop = false;      // its variant with dropout of the residual branch
   bool gsm = false;       // forward: gamma/beta read per row from shared memory
   int par_bpc = 0;        // gsm: staged parameter bytes per column
   int G = 0;       // groups per CTA
@@ -177,6 +190,10 @@ const void *fwd_fp8_kernel_ptr(int mode, int K, bool exact, bool resid, int out,
 const void *fwd_gsm_kernel_ptr(int mode, int K, bool resid, int out);
 const void *bwd_kernel_ptr(int mode, int K, bool cluster, bool exact, bool resid = false);
 const void *reduce_kernel_ptr();
+// Dropout + residual add, register-resident (long_rows = false, no clusters)
+// or long-row kernels (drop_add.cu); nullptr if not instantiated.
+const void *drop_add_kernel_ptr(int mode, int K, bool cluster, bool exact, bool bwd,
+                                bool long_rows);
 // Long-row kernels (row slice re-read from shared memory), K in {4, 8}.
 const void *long_kernel_ptr(int mode, int K, bool cluster, bool exact, bool bwd,
                             bool resid = false);

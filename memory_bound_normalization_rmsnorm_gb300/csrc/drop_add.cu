@@ -1,0 +1,75 @@
+// drop_add.cu -- instantiations of the row kernels with dropout of the
+// residual branch in front of the residual add: the forward reads x and r,
+// writes h = bf16(r + drop(x)) and y = norm(h); the backward writes dr (the
+// fused residual backward's dx) and dx = drop(dr).  The generator runs on
+// each 16-byte chunk where the fused residual kernels add it, about 8 issue
+// slots per element on passes that move 8 and 10 bytes per element.
+#include "bwd_kernel.cuh"
+#include "fwd_kernel.cuh"
+#include "long_kernel.cuh"
+
+namespace gbn {
+
+namespace {
+
+template <int MODE, int K, bool EXACT>
+const void *fwd_ptr() {
+  return reinterpret_cast<const void *>(
+      &norm_fwd_kernel<MODE, K, false, EXACT, true, kOutBf16, false, false, true>);
+}
+template <int MODE, int K, bool EXACT>
+const void *bwd_ptr() {
+  return reinterpret_cast<const void *>(&norm_bwd_kernel<MODE, K, false, EXACT, true, true>);
+}
+template <int MODE, int K, bool CLUSTER, bool EXACT>
+const void *long_ptr(bool bwd) {
+  return bwd ? reinterpret_cast<const void *>(
+                   &norm_bwd_long_kernel<MODE, K, CLUSTER, EXACT, true, true>)
+             : reinterpret_cast<const void *>(
+                   &norm_fwd_long_kernel<MODE, K, CLUSTER, EXACT, true, kOutBf16, true>);
+}
+
+// Chunks per thread as the planner gives them: 1 to 6 and 8 in the forward,
+// 1 to 4 in the backward.
+template <int MODE, bool EXACT>
+const void *pick_short(int K, bool bwd) {
+  switch (K) {
+    case 1: return bwd ? bwd_ptr<MODE, 1, EXACT>() : fwd_ptr<MODE, 1, EXACT>();
+    case 2: return bwd ? bwd_ptr<MODE, 2, EXACT>() : fwd_ptr<MODE, 2, EXACT>();
+    case 3: return bwd ? bwd_ptr<MODE, 3, EXACT>() : fwd_ptr<MODE, 3, EXACT>();
+    case 4: return bwd ? bwd_ptr<MODE, 4, EXACT>() : fwd_ptr<MODE, 4, EXACT>();
+    case 5: return bwd ? nullptr : fwd_ptr<MODE, 5, EXACT>();
+    case 6: return bwd ? nullptr : fwd_ptr<MODE, 6, EXACT>();
+    case 8: return bwd ? nullptr : fwd_ptr<MODE, 8, EXACT>();
+    default: return nullptr;
+  }
+}
+
+// Long rows: 8 chunks per thread in the forward, 4 in the backward.
+template <int MODE, bool CLUSTER, bool EXACT>
+const void *pick_long(int K, bool bwd) {
+  switch (K) {
+    case 4: return long_ptr<MODE, 4, CLUSTER, EXACT>(bwd);
+    case 8: return bwd ? nullptr : long_ptr<MODE, 8, CLUSTER, EXACT>(false);
+    default: return nullptr;
+  }
+}
+
+template <int MODE, bool EXACT>
+const void *pick(int K, bool cluster, bool bwd, bool long_rows) {
+  if (!long_rows) return cluster ? nullptr : pick_short<MODE, EXACT>(K, bwd);
+  return cluster ? pick_long<MODE, true, EXACT>(K, bwd) : pick_long<MODE, false, EXACT>(K, bwd);
+}
+
+}  // namespace
+
+const void *drop_add_kernel_ptr(int mode, int K, bool cluster, bool exact, bool bwd,
+                                bool long_rows) {
+  if (mode == kRMS)
+    return exact ? pick<kRMS, true>(K, cluster, bwd, long_rows)
+                 : pick<kRMS, false>(K, cluster, bwd, long_rows);
+  return exact ? pick<kLayer, true>(K, cluster, bwd, long_rows)
+               : pick<kLayer, false>(K, cluster, bwd, long_rows);
+}
+
+}  // namespace gbn

@@ -1,0 +1,114 @@
+// dropout.cu -- dropout of a flat tensor (norm_dropout): y = mask * x / keep
+// with the mask of dropout.cuh.  The backward pass is the same call on dy.
+#include <cuda_runtime.h>
+
+#include "../../include/gbnorm.h"
+#include "common.cuh"
+#include "dropout.cuh"
+#include "host_util.h"
+
+namespace gbn {
+
+namespace {
+
+constexpr int kDropThreads = 256;
+constexpr int kDropUnroll = 4;  // blocks of eight elements in flight per thread
+
+// A thread owns kDropUnroll blocks of eight elements, kDropThreads blocks
+// apart; the loads of all of them are issued before the first generator
+// call.  x and y may be the same tensor (each element is read before its
+// thread writes it), so the loads are ordinary ones.
+template <int DT>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const void *x, void *y, int64_t n,
+                                                               const DropArgs d) {
+  constexpr int V = chunk_elems(DT);
+  constexpr int CB = 8 / V;  // 16-byte chunks per block
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const DropGen gen(d);
+  const int64_t full = n >> 3;
+  const int64_t first =
+      static_cast<int64_t>(blockIdx.x) * (kDropThreads * kDropUnroll) + threadIdx.x;
+  const uint4 *src = static_cast<const uint4 *>(x);
+  uint4 *dst = static_cast<uint4 *>(y);
+  uint4 v[kDropUnroll][CB];
+#pragma unroll
+  for (int u = 0; u < kDropUnroll; ++u) {
+    const int64_t b = first + u * kDropThreads;
+    if (b < full) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) v[u][c] = __ldcs(src + b * CB + c);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kDropUnroll; ++u) {
+    const int64_t b = first + u * kDropThreads;
+    if (b < full) {
+      const uint4 w = gen.words(static_cast<uint64_t>(b));
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        float2 f[V / 2];
+        unpack<DT>(v[u][c], f);
+#pragma unroll
+        for (int p = 0; p < V / 2; ++p) f[p] = gen.pair(f[p], ws[c * (V / 2) + p]);
+        __stcs(dst + b * CB + c, pack<DT>(f));
+      }
+    } else if (b == full && (n & 7)) {
+      const uint4 w = gen.words(static_cast<uint64_t>(b));
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 7; ++e) {
+        if (b * 8 + e < n) {
+          const float2 o = gen.pair(splat2(load_elem<DT>(x, b * 8 + e)), ws[e >> 1]);
+          store_elem<DT>(y, b * 8 + e, (e & 1) ? o.y : o.x);
+        }
+      }
+    }
+  }
+}
+
+const void *dropout_kernel_ptr(int dt) {
+  switch (dt) {
+    case kBF16: return reinterpret_cast<const void *>(&dropout_kernel<kBF16>);
+    case kFP16: return reinterpret_cast<const void *>(&dropout_kernel<kFP16>);
+    default: return reinterpret_cast<const void *>(&dropout_kernel<kFP32>);
+  }
+}
+
+}  // namespace
+
+norm_status_t make_drop(float p, uint64_t seed, uint64_t offset, const void *offset_dev,
+                        DropArgs *out) {
+  if (!(p >= 0.f && p <= 1.f)) return NORM_ERR_ARG;
+  const uint32_t T = static_cast<uint32_t>(static_cast<double>(p) * 65536.0 + 0.5);
+  if (T > 65535) return NORM_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(offset_dev) & 7u) return NORM_ERR_ALIGN;
+  out->seed = seed;
+  out->offset = offset;
+  out->offset_dev = static_cast<const uint64_t *>(offset_dev);
+  out->thr = T << 16;
+  out->scale = 65536.0f / static_cast<float>(65536u - T);
+  return NORM_OK;
+}
+
+}  // namespace gbn
+
+using namespace gbn;
+
+extern "C" norm_status_t norm_dropout(const void *x, int64_t n, float p, uint64_t seed,
+                                      uint64_t offset, const void *offset_dev, norm_dtype_t dtype,
+                                      void *y, norm_stream_t stream) {
+  if (!x || !y) return NORM_ERR_NULL;
+  if (n < 1 || n > (int64_t(1) << 40)) return NORM_ERR_SHAPE;
+  if (dtype != NORM_BF16 && dtype != NORM_FP16 && dtype != NORM_FP32) return NORM_ERR_ARG;
+  DropArgs d;
+  norm_status_t st = make_drop(p, seed, offset, offset_dev, &d);
+  if (st != NORM_OK) return st;
+  if (!aligned_to_16(x) || !aligned_to_16(y)) return NORM_ERR_ALIGN;
+  const int64_t per = int64_t(kDropThreads) * kDropUnroll;
+  const int64_t grid = ((n + 7) / 8 + per - 1) / per;
+  void *args[] = {&x, &y, &n, &d};
+  return launch_serial(dropout_kernel_ptr(dtype), dim3(static_cast<unsigned>(grid)),
+                       dim3(kDropThreads), 0, 1, args, reinterpret_cast<cudaStream_t>(stream));
+}

@@ -26,6 +26,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dropout.cuh"
 #include "ptx.cuh"
 #include "rowops.cuh"
 #include "tiles.cuh"
@@ -42,8 +43,9 @@ namespace gbn {
 // per row instead of living in registers, so a thread can hold more chunks
 // of x.
 // SLEEP: the stage waits carry the plan's suspend hint (a.wait_ns).
+// DROP: (with RESID) x is dropped out before the add: h = bf16(drop(x) + r).
 template <int MODE, int K, bool CLUSTER, bool EXACT, bool RESID, int OUT, bool GSM,
-          bool SLEEP = false>
+          bool SLEEP = false, bool DROP = false>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_kernel(const NormArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   // Staged parameters as fp32 (bf16 output) or bf16 (E4M3 output).
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_kernel(const NormArgs
 
   if (CLUSTER) cluster_sync(); else __syncthreads();
 
+  const DropGen gen = DROP ? DropGen(a.drop) : DropGen();
   const float invN = a.invN;
   int rpar = 0;
   ClusterXch xch = make_xch(smem, L, a.RT, CLUSTER ? a.C : 1, crank);
@@ -209,6 +212,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_kernel(const NormArgs
           float2 xs[4], rs_[4];
           chunk_to_f2(v, xs);
           chunk_to_f2(rv, rs_);
+          if (DROP)
+            gen.template chunk<8>(xs, static_cast<uint64_t>((row0 + r) * a.N + col0 +
+                                                            (t + k * a.tpr) * 8));
 #pragma unroll
           for (int p = 0; p < 4; ++p) xs[p] = add2(xs[p], rs_[p]);
           v = f2_to_chunk(xs);

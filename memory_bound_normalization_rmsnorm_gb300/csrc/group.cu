@@ -1,0 +1,410 @@
+// group.cu -- the group-normalisation entry points of include/gbnorm.h:
+// argument validation, the choice between the resident and the streamed form
+// (group.cuh) with their launch shapes, and the launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <numeric>
+#include <tuple>
+
+#include "../../include/gbnorm.h"
+#include "common.cuh"
+#include "group.cuh"
+#include "host_util.h"
+
+namespace gbn {
+namespace {
+
+struct GroupPlan {
+  bool streamed = false;
+  int sg = 0, ncs = 0, nslab = 1, k = 1, R = 1, slots = 0, splits = 1;
+  int threads = 0;
+  int64_t grid = 0;
+  uint32_t smem = 0;  // resident kernel, or the streamed form's first pass
+  uint32_t smem2 = 0; // streamed form's second pass
+};
+
+// Shape override for sweeps and tests: GBNORM_GROUP="form=1,sg=4,k=2,R=8,
+// splits=3" (any subset; form 0 resident, 1 streamed).  Bypasses the cache.
+struct GroupOverride {
+  int form = -1, sg = 0, k = 0, R = 0, splits = 0;
+  bool any = false;
+};
+
+GroupOverride read_group_override() {
+  GroupOverride o;
+  const char *s = std::getenv("GBNORM_GROUP");
+  while (s && *s) {
+    char key[16];
+    int val = 0;
+    if (std::sscanf(s, "%15[^=]=%d", key, &val) == 2) {
+      if (!std::strcmp(key, "form")) o.form = val;
+      else if (!std::strcmp(key, "sg")) o.sg = val;
+      else if (!std::strcmp(key, "k")) o.k = val;
+      else if (!std::strcmp(key, "R")) o.R = val;
+      else if (!std::strcmp(key, "splits")) o.splits = val;
+      o.any = true;
+    }
+    s = std::strchr(s, ',');
+    if (s) ++s;
+  }
+  return o;
+}
+
+int round32(int v) { return (v + 31) & ~31; }
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// CTAs of `threads` threads and `smem` bytes that one SM holds (the kernels
+// use at most 128 registers per thread).
+int ctas_per_sm(int threads, int64_t smem, int smem_optin) {
+  const int64_t by_smem = (static_cast<int64_t>(smem_optin) + 1024) / (smem + 1024);
+  const int64_t by_regs = 65536 / (128 * threads);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(by_smem, by_regs), 16)));
+}
+
+// Estimated time (us) of a resident plan; the streamed form's estimate is
+// stream_cost.  Constants measured on GB300.
+double resident_cost(const GroupPlan &p, int64_t bytes, int seg_bytes, int sms, int smem_optin) {
+  const int occ = ctas_per_sm(p.threads, p.smem, smem_optin);
+  // clusters of 8 reach about 120 of the 152 SMs
+  const double usable = p.k >= 8 ? sms * 0.79 : (p.k >= 4 ? sms * 0.94 : sms);
+  const double waves = std::ceil(static_cast<double>(p.grid) / (usable * occ));
+  const double used = std::min(usable, static_cast<double>(p.grid));
+  const double seg = seg_bytes >= 128 ? 1.0 : seg_bytes >= 64 ? 0.9 : seg_bytes >= 32 ? 0.75 : 0.5;
+  const double rate = 6.6e6 * seg * std::min(1.0, used / (0.7 * sms));  // bytes per us
+  return bytes / rate + waves * 2.5 + (p.k > 1 ? 0.7 : 0.0);
+}
+
+double stream_cost(int64_t bytes, int64_t read_bytes, bool bwd) {
+  const double l2 = 60e6;  // re-read bytes that L2 still holds
+  const double again = read_bytes <= l2 ? 0.35 * read_bytes : read_bytes - 0.65 * l2;
+  return (bytes + again) / 6.6e6 + (bwd ? 7.5 : 5.0);
+}
+
+norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int sms,
+                              int smem_optin, const GroupOverride &ov, GroupPlan *out) {
+  const int V = chunk_elems(dt), es = elem_bytes(dt), nt = bwd ? 2 : 1;
+  const int D = C / G;
+  const int nc = C / V;
+  const int64_t n = static_cast<int64_t>(B) * S * C;
+  const int64_t bytes = n * es * (nt + 1);
+  GroupPlan best;
+  double best_cost = -1.0;
+  // Resident: slabs of `sg` groups whose channels are a multiple of 8 (so a
+  // slab starts on a 16-byte boundary in every type), clusters of 1 to 8.
+  const int sgu = 8 / std::gcd(D, 8);
+  const int nu = G / sgu;
+  if (ov.form != 1) {
+    int last = 0;
+    for (int t = 1; t <= nu; ++t) {
+      const int sg = ((nu + t - 1) / t) * sgu;
+      if (sg == last) continue;
+      last = sg;
+      if (ov.sg && sg != ov.sg) continue;
+      const int ncs = static_cast<int>(static_cast<int64_t>(sg) * D / V);
+      if (ncs > kGroupThreads) continue;
+      for (int k = 1; k <= 8 && k <= S; k *= 2) {
+        if (ov.k && k != ov.k) continue;
+        GroupPlan p;
+        p.sg = sg;
+        p.ncs = ncs;
+        p.nslab = (G + sg - 1) / sg;
+        p.k = k;
+        const int rows = static_cast<int>(ceil_div64(S, k));
+        const int rmax = std::min(kGroupThreads / ncs, std::max(1, S / k));
+        // at least four rows per thread (one block of the statistics)
+        p.R = std::max(1, std::min(rmax, (rows + 3) / 4));
+        if (ov.R) p.R = std::min(rmax, ov.R);
+        p.slots = (rows + p.R - 1) / p.R;
+        p.threads = round32(ncs * p.R);
+        const int64_t data = static_cast<int64_t>(p.slots) * ncs * p.R * 16 * nt;
+        if (data > smem_optin) continue;
+        p.smem = group_smem_bytes(p.slots, nt, p.R, ncs, V, sg);
+        if (static_cast<int64_t>(p.smem) > smem_optin) continue;
+        p.grid = static_cast<int64_t>(B) * p.nslab * k;
+        if (p.grid > 0x7fffffff) continue;
+        const double c = resident_cost(p, bytes, ncs * 16, sms, smem_optin);
+        if (best_cost < 0 || c < best_cost) {
+          best_cost = c;
+          best = p;
+        }
+      }
+    }
+    if (ov.form == 0 && best_cost < 0) return NORM_ERR_UNSUPPORTED;
+  }
+  if (ov.form != 0 && (best_cost < 0 || stream_cost(bytes, n * es * nt, bwd) < best_cost)) {
+    GroupPlan p;
+    p.streamed = true;
+    p.sg = G;
+    p.ncs = std::min(nc, kGroupThreads);
+    const int rmax = std::max(1, std::min(kGroupThreads / p.ncs, S));
+    p.R = ov.R ? std::min(rmax, ov.R) : rmax;
+    p.threads = round32(p.ncs * p.R);
+    // Row ranges: enough to fill the SMs once (with few samples) or in
+    // nearly full waves, each of at least eight rows per thread.
+    const int64_t resident =
+        static_cast<int64_t>(sms) * std::max(1, std::min(2, 1024 / p.threads / 2));
+    const int64_t most = std::max<int64_t>(1, S / (static_cast<int64_t>(p.R) * 8));
+    int64_t sp = std::max<int64_t>(1, resident / B);
+    for (; sp < most; ++sp) {
+      const int64_t total = sp * B;
+      if (total * 10 >= ceil_div64(total, resident) * resident * 9) break;
+    }
+    sp = std::min(sp, most);
+    if (ov.splits) sp = std::min<int64_t>(ov.splits, S);
+    p.splits = static_cast<int>(std::max<int64_t>(1, sp));
+    p.smem = static_cast<uint32_t>(C) * 8u + group_fold_bytes(p.R, p.ncs, V);
+    p.smem2 = static_cast<uint32_t>(G) * 8u;
+    p.grid = static_cast<int64_t>(B) * p.splits;
+    if (static_cast<int64_t>(p.smem) > smem_optin || p.grid > 0x7fffffff)
+      return NORM_ERR_UNSUPPORTED;
+    best = p;
+  }
+  *out = best;
+  return NORM_OK;
+}
+
+std::mutex g_group_mu;
+std::map<std::tuple<int, int64_t, int64_t, int64_t, int64_t, int>, GroupPlan> g_group_plans;
+
+norm_status_t group_plan(int dev, int sms, int optin, int64_t B, int64_t S, int64_t C, int64_t G,
+                         int dt, bool bwd, GroupPlan *out) {
+  const GroupOverride ov = read_group_override();
+  const auto key = std::make_tuple(dev, B, S, C, G, dt * 2 + (bwd ? 1 : 0));
+  if (!ov.any) {
+    std::lock_guard<std::mutex> lk(g_group_mu);
+    auto it = g_group_plans.find(key);
+    if (it != g_group_plans.end()) {
+      *out = it->second;
+      return NORM_OK;
+    }
+  }
+  norm_status_t st = make_group_plan(static_cast<int>(B), static_cast<int>(S), static_cast<int>(C),
+                                     static_cast<int>(G), dt, bwd, sms, optin, ov, out);
+  if (st == NORM_OK && !ov.any) {
+    std::lock_guard<std::mutex> lk(g_group_mu);
+    try {
+      g_group_plans[key] = *out;
+    } catch (...) {  // out of host memory: the plan is made again next time
+    }
+  }
+  return st;
+}
+
+norm_status_t check_group(int64_t B, int64_t S, int64_t C, int64_t G, norm_dtype_t dtype) {
+  if (dtype != NORM_BF16 && dtype != NORM_FP16 && dtype != NORM_FP32) return NORM_ERR_ARG;
+  if (B < 1 || S < 1 || C < 8 || C % 8 || C > NORM_MAX_GROUP_C) return NORM_ERR_SHAPE;
+  if (G < 1 || G > C || C % G) return NORM_ERR_SHAPE;
+  if (B > (int64_t(1) << 24) || S > (int64_t(1) << 30) || B * S > (int64_t(1) << 40))
+    return NORM_ERR_SHAPE;
+  return NORM_OK;
+}
+
+// Workspace regions (bytes from its start): the streamed form's group pairs,
+// then the backward's partial rows (dgamma, dbeta).
+struct GroupWs {
+  size_t cpart = 0, total = 0;
+  int P = 0;  // partial rows of dgamma (and of dbeta)
+};
+GroupWs group_ws(const GroupPlan &p, int64_t B, int64_t C, int64_t G, bool bwd) {
+  GroupWs w;
+  if (p.streamed) w.cpart = (static_cast<size_t>(p.grid) * G * 8 + 15) & ~size_t(15);
+  w.total = w.cpart;
+  if (bwd) {
+    w.P = static_cast<int>(p.streamed ? p.grid : B);
+    if (w.P > 1) w.total += static_cast<size_t>(w.P) * C * 8;
+  }
+  return w;
+}
+
+GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_t G, int dt) {
+  GroupArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.B = static_cast<int>(B);
+  a.S = static_cast<int>(S);
+  a.C = static_cast<int>(C);
+  a.G = static_cast<int>(G);
+  a.D = static_cast<int>(C / G);
+  a.nc = static_cast<int>(C / chunk_elems(dt));
+  a.sg = p.sg;
+  a.ncs = p.ncs;
+  a.nslab = p.nslab;
+  a.k = p.k;
+  a.R = p.R;
+  a.slots = p.slots;
+  a.splits = p.splits;
+  return a;
+}
+
+norm_status_t run(int dev, int optin, const void *fn, const GroupPlan &p, uint32_t smem, int cluster,
+                  GroupArgs &a, cudaStream_t s) {
+  norm_status_t st = function_ready(dev, fn, optin);
+  if (st != NORM_OK) return st;
+  void *args[] = {&a};
+  return launch_serial(fn, dim3(static_cast<unsigned>(p.grid)), dim3(p.threads), smem, cluster,
+                       args, s);
+}
+
+norm_status_t group_workspace(int64_t B, int64_t S, int64_t C, int64_t G, norm_dtype_t dtype,
+                              bool bwd, size_t *bytes) {
+  if (!bytes) return NORM_ERR_NULL;
+  norm_status_t st = check_group(B, S, C, G, dtype);
+  if (st != NORM_OK) return st;
+  int dev = 0, sms = 0, optin = 0;
+  unsigned *err = nullptr;
+  if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
+  GroupPlan p;
+  if ((st = group_plan(dev, sms, optin, B, S, C, G, dtype, bwd, &p)) != NORM_OK) return st;
+  *bytes = group_ws(p, B, C, G, bwd).total;
+  return NORM_OK;
+}
+
+}  // namespace
+}  // namespace gbn
+
+using namespace gbn;
+
+extern "C" {
+
+norm_status_t norm_group_fwd_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t groups,
+                                             norm_dtype_t dtype, size_t *bytes) {
+  return group_workspace(B, S, C, groups, dtype, false, bytes);
+}
+
+norm_status_t norm_group_bwd_workspace_bytes(int64_t B, int64_t S, int64_t C, int64_t groups,
+                                             norm_dtype_t dtype, size_t *bytes) {
+  return group_workspace(B, S, C, groups, dtype, true, bytes);
+}
+
+norm_status_t norm_group_fwd(const void *x, const void *gamma, const void *beta, int64_t B,
+                             int64_t S, int64_t C, int64_t groups, float eps, norm_act_t act,
+                             norm_dtype_t dtype, float p, uint64_t seed, uint64_t offset,
+                             const void *offset_dev, void *y, float *rstd, float *mean,
+                             void *workspace, size_t workspace_bytes, norm_stream_t stream) {
+  if (!x || !gamma || !y || !rstd || !mean) return NORM_ERR_NULL;
+  norm_status_t st = check_group(B, S, C, groups, dtype);
+  if (st != NORM_OK) return st;
+  if (act != NORM_ACT_NONE && act != NORM_ACT_SILU && act != NORM_ACT_GELU) return NORM_ERR_ARG;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return NORM_ERR_ARG;
+  DropArgs drop;
+  if ((st = make_drop(p, seed, offset, offset_dev, &drop)) != NORM_OK) return st;
+  const void *ptrs[] = {x, gamma, beta, y, rstd, mean, workspace};
+  for (const void *q : ptrs)
+    if (q && !aligned_to_16(q)) return NORM_ERR_ALIGN;
+  int dev = 0, sms = 0, optin = 0;
+  unsigned *err = nullptr;
+  if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
+  GroupPlan pl;
+  if ((st = group_plan(dev, sms, optin, B, S, C, groups, dtype, false, &pl)) != NORM_OK) return st;
+  const GroupWs w = group_ws(pl, B, C, groups, false);
+  if (w.total && (!workspace || workspace_bytes < w.total)) return NORM_ERR_WORKSPACE;
+  GroupArgs a = group_args(pl, B, S, C, groups, dtype);
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.out = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.gpart = static_cast<float *>(workspace);
+  a.drop = drop;
+  a.eps = eps;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool dropping = drop.thr != 0;
+  if (!pl.streamed)
+    return run(dev, optin, group_fwd_kernel_ptr(dtype, act, dropping), pl, pl.smem, pl.k, a, s);
+  if ((st = run(dev, optin, group_stats_kernel_ptr(dtype), pl, pl.smem, 1, a, s)) != NORM_OK)
+    return st;
+  return run(dev, optin, group_apply_kernel_ptr(dtype, act, dropping), pl, pl.smem2, 1, a, s);
+}
+
+norm_status_t norm_group_bwd(const void *dy, const void *x, const void *gamma, const void *beta,
+                             const float *rstd, const float *mean, int64_t B, int64_t S, int64_t C,
+                             int64_t groups, norm_act_t act, norm_dtype_t dtype, float p,
+                             uint64_t seed, uint64_t offset, const void *offset_dev, void *dx,
+                             float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                             norm_stream_t stream) {
+  if (!dy || !x || !gamma || !rstd || !mean || !dx || !dgamma) return NORM_ERR_NULL;
+  norm_status_t st = check_group(B, S, C, groups, dtype);
+  if (st != NORM_OK) return st;
+  if (act != NORM_ACT_NONE && act != NORM_ACT_SILU && act != NORM_ACT_GELU) return NORM_ERR_ARG;
+  DropArgs drop;
+  if ((st = make_drop(p, seed, offset, offset_dev, &drop)) != NORM_OK) return st;
+  const void *ptrs[] = {dy, x, gamma, beta, rstd, mean, dx, dgamma, dbeta, workspace};
+  for (const void *q : ptrs)
+    if (q && !aligned_to_16(q)) return NORM_ERR_ALIGN;
+  int dev = 0, sms = 0, optin = 0;
+  unsigned *err = nullptr;
+  if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
+  GroupPlan pl;
+  if ((st = group_plan(dev, sms, optin, B, S, C, groups, dtype, true, &pl)) != NORM_OK) return st;
+  const GroupWs w = group_ws(pl, B, C, groups, true);
+  if (w.total && (!workspace || workspace_bytes < w.total)) return NORM_ERR_WORKSPACE;
+  GroupArgs a = group_args(pl, B, S, C, groups, dtype);
+  a.x = x;
+  a.dy = dy;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.out = dx;
+  a.mean = const_cast<float *>(mean);
+  a.rstd = const_cast<float *>(rstd);
+  a.gpart = static_cast<float *>(workspace);
+  a.drop = drop;
+  float *rows = w.P > 1 ? reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.cpart)
+                        : nullptr;
+  a.cpart = rows ? rows : dgamma;
+  a.dbeta_part = !dbeta ? nullptr : rows ? rows + static_cast<size_t>(w.P) * C : dbeta;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool dropping = drop.thr != 0;
+  if (!pl.streamed) {
+    st = run(dev, optin, group_bwd_kernel_ptr(dtype, act, dropping), pl, pl.smem, pl.k, a, s);
+  } else {
+    st = run(dev, optin, group_sums_kernel_ptr(dtype, act, dropping), pl, pl.smem, 1, a, s);
+    if (st == NORM_OK)
+      st = run(dev, optin, group_dx_kernel_ptr(dtype, act, dropping), pl, pl.smem2, 1, a, s);
+  }
+  if (st != NORM_OK || !rows) return st;
+  return reduce_rows(rows, w.P, static_cast<int>(C), dgamma, dbeta, s);
+}
+
+norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups, norm_dtype_t dtype,
+                              int backward, int sm_count, int smem_optin_bytes,
+                              norm_group_plan_t *out) {
+  if (!out) return NORM_ERR_NULL;
+  norm_status_t st = check_group(B, S, C, groups, dtype);
+  if (st != NORM_OK) return st;
+  if (backward & ~1) return NORM_ERR_ARG;
+  GroupPlan p;
+  if (sm_count > 0) {
+    if (smem_optin_bytes <= 0) return NORM_ERR_ARG;
+    st = make_group_plan(static_cast<int>(B), static_cast<int>(S), static_cast<int>(C),
+                         static_cast<int>(groups), dtype, backward != 0, sm_count,
+                         smem_optin_bytes, read_group_override(), &p);
+  } else {
+    int dev = 0, sms = 0, optin = 0;
+    unsigned *err = nullptr;
+    if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
+    st = group_plan(dev, sms, optin, B, S, C, groups, dtype, backward != 0, &p);
+  }
+  if (st != NORM_OK) return st;
+  out->streamed = p.streamed ? 1 : 0;
+  out->groups_per_slab = p.sg;
+  out->slabs = p.nslab;
+  out->chunk_columns = p.ncs;
+  out->cluster = p.k;
+  out->row_lanes = p.R;
+  out->rows_per_thread = p.slots;
+  out->row_splits = p.splits;
+  out->threads = p.threads;
+  out->smem_bytes = static_cast<int32_t>(p.smem);
+  out->grid = static_cast<int32_t>(p.grid);
+  out->workspace_bytes = static_cast<int64_t>(group_ws(p, B, C, groups, backward != 0).total);
+  return NORM_OK;
+}
+
+}  // extern "C"

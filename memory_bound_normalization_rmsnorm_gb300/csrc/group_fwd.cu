@@ -1,0 +1,347 @@
+// group_fwd.cu -- forward group normalisation with an activation (and
+// dropout) on channels-last tensors: y = drop(act(xhat * gamma + beta)),
+// xhat = (x - mean) * rstd with the statistics of each (sample, group).
+#include "common.cuh"
+#include "group.cuh"
+
+namespace gbn {
+
+namespace {
+
+// y of one chunk: z = (x - mean) * (rstd gamma) + beta, activation, dropout.
+template <int DT, int ACT, bool DROP>
+__device__ __forceinline__ uint4 out_chunk(const uint4 &xv, const float2 (&nmu)[chunk_elems(DT) / 2],
+                                           const float2 (&sc)[chunk_elems(DT) / 2],
+                                           const float2 (&bf)[chunk_elems(DT) / 2],
+                                           const DropGen &gen, int64_t elem) {
+  constexpr int V = chunk_elems(DT);
+  float2 f[V / 2];
+  unpack<DT>(xv, f);
+#pragma unroll
+  for (int p = 0; p < V / 2; ++p) {
+    const float2 z = fma2(add2(f[p], nmu[p]), sc[p], bf[p]);
+    f[p] = make_float2(act_fwd<ACT>(z.x), act_fwd<ACT>(z.y));
+  }
+  if (DROP) gen.template chunk<V>(f, static_cast<uint64_t>(elem));
+  return pack<DT>(f);
+}
+
+// Per-channel constants of the output pass: -mean, rstd gamma, beta.
+// `gst` holds (mean, rstd) of the groups from g0 on.
+template <int DT>
+__device__ __forceinline__ void out_constants(const GroupArgs &a, const float2 *gst, int g0,
+                                              int chunk, float2 (&nmu)[chunk_elems(DT) / 2],
+                                              float2 (&sc)[chunk_elems(DT) / 2],
+                                              float2 (&bf)[chunk_elems(DT) / 2]) {
+  constexpr int V = chunk_elems(DT);
+  load_affine<DT>(a, chunk, sc, bf);
+#pragma unroll
+  for (int p = 0; p < V / 2; ++p) {
+    const int c = chunk * V + 2 * p;
+    const float2 s0 = gst[c / a.D - g0], s1 = gst[(c + 1) / a.D - g0];
+    nmu[p] = make_float2(-s0.x, -s1.x);
+    sc[p] = mul2(sc[p], make_float2(s0.y, s1.y));
+  }
+}
+
+template <int DT, int ACT, bool DROP>
+__global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const GroupArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int V = chunk_elems(DT);
+  const int nthr = blockDim.x;
+  const int tid = threadIdx.x;
+  const int nact = a.ncs * a.R;  // threads that own a chunk column
+  const int unit = static_cast<int>(blockIdx.x) / a.k;
+  const int q = static_cast<int>(blockIdx.x) - unit * a.k;
+  const int b = unit / a.nslab;
+  const int slab = unit - b * a.nslab;
+  const int rl = tid / a.ncs;
+  const int cc = tid - rl * a.ncs;
+  const int chunk0 = slab * a.ncs;
+  const int ncs_me = min(a.ncs, a.nc - chunk0);
+  const int g0 = slab * a.sg;
+  const int ng = min(a.sg, a.G - g0);
+  const bool on = rl < a.R && cc < ncs_me;
+  const int64_t s0 = part_begin(a.S, q, a.k);
+  const int nrow = static_cast<int>(part_begin(a.S, q + 1, a.k) - s0);
+  const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
+
+  uint4 *data = reinterpret_cast<uint4 *>(smem) + tid;  // slot i of this thread: data[i * nact]
+  unsigned char *fold = smem + static_cast<size_t>(a.slots) * nact * 16;
+  float2 *gst = reinterpret_cast<float2 *>(fold + group_fold_bytes(a.R, a.ncs, V));
+  float2 *gfin = gst + a.sg;
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  const int64_t e0 = group_elem(a, b, s0 + rl, chunk0 + cc, V);  // this thread's first element
+  const int64_t estep = static_cast<int64_t>(a.R) * a.C;
+  const unsigned char *src = static_cast<const unsigned char *>(a.x) + e0 * elem_bytes(DT);
+  const int64_t bstep = estep * elem_bytes(DT);
+  for (int i = 0; i < nr; ++i) {
+    cp_async_16(data + static_cast<size_t>(i) * nact, src + i * bstep);
+    if ((i & 3) == 3) cp_async_commit();
+  }
+  cp_async_commit();
+
+  // Statistics of this thread's channels, four rows at a time as they land.
+  ChannelStats<V> st;
+  st.clear();
+  const int nblk = nr >> 2;
+  for (int j = 0; j < nblk; ++j) {
+    cp_async_wait_upto(nblk - j);  // groups after this block's: nblk - j - 1 and the last
+    float2 f[4][V / 2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) unpack<DT>(data[static_cast<size_t>(4 * j + u) * nact], f[u]);
+    st.add4(f[0], f[1], f[2], f[3]);
+  }
+  cp_async_wait<0>();
+  for (int i = 4 * nblk; i < nr; ++i) {
+    float2 f[V / 2];
+    unpack<DT>(data[static_cast<size_t>(i) * nact], f);
+    st.add1(f);
+  }
+
+  // Row lanes -> channels -> groups -> cluster.
+  fold_stats<V>(st, fold, a.R, rl, cc, a.ncs, on);
+  float *chm = reinterpret_cast<float *>(fold);
+  float *chq = chm + a.ncs * V;
+  if (on && rl == 0) {
+#pragma unroll
+    for (int p = 0; p < V / 2; ++p) {
+      *reinterpret_cast<float2 *>(chm + cc * V + 2 * p) = st.m[p];
+      *reinterpret_cast<float2 *>(chq + cc * V + 2 * p) = st.q[p];
+    }
+  }
+  __syncthreads();
+  for (int g = tid >> 5; g < ng; g += nthr >> 5) {
+    const float2 r = group_of_channels(chm + g * a.D, chq + g * a.D, a.D, static_cast<float>(nrow));
+    if ((tid & 31) == 0) gst[g] = r;
+  }
+  if (a.k > 1) cluster_sync(); else __syncthreads();
+  const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
+  for (int g = tid; g < ng; g += nthr) {
+    float m, m2;
+    if (a.k == 1) {
+      m = gst[g].x;
+      m2 = gst[g].y;
+    } else {
+      // fixed rank order; counts n_r = rows of CTA r (times D)
+      float acc = 0.f;
+      for (int r = 0; r < a.k; ++r) {
+        const float n = static_cast<float>(part_begin(a.S, r + 1, a.k) - part_begin(a.S, r, a.k));
+        acc = fmaf(n, ld_cluster_f2(gst + g, r).x, acc);
+      }
+      m = acc / static_cast<float>(a.S);
+      m2 = 0.f;
+      for (int r = 0; r < a.k; ++r) {
+        const float n = static_cast<float>(part_begin(a.S, r + 1, a.k) - part_begin(a.S, r, a.k)) *
+                        static_cast<float>(a.D);
+        const float2 v = ld_cluster_f2(gst + g, r);
+        m2 += fmaf(n * (v.x - m), v.x - m, v.y);
+      }
+    }
+    const float rs = rsqrtf(m2 / count + a.eps);
+    gfin[g] = make_float2(m, rs);
+    if (q == 0) {
+      a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;
+      a.rstd[static_cast<int64_t>(b) * a.G + g0 + g] = rs;
+    }
+  }
+  __syncthreads();
+  if (a.k > 1) cluster_arrive_release();  // this CTA has read its peers' partials
+
+  if (nr) {
+    float2 nmu[V / 2], sc[V / 2], bf[V / 2];
+    out_constants<DT>(a, gfin, g0, chunk0 + cc, nmu, sc, bf);
+    const DropGen gen(a.drop);
+    unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
+#pragma unroll 4
+    for (int i = 0; i < nr; ++i)
+      st_global_cs_v4(dst + i * bstep,
+                      out_chunk<DT, ACT, DROP>(data[static_cast<size_t>(i) * nact], nmu, sc, bf, gen,
+                                               e0 + i * estep));
+  }
+  if (a.k > 1) cluster_wait_acquire();  // no CTA leaves while a peer may read it
+}
+
+// Streamed form, first pass: (mean, M2) of every group over one row range of
+// one sample.  Chunk columns beyond the CTA's width are taken in turn.
+template <int DT>
+__global__ void __launch_bounds__(kGroupThreads, 1) group_stats_kernel(const GroupArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int V = chunk_elems(DT);
+  const int tid = threadIdx.x;
+  const int b = static_cast<int>(blockIdx.x) / a.splits;
+  const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
+  const int rl = tid / a.ncs;
+  const int cc = tid - rl * a.ncs;
+  const int64_t s0 = part_begin(a.S, sp, a.splits);
+  const int nrow = static_cast<int>(part_begin(a.S, sp + 1, a.splits) - s0);
+  float *chm = reinterpret_cast<float *>(smem);
+  float *chq = chm + a.C;
+  unsigned char *fold = smem + static_cast<size_t>(a.C) * 8;
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  for (int col = 0; col < a.nc; col += a.ncs) {
+    const bool on = rl < a.R && cc < min(a.ncs, a.nc - col);
+    const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
+    const uint4 *src = static_cast<const uint4 *>(a.x) +
+                       (static_cast<int64_t>(b) * a.S + s0 + rl) * a.nc + col + cc;
+    const int64_t step = static_cast<int64_t>(a.R) * a.nc;
+    ChannelStats<V> st;
+    st.clear();
+    int i = 0;
+    for (; i + 8 <= nr; i += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = __ldg(src + (i + u) * step);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float2 f[4][V / 2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) unpack<DT>(v[4 * h + u], f[u]);
+        st.add4(f[0], f[1], f[2], f[3]);
+      }
+    }
+    for (; i < nr; ++i) {
+      float2 f[V / 2];
+      unpack<DT>(__ldg(src + i * step), f);
+      st.add1(f);
+    }
+    fold_stats<V>(st, fold, a.R, rl, cc, a.ncs, on);
+    if (on && rl == 0) {
+#pragma unroll
+      for (int p = 0; p < V / 2; ++p) {
+        *reinterpret_cast<float2 *>(chm + (col + cc) * V + 2 * p) = st.m[p];
+        *reinterpret_cast<float2 *>(chq + (col + cc) * V + 2 * p) = st.q[p];
+      }
+    }
+  }
+  __syncthreads();
+  float2 *out = reinterpret_cast<float2 *>(a.gpart) + static_cast<int64_t>(blockIdx.x) * a.G;
+  for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
+    const float2 r = group_of_channels(chm + g * a.D, chq + g * a.D, a.D, static_cast<float>(nrow));
+    if ((tid & 31) == 0) out[g] = r;
+  }
+}
+
+// Streamed form, second pass: folds the splits' statistics, then the output
+// of one row range, last row first (the first pass read it first row first).
+template <int DT, int ACT, bool DROP>
+__global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const GroupArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int V = chunk_elems(DT);
+  const int tid = threadIdx.x;
+  const int lane = tid & 31;
+  const int b = static_cast<int>(blockIdx.x) / a.splits;
+  const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
+  const int rl = tid / a.ncs;
+  const int cc = tid - rl * a.ncs;
+  const int64_t s0 = part_begin(a.S, sp, a.splits);
+  const int nrow = static_cast<int>(part_begin(a.S, sp + 1, a.splits) - s0);
+  float2 *gfin = reinterpret_cast<float2 *>(smem);
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  const float2 *part =
+      reinterpret_cast<const float2 *>(a.gpart) + static_cast<int64_t>(b) * a.splits * a.G;
+  const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
+  for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
+    float acc = 0.f;
+    for (int r = lane; r < a.splits; r += 32) {
+      const float n = static_cast<float>(part_begin(a.S, r + 1, a.splits) - part_begin(a.S, r, a.splits));
+      acc = fmaf(n, __ldcg(part + static_cast<int64_t>(r) * a.G + g).x, acc);
+    }
+    const float m = warp_sum(acc) / static_cast<float>(a.S);
+    float m2 = 0.f;
+    for (int r = lane; r < a.splits; r += 32) {
+      const float n = static_cast<float>(part_begin(a.S, r + 1, a.splits) - part_begin(a.S, r, a.splits)) *
+                      static_cast<float>(a.D);
+      const float2 v = __ldcg(part + static_cast<int64_t>(r) * a.G + g);
+      m2 += fmaf(n * (v.x - m), v.x - m, v.y);
+    }
+    m2 = warp_sum(m2);
+    if (lane == 0) {
+      const float rs = rsqrtf(m2 / count + a.eps);
+      gfin[g] = make_float2(m, rs);
+      if (sp == 0) {
+        a.mean[static_cast<int64_t>(b) * a.G + g] = m;
+        a.rstd[static_cast<int64_t>(b) * a.G + g] = rs;
+      }
+    }
+  }
+  __syncthreads();
+
+  const DropGen gen(a.drop);
+  for (int col = 0; col < a.nc; col += a.ncs) {
+    if (rl >= a.R || cc >= min(a.ncs, a.nc - col) || rl >= nrow) continue;
+    const int nr = (nrow - rl + a.R - 1) / a.R;
+    float2 nmu[V / 2], sc[V / 2], bf[V / 2];
+    out_constants<DT>(a, gfin, 0, col + cc, nmu, sc, bf);
+    const int64_t row = static_cast<int64_t>(b) * a.S + s0 + rl;
+    const int64_t c0 = row * a.nc + col + cc;
+    const int64_t step = static_cast<int64_t>(a.R) * a.nc;
+    const uint4 *src = static_cast<const uint4 *>(a.x);
+    uint4 *dst = static_cast<uint4 *>(a.out);
+    int i = nr;
+    for (; i >= 4; i -= 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = __ldcs(src + c0 + (i - 1 - u) * step);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t c = c0 + (i - 1 - u) * step;
+        st_global_cs_v4(dst + c, out_chunk<DT, ACT, DROP>(v[u], nmu, sc, bf, gen, c * V));
+      }
+    }
+    for (; i > 0; --i) {
+      const int64_t c = c0 + (i - 1) * step;
+      st_global_cs_v4(dst + c, out_chunk<DT, ACT, DROP>(__ldcs(src + c), nmu, sc, bf, gen, c * V));
+    }
+  }
+}
+
+template <int DT, int ACT>
+const void *pick_fwd(bool drop, bool streamed) {
+  if (streamed)
+    return drop ? reinterpret_cast<const void *>(&group_apply_kernel<DT, ACT, true>)
+                : reinterpret_cast<const void *>(&group_apply_kernel<DT, ACT, false>);
+  return drop ? reinterpret_cast<const void *>(&group_fwd_kernel<DT, ACT, true>)
+              : reinterpret_cast<const void *>(&group_fwd_kernel<DT, ACT, false>);
+}
+
+template <int DT>
+const void *pick_act(int act, bool drop, bool streamed) {
+  switch (act) {
+    case kActSilu: return pick_fwd<DT, kActSilu>(drop, streamed);
+    case kActGelu: return pick_fwd<DT, kActGelu>(drop, streamed);
+    default: return pick_fwd<DT, kActNone>(drop, streamed);
+  }
+}
+
+const void *pick(int dt, int act, bool drop, bool streamed) {
+  switch (dt) {
+    case kBF16: return pick_act<kBF16>(act, drop, streamed);
+    case kFP16: return pick_act<kFP16>(act, drop, streamed);
+    default: return pick_act<kFP32>(act, drop, streamed);
+  }
+}
+
+}  // namespace
+
+const void *group_fwd_kernel_ptr(int dt, int act, bool drop) { return pick(dt, act, drop, false); }
+const void *group_apply_kernel_ptr(int dt, int act, bool drop) { return pick(dt, act, drop, true); }
+
+const void *group_stats_kernel_ptr(int dt) {
+  switch (dt) {
+    case kBF16: return reinterpret_cast<const void *>(&group_stats_kernel<kBF16>);
+    case kFP16: return reinterpret_cast<const void *>(&group_stats_kernel<kFP16>);
+    default: return reinterpret_cast<const void *>(&group_stats_kernel<kFP32>);
+  }
+}
+
+}  // namespace gbn

@@ -23,6 +23,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dropout.cuh"
 #include "ptx.cuh"
 #include "rowops.cuh"
 #include "tiles.cuh"
@@ -51,7 +52,9 @@ struct Pending {
 // maxima of a row travel in the next row's exchange round, so its codes are
 // written one round later) or with per-32-column E8M0 exponents
 // (kOutFp8Mx; slices start on a block).
-template <int MODE, int K, bool CLUSTER, bool EXACT, bool RESID, int OUT = kOutBf16>
+// DROP: (with RESID) x is dropped out before the add: h = bf16(drop(x) + r).
+template <int MODE, int K, bool CLUSTER, bool EXACT, bool RESID, int OUT = kOutBf16,
+          bool DROP = false>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const NormArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const SmemLayout L = make_layout(a.RT, a.NS, a.S, a.G, a.tpr, RESID ? 2 : 1, false, a.C);
@@ -113,6 +116,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
     }
   }
 
+  const DropGen gen = DROP ? DropGen(a.drop) : DropGen();
   const float invN = a.invN;
   const int cstep = a.tpr * 16;
   int rpar = 0;
@@ -121,12 +125,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
   // First read of chunk k of a row slot: x, or with RESID h = bf16(x + r),
   // which replaces x in the stage for the later passes (each chunk is read
   // and written by its one owning thread only).
-  auto first_chunk = [&](const unsigned char *rowp, int k) -> uint4 {
+  // `row` is the row's index in the tensor.
+  auto first_chunk = [&](const unsigned char *rowp, int k, int64_t row) -> uint4 {
     const unsigned char *p = rowp + k * cstep;
     if (!RESID) return lds_chunk(p);
     float2 xs[4], rs_[4];
     chunk_to_f2(lds_chunk(p), xs);
     chunk_to_f2(lds_chunk(p + L.tensor_bytes), rs_);
+    if (DROP)
+      gen.template chunk<8>(xs,
+                            static_cast<uint64_t>(row * a.N + col0 + (t + k * a.tpr) * 8));
 #pragma unroll
     for (int q = 0; q < 4; ++q) xs[q] = add2(xs[q], rs_[q]);
     const uint4 h = f2_to_chunk(xs);
@@ -136,8 +144,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
 
   // Statistics pass of row slot r of the stage at `st`: this row group's
   // partial, (n, mean, M2) for LayerNorm or (sum x^2) for RMSNorm.
-  auto stats_pass = [&](const unsigned char *st, int r, bool active, float &pa, float &pb,
-                        float &pc) {
+  auto stats_pass = [&](const unsigned char *st, int64_t row0, int r, bool active, float &pa,
+                        float &pb, float &pc) {
     const unsigned char *rowp = st + static_cast<size_t>(r) * a.NS * 2 + t * 16;
     if (MODE == kLayer) {
       float2 a0 = splat2(0.f), a1 = splat2(0.f);
@@ -146,7 +154,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
         for (int k = 0; k < K; ++k) {
           if (EXACT || t + k * a.tpr < nsc_me) {
             float2 xf[4];
-            chunk_to_f2(first_chunk(rowp, k), xf);
+            chunk_to_f2(first_chunk(rowp, k, row0 + r), xf);
             a0 = add2(a0, add2(xf[0], xf[1]));
             a1 = add2(a1, add2(xf[2], xf[3]));
           }
@@ -193,7 +201,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
         for (int k = 0; k < K; ++k) {
           if (EXACT || t + k * a.tpr < nsc_me) {
             float2 xf[4];
-            chunk_to_f2(first_chunk(rowp, k), xf);
+            chunk_to_f2(first_chunk(rowp, k, row0 + r), xf);
             q0 = fma2(xf[0], xf[0], fma2(xf[1], xf[1], q0));
             q1 = fma2(xf[2], xf[2], fma2(xf[3], xf[3], q1));
             if (OUT == kOutFp8Row) {
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
       Pending cur;
       cur.tile = tile;
       cur.s = s;
-      stats_pass(st, r, r < nrows, cur.a, cur.b, cur.c);
+      stats_pass(st, row0, r, r < nrows, cur.a, cur.b, cur.c);
       if (OUT == kOutFp8Row && MODE == kLayer) {
         cluster_push(cur.a, cur.b, cur.c, r, t, xch, have_pend ? pend_am : 0.f);
         const float *row = cluster_wait_row(r, xch, a.err, abort_flag);
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
         const int r = g + q * a.G;
         const bool active = r < nrows;
         float pa, pb, pc;
-        stats_pass(st, r, active, pa, pb, pc);
+        stats_pass(st, row0, r, active, pa, pb, pc);
         if (active) output_pass(st, row0, r, pa, pb, kFp8Whole, pb);
       }
       release(tile, s);
@@ -475,7 +483,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
 // ahead of that row's dx pass (before the dot pass without a cluster; after
 // the previous tile's push in a cluster), so the stage holds h and dy like
 // the plain backward and takes the same (narrower) clusters.
-template <int MODE, int K, bool CLUSTER, bool EXACT, bool RESID>
+// DROP: (with RESID) that sum is dr and dx = drop(dr).
+template <int MODE, int K, bool CLUSTER, bool EXACT, bool RESID, bool DROP = false>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_long_kernel(const NormArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const SmemLayout L = make_layout(a.RT, a.NS, a.S, a.G, a.tpr, 2, true, a.C);
@@ -537,6 +546,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_long_kernel(const Nor
     }
   }
 
+  const DropGen gen = DROP ? DropGen(a.drop) : DropGen();
   const float invN = a.invN;
   const int cstep = a.tpr * 16;
   int rpar = 0;
@@ -639,6 +649,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_long_kernel(const Nor
           chunk_to_f2(dhr[RESID ? k : 0], hf);
 #pragma unroll
           for (int p = 0; p < 4; ++p) o[p] = add2(o[p], hf[p]);
+        }
+        if (DROP) {
+          const int64_t at = (row0 + r) * a.N + col0 + (t + k * a.tpr) * 8;
+          st_global_cs_v4(a.out2 + at, f2_to_chunk(o));
+          gen.template chunk<8>(o, static_cast<uint64_t>(at));
         }
         st_global_cs_v4(dxrow + k * a.tpr * 8, f2_to_chunk(o));
       }

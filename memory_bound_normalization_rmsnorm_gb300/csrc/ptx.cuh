@@ -184,6 +184,17 @@ __device__ __forceinline__ uint32_t mapa_shared(const void *local, uint32_t rank
   return remote;
 }
 
+// Two floats at the address of `local` in the shared memory of CTA `rank` of
+// the cluster.
+__device__ __forceinline__ float2 ld_cluster_f2(const float2 *local, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(mapa_shared(local, rank))
+               : "memory");
+  return v;
+}
+
 // Asynchronous 16-byte store into another CTA's shared memory whose
 // completion is counted (in bytes) on that CTA's mbarrier `remote_bar`.
 // Orders nothing else: no fence over this thread's other memory traffic.

@@ -1,0 +1,164 @@
+"""The dropout and group-normalisation entry points without a GPU: refusals
+with the documented status codes before CUDA is touched, and the group plans
+of a described GB300 (152 SMs, 227 KB of shared memory) in bounds, owning
+every row and group once."""
+import ctypes
+
+import pytest
+import torch
+
+import memory_bound_normalization_rmsnorm_gb300 as gb
+
+F = 16  # a fake, 16-byte aligned address: validation fails before any use
+SMS, OPTIN = 152, 232448
+
+
+def test_dropout_refusals():
+    f = gb.lib().norm_dropout
+    ok = dict(x=F, n=64, p=0.1, seed=1, off=2, od=None, dt=0, y=F)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return f(a["x"], a["n"], a["p"], a["seed"], a["off"], a["od"], a["dt"], a["y"], None)
+
+    assert call(x=None) == 1 and call(y=None) == 1
+    assert call(n=0) == 2 and call(n=-1) == 2 and call(n=(1 << 40) + 1) == 2
+    assert call(dt=3) == 9 and call(dt=-1) == 9
+    for p in (-0.1, 1.0, 2.0, float("nan"), 1 - 2.0 ** -17):
+        assert call(p=p) == 9, p
+    assert call(x=F + 8) == 3 and call(y=F + 2) == 3 and call(od=F + 4) == 3
+
+
+def test_dropout_add_refusals():
+    f = gb.lib().norm_dropout_add_fwd
+    ok = dict(x=F, r=F, g=F, b=None, M=4, N=64, eps=1e-5, mode=0, p=0.1, od=None, h=F, y=F, rs=F,
+              m=None)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return f(a["x"], a["r"], a["g"], a["b"], a["M"], a["N"], a["eps"], a["mode"], a["p"], 1, 2,
+                 a["od"], a["h"], a["y"], a["rs"], a["m"], None)
+
+    for k in ("x", "r", "g", "h", "y", "rs"):
+        assert call(**{k: None}) == 1, k
+        assert call(**{k: F + 8}) == 3, k
+    assert call(N=12) == 2 and call(M=0) == 2 and call(N=262144 + 8) == 2
+    assert call(mode=2) == 4 and call(b=F) == 4 and call(m=F) == 4 and call(mode=1) == 4
+    assert call(eps=-1.0) == 9 and call(p=1.0) == 9 and call(p=-0.5) == 9 and call(od=F + 4) == 3
+    assert call(p=0.0, x=F + 8) == 3
+
+    fb = gb.lib().norm_dropout_add_bwd
+    okb = dict(dy=F, dh=F, h=F, g=F, rs=F, m=None, M=4, N=64, mode=0, p=0.1, dx=F, dr=F, dg=F,
+              db=None, ws=F, wsb=1 << 20)
+
+    def bwd(**kw):
+        a = dict(okb, **kw)
+        return fb(a["dy"], a["dh"], a["h"], a["g"], a["rs"], a["m"], a["M"], a["N"], a["mode"],
+                 a["p"], 1, 2, None, a["dx"], a["dr"], a["dg"], a["db"], a["ws"], a["wsb"], None)
+
+    for k in ("dy", "dh", "h", "g", "rs", "dx", "dr", "dg"):
+        assert bwd(**{k: None}) == 1, k
+        assert bwd(**{k: F + 8}) == 3, k
+    assert bwd(ws=None) == 5 and bwd(ws=F + 4) == 3
+    assert bwd(mode=1) == 4 and bwd(db=F) == 4 and bwd(p=float("inf")) == 9 and bwd(N=20) == 2
+
+
+def test_group_refusals():
+    f = gb.lib().norm_group_fwd
+    ok = dict(x=F, g=F, b=F, B=2, S=5, C=32, G=4, eps=1e-5, act=1, dt=0, p=0.0, od=None, y=F, rs=F,
+              m=F, ws=None, wsb=0)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return f(a["x"], a["g"], a["b"], a["B"], a["S"], a["C"], a["G"], a["eps"], a["act"],
+                 a["dt"], a["p"], 1, 2, a["od"], a["y"], a["rs"], a["m"], a["ws"], a["wsb"], None)
+
+    for k in ("x", "g", "y", "rs", "m"):
+        assert call(**{k: None}) == 1, k
+    for k in ("x", "g", "b", "y", "rs", "m", "ws"):
+        assert call(**{k: F + 8}) == 3, k
+    for kw in (dict(B=0), dict(S=0), dict(C=0), dict(C=12, G=4), dict(C=8200, G=8), dict(G=0),
+               dict(G=5), dict(G=64), dict(B=(1 << 24) + 1), dict(S=(1 << 30) + 1),
+               dict(B=1 << 20, S=1 << 21)):
+        assert call(**kw) == 2, kw
+    for kw in (dict(act=3), dict(act=-1), dict(dt=3), dict(p=1.0), dict(p=-0.1), dict(eps=-1.0),
+               dict(eps=float("nan"))):
+        assert call(**kw) == 9, kw
+    assert call(od=F + 4) == 3
+    fb = gb.lib().norm_group_bwd
+    okb = dict(dy=F, x=F, g=F, b=None, rs=F, m=F, B=2, S=5, C=32, G=4, act=1, dt=0, p=0.0, dx=F,
+              dg=F, db=None, ws=None, wsb=0)
+
+    def bwd(**kw):
+        a = dict(okb, **kw)
+        return fb(a["dy"], a["x"], a["g"], a["b"], a["rs"], a["m"], a["B"], a["S"], a["C"], a["G"],
+                 a["act"], a["dt"], a["p"], 1, 2, None, a["dx"], a["dg"], a["db"], a["ws"],
+                 a["wsb"], None)
+
+    for k in ("dy", "x", "g", "rs", "m", "dx", "dg"):
+        assert bwd(**{k: None}) == 1, k
+        assert bwd(**{k: F + 8}) == 3, k
+    assert bwd(db=F + 4) == 3 and bwd(act=7) == 9 and bwd(C=20) == 2 and bwd(p=2.0) == 9
+    if not torch.cuda.is_available():
+        assert call() == 7 and bwd() == 7  # valid arguments, no device
+    n = ctypes.c_size_t(0)
+    for q in (gb.lib().norm_group_fwd_workspace_bytes, gb.lib().norm_group_bwd_workspace_bytes):
+        assert q(2, 5, 32, 4, 0, None) == 1 and q(2, 5, 32, 3, 0, ctypes.byref(n)) == 2
+        assert q(2, 5, 32, 4, 5, ctypes.byref(n)) == 9
+
+
+def _plan_cases():
+    for C, G in ((8, 1), (8, 8), (24, 8), (40, 4), (64, 32), (88, 11), (168, 12), (320, 32),
+                 (512, 1), (640, 32), (1280, 32), (2560, 32), (8192, 32), (8192, 8192), (8184, 3)):
+        for B in (1, 2, 16, 100, 5000):
+            for S in (1, 2, 7, 64, 221, 1024, 4096, 65536, 1 << 20):
+                yield B, S, C, G
+
+
+@pytest.mark.parametrize("override", ["", "form=0", "form=1", "form=1,splits=7", "form=0,k=8",
+                                      "form=0,R=2"])
+def test_group_plans_in_bounds(override, monkeypatch):
+    if override:
+        monkeypatch.setenv("GBNORM_GROUP", override)
+    seen = set()
+    for B, S, C, G in _plan_cases():
+        for dt in (0, 2):
+            for bwd in (False, True):
+                try:
+                    p = gb.norm_group_plan(B, S, C, G, dt, bwd, SMS, OPTIN)
+                except gb.NormError as e:
+                    assert e.status == 6 and override.startswith("form=0")
+                    continue
+                V, D, nt = (4 if dt == 2 else 8), C // G, 2 if bwd else 1
+                label = (B, S, C, G, dt, bwd, p)
+                seen.add(p["streamed"])
+                assert p["threads"] % 32 == 0 and 32 <= p["threads"] <= 512, label
+                assert p["chunk_columns"] * p["row_lanes"] <= p["threads"], label
+                assert 0 < p["smem_bytes"] <= OPTIN and 1 <= p["grid"] < 1 << 31, label
+                fold = max((p["row_lanes"] // 2) * p["chunk_columns"] * (8 * V + 4),
+                           p["chunk_columns"] * V * 8)
+                if p["streamed"]:
+                    assert p["grid"] == B * p["row_splits"] and p["row_splits"] <= max(S, 1), label
+                    assert p["smem_bytes"] >= 8 * C + fold, label
+                    need = (p["grid"] * G * 8 + 15) // 16 * 16 + (p["grid"] * C * 8 if bwd else 0)
+                    if bwd and p["grid"] == 1:
+                        need -= C * 8
+                    assert p["workspace_bytes"] == need, label
+                    continue
+                # slabs: whole groups, 16-byte borders, covering every group once
+                assert p["groups_per_slab"] * D == p["chunk_columns"] * V, label
+                assert p["groups_per_slab"] * D % 8 == 0, label
+                assert (p["slabs"] - 1) * p["groups_per_slab"] < G <= \
+                    p["slabs"] * p["groups_per_slab"], label
+                assert p["grid"] == B * p["slabs"] * p["cluster"], label
+                assert p["cluster"] in (1, 2, 4, 8) and p["cluster"] <= S, label
+                # rows: every CTA's range fits its threads' slots, and no row
+                # lane is empty
+                rows = [S * (i + 1) // p["cluster"] - S * i // p["cluster"]
+                        for i in range(p["cluster"])]
+                assert sum(rows) == S and max(rows) <= p["rows_per_thread"] * p["row_lanes"], label
+                assert p["row_lanes"] <= min(rows), label
+                data = p["rows_per_thread"] * p["chunk_columns"] * p["row_lanes"] * 16 * nt
+                assert p["smem_bytes"] >= data + fold + 16 * p["groups_per_slab"], label
+                assert p["workspace_bytes"] == (B * C * 8 if bwd and B > 1 else 0), label
+    assert seen == ({0, 1} if not override else {int(override[5])})
