@@ -1,7 +1,9 @@
 """ctypes binding of libgbnorm.so (the C ABI of include/gbnorm.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels of the library.  PyTorch supplies device memory (outputs and the
+kernels of the library.  The dropout and group-normalisation functions, whose
+small calls are shorter than ctypes marshalling, marshal in the extension
+module gbnorm_torch.so instead (csrc/torch_binding.cpp).  PyTorch supplies device memory (outputs and the
 backward workspace are allocated with torch when the caller passes none) and
 the stream (torch's current stream unless one is given).  There is no
 fallback: if the shared library is missing, every call raises.
@@ -9,6 +11,8 @@ fallback: if the shared library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
@@ -609,7 +613,6 @@ def norm_get_device_error(stream=None, device=None):
 BF16 = 0
 FP16 = 1
 FP32 = 2
-_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 
 ACT_NONE = 0
 ACT_SILU = 1
@@ -625,72 +628,32 @@ def _act(act):
     return int(act)
 
 
-def _dtype_code(x):
-    code = _DTYPES.get(x.dtype)
-    if code is None:
-        raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    return code
-
-
-def _check(t, name, dtype, shape, device):
-    """_check_tensor, quick where nothing is wrong."""
-    if (t is None or (t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape
-                      and t.is_contiguous())):
-        return
-    _check_tensor(t, name, dtype, shape, device)
-
-
-def _check_x(x):
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
-    return x.device
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _u64(v, name):
-    v = int(v)
-    if not 0 <= v < 1 << 64:
-        raise ValueError(f"{name} must be in [0, 2**64)")
-    return v
-
-
-def _offset_dev(t, device):
-    """Address of the device word added to a call's offset (a one-element
-    int64 or uint64 tensor), or None."""
-    if t is None:
+def _handle(stream):
+    """The native binding's stream argument: None or a stream handle."""
+    if stream is None:
         return None
-    if t.dtype not in (torch.int64, torch.uint64) or t.numel() != 1 or t.device != device:
-        raise ValueError(f"offset_dev must be one int64 or uint64 on {device}")
-    return t.data_ptr()
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _call(where, fn, dev, stream, *args):
-    """fn(*args, stream) on device `dev`, whichever device is current."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream, dev))
-    else:
-        st = fn(*args, _stream(stream, dev))
-    if st != 0:
-        raise NormError(st, where)
+_native_module = None
 
 
-def _scratch(where, query, dev, *shape):
-    """The workspace that `query` asks for, or None when it needs no bytes."""
-    out = ctypes.c_size_t(0)
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            st = query(*shape, ctypes.byref(out))
-    else:
-        st = query(*shape, ctypes.byref(out))
-    if st != 0:
-        raise NormError(st, where)
-    return torch.empty(out.value, dtype=torch.uint8, device=dev) if out.value else None
+def _native():
+    """The native tensor binding (gbnorm_torch.so; raises if not built)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        path = _build.TORCH_LIB
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it first "
+                "(python -m memory_bound_normalization_rmsnorm_gb300.builder)")
+        loader = importlib.machinery.ExtensionFileLoader("gbnorm_torch", path)
+        spec = importlib.util.spec_from_file_location("gbnorm_torch", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _native_module = module
+    return _native_module
 
 
 def norm_dropout(x, p, seed, offset=0, *, offset_dev=None, y=None, stream=None):
@@ -700,15 +663,11 @@ def norm_dropout(x, p, seed, offset=0, *, offset_dev=None, y=None, stream=None):
     offset_dev: a one-element int64 CUDA tensor whose value, read when the
     kernel runs, is added to offset (for captured graphs).  y=x drops in
     place."""
-    dev = _check_x(x)
-    code = _dtype_code(x)
-    if y is None:
-        y = torch.empty_like(x)
-    _check(y, "y", x.dtype, x.shape, dev)
-    _call("norm_dropout", lib().norm_dropout, dev, stream, x.data_ptr(), x.numel(), float(p),
-          _u64(seed, "seed"), _u64(offset, "offset"), _offset_dev(offset_dev, dev), code,
-          y.data_ptr())
-    return y
+    out = (_native_module or _native()).dropout(x, p, seed, offset, offset_dev, y,
+                                                _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_dropout")
+    return out[0]
 
 
 def norm_dropout_add_fwd(x, r, gamma, beta=None, eps=1e-5, mode=RMS, *, p, seed, offset=0,
@@ -716,28 +675,12 @@ def norm_dropout_add_fwd(x, r, gamma, beta=None, eps=1e-5, mode=RMS, *, p, seed,
     """Dropout + residual add + norm forward: h = bf16(r + dropout(x)), y =
     norm(h), with the mask of norm_dropout(x, p, seed, offset).  Returns (h,
     y, rstd, mean)."""
-    mode = int(mode)
-    dev = _check_x(x)
-    M, N = _rows(x)
-    bf, f32 = torch.bfloat16, torch.float32
-    shape, lead = x.shape, x.shape[:-1]
-    h = torch.empty_like(x) if h is None else h
-    y = torch.empty_like(x) if y is None else y
-    if rstd is None:
-        rstd = torch.empty(lead, dtype=f32, device=dev)
-    if mode == LAYER and mean is None:
-        mean = torch.empty(lead, dtype=f32, device=dev)
-    for t, n in ((x, "x"), (r, "r"), (h, "h"), (y, "y")):
-        _check(t, n, bf, shape, dev)
-    _check(gamma, "gamma", bf, (N,), dev)
-    _check(beta, "beta", bf, (N,), dev)
-    _check(rstd, "rstd", f32, lead, dev)
-    _check(mean, "mean", f32, lead, dev)
-    _call("norm_dropout_add_fwd", lib().norm_dropout_add_fwd, dev, stream, x.data_ptr(),
-          r.data_ptr(), gamma.data_ptr(), _addr(beta), M, N, float(eps), mode, float(p),
-          _u64(seed, "seed"), _u64(offset, "offset"), _offset_dev(offset_dev, dev), h.data_ptr(),
-          y.data_ptr(), rstd.data_ptr(), _addr(mean))
-    return h, y, rstd, mean
+    out = (_native_module or _native()).dropout_add_fwd(
+        x, r, gamma, beta, eps, mode, p, seed, offset, offset_dev, h, y, rstd, mean,
+        _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_dropout_add_fwd")
+    return out
 
 
 def norm_dropout_add_bwd_workspace_bytes(M, N, mode=RMS) -> int:
@@ -754,39 +697,12 @@ def norm_dropout_add_bwd(dy, dh, h, gamma, rstd, mean=None, mode=RMS, *, p, seed
     """Backward of norm_dropout_add_fwd: dr = norm backward at h + dh (the
     gradient of r), dx = dropout(dr) with the forward's mask.  Returns (dx,
     dr, dgamma, dbeta)."""
-    mode = int(mode)
-    dev = _check_x(h)
-    M, N = _rows(h)
-    bf, f32 = torch.bfloat16, torch.float32
-    shape, lead = h.shape, h.shape[:-1]
-    dx = torch.empty_like(h) if dx is None else dx
-    dr = torch.empty_like(h) if dr is None else dr
-    dgamma = torch.empty(N, dtype=f32, device=dev) if dgamma is None else dgamma
-    if mode == LAYER and want_dbeta and dbeta is None:
-        dbeta = torch.empty(N, dtype=f32, device=dev)
-    for t, n in ((dy, "dy"), (dh, "dh"), (h, "h"), (dx, "dx"), (dr, "dr")):
-        _check(t, n, bf, shape, dev)
-    _check(gamma, "gamma", bf, (N,), dev)
-    _check(rstd, "rstd", f32, lead, dev)
-    _check(mean, "mean", f32, lead, dev)
-    _check(dgamma, "dgamma", f32, (N,), dev)
-    _check(dbeta, "dbeta", f32, (N,), dev)
-    if workspace is None:
-        workspace = _scratch("norm_dropout_add_bwd_workspace_bytes",
-                             lib().norm_dropout_add_bwd_workspace_bytes, dev, M, N, mode)
-    _call("norm_dropout_add_bwd", lib().norm_dropout_add_bwd, dev, stream, dy.data_ptr(),
-          dh.data_ptr(), h.data_ptr(), gamma.data_ptr(), rstd.data_ptr(), _addr(mean), M, N, mode,
-          float(p), _u64(seed, "seed"), _u64(offset, "offset"), _offset_dev(offset_dev, dev),
-          dx.data_ptr(), dr.data_ptr(), dgamma.data_ptr(), _addr(dbeta), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
-    return dx, dr, dgamma, dbeta
-
-
-def _group_shape(x):
-    if x.dim() < 2:
-        raise ValueError("x must be [B, ..., C]")
-    B, C = x.shape[0], x.shape[-1]
-    return B, (x.numel() // (B * C) if B and C else 0), C
+    out = (_native_module or _native()).dropout_add_bwd(
+        dy, dh, h, gamma, rstd, mean, mode, p, seed, offset, offset_dev, dx, dr, dgamma, dbeta,
+        want_dbeta, workspace, _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_dropout_add_bwd")
+    return out
 
 
 def norm_group_fwd_workspace_bytes(B, S, C, groups, dtype=BF16) -> int:
@@ -814,34 +730,12 @@ def norm_group_fwd(x, gamma, beta, groups, eps=1e-5, act=ACT_NONE, *, p=0.0, see
     fp32; a torch channels_last [B, C, H, W] tensor is x.permute(0, 2, 3, 1)).
     gamma, beta: [C] of x's type (beta None: zero).  Returns (y, rstd, mean),
     rstd and mean fp32 [B, groups]."""
-    dev = _check_x(x)
-    code = _dtype_code(x)
-    act = _act(act)
-    groups = int(groups)
-    B, S, C = _group_shape(x)
-    dt, f32 = x.dtype, torch.float32
-    if y is None:
-        y = torch.empty_like(x)
-    gs = (B, groups)
-    if rstd is None:
-        rstd = torch.empty(gs, dtype=f32, device=dev)
-    if mean is None:
-        mean = torch.empty(gs, dtype=f32, device=dev)
-    _check(y, "y", dt, x.shape, dev)
-    _check(gamma, "gamma", dt, (C,), dev)
-    _check(beta, "beta", dt, (C,), dev)
-    _check(rstd, "rstd", f32, gs, dev)
-    _check(mean, "mean", f32, gs, dev)
-    L = lib()
-    if workspace is None:
-        workspace = _scratch("norm_group_fwd_workspace_bytes", L.norm_group_fwd_workspace_bytes,
-                             dev, B, S, C, groups, code)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call("norm_group_fwd", L.norm_group_fwd, dev, stream, x.data_ptr(), gamma.data_ptr(),
-          _addr(beta), B, S, C, groups, float(eps), act, code, float(p), _u64(seed, "seed"),
-          _u64(offset, "offset"), _offset_dev(offset_dev, dev), y.data_ptr(), rstd.data_ptr(),
-          mean.data_ptr(), _addr(workspace), nbytes)
-    return y, rstd, mean
+    out = (_native_module or _native()).group_fwd(
+        x, gamma, beta, groups, eps, _act(act), p, seed, offset, offset_dev, y, rstd, mean,
+        workspace, _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_group_fwd")
+    return out
 
 
 def norm_group_bwd(dy, x, gamma, beta, rstd, mean, groups, act=ACT_NONE, *, p=0.0, seed=0,
@@ -850,38 +744,12 @@ def norm_group_bwd(dy, x, gamma, beta, rstd, mean, groups, act=ACT_NONE, *, p=0.
     """Backward of norm_group_fwd from its saved rstd and mean (same beta, act,
     p, seed and offset).  Returns (dx, dgamma, dbeta), dgamma and dbeta fp32
     [C] (dbeta None when want_dbeta is False)."""
-    dev = _check_x(x)
-    code = _dtype_code(x)
-    act = _act(act)
-    groups = int(groups)
-    B, S, C = _group_shape(x)
-    dt, f32 = x.dtype, torch.float32
-    if dx is None:
-        dx = torch.empty_like(x)
-    if dgamma is None:
-        dgamma = torch.empty(C, dtype=f32, device=dev)
-    if want_dbeta and dbeta is None:
-        dbeta = torch.empty(C, dtype=f32, device=dev)
-    gs = (B, groups)
-    _check(dy, "dy", dt, x.shape, dev)
-    _check(gamma, "gamma", dt, (C,), dev)
-    _check(beta, "beta", dt, (C,), dev)
-    _check(rstd, "rstd", f32, gs, dev)
-    _check(mean, "mean", f32, gs, dev)
-    _check(dx, "dx", dt, x.shape, dev)
-    _check(dgamma, "dgamma", f32, (C,), dev)
-    _check(dbeta, "dbeta", f32, (C,), dev)
-    L = lib()
-    if workspace is None:
-        workspace = _scratch("norm_group_bwd_workspace_bytes", L.norm_group_bwd_workspace_bytes,
-                             dev, B, S, C, groups, code)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call("norm_group_bwd", L.norm_group_bwd, dev, stream, dy.data_ptr(), x.data_ptr(),
-          gamma.data_ptr(), _addr(beta), rstd.data_ptr(), mean.data_ptr(), B, S, C, groups, act,
-          code, float(p), _u64(seed, "seed"), _u64(offset, "offset"),
-          _offset_dev(offset_dev, dev), dx.data_ptr(), dgamma.data_ptr(), _addr(dbeta),
-          _addr(workspace), nbytes)
-    return dx, dgamma, dbeta
+    out = (_native_module or _native()).group_bwd(
+        dy, x, gamma, beta, rstd, mean, groups, _act(act), p, seed, offset, offset_dev, dx,
+        dgamma, dbeta, want_dbeta, workspace, _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_group_bwd")
+    return out
 
 
 def norm_group_plan(B, S, C, groups, dtype=BF16, backward=False, sm_count=0, smem_optin=0) -> dict:
