@@ -301,10 +301,12 @@ norm_status_t norm_dropout_add_bwd(const void *dy, const void *dh, const void *h
  * <= B <= 2^24, 1 <= S <= 2^30, B * S <= 2^40 (else NORM_ERR_SHAPE); every
  * pointer 16-byte aligned; outputs must not alias inputs.  Unknown act or
  * dtype: NORM_ERR_ARG.
- * One kernel where a cluster of up to 8 CTAs holds the samples' slabs in
- * shared memory (x, and dy, read once), two where the sample is read twice;
- * the backward adds a fixed-order reduction of dgamma / dbeta unless a single
- * partial row is left.
+ * Small samples take one kernel whose clusters of up to 8 CTAs hold slabs of
+ * them in shared memory (the backward of several samples adds a fixed-order
+ * reduction of dgamma / dbeta); large ones one cooperative kernel over the
+ * whole GPU, which waits for its CTAs to see each other's partials; groups
+ * wider than a CTA (lcm(C / groups, 8) channels above 512 16-byte chunks) a
+ * statistics and an output kernel.
  */
 #define NORM_MAX_GROUP_C 8192
 
@@ -338,15 +340,20 @@ norm_status_t norm_group_bwd(const void *dy, const void *x, const void *gamma,
  * norm_group_bwd (1) of a shape; sm_count and smem_optin_bytes as norm_plan.
  */
 typedef struct {
-    int32_t streamed;        /* 0: one kernel, data resident in shared memory;
-                                1: a statistics and an output kernel */
-    int32_t groups_per_slab; /* groups a cluster owns of one sample */
+    int32_t form;            /* 0 resident: one kernel, clusters hold slabs of
+                                a sample in shared memory; 1 streamed: a
+                                statistics and an output kernel; 2 ring: one
+                                cooperative kernel over the whole GPU */
+    int32_t groups_per_slab; /* groups a cluster (CTA) owns of one sample */
     int32_t slabs;           /* per sample */
     int32_t chunk_columns;   /* 16-byte columns per slab (streamed: per CTA) */
-    int32_t cluster;         /* CTAs sharing a slab's rows */
+    int32_t cluster;         /* resident: CTAs sharing a slab's rows */
     int32_t row_lanes;       /* rows a CTA works on side by side */
     int32_t rows_per_thread; /* resident: rows a thread holds (at most) */
-    int32_t row_splits;      /* streamed: row ranges per sample */
+    int32_t row_splits;      /* streamed, ring: row ranges per sample */
+    int32_t stages;          /* ring: tiles in shared memory */
+    int32_t samples_per_round; /* ring */
+    int32_t rounds;          /* ring */
     int32_t threads;         /* CTA size */
     int32_t smem_bytes;      /* dynamic shared memory per CTA */
     int32_t grid;            /* CTAs launched */

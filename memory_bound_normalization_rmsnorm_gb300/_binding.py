@@ -65,9 +65,9 @@ class Plan(ctypes.Structure):
 class GroupPlan(ctypes.Structure):
     """Mirror of norm_group_plan_t."""
     _fields_ = [(n, ctypes.c_int32) for n in
-                ("streamed", "groups_per_slab", "slabs", "chunk_columns", "cluster", "row_lanes",
-                 "rows_per_thread", "row_splits", "threads", "smem_bytes", "grid")
-                ] + [("workspace_bytes", ctypes.c_int64)]
+                ("form", "groups_per_slab", "slabs", "chunk_columns", "cluster", "row_lanes",
+                 "rows_per_thread", "row_splits", "stages", "samples_per_round", "rounds",
+                 "threads", "smem_bytes", "grid")] + [("workspace_bytes", ctypes.c_int64)]
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_}

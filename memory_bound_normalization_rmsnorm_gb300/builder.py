@@ -31,7 +31,8 @@ LIB = os.path.join(OUT_DIR, "libgbnorm.so")
 TORCH_LIB = os.path.join(OUT_DIR, "gbnorm_torch.so")
 SOURCES = ["fwd.cu", "fwd_fp8.cu", "fwd_gsm.cu", "bwd.cu", "long.cu", "long_resid.cu",
            "long_fp8.cu", "split.cu", "stream.cu", "api.cu", "host.cu", "gemm.cu", "dropout.cu",
-           "drop_add.cu", "group_fwd.cu", "group_bwd.cu", "group.cu"]
+           "drop_add.cu", "group_fwd.cu", "group_bwd.cu", "group_ring.cu",
+           "group.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1240,6 +1240,25 @@ norm_status_t launch_serial(const void *fn, dim3 grid, dim3 block, size_t smem, 
   return NORM_OK;
 }
 
+norm_status_t launch_cooperative(const void *fn, dim3 grid, dim3 block, size_t smem, void **args,
+                                 cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    cudaGetLastError();
+    return NORM_ERR_CUDA;
+  }
+  return NORM_OK;
+}
+
 }  // namespace gbn
 
 // ---------------------------------------------------------------------------

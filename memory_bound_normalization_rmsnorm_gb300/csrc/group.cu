@@ -21,19 +21,23 @@
 namespace gbn {
 namespace {
 
+constexpr int kResident = 0, kStreamed = 1, kRing = 2;
+
 struct GroupPlan {
-  bool streamed = false;
+  int form = kResident;
   int sg = 0, ncs = 0, nslab = 1, k = 1, R = 1, slots = 0, splits = 1;
+  int stages = 0, nsamp = 0, rounds = 0;  // ring
   int threads = 0;
   int64_t grid = 0;
-  uint32_t smem = 0;  // resident kernel, or the streamed form's first pass
+  uint32_t smem = 0;  // resident or ring kernel, or the streamed form's first pass
   uint32_t smem2 = 0; // streamed form's second pass
 };
 
 // Shape override for sweeps and tests: GBNORM_GROUP="form=1,sg=4,k=2,R=8,
-// splits=3" (any subset; form 0 resident, 1 streamed).  Bypasses the cache.
+// splits=3" (any subset; form 0 resident, 1 streamed, 2 ring; for the ring
+// also stages= and nsamp=).  Bypasses the cache.
 struct GroupOverride {
-  int form = -1, sg = 0, k = 0, R = 0, splits = 0;
+  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0;
   bool any = false;
 };
 
@@ -49,6 +53,8 @@ GroupOverride read_group_override() {
       else if (!std::strcmp(key, "k")) o.k = val;
       else if (!std::strcmp(key, "R")) o.R = val;
       else if (!std::strcmp(key, "splits")) o.splits = val;
+      else if (!std::strcmp(key, "stages")) o.stages = val;
+      else if (!std::strcmp(key, "nsamp")) o.nsamp = val;
       o.any = true;
     }
     s = std::strchr(s, ',');
@@ -81,10 +87,70 @@ double resident_cost(const GroupPlan &p, int64_t bytes, int seg_bytes, int sms, 
   return bytes / rate + waves * 2.5 + (p.k > 1 ? 0.7 : 0.0);
 }
 
-double stream_cost(int64_t bytes, int64_t read_bytes, bool bwd) {
-  const double l2 = 60e6;  // re-read bytes that L2 still holds
-  const double again = read_bytes <= l2 ? 0.35 * read_bytes : read_bytes - 0.65 * l2;
-  return (bytes + again) / 6.6e6 + (bwd ? 7.5 : 5.0);
+// Bytes of the first pass that are still near (shared memory and L2) when
+// the output pass comes to them.
+constexpr double kNearBytes = 80e6;
+
+double ring_cost(const GroupPlan &p, int64_t bytes, int64_t read_bytes, int sms) {
+  const double per_round = static_cast<double>(read_bytes) / p.rounds;
+  const double again = std::max(0.0, per_round - kNearBytes) * p.rounds;
+  const double used = static_cast<double>(p.grid) / sms;
+  return (bytes + again) / (6.6e6 * std::min(1.0, used / 0.7)) + 3.0 * p.rounds + 4.0;
+}
+
+// Ring plan (group_ring.cu): slabs as wide as a CTA has threads for (whole
+// rows where they fit), as many stages as shared memory holds, and rounds of
+// as many samples as stay near.
+norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int sms, int smem_optin,
+                             const GroupOverride &ov, GroupPlan *out) {
+  const int V = chunk_elems(dt), es = elem_bytes(dt), nt = bwd ? 2 : 1;
+  const int D = C / G, nc = C / V;
+  const int sgu = 8 / std::gcd(D, 8);
+  const int64_t unit = static_cast<int64_t>(sgu) * D / V;  // chunks of the narrowest slab
+  GroupPlan p;
+  p.form = kRing;
+  if (nc <= kGroupThreads && !ov.sg) {
+    p.sg = G;
+  } else {
+    if (unit > kGroupThreads) return NORM_ERR_UNSUPPORTED;
+    p.sg = ov.sg ? ov.sg : static_cast<int>(std::min<int64_t>(G, kGroupThreads / unit * sgu));
+    if (p.sg < 1 || p.sg > G || p.sg % sgu || static_cast<int64_t>(p.sg) * D / V > kGroupThreads)
+      return NORM_ERR_UNSUPPORTED;
+  }
+  p.ncs = p.sg * D / V;
+  p.nslab = (G + p.sg - 1) / p.sg;
+  const int U = nt == 1 ? 4 : 2;
+  p.R = std::max(1, std::min(kGroupThreads / p.ncs, (S + U - 1) / U));
+  if (ov.R) p.R = std::min(p.R, ov.R);
+  p.threads = round32(p.ncs * p.R);
+  const int TR = U * p.R;
+  const int64_t sample = static_cast<int64_t>(S) * C * es * nt;
+  int64_t n = std::max<int64_t>(1, static_cast<int64_t>(kNearBytes * 0.8) / sample);
+  if (ov.nsamp) n = ov.nsamp;
+  n = std::min<int64_t>(n, std::min(B, sms / p.nslab));
+  if (n < 1) return NORM_ERR_UNSUPPORTED;
+  p.rounds = static_cast<int>((B + n - 1) / n);
+  p.nsamp = (B + p.rounds - 1) / p.rounds;
+  const int tiles = (S + TR - 1) / TR;
+  p.splits = std::max(1, std::min({sms / (p.nsamp * p.nslab), tiles, kGroupRingSplits}));
+  if (ov.splits) p.splits = std::max(1, std::min({ov.splits, S, p.splits}));
+  int stages = 31;
+  while (stages >= 2 &&
+         static_cast<int64_t>(group_ring_layout(stages, U, p.R, p.ncs, V, p.sg, bwd).total) >
+             smem_optin)
+    --stages;
+  if (ov.stages) stages = std::min(stages, ov.stages);
+  // The stages turn over in full between rounds: no CTA may have fewer tiles
+  // than stages.
+  if (p.rounds > 1) stages = std::min(stages, (S / p.splits + TR - 1) / TR);
+  stages = std::min(stages, (static_cast<int>(ceil_div64(S, p.splits)) + TR - 1) / TR);
+  if (stages < 1) return NORM_ERR_UNSUPPORTED;
+  p.stages = stages;
+  p.smem = group_ring_layout(stages, U, p.R, p.ncs, V, p.sg, bwd).total;
+  if (static_cast<int64_t>(p.smem) > smem_optin) return NORM_ERR_UNSUPPORTED;
+  p.grid = static_cast<int64_t>(p.nsamp) * p.nslab * p.splits;
+  *out = p;
+  return NORM_OK;
 }
 
 norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int sms,
@@ -100,7 +166,7 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
   // slab starts on a 16-byte boundary in every type), clusters of 1 to 8.
   const int sgu = 8 / std::gcd(D, 8);
   const int nu = G / sgu;
-  if (ov.form != 1) {
+  if (ov.form < 1) {
     int last = 0;
     for (int t = 1; t <= nu; ++t) {
       const int sg = ((nu + t - 1) / t) * sgu;
@@ -138,9 +204,22 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
     }
     if (ov.form == 0 && best_cost < 0) return NORM_ERR_UNSUPPORTED;
   }
-  if (ov.form != 0 && (best_cost < 0 || stream_cost(bytes, n * es * nt, bwd) < best_cost)) {
+  if (ov.form < 0 || ov.form == 2) {
     GroupPlan p;
-    p.streamed = true;
+    const norm_status_t st = make_ring_plan(B, S, C, G, dt, bwd, sms, smem_optin, ov, &p);
+    if (st != NORM_OK && ov.form == 2) return st;
+    if (st == NORM_OK) {
+      const double c = ring_cost(p, bytes, n * es * nt, sms);
+      if (best_cost < 0 || c < best_cost) {
+        best_cost = c;
+        best = p;
+      }
+    }
+  }
+  // Streamed: groups too wide for the others.
+  if (best_cost < 0) {
+    GroupPlan p;
+    p.form = kStreamed;
     p.sg = G;
     p.ncs = std::min(nc, kGroupThreads);
     const int rmax = std::max(1, std::min(kGroupThreads / p.ncs, S));
@@ -206,7 +285,8 @@ norm_status_t check_group(int64_t B, int64_t S, int64_t C, int64_t G, norm_dtype
   return NORM_OK;
 }
 
-// Workspace regions (bytes from its start): the streamed form's group pairs,
+// Workspace regions (bytes from its start): the group pairs of the streamed
+// and ring forms,
 // then the backward's partial rows (dgamma, dbeta).
 struct GroupWs {
   size_t cpart = 0, total = 0;
@@ -214,11 +294,15 @@ struct GroupWs {
 };
 GroupWs group_ws(const GroupPlan &p, int64_t B, int64_t C, int64_t G, bool bwd) {
   GroupWs w;
-  if (p.streamed) w.cpart = (static_cast<size_t>(p.grid) * G * 8 + 15) & ~size_t(15);
+  if (p.form == kStreamed) w.cpart = static_cast<size_t>(p.grid) * G * 8;
+  if (p.form == kRing) w.cpart = static_cast<size_t>(B) * G * p.splits * 8;
+  w.cpart = (w.cpart + 15) & ~size_t(15);
   w.total = w.cpart;
   if (bwd) {
-    w.P = static_cast<int>(p.streamed ? p.grid : B);
-    if (w.P > 1) w.total += static_cast<size_t>(w.P) * C * 8;
+    w.P = static_cast<int>(p.form == kStreamed ? p.grid
+                           : p.form == kRing   ? static_cast<int64_t>(p.nsamp) * p.splits
+                                               : B);
+    if (w.P > 1 || p.form == kRing) w.total += static_cast<size_t>(w.P) * C * 8;
   }
   return w;
 }
@@ -239,6 +323,10 @@ GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_
   a.R = p.R;
   a.slots = p.slots;
   a.splits = p.splits;
+  a.stages = p.stages;
+  a.nsamp = p.nsamp;
+  a.rounds = p.rounds;
+  while ((p.sg << (a.lsh + 1)) <= p.threads && a.lsh < 5) ++a.lsh;
   return a;
 }
 
@@ -249,6 +337,18 @@ norm_status_t run(int dev, int optin, const void *fn, const GroupPlan &p, uint32
   void *args[] = {&a};
   return launch_serial(fn, dim3(static_cast<unsigned>(p.grid)), dim3(p.threads), smem, cluster,
                        args, s);
+}
+
+norm_status_t run_ring(int dev, int optin, const GroupPlan &p, int dt, int act, bool drop, bool bwd,
+                       unsigned *err, GroupArgs &a, cudaStream_t s) {
+  const void *fn = group_ring_kernel_ptr(dt, act, drop, bwd);
+  norm_status_t st = function_ready(dev, fn, optin);
+  if (st != NORM_OK) return st;
+  a.U = bwd ? 2 : 4;
+  a.err = err;
+  void *args[] = {&a};
+  return launch_cooperative(fn, dim3(static_cast<unsigned>(p.grid)), dim3(p.threads), p.smem, args,
+                            s);
 }
 
 norm_status_t group_workspace(int64_t B, int64_t S, int64_t C, int64_t G, norm_dtype_t dtype,
@@ -316,7 +416,8 @@ norm_status_t norm_group_fwd(const void *x, const void *gamma, const void *beta,
   a.eps = eps;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool dropping = drop.thr != 0;
-  if (!pl.streamed)
+  if (pl.form == kRing) return run_ring(dev, optin, pl, dtype, act, dropping, false, err, a, s);
+  if (pl.form == kResident)
     return run(dev, optin, group_fwd_kernel_ptr(dtype, act, dropping), pl, pl.smem, pl.k, a, s);
   if ((st = run(dev, optin, group_stats_kernel_ptr(dtype), pl, pl.smem, 1, a, s)) != NORM_OK)
     return st;
@@ -355,13 +456,16 @@ norm_status_t norm_group_bwd(const void *dy, const void *x, const void *gamma, c
   a.rstd = const_cast<float *>(rstd);
   a.gpart = static_cast<float *>(workspace);
   a.drop = drop;
-  float *rows = w.P > 1 ? reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.cpart)
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  float *rows = w.P > 1 || pl.form == kRing ? reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + w.cpart)
                         : nullptr;
   a.cpart = rows ? rows : dgamma;
   a.dbeta_part = !dbeta ? nullptr : rows ? rows + static_cast<size_t>(w.P) * C : dbeta;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool dropping = drop.thr != 0;
-  if (!pl.streamed) {
+  if (pl.form == kRing) return run_ring(dev, optin, pl, dtype, act, dropping, true, err, a, s);
+  if (pl.form == kResident) {
     st = run(dev, optin, group_bwd_kernel_ptr(dtype, act, dropping), pl, pl.smem, pl.k, a, s);
   } else {
     st = run(dev, optin, group_sums_kernel_ptr(dtype, act, dropping), pl, pl.smem, 1, a, s);
@@ -392,7 +496,7 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups, n
     st = group_plan(dev, sms, optin, B, S, C, groups, dtype, backward != 0, &p);
   }
   if (st != NORM_OK) return st;
-  out->streamed = p.streamed ? 1 : 0;
+  out->form = p.form;
   out->groups_per_slab = p.sg;
   out->slabs = p.nslab;
   out->chunk_columns = p.ncs;
@@ -400,6 +504,9 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups, n
   out->row_lanes = p.R;
   out->rows_per_thread = p.slots;
   out->row_splits = p.splits;
+  out->stages = p.stages;
+  out->samples_per_round = p.nsamp;
+  out->rounds = p.rounds;
   out->threads = p.threads;
   out->smem_bytes = static_cast<int32_t>(p.smem);
   out->grid = static_cast<int32_t>(p.grid);

@@ -9,13 +9,15 @@
 // are per channel whatever D is; channels meet in groups only after the rows
 // are folded.
 //
-// Two forms.  Resident: a cluster of k CTAs owns a slab of whole groups of
-// one sample, each CTA a range of its rows, copied once into shared memory
-// (each thread reads back only the chunks that it copied itself: the copy
-// needs no barrier), so x (and dy) is read from HBM once.  Streamed: the
-// sample is read twice, by a statistics kernel and an output kernel whose
-// CTAs own the same row ranges and walk them in opposite directions, so the
-// second read starts with what the first left in L2.
+// Three forms.  Resident, for small samples: a cluster of k CTAs owns a slab
+// of whole groups of one sample, each CTA a range of its rows, copied once
+// into shared memory (each thread reads back only the chunks that it copied
+// itself: the copy needs no barrier), so x (and dy) is read from HBM once.
+// Ring, for large samples: one cooperative kernel over the whole GPU whose
+// CTAs keep what fits of their rows in shared memory between the statistics
+// and the output pass and read the rest again, newest first, out of L2
+// (group_ring.cu).  Streamed, for groups wider than a CTA: a statistics and
+// an output kernel over the same row ranges, walked in opposite directions.
 #pragma once
 #include "dropout.cuh"
 
@@ -39,6 +41,8 @@ struct GroupArgs {
   float *gpart;       // streamed: per-(sample, split, group) pairs [B, splits, G, 2]
   float *cpart;       // backward: per-channel partial rows [P, C] (dgamma), then [P, C] (dbeta)
   float *dbeta_part;  // backward: where the dbeta rows start, or null
+  float *dgamma;      // ring backward: [C] outputs (dbeta may be null)
+  float *dbeta;
   DropArgs drop;
   int B, S, C, G, D;
   int nc;      // 16-byte chunks per row
@@ -48,57 +52,152 @@ struct GroupArgs {
   int k;       // CTAs per cluster (row split of a unit)
   int R;       // row lanes per CTA
   int slots;   // resident: rows per thread (at most)
-  int splits;  // streamed: row ranges per sample
+  int splits;  // streamed and ring: row ranges per sample
+  int lsh;     // log2 of the lanes that share a group in the folds
+  int U;       // ring: rows per thread and tile
+  int stages;  // ring: tiles in shared memory
+  int nsamp;   // ring: samples per round
+  int rounds;  // ring: ceil(B / nsamp)
+  unsigned *err;  // device error word
   float eps;
 };
 
-// Shared memory after the resident data: the fold buffers (also the
-// per-channel arrays, which are written after the folds), then two float2
-// per group of the slab.
+// Shared memory after the resident data: the fold buffer (V pairs and a count
+// per slot, half of R slots per column; a single row lane needs none), the
+// two per-channel arrays, then two float2 per group of the slab.
 __host__ __device__ inline uint32_t group_fold_bytes(int R, int ncs, int V) {
-  const uint32_t tree = static_cast<uint32_t>(R / 2) * static_cast<uint32_t>(ncs) *
-                        (static_cast<uint32_t>(V) * 8u + 4u);
-  const uint32_t chan = static_cast<uint32_t>(ncs) * static_cast<uint32_t>(V) * 8u;
-  return ((tree > chan ? tree : chan) + 15u) & ~15u;
+  if (R == 1) return 0;
+  const uint32_t slots = static_cast<uint32_t>((R + 1) / 2) * static_cast<uint32_t>(ncs);
+  return (slots * (static_cast<uint32_t>(V) * 8u + 4u) + 15u) & ~15u;
+}
+__host__ __device__ inline uint32_t group_chan_bytes(int ncs, int V) {
+  return static_cast<uint32_t>(ncs * V) * 8u;
+}
+// The ring kernels: `stages` tiles of U * R rows (one per tensor), the fold
+// buffer, the per-channel arrays, the backward's running per-channel totals,
+// a float2 per group of the slab, the stage mbarriers, and the abort flag
+// with the per-stage warp counters.
+constexpr int kGroupRingSplits = 192;  // row ranges of a sample, at most
+struct GroupRingLayout {
+  uint32_t tensor_bytes, stage_bytes, fold_off, chan_off, tot_off, gst_off, bar_off, flag_off,
+      total;
+};
+__host__ __device__ inline GroupRingLayout group_ring_layout(int stages, int U, int R, int ncs,
+                                                             int V, int sg, bool bwd) {
+  GroupRingLayout L;
+  L.tensor_bytes = static_cast<uint32_t>(U * R * ncs) * 16u;
+  L.stage_bytes = L.tensor_bytes * (bwd ? 2u : 1u);
+  L.fold_off = L.stage_bytes * static_cast<uint32_t>(stages);
+  L.chan_off = L.fold_off + group_fold_bytes(R, ncs, V);
+  // (the backward's column sums need a float per thread from fold_off on)
+  if (bwd && L.chan_off < L.fold_off + 4u * kGroupThreads)
+    L.chan_off = L.fold_off + 4u * kGroupThreads;
+  L.tot_off = L.chan_off + group_chan_bytes(ncs, V);
+  L.gst_off = L.tot_off + (bwd ? group_chan_bytes(ncs, V) : 0u);
+  L.bar_off = L.gst_off + static_cast<uint32_t>(sg) * 8u;
+  L.flag_off = L.bar_off + 8u * static_cast<uint32_t>(stages);
+  L.total = align16(L.flag_off + 4u + 4u * static_cast<uint32_t>(stages));
+  return L;
 }
 __host__ __device__ inline uint32_t group_smem_bytes(int slots, int ntensors, int R, int ncs, int V,
                                                      int sg) {
   return static_cast<uint32_t>(slots) * static_cast<uint32_t>(ncs * R) * 16u *
              static_cast<uint32_t>(ntensors) +
-         group_fold_bytes(R, ncs, V) + static_cast<uint32_t>(sg) * 16u;
+         group_fold_bytes(R, ncs, V) + group_chan_bytes(ncs, V) + static_cast<uint32_t>(sg) * 16u;
 }
 
 // ---------------------------------------------------------- activation
-__device__ __forceinline__ float sigmoid_fast(float k) {
-  // exp(-k) overflows to infinity for k below -88, and 1 / infinity is 0.
-  return __fdividef(1.0f, 1.0f + __expf(-k));
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// s = sigmoid(k) and e = exp(-k) (so 1 - s = e s, without cancellation) of the
+// same two channels in two rows, a and b: one reciprocal of (1 + e_a)(1 + e_b)
+// serves both rows, six special-function operations instead of eight (their
+// rate, 16 a cycle and SM, bounds the passes that take an activation).  Rows
+// of one channel share a group, so a NaN that reaches the other row through
+// the product finds it NaN already (the group's statistics are).  Needs k >=
+// -43.6, which keeps the product finite.
+__device__ __forceinline__ void sigmoid_rows(float2 ka, float2 kb, float2 &sa, float2 &sb,
+                                             float2 &ea, float2 &eb) {
+  const float2 ta = mul2(ka, splat2(-1.4426950408889634f));
+  const float2 tb = mul2(kb, splat2(-1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ea.x) : "f"(ta.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ea.y) : "f"(ta.y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(eb.x) : "f"(tb.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(eb.y) : "f"(tb.y));
+  const float2 da = add2(ea, splat2(1.f)), db = add2(eb, splat2(1.f));
+  const float2 p = mul2(da, db);
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(p.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(p.y));
+  sa = mul2(db, r);
+  sb = mul2(da, r);
 }
 
 constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
+// Arguments are clamped below where act(z) has fallen to 5e-18 (there it
+// stays: 18 orders below the argument), and for GELU's derivative above
+// where it is 1, so that z^3 cannot overflow into it.
+constexpr float kSiluMin = -43.6f;
+constexpr float kGeluMin = -7.6f;  // k = -43.4
+constexpr float kGeluMax = 12.0f;
+
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float z) {
-  if constexpr (ACT == kActNone) return z;
-  if constexpr (ACT == kActSilu) return z * sigmoid_fast(z);
-  const float k = z * fmaf(kGeluC * kGeluA * z, z, kGeluC);
-  return z * sigmoid_fast(k);
+__device__ __forceinline__ float2 clamp_low(float2 z) {
+  constexpr float lo = ACT == kActSilu ? kSiluMin : kGeluMin;
+  return make_float2(max_nan(z.x, lo), max_nan(z.y, lo));
 }
 
-// act'(z) = s + z s (1 - s) k'(z), s = sigmoid(k(z)).  Where s (1 - s) has
-// rounded to 0 the second term is 0, though z k'(z) may be infinite there.
+// k(z) of a clamped argument.
 template <int ACT>
-__device__ __forceinline__ float act_grad(float z) {
-  if constexpr (ACT == kActNone) return 1.0f;
-  if constexpr (ACT == kActSilu) {
-    const float s = sigmoid_fast(z);
-    return fmaf(z * s, 1.0f - s, s);
+__device__ __forceinline__ float2 act_arg(float2 z) {
+  if constexpr (ACT == kActSilu) return z;
+  return mul2(z, fma2(mul2(z, z), splat2(kGeluC * kGeluA), splat2(kGeluC)));
+}
+
+// a, b: z of the same two channels in two rows, replaced by act(z).
+template <int ACT>
+__device__ __forceinline__ void act_rows(float2 &a, float2 &b) {
+  if constexpr (ACT != kActNone) {
+    a = clamp_low<ACT>(a);
+    b = clamp_low<ACT>(b);
+    float2 sa, sb, ea, eb;
+    sigmoid_rows(act_arg<ACT>(a), act_arg<ACT>(b), sa, sb, ea, eb);
+    a = mul2(a, sa);
+    b = mul2(b, sb);
   }
-  const float z2 = z * z;
-  const float s = sigmoid_fast(z * fmaf(kGeluC * kGeluA, z2, kGeluC));
-  const float t = s * (1.0f - s);
-  const float zk = z * fmaf(3.0f * kGeluC * kGeluA, z2, kGeluC);
-  return t == 0.0f ? s : fmaf(zk, t, s);
+}
+
+// a, b: z, replaced by act'(z) = s + z s (1 - s) k'(z), s = sigmoid(k(z)).
+template <int ACT>
+__device__ __forceinline__ void act_grad_rows(float2 &a, float2 &b) {
+  a = clamp_low<ACT>(a);
+  b = clamp_low<ACT>(b);
+  float2 sa, sb, ea, eb;
+  if constexpr (ACT == kActSilu) {
+    sigmoid_rows(a, b, sa, sb, ea, eb);
+    a = fma2(mul2(a, sa), mul2(ea, sa), sa);
+    b = fma2(mul2(b, sb), mul2(eb, sb), sb);
+  } else {
+    a = make_float2(min_nan(a.x, kGeluMax), min_nan(a.y, kGeluMax));
+    b = make_float2(min_nan(b.x, kGeluMax), min_nan(b.y, kGeluMax));
+    const float2 c1 = splat2(kGeluC), c3 = splat2(kGeluC * kGeluA),
+                 c9 = splat2(3.0f * kGeluC * kGeluA);
+    const float2 a2 = mul2(a, a), b2 = mul2(b, b);
+    sigmoid_rows(mul2(a, fma2(a2, c3, c1)), mul2(b, fma2(b2, c3, c1)), sa, sb, ea, eb);
+    a = fma2(mul2(mul2(a, fma2(a2, c9, c1)), sa), mul2(ea, sa), sa);
+    b = fma2(mul2(mul2(b, fma2(b2, c9, c1)), sb), mul2(eb, sb), sb);
+  }
 }
 
 // ------------------------------------------------- asynchronous copies
@@ -225,75 +324,219 @@ __device__ __forceinline__ void get_pairs(const float4 *buf, int cap, int slot, 
   }
 }
 
-// Folds the R row lanes of each chunk column into lane 0, pairwise in a
-// fixed order.  Called by every thread of the CTA; `on`: the thread owns a
-// chunk column.  Ends with a barrier.
-template <int V>
-__device__ __forceinline__ void fold_stats(ChannelStats<V> &st, unsigned char *buf, int R, int rl,
-                                           int cc, int ncs, bool on) {
-  float4 *f4 = reinterpret_cast<float4 *>(buf);
-  const int cap = (R / 2) * ncs;
-  float *cnt = reinterpret_cast<float *>(f4 + (V / 2) * cap);
-  for (int r = R; r > 1;) {
-    const int h = (r + 1) >> 1;
-    if (on && rl >= h && rl < r) {
-      put_pairs<V>(f4, cap, (rl - h) * ncs + cc, st.m, st.q);
-      cnt[(rl - h) * ncs + cc] = st.n;
-    }
-    __syncthreads();
-    if (on && rl < r - h) {
-      float2 mb[V / 2], qb[V / 2];
-      get_pairs<V>(f4, cap, rl * ncs + cc, mb, qb);
-      st.merge(mb, qb, cnt[rl * ncs + cc]);
-    }
-    __syncthreads();
-    r = h;
-  }
-}
-template <int V>
-__device__ __forceinline__ void fold_sums(float2 (&a)[V / 2], float2 (&b)[V / 2],
-                                          unsigned char *buf, int R, int rl, int cc, int ncs,
-                                          bool on) {
-  float4 *f4 = reinterpret_cast<float4 *>(buf);
-  const int cap = (R / 2) * ncs;
-  for (int r = R; r > 1;) {
-    const int h = (r + 1) >> 1;
-    if (on && rl >= h && rl < r) put_pairs<V>(f4, cap, (rl - h) * ncs + cc, a, b);
-    __syncthreads();
-    if (on && rl < r - h) {
-      float2 ao[V / 2], bo[V / 2];
-      get_pairs<V>(f4, cap, rl * ncs + cc, ao, bo);
-#pragma unroll
-      for (int p = 0; p < V / 2; ++p) {
-        a[p] = add2(a[p], ao[p]);
-        b[p] = add2(b[p], bo[p]);
-      }
-    }
-    __syncthreads();
-    r = h;
-  }
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// (mean, M2) of a group from the (mean, M2) of its D channels over n rows
-// each, by one warp; every lane returns the result.
-__device__ __forceinline__ float2 group_of_channels(const float *chm, const float *chq, int D,
-                                                    float n) {
-  const int lane = threadIdx.x & 31;
-  float s = 0.f;
-  for (int j = lane; j < D; j += 32) s += chm[j];
-  const float gm = warp_sum(s) / static_cast<float>(D);
-  float q = 0.f;
-  for (int j = lane; j < D; j += 32) {
-    const float e = chm[j] - gm;
-    q += fmaf(n * e, e, chq[j]);
+// Row lanes that the pairwise folds leave: few enough for the loops over
+// them that follow, at most half of R, rounded up (the slots per column that
+// the buffer holds).
+constexpr int kFoldLanes = 8;
+__host__ __device__ inline int fold_lanes(int R) {
+  if (R == 1) return 1;
+  do R = (R + 1) / 2;
+  while (R > kFoldLanes);
+  return R;
+}
+
+// Folds the R > 1 row lanes of each chunk column pairwise, in a fixed order, to
+// fold_lanes(R), and leaves those in the buffer: lane l of column cc in slot l
+// * ncs + cc (see put_pairs; a partner's slot is the one its sum goes back
+// to).  Called by every thread of the CTA; `on`: the thread owns a chunk
+// column.  Ends with a barrier.  `merge(slot)` adds the partial in a slot to
+// the thread's, `put(slot)` writes the thread's there.
+template <typename Merge, typename Put>
+__device__ __forceinline__ void fold_rows(int R, int rl, int cc, int ncs, bool on, Merge merge,
+                                          Put put) {
+  int r = R;
+  const int left = fold_lanes(R);
+  while (r > left) {
+    const int h = (r + 1) >> 1;
+    if (r < R) __syncthreads();  // the slots of the last level have been read
+    if (on && rl >= h && rl < r) put((rl - h) * ncs + cc);
+    __syncthreads();
+    if (on && rl < r - h) merge(rl * ncs + cc);
+    r = h;
   }
-  return make_float2(gm, warp_sum(q));
+  // (an odd level's middle lane had no partner, so no slot was read there)
+  if (on && rl < r) put(rl * ncs + cc);
+  __syncthreads();
+}
+
+// Where value v of a slot lies in the buffer of put_pairs (first array: b =
+// 0, second: 1).
+template <int V>
+__device__ __forceinline__ int pair_at(int cap, int slot, int v, int b) {
+  return ((b * (V / 4) + (v >> 2)) * cap + slot) * 4 + (v & 3);
+}
+// Slots per column in the fold buffer.
+__host__ __device__ inline int fold_slots(int R) { return (R + 1) / 2; }
+
+template <int V>
+__device__ __forceinline__ void fold_stats(ChannelStats<V> &st, unsigned char *buf, int R, int rl,
+                                           int cc, int ncs, bool on) {
+  float4 *f4 = reinterpret_cast<float4 *>(buf);
+  const int cap = fold_slots(R) * ncs;
+  float *cnt = reinterpret_cast<float *>(f4 + (V / 2) * cap);
+  fold_rows(
+      R, rl, cc, ncs, on,
+      [&](int slot) {
+        float2 mb[V / 2], qb[V / 2];
+        get_pairs<V>(f4, cap, slot, mb, qb);
+        st.merge(mb, qb, cnt[slot]);
+      },
+      [&](int slot) {
+        put_pairs<V>(f4, cap, slot, st.m, st.q);
+        cnt[slot] = st.n;
+      });
+}
+template <int V>
+__device__ __forceinline__ void fold_sums(float2 (&a)[V / 2], float2 (&b)[V / 2],
+                                          unsigned char *buf, int R, int rl, int cc, int ncs,
+                                          bool on) {
+  float4 *f4 = reinterpret_cast<float4 *>(buf);
+  const int cap = fold_slots(R) * ncs;
+  fold_rows(
+      R, rl, cc, ncs, on,
+      [&](int slot) {
+        float2 ao[V / 2], bo[V / 2];
+        get_pairs<V>(f4, cap, slot, ao, bo);
+#pragma unroll
+        for (int p = 0; p < V / 2; ++p) {
+          a[p] = add2(a[p], ao[p]);
+          b[p] = add2(b[p], bo[p]);
+        }
+      },
+      [&](int slot) { put_pairs<V>(f4, cap, slot, a, b); });
+}
+
+// Row statistics of a CTA's threads -> (mean, M2) of each channel of the slab
+// over the CTA's `nrow` rows (chm, chq; `nch` channels).  Called by all
+// threads; the arrays are complete after the next barrier.
+template <int V>
+__device__ __forceinline__ void channel_stats(ChannelStats<V> &st, unsigned char *buf, float *chm,
+                                              float *chq, int R, int rl, int cc, int ncs, bool on,
+                                              int nch, int nrow) {
+  if (R == 1) {
+    if (on) {
+#pragma unroll
+      for (int p = 0; p < V / 2; ++p) {
+        *reinterpret_cast<float2 *>(chm + cc * V + 2 * p) = st.m[p];
+        *reinterpret_cast<float2 *>(chq + cc * V + 2 * p) = st.q[p];
+      }
+    }
+    return;
+  }
+  fold_stats<V>(st, buf, R, rl, cc, ncs, on);
+  const int cap = fold_slots(R) * ncs, rows = fold_lanes(R);
+  const float *f = reinterpret_cast<const float *>(buf);
+  const float *cnt = f + 2 * V * cap;
+  const float inv = 1.0f / static_cast<float>(nrow);
+  for (int j = threadIdx.x; j < nch; j += blockDim.x) {
+    const unsigned u = static_cast<unsigned>(j);
+    const int col = static_cast<int>(u / V), v = static_cast<int>(u % V);
+    const float *fm = f + pair_at<V>(cap, col, v, 0), *fq = f + pair_at<V>(cap, col, v, 1);
+    // the mean first, then the deviations from it: no digit of the variance
+    // is lost
+    float n[kFoldLanes], m[kFoldLanes], mean = 0.f, q = 0.f;
+#pragma unroll
+    for (int r = 0; r < kFoldLanes; ++r) {
+      const bool in = r < rows;
+      n[r] = in ? cnt[r * ncs + col] : 0.f;
+      m[r] = in ? fm[r * ncs * 4] : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < kFoldLanes; ++r)
+      if (r < rows) mean = fmaf(n[r], m[r], mean);
+    mean *= inv;
+#pragma unroll
+    for (int r = 0; r < kFoldLanes; ++r)
+      if (r < rows) q += fmaf(n[r] * (m[r] - mean), m[r] - mean, fq[r * ncs * 4]);
+    chm[j] = mean;
+    chq[j] = q;
+  }
+}
+
+// Sum of per-thread values over each channel of the slab: s1 and s2 of the R
+// row lanes, added up in a fixed order.  Called by all threads; the arrays
+// are complete after the next barrier.
+template <int V>
+__device__ __forceinline__ void channel_sums(float2 (&a)[V / 2], float2 (&b)[V / 2],
+                                             unsigned char *buf, float *ca, float *cb, int R, int rl,
+                                             int cc, int ncs, bool on, int nch) {
+  if (R == 1) {
+    if (on) {
+#pragma unroll
+      for (int p = 0; p < V / 2; ++p) {
+        *reinterpret_cast<float2 *>(ca + cc * V + 2 * p) = a[p];
+        *reinterpret_cast<float2 *>(cb + cc * V + 2 * p) = b[p];
+      }
+    }
+    return;
+  }
+  fold_sums<V>(a, b, buf, R, rl, cc, ncs, on);
+  const int cap = fold_slots(R) * ncs, rows = fold_lanes(R);
+  const float *f = reinterpret_cast<const float *>(buf);
+  for (int j = threadIdx.x; j < nch; j += blockDim.x) {
+    const unsigned u = static_cast<unsigned>(j);
+    const int col = static_cast<int>(u / V), v = static_cast<int>(u % V);
+    const float *fa = f + pair_at<V>(cap, col, v, 0), *fb = f + pair_at<V>(cap, col, v, 1);
+    float sa = fa[0], sb = fb[0];
+#pragma unroll
+    for (int r = 1; r < kFoldLanes; ++r)
+      if (r < rows) {
+        sa += fa[r * ncs * 4];
+        sb += fb[r * ncs * 4];
+      }
+    ca[j] = sa;
+    cb[j] = sb;
+  }
+}
+
+// Sum over the 2^lsh lanes that share a group.
+__device__ __forceinline__ float lanes_sum(float v, int lsh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < (1 << lsh)) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Runs fn(g, lane, valid) with 2^lsh lanes per group, as many groups at a
+// time as the CTA has lanes for: all groups of a slab side by side, so that
+// the latencies of their folds (shared memory, L2, shuffles) overlap.  Every
+// lane of a warp takes part in every step.
+template <typename Fn>
+__device__ __forceinline__ void each_group(int ng, int lsh, Fn fn) {
+  const int per = static_cast<int>(blockDim.x) >> lsh;
+#pragma unroll 1
+  for (int base = 0; base < ng; base += per) {
+    const int g = base + (static_cast<int>(threadIdx.x) >> lsh);
+    fn(g, static_cast<int>(threadIdx.x) & ((1 << lsh) - 1), g < ng);
+  }
+}
+
+// (mean, M2) of every group from the (mean, M2) of its D channels over n rows
+// each, handed to out(g, mean, M2) by one lane per group.
+template <typename Out>
+__device__ __forceinline__ void groups_of_channels(const float *chm, const float *chq, int ng, int D,
+                                                   int lsh, float n, Out out) {
+  const float inv = 1.0f / static_cast<float>(D);
+  each_group(ng, lsh, [&](int g, int l, bool in) {
+    const float *m = chm + g * D, *q = chq + g * D;
+    float s = 0.f, t = 0.f;
+    if (in)
+      for (int j = l; j < D; j += 1 << lsh) s += m[j];
+    const float gm = lanes_sum(s, lsh) * inv;
+    if (in)
+      for (int j = l; j < D; j += 1 << lsh) {
+        const float e = m[j] - gm;
+        t += fmaf(n * e, e, q[j]);
+      }
+    t = lanes_sum(t, lsh);
+    if (in && l == 0) out(g, gm, t);
+  });
 }
 
 // Address of the V-element chunk column cc (within the tensor) of row s of
@@ -303,8 +546,14 @@ __device__ __forceinline__ int64_t group_elem(const GroupArgs &a, int b, int64_t
   return (static_cast<int64_t>(b) * a.S + s) * a.C + static_cast<int64_t>(chunk) * V;
 }
 
-// First row of part i of n equal parts of S rows.
-__host__ __device__ inline int64_t part_begin(int64_t S, int i, int n) { return S * i / n; }
+// S rows cut into n ranges that differ by one row at most, the longer ones
+// first.
+struct Parts {
+  int q, rem;
+  __host__ __device__ Parts(int S, int n) : q(S / n), rem(S % n) {}
+  __host__ __device__ int rows(int i) const { return q + (i < rem ? 1 : 0); }
+  __host__ __device__ int begin(int i) const { return i * q + (i < rem ? i : rem); }
+};
 
 // Parameters of a thread's V channels as fp32 pairs: gamma, beta (0 when
 // absent).
@@ -318,6 +567,7 @@ __device__ __forceinline__ void load_affine(const GroupArgs &a, int chunk,
   unpack<DT>(bv, bf);
 }
 
+const void *group_ring_kernel_ptr(int dt, int act, bool drop, bool bwd);
 const void *group_fwd_kernel_ptr(int dt, int act, bool drop);     // resident
 const void *group_stats_kernel_ptr(int dt);                       // streamed, first pass
 const void *group_apply_kernel_ptr(int dt, int act, bool drop);   // streamed, second pass

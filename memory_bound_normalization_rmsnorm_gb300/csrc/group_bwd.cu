@@ -9,108 +9,11 @@
 // recomputed in the second pass (from x and dy in shared memory or L2)
 // rather than kept: kept in 16 bits it would be rounded.
 #include "common.cuh"
-#include "group.cuh"
+#include "group_rows.cuh"
 
 namespace gbn {
 
 namespace {
-
-// Per-channel constants of a thread's chunk.
-template <int V>
-struct BwdConst {
-  float2 nmu[V / 2], rs[V / 2], gf[V / 2], bf[V / 2];
-};
-
-template <int DT>
-__device__ __forceinline__ void load_const(const GroupArgs &a, int b, int chunk,
-                                           BwdConst<chunk_elems(DT)> &k) {
-  constexpr int V = chunk_elems(DT);
-  load_affine<DT>(a, chunk, k.gf, k.bf);
-  const int64_t base = static_cast<int64_t>(b) * a.G;
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    const int c = chunk * V + 2 * p;
-    const int g0 = c / a.D, g1 = (c + 1) / a.D;
-    k.nmu[p] = make_float2(-__ldg(a.mean + base + g0), -__ldg(a.mean + base + g1));
-    k.rs[p] = make_float2(__ldg(a.rstd + base + g0), __ldg(a.rstd + base + g1));
-  }
-}
-
-// xhat and dz of one chunk.
-template <int DT, int ACT, bool DROP>
-__device__ __forceinline__ void grad_chunk(const uint4 &xv, const uint4 &dv,
-                                           const BwdConst<chunk_elems(DT)> &k, const DropGen &gen,
-                                           int64_t elem, float2 (&xh)[chunk_elems(DT) / 2],
-                                           float2 (&dz)[chunk_elems(DT) / 2]) {
-  constexpr int V = chunk_elems(DT);
-  unpack<DT>(xv, xh);
-  unpack<DT>(dv, dz);
-  if (DROP) gen.template chunk<V>(dz, static_cast<uint64_t>(elem));
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    xh[p] = mul2(add2(xh[p], k.nmu[p]), k.rs[p]);
-    if (ACT != kActNone) {
-      const float2 z = fma2(xh[p], k.gf[p], k.bf[p]);
-      dz[p] = mul2(dz[p], make_float2(act_grad<ACT>(z.x), act_grad<ACT>(z.y)));
-    }
-  }
-}
-
-// dx of one chunk: rstd gamma dz - rstd m1 - xhat (rstd m2), with the group
-// constants ra = -rstd m1 and rc = -rstd m2.
-template <int DT, int ACT, bool DROP>
-__device__ __forceinline__ uint4 dx_chunk(const uint4 &xv, const uint4 &dv,
-                                          const BwdConst<chunk_elems(DT)> &k,
-                                          const float2 (&ra)[chunk_elems(DT) / 2],
-                                          const float2 (&rc)[chunk_elems(DT) / 2],
-                                          const DropGen &gen, int64_t elem) {
-  constexpr int V = chunk_elems(DT);
-  float2 xh[V / 2], dz[V / 2];
-  grad_chunk<DT, ACT, DROP>(xv, dv, k, gen, elem, xh, dz);
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p)
-    dz[p] = fma2(xh[p], rc[p], fma2(mul2(dz[p], k.gf[p]), k.rs[p], ra[p]));
-  return pack<DT>(dz);
-}
-
-// Group constants of the dx pass from gst = (-rstd m1, -rstd m2) per group.
-template <int DT>
-__device__ __forceinline__ void dx_constants(const GroupArgs &a, const float2 *gst, int g0,
-                                             int chunk, float2 (&ra)[chunk_elems(DT) / 2],
-                                             float2 (&rc)[chunk_elems(DT) / 2]) {
-  constexpr int V = chunk_elems(DT);
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    const int c = chunk * V + 2 * p;
-    const float2 s0 = gst[c / a.D - g0], s1 = gst[(c + 1) / a.D - g0];
-    ra[p] = make_float2(s0.x, s1.x);
-    rc[p] = make_float2(s0.y, s1.y);
-  }
-}
-
-// Sum over a group's D channels of gamma-weighted channel sums, by one warp.
-template <int DT>
-__device__ __forceinline__ float2 weighted_group(const GroupArgs &a, const float *cb,
-                                                 const float *cg, int c0, int c) {
-  const int lane = threadIdx.x & 31;
-  float s1 = 0.f, s2 = 0.f;
-  for (int j = lane; j < a.D; j += 32) {
-    const float gm = load_elem<DT>(a.gamma, c0 + c + j);
-    s1 = fmaf(gm, cb[c + j], s1);
-    s2 = fmaf(gm, cg[c + j], s2);
-  }
-  return make_float2(warp_sum(s1), warp_sum(s2));
-}
-
-template <int V>
-__device__ __forceinline__ void put_channels(float *cb, float *cg, int c, const float2 (&s1)[V / 2],
-                                             const float2 (&s2)[V / 2]) {
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    *reinterpret_cast<float2 *>(cb + c + 2 * p) = s1[p];
-    *reinterpret_cast<float2 *>(cg + c + 2 * p) = s2[p];
-  }
-}
 
 template <int DT, int ACT, bool DROP>
 __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const GroupArgs a) {
@@ -130,14 +33,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   const int g0 = slab * a.sg;
   const int ng = min(a.sg, a.G - g0);
   const bool on = rl < a.R && cc < ncs_me;
-  const int64_t s0 = part_begin(a.S, q, a.k);
-  const int nrow = static_cast<int>(part_begin(a.S, q + 1, a.k) - s0);
+  const Parts parts(a.S, a.k);
+  const int s0 = parts.begin(q), nrow = parts.rows(q);
   const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
 
   // slot i of this thread: x at data[2 i nact], dy at data[(2 i + 1) nact]
   uint4 *data = reinterpret_cast<uint4 *>(smem) + tid;
   unsigned char *fold = smem + static_cast<size_t>(a.slots) * nact * 32;
-  float2 *gst = reinterpret_cast<float2 *>(fold + group_fold_bytes(a.R, a.ncs, V));
+  float *cb = reinterpret_cast<float *>(fold + group_fold_bytes(a.R, a.ncs, V));
+  float *cg = cb + a.ncs * V;  // cb: sum dz per channel, cg: sum dz xhat
+  float2 *gst = reinterpret_cast<float2 *>(cg + a.ncs * V);
   float2 *gfin = gst + a.sg;
 
   grid_launch_dependents();
@@ -161,36 +66,26 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   float2 s1[V / 2], s2[V / 2];
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
-  auto take = [&](int i) {
-    float2 xh[V / 2], dz[V / 2];
-    grad_chunk<DT, ACT, DROP>(data[static_cast<size_t>(2 * i) * nact],
-                              data[static_cast<size_t>(2 * i + 1) * nact], k, gen, e0 + i * estep,
-                              xh, dz);
-#pragma unroll
-    for (int p = 0; p < V / 2; ++p) {
-      s1[p] = add2(s1[p], dz[p]);
-      s2[p] = fma2(dz[p], xh[p], s2[p]);
-    }
-  };
+  auto slot_x = [&](int i) { return data[static_cast<size_t>(2 * i) * nact]; };
+  auto slot_d = [&](int i) { return data[static_cast<size_t>(2 * i + 1) * nact]; };
   const int npair = nr >> 1;
   for (int j = 0; j < npair; ++j) {
     cp_async_wait_upto(npair - j);
-    take(2 * j);
-    take(2 * j + 1);
+    const int i = 2 * j;
+    sum_rows<DT, ACT, DROP>(slot_x(i), slot_d(i), slot_x(i + 1), slot_d(i + 1), true, k, gen,
+                            e0 + i * estep, e0 + (i + 1) * estep, s1, s2);
   }
   cp_async_wait<0>();
-  if (nr & 1) take(nr - 1);
-
-  fold_sums<V>(s1, s2, fold, a.R, rl, cc, a.ncs, on);
-  float *cb = reinterpret_cast<float *>(fold);  // sum dz per channel
-  float *cg = cb + a.ncs * V;                   // sum dz xhat per channel
-  if (on && rl == 0) put_channels<V>(cb, cg, cc * V, s1, s2);
-  __syncthreads();
-  const int ch0 = chunk0 * V;
-  for (int g = tid >> 5; g < ng; g += nthr >> 5) {
-    const float2 r = weighted_group<DT>(a, cb, cg, ch0, g * a.D);
-    if ((tid & 31) == 0) gst[g] = r;
+  if (nr & 1) {
+    const int i = nr - 1;
+    const uint4 xv = slot_x(i), dv = slot_d(i);
+    sum_rows<DT, ACT, DROP>(xv, dv, xv, dv, false, k, gen, e0 + i * estep, e0 + i * estep, s1, s2);
   }
+
+  const int ch0 = chunk0 * V;
+  channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ncs_me * V);
+  __syncthreads();
+  group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
   if (a.k > 1) cluster_sync(); else __syncthreads();
   const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
   for (int g = tid; g < ng; g += nthr) {
@@ -228,12 +123,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
     float2 ra[V / 2], rc[V / 2];
     dx_constants<DT>(a, gfin, g0, chunk0 + cc, ra, rc);
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
-#pragma unroll 2
-    for (int i = 0; i < nr; ++i)
-      st_global_cs_v4(dst + i * bstep,
-                      dx_chunk<DT, ACT, DROP>(data[static_cast<size_t>(2 * i) * nact],
-                                              data[static_cast<size_t>(2 * i + 1) * nact], k, ra,
-                                              rc, gen, e0 + i * estep));
+    for (int i = 0; i < nr; i += 2) {
+      const int i2 = i + 1 < nr ? i + 1 : i;
+      uint4 xa = slot_x(i), xb = slot_x(i2);
+      dx_rows<DT, ACT, DROP>(xa, slot_d(i), xb, slot_d(i2), k, ra, rc, gen, e0 + i * estep,
+                             e0 + i2 * estep);
+      st_global_cs_v4(dst + i * bstep, xa);
+      if (i2 != i) st_global_cs_v4(dst + i2 * bstep, xb);
+    }
   }
   if (a.k > 1) cluster_wait_acquire();
 }
@@ -249,8 +146,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
-  const int64_t s0 = part_begin(a.S, sp, a.splits);
-  const int nrow = static_cast<int>(part_begin(a.S, sp + 1, a.splits) - s0);
+  const Parts parts(a.S, a.splits);
+  const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float *cb = reinterpret_cast<float *>(smem);
   float *cg = cb + a.C;
   unsigned char *fold = smem + static_cast<size_t>(a.C) * 8;
@@ -271,15 +168,6 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
     for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
     BwdConst<V> k;
     if (on) load_const<DT>(a, b, col + cc, k);
-    auto take = [&](const uint4 &xv, const uint4 &dv, int i) {
-      float2 xh[V / 2], dz[V / 2];
-      grad_chunk<DT, ACT, DROP>(xv, dv, k, gen, (c0 + i * step) * V, xh, dz);
-#pragma unroll
-      for (int p = 0; p < V / 2; ++p) {
-        s1[p] = add2(s1[p], dz[p]);
-        s2[p] = fma2(dz[p], xh[p], s2[p]);
-      }
-    };
     int i = 0;
     for (; i + 4 <= nr; i += 4) {
       uint4 xv[4], dv[4];
@@ -289,18 +177,21 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
         dv[u] = __ldg(ds + (i + u) * step);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) take(xv[u], dv[u], i + u);
+      for (int u = 0; u < 4; u += 2)
+        sum_rows<DT, ACT, DROP>(xv[u], dv[u], xv[u + 1], dv[u + 1], true, k, gen,
+                                (c0 + (i + u) * step) * V, (c0 + (i + u + 1) * step) * V, s1, s2);
     }
-    for (; i < nr; ++i) take(__ldg(xs + i * step), __ldg(ds + i * step), i);
-    fold_sums<V>(s1, s2, fold, a.R, rl, cc, a.ncs, on);
-    if (on && rl == 0) put_channels<V>(cb, cg, (col + cc) * V, s1, s2);
+    for (; i < nr; ++i) {
+      const uint4 xv = __ldg(xs + i * step), dv = __ldg(ds + i * step);
+      const int64_t e = (c0 + i * step) * V;
+      sum_rows<DT, ACT, DROP>(xv, dv, xv, dv, false, k, gen, e, e, s1, s2);
+    }
+    channel_sums<V>(s1, s2, fold, cb + col * V, cg + col * V, a.R, rl, cc, a.ncs, on,
+                    min(a.ncs, a.nc - col) * V);
+    __syncthreads();  // the fold buffer is free again
   }
-  __syncthreads();
   float2 *out = reinterpret_cast<float2 *>(a.gpart) + static_cast<int64_t>(blockIdx.x) * a.G;
-  for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
-    const float2 r = weighted_group<DT>(a, cb, cg, 0, g * a.D);
-    if ((tid & 31) == 0) out[g] = r;
-  }
+  group_sums<DT>(a, cb, cg, 0, a.G, [&](int g, float2 v) { out[g] = v; });
   float *rg = a.cpart + static_cast<int64_t>(blockIdx.x) * a.C;
   float *rb = a.dbeta_part ? a.dbeta_part + static_cast<int64_t>(blockIdx.x) * a.C : nullptr;
   for (int j = tid; j < a.C / 4; j += blockDim.x) {
@@ -320,8 +211,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
-  const int64_t s0 = part_begin(a.S, sp, a.splits);
-  const int nrow = static_cast<int>(part_begin(a.S, sp + 1, a.splits) - s0);
+  const Parts parts(a.S, a.splits);
+  const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float2 *gfin = reinterpret_cast<float2 *>(smem);
 
   grid_launch_dependents();
@@ -365,15 +256,17 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
         xv[u] = __ldcs(xs + c);
         dv[u] = __ldcs(ds + c);
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t c = c0 + (i - 1 - u) * step;
-        st_global_cs_v4(dst + c, dx_chunk<DT, ACT, DROP>(xv[u], dv[u], k, ra, rc, gen, c * V));
-      }
+      const int64_t c = c0 + (i - 1) * step;
+      dx_rows<DT, ACT, DROP>(xv[0], dv[0], xv[1], dv[1], k, ra, rc, gen, c * V, (c - step) * V);
+      st_global_cs_v4(dst + c, xv[0]);
+      st_global_cs_v4(dst + c - step, xv[1]);
     }
-    if (i == 1)
-      st_global_cs_v4(dst + c0,
-                      dx_chunk<DT, ACT, DROP>(__ldcs(xs + c0), __ldcs(ds + c0), k, ra, rc, gen, c0 * V));
+    if (i == 1) {
+      uint4 xa = __ldcs(xs + c0), xb = xa;
+      const uint4 dv = __ldcs(ds + c0);
+      dx_rows<DT, ACT, DROP>(xa, dv, xb, dv, k, ra, rc, gen, c0 * V, c0 * V);
+      st_global_cs_v4(dst + c0, xa);
+    }
   }
 }
 

@@ -2,47 +2,11 @@
 // dropout) on channels-last tensors: y = drop(act(xhat * gamma + beta)),
 // xhat = (x - mean) * rstd with the statistics of each (sample, group).
 #include "common.cuh"
-#include "group.cuh"
+#include "group_rows.cuh"
 
 namespace gbn {
 
 namespace {
-
-// y of one chunk: z = (x - mean) * (rstd gamma) + beta, activation, dropout.
-template <int DT, int ACT, bool DROP>
-__device__ __forceinline__ uint4 out_chunk(const uint4 &xv, const float2 (&nmu)[chunk_elems(DT) / 2],
-                                           const float2 (&sc)[chunk_elems(DT) / 2],
-                                           const float2 (&bf)[chunk_elems(DT) / 2],
-                                           const DropGen &gen, int64_t elem) {
-  constexpr int V = chunk_elems(DT);
-  float2 f[V / 2];
-  unpack<DT>(xv, f);
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    const float2 z = fma2(add2(f[p], nmu[p]), sc[p], bf[p]);
-    f[p] = make_float2(act_fwd<ACT>(z.x), act_fwd<ACT>(z.y));
-  }
-  if (DROP) gen.template chunk<V>(f, static_cast<uint64_t>(elem));
-  return pack<DT>(f);
-}
-
-// Per-channel constants of the output pass: -mean, rstd gamma, beta.
-// `gst` holds (mean, rstd) of the groups from g0 on.
-template <int DT>
-__device__ __forceinline__ void out_constants(const GroupArgs &a, const float2 *gst, int g0,
-                                              int chunk, float2 (&nmu)[chunk_elems(DT) / 2],
-                                              float2 (&sc)[chunk_elems(DT) / 2],
-                                              float2 (&bf)[chunk_elems(DT) / 2]) {
-  constexpr int V = chunk_elems(DT);
-  load_affine<DT>(a, chunk, sc, bf);
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    const int c = chunk * V + 2 * p;
-    const float2 s0 = gst[c / a.D - g0], s1 = gst[(c + 1) / a.D - g0];
-    nmu[p] = make_float2(-s0.x, -s1.x);
-    sc[p] = mul2(sc[p], make_float2(s0.y, s1.y));
-  }
-}
 
 template <int DT, int ACT, bool DROP>
 __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const GroupArgs a) {
@@ -62,13 +26,15 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   const int g0 = slab * a.sg;
   const int ng = min(a.sg, a.G - g0);
   const bool on = rl < a.R && cc < ncs_me;
-  const int64_t s0 = part_begin(a.S, q, a.k);
-  const int nrow = static_cast<int>(part_begin(a.S, q + 1, a.k) - s0);
+  const Parts parts(a.S, a.k);
+  const int s0 = parts.begin(q), nrow = parts.rows(q);
   const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
 
   uint4 *data = reinterpret_cast<uint4 *>(smem) + tid;  // slot i of this thread: data[i * nact]
   unsigned char *fold = smem + static_cast<size_t>(a.slots) * nact * 16;
-  float2 *gst = reinterpret_cast<float2 *>(fold + group_fold_bytes(a.R, a.ncs, V));
+  float *chm = reinterpret_cast<float *>(fold + group_fold_bytes(a.R, a.ncs, V));
+  float *chq = chm + a.ncs * V;
+  float2 *gst = reinterpret_cast<float2 *>(chq + a.ncs * V);
   float2 *gfin = gst + a.sg;
 
   grid_launch_dependents();
@@ -103,21 +69,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   }
 
   // Row lanes -> channels -> groups -> cluster.
-  fold_stats<V>(st, fold, a.R, rl, cc, a.ncs, on);
-  float *chm = reinterpret_cast<float *>(fold);
-  float *chq = chm + a.ncs * V;
-  if (on && rl == 0) {
-#pragma unroll
-    for (int p = 0; p < V / 2; ++p) {
-      *reinterpret_cast<float2 *>(chm + cc * V + 2 * p) = st.m[p];
-      *reinterpret_cast<float2 *>(chq + cc * V + 2 * p) = st.q[p];
-    }
-  }
+  channel_stats<V>(st, fold, chm, chq, a.R, rl, cc, a.ncs, on, ncs_me * V, nrow);
   __syncthreads();
-  for (int g = tid >> 5; g < ng; g += nthr >> 5) {
-    const float2 r = group_of_channels(chm + g * a.D, chq + g * a.D, a.D, static_cast<float>(nrow));
-    if ((tid & 31) == 0) gst[g] = r;
-  }
+  groups_of_channels(chm, chq, ng, a.D, a.lsh, static_cast<float>(nrow),
+                     [&](int g, float m, float m2) { gst[g] = make_float2(m, m2); });
   if (a.k > 1) cluster_sync(); else __syncthreads();
   const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
   for (int g = tid; g < ng; g += nthr) {
@@ -129,14 +84,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
       // fixed rank order; counts n_r = rows of CTA r (times D)
       float acc = 0.f;
       for (int r = 0; r < a.k; ++r) {
-        const float n = static_cast<float>(part_begin(a.S, r + 1, a.k) - part_begin(a.S, r, a.k));
+        const float n = static_cast<float>(parts.rows(r));
         acc = fmaf(n, ld_cluster_f2(gst + g, r).x, acc);
       }
       m = acc / static_cast<float>(a.S);
       m2 = 0.f;
       for (int r = 0; r < a.k; ++r) {
-        const float n = static_cast<float>(part_begin(a.S, r + 1, a.k) - part_begin(a.S, r, a.k)) *
-                        static_cast<float>(a.D);
+        const float n = static_cast<float>(parts.rows(r)) * static_cast<float>(a.D);
         const float2 v = ld_cluster_f2(gst + g, r);
         m2 += fmaf(n * (v.x - m), v.x - m, v.y);
       }
@@ -156,11 +110,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
     out_constants<DT>(a, gfin, g0, chunk0 + cc, nmu, sc, bf);
     const DropGen gen(a.drop);
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
-#pragma unroll 4
-    for (int i = 0; i < nr; ++i)
-      st_global_cs_v4(dst + i * bstep,
-                      out_chunk<DT, ACT, DROP>(data[static_cast<size_t>(i) * nact], nmu, sc, bf, gen,
-                                               e0 + i * estep));
+#pragma unroll 2
+    for (int i = 0; i < nr; i += 2) {
+      const int i2 = i + 1 < nr ? i + 1 : i;
+      uint4 va = data[static_cast<size_t>(i) * nact], vb = data[static_cast<size_t>(i2) * nact];
+      out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, e0 + i * estep, e0 + i2 * estep);
+      st_global_cs_v4(dst + i * bstep, va);
+      if (i2 != i) st_global_cs_v4(dst + i2 * bstep, vb);
+    }
   }
   if (a.k > 1) cluster_wait_acquire();  // no CTA leaves while a peer may read it
 }
@@ -176,8 +133,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_stats_kernel(const Gro
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
-  const int64_t s0 = part_begin(a.S, sp, a.splits);
-  const int nrow = static_cast<int>(part_begin(a.S, sp + 1, a.splits) - s0);
+  const Parts parts(a.S, a.splits);
+  const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float *chm = reinterpret_cast<float *>(smem);
   float *chq = chm + a.C;
   unsigned char *fold = smem + static_cast<size_t>(a.C) * 8;
@@ -211,21 +168,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_stats_kernel(const Gro
       unpack<DT>(__ldg(src + i * step), f);
       st.add1(f);
     }
-    fold_stats<V>(st, fold, a.R, rl, cc, a.ncs, on);
-    if (on && rl == 0) {
-#pragma unroll
-      for (int p = 0; p < V / 2; ++p) {
-        *reinterpret_cast<float2 *>(chm + (col + cc) * V + 2 * p) = st.m[p];
-        *reinterpret_cast<float2 *>(chq + (col + cc) * V + 2 * p) = st.q[p];
-      }
-    }
+    channel_stats<V>(st, fold, chm + col * V, chq + col * V, a.R, rl, cc, a.ncs, on,
+                     min(a.ncs, a.nc - col) * V, nrow);
+    __syncthreads();  // the fold buffer is free again
   }
-  __syncthreads();
   float2 *out = reinterpret_cast<float2 *>(a.gpart) + static_cast<int64_t>(blockIdx.x) * a.G;
-  for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
-    const float2 r = group_of_channels(chm + g * a.D, chq + g * a.D, a.D, static_cast<float>(nrow));
-    if ((tid & 31) == 0) out[g] = r;
-  }
+  groups_of_channels(chm, chq, a.G, a.D, a.lsh, static_cast<float>(nrow),
+                     [&](int g, float m, float m2) { out[g] = make_float2(m, m2); });
 }
 
 // Streamed form, second pass: folds the splits' statistics, then the output
@@ -240,8 +189,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
-  const int64_t s0 = part_begin(a.S, sp, a.splits);
-  const int nrow = static_cast<int>(part_begin(a.S, sp + 1, a.splits) - s0);
+  const Parts parts(a.S, a.splits);
+  const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float2 *gfin = reinterpret_cast<float2 *>(smem);
 
   grid_launch_dependents();
@@ -253,14 +202,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
   for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
     float acc = 0.f;
     for (int r = lane; r < a.splits; r += 32) {
-      const float n = static_cast<float>(part_begin(a.S, r + 1, a.splits) - part_begin(a.S, r, a.splits));
+      const float n = static_cast<float>(parts.rows(r));
       acc = fmaf(n, __ldcg(part + static_cast<int64_t>(r) * a.G + g).x, acc);
     }
     const float m = warp_sum(acc) / static_cast<float>(a.S);
     float m2 = 0.f;
     for (int r = lane; r < a.splits; r += 32) {
-      const float n = static_cast<float>(part_begin(a.S, r + 1, a.splits) - part_begin(a.S, r, a.splits)) *
-                      static_cast<float>(a.D);
+      const float n = static_cast<float>(parts.rows(r)) * static_cast<float>(a.D);
       const float2 v = __ldcg(part + static_cast<int64_t>(r) * a.G + g);
       m2 += fmaf(n * (v.x - m), v.x - m, v.y);
     }
@@ -293,14 +241,18 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[u] = __ldcs(src + c0 + (i - 1 - u) * step);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 4; u += 2) {
         const int64_t c = c0 + (i - 1 - u) * step;
-        st_global_cs_v4(dst + c, out_chunk<DT, ACT, DROP>(v[u], nmu, sc, bf, gen, c * V));
+        out_rows<DT, ACT, DROP>(v[u], v[u + 1], nmu, sc, bf, gen, c * V, (c - step) * V);
+        st_global_cs_v4(dst + c, v[u]);
+        st_global_cs_v4(dst + c - step, v[u + 1]);
       }
     }
     for (; i > 0; --i) {
       const int64_t c = c0 + (i - 1) * step;
-      st_global_cs_v4(dst + c, out_chunk<DT, ACT, DROP>(__ldcs(src + c), nmu, sc, bf, gen, c * V));
+      uint4 va = __ldcs(src + c), vb = va;
+      out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, c * V, c * V);
+      st_global_cs_v4(dst + c, va);
     }
   }
 }

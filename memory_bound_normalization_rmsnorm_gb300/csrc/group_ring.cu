@@ -1,0 +1,463 @@
+// group_ring.cu -- group normalisation of large samples: one cooperative
+// kernel, one CTA per SM, forward and backward.
+//
+// The samples are taken in rounds.  In a round every CTA owns one row range
+// of one sample and walks it twice: a statistics pass (or, backward, the
+// per-channel sums), a grid-wide barrier at which the CTAs of a sample see
+// each other's partials, and an output pass.  A round holds as many samples
+// as shared memory and L2 keep between the two passes (group.cu).
+//
+// Rows move as tiles (contiguous in memory) through a ring of shared-memory
+// stages filled by bulk copies.  The first pass leaves the last `stages`
+// tiles where they are; the output pass walks the tiles in the opposite
+// order, so it starts with those, and as each is consumed its stage takes the
+// tile that the first pass read latest among those dropped: the second read
+// goes from the newest to the oldest line of L2.  Once a round has no tile
+// left to read again, freed stages take the next round's first tiles.
+//
+// What that does to the ring: a stage is always filled in the order in which
+// stages are freed, so the walk through the stages turns round at the end of
+// the first pass (where it stays on the last tile) and goes on in the new
+// direction through the output pass and the next round's first pass.
+//
+// The bound is HBM: x (and dy) read once, y (dx) written once, plus whatever
+// of the second read neither shared memory (about 29 MB over the GPU) nor L2
+// still holds.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "group_rows.cuh"
+
+namespace gbn {
+
+namespace {
+
+// One CTA's view of the ring: rows [row0, row0 + nrow) of one sample (in
+// rounds: of sample b, b + nsamp, ...), chunk columns [chunk0, chunk0 + ncs).
+template <int DT, int NT>
+struct Ring {
+  const GroupArgs &a;
+  unsigned char *base;
+  uint64_t *full;
+  volatile int *abort_flag;
+  int *done;
+  GroupRingLayout L;
+  uint64_t pol;
+  int row0, nrow, TR, T, chunk0, ncs;
+  int cur, dir, nwarps;
+  uint32_t par;  // bit s: parity of stage s's next phase
+
+  __device__ __forceinline__ Ring(const GroupArgs &args, unsigned char *smem, int split, int slab)
+      : a(args), base(smem), cur(0), dir(1), nwarps(blockDim.x >> 5), par(0) {
+    L = group_ring_layout(a.stages, a.U, a.R, a.ncs, chunk_elems(DT), a.sg, NT == 2);
+    full = reinterpret_cast<uint64_t *>(smem + L.bar_off);
+    abort_flag = reinterpret_cast<volatile int *>(smem + L.flag_off);
+    done = reinterpret_cast<int *>(smem + L.flag_off) + 1;
+    pol = l2_evict_first_policy();
+    const Parts parts(a.S, a.splits);
+    row0 = parts.begin(split);
+    nrow = parts.rows(split);
+    TR = a.U * a.R;
+    T = (nrow + TR - 1) / TR;
+    chunk0 = slab * a.ncs;
+    ncs = min(a.ncs, a.nc - chunk0);
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < a.stages; ++s) {
+        mbar_init(full + s, 1);
+        done[s] = 0;
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ int rows_of(int tile) const { return min(TR, nrow - tile * TR); }
+
+  // Fills stage s with tile `tile` of sample b (all lanes of one warp).
+  // `last`: nothing reads the lines again.
+  __device__ __forceinline__ void issue(int b, int tile, int s, bool last) {
+    const int lane = threadIdx.x & 31;
+    const int rows = rows_of(tile);
+    const int64_t c = (static_cast<int64_t>(b) * a.S + row0 + static_cast<int64_t>(tile) * TR) *
+                          a.nc + chunk0;
+    const uint4 *srcs[2] = {static_cast<const uint4 *>(a.x) + c,
+                            static_cast<const uint4 *>(a.dy) + c};
+    unsigned char *dst = base + static_cast<size_t>(s) * L.stage_bytes;
+    const uint32_t rb = static_cast<uint32_t>(ncs) * 16u;
+    if (lane == 0) mbar_arrive_expect_tx(full + s, NT * rb * rows);
+    __syncwarp();
+    if (ncs == a.nc) {
+      if (lane < NT) copy(dst + lane * L.tensor_bytes, srcs[lane], rb * rows, full + s, last);
+    } else {
+      // stage rows are a.ncs chunks apart, whatever this slab's width
+      for (int r = lane; r < rows; r += 32)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          copy(dst + t * L.tensor_bytes + static_cast<size_t>(r) * a.ncs * 16,
+               srcs[t] + static_cast<int64_t>(r) * a.nc, rb, full + s, last);
+    }
+  }
+  __device__ __forceinline__ void copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                       bool last) {
+    if (last) bulk_g2s(dst, src, bytes, bar, pol);
+    else bulk_g2s_keep(dst, src, bytes, bar);
+  }
+
+  __device__ __forceinline__ void wait() {
+    mbar_wait(full + cur, (par >> cur) & 1u, a.err, abort_flag);
+    par ^= 1u << cur;
+  }
+  __device__ __forceinline__ void step() {
+    cur += dir;
+    if (cur == a.stages) cur = 0;
+    if (cur < 0) cur = a.stages - 1;
+  }
+  // The current stage is free: its last reader fills it with `tile` of b.
+  __device__ __forceinline__ void refill(int b, int tile, bool last) {
+    if (last_warp_done(done, cur, nwarps)) {
+      if ((threadIdx.x & 31) == 0) fence_proxy_async_smem();
+      __syncwarp();
+      issue(b, tile, cur, last);
+    }
+  }
+  __device__ __forceinline__ const uint4 *stage(int tensor) const {
+    return reinterpret_cast<const uint4 *>(base + static_cast<size_t>(cur) * L.stage_bytes +
+                                           tensor * L.tensor_bytes);
+  }
+
+  // First pass over sample b: body(first row of the tile, its rows).
+  template <typename Body>
+  __device__ __forceinline__ void first_pass(int b, Body body) {
+    for (int j = 0; j < T; ++j) {
+      wait();
+      body(j * TR, rows_of(j));
+      if (j + a.stages < T) refill(b, j + a.stages, false);
+      if (j + 1 < T) step();
+    }
+    dir = -dir;
+  }
+  // Output pass over sample b, last tile first; `next`: the sample of this
+  // CTA's next round, or -1.
+  template <typename Body>
+  __device__ __forceinline__ void output_pass(int b, int next, Body body) {
+    for (int i = 0; i < T; ++i) {
+      if (i >= a.stages) wait();
+      const int tile = T - 1 - i;
+      body(tile * TR, rows_of(tile));
+      const int again = tile - a.stages;  // tile to read again, or the next round's -again - 1
+      if (again >= 0) refill(b, again, true);
+      else if (next >= 0 && -again - 1 < T) refill(next, -again - 1, false);
+      step();
+    }
+  }
+};
+
+// Roles of a CTA: sample within the round, slab, row range.
+struct Role {
+  int sj, slab, sp;
+  __device__ __forceinline__ explicit Role(const GroupArgs &a) {
+    const int u = static_cast<int>(blockIdx.x);
+    sp = u % a.splits;
+    slab = (u / a.splits) % a.nslab;
+    sj = u / (a.splits * a.nslab);
+  }
+};
+
+template <int DT, int ACT, bool DROP>
+__global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const GroupArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int V = chunk_elems(DT);
+  constexpr int U = 4;  // rows per thread and tile: one block of the statistics
+  const Role role(a);
+  Ring<DT, 1> ring(a, smem, role.sp, role.slab);
+  const int tid = threadIdx.x;
+  const int rl = tid / a.ncs;
+  const int cc = tid - rl * a.ncs;
+  const bool on = rl < a.R && cc < ring.ncs;
+  const int g0 = role.slab * a.sg;
+  const int ng = min(a.sg, a.G - g0);
+  unsigned char *fold = smem + ring.L.fold_off;
+  float *chm = reinterpret_cast<float *>(smem + ring.L.chan_off);
+  float *chq = chm + a.ncs * V;
+  float2 *gfin = reinterpret_cast<float2 *>(smem + ring.L.gst_off);
+  float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
+  const Parts parts(a.S, a.splits);
+  const float invS = 1.0f / static_cast<float>(a.S);
+  const float fD = static_cast<float>(a.D);
+  const float invCount = 1.0f / (static_cast<float>(a.S) * fD);
+  const DropGen gen(a.drop);
+  auto grid = cooperative_groups::this_grid();
+
+  if (tid < 32 && role.sj < a.B)
+    for (int j = 0; j < min(a.stages, ring.T); ++j) ring.issue(role.sj, j, j, false);
+
+  for (int round = 0; round < a.rounds; ++round) {
+    const int b = round * a.nsamp + role.sj;
+    const int next = (round + 1 < a.rounds && b + a.nsamp < a.B) ? b + a.nsamp : -1;
+    if (b < a.B) {
+      ChannelStats<V> st;
+      st.clear();
+      ring.first_pass(b, [&](int, int rows) {
+        if (!on) return;
+        const uint4 *t = ring.stage(0) + rl * a.ncs + cc;
+        const int step = a.R * a.ncs;
+        if (rl + (U - 1) * a.R < rows) {
+          float2 f[U][V / 2];
+#pragma unroll
+          for (int u = 0; u < U; ++u) unpack<DT>(t[u * step], f[u]);
+          st.add4(f[0], f[1], f[2], f[3]);
+        } else {
+          for (int u = 0; rl + u * a.R < rows; ++u) {
+            float2 f[V / 2];
+            unpack<DT>(t[u * step], f);
+            st.add1(f);
+          }
+        }
+      });
+      channel_stats<V>(st, fold, chm, chq, a.R, rl, cc, a.ncs, on, ring.ncs * V, ring.nrow);
+      __syncthreads();
+      // partials laid out [b][group][split]: the fold below reads a group's
+      // splits side by side
+      groups_of_channels(chm, chq, ng, a.D, a.lsh, static_cast<float>(ring.nrow),
+                         [&](int g, float m, float m2) {
+                           gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * a.splits + role.sp] =
+                               make_float2(m, m2);
+                         });
+    }
+    grid.sync();
+    if (b < a.B) {
+      each_group(ng, a.lsh, [&](int g, int l, bool in) {
+        const float2 *part = gpart + (static_cast<int64_t>(b) * a.G + g0 + g) * a.splits;
+        // the mean first, then the deviations from it; a lane's first
+        // kNear splits stay in registers in between
+        constexpr int kNear = 12;
+        float2 v[kNear];
+        float m = 0.f, m2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < kNear; ++i) {
+          const int r = l + (i << a.lsh);
+          v[i] = in && r < a.splits ? __ldcg(part + r) : splat2(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kNear; ++i) {
+          const int r = l + (i << a.lsh);
+          if (r < a.splits) m = fmaf(static_cast<float>(parts.rows(r)), v[i].x, m);
+        }
+        const int far = in ? l + (kNear << a.lsh) : a.splits;
+        for (int r = far; r < a.splits; r += 1 << a.lsh)
+          m = fmaf(static_cast<float>(parts.rows(r)), __ldcg(part + r).x, m);
+        m = lanes_sum(m, a.lsh) * invS;
+        auto deviation = [&](int r, float2 u) {
+          const float e = u.x - m;
+          m2 += fmaf(static_cast<float>(parts.rows(r)) * fD * e, e, u.y);
+        };
+#pragma unroll
+        for (int i = 0; i < kNear; ++i) {
+          const int r = l + (i << a.lsh);
+          if (r < a.splits) deviation(r, v[i]);
+        }
+        for (int r = far; r < a.splits; r += 1 << a.lsh) deviation(r, __ldcg(part + r));
+        m2 = lanes_sum(m2, a.lsh);
+        if (in && l == 0) {
+          const float rs = rsqrtf(m2 * invCount + a.eps);
+          gfin[g] = make_float2(m, rs);
+          if (role.sp == 0) {
+            a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;
+            a.rstd[static_cast<int64_t>(b) * a.G + g0 + g] = rs;
+          }
+        }
+      });
+      __syncthreads();
+      float2 nmu[V / 2], sc[V / 2], bf[V / 2];
+      if (on) out_constants<DT>(a, gfin, g0, ring.chunk0 + cc, nmu, sc, bf);
+      const int64_t e0 = group_elem(a, b, ring.row0 + rl, ring.chunk0 + cc, V);
+      const int64_t estep = static_cast<int64_t>(a.R) * a.C;
+      unsigned char *out = static_cast<unsigned char *>(a.out);
+      ring.output_pass(b, next, [&](int first, int rows) {
+        if (!on) return;
+        const uint4 *t = ring.stage(0) + rl * a.ncs + cc;
+        const int step = a.R * a.ncs;
+        int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+          const bool in1 = rl + u * a.R < rows, in2 = rl + (u + 1) * a.R < rows;
+          if (in1) {
+            uint4 va = t[u * step], vb = in2 ? t[(u + 1) * step] : va;
+            out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, e, e + estep);
+            st_global_cs_v4(out + e * elem_bytes(DT), va);
+            if (in2) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), vb);
+          }
+          e += 2 * estep;
+        }
+      });
+    }
+  }
+}
+
+template <int DT, int ACT, bool DROP>
+__global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const GroupArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int V = chunk_elems(DT);  // (two rows per thread and tile)
+  const Role role(a);
+  Ring<DT, 2> ring(a, smem, role.sp, role.slab);
+  const int tid = threadIdx.x;
+  const int lane = tid & 31;
+  const int rl = tid / a.ncs;
+  const int cc = tid - rl * a.ncs;
+  const bool on = rl < a.R && cc < ring.ncs;
+  const int g0 = role.slab * a.sg;
+  const int ng = min(a.sg, a.G - g0);
+  const int ch0 = ring.chunk0 * V;
+  unsigned char *fold = smem + ring.L.fold_off;
+  float *cb = reinterpret_cast<float *>(smem + ring.L.chan_off);  // sum dz per channel
+  float *cg = cb + a.ncs * V;                                     // sum dz xhat per channel
+  float *tb = reinterpret_cast<float *>(smem + ring.L.tot_off);  // their totals over rounds
+  float *tg = tb + a.ncs * V;
+  float2 *gfin = reinterpret_cast<float2 *>(smem + ring.L.gst_off);
+  float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
+  const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
+  const DropGen gen(a.drop);
+  auto grid = cooperative_groups::this_grid();
+
+  if (tid < 32 && role.sj < a.B)
+    for (int j = 0; j < min(a.stages, ring.T); ++j) ring.issue(role.sj, j, j, false);
+
+  for (int round = 0; round < a.rounds; ++round) {
+    const int b = round * a.nsamp + role.sj;
+    const int next = (round + 1 < a.rounds && b + a.nsamp < a.B) ? b + a.nsamp : -1;
+    const int64_t estep = static_cast<int64_t>(a.R) * a.C;
+    int64_t e0 = 0;
+    BwdConst<V> k;
+    if (b < a.B) {
+      e0 = group_elem(a, b, ring.row0 + rl, ring.chunk0 + cc, V);
+      if (on) load_const<DT>(a, b, ring.chunk0 + cc, k);
+      float2 s1[V / 2], s2[V / 2];
+#pragma unroll
+      for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
+      ring.first_pass(b, [&](int first, int rows) {
+        if (!on || rl >= rows) return;
+        const int step = a.R * a.ncs;
+        const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
+        const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
+        const bool two = rl + a.R < rows;
+        const int o = two ? step : 0;
+        const int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+        sum_rows<DT, ACT, DROP>(tx[0], td[0], tx[o], td[o], two, k, gen, e, e + estep, s1, s2);
+      });
+      channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ring.ncs * V);
+      __syncthreads();
+      group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) {
+        gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * a.splits + role.sp] = v;
+      });
+      // running dgamma / dbeta of this CTA's rows over the rounds; after the
+      // last one they are its partial row
+      float *rg = a.cpart + static_cast<int64_t>(role.sj * a.splits + role.sp) * a.C + ch0;
+      float *rb = a.dbeta_part
+                      ? a.dbeta_part + static_cast<int64_t>(role.sj * a.splits + role.sp) * a.C + ch0
+                      : nullptr;
+      for (int j = tid; j < ring.ncs * V; j += blockDim.x) {
+        float vg = cg[j], vb = cb[j];
+        if (round > 0) {
+          vg += tg[j];
+          vb += tb[j];
+        }
+        if (next < 0) {
+          rg[j] = vg;
+          if (rb) rb[j] = vb;
+        } else {
+          tg[j] = vg;
+          tb[j] = vb;
+        }
+      }
+    }
+    grid.sync();
+    if (b < a.B) {
+      each_group(ng, a.lsh, [&](int g, int l, bool in) {
+        const float2 *part = gpart + (static_cast<int64_t>(b) * a.G + g0 + g) * a.splits;
+        float2 t = splat2(0.f);
+        if (in) {
+#pragma unroll 4
+          for (int r = l; r < a.splits; r += 1 << a.lsh) t = add2(t, __ldcg(part + r));
+        }
+        t.x = lanes_sum(t.x, a.lsh);
+        t.y = lanes_sum(t.y, a.lsh);
+        if (in && l == 0) {
+          const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
+          gfin[g] = make_float2(-rs * (t.x * inv), -rs * (t.y * inv));
+        }
+      });
+      __syncthreads();
+      float2 ra[V / 2], rc[V / 2];
+      if (on) dx_constants<DT>(a, gfin, g0, ring.chunk0 + cc, ra, rc);
+      unsigned char *out = static_cast<unsigned char *>(a.out);
+      ring.output_pass(b, next, [&](int first, int rows) {
+        if (!on || rl >= rows) return;
+        const int step = a.R * a.ncs;
+        const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
+        const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
+        const bool two = rl + a.R < rows;
+        const int o = two ? step : 0;
+        const int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+        uint4 xa = tx[0], xb = tx[o];
+        dx_rows<DT, ACT, DROP>(xa, td[0], xb, td[o], k, ra, rc, gen, e, e + estep);
+        st_global_cs_v4(out + e * elem_bytes(DT), xa);
+        if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), xb);
+      });
+    }
+  }
+
+  // dgamma / dbeta: column sums of the partial rows, which every CTA wrote
+  // before the last barrier (samples of earlier rounds only, where the last
+  // round has none for it).  A CTA takes 32 columns at a time, its warps
+  // every 16th row; the warps' sums are added in warp order.
+  __syncthreads();
+  const int P = min(a.nsamp, a.B) * a.splits;
+  const int cols = (a.C + 31) / 32;
+  float *part = reinterpret_cast<float *>(fold);  // [16][32]
+  for (int t = blockIdx.x; t < cols * (a.dbeta ? 2 : 1); t += gridDim.x) {
+    const bool beta = t >= cols;
+    const int c = (beta ? t - cols : t) * 32 + lane;
+    const float *rows = beta ? a.dbeta_part : a.cpart;
+    float acc = 0.f;
+    if (c < a.C) {
+#pragma unroll 4
+      for (int r = tid >> 5; r < P; r += ring.nwarps)
+        acc += __ldcg(rows + static_cast<int64_t>(r) * a.C + c);
+    }
+    part[tid] = acc;
+    __syncthreads();
+    if (tid < 32 && c < a.C) {
+      for (int w = 1; w < ring.nwarps; ++w) acc += part[w * 32 + lane];
+      (beta ? a.dbeta : a.dgamma)[c] = acc;
+    }
+    __syncthreads();
+  }
+}
+
+template <int DT, int ACT, bool DROP>
+const void *pick_dir(bool bwd) {
+  return bwd ? reinterpret_cast<const void *>(&group_ring_bwd_kernel<DT, ACT, DROP>)
+             : reinterpret_cast<const void *>(&group_ring_fwd_kernel<DT, ACT, DROP>);
+}
+
+template <int DT>
+const void *pick_act(int act, bool drop, bool bwd) {
+  switch (act) {
+    case kActSilu: return drop ? pick_dir<DT, kActSilu, true>(bwd) : pick_dir<DT, kActSilu, false>(bwd);
+    case kActGelu: return drop ? pick_dir<DT, kActGelu, true>(bwd) : pick_dir<DT, kActGelu, false>(bwd);
+    default: return drop ? pick_dir<DT, kActNone, true>(bwd) : pick_dir<DT, kActNone, false>(bwd);
+  }
+}
+
+}  // namespace
+
+const void *group_ring_kernel_ptr(int dt, int act, bool drop, bool bwd) {
+  switch (dt) {
+    case kBF16: return pick_act<kBF16>(act, drop, bwd);
+    case kFP16: return pick_act<kFP16>(act, drop, bwd);
+    default: return pick_act<kFP32>(act, drop, bwd);
+  }
+}
+
+}  // namespace gbn

@@ -32,6 +32,10 @@ norm_status_t function_ready(int dev, const void *fn, int smem_optin);
 norm_status_t launch_serial(const void *fn, dim3 grid, dim3 block, size_t smem, int cluster,
                             void **args, cudaStream_t s);
 
+// One launch whose CTAs are all resident at once (grid-wide barriers) (api.cu).
+norm_status_t launch_cooperative(const void *fn, dim3 grid, dim3 block, size_t smem, void **args,
+                                 cudaStream_t s);
+
 // Fixed-order column sum of P fp32 rows [P][n] (and, with dbeta, of the P
 // rows that follow them) into dgamma (dbeta), on `s` (api.cu).
 norm_status_t reduce_rows(const float *rows, int P, int n, float *dgamma, float *dbeta,

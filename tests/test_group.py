@@ -79,9 +79,41 @@ def test_parity_streamed(shape, dtype, monkeypatch):
     for splits in ("", ",splits=1", ",splits=3", ",splits=5"):
         monkeypatch.setenv("GBNORM_GROUP", "form=1" + splits)
         plan = gb.norm_group_plan(B, S, C, G, ["bf16", "fp16", "fp32"].index(dtype))
-        assert plan["streamed"] == 1
+        assert plan["form"] == 1
         check_both(x, g, b, dy, G, "gelu", 0.25, f"{shape} {dtype} streamed{splits}")
         check_both(x, g, None, dy, G, "none", 0.0, f"{shape} {dtype} streamed{splits} no beta")
+
+
+RINGS = ["", ",R=1", ",splits=1,R=1,stages=3", ",splits=2,R=2,stages=2", ",splits=3,R=1,stages=4",
+         ",nsamp=1,splits=1,R=1,stages=2", ",nsamp=1,splits=2,R=1", ",nsamp=2,splits=1,R=2,stages=3"]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s != (1, 2, 8192, 8192)], ids=str)
+def test_parity_ring(shape, dtype, monkeypatch):
+    """One tile, fewer tiles than stages, many turns of the ring, several
+    rounds (a last one with fewer samples), row ranges of unequal length."""
+    B, S, C, G = shape
+    x, g, b, dy = make(B, S, C, DT[dtype], seed=B + S + C + 2)
+    for ring in RINGS:
+        monkeypatch.setenv("GBNORM_GROUP", "form=2" + ring)
+        assert gb.norm_group_plan(B, S, C, G, list(DT).index(dtype))["form"] == 2
+        check_both(x, g, b, dy, G, "silu", 0.1, f"{shape} {dtype} ring{ring}")
+        check_both(x, g, None, dy, G, "none", 0.0, f"{shape} {dtype} ring{ring} no beta")
+    assert gb.norm_get_device_error() == 0
+
+
+@pytest.mark.parametrize("shape,sg", [((2, 100, 320, 32), 12), ((5, 33, 168, 12), 8),
+                                      ((3, 64, 40, 4), 4), ((2, 221, 88, 11), 4)], ids=str)
+def test_parity_ring_slabs(shape, sg, monkeypatch):
+    """Slabs narrower than a row (copied row by row), the last one narrower."""
+    B, S, C, G = shape
+    for dtype in DT.values():
+        x, g, b, dy = make(B, S, C, dtype, seed=sg)
+        for ring in RINGS[:5]:
+            monkeypatch.setenv("GBNORM_GROUP", f"form=2,sg={sg}" + ring)
+            check_both(x, g, b, dy, G, "gelu", 0.1, f"{shape} sg={sg} ring{ring}")
+    assert gb.norm_get_device_error() == 0
 
 
 @pytest.mark.parametrize("k", [1, 2, 4, 8])
@@ -96,11 +128,11 @@ def test_parity_resident_splits(shape, sg, k, monkeypatch):
     for R in ("", ",R=1", ",R=3"):
         monkeypatch.setenv("GBNORM_GROUP", f"form=0,sg={sg},k={k}{R}")
         plan = gb.norm_group_plan(B, S, C, G)
-        assert plan["streamed"] == 0 and plan["cluster"] == k
+        assert plan["form"] == 0 and plan["cluster"] == k
         check_both(x, g, b, dy, G, "silu", 0.1, f"{shape} sg={sg} k={k}{R}")
 
 
-@pytest.mark.parametrize("form", [0, 1])
+@pytest.mark.parametrize("form", [0, 1, 2])
 def test_statistics_far_from_the_origin(form, monkeypatch):
     """Mean 1000 times the deviation, and a sample whose first rows are zero:
     a sum of squares about the origin would lose every digit of the variance."""
@@ -124,7 +156,7 @@ def test_constant_groups_and_eps():
     assert torch.allclose(y, torch.nn.functional.silu(b).expand_as(y), rtol=1e-5, atol=1e-7)
 
 
-@pytest.mark.parametrize("form", [0, 1])
+@pytest.mark.parametrize("form", [0, 1, 2])
 def test_nan_and_infinity_stay_in_their_group(form, monkeypatch):
     monkeypatch.setenv("GBNORM_GROUP", f"form={form}")
     x, g, b, dy = make(3, 40, 40, torch.bfloat16)
@@ -149,12 +181,17 @@ def test_large_activations_have_finite_gradients():
             y, rstd, mean = gb.norm_group_fwd(x, gg, b, 2, 1e-5, name)
             dx, dg, db = gb.norm_group_bwd(dy, x, gg, b, rstd, mean, 2, name)
             assert all(torch.isfinite(t).all() for t in (y, dg, db)), (name, big)
+            y64, _, _, mag = ref.forward(x, gg, b, 2, 1e-5, name)
+            ref.check(y, y64, mag, f"{name} {big} y")
+            want = ref.backward(dy, x, gg, b, rstd, mean, 2, name)
+            ref.check(db, want[2], want[5], f"{name} {big} dbeta")
+            ref.check(dg, want[1], want[4], f"{name} {big} dgamma")
 
 
 def test_determinism_streams_and_graph():
     """Bitwise the same on another stream and from a replayed graph that
     captured forward and backward."""
-    for shape in ((2, 600, 320, 32), (1, 40000, 256, 32)):
+    for shape in ((2, 600, 320, 32), (1, 40000, 256, 32), (3, 30000, 512, 32)):
         B, S, C, G = shape
         x, g, b, dy = make(B, S, C, torch.bfloat16)
         a = check_both(x, g, b, dy, G, "silu", 0.1, str(shape)) if S < 1000 else None
@@ -180,7 +217,7 @@ def test_determinism_streams_and_graph():
             assert torch.equal(u, v) and torch.equal(u, w)
 
 
-@pytest.mark.parametrize("form", [0, 1])
+@pytest.mark.parametrize("form", [0, 1, 2])
 @pytest.mark.parametrize("dtype", list(DT))
 def test_guard_bands(dtype, form, monkeypatch):
     """Nothing is written outside the outputs and the stated workspace."""

@@ -116,7 +116,8 @@ def _plan_cases():
 
 
 @pytest.mark.parametrize("override", ["", "form=0", "form=1", "form=1,splits=7", "form=0,k=8",
-                                      "form=0,R=2"])
+                                      "form=0,R=2", "form=2", "form=2,R=1,stages=3",
+                                      "form=2,nsamp=2,splits=5"])
 def test_group_plans_in_bounds(override, monkeypatch):
     if override:
         monkeypatch.setenv("GBNORM_GROUP", override)
@@ -127,38 +128,57 @@ def test_group_plans_in_bounds(override, monkeypatch):
                 try:
                     p = gb.norm_group_plan(B, S, C, G, dt, bwd, SMS, OPTIN)
                 except gb.NormError as e:
-                    assert e.status == 6 and override.startswith("form=0")
+                    assert e.status == 6 and override[:6] in ("form=0", "form=2")
                     continue
                 V, D, nt = (4 if dt == 2 else 8), C // G, 2 if bwd else 1
                 label = (B, S, C, G, dt, bwd, p)
-                seen.add(p["streamed"])
+                seen.add(p["form"])
+                R, ncs = p["row_lanes"], p["chunk_columns"]
                 assert p["threads"] % 32 == 0 and 32 <= p["threads"] <= 512, label
-                assert p["chunk_columns"] * p["row_lanes"] <= p["threads"], label
+                assert ncs * R <= p["threads"], label
                 assert 0 < p["smem_bytes"] <= OPTIN and 1 <= p["grid"] < 1 << 31, label
-                fold = max((p["row_lanes"] // 2) * p["chunk_columns"] * (8 * V + 4),
-                           p["chunk_columns"] * V * 8)
-                if p["streamed"]:
+                fold = ((R + 1) // 2 * ncs * (8 * V + 4) if R > 1 else 0) + ncs * V * 8
+                if p["form"] == 1:
                     assert p["grid"] == B * p["row_splits"] and p["row_splits"] <= max(S, 1), label
-                    assert p["smem_bytes"] >= 8 * C + fold, label
+                    assert p["smem_bytes"] >= 8 * C + fold - ncs * V * 8, label
                     need = (p["grid"] * G * 8 + 15) // 16 * 16 + (p["grid"] * C * 8 if bwd else 0)
                     if bwd and p["grid"] == 1:
                         need -= C * 8
                     assert p["workspace_bytes"] == need, label
                     continue
                 # slabs: whole groups, 16-byte borders, covering every group once
-                assert p["groups_per_slab"] * D == p["chunk_columns"] * V, label
+                assert p["groups_per_slab"] * D == ncs * V, label
                 assert p["groups_per_slab"] * D % 8 == 0, label
                 assert (p["slabs"] - 1) * p["groups_per_slab"] < G <= \
                     p["slabs"] * p["groups_per_slab"], label
+                if p["form"] == 2:
+                    # one CTA per SM, all resident; every sample in one round;
+                    # no CTA with fewer tiles than stages when the ring goes on
+                    n, sp, TR = p["samples_per_round"], p["row_splits"], (2 if bwd else 4) * R
+                    assert p["grid"] == n * p["slabs"] * sp <= SMS, label
+                    assert (p["rounds"] - 1) * n < B <= p["rounds"] * n and sp <= S, label
+                    assert 1 <= p["stages"] <= 31, label
+                    if p["rounds"] > 1:
+                        assert -(-(S // sp) // TR) >= p["stages"], label
+                    stage = TR * ncs * 16 * nt
+                    assert p["smem_bytes"] >= p["stages"] * stage + fold + \
+                        (ncs * V * 8 if bwd else 0) + 8 * p["groups_per_slab"] + \
+                        12 * p["stages"] + 4, label
+                    if bwd:  # the column sums' float per thread before the channel arrays
+                        assert p["smem_bytes"] >= p["stages"] * stage + 2048 + 16 * ncs * V
+                    assert stage < 1 << 20, label  # bytes one stage barrier counts
+                    assert p["workspace_bytes"] == (B * G * sp * 8 + 15) // 16 * 16 + \
+                        (n * sp * C * 8 if bwd else 0), label
+                    continue
                 assert p["grid"] == B * p["slabs"] * p["cluster"], label
                 assert p["cluster"] in (1, 2, 4, 8) and p["cluster"] <= S, label
                 # rows: every CTA's range fits its threads' slots, and no row
                 # lane is empty
                 rows = [S * (i + 1) // p["cluster"] - S * i // p["cluster"]
                         for i in range(p["cluster"])]
-                assert sum(rows) == S and max(rows) <= p["rows_per_thread"] * p["row_lanes"], label
-                assert p["row_lanes"] <= min(rows), label
-                data = p["rows_per_thread"] * p["chunk_columns"] * p["row_lanes"] * 16 * nt
+                assert sum(rows) == S and max(rows) <= p["rows_per_thread"] * R, label
+                assert R <= min(rows), label
+                data = p["rows_per_thread"] * ncs * R * 16 * nt
                 assert p["smem_bytes"] >= data + fold + 16 * p["groups_per_slab"], label
                 assert p["workspace_bytes"] == (B * C * 8 if bwd and B > 1 else 0), label
-    assert seen == ({0, 1} if not override else {int(override[5])})
+    assert seen == ({0, 1, 2} if not override else {int(override[5])})
