@@ -26,7 +26,7 @@ constexpr int kResident = 0, kStreamed = 1, kRing = 2;
 struct GroupPlan {
   int form = kResident;
   int sg = 0, ncs = 0, nslab = 1, k = 1, R = 1, slots = 0, splits = 1;
-  int stages = 0, nsamp = 0, rounds = 0;  // ring
+  int stages = 0, nsamp = 0, rounds = 0, keep = 0;  // ring
   int threads = 0;
   int64_t grid = 0;
   uint32_t smem = 0;  // resident or ring kernel, or the streamed form's first pass
@@ -35,9 +35,9 @@ struct GroupPlan {
 
 // Shape override for sweeps and tests: GBNORM_GROUP="form=1,sg=4,k=2,R=8,
 // splits=3" (any subset; form 0 resident, 1 streamed, 2 ring; for the ring
-// also stages= and nsamp=).  Bypasses the cache.
+// also stages=, nsamp= and keep=).  Bypasses the cache.
 struct GroupOverride {
-  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0;
+  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0, keep = -1;
   bool any = false;
 };
 
@@ -55,6 +55,7 @@ GroupOverride read_group_override() {
       else if (!std::strcmp(key, "splits")) o.splits = val;
       else if (!std::strcmp(key, "stages")) o.stages = val;
       else if (!std::strcmp(key, "nsamp")) o.nsamp = val;
+      else if (!std::strcmp(key, "keep")) o.keep = val;
       o.any = true;
     }
     s = std::strchr(s, ',');
@@ -97,6 +98,9 @@ double ring_cost(const GroupPlan &p, int64_t bytes, int64_t read_bytes, int sms)
   const double used = static_cast<double>(p.grid) / sms;
   return (bytes + again) / (6.6e6 * std::min(1.0, used / 0.7)) + 3.0 * p.rounds + 4.0;
 }
+
+// What L2 is asked to hold of it.
+constexpr int64_t kL2KeepBytes = 64 << 20;
 
 // Ring plan (group_ring.cu): slabs as wide as a CTA has threads for (whole
 // rows where they fit), as many stages as shared memory holds, and rounds of
@@ -149,6 +153,8 @@ norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int s
   p.smem = group_ring_layout(stages, U, p.R, p.ncs, V, p.sg, bwd).total;
   if (static_cast<int64_t>(p.smem) > smem_optin) return NORM_ERR_UNSUPPORTED;
   p.grid = static_cast<int64_t>(p.nsamp) * p.nslab * p.splits;
+  const int64_t tile_bytes = static_cast<int64_t>(TR) * p.ncs * 16 * nt;
+  p.keep = ov.keep >= 0 ? ov.keep : static_cast<int>(kL2KeepBytes / (tile_bytes * p.grid));
   *out = p;
   return NORM_OK;
 }
@@ -295,7 +301,7 @@ struct GroupWs {
 GroupWs group_ws(const GroupPlan &p, int64_t B, int64_t C, int64_t G, bool bwd) {
   GroupWs w;
   if (p.form == kStreamed) w.cpart = static_cast<size_t>(p.grid) * G * 8;
-  if (p.form == kRing) w.cpart = static_cast<size_t>(B) * G * p.splits * 8;
+  if (p.form == kRing) w.cpart = static_cast<size_t>(B) * G * ((p.splits + 1) & ~1) * 8;
   w.cpart = (w.cpart + 15) & ~size_t(15);
   w.total = w.cpart;
   if (bwd) {
@@ -326,6 +332,7 @@ GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_
   a.stages = p.stages;
   a.nsamp = p.nsamp;
   a.rounds = p.rounds;
+  a.keep = p.keep;
   while ((p.sg << (a.lsh + 1)) <= p.threads && a.lsh < 5) ++a.lsh;
   return a;
 }

@@ -58,6 +58,7 @@ struct GroupArgs {
   int stages;  // ring: tiles in shared memory
   int nsamp;   // ring: samples per round
   int rounds;  // ring: ceil(B / nsamp)
+  int keep;    // ring: tiles per CTA that L2 is asked to hold between the passes
   unsigned *err;  // device error word
   float eps;
 };
@@ -75,8 +76,8 @@ __host__ __device__ inline uint32_t group_chan_bytes(int ncs, int V) {
 }
 // The ring kernels: `stages` tiles of U * R rows (one per tensor), the fold
 // buffer, the per-channel arrays, the backward's running per-channel totals,
-// a float2 per group of the slab, the stage mbarriers, and the abort flag
-// with the per-stage warp counters.
+// a float2 per group of the slab, the stages' full and free mbarriers, and
+// the abort flag.
 constexpr int kGroupRingSplits = 192;  // row ranges of a sample, at most
 struct GroupRingLayout {
   uint32_t tensor_bytes, stage_bytes, fold_off, chan_off, tot_off, gst_off, bar_off, flag_off,
@@ -95,8 +96,8 @@ __host__ __device__ inline GroupRingLayout group_ring_layout(int stages, int U, 
   L.tot_off = L.chan_off + group_chan_bytes(ncs, V);
   L.gst_off = L.tot_off + (bwd ? group_chan_bytes(ncs, V) : 0u);
   L.bar_off = L.gst_off + static_cast<uint32_t>(sg) * 8u;
-  L.flag_off = L.bar_off + 8u * static_cast<uint32_t>(stages);
-  L.total = align16(L.flag_off + 4u + 4u * static_cast<uint32_t>(stages));
+  L.flag_off = L.bar_off + 16u * static_cast<uint32_t>(stages);
+  L.total = align16(L.flag_off + 4u);
   return L;
 }
 __host__ __device__ inline uint32_t group_smem_bytes(int slots, int ntensors, int R, int ncs, int V,

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "group_rows.cuh"
+#include "tcgen05.cuh"
 
 namespace gbn {
 
@@ -34,26 +35,31 @@ namespace {
 
 // One CTA's view of the ring: rows [row0, row0 + nrow) of one sample (in
 // rounds: of sample b, b + nsamp, ...), chunk columns [chunk0, chunk0 + ncs).
+//
+// Every warp waits for a stage's copies on its `full` mbarrier and, where the
+// stage is to be filled again, arrives on its `free` one when it has read it.
+// Warp 0 fills a freed stage one item later (the others have then mostly
+// finished with it), so no warp waits for another on the way through a pass.
 template <int DT, int NT>
 struct Ring {
   const GroupArgs &a;
   unsigned char *base;
-  uint64_t *full;
+  uint64_t *full, *empty;
   volatile int *abort_flag;
-  int *done;
   GroupRingLayout L;
-  uint64_t pol;
   int row0, nrow, TR, T, chunk0, ncs;
-  int cur, dir, nwarps;
-  uint32_t par;  // bit s: parity of stage s's next phase
+  int cur, dir;
+  uint32_t par, epar;  // bit s: parity of stage s's next full / free phase
+  int pstage, pb, ptile;  // the refill that warp 0 still owes (pstage < 0: none)
+  bool pkeep;
 
   __device__ __forceinline__ Ring(const GroupArgs &args, unsigned char *smem, int split, int slab)
-      : a(args), base(smem), cur(0), dir(1), nwarps(blockDim.x >> 5), par(0) {
+      : a(args), base(smem), cur(0), dir(1), par(0), epar(0), pstage(-1), pb(0), ptile(0),
+        pkeep(false) {
     L = group_ring_layout(a.stages, a.U, a.R, a.ncs, chunk_elems(DT), a.sg, NT == 2);
     full = reinterpret_cast<uint64_t *>(smem + L.bar_off);
+    empty = full + a.stages;
     abort_flag = reinterpret_cast<volatile int *>(smem + L.flag_off);
-    done = reinterpret_cast<int *>(smem + L.flag_off) + 1;
-    pol = l2_evict_first_policy();
     const Parts parts(a.S, a.splits);
     row0 = parts.begin(split);
     nrow = parts.rows(split);
@@ -64,7 +70,7 @@ struct Ring {
     if (threadIdx.x == 0) {
       for (int s = 0; s < a.stages; ++s) {
         mbar_init(full + s, 1);
-        done[s] = 0;
+        mbar_init(empty + s, blockDim.x >> 5);
       }
       *abort_flag = 0;
       fence_mbar_init();
@@ -74,9 +80,14 @@ struct Ring {
 
   __device__ __forceinline__ int rows_of(int tile) const { return min(TR, nrow - tile * TR); }
 
+  // First-pass lines that the output pass reads again out of L2: the tiles
+  // read last before those that stay in shared memory.
+  __device__ __forceinline__ bool kept(int tile) const {
+    return tile < T - a.stages && tile >= T - a.stages - a.keep;
+  }
+
   // Fills stage s with tile `tile` of sample b (all lanes of one warp).
-  // `last`: nothing reads the lines again.
-  __device__ __forceinline__ void issue(int b, int tile, int s, bool last) {
+  __device__ __forceinline__ void issue(int b, int tile, int s, bool keep) {
     const int lane = threadIdx.x & 31;
     const int rows = rows_of(tile);
     const int64_t c = (static_cast<int64_t>(b) * a.S + row0 + static_cast<int64_t>(tile) * TR) *
@@ -85,25 +96,37 @@ struct Ring {
                             static_cast<const uint4 *>(a.dy) + c};
     unsigned char *dst = base + static_cast<size_t>(s) * L.stage_bytes;
     const uint32_t rb = static_cast<uint32_t>(ncs) * 16u;
+    const uint64_t pol = keep ? l2_evict_last_policy() : l2_evict_first_policy();
     if (lane == 0) mbar_arrive_expect_tx(full + s, NT * rb * rows);
     __syncwarp();
     if (ncs == a.nc) {
-      if (lane < NT) copy(dst + lane * L.tensor_bytes, srcs[lane], rb * rows, full + s, last);
+      if (lane < NT) bulk_g2s(dst + lane * L.tensor_bytes, srcs[lane], rb * rows, full + s, pol);
     } else {
       // stage rows are a.ncs chunks apart, whatever this slab's width
       for (int r = lane; r < rows; r += 32)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          copy(dst + t * L.tensor_bytes + static_cast<size_t>(r) * a.ncs * 16,
-               srcs[t] + static_cast<int64_t>(r) * a.nc, rb, full + s, last);
+          bulk_g2s(dst + t * L.tensor_bytes + static_cast<size_t>(r) * a.ncs * 16,
+                   srcs[t] + static_cast<int64_t>(r) * a.nc, rb, full + s, pol);
     }
   }
-  __device__ __forceinline__ void copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
-                                       bool last) {
-    if (last) bulk_g2s(dst, src, bytes, bar, pol);
-    else bulk_g2s_keep(dst, src, bytes, bar);
+  // The first tiles of sample b, by warp 0.
+  __device__ __forceinline__ void start(int b) {
+    if (threadIdx.x < 32)
+      for (int j = 0; j < min(a.stages, T); ++j) issue(b, j, j, kept(j));
   }
 
+  // Warp 0 fills the stage that was freed one item ago.
+  __device__ __forceinline__ void flush() {
+    if (threadIdx.x < 32 && pstage >= 0) {
+      mbar_wait(empty + pstage, (epar >> pstage) & 1u, a.err, abort_flag);
+      epar ^= 1u << pstage;
+      fence_proxy_async_smem();
+      __syncwarp();
+      issue(pb, ptile, pstage, pkeep);
+      pstage = -1;
+    }
+  }
   __device__ __forceinline__ void wait() {
     mbar_wait(full + cur, (par >> cur) & 1u, a.err, abort_flag);
     par ^= 1u << cur;
@@ -113,13 +136,14 @@ struct Ring {
     if (cur == a.stages) cur = 0;
     if (cur < 0) cur = a.stages - 1;
   }
-  // The current stage is free: its last reader fills it with `tile` of b.
-  __device__ __forceinline__ void refill(int b, int tile, bool last) {
-    if (last_warp_done(done, cur, nwarps)) {
-      if ((threadIdx.x & 31) == 0) fence_proxy_async_smem();
-      __syncwarp();
-      issue(b, tile, cur, last);
-    }
+  // This warp has read the current stage, which takes `tile` of b next.
+  __device__ __forceinline__ void refill(int b, int tile, bool keep) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + cur);
+    pstage = cur;
+    pb = b;
+    ptile = tile;
+    pkeep = keep;
   }
   __device__ __forceinline__ const uint4 *stage(int tensor) const {
     return reinterpret_cast<const uint4 *>(base + static_cast<size_t>(cur) * L.stage_bytes +
@@ -129,10 +153,12 @@ struct Ring {
   // First pass over sample b: body(first row of the tile, its rows).
   template <typename Body>
   __device__ __forceinline__ void first_pass(int b, Body body) {
+#pragma unroll 1
     for (int j = 0; j < T; ++j) {
+      flush();
       wait();
       body(j * TR, rows_of(j));
-      if (j + a.stages < T) refill(b, j + a.stages, false);
+      if (j + a.stages < T) refill(b, j + a.stages, kept(j + a.stages));
       if (j + 1 < T) step();
     }
     dir = -dir;
@@ -141,13 +167,15 @@ struct Ring {
   // CTA's next round, or -1.
   template <typename Body>
   __device__ __forceinline__ void output_pass(int b, int next, Body body) {
+#pragma unroll 1
     for (int i = 0; i < T; ++i) {
+      flush();
       if (i >= a.stages) wait();
       const int tile = T - 1 - i;
       body(tile * TR, rows_of(tile));
       const int again = tile - a.stages;  // tile to read again, or the next round's -again - 1
-      if (again >= 0) refill(b, again, true);
-      else if (next >= 0 && -again - 1 < T) refill(next, -again - 1, false);
+      if (again >= 0) refill(b, again, false);
+      else if (next >= 0 && -again - 1 < T) refill(next, -again - 1, kept(-again - 1));
       step();
     }
   }
@@ -182,6 +210,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   float *chq = chm + a.ncs * V;
   float2 *gfin = reinterpret_cast<float2 *>(smem + ring.L.gst_off);
   float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
+  const int pstride = (a.splits + 1) & ~1;  // (rows of partials start on 16 bytes)
   const Parts parts(a.S, a.splits);
   const float invS = 1.0f / static_cast<float>(a.S);
   const float fD = static_cast<float>(a.D);
@@ -189,8 +218,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   const DropGen gen(a.drop);
   auto grid = cooperative_groups::this_grid();
 
-  if (tid < 32 && role.sj < a.B)
-    for (int j = 0; j < min(a.stages, ring.T); ++j) ring.issue(role.sj, j, j, false);
+  if (role.sj < a.B) ring.start(role.sj);
 
   for (int round = 0; round < a.rounds; ++round) {
     const int b = round * a.nsamp + role.sj;
@@ -221,43 +249,53 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
       // splits side by side
       groups_of_channels(chm, chq, ng, a.D, a.lsh, static_cast<float>(ring.nrow),
                          [&](int g, float m, float m2) {
-                           gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * a.splits + role.sp] =
+                           gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * pstride + role.sp] =
                                make_float2(m, m2);
                          });
     }
     grid.sync();
     if (b < a.B) {
       each_group(ng, a.lsh, [&](int g, int l, bool in) {
-        const float2 *part = gpart + (static_cast<int64_t>(b) * a.G + g0 + g) * a.splits;
-        // the mean first, then the deviations from it; a lane's first
-        // kNear splits stay in registers in between
-        constexpr int kNear = 12;
-        float2 v[kNear];
+        const float2 *part = gpart + (static_cast<int64_t>(b) * a.G + g0 + g) * pstride;
+        // two splits per load; the mean first, then the deviations from it,
+        // a lane's first kNear pairs staying in registers in between
+        constexpr int kNear = 6;
+        float4 v[kNear];
         float m = 0.f, m2 = 0.f;
 #pragma unroll
         for (int i = 0; i < kNear; ++i) {
-          const int r = l + (i << a.lsh);
-          v[i] = in && r < a.splits ? __ldcg(part + r) : splat2(0.f);
+          const int r = 2 * (l + (i << a.lsh));
+          v[i] = in && r < a.splits ? __ldcg(reinterpret_cast<const float4 *>(part + r))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll
-        for (int i = 0; i < kNear; ++i) {
-          const int r = l + (i << a.lsh);
-          if (r < a.splits) m = fmaf(static_cast<float>(parts.rows(r)), v[i].x, m);
-        }
-        const int far = in ? l + (kNear << a.lsh) : a.splits;
-        for (int r = far; r < a.splits; r += 1 << a.lsh)
-          m = fmaf(static_cast<float>(parts.rows(r)), __ldcg(part + r).x, m);
-        m = lanes_sum(m, a.lsh) * invS;
-        auto deviation = [&](int r, float2 u) {
+        auto mean_of = [&](int r, float4 u) {
+          m = fmaf(static_cast<float>(parts.rows(r)), u.x, m);
+          if (r + 1 < a.splits) m = fmaf(static_cast<float>(parts.rows(r + 1)), u.z, m);
+        };
+        auto deviation = [&](int r, float4 u) {
           const float e = u.x - m;
           m2 += fmaf(static_cast<float>(parts.rows(r)) * fD * e, e, u.y);
+          if (r + 1 < a.splits) {
+            const float f = u.z - m;
+            m2 += fmaf(static_cast<float>(parts.rows(r + 1)) * fD * f, f, u.w);
+          }
         };
 #pragma unroll
         for (int i = 0; i < kNear; ++i) {
-          const int r = l + (i << a.lsh);
+          const int r = 2 * (l + (i << a.lsh));
+          if (r < a.splits) mean_of(r, v[i]);
+        }
+        const int far = in ? 2 * (l + (kNear << a.lsh)) : a.splits;
+        for (int r = far; r < a.splits; r += 2 << a.lsh)
+          mean_of(r, __ldcg(reinterpret_cast<const float4 *>(part + r)));
+        m = lanes_sum(m, a.lsh) * invS;
+#pragma unroll
+        for (int i = 0; i < kNear; ++i) {
+          const int r = 2 * (l + (i << a.lsh));
           if (r < a.splits) deviation(r, v[i]);
         }
-        for (int r = far; r < a.splits; r += 1 << a.lsh) deviation(r, __ldcg(part + r));
+        for (int r = far; r < a.splits; r += 2 << a.lsh)
+          deviation(r, __ldcg(reinterpret_cast<const float4 *>(part + r)));
         m2 = lanes_sum(m2, a.lsh);
         if (in && l == 0) {
           const float rs = rsqrtf(m2 * invCount + a.eps);
@@ -316,12 +354,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   float *tg = tb + a.ncs * V;
   float2 *gfin = reinterpret_cast<float2 *>(smem + ring.L.gst_off);
   float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
+  const int pstride = (a.splits + 1) & ~1;  // (rows of partials start on 16 bytes)
   const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
   const DropGen gen(a.drop);
   auto grid = cooperative_groups::this_grid();
 
-  if (tid < 32 && role.sj < a.B)
-    for (int j = 0; j < min(a.stages, ring.T); ++j) ring.issue(role.sj, j, j, false);
+  if (role.sj < a.B) ring.start(role.sj);
 
   for (int round = 0; round < a.rounds; ++round) {
     const int b = round * a.nsamp + role.sj;
@@ -348,7 +386,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ring.ncs * V);
       __syncthreads();
       group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) {
-        gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * a.splits + role.sp] = v;
+        gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * pstride + role.sp] = v;
       });
       // running dgamma / dbeta of this CTA's rows over the rounds; after the
       // last one they are its partial row
@@ -374,11 +412,15 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
     grid.sync();
     if (b < a.B) {
       each_group(ng, a.lsh, [&](int g, int l, bool in) {
-        const float2 *part = gpart + (static_cast<int64_t>(b) * a.G + g0 + g) * a.splits;
+        const float2 *part = gpart + (static_cast<int64_t>(b) * a.G + g0 + g) * pstride;
         float2 t = splat2(0.f);
         if (in) {
 #pragma unroll 4
-          for (int r = l; r < a.splits; r += 1 << a.lsh) t = add2(t, __ldcg(part + r));
+          for (int r = 2 * l; r < a.splits; r += 2 << a.lsh) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + r));
+            t = add2(t, make_float2(v.x, v.y));
+            if (r + 1 < a.splits) t = add2(t, make_float2(v.z, v.w));
+          }
         }
         t.x = lanes_sum(t.x, a.lsh);
         t.y = lanes_sum(t.y, a.lsh);
@@ -422,13 +464,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
     float acc = 0.f;
     if (c < a.C) {
 #pragma unroll 4
-      for (int r = tid >> 5; r < P; r += ring.nwarps)
+      for (int r = tid >> 5; r < P; r += (static_cast<int>(blockDim.x) >> 5))
         acc += __ldcg(rows + static_cast<int64_t>(r) * a.C + c);
     }
     part[tid] = acc;
     __syncthreads();
     if (tid < 32 && c < a.C) {
-      for (int w = 1; w < ring.nwarps; ++w) acc += part[w * 32 + lane];
+      for (int w = 1; w < (static_cast<int>(blockDim.x) >> 5); ++w) acc += part[w * 32 + lane];
       (beta ? a.dbeta : a.dgamma)[c] = acc;
     }
     __syncthreads();

@@ -126,16 +126,6 @@ __device__ __forceinline__ void bulk_g2s(void *dst_smem, const void *src_gmem,
       : "memory");
 }
 
-// The same with the default L2 policy, for lines that are read again.
-__device__ __forceinline__ void bulk_g2s_keep(void *dst_smem, const void *src_gmem,
-                                              uint32_t bytes, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_addr(dst_smem)),
-      "l"(src_gmem), "r"(bytes), "r"(smem_addr(bar))
-      : "memory");
-}
-
 // 4-byte asynchronous copy global -> shared (non-bulk cp.async).
 __device__ __forceinline__ void cp_async_4(void *dst_smem, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
