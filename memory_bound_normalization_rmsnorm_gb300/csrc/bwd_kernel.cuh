@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_kernel(const NormArgs
 
   if (CLUSTER) cluster_sync(); else __syncthreads();
 
-  const DropGen gen = DROP ? DropGen(a.drop) : DropGen();
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   const float invN = a.invN;
   int rpar = 0;
   ClusterXch xch = make_xch(smem, L, a.RT, CLUSTER ? a.C : 1, crank);

@@ -21,7 +21,7 @@ constexpr int kXchBuffers = 4;
 // Dropout, by value (dropout.cuh).  thr = T << 16, T in [1, 65535] out of 2^16;
 // 0: none.
 struct DropArgs {
-  uint64_t seed;
+  uint32_t key[10][2];         // the generator's round keys: kernels read them as operands
   uint64_t offset;
   const uint64_t *offset_dev;  // device word added to offset, or null
   uint32_t thr;

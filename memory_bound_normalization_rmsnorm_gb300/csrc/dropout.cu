@@ -25,7 +25,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const void *x, vo
   constexpr int CB = 8 / V;  // 16-byte chunks per block
   grid_launch_dependents();
   grid_dependency_wait();
-  const DropGen gen(d);
+  DropGen gen(d);
+  gen.start();
   const int64_t full = n >> 3;
   const int64_t first =
       static_cast<int64_t>(blockIdx.x) * (kDropThreads * kDropUnroll) + threadIdx.x;
@@ -84,7 +85,13 @@ norm_status_t make_drop(float p, uint64_t seed, uint64_t offset, const void *off
   const uint32_t T = static_cast<uint32_t>(static_cast<double>(p) * 65536.0 + 0.5);
   if (T > 65535) return NORM_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(offset_dev) & 7u) return NORM_ERR_ALIGN;
-  out->seed = seed;
+  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+  for (auto &key : out->key) {
+    key[0] = k0;
+    key[1] = k1;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
   out->offset = offset;
   out->offset_dev = static_cast<const uint64_t *>(offset_dev);
   out->thr = T << 16;

@@ -12,7 +12,7 @@
 // the comparison keeps, so the expectation is the input's whatever p.
 //
 // Sixteen bits per element, so one generator call serves one 16-byte chunk
-// of bf16: the call is about 65 issue slots, 8 per element instead of 16
+// of bf16: the call is about 45 issue slots, 6 per element instead of 11
 // with 32 bits, which is what keeps plain dropout (4 bytes per element, 21
 // issue slots per element at the measured copy bandwidth) memory-bound.
 // The price is that p is held to the nearest multiple of 2^-16.
@@ -23,13 +23,12 @@ namespace gbn {
 
 // The generator of one kernel argument.
 struct DropGen {
-  uint32_t k0, k1, o0, o1, thr;
-  float scale;
+  const DropArgs &a;
+  uint32_t o0, o1;
 
-  __device__ __forceinline__ DropGen() : k0(0), k1(0), o0(0), o1(0), thr(0), scale(1.f) {}
-  __device__ __forceinline__ explicit DropGen(const DropArgs &a)
-      : k0(static_cast<uint32_t>(a.seed)), k1(static_cast<uint32_t>(a.seed >> 32)), thr(a.thr),
-        scale(a.scale) {
+  __device__ __forceinline__ explicit DropGen(const DropArgs &args) : a(args), o0(0), o1(0) {}
+  // Reads the offset word (after the previous kernel's writes are visible).
+  __device__ __forceinline__ void start() {
     uint64_t o = a.offset;
     if (a.offset_dev) o += *a.offset_dev;
     o0 = static_cast<uint32_t>(o);
@@ -39,17 +38,14 @@ struct DropGen {
   // The four words of block `i`.
   __device__ __forceinline__ uint4 words(uint64_t i) const {
     uint32_t c0 = static_cast<uint32_t>(i), c1 = static_cast<uint32_t>(i >> 32), c2 = o0, c3 = o1;
-    uint32_t a = k0, b = k1;
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
       const uint64_t m0 = static_cast<uint64_t>(c0) * 0xD2511F53u;
       const uint64_t m1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-      c0 = static_cast<uint32_t>(m1 >> 32) ^ c1 ^ a;
+      c0 = static_cast<uint32_t>(m1 >> 32) ^ c1 ^ a.key[r][0];
       c1 = static_cast<uint32_t>(m1);
-      c2 = static_cast<uint32_t>(m0 >> 32) ^ c3 ^ b;
+      c2 = static_cast<uint32_t>(m0 >> 32) ^ c3 ^ a.key[r][1];
       c3 = static_cast<uint32_t>(m0);
-      a += 0x9E3779B9u;
-      b += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
   }
@@ -57,8 +53,8 @@ struct DropGen {
   // Dropout of the pair whose halves are word w.  A dropped element is 0
   // whatever its value (infinities and NaN included), so this selects.
   __device__ __forceinline__ float2 pair(float2 v, uint32_t w) const {
-    const float2 s = mul2(v, splat2(scale));
-    return make_float2((w << 16) >= thr ? s.x : 0.f, w >= thr ? s.y : 0.f);
+    const float2 s = mul2(v, splat2(a.scale));
+    return make_float2((w << 16) >= a.thr ? s.x : 0.f, w >= a.thr ? s.y : 0.f);
   }
 
   // Dropout of the 16-byte chunk of V elements that starts at element

@@ -123,7 +123,7 @@ norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int s
   }
   p.ncs = p.sg * D / V;
   p.nslab = (G + p.sg - 1) / p.sg;
-  const int U = nt == 1 ? 4 : 2;
+  const int U = nt == 1 ? kRingRowsFwd : kRingRowsBwd;
   p.R = std::max(1, std::min(kGroupThreads / p.ncs, (S + U - 1) / U));
   if (ov.R) p.R = std::min(p.R, ov.R);
   p.threads = round32(p.ncs * p.R);
@@ -351,7 +351,7 @@ norm_status_t run_ring(int dev, int optin, const GroupPlan &p, int dt, int act, 
   const void *fn = group_ring_kernel_ptr(dt, act, drop, bwd);
   norm_status_t st = function_ready(dev, fn, optin);
   if (st != NORM_OK) return st;
-  a.U = bwd ? 2 : 4;
+  a.U = bwd ? kRingRowsBwd : kRingRowsFwd;
   a.err = err;
   void *args[] = {&a};
   return launch_cooperative(fn, dim3(static_cast<unsigned>(p.grid)), dim3(p.threads), p.smem, args,

@@ -29,6 +29,9 @@ constexpr int kActSilu = 1;  // k = z
 constexpr int kActGelu = 2;  // k = 2 sqrt(2 / pi) (z + 0.044715 z^3): the tanh form
 
 constexpr int kGroupThreads = 512;  // largest CTA of these kernels
+// Ring: rows per thread and tile.
+constexpr int kRingRowsFwd = 8;
+constexpr int kRingRowsBwd = 4;
 
 struct GroupArgs {
   const void *x;      // [B, S, C]

@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
 
   BwdConst<V> k;
   if (on) load_const<DT>(a, b, chunk0 + cc, k);
-  const DropGen gen(a.drop);
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   float2 s1[V / 2], s2[V / 2];
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   }
 
   const int ch0 = chunk0 * V;
+  if (on) scale_by_rstd<DT>(a, b, chunk0 + cc, s2);
   channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ncs_me * V);
   __syncthreads();
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
       for (int r = 0; r < a.k; ++r) t = add2(t, ld_cluster_f2(gst + g, r));
     }
     const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
-    gfin[g] = make_float2(-rs * (t.x * inv), -rs * (t.y * inv));
+    gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
   }
   // dgamma / dbeta row of this sample: CTA q sums every k-th channel pair of
   // the slab over the cluster, in rank order.
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
 
   grid_launch_dependents();
   grid_dependency_wait();
-  const DropGen gen(a.drop);
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
 
   for (int col = 0; col < a.nc; col += a.ncs) {
     const bool on = rl < a.R && cc < min(a.ncs, a.nc - col);
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
       const int64_t e = (c0 + i * step) * V;
       sum_rows<DT, ACT, DROP>(xv, dv, xv, dv, false, k, gen, e, e, s1, s2);
     }
+    if (on) scale_by_rstd<DT>(a, b, col + cc, s2);
     channel_sums<V>(s1, s2, fold, cb + col * V, cg + col * V, a.R, rl, cc, a.ncs, on,
                     min(a.ncs, a.nc - col) * V);
     __syncthreads();  // the fold buffer is free again
@@ -229,12 +233,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
     t.y = warp_sum(t.y);
     if (lane == 0) {
       const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g);
-      gfin[g] = make_float2(-rs * (t.x * inv), -rs * (t.y * inv));
+      gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
     }
   }
   __syncthreads();
 
-  const DropGen gen(a.drop);
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   for (int col = 0; col < a.nc; col += a.ncs) {
     if (rl >= a.R || cc >= min(a.ncs, a.nc - col) || rl >= nrow) continue;
     const int nr = (nrow - rl + a.R - 1) / a.R;

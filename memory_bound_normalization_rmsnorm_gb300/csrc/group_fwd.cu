@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   if (nr) {
     float2 nmu[V / 2], sc[V / 2], bf[V / 2];
     out_constants<DT>(a, gfin, g0, chunk0 + cc, nmu, sc, bf);
-    const DropGen gen(a.drop);
+    DropGen gen(a.drop);
+  if (DROP) gen.start();
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
 #pragma unroll 2
     for (int i = 0; i < nr; i += 2) {
@@ -224,7 +225,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
   }
   __syncthreads();
 
-  const DropGen gen(a.drop);
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   for (int col = 0; col < a.nc; col += a.ncs) {
     if (rl >= a.R || cc >= min(a.ncs, a.nc - col) || rl >= nrow) continue;
     const int nr = (nrow - rl + a.R - 1) / a.R;

@@ -196,7 +196,7 @@ template <int DT, int ACT, bool DROP>
 __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const GroupArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
-  constexpr int U = 4;  // rows per thread and tile: one block of the statistics
+  constexpr int U = kRingRowsFwd;
   const Role role(a);
   Ring<DT, 1> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   const float invS = 1.0f / static_cast<float>(a.S);
   const float fD = static_cast<float>(a.D);
   const float invCount = 1.0f / (static_cast<float>(a.S) * fD);
-  const DropGen gen(a.drop);
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   auto grid = cooperative_groups::this_grid();
 
   if (role.sj < a.B) ring.start(role.sj);
@@ -231,10 +232,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
         const uint4 *t = ring.stage(0) + rl * a.ncs + cc;
         const int step = a.R * a.ncs;
         if (rl + (U - 1) * a.R < rows) {
-          float2 f[U][V / 2];
 #pragma unroll
-          for (int u = 0; u < U; ++u) unpack<DT>(t[u * step], f[u]);
-          st.add4(f[0], f[1], f[2], f[3]);
+          for (int h = 0; h < U; h += 4) {
+            float2 f[4][V / 2];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) unpack<DT>(t[(h + u) * step], f[u]);
+            st.add4(f[0], f[1], f[2], f[3]);
+          }
         } else {
           for (int u = 0; rl + u * a.R < rows; ++u) {
             float2 f[V / 2];
@@ -336,7 +340,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
 template <int DT, int ACT, bool DROP>
 __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const GroupArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int V = chunk_elems(DT);  // (two rows per thread and tile)
+  constexpr int V = chunk_elems(DT);
+  constexpr int U = kRingRowsBwd;
   const Role role(a);
   Ring<DT, 2> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
@@ -356,7 +361,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
   const int pstride = (a.splits + 1) & ~1;  // (rows of partials start on 16 bytes)
   const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
-  const DropGen gen(a.drop);
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   auto grid = cooperative_groups::this_grid();
 
   if (role.sj < a.B) ring.start(role.sj);
@@ -374,15 +380,23 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
 #pragma unroll
       for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
       ring.first_pass(b, [&](int first, int rows) {
-        if (!on || rl >= rows) return;
+        if (!on) return;
         const int step = a.R * a.ncs;
         const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
         const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
-        const bool two = rl + a.R < rows;
-        const int o = two ? step : 0;
-        const int64_t e = e0 + static_cast<int64_t>(first) * a.C;
-        sum_rows<DT, ACT, DROP>(tx[0], td[0], tx[o], td[o], two, k, gen, e, e + estep, s1, s2);
+        int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+          if (rl + u * a.R < rows) {
+            const bool two = rl + (u + 1) * a.R < rows;
+            const int o = (u + (two ? 1 : 0)) * step;
+            sum_rows<DT, ACT, DROP>(tx[u * step], td[u * step], tx[o], td[o], two, k, gen, e,
+                                    e + estep, s1, s2);
+          }
+          e += 2 * estep;
+        }
       });
+      if (on) scale_by_rstd<DT>(a, b, ring.chunk0 + cc, s2);
       channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ring.ncs * V);
       __syncthreads();
       group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) {
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
         t.y = lanes_sum(t.y, a.lsh);
         if (in && l == 0) {
           const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
-          gfin[g] = make_float2(-rs * (t.x * inv), -rs * (t.y * inv));
+          gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
         }
       });
       __syncthreads();
@@ -434,17 +448,23 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       if (on) dx_constants<DT>(a, gfin, g0, ring.chunk0 + cc, ra, rc);
       unsigned char *out = static_cast<unsigned char *>(a.out);
       ring.output_pass(b, next, [&](int first, int rows) {
-        if (!on || rl >= rows) return;
+        if (!on) return;
         const int step = a.R * a.ncs;
         const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
         const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
-        const bool two = rl + a.R < rows;
-        const int o = two ? step : 0;
-        const int64_t e = e0 + static_cast<int64_t>(first) * a.C;
-        uint4 xa = tx[0], xb = tx[o];
-        dx_rows<DT, ACT, DROP>(xa, td[0], xb, td[o], k, ra, rc, gen, e, e + estep);
-        st_global_cs_v4(out + e * elem_bytes(DT), xa);
-        if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), xb);
+        int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+#pragma unroll
+        for (int u = 0; u < U; u += 2) {
+          if (rl + u * a.R < rows) {
+            const bool two = rl + (u + 1) * a.R < rows;
+            const int o = (u + (two ? 1 : 0)) * step;
+            uint4 xa = tx[u * step], xb = tx[o];
+            dx_rows<DT, ACT, DROP>(xa, td[u * step], xb, td[o], k, ra, rc, gen, e, e + estep);
+            st_global_cs_v4(out + e * elem_bytes(DT), xa);
+            if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), xb);
+          }
+          e += 2 * estep;
+        }
       });
     }
   }

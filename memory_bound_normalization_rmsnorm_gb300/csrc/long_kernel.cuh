@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_fwd_long_kernel(const Nor
     }
   }
 
-  const DropGen gen = DROP ? DropGen(a.drop) : DropGen();
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   const float invN = a.invN;
   const int cstep = a.tpr * 16;
   int rpar = 0;
@@ -546,7 +547,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_long_kernel(const Nor
     }
   }
 
-  const DropGen gen = DROP ? DropGen(a.drop) : DropGen();
+  DropGen gen(a.drop);
+  if (DROP) gen.start();
   const float invN = a.invN;
   const int cstep = a.tpr * 16;
   int rpar = 0;

@@ -154,7 +154,7 @@ def test_group_plans_in_bounds(override, monkeypatch):
                 if p["form"] == 2:
                     # one CTA per SM, all resident; every sample in one round;
                     # no CTA with fewer tiles than stages when the ring goes on
-                    n, sp, TR = p["samples_per_round"], p["row_splits"], (2 if bwd else 4) * R
+                    n, sp, TR = p["samples_per_round"], p["row_splits"], (4 if bwd else 8) * R
                     assert p["grid"] == n * p["slabs"] * sp <= SMS, label
                     assert (p["rounds"] - 1) * n < B <= p["rounds"] * n and sp <= S, label
                     assert 1 <= p["stages"] <= 31, label
