@@ -75,28 +75,42 @@ int ctas_per_sm(int threads, int64_t smem, int smem_optin) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(by_smem, by_regs), 16)));
 }
 
-// Estimated time (us) of a resident plan; the streamed form's estimate is
-// stream_cost.  Constants measured on GB300.
-double resident_cost(const GroupPlan &p, int64_t bytes, int seg_bytes, int sms, int smem_optin) {
+// Estimated times (us), for choosing among the plans of a shape.  Form of the
+// estimate: memory time at the measured bandwidth (less for slabs narrower
+// than 128 bytes of a row and where few SMs work), issue time (an element
+// takes about 20 instructions forward, 15 backward and pass), and fixed times
+// per launch, cluster, fold level, row of a thread and wave.  The constants
+// were fitted to about 1500 measured plans of 38 shapes (1 to 5000 samples, 1
+// to 65536 positions, 64 to 2560 channels, both directions, 16 and 32 bits):
+// the plan of least estimate is within 1 % of the fastest measured one in the
+// geometric mean (a rule of one wave of widest CTAs was 8 % off).
+double resident_cost(const GroupPlan &p, double elems, double bytes, bool bwd, int seg_bytes,
+                     int sms, int smem_optin) {
   const int occ = ctas_per_sm(p.threads, p.smem, smem_optin);
-  // clusters of 8 reach about 120 of the 152 SMs
-  const double usable = p.k >= 8 ? sms * 0.79 : (p.k >= 4 ? sms * 0.94 : sms);
+  const double usable = sms * (p.k >= 8 ? 0.79 : p.k >= 4 ? 0.94 : 1.0);  // clusters fragment
   const double waves = std::ceil(static_cast<double>(p.grid) / (usable * occ));
   const double used = std::min(usable, static_cast<double>(p.grid));
-  const double seg = seg_bytes >= 128 ? 1.0 : seg_bytes >= 64 ? 0.9 : seg_bytes >= 32 ? 0.75 : 0.5;
-  const double rate = 6.6e6 * seg * std::min(1.0, used / (0.7 * sms));  // bytes per us
-  return bytes / rate + waves * 2.5 + (p.k > 1 ? 0.7 : 0.0);
+  const double conc = std::min<double>(occ, std::ceil(static_cast<double>(p.grid) / usable));
+  const double seg = seg_bytes >= 128 ? 1.0 : seg_bytes >= 64 ? 0.9 : seg_bytes >= 32 ? 0.75 : 0.55;
+  const double mem = bytes / (6.6e6 * seg * std::min(1.0, used / (0.7 * sms)));
+  const double warps = conc * p.threads / 32;
+  const double issue = elems * (bwd ? 0.26e-6 : 0.35e-6) * sms / used /
+                       std::min(1.0, std::pow(warps / 16.0, 0.26));
+  const double level = p.R > 8 ? std::log2(p.R / 8.0) : p.R > 1 ? 1.0 : 0.0;
+  return 3.0 + (bwd ? 1.0 : 0.0) + (p.k > 1 ? 1.8 : 0.0) + (p.k >= 8 ? 0.7 : 0.0) + 0.18 * level +
+         (bwd ? 0.124 : 0.062) * p.slots +
+         (mem + issue) * (1.0 + 0.55 * (waves > 1 ? 1.0 / conc : 1.0)) + 1.5 * (waves - 1);
 }
 
-// Bytes of the first pass that are still near (shared memory and L2) when
-// the output pass comes to them.
-constexpr double kNearBytes = 80e6;
+// Bytes of a round's first pass that are still near (shared memory and L2)
+// when the output pass comes to them.
+constexpr double kNearBytes = 100e6;
 
-double ring_cost(const GroupPlan &p, int64_t bytes, int64_t read_bytes, int sms) {
-  const double per_round = static_cast<double>(read_bytes) / p.rounds;
-  const double again = std::max(0.0, per_round - kNearBytes) * p.rounds;
-  const double used = static_cast<double>(p.grid) / sms;
-  return (bytes + again) / (6.6e6 * std::min(1.0, used / 0.7)) + 3.0 * p.rounds + 4.0;
+double ring_cost(const GroupPlan &p, double elems, double bytes, double read_bytes, bool bwd,
+                 int sms) {
+  const double again = std::max(0.0, read_bytes / p.rounds - kNearBytes) * p.rounds;
+  const double issue = elems * (bwd ? 0.26e-6 : 0.35e-6) * 0.8 * sms / static_cast<double>(p.grid);
+  return 3.0 + 12.0 * p.rounds + (bytes + again) / 6.6e6 + issue;
 }
 
 // What L2 is asked to hold of it.
@@ -104,10 +118,10 @@ constexpr int64_t kL2KeepBytes = 64 << 20;
 
 // Ring plan (group_ring.cu): slabs as wide as a CTA has threads for (whole
 // rows where they fit), as many stages as shared memory holds, and rounds of
-// as many samples as stay near.
+// at most n samples.
 norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int sms, int smem_optin,
-                             const GroupOverride &ov, GroupPlan *out) {
-  const int V = chunk_elems(dt), es = elem_bytes(dt), nt = bwd ? 2 : 1;
+                             const GroupOverride &ov, int64_t n, GroupPlan *out) {
+  const int V = chunk_elems(dt), nt = bwd ? 2 : 1;
   const int D = C / G, nc = C / V;
   const int sgu = 8 / std::gcd(D, 8);
   const int64_t unit = static_cast<int64_t>(sgu) * D / V;  // chunks of the narrowest slab
@@ -128,9 +142,6 @@ norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int s
   if (ov.R) p.R = std::min(p.R, ov.R);
   p.threads = round32(p.ncs * p.R);
   const int TR = U * p.R;
-  const int64_t sample = static_cast<int64_t>(S) * C * es * nt;
-  int64_t n = std::max<int64_t>(1, static_cast<int64_t>(kNearBytes * 0.8) / sample);
-  if (ov.nsamp) n = ov.nsamp;
   n = std::min<int64_t>(n, std::min(B, sms / p.nslab));
   if (n < 1) return NORM_ERR_UNSUPPORTED;
   p.rounds = static_cast<int>((B + n - 1) / n);
@@ -164,8 +175,8 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
   const int V = chunk_elems(dt), es = elem_bytes(dt), nt = bwd ? 2 : 1;
   const int D = C / G;
   const int nc = C / V;
-  const int64_t n = static_cast<int64_t>(B) * S * C;
-  const int64_t bytes = n * es * (nt + 1);
+  const double elems = static_cast<double>(B) * S * C;
+  const double bytes = elems * es * (nt + 1);
   GroupPlan best;
   double best_cost = -1.0;
   // Resident: slabs of `sg` groups whose channels are a multiple of 8 (so a
@@ -183,44 +194,53 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
       if (ncs > kGroupThreads) continue;
       for (int k = 1; k <= 8 && k <= S; k *= 2) {
         if (ov.k && k != ov.k) continue;
-        GroupPlan p;
-        p.sg = sg;
-        p.ncs = ncs;
-        p.nslab = (G + sg - 1) / sg;
-        p.k = k;
         const int rows = static_cast<int>(ceil_div64(S, k));
         const int rmax = std::min(kGroupThreads / ncs, std::max(1, S / k));
-        // at least four rows per thread (one block of the statistics)
-        p.R = std::max(1, std::min(rmax, (rows + 3) / 4));
-        if (ov.R) p.R = std::min(rmax, ov.R);
-        p.slots = (rows + p.R - 1) / p.R;
-        p.threads = round32(ncs * p.R);
-        const int64_t data = static_cast<int64_t>(p.slots) * ncs * p.R * 16 * nt;
-        if (data > smem_optin) continue;
-        p.smem = group_smem_bytes(p.slots, nt, p.R, ncs, V, sg);
-        if (static_cast<int64_t>(p.smem) > smem_optin) continue;
-        p.grid = static_cast<int64_t>(B) * p.nslab * k;
-        if (p.grid > 0x7fffffff) continue;
-        const double c = resident_cost(p, bytes, ncs * 16, sms, smem_optin);
-        if (best_cost < 0 || c < best_cost) {
-          best_cost = c;
-          best = p;
+        // row lanes: all that a CTA has threads for, then fewer (several
+        // smaller CTAs per SM overlap their loads, folds and stores)
+        for (int R = ov.R ? std::min(rmax, ov.R) : rmax; R >= 1; R = R / 2) {
+          GroupPlan p;
+          p.sg = sg;
+          p.ncs = ncs;
+          p.nslab = (G + sg - 1) / sg;
+          p.k = k;
+          p.R = R;
+          p.slots = (rows + R - 1) / R;
+          p.threads = round32(ncs * R);
+          const int64_t data = static_cast<int64_t>(p.slots) * ncs * R * 16 * nt;
+          p.grid = static_cast<int64_t>(B) * p.nslab * k;
+          if (data <= smem_optin && p.grid <= 0x7fffffff) {
+            p.smem = group_smem_bytes(p.slots, nt, R, ncs, V, sg);
+            if (static_cast<int64_t>(p.smem) <= smem_optin) {
+              const double c =
+                  resident_cost(p, elems, bytes, bwd, ncs * 16, sms, smem_optin);
+              if (best_cost < 0 || c < best_cost) {
+                best_cost = c;
+                best = p;
+              }
+            }
+          }
+          if (ov.R) break;
         }
       }
     }
     if (ov.form == 0 && best_cost < 0) return NORM_ERR_UNSUPPORTED;
   }
   if (ov.form < 0 || ov.form == 2) {
-    GroupPlan p;
-    const norm_status_t st = make_ring_plan(B, S, C, G, dt, bwd, sms, smem_optin, ov, &p);
-    if (st != NORM_OK && ov.form == 2) return st;
-    if (st == NORM_OK) {
-      const double c = ring_cost(p, bytes, n * es * nt, sms);
+    // rounds of all samples, a half of them, a quarter, ...
+    norm_status_t st = NORM_OK;
+    for (int64_t n = ov.nsamp ? ov.nsamp : B; n >= 1; n /= 2) {
+      GroupPlan p;
+      st = make_ring_plan(B, S, C, G, dt, bwd, sms, smem_optin, ov, n, &p);
+      if (st != NORM_OK) break;
+      const double c = ring_cost(p, elems, bytes, elems * es * nt, bwd, sms);
       if (best_cost < 0 || c < best_cost) {
         best_cost = c;
         best = p;
       }
+      if (ov.nsamp) break;
     }
+    if (best_cost < 0 && ov.form == 2) return st;
   }
   // Streamed: groups too wide for the others.
   if (best_cost < 0) {
