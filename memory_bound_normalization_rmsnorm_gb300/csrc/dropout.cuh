@@ -73,6 +73,29 @@ struct DropGen {
       v[1] = pair(v[1], hi ? w.w : w.y);
     }
   }
+
+  // Zeroes the dropped elements of a 16-byte chunk as it lies in memory (the
+  // kept ones still want the factor).
+  template <int DT>
+  __device__ __forceinline__ void mask(uint4 &c, uint64_t e) const {
+    const uint4 w = words(e >> 3);
+    if constexpr (DT == kFP32) {
+      const bool hi = (e & 4) != 0;
+      const uint32_t u = hi ? w.z : w.x, v = hi ? w.w : w.y;
+      c.x = (u << 16) >= a.thr ? c.x : 0u;
+      c.y = u >= a.thr ? c.y : 0u;
+      c.z = (v << 16) >= a.thr ? c.z : 0u;
+      c.w = v >= a.thr ? c.w : 0u;
+    } else {
+      auto kept = [&](uint32_t u) {
+        return ((u << 16) >= a.thr ? 0xffffu : 0u) | (u >= a.thr ? 0xffff0000u : 0u);
+      };
+      c.x &= kept(w.x);
+      c.y &= kept(w.y);
+      c.z &= kept(w.z);
+      c.w &= kept(w.w);
+    }
+  }
 };
 
 }  // namespace gbn

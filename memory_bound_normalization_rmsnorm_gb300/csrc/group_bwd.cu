@@ -67,24 +67,33 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   float2 s1[V / 2], s2[V / 2];
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
-  auto slot_x = [&](int i) { return data[static_cast<size_t>(2 * i) * nact]; };
-  auto slot_d = [&](int i) { return data[static_cast<size_t>(2 * i + 1) * nact]; };
+  auto slot_x = [&](int i) -> uint4 & { return data[static_cast<size_t>(2 * i) * nact]; };
+  auto slot_d = [&](int i) -> uint4 & { return data[static_cast<size_t>(2 * i + 1) * nact]; };
+  // dy of row i, its dropped elements zeroed -- in the slot too, so that the
+  // dx pass need not ask the generator again.
+  auto take_d = [&](int i) {
+    uint4 v = slot_d(i);
+    if (DROP) {
+      gen.template mask<DT>(v, static_cast<uint64_t>(e0 + i * estep));
+      slot_d(i) = v;
+    }
+    return v;
+  };
   const int npair = nr >> 1;
   for (int j = 0; j < npair; ++j) {
     cp_async_wait_upto(npair - j);
     const int i = 2 * j;
-    sum_rows<DT, ACT, DROP>(slot_x(i), slot_d(i), slot_x(i + 1), slot_d(i + 1), true, k, gen,
-                            e0 + i * estep, e0 + (i + 1) * estep, s1, s2);
+    const uint4 da = take_d(i), db = take_d(i + 1);
+    sum_rows<DT, ACT>(slot_x(i), da, slot_x(i + 1), db, true, k, s1, s2);
   }
   cp_async_wait<0>();
   if (nr & 1) {
-    const int i = nr - 1;
-    const uint4 xv = slot_x(i), dv = slot_d(i);
-    sum_rows<DT, ACT, DROP>(xv, dv, xv, dv, false, k, gen, e0 + i * estep, e0 + i * estep, s1, s2);
+    const uint4 xv = slot_x(nr - 1), dv = take_d(nr - 1);
+    sum_rows<DT, ACT>(xv, dv, xv, dv, false, k, s1, s2);
   }
 
   const int ch0 = chunk0 * V;
-  if (on) scale_by_rstd<DT>(a, b, chunk0 + cc, s2);
+  if (on) scale_sums<DT, DROP>(a, b, chunk0 + cc, s1, s2);
   channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ncs_me * V);
   __syncthreads();
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
@@ -128,8 +137,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
     for (int i = 0; i < nr; i += 2) {
       const int i2 = i + 1 < nr ? i + 1 : i;
       uint4 xa = slot_x(i), xb = slot_x(i2);
-      dx_rows<DT, ACT, DROP>(xa, slot_d(i), xb, slot_d(i2), k, ra, rc, gen, e0 + i * estep,
-                             e0 + i2 * estep);
+      dx_rows<DT, ACT, DROP>(a, xa, slot_d(i), xb, slot_d(i2), k, ra, rc);
       st_global_cs_v4(dst + i * bstep, xa);
       if (i2 != i) st_global_cs_v4(dst + i2 * bstep, xb);
     }
@@ -180,16 +188,19 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
         dv[u] = __ldg(ds + (i + u) * step);
       }
 #pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (DROP) gen.template mask<DT>(dv[u], static_cast<uint64_t>((c0 + (i + u) * step) * V));
+#pragma unroll
       for (int u = 0; u < 4; u += 2)
-        sum_rows<DT, ACT, DROP>(xv[u], dv[u], xv[u + 1], dv[u + 1], true, k, gen,
-                                (c0 + (i + u) * step) * V, (c0 + (i + u + 1) * step) * V, s1, s2);
+        sum_rows<DT, ACT>(xv[u], dv[u], xv[u + 1], dv[u + 1], true, k, s1, s2);
     }
     for (; i < nr; ++i) {
-      const uint4 xv = __ldg(xs + i * step), dv = __ldg(ds + i * step);
-      const int64_t e = (c0 + i * step) * V;
-      sum_rows<DT, ACT, DROP>(xv, dv, xv, dv, false, k, gen, e, e, s1, s2);
+      const uint4 xv = __ldg(xs + i * step);
+      uint4 dv = __ldg(ds + i * step);
+      if (DROP) gen.template mask<DT>(dv, static_cast<uint64_t>((c0 + i * step) * V));
+      sum_rows<DT, ACT>(xv, dv, xv, dv, false, k, s1, s2);
     }
-    if (on) scale_by_rstd<DT>(a, b, col + cc, s2);
+    if (on) scale_sums<DT, DROP>(a, b, col + cc, s1, s2);
     channel_sums<V>(s1, s2, fold, cb + col * V, cg + col * V, a.R, rl, cc, a.ncs, on,
                     min(a.ncs, a.nc - col) * V);
     __syncthreads();  // the fold buffer is free again
@@ -262,14 +273,19 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
         dv[u] = __ldcs(ds + c);
       }
       const int64_t c = c0 + (i - 1) * step;
-      dx_rows<DT, ACT, DROP>(xv[0], dv[0], xv[1], dv[1], k, ra, rc, gen, c * V, (c - step) * V);
+      if (DROP) {
+        gen.template mask<DT>(dv[0], static_cast<uint64_t>(c * V));
+        gen.template mask<DT>(dv[1], static_cast<uint64_t>((c - step) * V));
+      }
+      dx_rows<DT, ACT, DROP>(a, xv[0], dv[0], xv[1], dv[1], k, ra, rc);
       st_global_cs_v4(dst + c, xv[0]);
       st_global_cs_v4(dst + c - step, xv[1]);
     }
     if (i == 1) {
       uint4 xa = __ldcs(xs + c0), xb = xa;
-      const uint4 dv = __ldcs(ds + c0);
-      dx_rows<DT, ACT, DROP>(xa, dv, xb, dv, k, ra, rc, gen, c0 * V, c0 * V);
+      uint4 dv = __ldcs(ds + c0);
+      if (DROP) gen.template mask<DT>(dv, static_cast<uint64_t>(c0 * V));
+      dx_rows<DT, ACT, DROP>(a, xa, dv, xb, dv, k, ra, rc);
       st_global_cs_v4(dst + c0, xa);
     }
   }

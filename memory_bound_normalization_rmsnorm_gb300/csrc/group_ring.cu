@@ -145,19 +145,19 @@ struct Ring {
     ptile = tile;
     pkeep = keep;
   }
-  __device__ __forceinline__ const uint4 *stage(int tensor) const {
-    return reinterpret_cast<const uint4 *>(base + static_cast<size_t>(cur) * L.stage_bytes +
+  __device__ __forceinline__ uint4 *stage(int tensor) const {
+    return reinterpret_cast<uint4 *>(base + static_cast<size_t>(cur) * L.stage_bytes +
                                            tensor * L.tensor_bytes);
   }
 
-  // First pass over sample b: body(first row of the tile, its rows).
+  // First pass over sample b: body(tile, its rows).
   template <typename Body>
   __device__ __forceinline__ void first_pass(int b, Body body) {
 #pragma unroll 1
     for (int j = 0; j < T; ++j) {
       flush();
       wait();
-      body(j * TR, rows_of(j));
+      body(j, rows_of(j));
       if (j + a.stages < T) refill(b, j + a.stages, kept(j + a.stages));
       if (j + 1 < T) step();
     }
@@ -172,7 +172,7 @@ struct Ring {
       flush();
       if (i >= a.stages) wait();
       const int tile = T - 1 - i;
-      body(tile * TR, rows_of(tile));
+      body(tile, rows_of(tile));
       const int again = tile - a.stages;  // tile to read again, or the next round's -again - 1
       if (again >= 0) refill(b, again, false);
       else if (next >= 0 && -again - 1 < T) refill(next, -again - 1, kept(-again - 1));
@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
       const int64_t e0 = group_elem(a, b, ring.row0 + rl, ring.chunk0 + cc, V);
       const int64_t estep = static_cast<int64_t>(a.R) * a.C;
       unsigned char *out = static_cast<unsigned char *>(a.out);
-      ring.output_pass(b, next, [&](int first, int rows) {
+      ring.output_pass(b, next, [&](int tile, int rows) {
         if (!on) return;
         const uint4 *t = ring.stage(0) + rl * a.ncs + cc;
         const int step = a.R * a.ncs;
-        int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+        int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
 #pragma unroll
         for (int u = 0; u < U; u += 2) {
           const bool in1 = rl + u * a.R < rows, in2 = rl + (u + 1) * a.R < rows;
@@ -379,24 +379,35 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       float2 s1[V / 2], s2[V / 2];
 #pragma unroll
       for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
-      ring.first_pass(b, [&](int first, int rows) {
+      ring.first_pass(b, [&](int tile, int rows) {
         if (!on) return;
         const int step = a.R * a.ncs;
         const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
-        const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
-        int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+        uint4 *td = ring.stage(1) + rl * a.ncs + cc;
+        int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
+        // dropped elements of dy are zeroed; in a tile that stays, in the
+        // stage too, so that the dx pass need not ask the generator again
+        const bool stays = tile >= ring.T - a.stages;
 #pragma unroll
         for (int u = 0; u < U; u += 2) {
           if (rl + u * a.R < rows) {
             const bool two = rl + (u + 1) * a.R < rows;
             const int o = (u + (two ? 1 : 0)) * step;
-            sum_rows<DT, ACT, DROP>(tx[u * step], td[u * step], tx[o], td[o], two, k, gen, e,
-                                    e + estep, s1, s2);
+            uint4 da = td[u * step], db = td[o];
+            if (DROP) {
+              gen.template mask<DT>(da, static_cast<uint64_t>(e));
+              gen.template mask<DT>(db, static_cast<uint64_t>(e + estep));
+              if (stays) {
+                td[u * step] = da;
+                if (two) td[o] = db;
+              }
+            }
+            sum_rows<DT, ACT>(tx[u * step], da, tx[o], db, two, k, s1, s2);
           }
           e += 2 * estep;
         }
       });
-      if (on) scale_by_rstd<DT>(a, b, ring.chunk0 + cc, s2);
+      if (on) scale_sums<DT, DROP>(a, b, ring.chunk0 + cc, s1, s2);
       channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ring.ncs * V);
       __syncthreads();
       group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) {
@@ -447,19 +458,24 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       float2 ra[V / 2], rc[V / 2];
       if (on) dx_constants<DT>(a, gfin, g0, ring.chunk0 + cc, ra, rc);
       unsigned char *out = static_cast<unsigned char *>(a.out);
-      ring.output_pass(b, next, [&](int first, int rows) {
+      ring.output_pass(b, next, [&](int tile, int rows) {
         if (!on) return;
         const int step = a.R * a.ncs;
         const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
         const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
-        int64_t e = e0 + static_cast<int64_t>(first) * a.C;
+        int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
+        const bool stayed = tile >= ring.T - a.stages;
 #pragma unroll
         for (int u = 0; u < U; u += 2) {
           if (rl + u * a.R < rows) {
             const bool two = rl + (u + 1) * a.R < rows;
             const int o = (u + (two ? 1 : 0)) * step;
-            uint4 xa = tx[u * step], xb = tx[o];
-            dx_rows<DT, ACT, DROP>(xa, td[u * step], xb, td[o], k, ra, rc, gen, e, e + estep);
+            uint4 xa = tx[u * step], xb = tx[o], da = td[u * step], db = td[o];
+            if (DROP && !stayed) {
+              gen.template mask<DT>(da, static_cast<uint64_t>(e));
+              gen.template mask<DT>(db, static_cast<uint64_t>(e + estep));
+            }
+            dx_rows<DT, ACT, DROP>(a, xa, da, xb, db, k, ra, rc);
             st_global_cs_v4(out + e * elem_bytes(DT), xa);
             if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), xb);
           }

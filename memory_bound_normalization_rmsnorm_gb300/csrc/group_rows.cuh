@@ -91,35 +91,37 @@ __device__ __forceinline__ void load_const(const GroupArgs &a, int b, int chunk,
   }
 }
 
-// sum of dz d -> sum of dz xhat.
-template <int DT>
-__device__ __forceinline__ void scale_by_rstd(const GroupArgs &a, int b, int chunk,
-                                              float2 (&s2)[chunk_elems(DT) / 2]) {
+// Sums of dz and dz d as sum_rows leaves them -> sums of dz and dz xhat.
+template <int DT, bool DROP>
+__device__ __forceinline__ void scale_sums(const GroupArgs &a, int b, int chunk,
+                                           float2 (&s1)[chunk_elems(DT) / 2],
+                                           float2 (&s2)[chunk_elems(DT) / 2]) {
   const float *rs = a.rstd + static_cast<int64_t>(b) * a.G;
   GroupWalk g(a, chunk * chunk_elems(DT));
 #pragma unroll
   for (int p = 0; p < chunk_elems(DT) / 2; ++p) {
     const int g0 = g.next(), g1 = g.next();
     s2[p] = mul2(s2[p], make_float2(__ldg(rs + g0), __ldg(rs + g1)));
+    if (DROP) {
+      s1[p] = mul2(s1[p], splat2(a.drop.scale));
+      s2[p] = mul2(s2[p], splat2(a.drop.scale));
+    }
   }
 }
 
-// d = x - mean and dz of the same chunk column in two rows.
-template <int DT, int ACT, bool DROP>
+// d = x - mean and dz of the same chunk column in two rows.  With dropout the
+// dropped elements of dy are 0 already and dz lacks the kept ones' factor.
+template <int DT, int ACT>
 __device__ __forceinline__ void grad_rows(
     const uint4 &xa, const uint4 &da, const uint4 &xb, const uint4 &db,
-    const BwdConst<chunk_elems(DT)> &k, const DropGen &gen, int64_t ea, int64_t eb,
-    float2 (&ca)[chunk_elems(DT) / 2], float2 (&dza)[chunk_elems(DT) / 2],
-    float2 (&cb)[chunk_elems(DT) / 2], float2 (&dzb)[chunk_elems(DT) / 2]) {
+    const BwdConst<chunk_elems(DT)> &k, float2 (&ca)[chunk_elems(DT) / 2],
+    float2 (&dza)[chunk_elems(DT) / 2], float2 (&cb)[chunk_elems(DT) / 2],
+    float2 (&dzb)[chunk_elems(DT) / 2]) {
   constexpr int V = chunk_elems(DT);
   unpack<DT>(xa, ca);
   unpack<DT>(da, dza);
   unpack<DT>(xb, cb);
   unpack<DT>(db, dzb);
-  if (DROP) {
-    gen.template chunk<V>(dza, static_cast<uint64_t>(ea));
-    gen.template chunk<V>(dzb, static_cast<uint64_t>(eb));
-  }
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) {
     ca[p] = add2(ca[p], k.nmu[p]);
@@ -133,18 +135,22 @@ __device__ __forceinline__ void grad_rows(
   }
 }
 
-// dx of the same chunk column in two rows, left in xa and xb.
+// dx of the same chunk column in two rows, left in xa and xb (dropped elements
+// of dy are 0 already).
 template <int DT, int ACT, bool DROP>
-__device__ __forceinline__ void dx_rows(uint4 &xa, const uint4 &da, uint4 &xb, const uint4 &db,
-                                        const BwdConst<chunk_elems(DT)> &k,
+__device__ __forceinline__ void dx_rows(const GroupArgs &a, uint4 &xa, const uint4 &da, uint4 &xb,
+                                        const uint4 &db, const BwdConst<chunk_elems(DT)> &k,
                                         const float2 (&ra)[chunk_elems(DT) / 2],
-                                        const float2 (&rc)[chunk_elems(DT) / 2],
-                                        const DropGen &gen, int64_t ea, int64_t eb) {
+                                        const float2 (&rc)[chunk_elems(DT) / 2]) {
   constexpr int V = chunk_elems(DT);
   float2 ca[V / 2], dza[V / 2], cb[V / 2], dzb[V / 2];
-  grad_rows<DT, ACT, DROP>(xa, da, xb, db, k, gen, ea, eb, ca, dza, cb, dzb);
+  grad_rows<DT, ACT>(xa, da, xb, db, k, ca, dza, cb, dzb);
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) {
+    if (DROP) {
+      dza[p] = mul2(dza[p], splat2(a.drop.scale));
+      dzb[p] = mul2(dzb[p], splat2(a.drop.scale));
+    }
     dza[p] = fma2(ca[p], rc[p], fma2(dza[p], k.sc[p], ra[p]));
     dzb[p] = fma2(cb[p], rc[p], fma2(dzb[p], k.sc[p], ra[p]));
   }
@@ -153,16 +159,15 @@ __device__ __forceinline__ void dx_rows(uint4 &xa, const uint4 &da, uint4 &xb, c
 }
 
 // Adds dz and dz d of two rows (`two`: the second counts) to the sums.
-template <int DT, int ACT, bool DROP>
+template <int DT, int ACT>
 __device__ __forceinline__ void sum_rows(const uint4 &xa, const uint4 &da, const uint4 &xb,
                                          const uint4 &db, bool two,
-                                         const BwdConst<chunk_elems(DT)> &k, const DropGen &gen,
-                                         int64_t ea, int64_t eb,
+                                         const BwdConst<chunk_elems(DT)> &k,
                                          float2 (&s1)[chunk_elems(DT) / 2],
                                          float2 (&s2)[chunk_elems(DT) / 2]) {
   constexpr int V = chunk_elems(DT);
   float2 ca[V / 2], dza[V / 2], cb[V / 2], dzb[V / 2];
-  grad_rows<DT, ACT, DROP>(xa, da, xb, db, k, gen, ea, eb, ca, dza, cb, dzb);
+  grad_rows<DT, ACT>(xa, da, xb, db, k, ca, dza, cb, dzb);
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) {
     s1[p] = add2(s1[p], dza[p]);
