@@ -302,7 +302,7 @@ norm_status_t norm_dropout_add_bwd(const void *dy, const void *dh, const void *h
  * pointer 16-byte aligned; outputs must not alias inputs.  Unknown act or
  * dtype: NORM_ERR_ARG.
  * Small samples take one kernel whose clusters of up to 8 CTAs hold slabs of
- * them in shared memory (the backward of several samples adds a fixed-order
+ * them in shared memory (the backward of a larger batch adds a fixed-order
  * reduction of dgamma / dbeta); large ones one cooperative kernel over the
  * whole GPU, which waits for its CTAs to see each other's partials; groups
  * wider than a CTA (lcm(C / groups, 8) channels above 512 16-byte chunks) a
@@ -348,6 +348,9 @@ typedef struct {
     int32_t slabs;           /* per sample */
     int32_t chunk_columns;   /* 16-byte columns per slab (streamed: per CTA) */
     int32_t cluster;         /* resident: CTAs sharing a slab's rows */
+    int32_t cluster_samples; /* resident backward: samples per cluster (all of
+                                a small batch, whose dgamma and dbeta then
+                                need no further reduction); else 1 */
     int32_t row_lanes;       /* rows a CTA works on side by side */
     int32_t rows_per_thread; /* resident: rows a thread holds (at most) */
     int32_t row_splits;      /* streamed, ring: row ranges per sample */

@@ -65,7 +65,8 @@ class Plan(ctypes.Structure):
 class GroupPlan(ctypes.Structure):
     """Mirror of norm_group_plan_t."""
     _fields_ = [(n, ctypes.c_int32) for n in
-                ("form", "groups_per_slab", "slabs", "chunk_columns", "cluster", "row_lanes",
+                ("form", "groups_per_slab", "slabs", "chunk_columns", "cluster", "cluster_samples",
+                 "row_lanes",
                  "rows_per_thread", "row_splits", "stages", "samples_per_round", "rounds",
                  "threads", "smem_bytes", "grid")] + [("workspace_bytes", ctypes.c_int64)]
 

@@ -22,10 +22,11 @@ namespace gbn {
 namespace {
 
 constexpr int kResident = 0, kStreamed = 1, kRing = 2;
+constexpr int kMaxCluster = 8;  // the portable size
 
 struct GroupPlan {
   int form = kResident;
-  int sg = 0, ncs = 0, nslab = 1, k = 1, R = 1, slots = 0, splits = 1;
+  int sg = 0, ncs = 0, nslab = 1, k = 1, cb = 1, R = 1, slots = 0, splits = 1;
   int stages = 0, nsamp = 0, rounds = 0, keep = 0;  // ring
   int threads = 0;
   int64_t grid = 0;
@@ -35,9 +36,9 @@ struct GroupPlan {
 
 // Shape override for sweeps and tests: GBNORM_GROUP="form=1,sg=4,k=2,R=8,
 // splits=3" (any subset; form 0 resident, 1 streamed, 2 ring; for the ring
-// also stages=, nsamp= and keep=).  Bypasses the cache.
+// also stages=, nsamp= and keep=; cb=1 one sample per cluster).  Bypasses the cache.
 struct GroupOverride {
-  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0, keep = -1;
+  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0, keep = -1, cb = 0;
   bool any = false;
 };
 
@@ -56,6 +57,7 @@ GroupOverride read_group_override() {
       else if (!std::strcmp(key, "stages")) o.stages = val;
       else if (!std::strcmp(key, "nsamp")) o.nsamp = val;
       else if (!std::strcmp(key, "keep")) o.keep = val;
+      else if (!std::strcmp(key, "cb")) o.cb = val;
       o.any = true;
     }
     s = std::strchr(s, ',');
@@ -84,10 +86,11 @@ int ctas_per_sm(int threads, int64_t smem, int smem_optin) {
 // to 65536 positions, 64 to 2560 channels, both directions, 16 and 32 bits):
 // the plan of least estimate is within 1 % of the fastest measured one in the
 // geometric mean (a rule of one wave of widest CTAs was 8 % off).
-double resident_cost(const GroupPlan &p, double elems, double bytes, bool bwd, int seg_bytes,
-                     int sms, int smem_optin) {
+double resident_cost(const GroupPlan &p, double elems, double bytes, bool bwd, bool reduce,
+                     int seg_bytes, int sms, int smem_optin) {
   const int occ = ctas_per_sm(p.threads, p.smem, smem_optin);
-  const double usable = sms * (p.k >= 8 ? 0.79 : p.k >= 4 ? 0.94 : 1.0);  // clusters fragment
+  const int cluster = p.k * p.cb;
+  const double usable = sms * (cluster > 4 ? 0.79 : cluster > 2 ? 0.94 : 1.0);  // they fragment
   const double waves = std::ceil(static_cast<double>(p.grid) / (usable * occ));
   const double used = std::min(usable, static_cast<double>(p.grid));
   const double conc = std::min<double>(occ, std::ceil(static_cast<double>(p.grid) / usable));
@@ -97,7 +100,8 @@ double resident_cost(const GroupPlan &p, double elems, double bytes, bool bwd, i
   const double issue = elems * (bwd ? 0.26e-6 : 0.35e-6) * sms / used /
                        std::min(1.0, std::pow(warps / 16.0, 0.26));
   const double level = p.R > 8 ? std::log2(p.R / 8.0) : p.R > 1 ? 1.0 : 0.0;
-  return 3.0 + (bwd ? 1.0 : 0.0) + (p.k > 1 ? 1.8 : 0.0) + (p.k >= 8 ? 0.7 : 0.0) + 0.18 * level +
+  return 3.0 + (reduce ? 3.0 : 0.0) + (cluster > 1 ? 1.8 : 0.0) + (cluster > 4 ? 0.7 : 0.0) +
+         0.18 * level +
          (bwd ? 0.124 : 0.062) * p.slots +
          (mem + issue) * (1.0 + 0.55 * (waves > 1 ? 1.0 / conc : 1.0)) + 1.5 * (waves - 1);
 }
@@ -204,6 +208,9 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
           p.ncs = ncs;
           p.nslab = (G + sg - 1) / sg;
           p.k = k;
+          // a small batch in one cluster: dgamma and dbeta come out of it
+          // whole, without a second launch
+          if (bwd && static_cast<int64_t>(B) * k <= kMaxCluster && ov.cb != 1) p.cb = B;
           p.R = R;
           p.slots = (rows + R - 1) / R;
           p.threads = round32(ncs * R);
@@ -213,7 +220,7 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
             p.smem = group_smem_bytes(p.slots, nt, R, ncs, V, sg);
             if (static_cast<int64_t>(p.smem) <= smem_optin) {
               const double c =
-                  resident_cost(p, elems, bytes, bwd, ncs * 16, sms, smem_optin);
+                  resident_cost(p, elems, bytes, bwd, bwd && B > p.cb, ncs * 16, sms, smem_optin);
               if (best_cost < 0 || c < best_cost) {
                 best_cost = c;
                 best = p;
@@ -327,7 +334,7 @@ GroupWs group_ws(const GroupPlan &p, int64_t B, int64_t C, int64_t G, bool bwd) 
   if (bwd) {
     w.P = static_cast<int>(p.form == kStreamed ? p.grid
                            : p.form == kRing   ? static_cast<int64_t>(p.nsamp) * p.splits
-                                               : B);
+                                               : B / p.cb);
     if (w.P > 1 || p.form == kRing) w.total += static_cast<size_t>(w.P) * C * 8;
   }
   return w;
@@ -346,6 +353,7 @@ GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_
   a.ncs = p.ncs;
   a.nslab = p.nslab;
   a.k = p.k;
+  a.cb = p.cb;
   a.R = p.R;
   a.slots = p.slots;
   a.splits = p.splits;
@@ -493,7 +501,7 @@ norm_status_t norm_group_bwd(const void *dy, const void *x, const void *gamma, c
   const bool dropping = drop.thr != 0;
   if (pl.form == kRing) return run_ring(dev, optin, pl, dtype, act, dropping, true, err, a, s);
   if (pl.form == kResident) {
-    st = run(dev, optin, group_bwd_kernel_ptr(dtype, act, dropping), pl, pl.smem, pl.k, a, s);
+    st = run(dev, optin, group_bwd_kernel_ptr(dtype, act, dropping), pl, pl.smem, pl.k * pl.cb, a, s);
   } else {
     st = run(dev, optin, group_sums_kernel_ptr(dtype, act, dropping), pl, pl.smem, 1, a, s);
     if (st == NORM_OK)
@@ -528,6 +536,7 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups, n
   out->slabs = p.nslab;
   out->chunk_columns = p.ncs;
   out->cluster = p.k;
+  out->cluster_samples = p.cb;
   out->row_lanes = p.R;
   out->rows_per_thread = p.slots;
   out->row_splits = p.splits;

@@ -52,7 +52,8 @@ struct GroupArgs {
   int sg;      // groups per slab
   int ncs;     // chunk columns per (full) slab
   int nslab;   // slabs per sample
-  int k;       // CTAs per cluster (row split of a unit)
+  int k;       // resident: CTAs that share a slab's rows
+  int cb;      // resident backward: samples per cluster (1 or B)
   int R;       // row lanes per CTA
   int slots;   // resident: rows per thread (at most)
   int splits;  // streamed and ring: row ranges per sample

@@ -22,10 +22,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   const int nthr = blockDim.x;
   const int tid = threadIdx.x;
   const int nact = a.ncs * a.R;  // threads that own a chunk column
-  const int unit = static_cast<int>(blockIdx.x) / a.k;
-  const int q = static_cast<int>(blockIdx.x) - unit * a.k;
-  const int b = unit / a.nslab;
-  const int slab = unit - b * a.nslab;
+  // A cluster owns a slab of cb samples (one, or all of a small batch), k CTAs
+  // each.
+  const int csize = a.cb * a.k;
+  const int unit = static_cast<int>(blockIdx.x) / csize;
+  const int rank = static_cast<int>(blockIdx.x) - unit * csize;
+  const int bl = rank / a.k;
+  const int q = rank - bl * a.k;
+  const int ub = unit / a.nslab;
+  const int b = ub * a.cb + bl;
+  const int slab = unit - ub * a.nslab;
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
   const int chunk0 = slab * a.ncs;
@@ -97,38 +103,38 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ncs_me * V);
   __syncthreads();
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
-  if (a.k > 1) cluster_sync(); else __syncthreads();
+  if (csize > 1) cluster_sync(); else __syncthreads();
   const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
   for (int g = tid; g < ng; g += nthr) {
     float2 t = gst[g];
     if (a.k > 1) {
       t = make_float2(0.f, 0.f);
-      for (int r = 0; r < a.k; ++r) t = add2(t, ld_cluster_f2(gst + g, r));
+      for (int r = 0; r < a.k; ++r) t = add2(t, ld_cluster_f2(gst + g, bl * a.k + r));
     }
     const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
     gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
   }
-  // dgamma / dbeta row of this sample: CTA q sums every k-th channel pair of
-  // the slab over the cluster, in rank order.
-  for (int j = q * nthr + tid; j < ncs_me * (V / 2); j += a.k * nthr) {
+  // dgamma / dbeta row of this cluster's samples: the CTAs share its channel
+  // pairs out among them and sum over the cluster in rank order.
+  for (int j = rank * nthr + tid; j < ncs_me * (V / 2); j += csize * nthr) {
     float2 tg = make_float2(0.f, 0.f), tb = tg;
     const float2 *pg = reinterpret_cast<const float2 *>(cg) + j;
     const float2 *pb = reinterpret_cast<const float2 *>(cb) + j;
-    if (a.k == 1) {
+    if (csize == 1) {
       tg = *pg;
       tb = *pb;
     } else {
-      for (int r = 0; r < a.k; ++r) {
+      for (int r = 0; r < csize; ++r) {
         tg = add2(tg, ld_cluster_f2(pg, r));
         tb = add2(tb, ld_cluster_f2(pb, r));
       }
     }
-    const int64_t at = static_cast<int64_t>(b) * a.C + ch0 + 2 * j;
+    const int64_t at = static_cast<int64_t>(ub) * a.C + ch0 + 2 * j;
     *reinterpret_cast<float2 *>(a.cpart + at) = tg;
     if (a.dbeta_part) *reinterpret_cast<float2 *>(a.dbeta_part + at) = tb;
   }
   __syncthreads();
-  if (a.k > 1) cluster_arrive_release();
+  if (csize > 1) cluster_arrive_release();
 
   if (nr) {
     float2 ra[V / 2], rc[V / 2];
@@ -142,7 +148,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
       if (i2 != i) st_global_cs_v4(dst + i2 * bstep, xb);
     }
   }
-  if (a.k > 1) cluster_wait_acquire();
+  if (csize > 1) cluster_wait_acquire();
 }
 
 // Streamed form, first pass: per-channel sums of one row range of one sample

@@ -125,7 +125,7 @@ def test_parity_resident_splits(shape, sg, k, monkeypatch):
     """Every cluster size, slabs narrower than the last one, one row lane."""
     B, S, C, G = shape
     x, g, b, dy = make(B, S, C, torch.bfloat16, seed=k)
-    for R in ("", ",R=1", ",R=3"):
+    for R in ("", ",R=1", ",R=3", ",cb=1"):
         monkeypatch.setenv("GBNORM_GROUP", f"form=0,sg={sg},k={k}{R}")
         plan = gb.norm_group_plan(B, S, C, G)
         assert plan["form"] == 0 and plan["cluster"] == k
@@ -335,8 +335,9 @@ def test_binding_refuses():
         gb.norm_group_fwd(x, g, b, 4, p=1.0)
     assert e.value.status == 9
     with pytest.raises(gb.NormError) as e:
-        gb.norm_group_bwd(dy, x, g, b, torch.ones(2, 4, device="cuda"),
-                          torch.zeros(2, 4, device="cuda"), 4,
+        many = x.repeat(10, 1, 1)  # a batch that one cluster does not hold
+        gb.norm_group_bwd(many, many, g, b, torch.ones(20, 4, device="cuda"),
+                          torch.zeros(20, 4, device="cuda"), 4,
                           workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 5
     with pytest.raises(gb.NormError) as e:

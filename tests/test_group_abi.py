@@ -172,6 +172,8 @@ def test_group_plans_in_bounds(override, monkeypatch):
                     continue
                 assert p["grid"] == B * p["slabs"] * p["cluster"], label
                 assert p["cluster"] in (1, 2, 4, 8) and p["cluster"] <= S, label
+                assert p["cluster_samples"] in (1, B) and (bwd or p["cluster_samples"] == 1)
+                assert p["cluster"] * p["cluster_samples"] <= 8, label
                 # rows: every CTA's range fits its threads' slots, and no row
                 # lane is empty
                 rows = [S * (i + 1) // p["cluster"] - S * i // p["cluster"]
@@ -180,5 +182,6 @@ def test_group_plans_in_bounds(override, monkeypatch):
                 assert R <= min(rows), label
                 data = p["rows_per_thread"] * ncs * R * 16 * nt
                 assert p["smem_bytes"] >= data + fold + 16 * p["groups_per_slab"], label
-                assert p["workspace_bytes"] == (B * C * 8 if bwd and B > 1 else 0), label
+                assert p["workspace_bytes"] == (
+                    B * C * 8 if bwd and B > p["cluster_samples"] else 0), label
     assert seen == ({0, 1, 2} if not override else {int(override[5])})
