@@ -438,7 +438,8 @@ __device__ __forceinline__ void channel_stats(ChannelStats<V> &st, unsigned char
   const int cap = fold_slots(R) * ncs, rows = fold_lanes(R);
   const float *f = reinterpret_cast<const float *>(buf);
   const float *cnt = f + 2 * V * cap;
-  const float inv = 1.0f / static_cast<float>(nrow);
+  const float inv = __fdividef(1.0f, static_cast<float>(nrow));
+#pragma unroll 1
   for (int j = threadIdx.x; j < nch; j += blockDim.x) {
     const unsigned u = static_cast<unsigned>(j);
     const int col = static_cast<int>(u / V), v = static_cast<int>(u % V);
@@ -484,6 +485,7 @@ __device__ __forceinline__ void channel_sums(float2 (&a)[V / 2], float2 (&b)[V /
   fold_sums<V>(a, b, buf, R, rl, cc, ncs, on);
   const int cap = fold_slots(R) * ncs, rows = fold_lanes(R);
   const float *f = reinterpret_cast<const float *>(buf);
+#pragma unroll 1
   for (int j = threadIdx.x; j < nch; j += blockDim.x) {
     const unsigned u = static_cast<unsigned>(j);
     const int col = static_cast<int>(u / V), v = static_cast<int>(u % V);
@@ -511,7 +513,9 @@ __device__ __forceinline__ float lanes_sum(float v, int lsh) {
 // Runs fn(g, lane, valid) with 2^lsh lanes per group, as many groups at a
 // time as the CTA has lanes for: all groups of a slab side by side, so that
 // the latencies of their folds (shared memory, L2, shuffles) overlap.  Every
-// lane of a warp takes part in every step.
+// lane of a warp takes part in every step.  (Loops with a stride known only
+// at run time stay rolled here: unrolling them costs an integer division for
+// the trip count, more than the few turns they take.)
 template <typename Fn>
 __device__ __forceinline__ void each_group(int ng, int lsh, Fn fn) {
   const int per = static_cast<int>(blockDim.x) >> lsh;
@@ -527,18 +531,22 @@ __device__ __forceinline__ void each_group(int ng, int lsh, Fn fn) {
 template <typename Out>
 __device__ __forceinline__ void groups_of_channels(const float *chm, const float *chq, int ng, int D,
                                                    int lsh, float n, Out out) {
-  const float inv = 1.0f / static_cast<float>(D);
+  const float inv = __fdividef(1.0f, static_cast<float>(D));
   each_group(ng, lsh, [&](int g, int l, bool in) {
     const float *m = chm + g * D, *q = chq + g * D;
     float s = 0.f, t = 0.f;
-    if (in)
+    if (in) {
+#pragma unroll 1
       for (int j = l; j < D; j += 1 << lsh) s += m[j];
+    }
     const float gm = lanes_sum(s, lsh) * inv;
-    if (in)
+    if (in) {
+#pragma unroll 1
       for (int j = l; j < D; j += 1 << lsh) {
         const float e = m[j] - gm;
         t += fmaf(n * e, e, q[j]);
       }
+    }
     t = lanes_sum(t, lsh);
     if (in && l == 0) out(g, gm, t);
   });

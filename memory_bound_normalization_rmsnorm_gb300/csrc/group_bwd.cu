@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   __syncthreads();
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
   if (csize > 1) cluster_sync(); else __syncthreads();
-  const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
+  const float inv = __fdividef(1.0f, static_cast<float>(a.S) * static_cast<float>(a.D));
+#pragma unroll 1
   for (int g = tid; g < ng; g += nthr) {
     float2 t = gst[g];
     if (a.k > 1) {
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   }
   // dgamma / dbeta row of this cluster's samples: the CTAs share its channel
   // pairs out among them and sum over the cluster in rank order.
+#pragma unroll 1
   for (int j = rank * nthr + tid; j < ncs_me * (V / 2); j += csize * nthr) {
     float2 tg = make_float2(0.f, 0.f), tb = tg;
     const float2 *pg = reinterpret_cast<const float2 *>(cg) + j;

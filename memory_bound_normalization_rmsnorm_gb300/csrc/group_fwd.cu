@@ -74,7 +74,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   groups_of_channels(chm, chq, ng, a.D, a.lsh, static_cast<float>(nrow),
                      [&](int g, float m, float m2) { gst[g] = make_float2(m, m2); });
   if (a.k > 1) cluster_sync(); else __syncthreads();
-  const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
+  const float invS = __fdividef(1.0f, static_cast<float>(a.S));
+  const float invD = __fdividef(1.0f, static_cast<float>(a.D));
+#pragma unroll 1
   for (int g = tid; g < ng; g += nthr) {
     float m, m2;
     if (a.k == 1) {
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
         const float n = static_cast<float>(parts.rows(r));
         acc = fmaf(n, ld_cluster_f2(gst + g, r).x, acc);
       }
-      m = acc / static_cast<float>(a.S);
+      m = acc * invS;
       m2 = 0.f;
       for (int r = 0; r < a.k; ++r) {
         const float n = static_cast<float>(parts.rows(r)) * static_cast<float>(a.D);
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
         m2 += fmaf(n * (v.x - m), v.x - m, v.y);
       }
     }
-    const float rs = rsqrtf(m2 / count + a.eps);
+    const float rs = rsqrtf(m2 * invS * invD + a.eps);
     gfin[g] = make_float2(m, rs);
     if (q == 0) {
       a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;

@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
           if (r < a.splits) mean_of(r, v[i]);
         }
         const int far = in ? 2 * (l + (kNear << a.lsh)) : a.splits;
+#pragma unroll 1
         for (int r = far; r < a.splits; r += 2 << a.lsh)
           mean_of(r, __ldcg(reinterpret_cast<const float4 *>(part + r)));
         m = lanes_sum(m, a.lsh) * invS;
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
           const int r = 2 * (l + (i << a.lsh));
           if (r < a.splits) deviation(r, v[i]);
         }
+#pragma unroll 1
         for (int r = far; r < a.splits; r += 2 << a.lsh)
           deviation(r, __ldcg(reinterpret_cast<const float4 *>(part + r)));
         m2 = lanes_sum(m2, a.lsh);
@@ -419,6 +421,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       float *rb = a.dbeta_part
                       ? a.dbeta_part + static_cast<int64_t>(role.sj * a.splits + role.sp) * a.C + ch0
                       : nullptr;
+#pragma unroll 1
       for (int j = tid; j < ring.ncs * V; j += blockDim.x) {
         float vg = cg[j], vb = cb[j];
         if (round > 0) {

@@ -205,12 +205,14 @@ __device__ __forceinline__ void group_sums(const GroupArgs &a, const float *cb, 
                                            int ch0, int ng, Out out) {
   each_group(ng, a.lsh, [&](int g, int l, bool in) {
     float s1 = 0.f, s2 = 0.f;
-    if (in)
+    if (in) {
+#pragma unroll 1
       for (int j = g * a.D + l; j < (g + 1) * a.D; j += 1 << a.lsh) {
         const float gm = load_elem<DT>(a.gamma, ch0 + j);
         s1 = fmaf(gm, cb[j], s1);
         s2 = fmaf(gm, cg[j], s2);
       }
+    }
     s1 = lanes_sum(s1, a.lsh);
     s2 = lanes_sum(s2, a.lsh);
     if (in && l == 0) out(g, make_float2(s1, s2));
