@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
   constexpr int U = kRingRowsFwd;
+  static_assert(U % 4 == 0, "a tile is whole blocks of four rows per thread");
   const Role role(a);
   Ring<DT, 1> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
   constexpr int U = kRingRowsBwd;
+  static_assert(U % 2 == 0, "a tile is whole pairs of rows per thread");
   const Role role(a);
   Ring<DT, 2> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;

@@ -58,7 +58,7 @@ def check_both(x, gamma, beta, dy, G, act, p, label, eps=1e-5):
 SHAPES = [(1, 1, 8, 1), (1, 1, 8, 8), (2, 1, 64, 4), (2, 7, 16, 2), (3, 64, 40, 4),
           (1, 257, 24, 8), (2, 100, 320, 32), (5, 33, 168, 12), (1, 2048, 64, 32),
           (2, 1024, 512, 1), (1, 70, 8192, 32), (1, 2, 8192, 8192), (40, 9, 64, 8),
-          (2, 221, 88, 11), (1, 64, 1280, 32), (3, 1517, 168, 12)]
+          (2, 221, 88, 11), (1, 64, 1280, 32), (3, 1517, 168, 12), (700, 3, 64, 8)]
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -130,6 +130,45 @@ def test_parity_resident_splits(shape, sg, k, monkeypatch):
         plan = gb.norm_group_plan(B, S, C, G)
         assert plan["form"] == 0 and plan["cluster"] == k
         check_both(x, g, b, dy, G, "silu", 0.1, f"{shape} sg={sg} k={k}{R}")
+
+
+@pytest.mark.parametrize("form", [0, 1, 2])
+@pytest.mark.parametrize("B", [1, 3, 9, 40])
+def test_gradients_without_dbeta(B, form, monkeypatch):
+    """dbeta left out, for one partial row, a batch in a cluster and more."""
+    monkeypatch.setenv("GBNORM_GROUP", f"form={form}")
+    x, g, b, dy = make(B, 30, 64, torch.bfloat16, seed=B)
+    y, rstd, mean = gb.norm_group_fwd(x, g, b, 8, 1e-5, "silu")
+    full = gb.norm_group_bwd(dy, x, g, b, rstd, mean, 8, "silu")
+    part = gb.norm_group_bwd(dy, x, g, b, rstd, mean, 8, "silu", want_dbeta=False)
+    assert part[2] is None
+    assert torch.equal(part[0], full[0]) and torch.equal(part[1], full[1])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with workspaces of its own, resident and
+    whole-GPU forms side by side."""
+    big = make(1, 60000, 256, torch.bfloat16, seed=1)
+    small = make(20, 300, 64, torch.bfloat16, seed=2)
+
+    def step(case, G):
+        x, g, b, dy = case
+        y, rstd, mean = gb.norm_group_fwd(x, g, b, G, 1e-5, "silu")
+        return (y, rstd, mean, *gb.norm_group_bwd(dy, x, g, b, rstd, mean, G, "silu"))
+
+    want = [step(big, 32), step(small, 8)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(4):
+        for s, (case, G) in zip(streams, ((big, 32), (small, 8), (big, 32))):
+            with torch.cuda.stream(s):
+                got.append(step(case, G))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for u, v in zip(g, want[1 if i % 3 == 1 else 0]):
+            assert torch.equal(u, v)
+    assert gb.norm_get_device_error() == 0
 
 
 @pytest.mark.parametrize("form", [0, 1, 2])
