@@ -355,6 +355,7 @@ typedef struct {
     int32_t rows_per_thread; /* resident: rows a thread holds (at most) */
     int32_t row_splits;      /* streamed, ring: row ranges per sample */
     int32_t stages;          /* ring: tiles in shared memory */
+    int32_t tensor_memory_tiles; /* ring: tiles in tensor memory (at most) */
     int32_t samples_per_round; /* ring */
     int32_t rounds;          /* ring */
     int32_t threads;         /* CTA size */

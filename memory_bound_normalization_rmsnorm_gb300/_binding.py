@@ -67,8 +67,9 @@ class GroupPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("form", "groups_per_slab", "slabs", "chunk_columns", "cluster", "cluster_samples",
                  "row_lanes",
-                 "rows_per_thread", "row_splits", "stages", "samples_per_round", "rounds",
-                 "threads", "smem_bytes", "grid")] + [("workspace_bytes", ctypes.c_int64)]
+                 "rows_per_thread", "row_splits", "stages", "tensor_memory_tiles",
+                 "samples_per_round", "rounds", "threads", "smem_bytes", "grid")
+                ] + [("workspace_bytes", ctypes.c_int64)]
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_}

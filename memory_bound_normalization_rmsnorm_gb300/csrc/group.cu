@@ -27,7 +27,7 @@ constexpr int kMaxCluster = 8;  // the portable size
 struct GroupPlan {
   int form = kResident;
   int sg = 0, ncs = 0, nslab = 1, k = 1, cb = 1, R = 1, slots = 0, splits = 1;
-  int stages = 0, nsamp = 0, rounds = 0, keep = 0;  // ring
+  int stages = 0, nsamp = 0, rounds = 0, keep = 0, tm = 0;  // ring
   int threads = 0;
   int64_t grid = 0;
   uint32_t smem = 0;  // resident or ring kernel, or the streamed form's first pass
@@ -36,9 +36,9 @@ struct GroupPlan {
 
 // Shape override for sweeps and tests: GBNORM_GROUP="form=1,sg=4,k=2,R=8,
 // splits=3" (any subset; form 0 resident, 1 streamed, 2 ring; for the ring
-// also stages=, nsamp= and keep=; cb=1 one sample per cluster).  Bypasses the cache.
+// also stages=, nsamp=, tm= and keep=; cb=1 one sample per cluster).  Bypasses the cache.
 struct GroupOverride {
-  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0, keep = -1, cb = 0;
+  int form = -1, sg = 0, k = 0, R = 0, splits = 0, stages = 0, nsamp = 0, keep = -1, cb = 0, tm = -1;
   bool any = false;
 };
 
@@ -58,6 +58,7 @@ GroupOverride read_group_override() {
       else if (!std::strcmp(key, "nsamp")) o.nsamp = val;
       else if (!std::strcmp(key, "keep")) o.keep = val;
       else if (!std::strcmp(key, "cb")) o.cb = val;
+      else if (!std::strcmp(key, "tm")) o.tm = val;
       o.any = true;
     }
     s = std::strchr(s, ',');
@@ -168,6 +169,15 @@ norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int s
   p.smem = group_ring_layout(stages, U, p.R, p.ncs, V, p.sg, bwd).total;
   if (static_cast<int64_t>(p.smem) > smem_optin) return NORM_ERR_UNSUPPORTED;
   p.grid = static_cast<int64_t>(p.nsamp) * p.nslab * p.splits;
+  // tensor memory for what the stages do not hold
+  const int most = (static_cast<int>(ceil_div64(S, p.splits)) + TR - 1) / TR;
+  p.tm = std::max(0, std::min(ov.tm >= 0 ? std::min(ov.tm, kRingTmemTiles) : kRingTmemTiles,
+                              most - p.stages));
+  // A CTA takes all of its SM's tensor memory, and its peers wait for it at
+  // the grid barrier: two of them on one SM would wait for each other.  So
+  // their shared memory is more than half of an SM's.
+  const uint32_t over_half = (static_cast<uint32_t>(smem_optin) + 1024u) / 2u;
+  if (p.tm && p.smem < over_half) p.smem = over_half;
   const int64_t tile_bytes = static_cast<int64_t>(TR) * p.ncs * 16 * nt;
   p.keep = ov.keep >= 0 ? ov.keep : static_cast<int>(kL2KeepBytes / (tile_bytes * p.grid));
   *out = p;
@@ -361,6 +371,7 @@ GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_
   a.nsamp = p.nsamp;
   a.rounds = p.rounds;
   a.keep = p.keep;
+  a.tm = p.tm;
   while ((p.sg << (a.lsh + 1)) <= p.threads && a.lsh < 5) ++a.lsh;
   return a;
 }
@@ -541,6 +552,7 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups, n
   out->rows_per_thread = p.slots;
   out->row_splits = p.splits;
   out->stages = p.stages;
+  out->tensor_memory_tiles = p.tm;
   out->samples_per_round = p.nsamp;
   out->rounds = p.rounds;
   out->threads = p.threads;

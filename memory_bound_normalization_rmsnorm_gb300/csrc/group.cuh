@@ -32,6 +32,9 @@ constexpr int kGroupThreads = 512;  // largest CTA of these kernels
 // Ring: rows per thread and tile.
 constexpr int kRingRowsFwd = 8;
 constexpr int kRingRowsBwd = 4;
+// Ring: tiles that tensor memory holds (a thread's chunks of a tile are 32
+// 32-bit columns of its lane; four warps share the 512 columns of a lane).
+constexpr int kRingTmemTiles = 4;
 
 struct GroupArgs {
   const void *x;      // [B, S, C]
@@ -62,7 +65,8 @@ struct GroupArgs {
   int stages;  // ring: tiles in shared memory
   int nsamp;   // ring: samples per round
   int rounds;  // ring: ceil(B / nsamp)
-  int keep;    // ring: tiles per CTA that L2 is asked to hold between the passes
+  int tm;      // ring: tiles per CTA that tensor memory holds between the passes
+  int keep;    // ring: tiles per CTA that L2 is asked to hold
   unsigned *err;  // device error word
   float eps;
 };
@@ -81,7 +85,7 @@ __host__ __device__ inline uint32_t group_chan_bytes(int ncs, int V) {
 // The ring kernels: `stages` tiles of U * R rows (one per tensor), the fold
 // buffer, the per-channel arrays, the backward's running per-channel totals,
 // a float2 per group of the slab, the stages' full and free mbarriers, and
-// the abort flag.
+// the abort flag with the tensor-memory address.
 constexpr int kGroupRingSplits = 192;  // row ranges of a sample, at most
 struct GroupRingLayout {
   uint32_t tensor_bytes, stage_bytes, fold_off, chan_off, tot_off, gst_off, bar_off, flag_off,
@@ -101,7 +105,7 @@ __host__ __device__ inline GroupRingLayout group_ring_layout(int stages, int U, 
   L.gst_off = L.tot_off + (bwd ? group_chan_bytes(ncs, V) : 0u);
   L.bar_off = L.gst_off + static_cast<uint32_t>(sg) * 8u;
   L.flag_off = L.bar_off + 16u * static_cast<uint32_t>(stages);
-  L.total = align16(L.flag_off + 4u);
+  L.total = align16(L.flag_off + 8u);  // abort flag, tensor-memory address
   return L;
 }
 __host__ __device__ inline uint32_t group_smem_bytes(int slots, int ntensors, int R, int ncs, int V,

@@ -9,11 +9,14 @@
 //
 // Rows move as tiles (contiguous in memory) through a ring of shared-memory
 // stages filled by bulk copies.  The first pass leaves the last `stages`
-// tiles where they are; the output pass walks the tiles in the opposite
-// order, so it starts with those, and as each is consumed its stage takes the
-// tile that the first pass read latest among those dropped: the second read
-// goes from the newest to the oldest line of L2.  Once a round has no tile
-// left to read again, freed stages take the next round's first tiles.
+// tiles where they are and puts the up to four before those into tensor
+// memory (each thread its own chunks, into columns of its own lane: 256 KB of
+// an SM that this kernel has no other use for).  The output pass walks the
+// tiles in the opposite order, so it starts with those, and as each stage is
+// consumed it takes the tile that the first pass read latest among those
+// dropped: the second read goes from the newest to the oldest line of L2.
+// Once a round has no tile left to read again, freed stages take the next
+// round's first tiles.
 //
 // What that does to the ring: a stage is always filled in the order in which
 // stages are freed, so the walk through the stages turns round at the end of
@@ -21,8 +24,8 @@
 // direction through the output pass and the next round's first pass.
 //
 // The bound is HBM: x (and dy) read once, y (dx) written once, plus whatever
-// of the second read neither shared memory (about 29 MB over the GPU) nor L2
-// still holds.
+// of the second read neither shared memory (29 MB over the GPU), nor tensor
+// memory (39 MB), nor L2 still holds.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -49,6 +52,8 @@ struct Ring {
   GroupRingLayout L;
   int row0, nrow, TR, T, chunk0, ncs;
   int cur, dir;
+  int tm;              // tiles of this CTA that stay in tensor memory
+  uint32_t tq;         // this warp's columns there
   uint32_t par, epar;  // bit s: parity of stage s's next full / free phase
   int pstage, pb, ptile;  // the refill that warp 0 still owes (pstage < 0: none)
   bool pkeep;
@@ -67,6 +72,7 @@ struct Ring {
     T = (nrow + TR - 1) / TR;
     chunk0 = slab * a.ncs;
     ncs = min(a.ncs, a.nc - chunk0);
+    tm = max(0, min(a.tm, T - a.stages));
     if (threadIdx.x == 0) {
       for (int s = 0; s < a.stages; ++s) {
         mbar_init(full + s, 1);
@@ -75,7 +81,64 @@ struct Ring {
       *abort_flag = 0;
       fence_mbar_init();
     }
+    uint32_t *slot = reinterpret_cast<uint32_t *>(smem + L.flag_off) + 1;
+    const int warp = threadIdx.x >> 5;
+    if (a.tm && warp == 0) {
+      tmem_alloc(slot, 512);
+      tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    // warp w reaches lanes 32 (w % 4) ..; the four warps that share them take
+    // 128 columns each
+    tq = a.tm ? *slot + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                    static_cast<uint32_t>((warp >> 2) * 128)
+              : 0u;
+  }
+  // Frees the tensor memory; every thread has read what it put there.
+  __device__ __forceinline__ void finish() {
+    tc_fence_before();
+    __syncthreads();
+    if (a.tm && threadIdx.x < 32) {
+      tc_fence_after();
+      tmem_dealloc(*(reinterpret_cast<uint32_t *>(base + L.flag_off) + 1), 512);
+    }
+  }
+
+  // Half h of this thread's chunks of a tile: four rows of x (forward), or
+  // all four of x (h = 0) or dy (h = 1).  `i`: the thread's chunk in row lane
+  // 0 (negative: it owns none).
+  __device__ __forceinline__ const uint4 *half(int h, int i) const {
+    return stage(NT == 2 ? h : 0) + i + (NT == 2 ? 0 : 4 * h) * a.R * a.ncs;
+  }
+  // Puts the current stage's tile into tensor memory as tile m (whole warps).
+  __device__ __forceinline__ void stash(int m, int i) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[16];
+      const uint4 *t = half(h, i);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint4 v = i >= 0 ? t[u * a.R * a.ncs] : make_uint4(0, 0, 0, 0);
+        r[4 * u] = v.x;
+        r[4 * u + 1] = v.y;
+        r[4 * u + 2] = v.z;
+        r[4 * u + 3] = v.w;
+      }
+      __syncwarp();
+      tmem_st_n<16>(tq + m * 32 + h * 16, r);
+    }
+  }
+  // Takes two neighbouring chunks, c and c + 1 of half h, of tile m back
+  // (whole warps).
+  __device__ __forceinline__ void unstash(int m, int h, int c, uint4 &v, uint4 &w) const {
+    uint32_t r[8];
+    __syncwarp();
+    tmem_ld_n<8>(tq + m * 32 + h * 16 + c * 4, r);
+    tmem_wait_ld_n<8>(r);
+    v = make_uint4(r[0], r[1], r[2], r[3]);
+    w = make_uint4(r[4], r[5], r[6], r[7]);
   }
 
   __device__ __forceinline__ int rows_of(int tile) const { return min(TR, nrow - tile * TR); }
@@ -83,7 +146,7 @@ struct Ring {
   // First-pass lines that the output pass reads again out of L2: the tiles
   // read last before those that stay in shared memory.
   __device__ __forceinline__ bool kept(int tile) const {
-    return tile < T - a.stages && tile >= T - a.stages - a.keep;
+    return tile < T - a.stages - tm && tile >= T - a.stages - tm - a.keep;
   }
 
   // Fills stage s with tile `tile` of sample b (all lanes of one warp).
@@ -150,34 +213,53 @@ struct Ring {
                                            tensor * L.tensor_bytes);
   }
 
-  // First pass over sample b: body(tile, its rows).
+  // First pass over sample b: body(tile, its rows).  `i`: see half().
   template <typename Body>
-  __device__ __forceinline__ void first_pass(int b, Body body) {
+  __device__ __forceinline__ void first_pass(int b, int i, Body body) {
 #pragma unroll 1
     for (int j = 0; j < T; ++j) {
       flush();
       wait();
       body(j, rows_of(j));
+      const int m = j - (T - a.stages - tm);
+      if (m >= 0 && m < tm) stash(m, i);
       if (j + a.stages < T) refill(b, j + a.stages, kept(j + a.stages));
       if (j + 1 < T) step();
     }
     dir = -dir;
   }
-  // Output pass over sample b, last tile first; `next`: the sample of this
-  // CTA's next round, or -1.
-  template <typename Body>
-  __device__ __forceinline__ void output_pass(int b, int next, Body body) {
+  // Output pass over sample b, last tile first: body(tile, its rows) on the
+  // current stage, far(m, tile, its rows) for the tiles in tensor memory.
+  // `next`: the sample of this CTA's next round, or -1.
+  template <typename Body, typename Far>
+  __device__ __forceinline__ void output_pass(int b, int next, Body body, Far far) {
+    const int n = T - tm;  // tiles of this pass that come by way of a stage
+    auto far_tiles = [&]() {
 #pragma unroll 1
-    for (int i = 0; i < T; ++i) {
+      for (int m = tm - 1; m >= 0; --m) {
+        const int tile = T - a.stages - tm + m;
+        far(m, tile, rows_of(tile));
+      }
+    };
+    if (tm) {
+      __syncwarp();
+      tmem_wait_st();
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
       flush();
+      if (i == a.stages) far_tiles();
       if (i >= a.stages) wait();
-      const int tile = T - 1 - i;
+      const int tile = T - 1 - i - (i < a.stages ? 0 : tm);
       body(tile, rows_of(tile));
-      const int again = tile - a.stages;  // tile to read again, or the next round's -again - 1
-      if (again >= 0) refill(b, again, false);
-      else if (next >= 0 && -again - 1 < T) refill(next, -again - 1, kept(-again - 1));
+      // the freed stage takes this pass's tile i + stages, or else the next
+      // round's first ones
+      const int k = i + a.stages;
+      if (k < n) refill(b, T - 1 - tm - k, false);
+      else if (next >= 0 && k - n < T) refill(next, k - n, kept(k - n));
       step();
     }
+    if (n <= a.stages) far_tiles();
   }
 };
 
@@ -197,13 +279,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
   constexpr int U = kRingRowsFwd;
-  static_assert(U % 4 == 0, "a tile is whole blocks of four rows per thread");
+  static_assert(U == 8, "a thread's part of a tile is two halves of four rows");
   const Role role(a);
   Ring<DT, 1> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
   const bool on = rl < a.R && cc < ring.ncs;
+  const int own = on ? rl * a.ncs + cc : -1;  // this thread's chunk in a tile
   const int g0 = role.slab * a.sg;
   const int ng = min(a.sg, a.G - g0);
   unsigned char *fold = smem + ring.L.fold_off;
@@ -228,9 +311,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
     if (b < a.B) {
       ChannelStats<V> st;
       st.clear();
-      ring.first_pass(b, [&](int, int rows) {
+      ring.first_pass(b, own, [&](int, int rows) {
         if (!on) return;
-        const uint4 *t = ring.stage(0) + rl * a.ncs + cc;
+        const uint4 *t = ring.stage(0) + own;
         const int step = a.R * a.ncs;
         if (rl + (U - 1) * a.R < rows) {
 #pragma unroll
@@ -319,25 +402,41 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
       const int64_t e0 = group_elem(a, b, ring.row0 + rl, ring.chunk0 + cc, V);
       const int64_t estep = static_cast<int64_t>(a.R) * a.C;
       unsigned char *out = static_cast<unsigned char *>(a.out);
-      ring.output_pass(b, next, [&](int tile, int rows) {
-        if (!on) return;
-        const uint4 *t = ring.stage(0) + rl * a.ncs + cc;
-        const int step = a.R * a.ncs;
-        int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
+      // rows u and u + 1 of this thread in a tile of `rows` rows
+      auto emit = [&](int64_t e, int u, int rows, uint4 va, uint4 vb) {
+        if (rl + u * a.R >= rows) return;
+        const bool two = rl + (u + 1) * a.R < rows;
+        if (!two) vb = va;
+        out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, e, e + estep);
+        st_global_cs_v4(out + e * elem_bytes(DT), va);
+        if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), vb);
+      };
+      ring.output_pass(
+          b, next,
+          [&](int tile, int rows) {
+            if (!on) return;
+            const uint4 *t = ring.stage(0) + own;
+            const int step = a.R * a.ncs;
+            int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
 #pragma unroll
-        for (int u = 0; u < U; u += 2) {
-          const bool in1 = rl + u * a.R < rows, in2 = rl + (u + 1) * a.R < rows;
-          if (in1) {
-            uint4 va = t[u * step], vb = in2 ? t[(u + 1) * step] : va;
-            out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, e, e + estep);
-            st_global_cs_v4(out + e * elem_bytes(DT), va);
-            if (in2) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), vb);
-          }
-          e += 2 * estep;
-        }
-      });
+            for (int u = 0; u < U; u += 2) {
+              emit(e, u, rows, t[u * step], t[(u + 1) * step]);
+              e += 2 * estep;
+            }
+          },
+          [&](int m, int tile, int rows) {
+            int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
+#pragma unroll 1
+            for (int u = 0; u < U; u += 2) {
+              uint4 va, vb;
+              ring.unstash(m, u >> 2, u & 3, va, vb);
+              if (on) emit(e, u, rows, va, vb);
+              e += 2 * estep;
+            }
+          });
     }
   }
+  ring.finish();
 }
 
 template <int DT, int ACT, bool DROP>
@@ -345,7 +444,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
   constexpr int U = kRingRowsBwd;
-  static_assert(U % 2 == 0, "a tile is whole pairs of rows per thread");
+  static_assert(U == 4, "a thread's part of a tile is four rows of x and of dy");
   const Role role(a);
   Ring<DT, 2> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
@@ -353,6 +452,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   const int rl = tid / a.ncs;
   const int cc = tid - rl * a.ncs;
   const bool on = rl < a.R && cc < ring.ncs;
+  const int own = on ? rl * a.ncs + cc : -1;  // this thread's chunk in a tile
   const int g0 = role.slab * a.sg;
   const int ng = min(a.sg, a.G - g0);
   const int ch0 = ring.chunk0 * V;
@@ -383,15 +483,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       float2 s1[V / 2], s2[V / 2];
 #pragma unroll
       for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
-      ring.first_pass(b, [&](int tile, int rows) {
+      ring.first_pass(b, own, [&](int tile, int rows) {
         if (!on) return;
         const int step = a.R * a.ncs;
-        const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
-        uint4 *td = ring.stage(1) + rl * a.ncs + cc;
+        const uint4 *tx = ring.stage(0) + own;
+        uint4 *td = ring.stage(1) + own;
         int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
-        // dropped elements of dy are zeroed; in a tile that stays, in the
-        // stage too, so that the dx pass need not ask the generator again
-        const bool stays = tile >= ring.T - a.stages;
+        // dropped elements of dy are zeroed; in a tile that stays on the SM,
+        // in the stage too, so that the dx pass need not ask the generator
+        // again
+        const bool stays = tile >= ring.T - a.stages - ring.tm;
 #pragma unroll
         for (int u = 0; u < U; u += 2) {
           if (rl + u * a.R < rows) {
@@ -463,38 +564,60 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
       float2 ra[V / 2], rc[V / 2];
       if (on) dx_constants<DT>(a, gfin, g0, ring.chunk0 + cc, ra, rc);
       unsigned char *out = static_cast<unsigned char *>(a.out);
-      ring.output_pass(b, next, [&](int tile, int rows) {
-        if (!on) return;
-        const int step = a.R * a.ncs;
-        const uint4 *tx = ring.stage(0) + rl * a.ncs + cc;
-        const uint4 *td = ring.stage(1) + rl * a.ncs + cc;
-        int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
-        const bool stayed = tile >= ring.T - a.stages;
-#pragma unroll
-        for (int u = 0; u < U; u += 2) {
-          if (rl + u * a.R < rows) {
-            const bool two = rl + (u + 1) * a.R < rows;
-            const int o = (u + (two ? 1 : 0)) * step;
-            uint4 xa = tx[u * step], xb = tx[o], da = td[u * step], db = td[o];
-            if (DROP && !stayed) {
-              gen.template mask<DT>(da, static_cast<uint64_t>(e));
-              gen.template mask<DT>(db, static_cast<uint64_t>(e + estep));
-            }
-            dx_rows<DT, ACT, DROP>(a, xa, da, xb, db, k, ra, rc);
-            st_global_cs_v4(out + e * elem_bytes(DT), xa);
-            if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), xb);
-          }
-          e += 2 * estep;
+      // rows u and u + 1 of this thread in a tile of `rows` rows; `ask`: the
+      // dropped elements of dy are not zeroed yet
+      auto emit = [&](int64_t e, int u, int rows, bool ask, uint4 xa, uint4 da, uint4 xb,
+                      uint4 db) {
+        if (rl + u * a.R >= rows) return;
+        const bool two = rl + (u + 1) * a.R < rows;
+        if (DROP && ask) {
+          gen.template mask<DT>(da, static_cast<uint64_t>(e));
+          gen.template mask<DT>(db, static_cast<uint64_t>(e + estep));
         }
-      });
+        if (!two) {
+          xb = xa;
+          db = da;
+        }
+        dx_rows<DT, ACT, DROP>(a, xa, da, xb, db, k, ra, rc);
+        st_global_cs_v4(out + e * elem_bytes(DT), xa);
+        if (two) st_global_cs_v4(out + (e + estep) * elem_bytes(DT), xb);
+      };
+      ring.output_pass(
+          b, next,
+          [&](int tile, int rows) {
+            if (!on) return;
+            const int step = a.R * a.ncs;
+            const uint4 *tx = ring.stage(0) + own;
+            const uint4 *td = ring.stage(1) + own;
+            int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
+            const bool ask = tile < ring.T - a.stages;
+#pragma unroll
+            for (int u = 0; u < U; u += 2) {
+              emit(e, u, rows, ask, tx[u * step], td[u * step], tx[(u + 1) * step],
+                   td[(u + 1) * step]);
+              e += 2 * estep;
+            }
+          },
+          [&](int m, int tile, int rows) {
+            int64_t e = e0 + static_cast<int64_t>(tile) * ring.TR * a.C;
+#pragma unroll 1
+            for (int u = 0; u < U; u += 2) {
+              uint4 xa, xb, da, db;
+              ring.unstash(m, 0, u, xa, xb);
+              ring.unstash(m, 1, u, da, db);
+              if (on) emit(e, u, rows, false, xa, da, xb, db);
+              e += 2 * estep;
+            }
+          });
     }
   }
+
+  ring.finish();
 
   // dgamma / dbeta: column sums of the partial rows, which every CTA wrote
   // before the last barrier (samples of earlier rounds only, where the last
   // round has none for it).  A CTA takes 32 columns at a time, its warps
   // every 16th row; the warps' sums are added in warp order.
-  __syncthreads();
   const int P = min(a.nsamp, a.B) * a.splits;
   const int cols = (a.C + 31) / 32;
   float *part = reinterpret_cast<float *>(fold);  // [16][32]

@@ -85,7 +85,8 @@ def test_parity_streamed(shape, dtype, monkeypatch):
 
 
 RINGS = ["", ",R=1", ",splits=1,R=1,stages=3", ",splits=2,R=2,stages=2", ",splits=3,R=1,stages=4",
-         ",nsamp=1,splits=1,R=1,stages=2", ",nsamp=1,splits=2,R=1", ",nsamp=2,splits=1,R=2,stages=3"]
+         ",nsamp=1,splits=1,R=1,stages=2", ",nsamp=1,splits=2,R=1", ",nsamp=2,splits=1,R=2,stages=3",
+         ",splits=1,R=1,stages=2,tm=0", ",splits=1,R=1,stages=1,tm=2"]
 
 
 @pytest.mark.parametrize("dtype", list(DT))

@@ -158,14 +158,17 @@ def test_group_plans_in_bounds(override, monkeypatch):
                     assert p["grid"] == n * p["slabs"] * sp <= SMS, label
                     assert (p["rounds"] - 1) * n < B <= p["rounds"] * n and sp <= S, label
                     assert 1 <= p["stages"] <= 31, label
+                    assert 0 <= p["tensor_memory_tiles"] <= max(0, min(4, -(-(-(-S // sp)) // TR) - p["stages"]))
                     if p["rounds"] > 1:
                         assert -(-(S // sp) // TR) >= p["stages"], label
                     stage = TR * ncs * 16 * nt
                     assert p["smem_bytes"] >= p["stages"] * stage + fold + \
                         (ncs * V * 8 if bwd else 0) + 8 * p["groups_per_slab"] + \
-                        16 * p["stages"] + 4, label
+                        16 * p["stages"] + 8, label
                     if bwd:  # the column sums' float per thread before the channel arrays
                         assert p["smem_bytes"] >= p["stages"] * stage + 2048 + 16 * ncs * V
+                    if p["tensor_memory_tiles"]:  # never two CTAs on one SM
+                        assert 2 * (p["smem_bytes"] + 1024) > OPTIN + 1024, label
                     assert stage < 1 << 20, label  # bytes one stage barrier counts
                     assert p["workspace_bytes"] == (B * G * (sp + sp % 2) * 8) + \
                         (n * sp * C * 8 if bwd else 0), label
