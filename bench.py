@@ -69,8 +69,10 @@ def peak_hbm():
 # code: the plan a record was taken with is kept beside its counters instead.
 _SHARED = ("common.cuh", "ptx.cuh", "rowops.cuh")
 KERNEL_SOURCES = {
-    "norm_fwd_kernel": ("fwd.cu", "fwd_kernel.cuh", "tiles.cuh") + _SHARED,
-    "norm_bwd_kernel": ("bwd.cu", "tiles.cuh") + _SHARED,
+    "norm_fwd_kernel": ("fwd.cu", "fwd_kernel.cuh", "tiles.cuh", "dropout.cuh", "elem.cuh")
+                       + _SHARED,
+    "norm_bwd_kernel": ("bwd.cu", "bwd_kernel.cuh", "tiles.cuh", "dropout.cuh", "elem.cuh")
+                       + _SHARED,
     "norm_gemm_kernel": ("gemm.cu", "tcgen05.cuh") + _SHARED,
 }
 

@@ -48,7 +48,7 @@ GroupOverride read_group_override() {
   while (s && *s) {
     char key[16];
     int val = 0;
-    if (std::sscanf(s, "%15[^=]=%d", key, &val) == 2) {
+    if (std::sscanf(s, "%15[^=]=%d", key, &val) == 2 && val >= 0) {
       if (!std::strcmp(key, "form")) o.form = val;
       else if (!std::strcmp(key, "sg")) o.sg = val;
       else if (!std::strcmp(key, "k")) o.k = val;

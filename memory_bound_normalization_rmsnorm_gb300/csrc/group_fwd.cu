@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
     float2 nmu[V / 2], sc[V / 2], bf[V / 2];
     out_constants<DT>(a, gfin, g0, chunk0 + cc, nmu, sc, bf);
     DropGen gen(a.drop);
-  if (DROP) gen.start();
+    if (DROP) gen.start();
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
 #pragma unroll 2
     for (int i = 0; i < nr; i += 2) {

@@ -114,6 +114,13 @@ int64_t integer(PyObject *o) {
   return v;
 }
 
+// A mode or activation: -1, which the library refuses, for what an int
+// cannot hold.
+int code_of(PyObject *o) {
+  const int64_t v = integer(o);
+  return v < 0 || v > 255 ? -1 : static_cast<int>(v);
+}
+
 double number(PyObject *o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw PyFail{};
@@ -284,7 +291,7 @@ PyObject *dropout_add_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(gamma, "gamma", bf, {d.N}, dev);
     check(beta, "beta", bf, {d.N}, dev);
     const float eps = static_cast<float>(number(a[4]));
-    const int mode = static_cast<int>(integer(a[5]));
+    const int mode = code_of(a[5]);
     const Rng rng(a + 6, dev);
     const StreamScope on(a[14], dev);
     const at::Tensor h = output(a[10], "h", bf, d.shape, dev);
@@ -320,7 +327,7 @@ PyObject *dropout_add_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(gamma, "gamma", bf, {d.N}, dev);
     check(rstd, "rstd", f32, d.lead, dev);
     check(mean, "mean", f32, d.lead, dev);
-    const norm_mode_t mode = static_cast<norm_mode_t>(integer(a[6]));
+    const norm_mode_t mode = static_cast<norm_mode_t>(code_of(a[6]));
     const Rng rng(a + 7, dev);
     const StreamScope on(a[17], dev);
     const at::Tensor dx = output(a[11], "dx", bf, d.shape, dev);
@@ -368,9 +375,9 @@ PyObject *group_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(gamma, "gamma", dt, {d.C}, dev);
     check(beta, "beta", dt, {d.C}, dev);
     const int64_t groups = integer(a[3]);
-    if (groups < 1) return PyLong_FromLong(NORM_ERR_SHAPE);
+    if (groups < 1 || groups > d.C) return PyLong_FromLong(NORM_ERR_SHAPE);
     const float eps = static_cast<float>(number(a[4]));
-    const norm_act_t act = static_cast<norm_act_t>(integer(a[5]));
+    const norm_act_t act = static_cast<norm_act_t>(code_of(a[5]));
     const Rng rng(a + 6, dev);
     const StreamScope on(a[14], dev);
     const at::Tensor y = output(a[10], "y", dt, x.sizes(), dev);
@@ -401,13 +408,13 @@ PyObject *group_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
                      &beta = tensor(a[3], "beta", true), &rstd = tensor(a[4], "rstd"),
                      &mean = tensor(a[5], "mean");
     const int64_t groups = integer(a[6]);
-    if (groups < 1) return PyLong_FromLong(NORM_ERR_SHAPE);
+    if (groups < 1 || groups > d.C) return PyLong_FromLong(NORM_ERR_SHAPE);
     check(dy, "dy", dt, x.sizes(), dev);
     check(gamma, "gamma", dt, {d.C}, dev);
     check(beta, "beta", dt, {d.C}, dev);
     check(rstd, "rstd", f32, {d.B, groups}, dev);
     check(mean, "mean", f32, {d.B, groups}, dev);
-    const norm_act_t act = static_cast<norm_act_t>(integer(a[7]));
+    const norm_act_t act = static_cast<norm_act_t>(code_of(a[7]));
     const Rng rng(a + 8, dev);
     const StreamScope on(a[17], dev);
     const at::Tensor dx = output(a[12], "dx", dt, x.sizes(), dev);

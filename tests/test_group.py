@@ -388,3 +388,23 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         gb.norm_dropout(x, 0.1, -1)
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+def test_binding_refuses_counts_and_codes_out_of_range():
+    # refused by value, before an output of that size is asked for
+    x, g, b, dy = make(2, 8, 32, torch.bfloat16)
+    one = torch.ones(2, 4, device="cuda")
+    for groups in (0, -4, 33, 1 << 40):
+        with pytest.raises(gb.NormError) as e:
+            gb.norm_group_fwd(x, g, b, groups)
+        assert e.value.status == 2, groups
+        with pytest.raises(gb.NormError) as e:
+            gb.norm_group_bwd(dy, x, g, b, one, one, groups)
+        assert e.value.status == 2, groups
+    for act in (3, -1, 1 << 32):
+        with pytest.raises(gb.NormError) as e:
+            gb.norm_group_fwd(x, g, b, 4, act=act)
+        assert e.value.status == 9, act
+    with pytest.raises(gb.NormError) as e:
+        gb.norm_dropout_add_fwd(x, x, g, mode=1 << 32, p=0.1, seed=1)
+    assert e.value.status == 4

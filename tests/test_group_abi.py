@@ -188,3 +188,14 @@ def test_group_plans_in_bounds(override, monkeypatch):
                 assert p["workspace_bytes"] == (
                     B * C * 8 if bwd and B > p["cluster_samples"] else 0), label
     assert seen == ({0, 1, 2} if not override else {int(override[5])})
+
+
+@pytest.mark.parametrize("text", ["R=-3", "stages=-1,form=2", "splits=-2,form=2", "k=-1", "junk"])
+def test_shape_override_ignores_negative_values(text, monkeypatch):
+    form = ["form=2"] if "form=2" in text else []
+    monkeypatch.setenv("GBNORM_GROUP", ",".join(form))
+    for back in (False, True):
+        want = gb.norm_group_plan(4, 300, 320, 32, gb.BF16, back, SMS, OPTIN)
+        monkeypatch.setenv("GBNORM_GROUP", text)
+        assert gb.norm_group_plan(4, 300, 320, 32, gb.BF16, back, SMS, OPTIN) == want
+        monkeypatch.setenv("GBNORM_GROUP", ",".join(form))
