@@ -21,6 +21,35 @@ struct GroupWalk {
   }
 };
 
+// A 16-byte chunk taken pair by pair, so that few of its channels are live as
+// fp32 at a time.
+template <int DT>
+struct Pairs {
+  uint32_t w[4];
+  __device__ __forceinline__ explicit Pairs(const uint4 &c) : w{c.x, c.y, c.z, c.w} {}
+  __device__ __forceinline__ uint4 chunk() const { return make_uint4(w[0], w[1], w[2], w[3]); }
+  __device__ __forceinline__ float2 get(int p) const {
+    if constexpr (DT == kBF16) {
+      return bf2_to_f2(w[p]);
+    } else if constexpr (DT == kFP16) {
+      return __half22float2(*reinterpret_cast<const __half2 *>(&w[p]));
+    } else {
+      return make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1]));
+    }
+  }
+  __device__ __forceinline__ void set(int p, float2 v) {
+    if constexpr (DT == kBF16) {
+      w[p] = f2_to_bf2(v);
+    } else if constexpr (DT == kFP16) {
+      const __half2 h = __floats2half2_rn(v.x, v.y);
+      w[p] = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+      w[2 * p] = __float_as_uint(v.x);
+      w[2 * p + 1] = __float_as_uint(v.y);
+    }
+  }
+};
+
 // ------------------------------------------------------------- forward
 // y of the same chunk column in two rows: z = (x - mean) * (rstd gamma) +
 // beta, activation, dropout.
@@ -30,21 +59,27 @@ __device__ __forceinline__ void out_rows(uint4 &xa, uint4 &xb, const float2 (&nm
                                          const float2 (&bf)[chunk_elems(DT) / 2],
                                          const DropGen &gen, int64_t ea, int64_t eb) {
   constexpr int V = chunk_elems(DT);
+  Pairs<DT> ta(xa), tb(xb);
   float2 fa[V / 2], fb[V / 2];
-  unpack<DT>(xa, fa);
-  unpack<DT>(xb, fb);
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) {
-    fa[p] = fma2(add2(fa[p], nmu[p]), sc[p], bf[p]);
-    fb[p] = fma2(add2(fb[p], nmu[p]), sc[p], bf[p]);
+    fa[p] = fma2(add2(ta.get(p), nmu[p]), sc[p], bf[p]);
+    fb[p] = fma2(add2(tb.get(p), nmu[p]), sc[p], bf[p]);
     act_rows<ACT>(fa[p], fb[p]);
+    if (!DROP) {
+      ta.set(p, fa[p]);
+      tb.set(p, fb[p]);
+    }
   }
   if (DROP) {
     gen.template chunk<V>(fa, static_cast<uint64_t>(ea));
     gen.template chunk<V>(fb, static_cast<uint64_t>(eb));
+    xa = pack<DT>(fa);
+    xb = pack<DT>(fb);
+  } else {
+    xa = ta.chunk();
+    xb = tb.chunk();
   }
-  xa = pack<DT>(fa);
-  xb = pack<DT>(fb);
 }
 
 // Per-channel constants of the output pass: -mean, rstd gamma, beta.
@@ -109,29 +144,19 @@ __device__ __forceinline__ void scale_sums(const GroupArgs &a, int b, int chunk,
   }
 }
 
-// d = x - mean and dz of the same chunk column in two rows.  With dropout the
-// dropped elements of dy are 0 already and dz lacks the kept ones' factor.
-template <int DT, int ACT>
-__device__ __forceinline__ void grad_rows(
-    const uint4 &xa, const uint4 &da, const uint4 &xb, const uint4 &db,
-    const BwdConst<chunk_elems(DT)> &k, float2 (&ca)[chunk_elems(DT) / 2],
-    float2 (&dza)[chunk_elems(DT) / 2], float2 (&cb)[chunk_elems(DT) / 2],
-    float2 (&dzb)[chunk_elems(DT) / 2]) {
-  constexpr int V = chunk_elems(DT);
-  unpack<DT>(xa, ca);
-  unpack<DT>(da, dza);
-  unpack<DT>(xb, cb);
-  unpack<DT>(db, dzb);
-#pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    ca[p] = add2(ca[p], k.nmu[p]);
-    cb[p] = add2(cb[p], k.nmu[p]);
-    if (ACT != kActNone) {
-      float2 za = fma2(ca[p], k.sc[p], k.bf[p]), zb = fma2(cb[p], k.sc[p], k.bf[p]);
-      act_grad_rows<ACT>(za, zb);
-      dza[p] = mul2(dza[p], za);
-      dzb[p] = mul2(dzb[p], zb);
-    }
+// d = x - mean and dz of the same two channels in two rows, from x in ca and
+// cb and dy in dza and dzb.  With dropout the dropped elements of dy are 0
+// already and dz lacks the kept ones' factor.
+template <int ACT>
+__device__ __forceinline__ void grad_pairs(float2 nmu, float2 sc, float2 bf, float2 &ca, float2 &dza,
+                                           float2 &cb, float2 &dzb) {
+  ca = add2(ca, nmu);
+  cb = add2(cb, nmu);
+  if (ACT != kActNone) {
+    float2 za = fma2(ca, sc, bf), zb = fma2(cb, sc, bf);
+    act_grad_rows<ACT>(za, zb);
+    dza = mul2(dza, za);
+    dzb = mul2(dzb, zb);
   }
 }
 
@@ -142,43 +167,38 @@ __device__ __forceinline__ void dx_rows(const GroupArgs &a, uint4 &xa, const uin
                                         const uint4 &db, const BwdConst<chunk_elems(DT)> &k,
                                         const float2 (&ra)[chunk_elems(DT) / 2],
                                         const float2 (&rc)[chunk_elems(DT) / 2]) {
-  constexpr int V = chunk_elems(DT);
-  float2 ca[V / 2], dza[V / 2], cb[V / 2], dzb[V / 2];
-  grad_rows<DT, ACT>(xa, da, xb, db, k, ca, dza, cb, dzb);
+  Pairs<DT> tx(xa), ux(xb);
+  const Pairs<DT> td(da), ud(db);
 #pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
+  for (int p = 0; p < chunk_elems(DT) / 2; ++p) {
+    float2 ca = tx.get(p), cb = ux.get(p), dza = td.get(p), dzb = ud.get(p);
+    grad_pairs<ACT>(k.nmu[p], k.sc[p], k.bf[p], ca, dza, cb, dzb);
     if (DROP) {
-      dza[p] = mul2(dza[p], splat2(a.drop.scale));
-      dzb[p] = mul2(dzb[p], splat2(a.drop.scale));
+      dza = mul2(dza, splat2(a.drop.scale));
+      dzb = mul2(dzb, splat2(a.drop.scale));
     }
-    dza[p] = fma2(ca[p], rc[p], fma2(dza[p], k.sc[p], ra[p]));
-    dzb[p] = fma2(cb[p], rc[p], fma2(dzb[p], k.sc[p], ra[p]));
+    tx.set(p, fma2(ca, rc[p], fma2(dza, k.sc[p], ra[p])));
+    ux.set(p, fma2(cb, rc[p], fma2(dzb, k.sc[p], ra[p])));
   }
-  xa = pack<DT>(dza);
-  xb = pack<DT>(dzb);
+  xa = tx.chunk();
+  xb = ux.chunk();
 }
 
-// Adds dz and dz d of two rows (`two`: the second counts) to the sums.
+// Adds dz and dz d of two rows to the sums.  `two`: the second counts (else
+// it is the first again, and its dy is taken as zero).
 template <int DT, int ACT>
 __device__ __forceinline__ void sum_rows(const uint4 &xa, const uint4 &da, const uint4 &xb,
-                                         const uint4 &db, bool two,
-                                         const BwdConst<chunk_elems(DT)> &k,
+                                         uint4 db, bool two, const BwdConst<chunk_elems(DT)> &k,
                                          float2 (&s1)[chunk_elems(DT) / 2],
                                          float2 (&s2)[chunk_elems(DT) / 2]) {
-  constexpr int V = chunk_elems(DT);
-  float2 ca[V / 2], dza[V / 2], cb[V / 2], dzb[V / 2];
-  grad_rows<DT, ACT>(xa, da, xb, db, k, ca, dza, cb, dzb);
+  if (!two) db = make_uint4(0, 0, 0, 0);
+  const Pairs<DT> tx(xa), ux(xb), td(da), ud(db);
 #pragma unroll
-  for (int p = 0; p < V / 2; ++p) {
-    s1[p] = add2(s1[p], dza[p]);
-    s2[p] = fma2(dza[p], ca[p], s2[p]);
-  }
-  if (two) {
-#pragma unroll
-    for (int p = 0; p < V / 2; ++p) {
-      s1[p] = add2(s1[p], dzb[p]);
-      s2[p] = fma2(dzb[p], cb[p], s2[p]);
-    }
+  for (int p = 0; p < chunk_elems(DT) / 2; ++p) {
+    float2 ca = tx.get(p), cb = ux.get(p), dza = td.get(p), dzb = ud.get(p);
+    grad_pairs<ACT>(k.nmu[p], k.sc[p], k.bf[p], ca, dza, cb, dzb);
+    s1[p] = add2(s1[p], add2(dza, dzb));
+    s2[p] = fma2(dzb, cb, fma2(dza, ca, s2[p]));
   }
 }
 
