@@ -3,7 +3,13 @@
 // writes h = bf16(r + drop(x)) and y = norm(h); the backward writes dr (the
 // fused residual backward's dx) and dx = drop(dr).  The generator runs on
 // each 16-byte chunk where the fused residual kernels add it, about 8 issue
-// slots per element on passes that move 8 and 10 bytes per element.
+// slots per element on passes that move 8 and 10 bytes per element, so HBM
+// stays the bound of large calls: LayerNorm 32768 x 4096 forward in 171 us
+// (1.07 GB, 92 % of the measured copy bandwidth; 62 % of the issue slots),
+// backward with the partial reduction in 211 us (1.34 GB, 94 %).  RMSNorm 256
+// x 1024 forward takes 4.0 us, most of it launch and one row's latency.
+// Splitting the dropout off into its own pass would add 4 bytes per element,
+// 80 us at that size.
 #include "bwd_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "long_kernel.cuh"

@@ -8,6 +8,14 @@
 // dgamma and dbeta need, so one set of accumulators serves both.  dz is
 // recomputed in the second pass (from x and dy in shared memory or L2)
 // rather than kept: kept in 16 bits it would be rounded.
+//
+// Bound by instruction latency at 16 warps per SM (128 registers: a chunk
+// column's constants and sums stay in them): about 37 instructions per element
+// with SiLU over both passes, 51 with dropout, at half of the issue slots.
+// Resident form: 16 x 1024 x 640 bf16, SiLU and p = 0.1: 35.7 us (30.1 without
+// dropout; 63 MB, 26 % of the measured copy bandwidth).  2 x 221 x 88 fp16
+// GELU: 5.4 us in one launch.  Streamed form: 4 x 4096 x 8192 bf16 in one
+// group, SiLU: 326 us (282 without activation).
 #include "common.cuh"
 #include "group_rows.cuh"
 
