@@ -372,6 +372,16 @@ GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_
   a.rounds = p.rounds;
   a.keep = p.keep;
   a.tm = p.tm;
+  a.by_ncs.set(p.ncs);
+  a.by_k.set(p.k);
+  a.by_csize.set(p.k * p.cb);
+  a.by_nslab.set(p.nslab);
+  a.by_splits.set(p.splits);
+  a.by_R.set(p.R);
+  a.by_D.set(a.D);
+  const int ranges = p.form == kResident ? p.k : p.splits;
+  a.pq = a.S / ranges;
+  a.prem = a.S % ranges;
   while ((p.sg << (a.lsh + 1)) <= p.threads && a.lsh < 5) ++a.lsh;
   return a;
 }

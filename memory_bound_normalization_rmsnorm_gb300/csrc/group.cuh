@@ -36,6 +36,24 @@ constexpr int kRingRowsBwd = 4;
 // 32-bit columns of its lane; four warps share the 512 columns of a lane).
 constexpr int kRingTmemTiles = 4;
 
+// Division of n (0 <= n < 2^31) by a divisor known to the host, d >= 1: with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (hi(m n) + n)
+// >> l (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", PLDI 1994; n + hi(m n) stays below 2^32 here).  A CTA starts
+// with several divisions, one after the other, before its first copy.
+struct FastDiv {
+  uint32_t m, l;
+  void set(int d) {
+    l = 0;
+    while ((int64_t(1) << l) < d) ++l;
+    m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    const uint32_t u = static_cast<uint32_t>(n);
+    return static_cast<int>((__umulhi(m, u) + u) >> l);
+  }
+};
+
 struct GroupArgs {
   const void *x;      // [B, S, C]
   const void *dy;     // [B, S, C] (backward)
@@ -57,6 +75,8 @@ struct GroupArgs {
   int nslab;   // slabs per sample
   int k;       // resident: CTAs that share a slab's rows
   int cb;      // resident backward: samples per cluster (1 or B)
+  FastDiv by_ncs, by_k, by_csize, by_nslab, by_splits, by_R, by_D;  // csize = k cb
+  int pq, prem;  // S rows in k (resident) or `splits` ranges: quotient, remainder
   int R;       // row lanes per CTA
   int slots;   // resident: rows per thread (at most)
   int splits;  // streamed and ring: row ranges per sample
@@ -563,13 +583,13 @@ __device__ __forceinline__ int64_t group_elem(const GroupArgs &a, int b, int64_t
   return (static_cast<int64_t>(b) * a.S + s) * a.C + static_cast<int64_t>(chunk) * V;
 }
 
-// S rows cut into n ranges that differ by one row at most, the longer ones
+// S rows cut into ranges that differ by one row at most, the longer ones
 // first.
 struct Parts {
   int q, rem;
-  __host__ __device__ Parts(int S, int n) : q(S / n), rem(S % n) {}
-  __host__ __device__ int rows(int i) const { return q + (i < rem ? 1 : 0); }
-  __host__ __device__ int begin(int i) const { return i * q + (i < rem ? i : rem); }
+  __device__ __forceinline__ explicit Parts(const GroupArgs &a) : q(a.pq), rem(a.prem) {}
+  __device__ __forceinline__ int rows(int i) const { return q + (i < rem ? 1 : 0); }
+  __device__ __forceinline__ int begin(int i) const { return i * q + (i < rem ? i : rem); }
 };
 
 // Parameters of a thread's V channels as fp32 pairs: gamma, beta (0 when

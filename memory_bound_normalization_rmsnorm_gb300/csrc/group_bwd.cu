@@ -10,11 +10,13 @@
 // rather than kept: kept in 16 bits it would be rounded.
 //
 // Bound by instruction latency at 16 warps per SM (128 registers: a chunk
-// column's constants and sums stay in them): about 37 instructions per element
-// with SiLU over both passes, 51 with dropout, at half of the issue slots.
-// Resident form: 16 x 1024 x 640 bf16, SiLU and p = 0.1: 35.7 us (30.1 without
-// dropout; 63 MB, 26 % of the measured copy bandwidth).  2 x 221 x 88 fp16
-// GELU: 5.4 us in one launch.  Streamed form: 4 x 4096 x 8192 bf16 in one
+// column's constants and sums stay in them).  A chunk (8 elements of 16 bits)
+// costs a thread 95 instructions over both passes, 203 with SiLU, 281 with
+// dropout too (22 an element are the formulas' own with SiLU), and a thread about
+// 800 more for its start, constants and folds, which 11 rows share at 16 x 1024 x
+// 640: half of the issue slots are used, each warp waiting for its own results.
+// Resident form: 16 x 1024 x 640 bf16, SiLU and p = 0.1: 35.3 us (63 MB, 26 % of
+// the measured copy bandwidth).  2 x 221 x 88 fp16 GELU: 5.3 us in one launch.  Streamed form: 4 x 4096 x 8192 bf16 in one
 // group, SiLU: 326 us (282 without activation).
 #include "common.cuh"
 #include "group_rows.cuh"
@@ -33,23 +35,23 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   // A cluster owns a slab of cb samples (one, or all of a small batch), k CTAs
   // each.
   const int csize = a.cb * a.k;
-  const int unit = static_cast<int>(blockIdx.x) / csize;
+  const int unit = a.by_csize(blockIdx.x);
   const int rank = static_cast<int>(blockIdx.x) - unit * csize;
-  const int bl = rank / a.k;
+  const int bl = a.by_k(rank);
   const int q = rank - bl * a.k;
-  const int ub = unit / a.nslab;
+  const int ub = a.by_nslab(unit);
   const int b = ub * a.cb + bl;
   const int slab = unit - ub * a.nslab;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
   const int chunk0 = slab * a.ncs;
   const int ncs_me = min(a.ncs, a.nc - chunk0);
   const int g0 = slab * a.sg;
   const int ng = min(a.sg, a.G - g0);
   const bool on = rl < a.R && cc < ncs_me;
-  const Parts parts(a.S, a.k);
+  const Parts parts(a);
   const int s0 = parts.begin(q), nrow = parts.rows(q);
-  const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
+  const int nr = (on && rl < nrow) ? a.by_R(nrow - rl + a.R - 1) : 0;
 
   // slot i of this thread: x at data[2 i nact], dy at data[(2 i + 1) nact]
   uint4 *data = reinterpret_cast<uint4 *>(smem) + tid;
@@ -67,10 +69,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   const int64_t bstep = estep * elem_bytes(DT);
   const unsigned char *xs = static_cast<const unsigned char *>(a.x) + e0 * elem_bytes(DT);
   const unsigned char *ds = static_cast<const unsigned char *>(a.dy) + e0 * elem_bytes(DT);
-  for (int i = 0; i < nr; ++i) {
-    cp_async_16(data + static_cast<size_t>(2 * i) * nact, xs + i * bstep);
-    cp_async_16(data + static_cast<size_t>(2 * i + 1) * nact, ds + i * bstep);
-    if (i & 1) cp_async_commit();
+  {
+    uint4 *to = data;
+    for (int i = 0; i < nr; ++i) {
+      cp_async_16(to, xs);
+      cp_async_16(to + nact, ds);
+      to += 2 * nact;
+      xs += bstep;
+      ds += bstep;
+      if (i & 1) cp_async_commit();
+    }
   }
   cp_async_commit();
 
@@ -81,29 +89,33 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   float2 s1[V / 2], s2[V / 2];
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) s1[p] = s2[p] = splat2(0.f);
-  auto slot_x = [&](int i) -> uint4 & { return data[static_cast<size_t>(2 * i) * nact]; };
-  auto slot_d = [&](int i) -> uint4 & { return data[static_cast<size_t>(2 * i + 1) * nact]; };
-  // dy of row i, its dropped elements zeroed -- in the slot too, so that the
+  // dy in a slot, its dropped elements zeroed -- in the slot too, so that the
   // dx pass need not ask the generator again.
-  auto take_d = [&](int i) {
-    uint4 v = slot_d(i);
+  auto take_d = [&](uint4 &slot, int64_t e) {
+    uint4 v = slot;
     if (DROP) {
-      gen.template mask<DT>(v, static_cast<uint64_t>(e0 + i * estep));
-      slot_d(i) = v;
+      gen.template mask<DT>(v, static_cast<uint64_t>(e));
+      slot = v;
     }
     return v;
   };
   const int npair = nr >> 1;
-  for (int j = 0; j < npair; ++j) {
-    cp_async_wait_upto(npair - j);
-    const int i = 2 * j;
-    const uint4 da = take_d(i), db = take_d(i + 1);
-    sum_rows<DT, ACT>(slot_x(i), da, slot_x(i + 1), db, true, k, s1, s2);
-  }
-  cp_async_wait<0>();
-  if (nr & 1) {
-    const uint4 xv = slot_x(nr - 1), dv = take_d(nr - 1);
-    sum_rows<DT, ACT>(xv, dv, xv, dv, false, k, s1, s2);
+  {
+    uint4 *at = data;
+    int64_t e = e0;
+#pragma unroll 1
+    for (int j = npair; j > 0; --j) {
+      cp_async_wait_upto(j);
+      const uint4 da = take_d(at[nact], e), db = take_d(at[3 * nact], e + estep);
+      sum_rows<DT, ACT>(at[0], da, at[2 * nact], db, true, k, s1, s2);
+      at += 4 * nact;
+      e += 2 * estep;
+    }
+    cp_async_wait<0>();
+    if (nr & 1) {
+      const uint4 xv = at[0], dv = take_d(at[nact], e);
+      sum_rows<DT, ACT>(xv, dv, xv, dv, false, k, s1, s2);
+    }
   }
 
   const int ch0 = chunk0 * V;
@@ -150,12 +162,16 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
     float2 ra[V / 2], rc[V / 2];
     dx_constants<DT>(a, gfin, g0, chunk0 + cc, ra, rc);
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
-    for (int i = 0; i < nr; i += 2) {
-      const int i2 = i + 1 < nr ? i + 1 : i;
-      uint4 xa = slot_x(i), xb = slot_x(i2);
-      dx_rows<DT, ACT, DROP>(a, xa, slot_d(i), xb, slot_d(i2), k, ra, rc);
-      st_global_cs_v4(dst + i * bstep, xa);
-      if (i2 != i) st_global_cs_v4(dst + i2 * bstep, xb);
+    const uint4 *at = data;
+#pragma unroll 1
+    for (int left = nr; left > 0; left -= 2) {
+      const int o = left > 1 ? 2 * nact : 0;  // (a last row alone is taken twice)
+      uint4 xa = at[0], xb = at[o];
+      dx_rows<DT, ACT, DROP>(a, xa, at[nact], xb, at[o + nact], k, ra, rc);
+      st_global_cs_v4(dst, xa);
+      if (left > 1) st_global_cs_v4(dst + bstep, xb);
+      at += 4 * nact;
+      dst += 2 * bstep;
     }
   }
   if (csize > 1) cluster_wait_acquire();
@@ -168,11 +184,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
   const int tid = threadIdx.x;
-  const int b = static_cast<int>(blockIdx.x) / a.splits;
+  const int b = a.by_splits(blockIdx.x);
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
-  const Parts parts(a.S, a.splits);
+  const Parts parts(a);
   const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float *cb = reinterpret_cast<float *>(smem);
   float *cg = cb + a.C;
@@ -185,7 +201,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
 
   for (int col = 0; col < a.nc; col += a.ncs) {
     const bool on = rl < a.R && cc < min(a.ncs, a.nc - col);
-    const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
+    const int nr = (on && rl < nrow) ? a.by_R(nrow - rl + a.R - 1) : 0;
     const int64_t c0 = (static_cast<int64_t>(b) * a.S + s0 + rl) * a.nc + col + cc;
     const int64_t step = static_cast<int64_t>(a.R) * a.nc;
     const uint4 *xs = static_cast<const uint4 *>(a.x) + c0;
@@ -238,11 +254,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
   constexpr int V = chunk_elems(DT);
   const int tid = threadIdx.x;
   const int lane = tid & 31;
-  const int b = static_cast<int>(blockIdx.x) / a.splits;
+  const int b = a.by_splits(blockIdx.x);
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
-  const Parts parts(a.S, a.splits);
+  const Parts parts(a);
   const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float2 *gfin = reinterpret_cast<float2 *>(smem);
 
@@ -269,7 +285,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
   if (DROP) gen.start();
   for (int col = 0; col < a.nc; col += a.ncs) {
     if (rl >= a.R || cc >= min(a.ncs, a.nc - col) || rl >= nrow) continue;
-    const int nr = (nrow - rl + a.R - 1) / a.R;
+    const int nr = a.by_R(nrow - rl + a.R - 1);
     BwdConst<V> k;
     load_const<DT>(a, b, col + cc, k);
     float2 ra[V / 2], rc[V / 2];

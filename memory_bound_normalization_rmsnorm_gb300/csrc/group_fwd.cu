@@ -6,7 +6,7 @@
 // it is latency: a call is little more than one wave of CTAs, whose phases
 // (copy in, fold, cluster exchange, output) follow each other.  Smaller CTAs,
 // several per SM, overlap them; group.cu chooses by an estimate.  8 x 4096 x
-// 320 bf16 SiLU: 15.1 us, of which the two passes over HBM need 6.2; copy in
+// 320 bf16 SiLU: 15.0 us, of which the two passes over HBM need 6.2; copy in
 // 4.3, fold and exchange 2.6, output 4 to 5, launch 2 (42 MB, 41 % of the
 // measured copy bandwidth).  1 x 64 x 1280: 3.4 us.
 //
@@ -28,20 +28,20 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   const int nthr = blockDim.x;
   const int tid = threadIdx.x;
   const int nact = a.ncs * a.R;  // threads that own a chunk column
-  const int unit = static_cast<int>(blockIdx.x) / a.k;
+  const int unit = a.by_k(blockIdx.x);
   const int q = static_cast<int>(blockIdx.x) - unit * a.k;
-  const int b = unit / a.nslab;
+  const int b = a.by_nslab(unit);
   const int slab = unit - b * a.nslab;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
   const int chunk0 = slab * a.ncs;
   const int ncs_me = min(a.ncs, a.nc - chunk0);
   const int g0 = slab * a.sg;
   const int ng = min(a.sg, a.G - g0);
   const bool on = rl < a.R && cc < ncs_me;
-  const Parts parts(a.S, a.k);
+  const Parts parts(a);
   const int s0 = parts.begin(q), nrow = parts.rows(q);
-  const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
+  const int nr = (on && rl < nrow) ? a.by_R(nrow - rl + a.R - 1) : 0;
 
   uint4 *data = reinterpret_cast<uint4 *>(smem) + tid;  // slot i of this thread: data[i * nact]
   unsigned char *fold = smem + static_cast<size_t>(a.slots) * nact * 16;
@@ -57,9 +57,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   const int64_t estep = static_cast<int64_t>(a.R) * a.C;
   const unsigned char *src = static_cast<const unsigned char *>(a.x) + e0 * elem_bytes(DT);
   const int64_t bstep = estep * elem_bytes(DT);
-  for (int i = 0; i < nr; ++i) {
-    cp_async_16(data + static_cast<size_t>(i) * nact, src + i * bstep);
-    if ((i & 3) == 3) cp_async_commit();
+  {
+    uint4 *to = data;
+    for (int i = 0; i < nr; ++i) {
+      cp_async_16(to, src);
+      to += nact;
+      src += bstep;
+      if ((i & 3) == 3) cp_async_commit();
+    }
   }
   cp_async_commit();
 
@@ -126,13 +131,17 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
     DropGen gen(a.drop);
     if (DROP) gen.start();
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
+    const uint4 *at = data;
+    int64_t e = e0;
 #pragma unroll 2
-    for (int i = 0; i < nr; i += 2) {
-      const int i2 = i + 1 < nr ? i + 1 : i;
-      uint4 va = data[static_cast<size_t>(i) * nact], vb = data[static_cast<size_t>(i2) * nact];
-      out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, e0 + i * estep, e0 + i2 * estep);
-      st_global_cs_v4(dst + i * bstep, va);
-      if (i2 != i) st_global_cs_v4(dst + i2 * bstep, vb);
+    for (int left = nr; left > 0; left -= 2) {
+      uint4 va = at[0], vb = at[left > 1 ? nact : 0];  // (a last row alone is taken twice)
+      out_rows<DT, ACT, DROP>(va, vb, nmu, sc, bf, gen, e, e + estep);
+      st_global_cs_v4(dst, va);
+      if (left > 1) st_global_cs_v4(dst + bstep, vb);
+      at += 2 * nact;
+      e += 2 * estep;
+      dst += 2 * bstep;
     }
   }
   if (a.k > 1) cluster_wait_acquire();  // no CTA leaves while a peer may read it
@@ -145,11 +154,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_stats_kernel(const Gro
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
   const int tid = threadIdx.x;
-  const int b = static_cast<int>(blockIdx.x) / a.splits;
+  const int b = a.by_splits(blockIdx.x);
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
-  const Parts parts(a.S, a.splits);
+  const Parts parts(a);
   const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float *chm = reinterpret_cast<float *>(smem);
   float *chq = chm + a.C;
@@ -160,7 +169,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_stats_kernel(const Gro
 
   for (int col = 0; col < a.nc; col += a.ncs) {
     const bool on = rl < a.R && cc < min(a.ncs, a.nc - col);
-    const int nr = (on && rl < nrow) ? (nrow - rl + a.R - 1) / a.R : 0;
+    const int nr = (on && rl < nrow) ? a.by_R(nrow - rl + a.R - 1) : 0;
     const uint4 *src = static_cast<const uint4 *>(a.x) +
                        (static_cast<int64_t>(b) * a.S + s0 + rl) * a.nc + col + cc;
     const int64_t step = static_cast<int64_t>(a.R) * a.nc;
@@ -201,11 +210,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
   constexpr int V = chunk_elems(DT);
   const int tid = threadIdx.x;
   const int lane = tid & 31;
-  const int b = static_cast<int>(blockIdx.x) / a.splits;
+  const int b = a.by_splits(blockIdx.x);
   const int sp = static_cast<int>(blockIdx.x) - b * a.splits;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
-  const Parts parts(a.S, a.splits);
+  const Parts parts(a);
   const int s0 = parts.begin(sp), nrow = parts.rows(sp);
   float2 *gfin = reinterpret_cast<float2 *>(smem);
 
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
   if (DROP) gen.start();
   for (int col = 0; col < a.nc; col += a.ncs) {
     if (rl >= a.R || cc >= min(a.ncs, a.nc - col) || rl >= nrow) continue;
-    const int nr = (nrow - rl + a.R - 1) / a.R;
+    const int nr = a.by_R(nrow - rl + a.R - 1);
     float2 nmu[V / 2], sc[V / 2], bf[V / 2];
     out_constants<DT>(a, gfin, 0, col + cc, nmu, sc, bf);
     const int64_t row = static_cast<int64_t>(b) * a.S + s0 + rl;

@@ -70,7 +70,7 @@ struct Ring {
     full = reinterpret_cast<uint64_t *>(smem + L.bar_off);
     empty = full + a.stages;
     abort_flag = reinterpret_cast<volatile int *>(smem + L.flag_off);
-    const Parts parts(a.S, a.splits);
+    const Parts parts(a);
     row0 = parts.begin(split);
     nrow = parts.rows(split);
     TR = a.U * a.R;
@@ -273,9 +273,10 @@ struct Role {
   int sj, slab, sp;
   __device__ __forceinline__ explicit Role(const GroupArgs &a) {
     const int u = static_cast<int>(blockIdx.x);
-    sp = u % a.splits;
-    slab = (u / a.splits) % a.nslab;
-    sj = u / (a.splits * a.nslab);
+    const int v = a.by_splits(u);
+    sp = u - v * a.splits;
+    sj = a.by_nslab(v);
+    slab = v - sj * a.nslab;
   }
 };
 
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   const Role role(a);
   Ring<DT, 1> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
   const bool on = rl < a.R && cc < ring.ncs;
   const int own = on ? rl * a.ncs + cc : -1;  // this thread's chunk in a tile
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   float2 *gfin = reinterpret_cast<float2 *>(smem + ring.L.gst_off);
   float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
   const int pstride = (a.splits + 1) & ~1;  // (rows of partials start on 16 bytes)
-  const Parts parts(a.S, a.splits);
+  const Parts parts(a);
   const float invS = 1.0f / static_cast<float>(a.S);
   const float fD = static_cast<float>(a.D);
   const float invCount = 1.0f / (static_cast<float>(a.S) * fD);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   Ring<DT, 2> ring(a, smem, role.sp, role.slab);
   const int tid = threadIdx.x;
   const int lane = tid & 31;
-  const int rl = tid / a.ncs;
+  const int rl = a.by_ncs(tid);
   const int cc = tid - rl * a.ncs;
   const bool on = rl < a.R && cc < ring.ncs;
   const int own = on ? rl * a.ncs + cc : -1;  // this thread's chunk in a tile

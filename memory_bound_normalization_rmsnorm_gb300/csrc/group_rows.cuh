@@ -6,11 +6,11 @@
 
 namespace gbn {
 
-// The groups of consecutive channels, with one division for the first.
+// The groups of consecutive channels.
 struct GroupWalk {
   int g, left, D;
   __device__ __forceinline__ GroupWalk(const GroupArgs &a, int c)
-      : g(c / a.D), left(a.D - (c - g * a.D)), D(a.D) {}
+      : g(a.by_D(c)), left(a.D - (c - g * a.D)), D(a.D) {}
   __device__ __forceinline__ int next() {
     const int r = g;
     if (--left == 0) {
