@@ -174,10 +174,11 @@ norm_status_t make_ring_plan(int B, int S, int C, int G, int dt, bool bwd, int s
   p.tm = std::max(0, std::min(ov.tm >= 0 ? std::min(ov.tm, kRingTmemTiles) : kRingTmemTiles,
                               most - p.stages));
   // A CTA takes all of its SM's tensor memory, and its peers wait for it at
-  // the grid barrier: two of them on one SM would wait for each other.  So
-  // their shared memory is more than half of an SM's.
-  const uint32_t over_half = (static_cast<uint32_t>(smem_optin) + 1024u) / 2u;
-  if (p.tm && p.smem < over_half) p.smem = over_half;
+  // the grid barrier: beside another CTA that holds some (of this kernel or of
+  // one on another stream whose CTAs wait for each other too) the two could
+  // wait for each other.  So it takes all of the shared memory as well, which
+  // every kernel that feeds tensor memory needs.
+  if (p.tm) p.smem = static_cast<uint32_t>(smem_optin);
   const int64_t tile_bytes = static_cast<int64_t>(TR) * p.ncs * 16 * nt;
   p.keep = ov.keep >= 0 ? ov.keep : static_cast<int>(kL2KeepBytes / (tile_bytes * p.grid));
   *out = p;

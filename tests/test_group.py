@@ -408,3 +408,45 @@ def test_binding_refuses_counts_and_codes_out_of_range():
     with pytest.raises(gb.NormError) as e:
         gb.norm_dropout_add_fwd(x, x, g, mode=1 << 32, p=0.1, seed=1)
     assert e.value.status == 4
+
+
+def test_beside_other_kernels_with_tensor_memory():
+    """The whole-GPU form on one stream while the streamed row backward and the
+    normalisation-GEMM, which use tensor memory too, run on two others."""
+    x, g, b, dy = make(2, 30000, 256, torch.bfloat16, seed=4)
+    for back in (False, True):
+        assert gb.norm_group_plan(2, 30000, 256, 32, gb.BF16, back)["form"] == 2
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rows, drows = (torch.randn(160, 131072, device="cuda", generator=gen).bfloat16()
+                   for _ in range(2))
+    rg = torch.randn(131072, device="cuda", generator=gen).bfloat16()
+    _, rr, _ = gb.norm_fwd(rows, rg, None, 1e-5, gb.RMS)
+    a = torch.randn(4096, 1024, device="cuda", generator=gen).bfloat16()
+    ag = torch.randn(1024, device="cuda", generator=gen).bfloat16()
+    w = torch.randn(1024, 1024, device="cuda", generator=gen).bfloat16()
+    wg, u, v = gb.norm_gemm_prepare(w, ag, None, gb.RMS)
+
+    def group():
+        y, rstd, mean = gb.norm_group_fwd(x, g, b, 32, 1e-5, "silu")
+        return (y, *gb.norm_group_bwd(dy, x, g, b, rstd, mean, 32, "silu"))
+
+    def wide():
+        return gb.norm_bwd(drows, rows, rg, rr, None, gb.RMS)[:2]
+
+    def gemm():
+        return gb.norm_gemm_fwd(a, wg, u, v, 1e-5, gb.RMS)[:1]
+
+    jobs = (group, wide, gemm)
+    want = [j() for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = []
+    for _ in range(5):
+        for s, j in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                got.append(j())
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for p, q in zip(outs, want[i % 3]):
+            assert torch.equal(p, q)
+    assert gb.norm_get_device_error() == 0

@@ -199,3 +199,18 @@ def test_shape_override_ignores_negative_values(text, monkeypatch):
         monkeypatch.setenv("GBNORM_GROUP", text)
         assert gb.norm_group_plan(4, 300, 320, 32, gb.BF16, back, SMS, OPTIN) == want
         monkeypatch.setenv("GBNORM_GROUP", ",".join(form))
+
+
+def test_ring_with_tensor_memory_has_its_sm_alone():
+    # a CTA that holds all of an SM's tensor memory while it waits for its peers
+    # leaves no shared memory for one that would wait for that tensor memory
+    seen = 0
+    for B, S, C, G in ((1, 262144, 256, 32), (4, 16384, 512, 32), (16, 4096, 320, 32),
+                       (64, 1024, 640, 32), (3, 9000, 64, 8), (300, 2048, 1280, 32)):
+        for dtype in (gb.BF16, gb.FP16, gb.FP32):
+            for back in (False, True):
+                p = gb.norm_group_plan(B, S, C, G, dtype, back, SMS, OPTIN)
+                if p["form"] == 2 and p["tensor_memory_tiles"]:
+                    seen += 1
+                    assert p["smem_bytes"] == OPTIN, (B, S, C, dtype, back)
+    assert seen >= 6
