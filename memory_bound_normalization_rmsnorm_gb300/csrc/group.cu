@@ -80,42 +80,60 @@ int ctas_per_sm(int threads, int64_t smem, int smem_optin) {
 
 // Estimated times (us), for choosing among the plans of a shape.  Form of the
 // estimate: memory time at the measured bandwidth (less for slabs narrower
-// than 128 bytes of a row and where few SMs work), issue time (an element
-// takes about 20 instructions forward, 15 backward and pass), and fixed times
-// per launch, cluster, fold level, row of a thread and wave.  The constants
-// were fitted to about 1500 measured plans of 38 shapes (1 to 5000 samples, 1
-// to 65536 positions, 64 to 2560 channels, both directions, 16 and 32 bits):
-// the plan of least estimate is within 1 % of the fastest measured one in the
-// geometric mean (a rule of one wave of widest CTAs was 8 % off).
+// than 128 bytes of a row and where few SMs work), issue time per element and
+// per thread, both stretched where the last wave of single CTAs, or the SMs'
+// shares of one wave, are uneven or slabs and row lanes reach past the sample,
+// and fixed times per launch, cluster and its CTAs, fold level, row of a thread
+// and wave.  Large clusters leave part of the SMs unused, less so the more CTAs
+// an SM takes.  The constants were fitted to 8400 measured plans of 156 shapes
+// (1 to 5000 samples, 1 to 65536 positions, 32 to 2560 channels, both
+// directions, 16 and 32 bits): the plan of least estimate is 1.5 % slower than
+// the fastest measured one in the geometric mean, 16 % at worst (a fit that knew
+// no unevenness: 5.5 %, 61 % at worst; one wave of widest CTAs: 8 %).
 double resident_cost(const GroupPlan &p, double elems, double bytes, bool bwd, bool reduce,
-                     int seg_bytes, int sms, int smem_optin) {
+                     int nc, int S, int sms, int smem_optin) {
   const int occ = ctas_per_sm(p.threads, p.smem, smem_optin);
-  const int cluster = p.k * p.cb;
-  const double usable = sms * (cluster > 4 ? 0.79 : cluster > 2 ? 0.94 : 1.0);  // they fragment
-  const double waves = std::ceil(static_cast<double>(p.grid) / (usable * occ));
-  const double used = std::min(usable, static_cast<double>(p.grid));
-  const double conc = std::min<double>(occ, std::ceil(static_cast<double>(p.grid) / usable));
-  const double seg = seg_bytes >= 128 ? 1.0 : seg_bytes >= 64 ? 0.9 : seg_bytes >= 32 ? 0.75 : 0.55;
-  const double mem = bytes / (6.6e6 * seg * std::min(1.0, used / (0.7 * sms)));
+  const int cluster = p.k * p.cb, seg_bytes = p.ncs * 16;
+  const double grid = static_cast<double>(p.grid);
+  const double usable =
+      sms * (1.0 - (cluster > 4 ? 0.16 : cluster > 2 ? 0.095 : 0.0) / occ);
+  const double share = grid / usable, fill = share / occ, waves = std::ceil(fill);
+  const double conc = fill > 1 ? occ : std::max(1.0, std::ceil(share));
+  double uneven = 1.0;
+  if (fill > 1) {
+    if (occ == 1) uneven += 0.70 * (waves - fill) / fill;
+  } else if (share > 1) {
+    uneven += 0.225 * (std::ceil(share) - share) / share;
+  }
+  const double past_slabs = static_cast<double>(p.ncs) * p.nslab / nc;
+  const double past_rows = static_cast<double>(p.slots) * p.R * p.k / S;
+  const double used = std::min(usable, grid);
+  const double seg = seg_bytes >= 128 ? 1.0 : seg_bytes >= 64 ? 0.9 : seg_bytes >= 32 ? 0.8 : 0.7;
+  const double mem = bytes * std::pow(past_slabs, 0.24) /
+                     (6.6e6 * seg * std::min(1.0, used / (0.43 * sms)));
   const double warps = conc * p.threads / 32;
-  const double issue = elems * (bwd ? 0.26e-6 : 0.35e-6) * sms / used /
-                       std::min(1.0, std::pow(warps / 16.0, 0.26));
+  const double issue =
+      (elems * (bwd ? 0.378e-6 : 0.238e-6) * std::pow(past_slabs, 0.58) * past_rows +
+       grid * p.threads * (bwd ? 4.1e-6 : 0.12e-6)) *
+      sms / used / std::min(1.0, std::pow(warps / 16.0, 0.4));
   const double level = p.R > 8 ? std::log2(p.R / 8.0) : p.R > 1 ? 1.0 : 0.0;
-  return 3.0 + (reduce ? 3.0 : 0.0) + (cluster > 1 ? 1.8 : 0.0) + (cluster > 4 ? 0.7 : 0.0) +
-         0.18 * level +
-         (bwd ? 0.124 : 0.062) * p.slots +
-         (mem + issue) * (1.0 + 0.55 * (waves > 1 ? 1.0 / conc : 1.0)) + 1.5 * (waves - 1);
+  return 2.86 + (reduce ? 1.4 : 0.0) + (cluster > 1 ? 0.82 : 0.0) + (cluster > 4 ? 0.16 : 0.0) +
+         (bwd ? 0.072 * (cluster - 1) : 0.031 * (p.k - 1)) + 0.29 * level +
+         (bwd ? 0.14 : 0.07) * p.slots +
+         (mem + issue) * uneven * (1.0 + 0.083 * (fill > 1 ? 1.0 / conc : 1.0)) +
+         4.1 * (waves - 1);
 }
 
-// Bytes of a round's first pass that are still near (shared memory and L2)
-// when the output pass comes to them.
-constexpr double kNearBytes = 100e6;
+// Bytes of a round's first pass that cost nothing to read again in the output
+// pass (the rest of those that are still near, in shared memory, tensor memory
+// and L2, come at L2's price).
+constexpr double kNearBytes = 47e6;
 
 double ring_cost(const GroupPlan &p, double elems, double bytes, double read_bytes, bool bwd,
                  int sms) {
   const double again = std::max(0.0, read_bytes / p.rounds - kNearBytes) * p.rounds;
-  const double issue = elems * (bwd ? 0.26e-6 : 0.35e-6) * 0.8 * sms / static_cast<double>(p.grid);
-  return 3.0 + 12.0 * p.rounds + (bytes + again) / 6.6e6 + issue;
+  const double issue = elems * (bwd ? 0.38e-6 : 0.24e-6) * sms / static_cast<double>(p.grid);
+  return 1.0 + (bwd ? 3.5 : 0.0) + 9.0 * p.rounds + (bytes + again) / 6.6e6 + issue;
 }
 
 // What L2 is asked to hold of it.
@@ -231,7 +249,7 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
             p.smem = group_smem_bytes(p.slots, nt, R, ncs, V, sg);
             if (static_cast<int64_t>(p.smem) <= smem_optin) {
               const double c =
-                  resident_cost(p, elems, bytes, bwd, bwd && B > p.cb, ncs * 16, sms, smem_optin);
+                  resident_cost(p, elems, bytes, bwd, bwd && B > p.cb, nc, S, sms, smem_optin);
               if (best_cost < 0 || c < best_cost) {
                 best_cost = c;
                 best = p;
