@@ -88,22 +88,52 @@ at::Tensor output(PyObject *o, const char *name, at::ScalarType dt, c10::IntArra
   return t;
 }
 
-// Two fp32 outputs of the same small shape: the given ones, checked, or new
-// ones that share one allocation (an allocation costs 0.9 us of host time),
-// each on a 256-byte boundary.
-void two_outputs(PyObject *oa, PyObject *ob, const char *na, const char *nb, c10::IntArrayRef shape,
-                 c10::Device dev, at::Tensor &a, at::Tensor &b) {
-  if (oa != Py_None || ob != Py_None) {
-    a = output(oa, na, at::kFloat, shape, dev);
-    b = output(ob, nb, at::kFloat, shape, dev);
+// A contiguous tensor over a part of base's storage.
+at::Tensor part(const at::Tensor &base, int64_t byte_offset, at::ScalarType dt,
+                c10::IntArrayRef shape) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()),
+                                                          base.key_set(),
+                                                          c10::scalarTypeToTypeMeta(dt));
+  t.unsafeGetTensorImpl()->set_storage_offset(byte_offset /
+                                              static_cast<int64_t>(c10::elementSize(dt)));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
+int64_t pad256(int64_t bytes) { return (bytes + 255) & ~int64_t(255); }
+
+// A main output and one or two small fp32 outputs of a shape of their own
+// (statistics, parameter gradients): the given ones, checked, or new ones.  An
+// allocation costs 0.9 us of host time, so new small ones share one, each on a
+// 256-byte boundary, and lie behind a new main output of at most kShareBytes:
+// what one of them can keep alive of the others stays bounded by that, and
+// calls on larger tensors take longer on the device than on the host.
+constexpr int64_t kShareBytes = 1 << 20;
+
+void outputs(PyObject *om, const char *nm, at::ScalarType dt, c10::IntArrayRef main_shape,
+             PyObject *oa, const char *na, PyObject *ob, const char *nb, bool two,
+             c10::IntArrayRef shape, c10::Device dev, at::Tensor &m, at::Tensor &a, at::Tensor &b) {
+  const int64_t small = pad256(4 * c10::multiply_integers(shape));
+  const bool fresh = oa == Py_None && ob == Py_None;
+  const int64_t es = static_cast<int64_t>(c10::elementSize(dt));
+  const int64_t main_bytes = es * c10::multiply_integers(main_shape);
+  if (om == Py_None && fresh && main_bytes <= kShareBytes) {
+    const int64_t at = pad256(main_bytes);
+    m = at::detail::empty_cuda({(at + small * (two ? 2 : 1)) / es}, dt, dev, std::nullopt);
+    a = part(m, at, at::kFloat, shape);
+    if (two) b = part(m, at + small, at::kFloat, shape);
+    m.unsafeGetTensorImpl()->set_sizes_contiguous(main_shape);
     return;
   }
-  const int64_t n = (c10::multiply_integers(shape) + 63) & ~int64_t(63);
-  a = at::detail::empty_cuda({2 * n}, at::kFloat, dev, std::nullopt);
-  b = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(a.storage()), a.key_set(), a.dtype());
-  b.unsafeGetTensorImpl()->set_storage_offset(n);
-  b.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  a.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  m = output(om, nm, dt, main_shape, dev);
+  if (fresh && two) {
+    a = at::detail::empty_cuda({small / 2}, at::kFloat, dev, std::nullopt);
+    b = part(a, small, at::kFloat, shape);
+    a.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return;
+  }
+  a = output(oa, na, at::kFloat, shape, dev);
+  if (two) b = output(ob, nb, at::kFloat, shape, dev);
 }
 
 void *ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -283,7 +313,7 @@ PyObject *dropout_add_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor &x = lead(a[0], "x");
     const c10::Device dev = x.device();
     const Rows d(x);
-    const at::ScalarType bf = at::kBFloat16, f32 = at::kFloat;
+    const at::ScalarType bf = at::kBFloat16;
     const at::Tensor &r = tensor(a[1], "r"), &gamma = tensor(a[2], "gamma"),
                      &beta = tensor(a[3], "beta", true);
     check(x, "x", bf, d.shape, dev);
@@ -295,12 +325,9 @@ PyObject *dropout_add_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rng rng(a + 6, dev);
     const StreamScope on(a[14], dev);
     const at::Tensor h = output(a[10], "h", bf, d.shape, dev);
-    const at::Tensor y = output(a[11], "y", bf, d.shape, dev);
-    at::Tensor rstd, mean;
-    if (mode == NORM_LAYER || a[13] != Py_None)
-      two_outputs(a[12], a[13], "rstd", "mean", d.lead, dev, rstd, mean);
-    else
-      rstd = output(a[12], "rstd", f32, d.lead, dev);
+    at::Tensor y, rstd, mean;
+    outputs(a[11], "y", bf, d.shape, a[12], "rstd", a[13], "mean",
+            mode == NORM_LAYER || a[13] != Py_None, d.lead, dev, y, rstd, mean);
     return result(norm_dropout_add_fwd(ptr(x), ptr(r), ptr(gamma), ptr(beta), d.M, d.N, eps,
                                        static_cast<norm_mode_t>(mode), rng.p, rng.seed, rng.offset,
                                        rng.dev_word, ptr(h), ptr(y),
@@ -330,13 +357,10 @@ PyObject *dropout_add_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const norm_mode_t mode = static_cast<norm_mode_t>(code_of(a[6]));
     const Rng rng(a + 7, dev);
     const StreamScope on(a[17], dev);
-    const at::Tensor dx = output(a[11], "dx", bf, d.shape, dev);
     const at::Tensor dr = output(a[12], "dr", bf, d.shape, dev);
-    at::Tensor dg, db;
-    if ((mode == NORM_LAYER && truth(a[15])) || a[14] != Py_None)
-      two_outputs(a[13], a[14], "dgamma", "dbeta", {d.N}, dev, dg, db);
-    else
-      dg = output(a[13], "dgamma", f32, {d.N}, dev);
+    at::Tensor dx, dg, db;
+    outputs(a[11], "dx", bf, d.shape, a[13], "dgamma", a[14], "dbeta",
+            (mode == NORM_LAYER && truth(a[15])) || a[14] != Py_None, {d.N}, dev, dx, dg, db);
     const Workspace ws(a[16], dev, [&](size_t *b) {
       return norm_dropout_add_bwd_workspace_bytes(d.M, d.N, mode, b);
     });
@@ -380,9 +404,9 @@ PyObject *group_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const norm_act_t act = static_cast<norm_act_t>(code_of(a[5]));
     const Rng rng(a + 6, dev);
     const StreamScope on(a[14], dev);
-    const at::Tensor y = output(a[10], "y", dt, x.sizes(), dev);
-    at::Tensor rstd, mean;
-    two_outputs(a[11], a[12], "rstd", "mean", {d.B, groups}, dev, rstd, mean);
+    at::Tensor y, rstd, mean;
+    outputs(a[10], "y", dt, x.sizes(), a[11], "rstd", a[12], "mean", true, {d.B, groups}, dev, y,
+            rstd, mean);
     const Workspace ws(a[13], dev, [&](size_t *b) {
       return norm_group_fwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
     });
@@ -417,12 +441,9 @@ PyObject *group_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const norm_act_t act = static_cast<norm_act_t>(code_of(a[7]));
     const Rng rng(a + 8, dev);
     const StreamScope on(a[17], dev);
-    const at::Tensor dx = output(a[12], "dx", dt, x.sizes(), dev);
-    at::Tensor dg, db;
-    if (truth(a[15]) || a[14] != Py_None)
-      two_outputs(a[13], a[14], "dgamma", "dbeta", {d.C}, dev, dg, db);
-    else
-      dg = output(a[13], "dgamma", f32, {d.C}, dev);
+    at::Tensor dx, dg, db;
+    outputs(a[12], "dx", dt, x.sizes(), a[13], "dgamma", a[14], "dbeta",
+            truth(a[15]) || a[14] != Py_None, {d.C}, dev, dx, dg, db);
     const Workspace ws(a[16], dev, [&](size_t *b) {
       return norm_group_bwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
     });

@@ -1,6 +1,6 @@
 """Outputs that the native binding allocates: the statistics (and the
-parameter gradients) of a call share one allocation, as tensors of their own
-that behave like any other."""
+parameter gradients) of a call share one allocation, up to 1 MB with the main
+output, as tensors of their own that behave like any other."""
 import pytest
 import torch
 
@@ -63,3 +63,30 @@ def test_streams_given_as_tensors_streams_and_handles():
         for u, v in zip(got + back, want + grads):
             assert torch.equal(u, v)
     assert torch.cuda.current_stream() != s
+
+
+def test_small_main_outputs_share_with_their_statistics():
+    """Up to 1 MB the main output, too, lies in the statistics' allocation:
+    none overlaps another, each keeps its values when another is written or
+    freed, and a larger output stands alone."""
+    for S in (1, 37, 1000, 40000):
+        x = torch.randn(2, S, 40, device="cuda", dtype=torch.bfloat16)
+        g, b = torch.ones_like(x[0, 0]), torch.zeros_like(x[0, 0])
+        y, rstd, mean = gb.norm_group_fwd(x, g, b, 4, 1e-5, "gelu")
+        outs = [y, rstd, mean, *gb.norm_group_bwd(x, x, g, b, rstd, mean, 4, "gelu")]
+        r2 = x.view(-1, 40)
+        outs += gb.norm_dropout_add_fwd(r2, r2, g, b, 1e-5, gb.LAYER, p=0.5, seed=3)
+        outs += gb.norm_dropout_add_bwd(r2, r2, outs[6], g, outs[8], outs[9], gb.LAYER, p=0.5, seed=3)
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs)
+        assert all(lo % 256 == 0 for lo, _ in spans)
+        assert all(hi <= lo for (_, hi), (lo, _) in zip(spans, spans[1:]))
+        alone = y.untyped_storage().nbytes() == y.numel() * 2
+        assert alone == (y.numel() * 2 > 1 << 20)
+        want = [t.clone() for t in outs]
+        while outs:
+            t, w = outs.pop(0), want.pop(0)
+            assert t.is_contiguous() and torch.equal(t, w)
+            t.fill_(float("nan"))
+            del t
+            torch.cuda.synchronize()
+        assert torch.isfinite(x).all()
