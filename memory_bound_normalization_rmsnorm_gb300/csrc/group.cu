@@ -22,7 +22,6 @@ namespace gbn {
 namespace {
 
 constexpr int kResident = 0, kStreamed = 1, kRing = 2;
-constexpr int kMaxCluster = 8;  // the portable size
 
 struct GroupPlan {
   int form = kResident;
@@ -225,7 +224,7 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
       if (ov.sg && sg != ov.sg) continue;
       const int ncs = static_cast<int>(static_cast<int64_t>(sg) * D / V);
       if (ncs > kGroupThreads) continue;
-      for (int k = 1; k <= 8 && k <= S; k *= 2) {
+      for (int k = 1; k <= kMaxGroupCluster && k <= S; k *= 2) {
         if (ov.k && k != ov.k) continue;
         const int rows = static_cast<int>(ceil_div64(S, k));
         const int rmax = std::min(kGroupThreads / ncs, std::max(1, S / k));
@@ -239,7 +238,7 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
           p.k = k;
           // a small batch in one cluster: dgamma and dbeta come out of it
           // whole, without a second launch
-          if (bwd && static_cast<int64_t>(B) * k <= kMaxCluster && ov.cb != 1) p.cb = B;
+          if (bwd && static_cast<int64_t>(B) * k <= kMaxGroupCluster && ov.cb != 1) p.cb = B;
           p.R = R;
           p.slots = (rows + R - 1) / R;
           p.threads = round32(ncs * R);

@@ -29,6 +29,7 @@ constexpr int kActSilu = 1;  // k = z
 constexpr int kActGelu = 2;  // k = 2 sqrt(2 / pi) (z + 0.044715 z^3): the tanh form
 
 constexpr int kGroupThreads = 512;  // largest CTA of these kernels
+constexpr int kMaxGroupCluster = 8;  // the portable size
 // Ring: rows per thread and tile.
 constexpr int kRingRowsFwd = 8;
 constexpr int kRingRowsBwd = 4;
@@ -594,14 +595,23 @@ struct Parts {
 
 // Parameters of a thread's V channels as fp32 pairs: gamma, beta (0 when
 // absent).
+struct AffineRaw {
+  uint4 g, b;
+};
+__device__ __forceinline__ AffineRaw load_affine_raw(const GroupArgs &a, int chunk) {
+  AffineRaw r;
+  r.g = ld_global_nc_v4(static_cast<const uint4 *>(a.gamma) + chunk);
+  r.b = make_uint4(0, 0, 0, 0);
+  if (a.beta) r.b = ld_global_nc_v4(static_cast<const uint4 *>(a.beta) + chunk);
+  return r;
+}
 template <int DT>
 __device__ __forceinline__ void load_affine(const GroupArgs &a, int chunk,
                                             float2 (&gf)[chunk_elems(DT) / 2],
                                             float2 (&bf)[chunk_elems(DT) / 2]) {
-  unpack<DT>(ld_global_nc_v4(static_cast<const uint4 *>(a.gamma) + chunk), gf);
-  uint4 bv = make_uint4(0, 0, 0, 0);
-  if (a.beta) bv = ld_global_nc_v4(static_cast<const uint4 *>(a.beta) + chunk);
-  unpack<DT>(bv, bf);
+  const AffineRaw r = load_affine_raw(a, chunk);
+  unpack<DT>(r.g, gf);
+  unpack<DT>(r.b, bf);
 }
 
 const void *group_ring_kernel_ptr(int dt, int act, bool drop, bool bwd);

@@ -125,16 +125,21 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
   if (csize > 1) cluster_sync(); else __syncthreads();
   const float inv = __fdividef(1.0f, static_cast<float>(a.S) * static_cast<float>(a.D));
-#pragma unroll 1
-  for (int g = tid; g < ng; g += nthr) {
-    float2 t = gst[g];
-    if (a.k > 1) {
-      t = make_float2(0.f, 0.f);
-      for (int r = 0; r < a.k; ++r) t = add2(t, ld_cluster_f2(gst + g, bl * a.k + r));
+  // (eight lanes per group, each with the partial of one CTA of the sample)
+  each_group(ng, 3, [&](int g, int r, bool in) {
+    float2 t = make_float2(0.f, 0.f);
+    if (a.k == 1) {
+      if (in) t = gst[g];
+    } else {
+      if (in && r < a.k) t = ld_cluster_f2(gst + g, bl * a.k + r);
+      t.x = lanes_sum(t.x, 3);
+      t.y = lanes_sum(t.y, 3);
     }
-    const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
-    gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
-  }
+    if (in && r == 0) {
+      const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
+      gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
+    }
+  });
   // dgamma / dbeta row of this cluster's samples: the CTAs share its channel
   // pairs out among them and sum over the cluster in rank order.
 #pragma unroll 1
@@ -146,9 +151,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
       tg = *pg;
       tb = *pb;
     } else {
-      for (int r = 0; r < csize; ++r) {
-        tg = add2(tg, ld_cluster_f2(pg, r));
-        tb = add2(tb, ld_cluster_f2(pb, r));
+      // (at most kMaxGroupCluster: all loads in flight together)
+#pragma unroll
+      for (int r = 0; r < kMaxGroupCluster; ++r) {
+        if (r < csize) {
+          tg = add2(tg, ld_cluster_f2(pg, r));
+          tb = add2(tb, ld_cluster_f2(pb, r));
+        }
       }
     }
     const int64_t at = static_cast<int64_t>(ub) * a.C + ch0 + 2 * j;

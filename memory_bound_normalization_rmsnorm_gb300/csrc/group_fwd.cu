@@ -25,7 +25,6 @@ template <int DT, int ACT, bool DROP>
 __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const GroupArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int V = chunk_elems(DT);
-  const int nthr = blockDim.x;
   const int tid = threadIdx.x;
   const int nact = a.ncs * a.R;  // threads that own a chunk column
   const int unit = a.by_k(blockIdx.x);
@@ -68,6 +67,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   }
   cp_async_commit();
 
+  AffineRaw aff;  // (their latency hides behind the statistics)
+  if (on) aff = load_affine_raw(a, chunk0 + cc);
+
   // Statistics of this thread's channels, four rows at a time as they land.
   ChannelStats<V> st;
   st.clear();
@@ -94,40 +96,32 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   if (a.k > 1) cluster_sync(); else __syncthreads();
   const float invS = __fdividef(1.0f, static_cast<float>(a.S));
   const float invD = __fdividef(1.0f, static_cast<float>(a.D));
-#pragma unroll 1
-  for (int g = tid; g < ng; g += nthr) {
-    float m, m2;
-    if (a.k == 1) {
-      m = gst[g].x;
-      m2 = gst[g].y;
-    } else {
-      // fixed rank order; counts n_r = rows of CTA r (times D)
-      float acc = 0.f;
-      for (int r = 0; r < a.k; ++r) {
-        const float n = static_cast<float>(parts.rows(r));
-        acc = fmaf(n, ld_cluster_f2(gst + g, r).x, acc);
-      }
-      m = acc * invS;
-      m2 = 0.f;
-      for (int r = 0; r < a.k; ++r) {
-        const float n = static_cast<float>(parts.rows(r)) * static_cast<float>(a.D);
-        const float2 v = ld_cluster_f2(gst + g, r);
-        m2 += fmaf(n * (v.x - m), v.x - m, v.y);
+  // Eight lanes per group, each with the partial of one CTA of the cluster
+  // (counts: that CTA's rows, times D): one round trip to the peers' shared
+  // memory, and the mean first, then the deviations from it.
+  each_group(ng, 3, [&](int g, int r, bool in) {
+    const bool mine = in && r < a.k;
+    const float2 v = !mine ? make_float2(0.f, 0.f) : a.k == 1 ? gst[g] : ld_cluster_f2(gst + g, r);
+    const float n = mine ? static_cast<float>(parts.rows(r)) : 0.f;
+    const float m = a.k == 1 ? v.x : lanes_sum(n * v.x, 3) * invS;
+    const float e = v.x - m;
+    const float m2 =
+        a.k == 1 ? v.y : lanes_sum(fmaf(n * static_cast<float>(a.D) * e, e, v.y), 3);
+    if (in && r == 0) {
+      const float rs = rsqrtf(m2 * invS * invD + a.eps);
+      gfin[g] = make_float2(m, rs);
+      if (q == 0) {
+        a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;
+        a.rstd[static_cast<int64_t>(b) * a.G + g0 + g] = rs;
       }
     }
-    const float rs = rsqrtf(m2 * invS * invD + a.eps);
-    gfin[g] = make_float2(m, rs);
-    if (q == 0) {
-      a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;
-      a.rstd[static_cast<int64_t>(b) * a.G + g0 + g] = rs;
-    }
-  }
+  });
   __syncthreads();
   if (a.k > 1) cluster_arrive_release();  // this CTA has read its peers' partials
 
   if (nr) {
     float2 nmu[V / 2], sc[V / 2], bf[V / 2];
-    out_constants<DT>(a, gfin, g0, chunk0 + cc, nmu, sc, bf);
+    out_constants<DT>(a, aff, gfin, g0, chunk0 + cc, nmu, sc, bf);
     DropGen gen(a.drop);
     if (DROP) gen.start();
     unsigned char *dst = static_cast<unsigned char *>(a.out) + e0 * elem_bytes(DT);
@@ -255,7 +249,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
     if (rl >= a.R || cc >= min(a.ncs, a.nc - col) || rl >= nrow) continue;
     const int nr = a.by_R(nrow - rl + a.R - 1);
     float2 nmu[V / 2], sc[V / 2], bf[V / 2];
-    out_constants<DT>(a, gfin, 0, col + cc, nmu, sc, bf);
+    out_constants<DT>(a, load_affine_raw(a, col + cc), gfin, 0, col + cc, nmu, sc, bf);
     const int64_t row = static_cast<int64_t>(b) * a.S + s0 + rl;
     const int64_t c0 = row * a.nc + col + cc;
     const int64_t step = static_cast<int64_t>(a.R) * a.nc;

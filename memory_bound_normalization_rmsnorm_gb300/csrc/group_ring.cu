@@ -404,7 +404,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
       });
       __syncthreads();
       float2 nmu[V / 2], sc[V / 2], bf[V / 2];
-      if (on) out_constants<DT>(a, gfin, g0, ring.chunk0 + cc, nmu, sc, bf);
+      if (on) {
+        const int chunk = ring.chunk0 + cc;
+        out_constants<DT>(a, load_affine_raw(a, chunk), gfin, g0, chunk, nmu, sc, bf);
+      }
       const int64_t e0 = group_elem(a, b, ring.row0 + rl, ring.chunk0 + cc, V);
       const int64_t estep = static_cast<int64_t>(a.R) * a.C;
       unsigned char *out = static_cast<unsigned char *>(a.out);

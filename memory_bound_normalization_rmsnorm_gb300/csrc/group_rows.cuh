@@ -85,12 +85,13 @@ __device__ __forceinline__ void out_rows(uint4 &xa, uint4 &xb, const float2 (&nm
 // Per-channel constants of the output pass: -mean, rstd gamma, beta.
 // `gst` holds (mean, rstd) of the groups from g0 on.
 template <int DT>
-__device__ __forceinline__ void out_constants(const GroupArgs &a, const float2 *gst, int g0,
-                                              int chunk, float2 (&nmu)[chunk_elems(DT) / 2],
+__device__ __forceinline__ void out_constants(const GroupArgs &a, const AffineRaw &aff,
+                                              const float2 *gst, int g0, int chunk, float2 (&nmu)[chunk_elems(DT) / 2],
                                               float2 (&sc)[chunk_elems(DT) / 2],
                                               float2 (&bf)[chunk_elems(DT) / 2]) {
   constexpr int V = chunk_elems(DT);
-  load_affine<DT>(a, chunk, sc, bf);
+  unpack<DT>(aff.g, sc);
+  unpack<DT>(aff.b, bf);
   GroupWalk g(a, chunk * V);
 #pragma unroll
   for (int p = 0; p < V / 2; ++p) {
