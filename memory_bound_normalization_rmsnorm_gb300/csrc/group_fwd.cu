@@ -6,9 +6,9 @@
 // it is latency: a call is little more than one wave of CTAs, whose phases
 // (copy in, fold, cluster exchange, output) follow each other.  Smaller CTAs,
 // several per SM, overlap them; group.cu chooses by an estimate.  8 x 4096 x
-// 320 bf16 SiLU: 14.4 us, of which the two passes over HBM need 6.2; copy in
-// about 4.3, fold and exchange 2.6, output 4 to 5, launch 2 (42 MB, 43 % of the
-// measured copy bandwidth).  1 x 64 x 1280: 3.5 us.
+// 320 bf16 SiLU: 13.8 us, of which the two passes over HBM need 6.2; copy in
+// about 4.3, fold and exchange 2, output 4 to 5, launch 2 (42 MB, 45 % of the
+// measured copy bandwidth).  1 x 64 x 1280: 3.4 us.
 //
 // Streamed form (groups wider than a CTA's 512 chunk columns): x is read twice,
 // the second time newest row first, partly from L2.  4 x 4096 x 8192 bf16 in one
