@@ -239,13 +239,15 @@ norm_status_t make_group_plan(int B, int S, int C, int G, int dt, bool bwd, int 
           // a small batch in one cluster: dgamma and dbeta come out of it
           // whole, without a second launch
           if (bwd && static_cast<int64_t>(B) * k <= kMaxGroupCluster && ov.cb != 1) p.cb = B;
-          p.R = R;
+          // (no more lanes than that many rows per thread need: idle ones cost
+          // folds and shared memory; 2 x 221 x 88 backward 5.9 -> 5.35 us)
           p.slots = (rows + R - 1) / R;
-          p.threads = round32(ncs * R);
-          const int64_t data = static_cast<int64_t>(p.slots) * ncs * R * 16 * nt;
+          p.R = ov.R ? R : (rows + p.slots - 1) / p.slots;
+          p.threads = round32(ncs * p.R);
+          const int64_t data = static_cast<int64_t>(p.slots) * ncs * p.R * 16 * nt;
           p.grid = static_cast<int64_t>(B) * p.nslab * k;
           if (data <= smem_optin && p.grid <= 0x7fffffff) {
-            p.smem = group_smem_bytes(p.slots, nt, R, ncs, V, sg);
+            p.smem = group_smem_bytes(p.slots, nt, p.R, ncs, V, sg);
             if (static_cast<int64_t>(p.smem) <= smem_optin) {
               const double c =
                   resident_cost(p, elems, bytes, bwd, bwd && B > p.cb, nc, S, sms, smem_optin);
