@@ -257,6 +257,15 @@ __device__ __forceinline__ void cp_async_wait_upto(int pending) {
   }
 }
 
+// Arrival at the barrier that keeps a cluster's CTAs from leaving while a peer
+// may still read their shared memory.  It passes on no data, so it is relaxed: a
+// releasing one waits for the thread's global stores (its reads of the peers are
+// done, their values having been used).  2 x 221 x 88 backward 5.3 -> 5.0 us, 3 x
+// 1517 x 168 fp32 forward 5.8 -> 5.55.
+__device__ __forceinline__ void cluster_arrive_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
 // ------------------------------------------- per-channel accumulators
 // Running (count, mean, M2) of a thread's V channels.  Rows enter in blocks
 // of four whose own mean and squared deviations are formed first, then

@@ -6,7 +6,7 @@
 // it is latency: a call is little more than one wave of CTAs, whose phases
 // (copy in, fold, cluster exchange, output) follow each other.  Smaller CTAs,
 // several per SM, overlap them; group.cu chooses by an estimate.  8 x 4096 x
-// 320 bf16 SiLU: 13.8 us, of which the two passes over HBM need 6.2; copy in
+// 320 bf16 SiLU: 13.6 us, of which the two passes over HBM need 6.2; copy in
 // about 4.3, fold and exchange 2, output 4 to 5, launch 2 (42 MB, 45 % of the
 // measured copy bandwidth).  1 x 64 x 1280: 3.4 us.
 //
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
     }
   });
   __syncthreads();
-  if (a.k > 1) cluster_arrive_release();  // this CTA has read its peers' partials
+  if (a.k > 1) cluster_arrive_leave();  // this CTA has read its peers' partials
 
   if (nr) {
     float2 nmu[V / 2], sc[V / 2], bf[V / 2];
