@@ -141,9 +141,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
     }
   });
   // dgamma / dbeta row of this cluster's samples: the CTAs share its channel
-  // pairs out among them and sum over the cluster in rank order.
+  // pairs out among them and sum over the cluster in rank order (by the last
+  // warps: the first have the groups).
 #pragma unroll 1
-  for (int j = rank * nthr + tid; j < ncs_me * (V / 2); j += csize * nthr) {
+  for (int j = rank * nthr + nthr - 1 - tid; j < ncs_me * (V / 2); j += csize * nthr) {
     float2 tg = make_float2(0.f, 0.f), tb = tg;
     const float2 *pg = reinterpret_cast<const float2 *>(cg) + j;
     const float2 *pb = reinterpret_cast<const float2 *>(cb) + j;
