@@ -499,40 +499,43 @@ __device__ __forceinline__ void channel_stats(ChannelStats<V> &st, unsigned char
   }
 }
 
-// Sum of per-thread values over each channel of the slab: s1 and s2 of the R
-// row lanes, added up in a fixed order.  Called by all threads; the arrays
-// are complete after the next barrier.
-template <int V>
+// Sum of per-thread values over each channel j of the slab: s1 and s2 of the R
+// row lanes, added up in a fixed order, times fa and fb(j).  Called by all
+// threads; the arrays are complete after the next barrier.
+template <int V, typename Factor>
 __device__ __forceinline__ void channel_sums(float2 (&a)[V / 2], float2 (&b)[V / 2],
                                              unsigned char *buf, float *ca, float *cb, int R, int rl,
-                                             int cc, int ncs, bool on, int nch) {
+                                             int cc, int ncs, bool on, int nch, float fa,
+                                             Factor fb) {
   if (R == 1) {
     if (on) {
 #pragma unroll
       for (int p = 0; p < V / 2; ++p) {
-        *reinterpret_cast<float2 *>(ca + cc * V + 2 * p) = a[p];
-        *reinterpret_cast<float2 *>(cb + cc * V + 2 * p) = b[p];
+        const int j = cc * V + 2 * p;
+        *reinterpret_cast<float2 *>(ca + j) = mul2(a[p], splat2(fa));
+        *reinterpret_cast<float2 *>(cb + j) = mul2(b[p], make_float2(fb(j), fb(j + 1)));
       }
     }
     return;
   }
   fold_sums<V>(a, b, buf, R, rl, cc, ncs, on);
   const int cap = fold_slots(R) * ncs, rows = fold_lanes(R);
-  const float *f = reinterpret_cast<const float *>(buf);
+  const float *at = reinterpret_cast<const float *>(buf);
 #pragma unroll 1
   for (int j = threadIdx.x; j < nch; j += blockDim.x) {
     const unsigned u = static_cast<unsigned>(j);
     const int col = static_cast<int>(u / V), v = static_cast<int>(u % V);
-    const float *fa = f + pair_at<V>(cap, col, v, 0), *fb = f + pair_at<V>(cap, col, v, 1);
-    float sa = fa[0], sb = fb[0];
+    const float *pa = at + pair_at<V>(cap, col, v, 0), *pb = at + pair_at<V>(cap, col, v, 1);
+    const float f = fb(j);
+    float sa = pa[0], sb = pb[0];
 #pragma unroll
     for (int r = 1; r < kFoldLanes; ++r)
       if (r < rows) {
-        sa += fa[r * ncs * 4];
-        sb += fb[r * ncs * 4];
+        sa += pa[r * ncs * 4];
+        sb += pb[r * ncs * 4];
       }
-    ca[j] = sa;
-    cb[j] = sb;
+    ca[j] = sa * fa;
+    cb[j] = sb * f;
   }
 }
 

@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   }
 
   const int ch0 = chunk0 * V;
-  if (on) scale_sums<DT, DROP>(a, b, chunk0 + cc, s1, s2);
-  channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ncs_me * V);
+  channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ncs_me * V, sum_factor<DROP>(a),
+                  [&](int j) { return xhat_factor<DROP>(a, b, ch0 + j); });
   __syncthreads();
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
   if (csize > 1) cluster_sync(); else __syncthreads();
@@ -242,9 +242,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_sums_kernel(const Grou
       if (DROP) gen.template mask<DT>(dv, static_cast<uint64_t>((c0 + i * step) * V));
       sum_rows<DT, ACT>(xv, dv, xv, dv, false, k, s1, s2);
     }
-    if (on) scale_sums<DT, DROP>(a, b, col + cc, s1, s2);
     channel_sums<V>(s1, s2, fold, cb + col * V, cg + col * V, a.R, rl, cc, a.ncs, on,
-                    min(a.ncs, a.nc - col) * V);
+                    min(a.ncs, a.nc - col) * V, sum_factor<DROP>(a),
+                    [&](int j) { return xhat_factor<DROP>(a, b, col * V + j); });
     __syncthreads();  // the fold buffer is free again
   }
   float2 *out = reinterpret_cast<float2 *>(a.gpart) + static_cast<int64_t>(blockIdx.x) * a.G;

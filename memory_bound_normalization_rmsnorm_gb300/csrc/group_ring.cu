@@ -521,8 +521,9 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
           e += 2 * estep;
         }
       });
-      if (on) scale_sums<DT, DROP>(a, b, ring.chunk0 + cc, s1, s2);
-      channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ring.ncs * V);
+      channel_sums<V>(s1, s2, fold, cb, cg, a.R, rl, cc, a.ncs, on, ring.ncs * V,
+                      sum_factor<DROP>(a),
+                      [&](int j) { return xhat_factor<DROP>(a, b, ch0 + j); });
       __syncthreads();
       group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) {
         gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * pstride + role.sp] = v;

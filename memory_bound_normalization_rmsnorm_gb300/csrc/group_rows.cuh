@@ -127,22 +127,16 @@ __device__ __forceinline__ void load_const(const GroupArgs &a, int b, int chunk,
   }
 }
 
-// Sums of dz and dz d as sum_rows leaves them -> sums of dz and dz xhat.
-template <int DT, bool DROP>
-__device__ __forceinline__ void scale_sums(const GroupArgs &a, int b, int chunk,
-                                           float2 (&s1)[chunk_elems(DT) / 2],
-                                           float2 (&s2)[chunk_elems(DT) / 2]) {
-  const float *rs = a.rstd + static_cast<int64_t>(b) * a.G;
-  GroupWalk g(a, chunk * chunk_elems(DT));
-#pragma unroll
-  for (int p = 0; p < chunk_elems(DT) / 2; ++p) {
-    const int g0 = g.next(), g1 = g.next();
-    s2[p] = mul2(s2[p], make_float2(__ldg(rs + g0), __ldg(rs + g1)));
-    if (DROP) {
-      s1[p] = mul2(s1[p], splat2(a.drop.scale));
-      s2[p] = mul2(s2[p], splat2(a.drop.scale));
-    }
-  }
+// What turns a channel's sums of dz and dz d, as sum_rows leaves them, into
+// those of dz and dz xhat: the kept elements' factor of the dropout, and with
+// it rstd of the channel's group (of sample b; c counts within the tensor).
+template <bool DROP>
+__device__ __forceinline__ float sum_factor(const GroupArgs &a) {
+  return DROP ? a.drop.scale : 1.0f;
+}
+template <bool DROP>
+__device__ __forceinline__ float xhat_factor(const GroupArgs &a, int b, int c) {
+  return __ldg(a.rstd + static_cast<int64_t>(b) * a.G + a.by_D(c)) * sum_factor<DROP>(a);
 }
 
 // d = x - mean and dz of the same two channels in two rows, from x in ca and
