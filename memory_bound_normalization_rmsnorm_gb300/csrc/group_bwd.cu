@@ -15,9 +15,10 @@
 // dropout too (22 an element are the formulas' own with SiLU), and a thread about
 // 800 more for its start, constants and folds, which 11 rows share at 16 x 1024 x
 // 640: half of the issue slots are used, each warp waiting for its own results.
-// Resident form: 16 x 1024 x 640 bf16, SiLU and p = 0.1: 34.2 us (63 MB, 27 % of
-// the measured copy bandwidth).  2 x 221 x 88 fp16 GELU: 5.0 us in one launch.  Streamed form: 4 x 4096 x 8192 bf16 in one
-// group, SiLU: 325 us (282 without activation).
+// Resident form: 16 x 1024 x 640 bf16, SiLU and p = 0.1: 33.3 us (63 MB, 28 % of
+// the measured copy bandwidth).  2 x 221 x 88 fp16 GELU: 4.6 us in one launch.
+// Streamed form: 4 x 4096 x 8192 bf16 in one group, SiLU: 310 us (282 without
+// activation).
 #include "common.cuh"
 #include "group_rows.cuh"
 
