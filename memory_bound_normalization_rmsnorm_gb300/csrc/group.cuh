@@ -259,9 +259,10 @@ __device__ __forceinline__ void cp_async_wait_upto(int pending) {
 
 // Arrival at the barrier that keeps a cluster's CTAs from leaving while a peer
 // may still read their shared memory.  It passes on no data, so it is relaxed: a
-// releasing one waits for the thread's global stores (its reads of the peers are
-// done, their values having been used).  2 x 221 x 88 backward 5.3 -> 5.0 us, 3 x
-// 1517 x 168 fp32 forward 5.8 -> 5.55.
+// releasing one waits for the thread's global stores.  The thread's reads of the
+// peers have to be complete, so every value read has to have been used (shuffled
+// or stored): a read whose value nothing waits for may still be on its way.  2 x
+// 221 x 88 backward 5.3 -> 5.0 us, 3 x 1517 x 168 fp32 forward 5.8 -> 5.55.
 __device__ __forceinline__ void cluster_arrive_leave() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }

@@ -143,7 +143,10 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   });
   // dgamma / dbeta row of this cluster's samples: the CTAs share its channel
   // pairs out among them and sum over the cluster in rank order (by the last
-  // warps: the first have the groups).
+  // warps: the first have the groups).  Only sums that are stored are read: the
+  // store waits for the peers' values, so none is still on its way when this CTA
+  // arrives at the barrier that lets the peers leave.
+  const bool want_b = a.dbeta_part != nullptr;
 #pragma unroll 1
   for (int j = rank * nthr + nthr - 1 - tid; j < ncs_me * (V / 2); j += csize * nthr) {
     float2 tg = make_float2(0.f, 0.f), tb = tg;
@@ -158,13 +161,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
       for (int r = 0; r < kMaxGroupCluster; ++r) {
         if (r < csize) {
           tg = add2(tg, ld_cluster_f2(pg, r));
-          tb = add2(tb, ld_cluster_f2(pb, r));
+          if (want_b) tb = add2(tb, ld_cluster_f2(pb, r));
         }
       }
     }
     const int64_t at = static_cast<int64_t>(ub) * a.C + ch0 + 2 * j;
     *reinterpret_cast<float2 *>(a.cpart + at) = tg;
-    if (a.dbeta_part) *reinterpret_cast<float2 *>(a.dbeta_part + at) = tb;
+    if (want_b) *reinterpret_cast<float2 *>(a.dbeta_part + at) = tb;
   }
   __syncthreads();
   if (csize > 1) cluster_arrive_leave();
