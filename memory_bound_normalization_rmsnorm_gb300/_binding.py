@@ -731,8 +731,7 @@ def norm_group_fwd(x, gamma, beta, groups, eps=1e-5, act=ACT_NONE, *, p=0.0, see
     dropout of a channels-last tensor x [B, ..., C] (contiguous bf16, fp16 or
     fp32; a torch channels_last [B, C, H, W] tensor is x.permute(0, 2, 3, 1)).
     gamma, beta: [C] of x's type (beta None: zero).  Returns (y, rstd, mean),
-    rstd and mean fp32 [B, groups] (new outputs of a small call are parts of
-    one allocation)."""
+    rstd and mean fp32 [B, groups]."""
     out = (_native_module or _native()).group_fwd(
         x, gamma, beta, groups, eps, _act(act), p, seed, offset, offset_dev, y, rstd, mean,
         workspace, _handle(stream))

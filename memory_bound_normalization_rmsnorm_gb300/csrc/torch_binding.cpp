@@ -79,61 +79,25 @@ norm_dtype_t dtype_code(const at::Tensor &x) {
   }
 }
 
-// The given output, checked, or a new one.
+// The given output, checked, or a new one.  A new one owns its memory: callers
+// release and grow the storages of activations one by one, and the statistics
+// that a backward pass reads must outlive that.  (One allocation shared by the
+// outputs of a small call saved 0.7 us of host time and broke there.)
+// Its storage is a whole number of the caching allocator's 512-byte blocks, the
+// memory that it takes either way.
 at::Tensor output(PyObject *o, const char *name, at::ScalarType dt, c10::IntArrayRef shape,
                   c10::Device dev) {
-  if (o == Py_None) return at::detail::empty_cuda(shape, dt, dev, std::nullopt);
+  if (o == Py_None) {
+    const int64_t es = static_cast<int64_t>(c10::elementSize(dt));
+    const int64_t bytes = es * c10::multiply_integers(shape);
+    const at::Tensor t =
+        at::detail::empty_cuda({((bytes + 511) & ~int64_t(511)) / es}, dt, dev, std::nullopt);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return t;
+  }
   const at::Tensor &t = tensor(o, name);
   check(t, name, dt, shape, dev);
   return t;
-}
-
-// A contiguous tensor over a part of base's storage.
-at::Tensor part(const at::Tensor &base, int64_t byte_offset, at::ScalarType dt,
-                c10::IntArrayRef shape) {
-  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()),
-                                                          base.key_set(),
-                                                          c10::scalarTypeToTypeMeta(dt));
-  t.unsafeGetTensorImpl()->set_storage_offset(byte_offset /
-                                              static_cast<int64_t>(c10::elementSize(dt)));
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  return t;
-}
-
-int64_t pad256(int64_t bytes) { return (bytes + 255) & ~int64_t(255); }
-
-// A main output and one or two small fp32 outputs of a shape of their own
-// (statistics, parameter gradients): the given ones, checked, or new ones.  An
-// allocation costs 0.9 us of host time, so new small ones share one, each on a
-// 256-byte boundary, and lie behind a new main output of at most kShareBytes:
-// what one of them can keep alive of the others stays bounded by that, and
-// calls on larger tensors take longer on the device than on the host.
-constexpr int64_t kShareBytes = 1 << 20;
-
-void outputs(PyObject *om, const char *nm, at::ScalarType dt, c10::IntArrayRef main_shape,
-             PyObject *oa, const char *na, PyObject *ob, const char *nb, bool two,
-             c10::IntArrayRef shape, c10::Device dev, at::Tensor &m, at::Tensor &a, at::Tensor &b) {
-  const int64_t small = pad256(4 * c10::multiply_integers(shape));
-  const bool fresh = oa == Py_None && ob == Py_None;
-  const int64_t es = static_cast<int64_t>(c10::elementSize(dt));
-  const int64_t main_bytes = es * c10::multiply_integers(main_shape);
-  if (om == Py_None && fresh && main_bytes <= kShareBytes) {
-    const int64_t at = pad256(main_bytes);
-    m = at::detail::empty_cuda({(at + small * (two ? 2 : 1)) / es}, dt, dev, std::nullopt);
-    a = part(m, at, at::kFloat, shape);
-    if (two) b = part(m, at + small, at::kFloat, shape);
-    m.unsafeGetTensorImpl()->set_sizes_contiguous(main_shape);
-    return;
-  }
-  m = output(om, nm, dt, main_shape, dev);
-  if (fresh && two) {
-    a = at::detail::empty_cuda({small / 2}, at::kFloat, dev, std::nullopt);
-    b = part(a, small, at::kFloat, shape);
-    a.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    return;
-  }
-  a = output(oa, na, at::kFloat, shape, dev);
-  if (two) b = output(ob, nb, at::kFloat, shape, dev);
 }
 
 void *ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -325,9 +289,11 @@ PyObject *dropout_add_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rng rng(a + 6, dev);
     const StreamScope on(a[14], dev);
     const at::Tensor h = output(a[10], "h", bf, d.shape, dev);
-    at::Tensor y, rstd, mean;
-    outputs(a[11], "y", bf, d.shape, a[12], "rstd", a[13], "mean",
-            mode == NORM_LAYER || a[13] != Py_None, d.lead, dev, y, rstd, mean);
+    const at::Tensor y = output(a[11], "y", bf, d.shape, dev);
+    const at::Tensor rstd = output(a[12], "rstd", at::kFloat, d.lead, dev);
+    at::Tensor mean;
+    if (mode == NORM_LAYER || a[13] != Py_None)
+      mean = output(a[13], "mean", at::kFloat, d.lead, dev);
     return result(norm_dropout_add_fwd(ptr(x), ptr(r), ptr(gamma), ptr(beta), d.M, d.N, eps,
                                        static_cast<norm_mode_t>(mode), rng.p, rng.seed, rng.offset,
                                        rng.dev_word, ptr(h), ptr(y),
@@ -358,9 +324,11 @@ PyObject *dropout_add_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Rng rng(a + 7, dev);
     const StreamScope on(a[17], dev);
     const at::Tensor dr = output(a[12], "dr", bf, d.shape, dev);
-    at::Tensor dx, dg, db;
-    outputs(a[11], "dx", bf, d.shape, a[13], "dgamma", a[14], "dbeta",
-            (mode == NORM_LAYER && truth(a[15])) || a[14] != Py_None, {d.N}, dev, dx, dg, db);
+    const at::Tensor dx = output(a[11], "dx", bf, d.shape, dev);
+    const at::Tensor dg = output(a[13], "dgamma", f32, {d.N}, dev);
+    at::Tensor db;
+    if ((mode == NORM_LAYER && truth(a[15])) || a[14] != Py_None)
+      db = output(a[14], "dbeta", f32, {d.N}, dev);
     const Workspace ws(a[16], dev, [&](size_t *b) {
       return norm_dropout_add_bwd_workspace_bytes(d.M, d.N, mode, b);
     });
@@ -404,9 +372,9 @@ PyObject *group_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const norm_act_t act = static_cast<norm_act_t>(code_of(a[5]));
     const Rng rng(a + 6, dev);
     const StreamScope on(a[14], dev);
-    at::Tensor y, rstd, mean;
-    outputs(a[10], "y", dt, x.sizes(), a[11], "rstd", a[12], "mean", true, {d.B, groups}, dev, y,
-            rstd, mean);
+    const at::Tensor y = output(a[10], "y", dt, x.sizes(), dev);
+    const at::Tensor rstd = output(a[11], "rstd", at::kFloat, {d.B, groups}, dev);
+    const at::Tensor mean = output(a[12], "mean", at::kFloat, {d.B, groups}, dev);
     const Workspace ws(a[13], dev, [&](size_t *b) {
       return norm_group_fwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
     });
@@ -441,9 +409,10 @@ PyObject *group_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const norm_act_t act = static_cast<norm_act_t>(code_of(a[7]));
     const Rng rng(a + 8, dev);
     const StreamScope on(a[17], dev);
-    at::Tensor dx, dg, db;
-    outputs(a[12], "dx", dt, x.sizes(), a[13], "dgamma", a[14], "dbeta",
-            truth(a[15]) || a[14] != Py_None, {d.C}, dev, dx, dg, db);
+    const at::Tensor dx = output(a[12], "dx", dt, x.sizes(), dev);
+    const at::Tensor dg = output(a[13], "dgamma", f32, {d.C}, dev);
+    at::Tensor db;
+    if (truth(a[15]) || a[14] != Py_None) db = output(a[14], "dbeta", f32, {d.C}, dev);
     const Workspace ws(a[16], dev, [&](size_t *b) {
       return norm_group_bwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
     });
