@@ -79,26 +79,46 @@ norm_dtype_t dtype_code(const at::Tensor &x) {
   }
 }
 
-// The given output, checked, or a new one.  A new one owns its memory: callers
-// release and grow the storages of activations one by one, and the statistics
-// that a backward pass reads must outlive that.  (One allocation shared by the
-// outputs of a small call saved 0.7 us of host time and broke there.)
-// Its storage is a whole number of the caching allocator's 512-byte blocks, the
-// memory that it takes either way.
-at::Tensor output(PyObject *o, const char *name, at::ScalarType dt, c10::IntArrayRef shape,
-                  c10::Device dev) {
-  if (o == Py_None) {
+// Lets other Python threads run in its scope.  A call may wait there, for
+// memory, for a kernel to be loaded, or in a launch for room in a full queue;
+// inside, no Python object is touched.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked &) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// An output: the given tensor, checked, or one that make() allocates (on the
+// current device and stream).  A new one owns its memory: callers release and
+// grow the storages of activations one by one, and the statistics that a
+// backward pass reads must outlive that.  (One allocation shared by the outputs
+// of a small call saved 0.7 us of host time and broke there.)  Its storage is a
+// whole number of the caching allocator's 512-byte blocks, the memory that it
+// takes either way.
+struct Output {
+  at::Tensor t;
+  at::ScalarType dt;
+  c10::DimVector shape;
+  c10::Device dev;
+  bool wanted;
+
+  // `wanted`: None asks for a new tensor (else for no output).
+  Output(PyObject *o, const char *name, at::ScalarType type, c10::IntArrayRef sizes,
+         c10::Device device, bool want = true)
+      : dt(type), shape(sizes.begin(), sizes.end()), dev(device), wanted(want) {
+    if (o == Py_None) return;
+    t = tensor(o, name);
+    check(t, name, dt, sizes, dev);
+  }
+  void make() {
+    if (t.defined() || !wanted) return;
     const int64_t es = static_cast<int64_t>(c10::elementSize(dt));
     const int64_t bytes = es * c10::multiply_integers(shape);
-    const at::Tensor t =
-        at::detail::empty_cuda({((bytes + 511) & ~int64_t(511)) / es}, dt, dev, std::nullopt);
+    t = at::detail::empty_cuda({((bytes + 511) & ~int64_t(511)) / es}, dt, dev, std::nullopt);
     t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    return t;
   }
-  const at::Tensor &t = tensor(o, name);
-  check(t, name, dt, shape, dev);
-  return t;
-}
+};
 
 void *ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
@@ -156,7 +176,19 @@ struct Rng {
   }
 };
 
-// The stream of a call: the current stream of the device (None) or a handle.
+// The stream argument of a call: None (the device's current stream) or a
+// handle.
+struct StreamArg {
+  std::optional<uintptr_t> handle;
+
+  explicit StreamArg(PyObject *o) {
+    if (o == Py_None) return;
+    const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+    if (PyErr_Occurred()) throw PyFail{};
+    handle = static_cast<uintptr_t>(v);
+  }
+};
+
 // The device is current inside the scope, and so is the stream, so outputs
 // and workspaces come from that stream's memory: a workspace that is freed
 // when the call returns is used again by later work of the same stream only.
@@ -165,38 +197,39 @@ struct StreamScope {
   std::optional<c10::cuda::CUDAStreamGuard> stream;
   std::optional<c10::cuda::CUDAGuard> device;
 
-  StreamScope(PyObject *o, c10::Device dev) {
-    if (o == Py_None) {
+  StreamScope(const StreamArg &arg, c10::Device dev) {
+    if (!arg.handle) {
       device.emplace(dev);
       s = reinterpret_cast<norm_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
       return;
     }
-    const unsigned long long v = PyLong_AsUnsignedLongLong(o);
-    if (PyErr_Occurred()) throw PyFail{};
-    s = reinterpret_cast<norm_stream_t>(static_cast<uintptr_t>(v));
+    s = reinterpret_cast<norm_stream_t>(*arg.handle);
     stream.emplace(
         c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s), dev.index()));
   }
 };
 
-// The given workspace, or a new one of the bytes that `query` asks for.
+// The given workspace, checked, or one that make() allocates of the bytes that
+// `query` asks for.
 struct Workspace {
   at::Tensor t;
   size_t bytes = 0;
-  norm_status_t status = NORM_OK;
+  c10::Device dev;
 
+  Workspace(PyObject *o, c10::Device device) : dev(device) {
+    if (o == Py_None) return;
+    t = tensor(o, "workspace");
+    if (t.device() != dev || !t.is_contiguous())
+      fail("workspace must be contiguous and on " + dev.str());
+    bytes = t.nbytes();
+  }
   template <typename Query>
-  Workspace(PyObject *o, c10::Device dev, Query query) {
-    if (o != Py_None) {
-      t = tensor(o, "workspace");
-      if (t.device() != dev || !t.is_contiguous())
-        fail("workspace must be contiguous and on " + dev.str());
-      bytes = t.nbytes();
-      return;
-    }
-    status = query(&bytes);
-    if (status == NORM_OK && bytes)
+  norm_status_t make(Query query) {
+    if (t.defined()) return NORM_OK;
+    const norm_status_t st = query(&bytes);
+    if (st == NORM_OK && bytes)
       t = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, at::kByte, dev, std::nullopt);
+    return st;
   }
 };
 
@@ -251,11 +284,17 @@ PyObject *dropout(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const norm_dtype_t dt = dtype_code(x);
     const c10::Device dev = x.device();
     const Rng rng(a + 1, dev);
-    const StreamScope on(a[6], dev);
-    const at::Tensor y = output(a[5], "y", x.scalar_type(), x.sizes(), dev);
-    return result(norm_dropout(ptr(x), x.numel(), rng.p, rng.seed, rng.offset, rng.dev_word, dt,
-                               ptr(y), on.s),
-                  {y});
+    const StreamArg stream(a[6]);
+    Output y(a[5], "y", x.scalar_type(), x.sizes(), dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      y.make();
+      st = norm_dropout(ptr(x), x.numel(), rng.p, rng.seed, rng.offset, rng.dev_word, dt, ptr(y.t),
+                        on.s);
+    }
+    return result(st, {y.t});
   });
 }
 
@@ -287,19 +326,21 @@ PyObject *dropout_add_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const float eps = static_cast<float>(number(a[4]));
     const int mode = code_of(a[5]);
     const Rng rng(a + 6, dev);
-    const StreamScope on(a[14], dev);
-    const at::Tensor h = output(a[10], "h", bf, d.shape, dev);
-    const at::Tensor y = output(a[11], "y", bf, d.shape, dev);
-    const at::Tensor rstd = output(a[12], "rstd", at::kFloat, d.lead, dev);
-    at::Tensor mean;
-    if (mode == NORM_LAYER || a[13] != Py_None)
-      mean = output(a[13], "mean", at::kFloat, d.lead, dev);
-    return result(norm_dropout_add_fwd(ptr(x), ptr(r), ptr(gamma), ptr(beta), d.M, d.N, eps,
-                                       static_cast<norm_mode_t>(mode), rng.p, rng.seed, rng.offset,
-                                       rng.dev_word, ptr(h), ptr(y),
-                                       static_cast<float *>(ptr(rstd)),
-                                       static_cast<float *>(ptr(mean)), on.s),
-                  {h, y, rstd, mean});
+    const StreamArg stream(a[14]);
+    Output h(a[10], "h", bf, d.shape, dev), y(a[11], "y", bf, d.shape, dev);
+    Output rstd(a[12], "rstd", at::kFloat, d.lead, dev);
+    Output mean(a[13], "mean", at::kFloat, d.lead, dev, mode == NORM_LAYER);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      for (Output *o : {&h, &y, &rstd, &mean}) o->make();
+      st = norm_dropout_add_fwd(ptr(x), ptr(r), ptr(gamma), ptr(beta), d.M, d.N, eps,
+                                static_cast<norm_mode_t>(mode), rng.p, rng.seed, rng.offset,
+                                rng.dev_word, ptr(h.t), ptr(y.t), static_cast<float *>(ptr(rstd.t)),
+                                static_cast<float *>(ptr(mean.t)), on.s);
+    }
+    return result(st, {h.t, y.t, rstd.t, mean.t});
   });
 }
 
@@ -322,25 +363,26 @@ PyObject *dropout_add_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(mean, "mean", f32, d.lead, dev);
     const norm_mode_t mode = static_cast<norm_mode_t>(code_of(a[6]));
     const Rng rng(a + 7, dev);
-    const StreamScope on(a[17], dev);
-    const at::Tensor dr = output(a[12], "dr", bf, d.shape, dev);
-    const at::Tensor dx = output(a[11], "dx", bf, d.shape, dev);
-    const at::Tensor dg = output(a[13], "dgamma", f32, {d.N}, dev);
-    at::Tensor db;
-    if ((mode == NORM_LAYER && truth(a[15])) || a[14] != Py_None)
-      db = output(a[14], "dbeta", f32, {d.N}, dev);
-    const Workspace ws(a[16], dev, [&](size_t *b) {
-      return norm_dropout_add_bwd_workspace_bytes(d.M, d.N, mode, b);
-    });
-    if (ws.status != NORM_OK) return PyLong_FromLong(ws.status);
-    return result(
-        norm_dropout_add_bwd(ptr(dy), ptr(dh), ptr(h), ptr(gamma),
-                             static_cast<const float *>(ptr(rstd)),
-                             static_cast<const float *>(ptr(mean)), d.M, d.N, mode, rng.p, rng.seed,
-                             rng.offset, rng.dev_word, ptr(dx), ptr(dr),
-                             static_cast<float *>(ptr(dg)), static_cast<float *>(ptr(db)),
-                             ptr(ws.t), ws.bytes, on.s),
-        {dx, dr, dg, db});
+    const StreamArg stream(a[17]);
+    Output dx(a[11], "dx", bf, d.shape, dev), dr(a[12], "dr", bf, d.shape, dev);
+    Output dg(a[13], "dgamma", f32, {d.N}, dev);
+    Output db(a[14], "dbeta", f32, {d.N}, dev, mode == NORM_LAYER && truth(a[15]));
+    Workspace ws(a[16], dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      for (Output *o : {&dx, &dr, &dg, &db}) o->make();
+      st = ws.make([&](size_t *b) { return norm_dropout_add_bwd_workspace_bytes(d.M, d.N, mode, b); });
+      if (st == NORM_OK)
+        st = norm_dropout_add_bwd(ptr(dy), ptr(dh), ptr(h), ptr(gamma),
+                                  static_cast<const float *>(ptr(rstd)),
+                                  static_cast<const float *>(ptr(mean)), d.M, d.N, mode, rng.p,
+                                  rng.seed, rng.offset, rng.dev_word, ptr(dx.t), ptr(dr.t),
+                                  static_cast<float *>(ptr(dg.t)), static_cast<float *>(ptr(db.t)),
+                                  ptr(ws.t), ws.bytes, on.s);
+    }
+    return result(st, {dx.t, dr.t, dg.t, db.t});
   });
 }
 
@@ -371,19 +413,26 @@ PyObject *group_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const float eps = static_cast<float>(number(a[4]));
     const norm_act_t act = static_cast<norm_act_t>(code_of(a[5]));
     const Rng rng(a + 6, dev);
-    const StreamScope on(a[14], dev);
-    const at::Tensor y = output(a[10], "y", dt, x.sizes(), dev);
-    const at::Tensor rstd = output(a[11], "rstd", at::kFloat, {d.B, groups}, dev);
-    const at::Tensor mean = output(a[12], "mean", at::kFloat, {d.B, groups}, dev);
-    const Workspace ws(a[13], dev, [&](size_t *b) {
-      return norm_group_fwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
-    });
-    if (ws.status != NORM_OK) return PyLong_FromLong(ws.status);
-    return result(norm_group_fwd(ptr(x), ptr(gamma), ptr(beta), d.B, d.S, d.C, groups, eps, act,
-                                 code, rng.p, rng.seed, rng.offset, rng.dev_word, ptr(y),
-                                 static_cast<float *>(ptr(rstd)), static_cast<float *>(ptr(mean)),
-                                 ptr(ws.t), ws.bytes, on.s),
-                  {y, rstd, mean});
+    const StreamArg stream(a[14]);
+    Output y(a[10], "y", dt, x.sizes(), dev);
+    Output rstd(a[11], "rstd", at::kFloat, {d.B, groups}, dev);
+    Output mean(a[12], "mean", at::kFloat, {d.B, groups}, dev);
+    Workspace ws(a[13], dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      for (Output *o : {&y, &rstd, &mean}) o->make();
+      st = ws.make([&](size_t *b) {
+        return norm_group_fwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
+      });
+      if (st == NORM_OK)
+        st = norm_group_fwd(ptr(x), ptr(gamma), ptr(beta), d.B, d.S, d.C, groups, eps, act, code,
+                            rng.p, rng.seed, rng.offset, rng.dev_word, ptr(y.t),
+                            static_cast<float *>(ptr(rstd.t)), static_cast<float *>(ptr(mean.t)),
+                            ptr(ws.t), ws.bytes, on.s);
+    }
+    return result(st, {y.t, rstd.t, mean.t});
   });
 }
 
@@ -408,22 +457,28 @@ PyObject *group_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     check(mean, "mean", f32, {d.B, groups}, dev);
     const norm_act_t act = static_cast<norm_act_t>(code_of(a[7]));
     const Rng rng(a + 8, dev);
-    const StreamScope on(a[17], dev);
-    const at::Tensor dx = output(a[12], "dx", dt, x.sizes(), dev);
-    const at::Tensor dg = output(a[13], "dgamma", f32, {d.C}, dev);
-    at::Tensor db;
-    if (truth(a[15]) || a[14] != Py_None) db = output(a[14], "dbeta", f32, {d.C}, dev);
-    const Workspace ws(a[16], dev, [&](size_t *b) {
-      return norm_group_bwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
-    });
-    if (ws.status != NORM_OK) return PyLong_FromLong(ws.status);
-    return result(norm_group_bwd(ptr(dy), ptr(x), ptr(gamma), ptr(beta),
-                                 static_cast<const float *>(ptr(rstd)),
-                                 static_cast<const float *>(ptr(mean)), d.B, d.S, d.C, groups, act,
-                                 code, rng.p, rng.seed, rng.offset, rng.dev_word, ptr(dx),
-                                 static_cast<float *>(ptr(dg)), static_cast<float *>(ptr(db)),
-                                 ptr(ws.t), ws.bytes, on.s),
-                  {dx, dg, db});
+    const StreamArg stream(a[17]);
+    Output dx(a[12], "dx", dt, x.sizes(), dev);
+    Output dg(a[13], "dgamma", f32, {d.C}, dev);
+    Output db(a[14], "dbeta", f32, {d.C}, dev, truth(a[15]));
+    Workspace ws(a[16], dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      for (Output *o : {&dx, &dg, &db}) o->make();
+      st = ws.make([&](size_t *b) {
+        return norm_group_bwd_workspace_bytes(d.B, d.S, d.C, groups, code, b);
+      });
+      if (st == NORM_OK)
+        st = norm_group_bwd(ptr(dy), ptr(x), ptr(gamma), ptr(beta),
+                            static_cast<const float *>(ptr(rstd)),
+                            static_cast<const float *>(ptr(mean)), d.B, d.S, d.C, groups, act, code,
+                            rng.p, rng.seed, rng.offset, rng.dev_word, ptr(dx.t),
+                            static_cast<float *>(ptr(dg.t)), static_cast<float *>(ptr(db.t)),
+                            ptr(ws.t), ws.bytes, on.s);
+    }
+    return result(st, {dx.t, dg.t, db.t});
   });
 }
 
