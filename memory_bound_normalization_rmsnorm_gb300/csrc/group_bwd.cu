@@ -155,15 +155,19 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
     if (csize == 1) {
       tg = *pg;
       tb = *pb;
-    } else {
+    } else if (want_b) {
       // (at most kMaxGroupCluster: all loads in flight together)
 #pragma unroll
       for (int r = 0; r < kMaxGroupCluster; ++r) {
         if (r < csize) {
           tg = add2(tg, ld_cluster_f2(pg, r));
-          if (want_b) tb = add2(tb, ld_cluster_f2(pb, r));
+          tb = add2(tb, ld_cluster_f2(pb, r));
         }
       }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kMaxGroupCluster; ++r)
+        if (r < csize) tg = add2(tg, ld_cluster_f2(pg, r));
     }
     const int64_t at = static_cast<int64_t>(ub) * a.C + ch0 + 2 * j;
     *reinterpret_cast<float2 *>(a.cpart + at) = tg;

@@ -18,11 +18,12 @@ def test_every_remote_read_is_conditional_on_its_store():
     same condition."""
     with open(os.path.join(CSRC, "group_bwd.cu")) as f:
         text = f.read()
-    reads = re.findall(r"^.*ld_cluster_f2\(pb, .*$", text, re.M)
+    assert "const bool want_b = a.dbeta_part != nullptr;" in text
+    branch = re.search(r"\} else if \(want_b\) \{\n(.*?)\n    \} else \{\n", text, re.S)
+    assert branch and branch.group(1).count("ld_cluster_f2(pb, ") == 1
+    assert text.count("ld_cluster_f2(pb, ") == 1
     stores = re.findall(r"^.*a\.dbeta_part \+ at\) = tb.*$", text, re.M)
-    assert len(reads) == 1 and len(stores) == 1
-    assert reads[0].strip().startswith("if (want_b) ")
-    assert stores[0].strip().startswith("if (want_b) ")
+    assert len(stores) == 1 and stores[0].strip().startswith("if (want_b) ")
 
 
 @pytest.mark.gpu
