@@ -399,9 +399,14 @@ GroupArgs group_args(const GroupPlan &p, int64_t B, int64_t S, int64_t C, int64_
   a.by_splits.set(p.splits);
   a.by_R.set(p.R);
   a.by_D.set(a.D);
+  a.f_S.set(S);
+  a.f_D.set(a.D);
+  a.f_SD.set(S * a.D);
   const int ranges = p.form == kResident ? p.k : p.splits;
   a.pq = a.S / ranges;
   a.prem = a.S % ranges;
+  a.f_rows.set(std::max(a.pq, 1));
+  a.f_rows1.set(a.pq + 1);
   while ((p.sg << (a.lsh + 1)) <= p.threads && a.lsh < 5) ++a.lsh;
   return a;
 }

@@ -55,6 +55,24 @@ struct FastDiv {
   }
 };
 
+// Quotients by a divisor known to the host, with r = 1 / d rounded to nearest: a
+// product and one correction give the correctly rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Dev. 34, 1990) in three operations; a division in its place, three
+// times in a row between the copies and the output, cost 1 x 64 x 1280 0.13 us of
+// 3.3.  Infinities pass as they are (the correction would make them NaN).
+struct FloatDiv {
+  float d, r;
+  void set(int64_t n) {
+    d = static_cast<float>(n);
+    r = 1.0f / d;
+  }
+  __device__ __forceinline__ float operator()(float a) const {
+    const float q = a * r;
+    return isinf(q) ? q : fmaf(fmaf(-q, d, a), r, q);
+  }
+};
+
 struct GroupArgs {
   const void *x;      // [B, S, C]
   const void *dy;     // [B, S, C] (backward)
@@ -78,6 +96,8 @@ struct GroupArgs {
   int cb;      // resident backward: samples per cluster (1 or B)
   FastDiv by_ncs, by_k, by_csize, by_nslab, by_splits, by_R, by_D;  // csize = k cb
   int pq, prem;  // S rows in k (resident) or `splits` ranges: quotient, remainder
+  FloatDiv f_S, f_D, f_SD;   // by the positions, the channels of a group, its values
+  FloatDiv f_rows, f_rows1;  // by the rows of a range, pq and pq + 1
   int R;       // row lanes per CTA
   int slots;   // resident: rows per thread (at most)
   int splits;  // streamed and ring: row ranges per sample
@@ -271,7 +291,10 @@ __device__ __forceinline__ void cluster_arrive_leave() {
 // Running (count, mean, M2) of a thread's V channels.  Rows enter in blocks
 // of four whose own mean and squared deviations are formed first, then
 // merged, so no sum of squares is ever taken about a distant origin: the
-// statistics keep their accuracy whatever the ratio of mean to deviation.
+// statistics keep their accuracy whatever the ratio of mean to deviation.  The
+// merge weights are approximate quotients (2 steps): they multiply differences
+// of means, which are of the deviation's size, and an error of the mean reaches
+// the variance in the second order only.
 template <int V>
 struct ChannelStats {
   float2 m[V / 2], q[V / 2];
@@ -453,12 +476,12 @@ __device__ __forceinline__ void fold_sums(float2 (&a)[V / 2], float2 (&b)[V / 2]
 }
 
 // Row statistics of a CTA's threads -> (mean, M2) of each channel of the slab
-// over the CTA's `nrow` rows (chm, chq; `nch` channels).  Called by all
-// threads; the arrays are complete after the next barrier.
+// over the CTA's rows (chm, chq; `nch` channels; f_rows divides by the rows).
+// Called by all threads; the arrays are complete after the next barrier.
 template <int V>
 __device__ __forceinline__ void channel_stats(ChannelStats<V> &st, unsigned char *buf, float *chm,
                                               float *chq, int R, int rl, int cc, int ncs, bool on,
-                                              int nch, int nrow) {
+                                              int nch, const FloatDiv &f_rows) {
   if (R == 1) {
     if (on) {
 #pragma unroll
@@ -473,14 +496,14 @@ __device__ __forceinline__ void channel_stats(ChannelStats<V> &st, unsigned char
   const int cap = fold_slots(R) * ncs, rows = fold_lanes(R);
   const float *f = reinterpret_cast<const float *>(buf);
   const float *cnt = f + 2 * V * cap;
-  const float inv = __fdividef(1.0f, static_cast<float>(nrow));
 #pragma unroll 1
   for (int j = threadIdx.x; j < nch; j += blockDim.x) {
     const unsigned u = static_cast<unsigned>(j);
     const int col = static_cast<int>(u / V), v = static_cast<int>(u % V);
     const float *fm = f + pair_at<V>(cap, col, v, 0), *fq = f + pair_at<V>(cap, col, v, 1);
     // the mean first, then the deviations from it: no digit of the variance
-    // is lost
+    // is lost.  The quotient is the correctly rounded one, here and for the
+    // groups: an error of a mean shifts all of its values one way.
     float n[kFoldLanes], m[kFoldLanes], mean = 0.f, q = 0.f;
 #pragma unroll
     for (int r = 0; r < kFoldLanes; ++r) {
@@ -491,7 +514,7 @@ __device__ __forceinline__ void channel_stats(ChannelStats<V> &st, unsigned char
 #pragma unroll
     for (int r = 0; r < kFoldLanes; ++r)
       if (r < rows) mean = fmaf(n[r], m[r], mean);
-    mean *= inv;
+    mean = f_rows(mean);
 #pragma unroll
     for (int r = 0; r < kFoldLanes; ++r)
       if (r < rows) q += fmaf(n[r] * (m[r] - mean), m[r] - mean, fq[r * ncs * 4]);
@@ -540,6 +563,12 @@ __device__ __forceinline__ void channel_sums(float2 (&a)[V / 2], float2 (&b)[V /
   }
 }
 
+// rstd of a group: the quotient and the reciprocal root are correctly rounded (an
+// rstd that is a step off scales a whole group).  An M2 that overflowed gives 0.
+__device__ __forceinline__ float group_rstd(const GroupArgs &a, float m2) {
+  return __frsqrt_rn(a.f_SD(m2) + a.eps);
+}
+
 // Sum over the 2^lsh lanes that share a group.
 __device__ __forceinline__ float lanes_sum(float v, int lsh) {
 #pragma unroll
@@ -567,9 +596,9 @@ __device__ __forceinline__ void each_group(int ng, int lsh, Fn fn) {
 // (mean, M2) of every group from the (mean, M2) of its D channels over n rows
 // each, handed to out(g, mean, M2) by one lane per group.
 template <typename Out>
-__device__ __forceinline__ void groups_of_channels(const float *chm, const float *chq, int ng, int D,
-                                                   int lsh, float n, Out out) {
-  const float inv = __fdividef(1.0f, static_cast<float>(D));
+__device__ __forceinline__ void groups_of_channels(const GroupArgs &a, const float *chm,
+                                                   const float *chq, int ng, float n, Out out) {
+  const int D = a.D, lsh = a.lsh;
   each_group(ng, lsh, [&](int g, int l, bool in) {
     const float *m = chm + g * D, *q = chq + g * D;
     float s = 0.f, t = 0.f;
@@ -577,7 +606,7 @@ __device__ __forceinline__ void groups_of_channels(const float *chm, const float
 #pragma unroll 1
       for (int j = l; j < D; j += 1 << lsh) s += m[j];
     }
-    const float gm = lanes_sum(s, lsh) * inv;
+    const float gm = a.f_D(lanes_sum(s, lsh));
     if (in) {
 #pragma unroll 1
       for (int j = l; j < D; j += 1 << lsh) {
@@ -600,8 +629,13 @@ __device__ __forceinline__ int64_t group_elem(const GroupArgs &a, int b, int64_t
 // S rows cut into ranges that differ by one row at most, the longer ones
 // first.
 struct Parts {
+  const GroupArgs &a;
   int q, rem;
-  __device__ __forceinline__ explicit Parts(const GroupArgs &a) : q(a.pq), rem(a.prem) {}
+  __device__ __forceinline__ explicit Parts(const GroupArgs &args)
+      : a(args), q(a.pq), rem(a.prem) {}
+  __device__ __forceinline__ const FloatDiv &by_rows(int i) const {
+    return i < rem ? a.f_rows1 : a.f_rows;
+  }
   __device__ __forceinline__ int rows(int i) const { return q + (i < rem ? 1 : 0); }
   __device__ __forceinline__ int begin(int i) const { return i * q + (i < rem ? i : rem); }
 };

@@ -125,7 +125,6 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
   __syncthreads();
   group_sums<DT>(a, cb, cg, ch0, ng, [&](int g, float2 v) { gst[g] = v; });
   if (csize > 1) cluster_sync(); else __syncthreads();
-  const float inv = __fdividef(1.0f, static_cast<float>(a.S) * static_cast<float>(a.D));
   // (eight lanes per group, each with the partial of one CTA of the sample)
   each_group(ng, 3, [&](int g, int r, bool in) {
     float2 t = make_float2(0.f, 0.f);
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_bwd_kernel(const Group
     }
     if (in && r == 0) {
       const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
-      gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
+      gfin[g] = make_float2(-rs * a.f_SD(t.x), -rs * rs * a.f_SD(t.y));
     }
   });
   // dgamma / dbeta row of this cluster's samples: the CTAs share its channel
@@ -285,7 +284,6 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
 
   const float2 *part =
       reinterpret_cast<const float2 *>(a.gpart) + static_cast<int64_t>(b) * a.splits * a.G;
-  const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
   for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
     float2 t = splat2(0.f);
     for (int r = lane; r < a.splits; r += 32)
@@ -294,7 +292,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_dx_kernel(const GroupA
     t.y = warp_sum(t.y);
     if (lane == 0) {
       const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g);
-      gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
+      gfin[g] = make_float2(-rs * a.f_SD(t.x), -rs * rs * a.f_SD(t.y));
     }
   }
   __syncthreads();

@@ -89,13 +89,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
   }
 
   // Row lanes -> channels -> groups -> cluster.
-  channel_stats<V>(st, fold, chm, chq, a.R, rl, cc, a.ncs, on, ncs_me * V, nrow);
+  channel_stats<V>(st, fold, chm, chq, a.R, rl, cc, a.ncs, on, ncs_me * V,
+                   parts.by_rows(q));
   __syncthreads();
-  groups_of_channels(chm, chq, ng, a.D, a.lsh, static_cast<float>(nrow),
+  groups_of_channels(a, chm, chq, ng, static_cast<float>(nrow),
                      [&](int g, float m, float m2) { gst[g] = make_float2(m, m2); });
   if (a.k > 1) cluster_sync(); else __syncthreads();
-  const float invS = __fdividef(1.0f, static_cast<float>(a.S));
-  const float invD = __fdividef(1.0f, static_cast<float>(a.D));
+  const float fD = static_cast<float>(a.D);
   // Eight lanes per group, each with the partial of one CTA of the cluster
   // (counts: that CTA's rows, times D): one round trip to the peers' shared
   // memory, and the mean first, then the deviations from it.
@@ -103,12 +103,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_fwd_kernel(const Group
     const bool mine = in && r < a.k;
     const float2 v = !mine ? make_float2(0.f, 0.f) : a.k == 1 ? gst[g] : ld_cluster_f2(gst + g, r);
     const float n = mine ? static_cast<float>(parts.rows(r)) : 0.f;
-    const float m = a.k == 1 ? v.x : lanes_sum(n * v.x, 3) * invS;
+    const float m = a.k == 1 ? v.x : a.f_S(lanes_sum(n * v.x, 3));
     const float e = v.x - m;
     const float m2 =
-        a.k == 1 ? v.y : lanes_sum(fmaf(n * static_cast<float>(a.D) * e, e, v.y), 3);
+        a.k == 1 ? v.y : lanes_sum(fmaf(n * fD * e, e, v.y), 3);
     if (in && r == 0) {
-      const float rs = rsqrtf(m2 * invS * invD + a.eps);
+      const float rs = group_rstd(a, m2);
       gfin[g] = make_float2(m, rs);
       if (q == 0) {
         a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;
@@ -188,11 +188,11 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_stats_kernel(const Gro
       st.add1(f);
     }
     channel_stats<V>(st, fold, chm + col * V, chq + col * V, a.R, rl, cc, a.ncs, on,
-                     min(a.ncs, a.nc - col) * V, nrow);
+                     min(a.ncs, a.nc - col) * V, parts.by_rows(sp));
     __syncthreads();  // the fold buffer is free again
   }
   float2 *out = reinterpret_cast<float2 *>(a.gpart) + static_cast<int64_t>(blockIdx.x) * a.G;
-  groups_of_channels(chm, chq, a.G, a.D, a.lsh, static_cast<float>(nrow),
+  groups_of_channels(a, chm, chq, a.G, static_cast<float>(nrow),
                      [&](int g, float m, float m2) { out[g] = make_float2(m, m2); });
 }
 
@@ -217,14 +217,13 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
 
   const float2 *part =
       reinterpret_cast<const float2 *>(a.gpart) + static_cast<int64_t>(b) * a.splits * a.G;
-  const float count = static_cast<float>(a.S) * static_cast<float>(a.D);
   for (int g = tid >> 5; g < a.G; g += blockDim.x >> 5) {
     float acc = 0.f;
     for (int r = lane; r < a.splits; r += 32) {
       const float n = static_cast<float>(parts.rows(r));
       acc = fmaf(n, __ldcg(part + static_cast<int64_t>(r) * a.G + g).x, acc);
     }
-    const float m = warp_sum(acc) / static_cast<float>(a.S);
+    const float m = a.f_S(warp_sum(acc));
     float m2 = 0.f;
     for (int r = lane; r < a.splits; r += 32) {
       const float n = static_cast<float>(parts.rows(r)) * static_cast<float>(a.D);
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_apply_kernel(const Gro
     }
     m2 = warp_sum(m2);
     if (lane == 0) {
-      const float rs = rsqrtf(m2 / count + a.eps);
+      const float rs = group_rstd(a, m2);
       gfin[g] = make_float2(m, rs);
       if (sp == 0) {
         a.mean[static_cast<int64_t>(b) * a.G + g] = m;

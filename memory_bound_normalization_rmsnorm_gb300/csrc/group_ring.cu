@@ -302,9 +302,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
   float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
   const int pstride = (a.splits + 1) & ~1;  // (rows of partials start on 16 bytes)
   const Parts parts(a);
-  const float invS = 1.0f / static_cast<float>(a.S);
   const float fD = static_cast<float>(a.D);
-  const float invCount = 1.0f / (static_cast<float>(a.S) * fD);
   DropGen gen(a.drop);
   if (DROP) gen.start();
   auto grid = cooperative_groups::this_grid();
@@ -337,11 +335,12 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
           }
         }
       });
-      channel_stats<V>(st, fold, chm, chq, a.R, rl, cc, a.ncs, on, ring.ncs * V, ring.nrow);
+      channel_stats<V>(st, fold, chm, chq, a.R, rl, cc, a.ncs, on, ring.ncs * V,
+                       parts.by_rows(role.sp));
       __syncthreads();
       // partials laid out [b][group][split]: the fold below reads a group's
       // splits side by side
-      groups_of_channels(chm, chq, ng, a.D, a.lsh, static_cast<float>(ring.nrow),
+      groups_of_channels(a, chm, chq, ng, static_cast<float>(ring.nrow),
                          [&](int g, float m, float m2) {
                            gpart[(static_cast<int64_t>(b) * a.G + g0 + g) * pstride + role.sp] =
                                make_float2(m, m2);
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
 #pragma unroll 1
         for (int r = far; r < a.splits; r += 2 << a.lsh)
           mean_of(r, __ldcg(reinterpret_cast<const float4 *>(part + r)));
-        m = lanes_sum(m, a.lsh) * invS;
+        m = a.f_S(lanes_sum(m, a.lsh));
 #pragma unroll
         for (int i = 0; i < kNear; ++i) {
           const int r = 2 * (l + (i << a.lsh));
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_fwd_kernel(const 
           deviation(r, __ldcg(reinterpret_cast<const float4 *>(part + r)));
         m2 = lanes_sum(m2, a.lsh);
         if (in && l == 0) {
-          const float rs = rsqrtf(m2 * invCount + a.eps);
+          const float rs = group_rstd(a, m2);
           gfin[g] = make_float2(m, rs);
           if (role.sp == 0) {
             a.mean[static_cast<int64_t>(b) * a.G + g0 + g] = m;
@@ -473,7 +472,6 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
   float2 *gfin = reinterpret_cast<float2 *>(smem + ring.L.gst_off);
   float2 *gpart = reinterpret_cast<float2 *>(a.gpart);
   const int pstride = (a.splits + 1) & ~1;  // (rows of partials start on 16 bytes)
-  const float inv = 1.0f / (static_cast<float>(a.S) * static_cast<float>(a.D));
   DropGen gen(a.drop);
   if (DROP) gen.start();
   auto grid = cooperative_groups::this_grid();
@@ -567,7 +565,7 @@ __global__ void __launch_bounds__(kGroupThreads, 1) group_ring_bwd_kernel(const 
         t.y = lanes_sum(t.y, a.lsh);
         if (in && l == 0) {
           const float rs = __ldg(a.rstd + static_cast<int64_t>(b) * a.G + g0 + g);
-          gfin[g] = make_float2(-rs * (t.x * inv), -rs * rs * (t.y * inv));
+          gfin[g] = make_float2(-rs * a.f_SD(t.x), -rs * rs * a.f_SD(t.y));
         }
       });
       __syncthreads();
