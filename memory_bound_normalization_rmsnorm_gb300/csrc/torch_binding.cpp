@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -20,6 +20,7 @@
 #include <exception>
 #include <optional>
 #include <string>
+#include <utility>
 
 #include "../../include/gbnorm.h"
 
@@ -89,6 +90,22 @@ struct Unlocked {
   ~Unlocked() { PyEval_RestoreThread(state); }
 };
 
+// A new contiguous tensor over `bytes` of the current device's and stream's
+// memory, at least those of its elements.  (The allocator is asked directly: by
+// way of at::detail::empty_cuda, which sets the device and the sizes once more,
+// a call with three outputs takes 0.5 us longer.)
+at::Tensor device_tensor(int64_t bytes, at::ScalarType dt, c10::IntArrayRef shape) {
+  c10::Allocator *const alloc = c10::cuda::CUDACachingAllocator::get();
+  const size_t n = static_cast<size_t>(bytes);
+  auto storage = c10::make_intrusive<c10::StorageImpl>(
+      c10::StorageImpl::use_byte_size_t(), n, alloc->allocate(n), alloc, /*resizable=*/true);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(std::move(storage)), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+      c10::scalarTypeToTypeMeta(dt));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // An output: the given tensor, checked, or one that make() allocates (on the
 // current device and stream).  A new one owns its memory: callers release and
 // grow the storages of activations one by one, and the statistics that a
@@ -100,23 +117,21 @@ struct Output {
   at::Tensor t;
   at::ScalarType dt;
   c10::DimVector shape;
-  c10::Device dev;
   bool wanted;
 
   // `wanted`: None asks for a new tensor (else for no output).
   Output(PyObject *o, const char *name, at::ScalarType type, c10::IntArrayRef sizes,
-         c10::Device device, bool want = true)
-      : dt(type), shape(sizes.begin(), sizes.end()), dev(device), wanted(want) {
+         c10::Device dev, bool want = true)
+      : dt(type), shape(sizes.begin(), sizes.end()), wanted(want) {
     if (o == Py_None) return;
     t = tensor(o, name);
     check(t, name, dt, sizes, dev);
   }
   void make() {
     if (t.defined() || !wanted) return;
-    const int64_t es = static_cast<int64_t>(c10::elementSize(dt));
-    const int64_t bytes = es * c10::multiply_integers(shape);
-    t = at::detail::empty_cuda({((bytes + 511) & ~int64_t(511)) / es}, dt, dev, std::nullopt);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    const int64_t bytes =
+        static_cast<int64_t>(c10::elementSize(dt)) * c10::multiply_integers(shape);
+    t = device_tensor((bytes + 511) & ~int64_t(511), dt, shape);
   }
 };
 
@@ -214,9 +229,8 @@ struct StreamScope {
 struct Workspace {
   at::Tensor t;
   size_t bytes = 0;
-  c10::Device dev;
 
-  Workspace(PyObject *o, c10::Device device) : dev(device) {
+  Workspace(PyObject *o, c10::Device dev) {
     if (o == Py_None) return;
     t = tensor(o, "workspace");
     if (t.device() != dev || !t.is_contiguous())
@@ -227,8 +241,8 @@ struct Workspace {
   norm_status_t make(Query query) {
     if (t.defined()) return NORM_OK;
     const norm_status_t st = query(&bytes);
-    if (st == NORM_OK && bytes)
-      t = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, at::kByte, dev, std::nullopt);
+    const int64_t n = static_cast<int64_t>(bytes);
+    if (st == NORM_OK && n) t = device_tensor(n, at::kByte, {n});
     return st;
   }
 };

@@ -79,3 +79,20 @@ def test_backward_after_the_activation_was_released():
     got = gb.norm_group_bwd(dy, x, g, b, rstd, mean, 4, "silu")
     for u, v in zip(got, want):
         assert torch.equal(u, v)
+
+
+def test_recorded_streams_hold_an_output():
+    """record_stream keeps each output's memory from being given out again
+    while the other stream may still read it."""
+    s = torch.cuda.Stream()
+    for i in range(len(_outputs(37))):
+        outs = _outputs(37)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        n, at = outs[i].untyped_storage().nbytes(), outs[i].data_ptr()
+        outs[i].record_stream(s)
+        outs[i] = None
+        later = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        assert at not in [t.data_ptr() for t in later]
+        torch.cuda.synchronize()
