@@ -641,7 +641,8 @@ _native_module = None
 
 
 def _native():
-    """The native tensor binding (gbnorm_torch.so; raises if not built)."""
+    """The native tensor binding (gbnorm_torch.so; raises if it is not built,
+    or not for this PyTorch and Python)."""
     global _native_module
     if _native_module is None:
         lib()
@@ -649,6 +650,11 @@ def _native():
         if not os.path.exists(path):
             raise RuntimeError(
                 f"{path} is missing: build it first "
+                "(python -m memory_bound_normalization_rmsnorm_gb300.builder)")
+        if _build.torch_lib_stamp() != _build.torch_stamp():
+            raise RuntimeError(
+                f"{path} was built for {_build.torch_lib_stamp().strip() or 'another PyTorch'}, "
+                f"this is {_build.torch_stamp().strip()}: build it again "
                 "(python -m memory_bound_normalization_rmsnorm_gb300.builder)")
         loader = importlib.machinery.ExtensionFileLoader("gbnorm_torch", path)
         spec = importlib.util.spec_from_file_location("gbnorm_torch", path, loader=loader)

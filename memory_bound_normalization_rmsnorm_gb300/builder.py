@@ -9,7 +9,10 @@ compiled in parallel with nvcc and linked into one shared object with the
 CUDA runtime linked statically, so the library needs no CUDA library path at
 load time.  Beside it a small extension module, gbnorm_torch.so, is compiled
 against PyTorch's headers and linked to the library: the tensor side of the
-dropout and group-normalisation entry points.  `python -m memory_bound_normalization_rmsnorm_gb300.builder -v`
+dropout and group-normalisation entry points.  It belongs to one PyTorch and one
+Python, which gbnorm_torch.stamp names: for others it is built again, and not
+loaded before that.  A PyTorch without CUDA has no tensors for it, so there the
+library alone is built.  `python -m memory_bound_normalization_rmsnorm_gb300.builder -v`
 also prints ptxas register/spill/shared-memory figures.
 """
 from __future__ import annotations
@@ -29,6 +32,7 @@ OUT_DIR = os.path.join(PKG, "lib")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgbnorm.so")
 TORCH_LIB = os.path.join(OUT_DIR, "gbnorm_torch.so")
+TORCH_STAMP = os.path.join(OUT_DIR, "gbnorm_torch.stamp")
 SOURCES = ["fwd.cu", "fwd_fp8.cu", "fwd_gsm.cu", "bwd.cu", "long.cu", "long_resid.cu",
            "long_fp8.cu", "split.cu", "stream.cu", "api.cu", "host.cu", "gemm.cu", "dropout.cu",
            "drop_add.cu", "group_fwd.cu", "group_bwd.cu", "group_ring.cu",
@@ -50,11 +54,43 @@ def _deps():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(TORCH_LIB):
+def _fresh(path):
+    if not os.path.exists(path):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def torch_stamp() -> str:
+    """The PyTorch and Python that an extension module built now is for."""
+    import torch
+
+    return (f"torch {torch.__version__} cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"python {sysconfig.get_config_var('SOABI')}\n")
+
+
+def torch_lib_stamp() -> str:
+    """The PyTorch and Python that the present extension module is for."""
+    if not os.path.exists(TORCH_STAMP):
+        return ""
+    with open(TORCH_STAMP) as f:
+        return f.read()
+
+
+def _torch_has_cuda():
+    import torch
+
+    return torch.version.cuda is not None
+
+
+def _binding_up_to_date():
+    if not _torch_has_cuda():
+        return True
+    return _fresh(TORCH_LIB) and torch_lib_stamp() == torch_stamp()
+
+
+def up_to_date() -> bool:
+    return _fresh(LIB) and _binding_up_to_date()
 
 
 def _torch_compile():
@@ -85,15 +121,30 @@ def _torch_link(obj):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    # (no stamp while the module changes: a stale one must not vouch for it)
+    if os.path.exists(TORCH_STAMP):
+        os.remove(TORCH_STAMP)
     os.replace(tmp, TORCH_LIB)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(torch_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    nvcc = _nvcc()
+    library = force or not _fresh(LIB)
+    binding = _torch_has_cuda() and (library or not _binding_up_to_date())
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(BUILD_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        obj = ex.submit(_torch_compile) if binding else None
+        if library:
+            _build_library(verbose)
+        if obj:
+            _torch_link(obj.result())
+    return LIB
+
+
+def _build_library(verbose):
+    nvcc = _nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                     "-I", INCLUDE, "-I", CSRC]
     if verbose:
@@ -107,8 +158,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(_torch_compile)
+    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
     if verbose:
         for _, log in results:
@@ -119,8 +169,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _torch_link(binding.result())
-    return LIB
 
 
 if __name__ == "__main__":
