@@ -28,11 +28,14 @@ const void *bwd_ptr() {
   return reinterpret_cast<const void *>(&norm_bwd_kernel<MODE, K, false, EXACT, true, true>);
 }
 template <int MODE, int K, bool CLUSTER, bool EXACT>
-const void *long_ptr(bool bwd) {
-  return bwd ? reinterpret_cast<const void *>(
-                   &norm_bwd_long_kernel<MODE, K, CLUSTER, EXACT, true, true>)
-             : reinterpret_cast<const void *>(
-                   &norm_fwd_long_kernel<MODE, K, CLUSTER, EXACT, true, kOutBf16, true>);
+const void *long_fwd_ptr() {
+  return reinterpret_cast<const void *>(
+      &norm_fwd_long_kernel<MODE, K, CLUSTER, EXACT, true, kOutBf16, true>);
+}
+template <int MODE, int K, bool CLUSTER, bool EXACT>
+const void *long_bwd_ptr() {
+  return reinterpret_cast<const void *>(
+      &norm_bwd_long_kernel<MODE, K, CLUSTER, EXACT, true, true>);
 }
 
 // Chunks per thread as the planner gives them: 1 to 6 and 8 in the forward,
@@ -51,12 +54,14 @@ const void *pick_short(int K, bool bwd) {
   }
 }
 
-// Long rows: 8 chunks per thread in the forward, 4 in the backward.
+// Long rows: 8 chunks per thread in the forward (4 by the shape override), 4 in
+// the backward.
 template <int MODE, bool CLUSTER, bool EXACT>
 const void *pick_long(int K, bool bwd) {
   switch (K) {
-    case 4: return long_ptr<MODE, 4, CLUSTER, EXACT>(bwd);
-    case 8: return bwd ? nullptr : long_ptr<MODE, 8, CLUSTER, EXACT>(false);
+    case 4: return bwd ? long_bwd_ptr<MODE, 4, CLUSTER, EXACT>()
+                       : long_fwd_ptr<MODE, 4, CLUSTER, EXACT>();
+    case 8: return bwd ? nullptr : long_fwd_ptr<MODE, 8, CLUSTER, EXACT>();
     default: return nullptr;
   }
 }
