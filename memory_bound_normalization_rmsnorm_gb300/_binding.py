@@ -733,8 +733,8 @@ def norm_group_bwd_workspace_bytes(B, S, C, groups, dtype=BF16) -> int:
 
 def norm_group_fwd(x, gamma, beta, groups, eps=1e-5, act=ACT_NONE, *, p=0.0, seed=0, offset=0,
                    offset_dev=None, y=None, rstd=None, mean=None, workspace=None, stream=None):
-    """Group normalisation, activation ("none", "silu", "gelu" or ACT_*) and
-    dropout of a channels-last tensor x [B, ..., C] (contiguous bf16, fp16 or
+    """Group normalisation, activation ("none", "silu", "gelu" or ACT_*; "gelu"
+    is the tanh form, torch's approximate="tanh") and dropout of a channels-last tensor x [B, ..., C] (contiguous bf16, fp16 or
     fp32; a torch channels_last [B, C, H, W] tensor is x.permute(0, 2, 3, 1)).
     gamma, beta: [C] of x's type (beta None: zero).  Returns (y, rstd, mean),
     rstd and mean fp32 [B, groups]."""

@@ -69,8 +69,9 @@ GroupOverride read_group_override() {
 int round32(int v) { return (v + 31) & ~31; }
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// CTAs of `threads` threads and `smem` bytes that one SM holds (the kernels
-// use at most 128 registers per thread).
+// CTAs of `threads` threads and `smem` bytes that one SM holds, at 128 registers
+// per thread, the most that these kernels use (some need 64 to 104: for those
+// this is too few, and the estimate was fitted with it).
 int ctas_per_sm(int threads, int64_t smem, int smem_optin) {
   const int64_t by_smem = (static_cast<int64_t>(smem_optin) + 1024) / (smem + 1024);
   const int64_t by_regs = 65536 / (128 * threads);
@@ -86,9 +87,13 @@ int ctas_per_sm(int threads, int64_t smem, int smem_optin) {
 // and wave.  Large clusters leave part of the SMs unused, less so the more CTAs
 // an SM takes.  The constants were fitted to 8400 measured plans of 156 shapes
 // (1 to 5000 samples, 1 to 65536 positions, 32 to 2560 channels, both
-// directions, 16 and 32 bits): the plan of least estimate is 1.5 % slower than
-// the fastest measured one in the geometric mean, 16 % at worst (a fit that knew
-// no unevenness: 5.5 %, 61 % at worst; one wave of widest CTAs: 8 %).
+// directions, 16 and 32 bits).  For the kernels and candidates of that time, and
+// on the shapes of the fit, the plan of least estimate was 1.5 % slower than the
+// fastest measured one in the geometric mean, 16 % at worst (a fit that knew no
+// unevenness: 5.5 %, 61 % at worst; one wave of widest CTAs: 8 %).  The folds, the
+// cluster exchange and the number of row lanes changed afterwards without a new
+// fit, and no shape was held back from this one, so how far the choice is off on
+// the present kernels and on other shapes is not known.
 double resident_cost(const GroupPlan &p, double elems, double bytes, bool bwd, bool reduce,
                      int nc, int S, int sms, int smem_optin) {
   const int occ = ctas_per_sm(p.threads, p.smem, smem_optin);
