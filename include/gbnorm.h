@@ -376,6 +376,86 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
                               int smem_optin_bytes, norm_group_plan_t *out);
 
 /*
+ * Normalisation and rotation of query and key heads.  Attention blocks with a
+ * norm per head take, for each token t and head h, the row v of D values:
+ *   n = norm(v) over the D values (RMS, or LAYER with beta), the definitions at
+ *       the top of this file; or n = v where gamma_q is NULL
+ *   for each of the rd / 2 pairs p:  angle = pos[axis(p)][t] * inv_freq[p],
+ *       (n1, n2) -> (n1 cos - n2 sin, n2 cos + n1 sin)
+ *       with (n1, n2) the elements (p, p + rd / 2), or (2p, 2p + 1) where
+ *       `interleaved`; elements rd .. D - 1 are not turned
+ * rounded once.  Rotary positions of one axis are axes = 1; images and video
+ * have one axis for each of (time,) height and width, and every pair belongs to
+ * one of them.  The angle is reduced exactly (positions are integers: the
+ * product is taken in 64-bit fractions of a turn), so far positions are as
+ * exact as near ones.
+ * Backward, from the gradients dyq, dyk and the forward's inputs (the
+ * statistics are taken again):  dn = dy turned back, g = dn gamma,
+ *   xhat = (v - mean) rstd,  dv = rstd (g - mean(g) - xhat mean(g xhat))
+ *   (mean(g) for LAYER only),  dgamma = sum of dn xhat and dbeta = sum of dn
+ *   over all tokens and heads.
+ * Results are bitwise reproducible for a given shape, type and device.
+ *
+ * Arguments:
+ *   q, k, yq, yk, dyq, dyk, dq, dk   head tensors: element (t, h, d) at
+ *              data[t * token_stride + h * head_stride + d] (strides in
+ *              elements, >= 0), of `dtype`: views of a projection's rows, for
+ *              example.  Rows of an output must not overlap.  An output may be
+ *              its input (same data and strides), else it must not alias one.
+ *   T, Hq, Hk, D, rd   tokens, query and key heads, head size, turned elements;
+ *              Hk = 0: no keys (k, yk, ... are not read, gamma_k and beta_k must
+ *              be NULL)
+ *   pos        device int32 or int64 (pos_bits 32 or 64): the position of token
+ *              t on axis a at pos[a * pos_stride + t]; any integer
+ *   inv_freq   device fp64 [rd / 2]: radians per position, finite
+ *   pair_axis  HOST uint8 [rd / 2], read before the call returns: the axis of
+ *              each pair, below `axes`; NULL: all on axis 0 (axes = 1)
+ *   gamma_q, gamma_k, beta_q, beta_k   [D] of `dtype`.  gamma_q NULL: no
+ *              normalisation (and no gamma_k); beta: LAYER only, may be NULL
+ *   dgamma_q, ...  fp32 [D] outputs; dbeta may be NULL
+ *   workspace  norm_rope_bwd_workspace_bytes for this shape on the CURRENT
+ *              device, 16-byte aligned; may be NULL without normalisation.  Two
+ *              calls that overlap in time must not share it.
+ * Requirements: 1 <= T <= 2^31, 1 <= Hq <= 65536, 0 <= Hk <= 65536, 2 <= D <=
+ * 256, rd even, 2 <= rd <= D, strides below 2^40 (else NORM_ERR_SHAPE); axes 1
+ * to 4 (NORM_ERR_ARG); pointers aligned to their elements (NORM_ERR_ALIGN):
+ * any stride and address works, 16-byte multiples are fastest.
+ * One kernel; with normalisation the backward adds a fixed-order sum of the
+ * CTAs' dgamma and dbeta.
+ */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+} norm_heads_t;
+
+norm_status_t norm_rope_fwd(const norm_heads_t *q, const norm_heads_t *k, int64_t T,
+                            int64_t Hq, int64_t Hk, int64_t D, int64_t rd,
+                            const void *pos, int pos_bits, int64_t pos_stride,
+                            const double *inv_freq, const uint8_t *pair_axis,
+                            int axes, int interleaved, const void *gamma_q,
+                            const void *gamma_k, const void *beta_q,
+                            const void *beta_k, float eps, norm_mode_t mode,
+                            norm_dtype_t dtype, const norm_heads_t *yq,
+                            const norm_heads_t *yk, norm_stream_t stream);
+
+norm_status_t norm_rope_bwd_workspace_bytes(int64_t T, int64_t Hq, int64_t Hk,
+                                            int64_t D, int normed,
+                                            norm_mode_t mode, size_t *bytes);
+
+norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk,
+                            const norm_heads_t *q, const norm_heads_t *k, int64_t T,
+                            int64_t Hq, int64_t Hk, int64_t D, int64_t rd,
+                            const void *pos, int pos_bits, int64_t pos_stride,
+                            const double *inv_freq, const uint8_t *pair_axis,
+                            int axes, int interleaved, const void *gamma_q,
+                            const void *gamma_k, float eps, norm_mode_t mode,
+                            norm_dtype_t dtype, const norm_heads_t *dq,
+                            const norm_heads_t *dk, float *dgamma_q,
+                            float *dgamma_k, float *dbeta_q, float *dbeta_k,
+                            void *workspace, size_t workspace_bytes,
+                            norm_stream_t stream);
+
+/*
  * FP8 output.  The page "Otimizacao de Performance de GPU" (introl.com,
  * December 2025 update) reports FP8 training as production ready on
  * Blackwell; the next consumer of a norm's output is usually a GEMM, which

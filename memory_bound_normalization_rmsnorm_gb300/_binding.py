@@ -75,6 +75,12 @@ class GroupPlan(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+class Heads(ctypes.Structure):
+    """Mirror of norm_heads_t."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 class NormError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -165,6 +171,16 @@ def lib():
                       L.norm_dropout_add_bwd_workspace_bytes, L.norm_dropout_add_bwd,
                       L.norm_group_fwd_workspace_bytes, L.norm_group_bwd_workspace_bytes,
                       L.norm_group_fwd, L.norm_group_bwd, L.norm_group_plan):
+                f.restype = ci
+            heads = ctypes.POINTER(Heads)
+            rot = [_i64, _i64, _i64, _i64, _i64, _vp, ci, _i64, _vp, ctypes.c_char_p, ci, ci]
+            L.norm_rope_fwd.argtypes = [heads, heads, *rot, _vp, _vp, _vp, _vp, f32, ci, ci, heads,
+                                        heads, _vp]
+            L.norm_rope_bwd_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, ci, ci,
+                                                        ctypes.POINTER(sz)]
+            L.norm_rope_bwd.argtypes = [heads, heads, heads, heads, *rot, _vp, _vp, f32, ci, ci,
+                                        heads, heads, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+            for f in (L.norm_rope_fwd, L.norm_rope_bwd_workspace_bytes, L.norm_rope_bwd):
                 f.restype = ci
             L.norm_plan.argtypes = [_i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                     ctypes.c_int, ctypes.POINTER(Plan)]
@@ -769,3 +785,51 @@ def norm_group_plan(B, S, C, groups, dtype=BF16, backward=False, sm_count=0, sme
     if st != 0:
         raise NormError(st, "norm_group_plan")
     return out.as_dict()
+
+
+# ------------------------------------------- normalisation and rotation of heads
+def norm_rope_fwd(q, k, pos, inv_freq, gamma_q=None, gamma_k=None, beta_q=None, beta_k=None,
+                  eps=1e-6, mode=RMS, *, sections=None, interleaved=False, yq=None, yk=None,
+                  stream=None):
+    """Norm per head (where gamma_q is given; mode RMS or LAYER) and rotary
+    positions of query and key heads (norm_rope_fwd in gbnorm.h).
+
+    q [..., Hq, D] and k [..., Hk, D] (or None): bf16, fp16 or fp32, contiguous in
+    the last dimension, with evenly strided tokens (views of a projection's rows
+    are fine).  inv_freq: float64 CUDA tensor, the radians per position of each
+    pair; its 2 * len(inv_freq) first elements of a head turn.  pos: int32 or
+    int64, of the leading shape, or [axes, ...] with `sections`, the pairs of each
+    axis in order (e.g. (16, 24, 24) for time, height, width).  interleaved: pairs
+    of neighbours instead of (p, p + half).  yq=q, yk=k work in place.  Returns
+    (yq, yk)."""
+    out = (_native_module or _native()).rope_fwd(
+        q, k, pos, inv_freq, gamma_q, gamma_k, beta_q, beta_k, eps, mode, sections, interleaved,
+        yq, yk, _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_rope_fwd")
+    return out
+
+
+def norm_rope_bwd_workspace_bytes(T, Hq, Hk, D, normed=True, mode=RMS) -> int:
+    out = ctypes.c_size_t(0)
+    st = lib().norm_rope_bwd_workspace_bytes(int(T), int(Hq), int(Hk), int(D), int(bool(normed)),
+                                             int(mode), ctypes.byref(out))
+    if st != 0:
+        raise NormError(st, "norm_rope_bwd_workspace_bytes")
+    return int(out.value)
+
+
+def norm_rope_bwd(dyq, dyk, q, k, pos, inv_freq, gamma_q=None, gamma_k=None, eps=1e-6, mode=RMS,
+                  *, sections=None, interleaved=False, dq=None, dk=None, dgamma_q=None,
+                  dgamma_k=None, dbeta_q=None, dbeta_k=None, want_dbeta=True, workspace=None,
+                  stream=None):
+    """Backward of norm_rope_fwd from its inputs (q and k may be None without
+    gamma_q).  Returns (dq, dk, dgamma_q, dgamma_k, dbeta_q, dbeta_k): dgamma and
+    dbeta fp32 [D], None where there is no norm (or, dbeta, RMSNorm or want_dbeta
+    False)."""
+    out = (_native_module or _native()).rope_bwd(
+        dyq, dyk, q, k, pos, inv_freq, gamma_q, gamma_k, eps, mode, sections, interleaved, dq, dk,
+        dgamma_q, dgamma_k, dbeta_q, dbeta_k, want_dbeta, workspace, _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_rope_bwd")
+    return out

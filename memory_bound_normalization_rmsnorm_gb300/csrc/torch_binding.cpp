@@ -1,5 +1,5 @@
-// torch_binding.cpp -- the tensor side of the dropout and group-normalisation
-// entry points: argument checks, output and workspace allocation, the
+// torch_binding.cpp -- the tensor side of the dropout, group-normalisation and
+// head-rotation entry points: argument checks, output and workspace allocation, the
 // current stream, and the C ABI call, in one native call.
 //
 // These operators run in 2 to 10 us on small tensors, less than a binding
@@ -496,6 +496,261 @@ PyObject *group_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A tensor of heads [..., H, D] whose leading dimensions are evenly strided
+// tokens, as the library's view of it.
+struct Heads {
+  norm_heads_t v = {nullptr, 0, 0};
+  int64_t T = 0, H = 0, D = 0;
+
+  Heads() = default;
+  Heads(const at::Tensor &t, const char *name) {
+    if (t.dim() < 3) fail(std::string(name) + " must be [..., heads, head size]");
+    const int64_t n = t.dim();
+    D = t.size(n - 1);
+    H = t.size(n - 2);
+    if (D > 1 && t.stride(n - 1) != 1)
+      fail(std::string(name) + " must be contiguous in its last dimension");
+    T = 1;
+    bool any = false;
+    for (int64_t i = n - 3; i >= 0; --i) {
+      if (t.size(i) == 1) continue;
+      if (!any)
+        v.token_stride = t.stride(i);
+      else if (t.stride(i) != v.token_stride * T)
+        fail(std::string(name) + " must have evenly strided tokens in its leading dimensions");
+      any = true;
+      T *= t.size(i);
+    }
+    v.head_stride = H > 1 ? t.stride(n - 2) : 0;
+    v.data = t.numel() ? t.data_ptr() : nullptr;
+  }
+};
+
+void check_like(const at::Tensor &t, const char *name, at::ScalarType dt, c10::IntArrayRef shape,
+                c10::Device dev) {
+  if (!t.is_cuda()) fail(std::string(name) + " must be a CUDA tensor");
+  if (t.device() != dev)
+    fail(std::string(name) + " is on " + t.device().str() + ", expected " + dev.str());
+  if (t.scalar_type() != dt)
+    fail(std::string(name) + " must be " + c10::toString(dt) + ", got " +
+         c10::toString(t.scalar_type()));
+  if (t.sizes() != shape)
+    fail(std::string(name) + " has shape " + show(t.sizes()) + ", expected " + show(shape));
+}
+
+// An output of heads: the given tensor (any strides that Heads takes) or a new
+// contiguous one.
+struct HeadsOut {
+  at::Tensor t;
+  at::ScalarType dt;
+  c10::DimVector shape;
+  const char *name;
+
+  HeadsOut(PyObject *o, const char *what, const at::Tensor &like, c10::Device dev)
+      : dt(like.scalar_type()), shape(like.sizes().begin(), like.sizes().end()), name(what) {
+    if (o == Py_None) return;
+    t = tensor(o, name);
+    check_like(t, name, dt, shape, dev);
+    Heads checked(t, name);
+  }
+  Heads make() {
+    if (!t.defined()) {
+      const int64_t bytes =
+          static_cast<int64_t>(c10::elementSize(dt)) * c10::multiply_integers(shape);
+      t = device_tensor((bytes + 511) & ~int64_t(511), dt, shape);
+    }
+    return Heads(t, name);
+  }
+};
+
+// pos, inv_freq and the sections of a call.
+struct Rotation {
+  const void *pos;
+  const double *inv_freq;
+  int pos_bits, axes = 1;
+  int64_t pos_stride = 0, rd;
+  uint8_t axis[128] = {};
+
+  Rotation(PyObject *p, PyObject *f, PyObject *sections, const at::Tensor &q, c10::Device dev) {
+    const at::Tensor &freq = tensor(f, "inv_freq"), &ps = tensor(p, "pos");
+    if (freq.dim() != 1 || freq.numel() > 128) fail("inv_freq must be [pairs], 128 at most");
+    check(freq, "inv_freq", at::kDouble, freq.sizes(), dev);
+    rd = 2 * freq.numel();
+    inv_freq = static_cast<const double *>(freq.data_ptr());
+    if (sections != Py_None) {
+      PyObject *seq = PySequence_Fast(sections, "sections must be a sequence of pair counts");
+      if (!seq) throw PyFail{};
+      const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
+      int64_t at = 0;
+      bool good = n >= 1 && n <= 4;
+      for (Py_ssize_t i = 0; good && i < n; ++i) {
+        const long long c = PyLong_AsLongLong(PySequence_Fast_GET_ITEM(seq, i));
+        if (PyErr_Occurred()) {
+          Py_DECREF(seq);
+          throw PyFail{};
+        }
+        good = c >= 0 && c <= rd / 2 - at;
+        for (long long j = 0; good && j < c; ++j) axis[at++] = static_cast<uint8_t>(i);
+      }
+      Py_DECREF(seq);
+      if (!good || at != rd / 2)
+        fail("sections must be 1 to 4 pair counts that add up to the length of inv_freq");
+      axes = static_cast<int>(n);
+    }
+    const c10::IntArrayRef lead = q.sizes().slice(0, q.dim() - 2);
+    if (!ps.is_cuda() || ps.device() != dev) fail("pos must be on " + dev.str());
+    if (ps.scalar_type() != at::kInt && ps.scalar_type() != at::kLong)
+      fail("pos must be int32 or int64");
+    const bool rows = axes > 1 || ps.dim() == q.dim() - 1;
+    c10::DimVector want;
+    if (rows) want.push_back(axes);
+    want.insert(want.end(), lead.begin(), lead.end());
+    if (ps.sizes() != c10::IntArrayRef(want))
+      fail("pos has shape " + show(ps.sizes()) + ", expected " + show(want));
+    int64_t step = 1;
+    for (int64_t i = ps.dim() - 1; i >= (rows ? 1 : 0); --i) {
+      if (ps.size(i) != 1 && ps.stride(i) != step)
+        fail("pos must be contiguous in its token dimensions");
+      step *= ps.size(i);
+    }
+    if (axes > 1) pos_stride = ps.stride(0);
+    pos = ps.numel() ? ps.data_ptr() : nullptr;
+    pos_bits = ps.scalar_type() == at::kInt ? 32 : 64;
+  }
+};
+
+// The head tensor `o`, or an undefined one for None.
+const at::Tensor &heads_arg(PyObject *o, const char *name, bool optional, at::ScalarType dt,
+                            c10::Device dev) {
+  const at::Tensor &t = tensor(o, name, optional);
+  if (!t.defined()) return t;
+  if (!t.is_cuda()) fail(std::string(name) + " must be a CUDA tensor");
+  if (t.device() != dev)
+    fail(std::string(name) + " is on " + t.device().str() + ", expected " + dev.str());
+  if (t.scalar_type() != dt)
+    fail(std::string(name) + " must be " + c10::toString(dt) + ", got " +
+         c10::toString(t.scalar_type()));
+  return t;
+}
+
+// Keys have the tokens and the head size of the queries.
+void check_keys(const at::Tensor &q, const at::Tensor &k, const char *name) {
+  if (k.dim() != q.dim() || k.size(-1) != q.size(-1) ||
+      k.sizes().slice(0, k.dim() - 2) != q.sizes().slice(0, q.dim() - 2))
+    fail(std::string(name) + " has shape " + show(k.sizes()) +
+         ", expected that of the queries but for the heads, " + show(q.sizes()));
+}
+
+// (q, k, pos, inv_freq, gamma_q, gamma_k, beta_q, beta_k, eps, mode, sections,
+// interleaved, yq, yk, stream) -> (yq, yk)
+PyObject *rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<15>(n, [&]() -> PyObject * {
+    const at::Tensor &q = tensor(a[0], "q");
+    if (!q.is_cuda()) fail("q must be a CUDA tensor");
+    const norm_dtype_t code = dtype_code(q);
+    const c10::Device dev = q.device();
+    const at::ScalarType dt = q.scalar_type();
+    const at::Tensor &k = heads_arg(a[1], "k", true, dt, dev);
+    const Heads hq(q, "q");
+    Heads hk;
+    if (k.defined()) {
+      hk = Heads(k, "k");
+      check_keys(q, k, "k");
+    }
+    const Rotation rot(a[2], a[3], a[10], q, dev);
+    const at::Tensor *par[4];
+    static const char *const names[4] = {"gamma_q", "gamma_k", "beta_q", "beta_k"};
+    for (int i = 0; i < 4; ++i) {
+      par[i] = &tensor(a[4 + i], names[i], true);
+      check(*par[i], names[i], dt, {hq.D}, dev);
+    }
+    const float eps = static_cast<float>(number(a[8]));
+    const norm_mode_t mode = static_cast<norm_mode_t>(code_of(a[9]));
+    const bool inter = truth(a[11]);
+    const StreamArg stream(a[14]);
+    HeadsOut yq(a[12], "yq", q, dev), yk(k.defined() ? a[13] : Py_None, "yk", k.defined() ? k : q, dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      const Heads oq = yq.make();
+      const Heads ok = k.defined() ? yk.make() : Heads();
+      st = norm_rope_fwd(&hq.v, &hk.v, hq.T, hq.H, hk.H, hq.D, rot.rd, rot.pos, rot.pos_bits,
+                         rot.pos_stride, rot.inv_freq, rot.axis, rot.axes, inter, ptr(*par[0]),
+                         ptr(*par[1]), ptr(*par[2]), ptr(*par[3]), eps, mode, code, &oq.v, &ok.v,
+                         on.s);
+    }
+    return result(st, {yq.t, yk.t});
+  });
+}
+
+// (dyq, dyk, q, k, pos, inv_freq, gamma_q, gamma_k, eps, mode, sections,
+// interleaved, dq, dk, dgamma_q, dgamma_k, dbeta_q, dbeta_k, want_dbeta,
+// workspace, stream) -> (dq, dk, dgamma_q, dgamma_k, dbeta_q, dbeta_k)
+PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<21>(n, [&]() -> PyObject * {
+    const at::Tensor &dyq = tensor(a[0], "dyq");
+    if (!dyq.is_cuda()) fail("dyq must be a CUDA tensor");
+    const norm_dtype_t code = dtype_code(dyq);
+    const c10::Device dev = dyq.device();
+    const at::ScalarType dt = dyq.scalar_type(), f32 = at::kFloat;
+    const at::Tensor &dyk = heads_arg(a[1], "dyk", true, dt, dev);
+    const bool keys = dyk.defined();
+    const at::Tensor &gq = tensor(a[6], "gamma_q", true), &gk = tensor(a[7], "gamma_k", true);
+    const bool norm = gq.defined();
+    const at::Tensor &q = heads_arg(a[2], "q", !norm, dt, dev),
+                     &k = heads_arg(a[3], "k", !norm || !keys, dt, dev);
+    const Heads hdq(dyq, "dyq");
+    Heads hdk, hq, hk;
+    if (keys) {
+      hdk = Heads(dyk, "dyk");
+      check_keys(dyq, dyk, "dyk");
+    }
+    if (q.defined()) {
+      check_like(q, "q", dt, dyq.sizes(), dev);
+      hq = Heads(q, "q");
+    }
+    if (k.defined()) {
+      if (!keys) fail("k is given without dyk");
+      check_like(k, "k", dt, dyk.sizes(), dev);
+      hk = Heads(k, "k");
+    }
+    const Rotation rot(a[4], a[5], a[10], dyq, dev);
+    check(gq, "gamma_q", dt, {hdq.D}, dev);
+    check(gk, "gamma_k", dt, {hdq.D}, dev);
+    const float eps = static_cast<float>(number(a[8]));
+    const norm_mode_t mode = static_cast<norm_mode_t>(code_of(a[9]));
+    const bool inter = truth(a[11]);
+    const bool beta = norm && mode == NORM_LAYER && truth(a[18]);
+    const StreamArg stream(a[20]);
+    HeadsOut dq(a[12], "dq", dyq, dev), dk(keys ? a[13] : Py_None, "dk", keys ? dyk : dyq, dev);
+    Output dgq(a[14], "dgamma_q", f32, {hdq.D}, dev, norm);
+    Output dgk(a[15], "dgamma_k", f32, {hdq.D}, dev, norm && keys);
+    Output dbq(a[16], "dbeta_q", f32, {hdq.D}, dev, beta);
+    Output dbk(a[17], "dbeta_k", f32, {hdq.D}, dev, beta && keys);
+    Workspace ws(a[19], dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      const Heads oq = dq.make();
+      const Heads ok = keys ? dk.make() : Heads();
+      for (Output *o : {&dgq, &dgk, &dbq, &dbk}) o->make();
+      st = ws.make([&](size_t *b) {
+        return norm_rope_bwd_workspace_bytes(hdq.T, hdq.H, hdk.H, hdq.D, norm, mode, b);
+      });
+      if (st == NORM_OK)
+        st = norm_rope_bwd(&hdq.v, &hdk.v, &hq.v, &hk.v, hdq.T, hdq.H, hdk.H, hdq.D, rot.rd,
+                           rot.pos, rot.pos_bits, rot.pos_stride, rot.inv_freq, rot.axis, rot.axes,
+                           inter, ptr(gq), ptr(gk), eps, mode, code, &oq.v, &ok.v,
+                           static_cast<float *>(ptr(dgq.t)), static_cast<float *>(ptr(dgk.t)),
+                           static_cast<float *>(ptr(dbq.t)), static_cast<float *>(ptr(dbk.t)),
+                           ptr(ws.t), ws.bytes, on.s);
+    }
+    return result(st, {dq.t, dk.t, dgq.t, dgk.t, dbq.t, dbk.t});
+  });
+}
+
 template <typename F>
 PyCFunction as_method(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -507,6 +762,8 @@ PyMethodDef methods[] = {
     {"dropout_add_bwd", as_method(dropout_add_bwd), METH_FASTCALL, nullptr},
     {"group_fwd", as_method(group_fwd), METH_FASTCALL, nullptr},
     {"group_bwd", as_method(group_bwd), METH_FASTCALL, nullptr},
+    {"rope_fwd", as_method(rope_fwd), METH_FASTCALL, nullptr},
+    {"rope_bwd", as_method(rope_bwd), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gbnorm_torch", nullptr, -1, methods,
