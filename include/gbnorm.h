@@ -456,6 +456,71 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk,
                             norm_stream_t stream);
 
 /*
+ * Linear layer with bias, activation and residual.  The products around the
+ * normalisations of a transformer block: they read a norm's output and make the
+ * residual stream that the next one reads.
+ *   z = x W^T + bias          x [M, K]; W [N, K], one row per output feature
+ *   y = r + act(z)            y, z, r [M, N]
+ * fp32 accumulation, bias, activation (the definitions of norm_group_fwd) and
+ * residual in fp32, each output rounded once.  z, asked for where the backward
+ * pass needs it (any activation but NONE), is the rounded pre-activation.
+ * Backward, from dy, the forward's x and W, and z:
+ *   dz = dy * act'(z)         rounded to `dtype` for the tensor cores
+ *   dbias = column sums of dz (fp32, from the unrounded dz)
+ *   dx = dz W,  dw = dz^T x   (fp32 accumulation, rounded once)
+ * and the gradient of r is dy.  Results are bitwise reproducible for a given
+ * shape, type and device.
+ *
+ * Arguments:
+ *   x, w, bias, r, y, z, dy, dx, dw   of `dtype`, NORM_BF16 or NORM_FP16;
+ *              ldx, ...: row strides in elements, at least the row length
+ *              (ignored for a single row or a NULL matrix)
+ *   bias [N], r, z: may be NULL.  r may be y (same stride): the residual stream
+ *              is then updated in place.  Other outputs must not alias inputs.
+ *   dx, dw, dbias   outputs, NULL where not wanted (not all); x is read for dw,
+ *              w for dx, z for an activation
+ *   dbias      fp32 [N]
+ *   workspace  norm_linear_fwd_workspace_bytes / ..._bwd_... for these very
+ *              pointers, strides and sizes on the CURRENT device, 16-byte
+ *              aligned; may be NULL when that is 0.  Two calls that overlap in
+ *              time must not share it.
+ * Requirements: 1 <= M <= 2^24, 1 <= K, N <= 2^20, strides up to 2^32 (else
+ * NORM_ERR_SHAPE); element-aligned pointers (NORM_ERR_ALIGN); x, w, dy (and
+ * y, r, z of products with many rows) are device memory of the current device,
+ * or managed memory (NORM_ERR_MEMORY).  Unknown act, another dtype, or no
+ * output wanted: NORM_ERR_ARG.  Operands whose address and row stride are
+ * multiples of 16 bytes are read where they lie; others are first copied into
+ * the workspace (as much again as the operand, each call).
+ * Asynchronous on `stream`; a lost asynchronous copy or MMA surfaces through
+ * norm_get_device_error.
+ */
+norm_status_t norm_linear_fwd_workspace_bytes(const void *x, int64_t ldx,
+                                              const void *w, int64_t ldw, int64_t M,
+                                              int64_t K, int64_t N, size_t *bytes);
+
+norm_status_t norm_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
+                              const void *bias, const void *r, int64_t ldr, int64_t M,
+                              int64_t K, int64_t N, norm_act_t act,
+                              norm_dtype_t dtype, void *y, int64_t ldy, void *z,
+                              int64_t ldz, void *workspace, size_t workspace_bytes,
+                              norm_stream_t stream);
+
+norm_status_t norm_linear_bwd_workspace_bytes(const void *dy, int64_t lddy,
+                                              const void *x, int64_t ldx,
+                                              const void *w, int64_t ldw,
+                                              const void *z, int64_t ldz, int64_t M,
+                                              int64_t K, int64_t N, norm_act_t act,
+                                              int want_dx, int want_dw,
+                                              int want_dbias, size_t *bytes);
+
+norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                              const void *w, int64_t ldw, const void *z, int64_t ldz,
+                              int64_t M, int64_t K, int64_t N, norm_act_t act,
+                              norm_dtype_t dtype, void *dx, int64_t lddx, void *dw,
+                              int64_t lddw, float *dbias, void *workspace,
+                              size_t workspace_bytes, norm_stream_t stream);
+
+/*
  * FP8 output.  The page "Otimizacao de Performance de GPU" (introl.com,
  * December 2025 update) reports FP8 training as production ready on
  * Blackwell; the next consumer of a norm's output is usually a GEMM, which

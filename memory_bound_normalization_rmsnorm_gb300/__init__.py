@@ -14,7 +14,9 @@ from ._binding import (ACT_GELU, ACT_NONE, ACT_SILU, BF16, FP16, FP32, FP8_MX, F
                        norm_fwd_fp8, norm_gemm_fwd, norm_gemm_prepare, norm_get_device_error,
                        norm_group_bwd, norm_group_bwd_workspace_bytes, norm_group_fwd,
                        norm_group_fwd_workspace_bytes, norm_group_plan,
-                       norm_host_workspace_bytes, norm_plan, norm_rope_bwd,
+                       norm_host_workspace_bytes, norm_linear_bwd,
+                      norm_linear_bwd_workspace_bytes, norm_linear_fwd,
+                      norm_linear_fwd_workspace_bytes, norm_plan, norm_rope_bwd,
                       norm_rope_bwd_workspace_bytes, norm_rope_fwd, norm_tune_bwd, norm_tune_fwd, norm_tune_reset, strerror)
 from .builder import build
 
@@ -26,6 +28,8 @@ __all__ = [
     "norm_dropout", "norm_dropout_add_fwd", "norm_dropout_add_bwd",
     "norm_dropout_add_bwd_workspace_bytes", "norm_group_fwd", "norm_group_bwd",
     "norm_group_fwd_workspace_bytes", "norm_group_bwd_workspace_bytes", "norm_group_plan",
+    "norm_linear_fwd", "norm_linear_bwd", "norm_linear_fwd_workspace_bytes",
+    "norm_linear_bwd_workspace_bytes",
     "norm_rope_fwd", "norm_rope_bwd", "norm_rope_bwd_workspace_bytes",
     "BF16", "FP16", "FP32", "ACT_NONE", "ACT_SILU", "ACT_GELU",
     "norm_tune_reset", "norm_gemm_prepare", "norm_gemm_fwd", "strerror", "lib", "library_path", "declared_functions", "build",

@@ -180,7 +180,18 @@ def lib():
                                                         ctypes.POINTER(sz)]
             L.norm_rope_bwd.argtypes = [heads, heads, heads, heads, *rot, _vp, _vp, f32, ci, ci,
                                         heads, heads, _vp, _vp, _vp, _vp, _vp, sz, _vp]
-            for f in (L.norm_rope_fwd, L.norm_rope_bwd_workspace_bytes, L.norm_rope_bwd):
+            mat = [_vp, _i64]  # address, row stride
+            L.norm_linear_fwd_workspace_bytes.argtypes = [*mat, *mat, _i64, _i64, _i64,
+                                                          ctypes.POINTER(sz)]
+            L.norm_linear_fwd.argtypes = [*mat, *mat, _vp, *mat, _i64, _i64, _i64, ci, ci, *mat,
+                                          *mat, _vp, sz, _vp]
+            L.norm_linear_bwd_workspace_bytes.argtypes = [*mat, *mat, *mat, *mat, _i64, _i64, _i64,
+                                                          ci, ci, ci, ci, ctypes.POINTER(sz)]
+            L.norm_linear_bwd.argtypes = [*mat, *mat, *mat, *mat, _i64, _i64, _i64, ci, ci, *mat,
+                                          *mat, _vp, _vp, sz, _vp]
+            for f in (L.norm_rope_fwd, L.norm_rope_bwd_workspace_bytes, L.norm_rope_bwd,
+                      L.norm_linear_fwd_workspace_bytes, L.norm_linear_fwd,
+                      L.norm_linear_bwd_workspace_bytes, L.norm_linear_bwd):
                 f.restype = ci
             L.norm_plan.argtypes = [_i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                     ctypes.c_int, ctypes.POINTER(Plan)]
@@ -832,4 +843,54 @@ def norm_rope_bwd(dyq, dyk, q, k, pos, inv_freq, gamma_q=None, gamma_k=None, eps
         dgamma_q, dgamma_k, dbeta_q, dbeta_k, want_dbeta, workspace, _handle(stream))
     if type(out) is int:
         raise NormError(out, "norm_rope_bwd")
+    return out
+
+
+# ------------------------------------ linear layer with bias, activation, residual
+def norm_linear_fwd(x, w, bias=None, r=None, act=ACT_NONE, *, want_z=False, y=None, z=None,
+                    workspace=None, stream=None):
+    """y = r + act(x w^T + bias) (norm_linear_fwd in gbnorm.h).
+
+    x [..., K] and w [N, K] (the nn.Linear layout): bf16 or fp16, contiguous in
+    the last dimension, rows evenly strided; bias [N] and r [..., N] of the same
+    type, or None; act as norm_group_fwd.  y=r adds to the residual stream in
+    place.  Returns (y, z), z the pre-activation where want_z (or z is given),
+    else None."""
+    out = (_native_module or _native()).linear_fwd(x, w, bias, r, _act(act), want_z, y, z,
+                                                   workspace, _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_linear_fwd")
+    return out
+
+
+def norm_linear_bwd(dy, x, w, z=None, act=ACT_NONE, *, want_dx=True, want_dw=True,
+                    want_dbias=True, dx=None, dw=None, dbias=None, workspace=None, stream=None):
+    """Backward of norm_linear_fwd: (dx, dw, dbias) from dy [..., N], the forward's
+    x, w and (for an activation) z; dbias fp32 [N], each None where it is not
+    wanted.  x may be None without dw (or given for its shape alone), w without
+    dx.  The gradient of r is dy."""
+    out = (_native_module or _native()).linear_bwd(dy, x, w, z, _act(act), want_dx, want_dw,
+                                                   want_dbias, dx, dw, dbias, workspace,
+                                                   _handle(stream))
+    if type(out) is int:
+        raise NormError(out, "norm_linear_bwd")
+    return out
+
+
+def norm_linear_fwd_workspace_bytes(x, w) -> int:
+    """Workspace of norm_linear_fwd for these tensors (0 where their addresses and
+    row strides are multiples of 16 bytes)."""
+    out = (_native_module or _native()).linear_fwd_workspace(x, w)
+    if out < 0:
+        raise NormError(-out, "norm_linear_fwd_workspace_bytes")
+    return out
+
+
+def norm_linear_bwd_workspace_bytes(dy, x, w, z=None, act=ACT_NONE, *, want_dx=True, want_dw=True,
+                                    want_dbias=True) -> int:
+    """Workspace of norm_linear_bwd for these tensors."""
+    out = (_native_module or _native()).linear_bwd_workspace(dy, x, w, z, _act(act), want_dx,
+                                                             want_dw, want_dbias)
+    if out < 0:
+        raise NormError(-out, "norm_linear_bwd_workspace_bytes")
     return out

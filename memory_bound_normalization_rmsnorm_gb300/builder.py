@@ -36,7 +36,8 @@ TORCH_STAMP = os.path.join(OUT_DIR, "gbnorm_torch.stamp")
 SOURCES = ["fwd.cu", "fwd_fp8.cu", "fwd_gsm.cu", "bwd.cu", "long.cu", "long_resid.cu",
            "long_fp8.cu", "split.cu", "stream.cu", "api.cu", "host.cu", "gemm.cu", "dropout.cu",
            "drop_add.cu", "group_fwd.cu", "group_bwd.cu", "group_ring.cu",
-           "group.cu", "rope.cu", "rope_bwd.cu"]
+           "group.cu", "rope.cu", "rope_bwd.cu", "linear.cu",
+           "linear_pair.cu", "linear_split.cu", "linear_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

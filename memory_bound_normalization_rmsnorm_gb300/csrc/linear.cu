@@ -1,0 +1,422 @@
+// linear.cu -- entry points norm_linear_fwd / norm_linear_bwd: which kernels run
+// a product, its tensor maps, workspaces and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdlib>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "../../include/gbnorm.h"
+#include "common.cuh"
+#include "host_util.h"
+#include "linear.cuh"
+#include "tensor_map.h"
+
+namespace gbn {
+
+namespace {
+
+// A 16-bit matrix of `rows` rows of `cols` elements, `ld` elements apart.
+struct Matrix {
+  const void *p;
+  int64_t ld;
+  int64_t rows, cols;
+};
+
+// Tensor copies take addresses and row strides that are multiples of 16 bytes.
+bool tma_ready(const Matrix &t) {
+  return aligned_to_16(t.p) && (t.rows == 1 || t.ld % 8 == 0);
+}
+
+norm_status_t map_of(CUtensorMap *m, const Matrix &t, bool bf16, uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  norm_status_t st = tensor_map_encoder(&enc);
+  if (st != NORM_OK) return st;
+  const int64_t ld = t.rows == 1 ? (t.cols + 7) / 8 * 8 : t.ld;
+  cuuint64_t dims[2] = {cuuint64_t(t.cols), cuuint64_t(t.rows)};
+  cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  cuuint32_t box[2] = {kLinBK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+          const_cast<void *>(t.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? NORM_OK : NORM_ERR_CUDA;
+}
+
+struct Device {
+  int dev = 0, sms = 0, optin = 0;
+  unsigned *err = nullptr;
+};
+
+// How a product runs.
+struct ProductPlan {
+  bool pair = false;
+  int bn = 0, splits = 1, stages = 0;  // the split form
+};
+
+int round_up(int64_t v, int to) { return static_cast<int>((v + to - 1) / to * to); }
+
+ProductPlan plan_product(int64_t m, int64_t n, int64_t k, bool a_mn, const Device &d) {
+  const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
+  ProductPlan p;
+  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  p.pair = pair_tiles >= d.sms / 4;
+  const int unit = a_mn ? 64 : 16;
+  p.bn = m >= 128 ? 128 : round_up(m, unit);
+  const int64_t tiles = ((m + p.bn - 1) / p.bn) * ((n + 127) / 128);
+  int s = static_cast<int>((2 * d.sms) / tiles);
+  s = s < 1 ? 1 : s > 8 ? 8 : s;
+  p.splits = s > nk ? nk : s;
+  // GBNORM_LINEAR="pair=0,bn=64,splits=4" forces fields (for sweeps)
+  if (const char *o = std::getenv("GBNORM_LINEAR")) {
+    if (const char *q = std::strstr(o, "pair=")) p.pair = std::atoi(q + 5) != 0;
+    if (const char *q = std::strstr(o, "bn=")) {
+      const int bn = std::atoi(q + 3);
+      if (bn >= unit && bn <= 256 && bn % unit == 0) p.bn = bn;
+    }
+    if (const char *q = std::strstr(o, "splits=")) {
+      const int f = std::atoi(q + 7);
+      if (f >= 1 && f <= 8) p.splits = f > nk ? nk : f;
+    }
+  }
+  const int nkb = (nk + p.splits - 1) / p.splits;
+  // The stages hold the partial sums afterwards; two CTAs per SM where that
+  // leaves four stages, and no more than there are K blocks.
+  const uint32_t sb = split_stage_bytes(p.bn);
+  int least = static_cast<int>((uint32_t(p.bn) * 512u + sb - 1) / sb);
+  int most = static_cast<int>((113u * 1024u - split_smem(p.bn, 0)) / sb);
+  if (most < 4) most = static_cast<int>((uint32_t(d.optin) - split_smem(p.bn, 0)) / sb);
+  if (most > 12) most = 12;
+  p.stages = nkb < most ? nkb : most;
+  if (p.stages < least) p.stages = least;
+  return p;
+}
+
+std::mutex g_pairs_mu;
+std::map<std::pair<int, const void *>, int> g_pairs;  // co-resident CTA pairs
+
+norm_status_t resident_pairs(const Device &d, const void *fn, int *out) {
+  std::lock_guard<std::mutex> lk(g_pairs_mu);
+  auto it = g_pairs.find({d.dev, fn});
+  if (it == g_pairs.end()) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(d.sms - d.sms % 2));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = pair_smem();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return NORM_ERR_CUDA;
+    }
+    if (n < 1) return NORM_ERR_UNSUPPORTED;
+    it = g_pairs.emplace(std::make_pair(d.dev, fn), n).first;
+  }
+  *out = it->second;
+  return NORM_OK;
+}
+
+// out[j, i] = epilogue(sum_k A[j, k] B[i, k]); A and B are addressable by tensor
+// copies, stored [m or n, k], or [k, m or n] where a_mn / b_mn.
+norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix &b, bool b_mn,
+                      int64_t m, int64_t n, int64_t k, const LinEpilogue &e, bool bf16,
+                      cudaStream_t s) {
+  const ProductPlan plan = plan_product(m, n, k, a_mn, d);
+  const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
+  norm_status_t st;
+  CUtensorMap ta, tb;
+  if (plan.pair) {
+    const void *fn = linear_pair_kernel_ptr(a_mn, b_mn, bf16);
+    if (d.optin < int(pair_smem())) return NORM_ERR_UNSUPPORTED;
+    if ((st = function_ready(d.dev, fn, d.optin)) != NORM_OK) return st;
+    int pairs = 0;
+    if ((st = resident_pairs(d, fn, &pairs)) != NORM_OK) return st;
+    if ((st = map_of(&ta, a, bf16, a_mn ? kLinBK : 128)) != NORM_OK) return st;
+    if ((st = map_of(&tb, b, bf16, b_mn ? kLinBK : 128)) != NORM_OK) return st;
+    PairArgs p = {};
+    p.e = e;
+    p.m = static_cast<int>(m);
+    p.n = static_cast<int>(n);
+    p.nk = nk;
+    p.stages = e.r || e.z ? 5 : 6;
+    p.sets = e.r && !e.z ? 4 : 2;
+    p.ahead = p.sets / 2;
+    p.gm = 8;
+    p.err = d.err;
+    CUtensorMap ty = ta, tz = ta, tr = ta;
+    const Matrix out[3] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n}};
+    CUtensorMap *maps[3] = {&ty, &tz, &tr};
+    int *flags[3] = {&p.tma_y, &p.tma_z, &p.tma_r};
+    for (int i = 0; i < 3; ++i) {
+      if (!out[i].p || !tma_ready(out[i])) continue;
+      if ((st = check_device_memory(out[i].p, d.dev)) != NORM_OK) return st;
+      if ((st = map_of(maps[i], out[i], bf16, 32)) != NORM_OK) return st;
+      *flags[i] = 1;
+    }
+    const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
+    const int64_t grid = 2 * (tiles < pairs ? tiles : pairs);
+    void *args[] = {&ta, &tb, &ty, &tz, &tr, &p};
+    return launch_serial(fn, dim3(unsigned(grid)), dim3(kPairThreads), pair_smem(), 2, args, s);
+  }
+  const void *fn = linear_split_kernel_ptr(a_mn, b_mn, bf16);
+  const uint32_t smem = split_smem(plan.bn, plan.stages);
+  if (d.optin < int(smem)) return NORM_ERR_UNSUPPORTED;
+  if ((st = function_ready(d.dev, fn, d.optin)) != NORM_OK) return st;
+  if ((st = map_of(&ta, a, bf16, a_mn ? kLinBK : uint32_t(plan.bn))) != NORM_OK) return st;
+  if ((st = map_of(&tb, b, bf16, b_mn ? kLinBK : 128)) != NORM_OK) return st;
+  SplitArgs p = {};
+  p.e = e;
+  p.m = static_cast<int>(m);
+  p.n = static_cast<int>(n);
+  p.nk = nk;
+  p.bn = plan.bn;
+  p.splits = plan.splits;
+  p.stages = plan.stages;
+  p.tiles_j = static_cast<int>((m + plan.bn - 1) / plan.bn);
+  p.tmem = 32;
+  while (p.tmem < uint32_t(plan.bn)) p.tmem *= 2;
+  p.err = d.err;
+  p.vec = 1;
+  const Matrix rows[4] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n},
+                          {e.bias, 0, 1, n}};
+  for (const Matrix &t : rows)
+    if (reinterpret_cast<uintptr_t>(t.p) % 8 || (t.rows > 1 && t.p && t.ld % 4)) p.vec = 0;
+  const int64_t grid = int64_t(p.tiles_j) * ((n + 127) / 128) * plan.splits;
+  if (grid > 0x7fffffff) return NORM_ERR_UNSUPPORTED;
+  void *args[] = {&ta, &tb, &p};
+  return launch_serial(fn, dim3(unsigned(grid)), dim3(kSplitThreads), smem, plan.splits, args, s);
+}
+
+// Copies of operands in a workspace: whole multiples of 256 bytes.
+size_t packed_bytes(const Matrix &t) {
+  return (size_t(t.rows) * size_t(round_up(t.cols, 8)) * 2 + 255) & ~size_t(255);
+}
+
+norm_status_t pack(Matrix *t, char **ws, cudaStream_t s) {
+  if (tma_ready(*t)) return NORM_OK;
+  const uint16_t *src = static_cast<const uint16_t *>(t->p);
+  uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
+  int64_t ld = t->ld, ldd = round_up(t->cols, 8);
+  int rows = static_cast<int>(t->rows), cols = static_cast<int>(t->cols);
+  const int gy = (rows + 7) / 8 < 65535 ? (rows + 7) / 8 : 65535;
+  void *args[] = {&src, &ld, &rows, &cols, &dst, &ldd};
+  const norm_status_t st = launch_serial(linear_pack_kernel_ptr(),
+                                         dim3(unsigned((cols + 255) / 256), unsigned(gy)),
+                                         dim3(256), 0, 1, args, s);
+  *ws += packed_bytes(*t);
+  t->p = dst;
+  t->ld = ldd;
+  return st;
+}
+
+norm_status_t check_shape(int64_t M, int64_t K, int64_t N) {
+  const int64_t wide = int64_t(1) << 20;
+  if (M < 1 || M > (int64_t(1) << 24) || K < 1 || K > wide || N < 1 || N > wide)
+    return NORM_ERR_SHAPE;
+  return NORM_OK;
+}
+
+norm_status_t check_matrix(const Matrix &t) {
+  if (t.rows > 1 && (t.ld < t.cols || t.ld > (int64_t(1) << 32))) return NORM_ERR_SHAPE;
+  return reinterpret_cast<uintptr_t>(t.p) % 2 ? NORM_ERR_ALIGN : NORM_OK;
+}
+
+bool known_act(int act) {
+  return act == NORM_ACT_NONE || act == NORM_ACT_SILU || act == NORM_ACT_GELU;
+}
+
+// Row chunks of the gradient pass: enough CTAs to fill the GPU a few times, and
+// 32 rows or more in each.
+int grad_chunks(int64_t M, int64_t N, bool vec, int sms) {
+  const int64_t strips = (N + (vec ? 255 : 31)) / (vec ? 256 : 32);
+  int64_t c = (int64_t(sms) * 8 + strips - 1) / strips;
+  if (c > (M + 31) / 32) c = (M + 31) / 32;
+  if (c > 65535) c = 65535;
+  return static_cast<int>(c < 1 ? 1 : c);
+}
+
+// The parts of a backward workspace.
+struct GradPlan {
+  bool need_dz, vec;
+  int chunks;
+  size_t dz, part, x, w;
+  size_t total() const { return dz + part + x + w; }
+};
+
+GradPlan grad_plan(const Matrix &dy, const Matrix &x, const Matrix &w, const Matrix &z, int act,
+                   bool dx, bool dw, bool dbias, int sms) {
+  GradPlan g = {};
+  const bool products = dx || dw;
+  g.need_dz = products && (act != NORM_ACT_NONE || !tma_ready(dy));
+  g.vec = dy.cols % 8 == 0 && tma_ready(dy) && (act == NORM_ACT_NONE || tma_ready(z));
+  g.chunks = grad_chunks(dy.rows, dy.cols, g.vec, sms);
+  if (g.need_dz) g.dz = packed_bytes(dy);
+  if (dbias) g.part = (size_t(g.chunks) * size_t(dy.cols) * 4 + 255) & ~size_t(255);
+  if (dw && !tma_ready(x)) g.x = packed_bytes(x);
+  if (dx && !tma_ready(w)) g.w = packed_bytes(w);
+  return g;
+}
+
+norm_status_t device_of(Device *d) {
+  return device_context(&d->dev, &d->sms, &d->optin, &d->err, nullptr);
+}
+
+}  // namespace
+
+}  // namespace gbn
+
+using namespace gbn;
+
+extern "C" {
+
+norm_status_t norm_linear_fwd_workspace_bytes(const void *x, int64_t ldx, const void *w,
+                                              int64_t ldw, int64_t M, int64_t K, int64_t N,
+                                              size_t *bytes) {
+  if (!bytes || !x || !w) return NORM_ERR_NULL;
+  norm_status_t st = check_shape(M, K, N);
+  if (st != NORM_OK) return st;
+  *bytes = 0;
+  for (const Matrix &t : {Matrix{x, ldx, M, K}, Matrix{w, ldw, N, K}}) {
+    if ((st = check_matrix(t)) != NORM_OK) return st;
+    if (!tma_ready(t)) *bytes += packed_bytes(t);
+  }
+  return NORM_OK;
+}
+
+norm_status_t norm_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw,
+                              const void *bias, const void *r, int64_t ldr, int64_t M, int64_t K,
+                              int64_t N, norm_act_t act, norm_dtype_t dtype, void *y, int64_t ldy,
+                              void *z, int64_t ldz, void *workspace, size_t workspace_bytes,
+                              norm_stream_t stream) {
+  if (!x || !w || !y) return NORM_ERR_NULL;
+  norm_status_t st = check_shape(M, K, N);
+  if (st != NORM_OK) return st;
+  if (!known_act(act) || (dtype != NORM_BF16 && dtype != NORM_FP16)) return NORM_ERR_ARG;
+  Matrix mx{x, ldx, M, K}, mw{w, ldw, N, K};
+  for (const Matrix &t : {mx, mw, Matrix{y, ldy, M, N}, Matrix{z, z ? ldz : N, M, N},
+                          Matrix{r, r ? ldr : N, M, N}, Matrix{bias, N, 1, N}})
+    if ((st = check_matrix(t)) != NORM_OK) return st;
+  size_t need = 0;
+  if ((st = norm_linear_fwd_workspace_bytes(x, ldx, w, ldw, M, K, N, &need)) != NORM_OK) return st;
+  if (need && (!workspace || workspace_bytes < need)) return NORM_ERR_WORKSPACE;
+  if (need && !aligned_to_16(workspace)) return NORM_ERR_ALIGN;
+  Device d;
+  if ((st = device_of(&d)) != NORM_OK) return st;
+  for (const void *p : {x, w})
+    if ((st = check_device_memory(p, d.dev)) != NORM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  if ((st = pack(&mx, &ws, s)) != NORM_OK) return st;
+  if ((st = pack(&mw, &ws, s)) != NORM_OK) return st;
+  const LinEpilogue e = {bias, r, z, y, ldr, ldz, ldy, int(act)};
+  return product(d, mx, false, mw, false, M, N, K, e, dtype == NORM_BF16, s);
+}
+
+norm_status_t norm_linear_bwd_workspace_bytes(const void *dy, int64_t lddy, const void *x,
+                                              int64_t ldx, const void *w, int64_t ldw,
+                                              const void *z, int64_t ldz, int64_t M, int64_t K,
+                                              int64_t N, norm_act_t act, int want_dx, int want_dw,
+                                              int want_dbias, size_t *bytes) {
+  if (!bytes || !dy) return NORM_ERR_NULL;
+  if ((want_dw && !x) || (want_dx && !w)) return NORM_ERR_NULL;
+  norm_status_t st = check_shape(M, K, N);
+  if (st != NORM_OK) return st;
+  if (!known_act(act)) return NORM_ERR_ARG;
+  if (act != NORM_ACT_NONE && !z) return NORM_ERR_NULL;
+  Device d;
+  if ((st = device_of(&d)) != NORM_OK) return st;
+  *bytes = grad_plan({dy, lddy, M, N}, {x, ldx, M, K}, {w, ldw, N, K}, {z, ldz, M, N}, act,
+                     want_dx, want_dw, want_dbias, d.sms)
+               .total();
+  return NORM_OK;
+}
+
+norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                              const void *w, int64_t ldw, const void *z, int64_t ldz, int64_t M,
+                              int64_t K, int64_t N, norm_act_t act, norm_dtype_t dtype, void *dx,
+                              int64_t lddx, void *dw, int64_t lddw, float *dbias, void *workspace,
+                              size_t workspace_bytes, norm_stream_t stream) {
+  if (!dy) return NORM_ERR_NULL;
+  if ((dw && !x) || (dx && !w)) return NORM_ERR_NULL;
+  norm_status_t st = check_shape(M, K, N);
+  if (st != NORM_OK) return st;
+  if (!known_act(act) || (dtype != NORM_BF16 && dtype != NORM_FP16)) return NORM_ERR_ARG;
+  if (!dx && !dw && !dbias) return NORM_ERR_ARG;
+  if (act != NORM_ACT_NONE && !z) return NORM_ERR_NULL;
+  if (act == NORM_ACT_NONE) z = nullptr;
+  Matrix mdy{dy, lddy, M, N}, mx{x, dw ? ldx : K, M, K}, mw{w, dx ? ldw : K, N, K};
+  const Matrix mz{z, z ? ldz : N, M, N};
+  for (const Matrix &t : {mdy, mx, mw, mz, Matrix{dx, dx ? lddx : K, M, K},
+                          Matrix{dw, dw ? lddw : K, N, K}})
+    if ((st = check_matrix(t)) != NORM_OK) return st;
+  if (reinterpret_cast<uintptr_t>(dbias) % 4) return NORM_ERR_ALIGN;
+  Device d;
+  if ((st = device_of(&d)) != NORM_OK) return st;
+  const GradPlan g = grad_plan(mdy, mx, mw, mz, act, dx, dw, dbias, d.sms);
+  if (g.total() && (!workspace || workspace_bytes < g.total())) return NORM_ERR_WORKSPACE;
+  if (g.total() && !aligned_to_16(workspace)) return NORM_ERR_ALIGN;
+  for (const void *p : {dy, dw ? x : nullptr, dx ? w : nullptr})
+    if (p && (st = check_device_memory(p, d.dev)) != NORM_OK) return st;
+  const bool bf16 = dtype == NORM_BF16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  Matrix mdz = mdy;
+  if (g.need_dz || dbias) {
+    GradArgs a = {};
+    a.dy = dy;
+    a.z = z;
+    a.lddy = lddy;
+    a.ldz = ldz;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.chunks = g.chunks;
+    a.act = act;
+    if (g.need_dz) {
+      a.dz = ws;
+      a.lddz = round_up(N, 8);
+      ws += g.dz;
+      mdz.p = a.dz;
+      mdz.ld = a.lddz;
+    }
+    if (dbias) {
+      a.part = reinterpret_cast<float *>(ws);
+      ws += g.part;
+    }
+    void *args[] = {&a};
+    const int64_t strips = (N + (g.vec ? 255 : 31)) / (g.vec ? 256 : 32);
+    st = launch_serial(linear_grad_kernel_ptr(bf16, g.vec), dim3(unsigned(strips), unsigned(g.chunks)),
+                       dim3(kGradThreads), 0, 1, args, s);
+    if (st != NORM_OK) return st;
+    if (dbias) {
+      const float *part = a.part;
+      int n = a.N, rows = a.chunks;
+      void *fold[] = {&part, &n, &rows, &dbias};
+      st = launch_serial(linear_fold_kernel_ptr(), dim3(unsigned((n + 31) / 32)), dim3(1024), 0, 1,
+                         fold, s);
+      if (st != NORM_OK) return st;
+    }
+  }
+  if (dx) {
+    if ((st = pack(&mw, &ws, s)) != NORM_OK) return st;
+    const LinEpilogue e = {nullptr, nullptr, nullptr, dx, 0, 0, lddx, kLinNone};
+    if ((st = product(d, mdz, false, mw, true, M, K, N, e, bf16, s)) != NORM_OK) return st;
+  }
+  if (dw) {
+    if ((st = pack(&mx, &ws, s)) != NORM_OK) return st;
+    const LinEpilogue e = {nullptr, nullptr, nullptr, dw, 0, 0, lddw, kLinNone};
+    if ((st = product(d, mdz, true, mx, true, N, K, M, e, bf16, s)) != NORM_OK) return st;
+  }
+  return NORM_OK;
+}
+
+}  // extern "C"

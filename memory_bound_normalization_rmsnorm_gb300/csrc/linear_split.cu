@@ -1,0 +1,253 @@
+// linear_split.cu -- products of norm_linear_fwd / norm_linear_bwd with few or
+// middling rows (tokens): 128 output features x `bn` tokens per cluster, whose
+// CTAs share the contraction.
+//
+// Few tokens: bound by reading the weights once.  The weights are the MMA's
+// 128-row operand and the tokens its columns (16 at least), so a tile of W
+// feeds the tensor core whatever the number of tokens, and a layer of 4096
+// features has 32 tiles: the contraction is cut into up to 8 parts to keep
+// every SM's copies in flight.  Each CTA streams its part of W and x by TMA
+// (every stage in flight from the start where they all fit), leaves its fp32
+// partial sums in its own shared memory, frees its tensor memory and meets the
+// cluster; then each CTA adds the partials of its share of the tokens over
+// distributed shared memory in rank order (no atomics) and writes them with
+// the epilogue, whole 256-byte rows per warp.  A CTA holds no tensor memory
+// while it waits for a peer, so clusters of different streams cannot block each
+// other.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "linear.cuh"
+
+namespace gbn {
+
+namespace {
+
+__device__ __forceinline__ float4 ld_peer(uint32_t local, uint32_t rank) {
+  uint32_t remote;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote)
+               : "memory");
+  return v;
+}
+
+// Four consecutive elements (fewer at the end of a row).
+template <int DT>
+__device__ __forceinline__ void load4(const void *base, int64_t at, int count, bool vec, float (&f)[4]) {
+  if (vec && count == 4) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + at);
+    const float2 a = lin_unpack<DT>(w.x), b = lin_unpack<DT>(w.y);
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < count ? load_elem<DT>(base, at + i) : 0.f;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store4(void *base, int64_t at, int count, bool vec, const float (&f)[4]) {
+  if (vec && count == 4) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + at) =
+        make_uint2(lin_pack<DT>(f[0], f[1]), lin_pack<DT>(f[2], f[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count) store_elem<DT>(base, at + i, f[i]);
+  }
+}
+
+// AMN, BMN: storage of the token operand (A) and of the feature operand (B).
+template <bool AMN, bool BMN, int DT>
+__global__ void __launch_bounds__(kSplitThreads)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tm_a,
+                        const __grid_constant__ CUtensorMap tm_b, const SplitArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t *ring = smem_raw + pad;
+  const uint32_t stage_bytes = split_stage_bytes(p.bn);
+  uint64_t *full = reinterpret_cast<uint64_t *>(ring + p.stages * stage_bytes);
+  uint64_t *empty = full + 12;
+  uint64_t *acc = empty + 12;  // every MMA of the CTA finished
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
+  volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const int splits = p.splits;
+  const int rank = splits > 1 ? int(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / splits;
+  const int j0 = (tile % p.tiles_j) * p.bn;  // first token
+  const int i0 = (tile / p.tiles_j) * 128;   // first feature
+  const int kb0 = int(int64_t(p.nk) * rank / splits), kb1 = int(int64_t(p.nk) * (rank + 1) / splits);
+  const int nkb = kb1 - kb0;
+  const int stages = p.stages;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();  // before tensor memory is taken: never held while waiting
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (issued >= stages && !mbar_wait(&empty[s], ph ^ 1u, p.err, abort)) break;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        uint8_t *b = ring + s * stage_bytes, *a = b + 16384;
+        const int k0 = kb * kLinBK;
+        if (BMN) {
+          tma_load_2d(b, &tm_b, i0, k0, &full[s]);
+          tma_load_2d(b + 8192, &tm_b, i0 + 64, k0, &full[s]);
+        } else {
+          tma_load_2d(b, &tm_b, k0, i0, &full[s]);
+        }
+        if (AMN) {
+          for (int c = 0; c < p.bn; c += 64)
+            tma_load_2d(a + c * 128, &tm_a, j0 + c, k0, &full[s]);
+        } else {
+          tma_load_2d(a, &tm_a, k0, j0, &full[s]);
+        }
+        ++issued;
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      // every copy has landed before the ring is used for the partial sums
+      volatile int never = 0;
+      for (int i = 0; i < stages && i < issued; ++i) {
+        const int loads = (issued - i + stages - 1) / stages;
+        mbar_wait(&full[i], (loads - 1) & 1, p.err, &never);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // rows of the accumulator: features; columns: tokens
+      const uint32_t idesc = lin_idesc(128, p.bn, DT == kBF16, BMN, AMN);
+      constexpr uint32_t astep = lin_kstep(AMN), bstep = lin_kstep(BMN);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait(&full[s], ph, p.err, abort)) break;
+        tc_fence_after();
+        const uint32_t base = smem_addr(ring + s * stage_bytes);
+        const uint64_t bd = lin_desc(base, BMN), ad = lin_desc(base + 16384, AMN);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ss(tmem, bd + k * bstep, ad + k * astep, idesc, (kb | k) != 0);
+        mma_commit(&empty[s]);
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      mma_commit(acc);
+    }
+    __syncwarp();
+  }
+  __syncthreads();  // warp 0's copies have landed
+  // Partial sums [token][128 features] into the ring, once all MMAs have read it.
+  float *part = reinterpret_cast<float *>(ring);
+  if (warp >= 2) {
+    mbar_wait(acc, 0, p.err, abort);
+    __syncwarp();
+    tc_fence_after();
+    const int t0 = (warp & 3) * 32;
+    const uint32_t t_lane = tmem + (uint32_t(t0) << 16);
+    for (int c = 0; c < p.bn; c += 16) {
+      uint32_t v[16];
+      tmem_ld_n<16>(t_lane + c, v);
+      tmem_wait_ld_n<16>(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) part[(c + i) * 128 + t0 + lane] = __uint_as_float(v[i]);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem);
+  }
+  if (splits > 1) cluster_sync();
+
+  // This CTA's share of the tile's tokens, a warp per token, four features per
+  // lane.
+  const LinEpilogue &e = p.e;
+  const int tokens = min(p.bn, p.m - j0);
+  const int ja = tokens * rank / splits, jb = tokens * (rank + 1) / splits;
+  const int i = i0 + lane * 4;
+  const int count = min(4, p.n - i);
+  if (count > 0) {
+    const bool vec = p.vec;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (e.bias) load4<DT>(e.bias, i, count, vec, bias);
+    for (int j = ja + warp; j < jb; j += kSplitThreads / 32) {
+      const int64_t row = j0 + j;
+      float r[4] = {0.f, 0.f, 0.f, 0.f};
+      if (e.r) load4<DT>(e.r, row * e.ldr + i, count, vec, r);
+      const uint32_t at = smem_addr(part + j * 128 + lane * 4);
+      float f[4];
+      if (splits == 1) {
+        const float4 v = *reinterpret_cast<const float4 *>(part + j * 128 + lane * 4);
+        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+      } else {
+        float4 v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < splits) v[s] = ld_peer(at, uint32_t(s));
+        f[0] = v[0].x, f[1] = v[0].y, f[2] = v[0].z, f[3] = v[0].w;
+#pragma unroll
+        for (int s = 1; s < 8; ++s)
+          if (s < splits) f[0] += v[s].x, f[1] += v[s].y, f[2] += v[s].z, f[3] += v[s].w;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[q] += bias[q];
+      if (e.z) store4<DT>(e.z, row * e.ldz + i, count, vec, f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float z = f[q];
+        f[q] = (e.act == kLinNone ? z : e.act == kLinSilu ? lin_act<kLinSilu>(z)
+                                                          : lin_act<kLinGelu>(z)) +
+               r[q];
+      }
+      store4<DT>(e.y, row * e.ldy + i, count, vec, f);
+    }
+  }
+  __syncwarp();
+  if (splits > 1) cluster_sync();  // peers may still read this CTA's partials
+}
+
+template <bool AMN, bool BMN>
+const void *pick(bool bf16) {
+  return bf16 ? reinterpret_cast<const void *>(&linear_split_kernel<AMN, BMN, kBF16>)
+              : reinterpret_cast<const void *>(&linear_split_kernel<AMN, BMN, kFP16>);
+}
+
+}  // namespace
+
+const void *linear_split_kernel_ptr(bool a_mn, bool b_mn, bool bf16) {
+  if (a_mn) return b_mn ? pick<true, true>(bf16) : nullptr;
+  return b_mn ? pick<false, true>(bf16) : pick<false, false>(bf16);
+}
+
+}  // namespace gbn

@@ -1,5 +1,5 @@
 // torch_binding.cpp -- the tensor side of the dropout, group-normalisation and
-// head-rotation entry points: argument checks, output and workspace allocation, the
+// head-rotation and linear-layer entry points: argument checks, output and workspace allocation, the
 // current stream, and the C ABI call, in one native call.
 //
 // These operators run in 2 to 10 us on small tensors, less than a binding
@@ -751,6 +751,213 @@ PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A tensor of rows [..., C], contiguous in the last dimension, whose leading
+// dimensions are evenly strided rows.
+struct RowsView {
+  void *p = nullptr;
+  int64_t ld = 0, M = 0, C = 0;
+
+  RowsView() = default;
+  RowsView(const at::Tensor &t, const char *name) {
+    if (!t.defined()) return;
+    const int64_t n = t.dim();
+    if (n < 1) fail(std::string(name) + " must have at least one dimension");
+    C = t.size(n - 1);
+    if (C > 1 && t.stride(n - 1) != 1)
+      fail(std::string(name) + " must be contiguous in its last dimension");
+    M = 1;
+    ld = C;
+    bool any = false;
+    for (int64_t i = n - 2; i >= 0; --i) {
+      if (t.size(i) == 1) continue;
+      if (!any)
+        ld = t.stride(i);
+      else if (t.stride(i) != ld * M)
+        fail(std::string(name) + " must have evenly strided rows in its leading dimensions");
+      any = true;
+      M *= t.size(i);
+    }
+    p = t.numel() ? t.data_ptr() : nullptr;
+  }
+};
+
+// An output of rows: the given tensor (any strides that RowsView takes) or a new
+// contiguous one.
+struct RowsOut {
+  at::Tensor t;
+  at::ScalarType dt;
+  c10::DimVector shape;
+  const char *name;
+  bool wanted;
+
+  RowsOut(PyObject *o, const char *what, at::ScalarType type, c10::IntArrayRef sizes,
+          c10::Device dev, bool want = true)
+      : dt(type), shape(sizes.begin(), sizes.end()), name(what), wanted(want) {
+    if (o == Py_None) return;
+    t = tensor(o, name);
+    check_like(t, name, dt, sizes, dev);
+    RowsView checked(t, name);
+  }
+  RowsView make() {
+    if (!t.defined() && wanted) {
+      const int64_t bytes =
+          static_cast<int64_t>(c10::elementSize(dt)) * c10::multiply_integers(shape);
+      t = device_tensor((bytes + 511) & ~int64_t(511), dt, shape);
+    }
+    return RowsView(t, name);
+  }
+};
+
+norm_dtype_t half_code(const at::Tensor &t, const char *name) {
+  if (!t.is_cuda()) fail(std::string(name) + " must be a CUDA tensor");
+  if (t.scalar_type() == at::kBFloat16) return NORM_BF16;
+  if (t.scalar_type() == at::kHalf) return NORM_FP16;
+  fail(std::string(name) + " must be bfloat16 or float16, got " + c10::toString(t.scalar_type()));
+}
+
+c10::DimVector with_last(const at::Tensor &t, int64_t last) {
+  c10::DimVector d(t.sizes().begin(), t.sizes().end());
+  d.back() = last;
+  return d;
+}
+
+// The operands of a forward call.
+struct LinearIn {
+  const at::Tensor &x, &w;
+  RowsView vx, vw;
+  LinearIn(PyObject *ox, PyObject *ow) : x(tensor(ox, "x")), w(tensor(ow, "w")) {
+    half_code(x, "x");
+    if (w.dim() != 2) fail("w must be [N, K]");
+    vx = RowsView(x, "x");
+    check_like(w, "w", x.scalar_type(), {w.size(0), vx.C}, x.device());
+    vw = RowsView(w, "w");
+  }
+};
+
+// (x, w, bias, r, act, want_z, y, z, workspace, stream) -> (y, z)
+PyObject *linear_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<10>(n, [&]() -> PyObject * {
+    const LinearIn in(a[0], a[1]);
+    const norm_dtype_t code = half_code(in.x, "x");
+    const c10::Device dev = in.x.device();
+    const at::ScalarType dt = in.x.scalar_type();
+    const int64_t N = in.w.size(0);
+    const c10::DimVector shape = with_last(in.x, N);
+    const at::Tensor &bias = tensor(a[2], "bias", true), &r = tensor(a[3], "r", true);
+    check(bias, "bias", dt, {N}, dev);
+    if (r.defined()) check_like(r, "r", dt, shape, dev);
+    const RowsView vr(r, "r");
+    const norm_act_t act = static_cast<norm_act_t>(code_of(a[4]));
+    const StreamArg stream(a[9]);
+    RowsOut y(a[6], "y", dt, shape, dev), z(a[7], "z", dt, shape, dev, truth(a[5]));
+    Workspace ws(a[8], dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      const RowsView vy = y.make(), vz = z.make();
+      st = ws.make([&](size_t *b) {
+        return norm_linear_fwd_workspace_bytes(in.vx.p, in.vx.ld, in.vw.p, in.vw.ld, in.vx.M,
+                                               in.vx.C, N, b);
+      });
+      if (st == NORM_OK)
+        st = norm_linear_fwd(in.vx.p, in.vx.ld, in.vw.p, in.vw.ld, ptr(bias), vr.p, vr.ld, in.vx.M,
+                             in.vx.C, N, act, code, vy.p, vy.ld, vz.p, vz.ld, ptr(ws.t), ws.bytes,
+                             on.s);
+    }
+    return result(st, {y.t, z.t});
+  });
+}
+
+// What a backward call reads, and which outputs it wants.
+struct LinearGrad {
+  const at::Tensor &dy, &x, &w, &z;
+  RowsView vdy, vx, vw, vz;
+  int64_t M, K, N;
+  norm_act_t act;
+  bool dx, dw, dbias;
+  c10::DimVector xshape;
+
+  // (dy, x, w, z, act, want_dx, want_dw, want_dbias)
+  explicit LinearGrad(PyObject *const *a)
+      : dy(tensor(a[0], "dy")), x(tensor(a[1], "x", true)), w(tensor(a[2], "w", true)),
+        z(tensor(a[3], "z", true)), act(static_cast<norm_act_t>(code_of(a[4]))), dx(truth(a[5])),
+        dw(truth(a[6])), dbias(truth(a[7])) {
+    half_code(dy, "dy");
+    const c10::Device dev = dy.device();
+    const at::ScalarType dt = dy.scalar_type();
+    vdy = RowsView(dy, "dy");
+    M = vdy.M;
+    N = vdy.C;
+    if (!x.defined() && dw) fail("x must be given for dw");
+    if (!w.defined() && dx) fail("w must be given for dx");
+    if (w.defined() && (w.dim() != 2 || w.size(0) != N))
+      fail("w has shape " + show(w.sizes()) + ", expected " + std::to_string(N) + " rows");
+    K = w.defined() ? w.size(1) : x.defined() ? x.size(-1) : 1;
+    xshape = with_last(dy, K);
+    if (w.defined()) check_like(w, "w", dt, {N, K}, dev);
+    if (x.defined()) check_like(x, "x", dt, xshape, dev);
+    if (z.defined()) check_like(z, "z", dt, dy.sizes(), dev);
+    vx = RowsView(x, "x");
+    vw = RowsView(w, "w");
+    vz = RowsView(z, "z");
+  }
+  norm_status_t bytes(size_t *b) const {
+    return norm_linear_bwd_workspace_bytes(vdy.p, vdy.ld, vx.p, vx.ld, vw.p, vw.ld, vz.p, vz.ld, M,
+                                           K, N, act, dx, dw, dbias, b);
+  }
+};
+
+// (dy, x, w, z, act, want_dx, want_dw, want_dbias, dx, dw, dbias, workspace,
+// stream) -> (dx, dw, dbias)
+PyObject *linear_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<13>(n, [&]() -> PyObject * {
+    const LinearGrad in(a);
+    const norm_dtype_t code = half_code(in.dy, "dy");
+    const c10::Device dev = in.dy.device();
+    const at::ScalarType dt = in.dy.scalar_type();
+    const StreamArg stream(a[12]);
+    RowsOut dx(in.dx ? a[8] : Py_None, "dx", dt, in.xshape, dev, in.dx);
+    RowsOut dw(in.dw ? a[9] : Py_None, "dw", dt, {in.N, in.K}, dev, in.dw);
+    Output db(in.dbias ? a[10] : Py_None, "dbias", at::kFloat, {in.N}, dev, in.dbias);
+    Workspace ws(a[11], dev);
+    norm_status_t st;
+    {
+      const Unlocked unlocked;
+      const StreamScope on(stream, dev);
+      const RowsView vdx = dx.make(), vdw = dw.make();
+      db.make();
+      st = ws.make([&](size_t *b) { return in.bytes(b); });
+      if (st == NORM_OK)
+        st = norm_linear_bwd(in.vdy.p, in.vdy.ld, in.vx.p, in.vx.ld, in.vw.p, in.vw.ld, in.vz.p,
+                             in.vz.ld, in.M, in.K, in.N, in.act, code, vdx.p, vdx.ld, vdw.p, vdw.ld,
+                             static_cast<float *>(ptr(db.t)), ptr(ws.t), ws.bytes, on.s);
+    }
+    return result(st, {dx.t, dw.t, db.t});
+  });
+}
+
+// Workspace bytes, or minus the status.
+PyObject *linear_fwd_workspace(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<2>(n, [&]() -> PyObject * {
+    const LinearIn in(a[0], a[1]);
+    size_t b = 0;
+    const norm_status_t st = norm_linear_fwd_workspace_bytes(
+        in.vx.p, in.vx.ld, in.vw.p, in.vw.ld, in.vx.M, in.vx.C, in.w.size(0), &b);
+    return PyLong_FromLongLong(st == NORM_OK ? static_cast<long long>(b) : -st);
+  });
+}
+
+PyObject *linear_bwd_workspace(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<8>(n, [&]() -> PyObject * {
+    const LinearGrad in(a);
+    const c10::cuda::CUDAGuard on(in.dy.device());
+    size_t b = 0;
+    const norm_status_t st = in.bytes(&b);
+    return PyLong_FromLongLong(st == NORM_OK ? static_cast<long long>(b) : -st);
+  });
+}
+
 template <typename F>
 PyCFunction as_method(F f) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -762,6 +969,10 @@ PyMethodDef methods[] = {
     {"dropout_add_bwd", as_method(dropout_add_bwd), METH_FASTCALL, nullptr},
     {"group_fwd", as_method(group_fwd), METH_FASTCALL, nullptr},
     {"group_bwd", as_method(group_bwd), METH_FASTCALL, nullptr},
+    {"linear_fwd", as_method(linear_fwd), METH_FASTCALL, nullptr},
+    {"linear_bwd", as_method(linear_bwd), METH_FASTCALL, nullptr},
+    {"linear_fwd_workspace", as_method(linear_fwd_workspace), METH_FASTCALL, nullptr},
+    {"linear_bwd_workspace", as_method(linear_bwd_workspace), METH_FASTCALL, nullptr},
     {"rope_fwd", as_method(rope_fwd), METH_FASTCALL, nullptr},
     {"rope_bwd", as_method(rope_bwd), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
