@@ -13,107 +13,69 @@ namespace gbn {
 
 namespace {
 
-constexpr int kRopeBatch = 4;  // rows in flight per thread
-
 // One pass: read a row, normalise it in registers, turn its pairs, write it.
-// A warp takes a token (or, where tokens are few, a share of its heads): the
-// angles are computed once for all heads of the token, queries and keys.
 template <int DT, int V, int MODE>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int NU = rope_units(V);
-  __shared__ uint64_t turns[kRopeMaxD / 2];
+__global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
+    rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP, S = kRopeFwdStages;
+  extern __shared__ uint4 smem[];
+  RopeShared &sh = *reinterpret_cast<RopeShared *>(smem);
+  uint4 *ring_mem = smem + sizeof(RopeShared) / 16;
   grid_launch_dependents();
   grid_dependency_wait();
-  rope_table(a, turns);
-  __syncthreads();
-  const RopeLane<V> l(a);
-  const int warps = kRopeThreads / 32;
-  const int chunks = a.chunks[0];
-  const int64_t items = a.T * chunks;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * warps + threadIdx.x / 32; item < items;
-       item += static_cast<int64_t>(gridDim.x) * warps) {
-    const int64_t t = item / chunks;
-    const int c = static_cast<int>(item - t * chunks);
-    RopeAngles<V> ang;
-    ang.at(a, l, turns, t);
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const RopeSide &s = a.side[side];
-      if (s.H == 0) continue;
-      const int r0 = s.rounds * c / chunks, r1 = s.rounds * (c + 1) / chunks;
-      if (r0 == r1) continue;
-      float g[NU][2 * V], b[NU][2 * V];
+  const int side = static_cast<int>(blockIdx.x) >= a.ctas[0] ? 1 : 0;
+  const RopeSide &s = a.side[side];
+  const RopeLane<DT, V> l(a);
+  const int groups = 32 >> a.lanes_log2;
+  const int first = threadIdx.x / 32 * groups + l.group, per = kRopeThreads / 32 * groups;
+  RopeTiles<V> tile;
+  tile.start(a, side, static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0));
+  RopeRing<DT, V, 1, S> ring;
+  ring.start(a, side, ring_mem, tile.t, first, per);
+  for (int n = 0; n < S - 1; ++n) ring.fetch(a, side, l, first, per);
+  RopeUnit<V> g[NU];
+  RopeVec<DT, V> b[NU][2];
+  if (MODE != kNoNorm) l.param(g, s.gamma);
+  if (MODE == kLayer) l.load(b, static_cast<const char *>(s.beta), s.beta != nullptr);
+  RopeRow<1> out;
+  {
+    const void *base = s.out;
+    out.start<DT>(a, side, &base, &s.ot, &s.oh, first, per);
+  }
+  for (; tile.any(a); tile.t += tile.step) {
+    tile.angles(a, side, sh);
+    out.at(tile.t);
+    for (int left = tile.n * s.H; left > 0; left -= per) {
+      RopeUnit<V> f[NU];
+      RopeVec<DT, V> o[NU][2];
+      ring.wait();
+      ring.read(o, 0);
+      l.get(f, o);
+      ring.step();
+      ring.fetch(a, side, l, first, per);
       if constexpr (MODE != kNoNorm) {
+        const float2 rstd = splat2(rope_stats<MODE>(a, l, f));
+        RopeUnit<V> bf[NU];
+        if (MODE == kLayer) l.get(bf, b);
 #pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          RopeVec<DT, V> v;
-          v.zero();
-          if (l.in1[i]) v.load(s.gamma, l.o1[i]);
-          v.get(g[i]);
-          v.zero();
-          if (l.in2[i]) v.load(s.gamma, l.o2[i]);
-          v.get(g[i] + V);
-          if constexpr (MODE == kLayer) {
-            v.zero();
-            if (l.in1[i] && s.beta) v.load(s.beta, l.o1[i]);
-            v.get(b[i]);
-            v.zero();
-            if (l.in2[i] && s.beta) v.load(s.beta, l.o2[i]);
-            v.get(b[i] + V);
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            const float2 u = mul2(f[i].u[e], rstd), w = mul2(f[i].w[e], rstd);
+            f[i].u[e] = MODE == kLayer ? fma2(u, g[i].u[e], bf[i].u[e]) : mul2(u, g[i].u[e]);
+            f[i].w[e] = MODE == kLayer ? fma2(w, g[i].w[e], bf[i].w[e]) : mul2(w, g[i].w[e]);
           }
-        }
       }
-      for (int r = r0; r < r1; r += kRopeBatch) {
-        RopeVec<DT, V> v[kRopeBatch][NU][2];
+      const bool on = first < left;
+      RopeAngles<V> ang;
+      ang.get(a, l, sh.cs + (on ? out.tok * 2 * a.pairs : 0));
 #pragma unroll
-        for (int n = 0; n < kRopeBatch; ++n) {
-          const int h = ((r + n) << (5 - a.lanes_log2)) + l.group;
-          const bool row = r + n < r1 && h < s.H;
-          const int64_t at = t * s.xt + h * s.xh;
-#pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            v[n][i][0].zero();
-            v[n][i][1].zero();
-            if (row && l.in1[i]) v[n][i][0].load(s.x, at + l.o1[i]);
-            if (row && l.in2[i]) v[n][i][1].load(s.x, at + l.o2[i]);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < kRopeBatch; ++n) {
-          if (r + n >= r1) break;
-          const int h = ((r + n) << (5 - a.lanes_log2)) + l.group;
-          float f[NU][2 * V];
-#pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            v[n][i][0].get(f[i]);
-            v[n][i][1].get(f[i] + V);
-          }
-          if constexpr (MODE != kNoNorm) {
-            const float rstd = rope_stats<MODE, V>(a, l, f);
-#pragma unroll
-            for (int i = 0; i < NU; ++i)
-#pragma unroll
-              for (int e = 0; e < 2 * V; ++e)
-                f[i][e] = MODE == kLayer ? fmaf(f[i][e] * rstd, g[i][e], b[i][e])
-                                         : f[i][e] * rstd * g[i][e];
-          }
-          if (h >= s.H) continue;
-          const int64_t at = t * s.ot + h * s.oh;
-#pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            if (l.pair[i] >= 0) {
-              if (a.inter)
-                ang.turn(i, true, f[i]);
-              else
-                ang.turn(i, false, f[i]);
-            }
-            v[n][i][0].set(f[i]);
-            v[n][i][1].set(f[i] + V);
-            if (l.in1[i]) v[n][i][0].store(s.out, at + l.o1[i]);
-            if (l.in2[i]) v[n][i][1].store(s.out, at + l.o2[i]);
-          }
-        }
+      for (int i = 0; i < NU; ++i) {
+        if (l.pair[i] >= 0) ang.turn(i, f[i]);
+        f[i].set(o[i], l.mix[i]);
       }
+      if (on) l.store(o, const_cast<char *>(out.p[0]));
+      out.next();
     }
   }
 }
@@ -240,50 +202,53 @@ norm_status_t rope_args(const void *pos, int pos_bits, int64_t pos_stride, const
   return NORM_OK;
 }
 
-// Lanes per row and rounds, once the chunk width is known.
+// Lanes per row, once the chunk width is known.
 void rope_lanes(RopeArgs *a, int V) {
   a->units = a->pairs / V + (a->D - a->rd + 2 * V - 1) / (2 * V);
   const int l = pow2_log(a->units);
   a->lanes_log2 = l < 5 ? l : 5;
-  for (RopeSide &s : a->side) {
-    const int groups = 32 >> a->lanes_log2;
-    s.rounds = (s.H + groups - 1) / groups;
-  }
+  a->pairs_log2 = pow2_log(a->pairs);
 }
 
-constexpr int kRopeWarps = kRopeThreads / 32;
-
-// Warps that share a token: one where the tokens fill the GPU (the angles are
-// then computed once), else up to one per round of its longer side.
-int rope_chunks(int64_t T, int rounds, int sms) {
-  const int64_t want = int64_t(sms) * 16;
-  const int64_t c = (want + T - 1) / T;
-  return static_cast<int>(c < 1 ? 1 : c > rounds ? rounds : c);
+// CTAs of each side: `per_sm` per SM in all, shared in proportion to the sides'
+// work (a token's angles cost about as much as four rows).
+void rope_ctas(int64_t T, int64_t Hq, int64_t Hk, int sms, int per_sm, int *cq, int *ck) {
+  const int64_t most = int64_t(sms) * per_sm;
+  int64_t q = Hk ? (most * (Hq + 4) + (Hq + Hk + 8) / 2) / (Hq + Hk + 8) : most;
+  if (q > most - (Hk ? 1 : 0)) q = most - (Hk ? 1 : 0);
+  if (q < 1) q = 1;
+  *cq = static_cast<int>(q < T ? q : T);
+  *ck = Hk ? static_cast<int>(most - q < T ? most - q : T) : 0;
 }
 
-norm_status_t rope_launch_fwd(RopeArgs *a, int V, int mode, int dtype, int sms, cudaStream_t s) {
-  const int rounds = a->side[0].rounds > a->side[1].rounds ? a->side[0].rounds : a->side[1].rounds;
-  a->chunks[0] = rope_chunks(a->T, rounds, sms);
-  const int64_t items = a->T * a->chunks[0];
-  const int64_t ctas = (items + kRopeWarps - 1) / kRopeWarps;
-  const int64_t most = int64_t(sms) * 8;
-  void *args[] = {a};
-  return launch_serial(rope_fwd_kernel_ptr(dtype, V, mode),
-                       dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(kRopeThreads), 0,
-                       1, args, s);
-}
-
-// CTAs of each side of the backward, in proportion to its rows.
-void rope_bwd_ctas(int64_t T, int64_t Hq, int64_t Hk, int sms, int *cq, int *ck) {
-  const int64_t most = int64_t(sms) * 3;
-  const int64_t rows[2] = {T * Hq, T * Hk};
-  int *out[2] = {cq, ck};
+// Tokens per tile: 256 rows or so, fewer where that would leave CTAs without a
+// tile or the last round of tiles mostly empty.
+void rope_tiles(RopeArgs *a) {
   for (int i = 0; i < 2; ++i) {
-    int64_t c = (most * rows[i] + rows[0] + rows[1] - 1) / (rows[0] + rows[1]);
-    const int64_t use = (rows[i] + 15) / 16;  // two rows or more per warp
-    if (c > use) c = use;
-    *out[i] = static_cast<int>(c);
+    const int H = a->side[i].H;
+    if (H == 0) continue;
+    a->by_H[i].set(H);
+    int most = 256 / H;
+    if (most > kRopeMaxTile) most = kRopeMaxTile;
+    if (most > kRopeMaxAngles / a->pairs) most = kRopeMaxAngles / a->pairs;
+    if (most < 1) most = 1;
+    const int64_t per_cta = (a->T + a->ctas[i] - 1) / a->ctas[i];  // tokens
+    const int64_t tiles = (per_cta + most - 1) / most;
+    a->tile[i] = static_cast<int>((per_cta + tiles - 1) / tiles);
   }
+}
+
+norm_status_t rope_launch_fwd(RopeArgs *a, int V, int mode, int dtype, int dev, int sms, int optin,
+                              cudaStream_t s) {
+  const void *fn = rope_fwd_kernel_ptr(dtype, V, mode);
+  const norm_status_t st = function_ready(dev, fn, optin);
+  if (st != NORM_OK) return st;
+  rope_ctas(a->T, a->side[0].H, a->side[1].H, sms, rope_fwd_ctas(mode, V), &a->ctas[0], &a->ctas[1]);
+  rope_tiles(a);
+  void *args[] = {a};
+  return launch_serial(fn, dim3(unsigned(a->ctas[0] + a->ctas[1])),
+                       dim3(kRopeThreads),
+                       sizeof(RopeShared) + rope_ring_bytes(dtype, V, false), 1, args, s);
 }
 
 }  // namespace
@@ -338,7 +303,7 @@ norm_status_t norm_rope_fwd(const norm_heads_t *q, const norm_heads_t *k, int64_
   unsigned *err = nullptr;
   if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
   rope_lanes(&a, w.V);
-  return rope_launch_fwd(&a, w.V, norm ? mode : kNoNorm, dtype, sms,
+  return rope_launch_fwd(&a, w.V, norm ? mode : kNoNorm, dtype, dev, sms, optin,
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -353,7 +318,7 @@ norm_status_t norm_rope_bwd_workspace_bytes(int64_t T, int64_t Hq, int64_t Hk, i
   unsigned *err = nullptr;
   if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
   int cq = 0, ck = 0;
-  rope_bwd_ctas(T, Hq, Hk, sms, &cq, &ck);
+  rope_ctas(T, Hq, Hk, sms, kRopeBwdCtas, &cq, &ck);
   *bytes = size_t(cq + ck) * size_t(D) * 4 * (mode == NORM_LAYER ? 2 : 1);
   return NORM_OK;
 }
@@ -420,24 +385,21 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk, co
   rope_lanes(&a, w.V);
   a.sign = -1.f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!norm) return rope_launch_fwd(&a, w.V, kNoNorm, dtype, sms, s);
+  if (!norm) return rope_launch_fwd(&a, w.V, kNoNorm, dtype, dev, sms, optin, s);
   size_t need = 0;
   if ((st = norm_rope_bwd_workspace_bytes(T, Hq, Hk, D, 1, mode, &need)) != NORM_OK) return st;
   if (!workspace || workspace_bytes < need) return NORM_ERR_WORKSPACE;
   if (!aligned_to_16(workspace)) return NORM_ERR_ALIGN;
   a.part = static_cast<float *>(workspace);
-  rope_bwd_ctas(T, Hq, Hk, sms, &a.ctas[0], &a.ctas[1]);
-  for (int i = 0; i < 2; ++i) {
-    // warps that share a token: as many as leave every warp of the side work
-    const int64_t warps = int64_t(a.ctas[i]) * kRopeWarps;
-    int64_t c = (warps + T - 1) / T;
-    if (c > a.side[i].rounds) c = a.side[i].rounds;
-    a.chunks[i] = static_cast<int>(c < 1 ? 1 : c);
-  }
+  rope_ctas(T, Hq, Hk, sms, kRopeBwdCtas, &a.ctas[0], &a.ctas[1]);
+  rope_tiles(&a);
   const bool layer = mode == NORM_LAYER;
+  const void *fn = rope_bwd_kernel_ptr(dtype, w.V, mode);
+  if ((st = function_ready(dev, fn, optin)) != NORM_OK) return st;
+  const uint32_t ring = rope_ring_bytes(dtype, w.V, true), fold_bytes = rope_fold_floats(a.D, layer) * 4;
   void *args[] = {&a};
-  st = launch_serial(rope_bwd_kernel_ptr(dtype, w.V, mode), dim3(a.ctas[0] + a.ctas[1]),
-                     dim3(kRopeThreads), rope_fold_floats(a.D, layer) * 4, 1, args, s);
+  st = launch_serial(fn, dim3(a.ctas[0] + a.ctas[1]), dim3(kRopeThreads),
+                     sizeof(RopeShared) + (ring > fold_bytes ? ring : fold_bytes), 1, args, s);
   if (st != NORM_OK) return st;
   const float *part = a.part;
   int n = a.D, cq = a.ctas[0], ck = a.ctas[1];

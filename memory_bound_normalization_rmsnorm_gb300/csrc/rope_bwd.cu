@@ -16,137 +16,133 @@ namespace gbn {
 
 namespace {
 
-constexpr int kRopeBwdBatch = 2;  // rows in flight per thread
-
 template <int DT, int V, int MODE>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int NU = rope_units(V);
-  constexpr int B = kRopeBwdBatch;
-  __shared__ uint64_t turns[kRopeMaxD / 2];
-  extern __shared__ float fold[];
+__global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
+    rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP, S = kRopeBwdStages;
+  constexpr int es = elem_bytes(DT);
+  extern __shared__ uint4 smem[];
+  RopeShared &sh = *reinterpret_cast<RopeShared *>(smem);
+  uint4 *ring_mem = smem + sizeof(RopeShared) / 16;  // the ring, then the fold of the sums
+  float *fold = reinterpret_cast<float *>(ring_mem);
   grid_launch_dependents();
   grid_dependency_wait();
-  rope_table(a, turns);
-  __syncthreads();
-  const RopeLane<V> l(a);
   const int warps = kRopeThreads / 32, warp = threadIdx.x / 32;
   const int side = static_cast<int>(blockIdx.x) >= a.ctas[0] ? 1 : 0;
   const RopeSide &s = a.side[side];
-  const int cta = static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0);
-  const int chunks = a.chunks[side];
-  const int64_t items = a.T * chunks;
-  float g[NU][2 * V], dg[NU][2 * V], db[NU][2 * V];
-#pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    RopeVec<DT, V> v;
-    v.zero();
-    if (l.in1[i]) v.load(s.gamma, l.o1[i]);
-    v.get(g[i]);
-    v.zero();
-    if (l.in2[i]) v.load(s.gamma, l.o2[i]);
-    v.get(g[i] + V);
-#pragma unroll
-    for (int e = 0; e < 2 * V; ++e) dg[i][e] = db[i][e] = 0.f;
+  const RopeLane<DT, V> l(a);
+  const int groups = 32 >> a.lanes_log2;
+  const int first = warp * groups + l.group, per = warps * groups;
+  RopeTiles<V> tile;
+  tile.start(a, side, static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0));
+  RopeRing<DT, V, 2, S> ring;
+  ring.start(a, side, ring_mem, tile.t, first, per);
+  for (int n = 0; n < S - 1; ++n) ring.fetch(a, side, l, first, per);
+  RopeVec<DT, V> g[NU][2];
+  l.load(g, static_cast<const char *>(s.gamma), true);
+  RopeRow<1> out;
+  {
+    const void *base = s.out;
+    out.start<DT>(a, side, &base, &s.ot, &s.oh, first, per);
   }
-  for (int64_t item = static_cast<int64_t>(cta) * warps + warp; item < items;
-       item += static_cast<int64_t>(a.ctas[side]) * warps) {
-    const int64_t t = item / chunks;
-    const int c = static_cast<int>(item - t * chunks);
-    RopeAngles<V> ang;
-    ang.at(a, l, turns, t);
-    const int r0 = s.rounds * c / chunks, r1 = s.rounds * (c + 1) / chunks;
-    for (int r = r0; r < r1; r += B) {
-      RopeVec<DT, V> vx[B][NU][2], vd[B][NU][2];
-#pragma unroll
-      for (int n = 0; n < B; ++n) {
-        const int h = ((r + n) << (5 - a.lanes_log2)) + l.group;
-        const bool row = r + n < r1 && h < s.H;
-        const int64_t ax = t * s.xt + h * s.xh, ad = t * s.dt + h * s.dh;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            vx[n][i][k].zero();
-            vd[n][i][k].zero();
-            if (row && (k ? l.in2[i] : l.in1[i])) {
-              vx[n][i][k].load(s.x, ax + (k ? l.o2[i] : l.o1[i]));
-              vd[n][i][k].load(s.dy, ad + (k ? l.o2[i] : l.o1[i]));
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < B; ++n) {
-        if (r + n >= r1) break;
-        const int h = ((r + n) << (5 - a.lanes_log2)) + l.group;
-        float f[NU][2 * V], d[NU][2 * V];
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            vx[n][i][k].get(f[i] + k * V);
-            vd[n][i][k].get(d[i] + k * V);
-          }
-          if (l.pair[i] >= 0) {
-            if (a.inter)
-              ang.turn(i, true, d[i]);
-            else
-              ang.turn(i, false, d[i]);
-          }
-        }
-        const float rstd = rope_stats<MODE, V>(a, l, f);
-        // Lanes beyond the last head hold zeros; with eps = 0 their rstd is infinite.
-        const float rs = h < s.H ? rstd : 0.f;
-        float c1 = 0.f, c0 = 0.f;
+  RopeUnit<V> dg[NU], db[NU];
+  l.param(dg, nullptr);
+  l.param(db, nullptr);
+  for (; tile.any(a); tile.t += tile.step) {
+    tile.angles(a, side, sh);
+    out.at(tile.t);
+    for (int left = tile.n * s.H; left > 0; left -= per) {
+      const bool on = first < left;
+      RopeUnit<V> f[NU], d[NU];
+      RopeVec<DT, V> v[NU][2];
+      ring.wait();
+      ring.read(v, 0);
+      l.get(f, v);
+      ring.read(v, 1);
+      l.get(d, v);
+      ring.step();
+      ring.fetch(a, side, l, first, per);
+      {
+        RopeAngles<V> ang;
+        ang.get(a, l, sh.cs + (on ? out.tok * 2 * a.pairs : 0));
 #pragma unroll
         for (int i = 0; i < NU; ++i)
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            f[i][e] *= rs;  // xhat
-            dg[i][e] = fmaf(d[i][e], f[i][e], dg[i][e]);
-            if (MODE == kLayer) db[i][e] += d[i][e];
-            d[i][e] *= g[i][e];
-            c1 = fmaf(d[i][e], f[i][e], c1);
-            if (MODE == kLayer) c0 += d[i][e];
-          }
-        c1 = rope_sum(c1, a.lanes_log2) * a.invD;
-        if (MODE == kLayer) c0 = rope_sum(c0, a.lanes_log2) * a.invD;
-        if (h >= s.H) continue;
-        const int64_t at = t * s.ot + h * s.oh;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) {
-            const float m = MODE == kLayer ? d[i][e] - c0 : d[i][e];
-            d[i][e] = rs * fmaf(-f[i][e], c1, m);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            vd[n][i][k].set(d[i] + k * V);
-            if (k ? l.in2[i] : l.in1[i]) vd[n][i][k].store(s.out, at + (k ? l.o2[i] : l.o1[i]));
-          }
-        }
+          if (l.pair[i] >= 0) ang.turn(i, d[i]);
       }
+      // Lanes beyond the last head hold zeros; with eps = 0 their rstd is infinite.
+      const float rstd = rope_stats<MODE>(a, l, f);
+      const float rs = on ? rstd : 0.f;
+      RopeUnit<V> gf[NU];
+      l.get(gf, g);
+      float2 s1 = make_float2(0.f, 0.f), s0 = s1;
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int e = 0; e < 2 * NP; ++e) {
+          float2 &x = e < NP ? f[i].u[e] : f[i].w[e - NP], &y = e < NP ? d[i].u[e] : d[i].w[e - NP];
+          float2 &sg = e < NP ? dg[i].u[e] : dg[i].w[e - NP];
+          x = mul2(x, splat2(rs));  // xhat
+          sg = fma2(y, x, sg);
+          if (MODE == kLayer) {
+            float2 &sb = e < NP ? db[i].u[e] : db[i].w[e - NP];
+            sb = add2(sb, y);
+          }
+          y = mul2(y, e < NP ? gf[i].u[e] : gf[i].w[e - NP]);
+          s1 = fma2(y, x, s1);
+          if (MODE == kLayer) s0 = add2(s0, y);
+        }
+      // dx = rstd g - rstd mean(g) - xhat (rstd mean(g xhat))
+      const float2 c1 = splat2(-rs * (rope_sum(s1.x + s1.y, a.lanes_log2) * a.invD));
+      float2 c0 = make_float2(0.f, 0.f);
+      if (MODE == kLayer) c0 = splat2(-rs * (rope_sum(s0.x + s0.y, a.lanes_log2) * a.invD));
+      RopeVec<DT, V> o[NU][2];
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+#pragma unroll
+        for (int e = 0; e < 2 * NP; ++e) {
+          float2 &x = e < NP ? f[i].u[e] : f[i].w[e - NP], &y = e < NP ? d[i].u[e] : d[i].w[e - NP];
+          y = fma2(y, splat2(rs), MODE == kLayer ? fma2(x, c1, c0) : mul2(x, c1));
+        }
+        d[i].set(o[i], l.mix[i]);
+      }
+      if (on) l.store(o, const_cast<char *>(out.p[0]));
+      out.next();
     }
   }
+  __syncthreads();  // every round has been read
   // The warp's groups first (lanes that hold the same elements), then the warps.
+  const auto join = [&](RopeUnit<V> (&u)[NU], float *out) {
 #pragma unroll
-  for (int i = 0; i < NU; ++i)
+    for (int i = 0; i < NU; ++i) {
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) {
+      for (int e = 0; e < 2 * NP; ++e) {
+        float2 &x = e < NP ? u[i].u[e] : u[i].w[e - NP];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        if (o >= (1 << a.lanes_log2)) {
-          dg[i][e] += __shfl_xor_sync(0xffffffffu, dg[i][e], o);
-          if (MODE == kLayer) db[i][e] += __shfl_xor_sync(0xffffffffu, db[i][e], o);
+        for (int o = 16; o > 0; o >>= 1) {
+          if (o >= (1 << a.lanes_log2)) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+          }
         }
       }
-      if (l.group == 0 && (e < V ? l.in1[i] : l.in2[i])) {
-        const int at = warp * a.D + (e < V ? l.o1[i] + e : l.o2[i] + e - V);
-        fold[at] = dg[i][e];
-        if (MODE == kLayer) fold[warps * a.D + at] = db[i][e];
+      if (l.group != 0) continue;
+      const int e1 = l.o1[i] / es, e2 = l.o2[i] / es;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = e & 1 ? u[i].u[e / 2].y : u[i].u[e / 2].x;
+        const float y = e & 1 ? u[i].w[e / 2].y : u[i].w[e / 2].x;
+        if (V > 1 && l.mix[i]) {  // pair e: neighbours, the two chunks in a row
+          out[e1 + 2 * e] = x;
+          out[e1 + 2 * e + 1] = y;
+        } else {
+          if (l.in1[i]) out[e1 + e] = x;
+          if (l.in2[i]) out[e2 + e] = y;
+        }
       }
     }
+  };
+  join(dg, fold + warp * a.D);
+  if (MODE == kLayer) join(db, fold + (warps + warp) * a.D);
   __syncthreads();
   const int n = a.D * (MODE == kLayer ? 2 : 1);
   for (int i = threadIdx.x; i < n; i += kRopeThreads) {
