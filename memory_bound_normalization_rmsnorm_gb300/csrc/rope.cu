@@ -14,7 +14,7 @@ namespace gbn {
 namespace {
 
 // One pass: read a row, normalise it in registers, turn its pairs, write it.
-template <int DT, int V, int MODE>
+template <int DT, int V, int MODE, int MIX>
 __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
     rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP, S = kRopeFwdStages;
@@ -25,12 +25,12 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
   grid_dependency_wait();
   const int side = static_cast<int>(blockIdx.x) >= a.ctas[0] ? 1 : 0;
   const RopeSide &s = a.side[side];
-  const RopeLane<DT, V> l(a);
+  const RopeLane<DT, V, MIX> l(a);
   const int groups = 32 >> a.lanes_log2;
   const int first = threadIdx.x / 32 * groups + l.group, per = kRopeThreads / 32 * groups;
   RopeTiles<V> tile;
   tile.start(a, side, static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0));
-  RopeRing<DT, V, 1, S> ring;
+  RopeRing<DT, V, MIX, 1, S> ring;
   ring.start(a, side, ring_mem, tile.t, first, per);
   for (int n = 0; n < S - 1; ++n) ring.fetch(a, side, l, first, per);
   RopeUnit<V> g[NU];
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
     for (int left = tile.n * s.H; left > 0; left -= per) {
       RopeUnit<V> f[NU];
       RopeVec<DT, V> o[NU][2];
-      ring.wait();
+      ring.template wait<S - 2>();
       ring.read(o, 0);
       l.get(f, o);
       ring.step();
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (l.pair[i] >= 0) ang.turn(i, f[i]);
-        f[i].set(o[i], l.mix[i]);
+        f[i].template set<MIX>(o[i], l.mix[i]);
       }
       if (on) l.store(o, const_cast<char *>(out.p[0]));
       out.next();
@@ -80,34 +80,39 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
   }
 }
 
-template <int DT, int V>
+template <int DT, int V, int MIX>
 const void *pick_mode(int mode) {
   switch (mode) {
-    case kRMS: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kRMS>);
-    case kLayer: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kLayer>);
-    default: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kNoNorm>);
+    case kRMS: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kRMS, MIX>);
+    case kLayer: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kLayer, MIX>);
+    default: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kNoNorm, MIX>);
   }
 }
 
+template <int DT, int V>
+const void *pick_mix(int mode, bool inter) {
+  return inter ? pick_mode<DT, V, kMixed>(mode) : pick_mode<DT, V, kApart>(mode);
+}
+
 template <int DT>
-const void *pick_width(int V, int mode) {
+const void *pick_width(int V, int mode, bool inter) {
   switch (V) {
     case 8:
-      if constexpr (DT != kFP32) return pick_mode<DT, 8>(mode);
+      if constexpr (DT != kFP32) return pick_mix<DT, 8>(mode, inter);
       return nullptr;
-    case 4: return pick_mode<DT, 4>(mode);
-    case 2: return pick_mode<DT, 2>(mode);
-    default: return pick_mode<DT, 1>(mode);
+    case 4: return pick_mix<DT, 4>(mode, inter);
+    case 2: return pick_mode<DT, 2, kEither>(mode);
+    default: return pick_mode<DT, 1, kApart>(mode);
   }
 }
 
 }  // namespace
 
-const void *rope_fwd_kernel_ptr(int dt, int V, int mode) {
+const void *rope_fwd_kernel_ptr(int dt, int V, int mode, bool inter) {
   switch (dt) {
-    case kBF16: return pick_width<kBF16>(V, mode);
-    case kFP16: return pick_width<kFP16>(V, mode);
-    default: return pick_width<kFP32>(V, mode);
+    case kBF16: return pick_width<kBF16>(V, mode, inter);
+    case kFP16: return pick_width<kFP16>(V, mode, inter);
+    default: return pick_width<kFP32>(V, mode, inter);
   }
 }
 
@@ -211,28 +216,31 @@ void rope_lanes(RopeArgs *a, int V) {
 }
 
 // CTAs of each side: `per_sm` per SM in all, shared in proportion to the sides'
-// work (a token's angles cost about as much as four rows).
+// work.  A token's angles cost about as much as two of its rows: at 32768 tokens
+// of 32 + 8 heads the forward takes 126, 120, 117, 120 and 124 us where they are
+// counted as 0, 1, 2, 3 and 6.
 void rope_ctas(int64_t T, int64_t Hq, int64_t Hk, int sms, int per_sm, int *cq, int *ck) {
   const int64_t most = int64_t(sms) * per_sm;
-  int64_t q = Hk ? (most * (Hq + 4) + (Hq + Hk + 8) / 2) / (Hq + Hk + 8) : most;
+  int64_t q = Hk ? (most * (Hq + 2) + (Hq + Hk + 4) / 2) / (Hq + Hk + 4) : most;
   if (q > most - (Hk ? 1 : 0)) q = most - (Hk ? 1 : 0);
   if (q < 1) q = 1;
   *cq = static_cast<int>(q < T ? q : T);
   *ck = Hk ? static_cast<int>(most - q < T ? most - q : T) : 0;
 }
 
-// Tokens per tile: 256 rows or so, fewer where that would leave CTAs without a
-// tile or the last round of tiles mostly empty.
-void rope_tiles(RopeArgs *a) {
+// Tokens per tile: all of a CTA's where shared memory holds their angles (5476
+// tokens of 16 heads: 30 us in one tile, 32 in two), else `rows` rows or so, few
+// enough for the CTAs to end together.
+void rope_tiles(RopeArgs *a, int rows) {
   for (int i = 0; i < 2; ++i) {
     const int H = a->side[i].H;
     if (H == 0) continue;
     a->by_H[i].set(H);
-    int most = 256 / H;
-    if (most > kRopeMaxTile) most = kRopeMaxTile;
-    if (most > kRopeMaxAngles / a->pairs) most = kRopeMaxAngles / a->pairs;
-    if (most < 1) most = 1;
     const int64_t per_cta = (a->T + a->ctas[i] - 1) / a->ctas[i];  // tokens
+    int most = kRopeMaxAngles / a->pairs;
+    if (most > kRopeMaxTile) most = kRopeMaxTile;
+    if (per_cta > most && most > rows / H) most = rows / H;
+    if (most < 1) most = 1;
     const int64_t tiles = (per_cta + most - 1) / most;
     a->tile[i] = static_cast<int>((per_cta + tiles - 1) / tiles);
   }
@@ -240,11 +248,14 @@ void rope_tiles(RopeArgs *a) {
 
 norm_status_t rope_launch_fwd(RopeArgs *a, int V, int mode, int dtype, int dev, int sms, int optin,
                               cudaStream_t s) {
-  const void *fn = rope_fwd_kernel_ptr(dtype, V, mode);
+  const void *fn = rope_fwd_kernel_ptr(dtype, V, mode, a->inter);
   const norm_status_t st = function_ready(dev, fn, optin);
   if (st != NORM_OK) return st;
-  rope_ctas(a->T, a->side[0].H, a->side[1].H, sms, rope_fwd_ctas(mode, V), &a->ctas[0], &a->ctas[1]);
-  rope_tiles(a);
+  // With few tokens per CTA a third CTA per SM costs more to start than it brings
+  // (333 tokens: 4.7 us with three, 3.2 with two).
+  const int per_sm = a->T < int64_t(sms) * 16 ? 2 : rope_fwd_ctas(mode, V);
+  rope_ctas(a->T, a->side[0].H, a->side[1].H, sms, per_sm, &a->ctas[0], &a->ctas[1]);
+  rope_tiles(a, 128);
   void *args[] = {a};
   return launch_serial(fn, dim3(unsigned(a->ctas[0] + a->ctas[1])),
                        dim3(kRopeThreads),
@@ -392,9 +403,9 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk, co
   if (!aligned_to_16(workspace)) return NORM_ERR_ALIGN;
   a.part = static_cast<float *>(workspace);
   rope_ctas(T, Hq, Hk, sms, kRopeBwdCtas, &a.ctas[0], &a.ctas[1]);
-  rope_tiles(&a);
+  rope_tiles(&a, 256);
   const bool layer = mode == NORM_LAYER;
-  const void *fn = rope_bwd_kernel_ptr(dtype, w.V, mode);
+  const void *fn = rope_bwd_kernel_ptr(dtype, w.V, mode, a.inter);
   if ((st = function_ready(dev, fn, optin)) != NORM_OK) return st;
   const uint32_t ring = rope_ring_bytes(dtype, w.V, true), fold_bytes = rope_fold_floats(a.D, layer) * 4;
   void *args[] = {&a};

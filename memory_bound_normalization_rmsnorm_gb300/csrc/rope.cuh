@@ -148,18 +148,25 @@ struct RopeVec {
 // A unit's 2V values: the first elements of its pairs in u and the second in w,
 // packed two by two for the packed fp32 instructions, whichever way the pairs
 // lie in memory.
+// Pairs of neighbours: never, always, or as the unit says.  (A branch at run time
+// costs copies of the row's registers: 16384 tokens backward 96 us with it, 81
+// without; the narrow chunks of odd sizes have it to save kernels.)
+constexpr int kApart = 0, kMixed = 1, kEither = 2;
+__host__ __device__ constexpr bool rope_mixed(int mix, bool unit) {
+  return mix == kMixed || (mix == kEither && unit);
+}
+
 template <int V>
 struct RopeUnit {
   static constexpr int NP = V > 1 ? V / 2 : 1;
   float2 u[NP], w[NP];
 
-  // mix: the pairs are neighbours (V > 1).
-  template <int DT>
+  template <int MIX, int DT>
   __device__ __forceinline__ void get(const RopeVec<DT, V> (&v)[2], bool mix) {
     float2 a[NP], b[NP];
     v[0].get(a);
     v[1].get(b);
-    if (V > 1 && mix) {
+    if (V > 1 && rope_mixed(MIX, mix)) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         put(i, a[i]);
@@ -170,9 +177,9 @@ struct RopeUnit {
       for (int i = 0; i < NP; ++i) u[i] = a[i], w[i] = b[i];
     }
   }
-  template <int DT>
+  template <int MIX, int DT>
   __device__ __forceinline__ void set(RopeVec<DT, V> (&v)[2], bool mix) const {
-    if (V > 1 && mix) {
+    if (V > 1 && rope_mixed(MIX, mix)) {
       float2 a[NP], b[NP];
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -201,13 +208,13 @@ struct RopeUnit {
 
 // ----------------------------------------------------------------- lanes
 // Where the units of this lane lie in a row.
-template <int DT, int V>
+template <int DT, int V, int MIX>
 struct RopeLane {
   static constexpr int NU = rope_units(V);
   int o1[NU], o2[NU];     // bytes from the row to the two chunks
   int pair[NU];           // first pair of the unit, or -1: not turned
   bool in1[NU], in2[NU];  // the chunk exists
-  bool mix[NU];
+  bool mix[NU];           // kEither
   int group;              // this lane's row among the warp's
 
   __device__ __forceinline__ explicit RopeLane(const RopeArgs &a) {
@@ -255,7 +262,7 @@ struct RopeLane {
   }
   __device__ __forceinline__ void get(RopeUnit<V> (&f)[NU], const RopeVec<DT, V> (&v)[NU][2]) const {
 #pragma unroll
-    for (int i = 0; i < NU; ++i) f[i].get(v[i], mix[i]);
+    for (int i = 0; i < NU; ++i) f[i].template get<MIX>(v[i], mix[i]);
   }
   // A parameter row (gamma or beta); zeros for null.
   __device__ __forceinline__ void param(RopeUnit<V> (&f)[NU], const void *p) const {
@@ -270,12 +277,27 @@ struct RopeLane {
 // binary fraction of a turn, pos * f modulo 2^64 is the angle modulo a whole
 // turn exactly, however far the position: an integer product in place of a
 // range reduction.  (A product in 32 bits is off by 0.06 radians at position
-// 2^20; in float64 it is exact enough, at 1/64 of the rate.)  f is rounded to
-// 2^-54 of itself, the angle to 2^-32 of a turn and then to fp32.
+// 2^20.)  f is formed from the bits of inv_freq in integers too, truncated to
+// 2^-64 of a turn (float64 products, at 1/64 of the fp32 rate, made 333 tokens
+// take 5.1 us instead of 4.7).
 __device__ __forceinline__ uint64_t rope_turns(double inv_freq) {
-  double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= rint(t);
-  return static_cast<uint64_t>(__double2ll_rn(t * 18446744073709551616.0));  // 2^64
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(inv_freq));
+  const int e = static_cast<int>(bits >> 52) & 2047;
+  if (e == 0) return 0;  // below 2^-1022
+  const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  const uint64_t r = 0xa2f9836e4e44152aull;  // 2^66 / (2 pi)
+  const uint64_t hi = __umul64hi(m, r), lo = m * r;
+  // inv_freq = m 2^(e - 1075): the turns are (hi, lo) 2^(e - 1141), the fraction
+  // in units of 2^-64 (hi, lo) >> s
+  const int s = 1077 - e;
+  uint64_t f = 0;
+  if (s >= 128)
+    f = 0;
+  else if (s >= 64)
+    f = hi >> (s - 64);
+  else if (s > 0)
+    f = (hi << (64 - s)) | (lo >> s);
+  return bits >> 63 ? 0 - f : f;
 }
 
 // cos and sin of a fraction of a turn given as a 32-bit binary fraction: the
@@ -379,8 +401,9 @@ struct RopeAngles {
   float2 c[NU][NP], s[NU][NP];
 
   // cs: the token's angles
-  template <int DT>
-  __device__ __forceinline__ void get(const RopeArgs &a, const RopeLane<DT, V> &l, const float *cs) {
+  template <int DT, int MIX>
+  __device__ __forceinline__ void get(const RopeArgs &a, const RopeLane<DT, V, MIX> &l,
+                                      const float *cs) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
 #pragma unroll
@@ -461,7 +484,7 @@ struct RopeRow {
 // memory, zeros where there is no row.  No registers hold what is in flight and
 // no barrier joins the threads.  A round is fetched into the slots of the one
 // before the round that is being read, whose values have been used up.
-template <int DT, int V, int N, int S>
+template <int DT, int V, int MIX, int N, int S>
 struct RopeRing {
   static constexpr int NU = rope_units(V);
   static constexpr int kBytes = RopeVec<DT, V>::kBytes;
@@ -509,7 +532,7 @@ struct RopeRing {
     }
   }
   // Fetches the next round.
-  __device__ __forceinline__ void fetch(const RopeArgs &a, int side, const RopeLane<DT, V> &l,
+  __device__ __forceinline__ void fetch(const RopeArgs &a, int side, const RopeLane<DT, V, MIX> &l,
                                         int first, int per) {
     if (left > 0) {
       const bool on = first < left;
@@ -533,8 +556,9 @@ struct RopeRing {
     stage = stage + kStage == kTotal ? 0u : stage + kStage;
   }
   // Waits for the oldest round in flight.
+  template <int LEFT>
   __device__ __forceinline__ void wait() const {
-    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
   }
   // On to the next round.
   __device__ __forceinline__ void step() { now = now + kStage == kTotal ? 0u : now + kStage; }
@@ -572,8 +596,8 @@ __device__ __forceinline__ float rope_sum(float v, int lanes_log2) {
 }
 
 // x - mean (LayerNorm) in f, zero where there is no element; returns rstd.
-template <int MODE, int DT, int V>
-__device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT, V> &l,
+template <int MODE, int DT, int V, int MIX>
+__device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT, V, MIX> &l,
                                             RopeUnit<V> (&f)[rope_units(V)]) {
   constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP;
   if constexpr (MODE == kLayer) {
@@ -588,8 +612,11 @@ __device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT
       const float2 m1 = splat2(l.in1[i] ? -mean : 0.f), m2 = splat2(l.in2[i] ? -mean : 0.f);
 #pragma unroll
       for (int e = 0; e < NP; ++e) {
-        f[i].u[e] = add2(f[i].u[e], m1);
-        f[i].w[e] = add2(f[i].w[e], m2);
+        // (mixed, the first half of u and w is the first chunk; with kEither a
+        // unit that lacks its second chunk is not mixed)
+        const bool one = MIX != kMixed || e < NP / 2;
+        f[i].u[e] = add2(f[i].u[e], one ? m1 : m2);
+        f[i].w[e] = add2(f[i].w[e], MIX == kMixed && one ? m1 : m2);
         if (V == 1) f[i].u[e].y = f[i].w[e].y = 0.f;
       }
     }
@@ -604,8 +631,8 @@ __device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT
 
 
 // Kernels, and the shared memory of their rings.
-const void *rope_fwd_kernel_ptr(int dt, int V, int mode);
-const void *rope_bwd_kernel_ptr(int dt, int V, int mode);
+const void *rope_fwd_kernel_ptr(int dt, int V, int mode, bool inter);
+const void *rope_bwd_kernel_ptr(int dt, int V, int mode, bool inter);
 __host__ __device__ inline uint32_t rope_ring_bytes(int dt, int V, bool bwd) {
   return uint32_t(kRopeThreads * 2 * rope_units(V) * V * elem_bytes(dt)) *
          (bwd ? 2 * kRopeBwdStages : kRopeFwdStages);

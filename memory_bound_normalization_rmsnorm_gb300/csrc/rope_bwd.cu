@@ -16,7 +16,7 @@ namespace gbn {
 
 namespace {
 
-template <int DT, int V, int MODE>
+template <int DT, int V, int MODE, int MIX>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
     rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP, S = kRopeBwdStages;
@@ -30,12 +30,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
   const int warps = kRopeThreads / 32, warp = threadIdx.x / 32;
   const int side = static_cast<int>(blockIdx.x) >= a.ctas[0] ? 1 : 0;
   const RopeSide &s = a.side[side];
-  const RopeLane<DT, V> l(a);
+  const RopeLane<DT, V, MIX> l(a);
   const int groups = 32 >> a.lanes_log2;
   const int first = warp * groups + l.group, per = warps * groups;
   RopeTiles<V> tile;
   tile.start(a, side, static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0));
-  RopeRing<DT, V, 2, S> ring;
+  RopeRing<DT, V, MIX, 2, S> ring;
   ring.start(a, side, ring_mem, tile.t, first, per);
   for (int n = 0; n < S - 1; ++n) ring.fetch(a, side, l, first, per);
   RopeVec<DT, V> g[NU][2];
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
       const bool on = first < left;
       RopeUnit<V> f[NU], d[NU];
       RopeVec<DT, V> v[NU][2];
-      ring.wait();
+      ring.template wait<S - 2>();
       ring.read(v, 0);
       l.get(f, v);
       ring.read(v, 1);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
           float2 &x = e < NP ? f[i].u[e] : f[i].w[e - NP], &y = e < NP ? d[i].u[e] : d[i].w[e - NP];
           y = fma2(y, splat2(rs), MODE == kLayer ? fma2(x, c1, c0) : mul2(x, c1));
         }
-        d[i].set(o[i], l.mix[i]);
+        d[i].template set<MIX>(o[i], l.mix[i]);
       }
       if (on) l.store(o, const_cast<char *>(out.p[0]));
       out.next();
@@ -131,9 +131,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
       for (int e = 0; e < V; ++e) {
         const float x = e & 1 ? u[i].u[e / 2].y : u[i].u[e / 2].x;
         const float y = e & 1 ? u[i].w[e / 2].y : u[i].w[e / 2].x;
-        if (V > 1 && l.mix[i]) {  // pair e: neighbours, the two chunks in a row
-          out[e1 + 2 * e] = x;
-          out[e1 + 2 * e + 1] = y;
+        if (V > 1 && rope_mixed(MIX, l.mix[i])) {  // neighbours, the two chunks in a row
+          if (2 * e < V ? l.in1[i] : l.in2[i]) {
+            out[e1 + 2 * e] = x;
+            out[e1 + 2 * e + 1] = y;
+          }
         } else {
           if (l.in1[i]) out[e1 + e] = x;
           if (l.in2[i]) out[e2 + e] = y;
@@ -181,31 +183,36 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-template <int DT, int V>
+template <int DT, int V, int MIX>
 const void *pick_mode(int mode) {
-  return mode == kLayer ? reinterpret_cast<const void *>(&rope_bwd_kernel<DT, V, kLayer>)
-                        : reinterpret_cast<const void *>(&rope_bwd_kernel<DT, V, kRMS>);
+  return mode == kLayer ? reinterpret_cast<const void *>(&rope_bwd_kernel<DT, V, kLayer, MIX>)
+                        : reinterpret_cast<const void *>(&rope_bwd_kernel<DT, V, kRMS, MIX>);
+}
+
+template <int DT, int V>
+const void *pick_mix(int mode, bool inter) {
+  return inter ? pick_mode<DT, V, kMixed>(mode) : pick_mode<DT, V, kApart>(mode);
 }
 
 template <int DT>
-const void *pick_width(int V, int mode) {
+const void *pick_width(int V, int mode, bool inter) {
   switch (V) {
     case 8:
-      if constexpr (DT != kFP32) return pick_mode<DT, 8>(mode);
+      if constexpr (DT != kFP32) return pick_mix<DT, 8>(mode, inter);
       return nullptr;
-    case 4: return pick_mode<DT, 4>(mode);
-    case 2: return pick_mode<DT, 2>(mode);
-    default: return pick_mode<DT, 1>(mode);
+    case 4: return pick_mix<DT, 4>(mode, inter);
+    case 2: return pick_mode<DT, 2, kEither>(mode);
+    default: return pick_mode<DT, 1, kApart>(mode);
   }
 }
 
 }  // namespace
 
-const void *rope_bwd_kernel_ptr(int dt, int V, int mode) {
+const void *rope_bwd_kernel_ptr(int dt, int V, int mode, bool inter) {
   switch (dt) {
-    case kBF16: return pick_width<kBF16>(V, mode);
-    case kFP16: return pick_width<kFP16>(V, mode);
-    default: return pick_width<kFP32>(V, mode);
+    case kBF16: return pick_width<kBF16>(V, mode, inter);
+    case kFP16: return pick_width<kFP16>(V, mode, inter);
+    default: return pick_width<kFP32>(V, mode, inter);
   }
 }
 
