@@ -56,7 +56,9 @@ struct Device {
 // How a product runs.
 struct ProductPlan {
   bool pair = false;
-  int bn = 0, splits = 1, stages = 0;  // the split form
+  int bn = 0;      // tile columns (pair), or tokens per tile (split)
+  int splits = 1;  // the split form
+  int stages = 0;
 };
 
 int round_up(int64_t v, int to) { return static_cast<int>((v + to - 1) / to * to); }
@@ -67,6 +69,7 @@ ProductPlan plan_product(int64_t m, int64_t n, int64_t k, bool a_mn, const Devic
   const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
   p.pair = pair_tiles >= d.sms / 4;
   const int unit = a_mn ? 64 : 16;
+  int pair_bn = 256;
   p.bn = m >= 128 ? 128 : round_up(m, unit);
   const int64_t tiles = ((m + p.bn - 1) / p.bn) * ((n + 127) / 128);
   int s = static_cast<int>((2 * d.sms) / tiles);
@@ -78,22 +81,27 @@ ProductPlan plan_product(int64_t m, int64_t n, int64_t k, bool a_mn, const Devic
     if (const char *q = std::strstr(o, "bn=")) {
       const int bn = std::atoi(q + 3);
       if (bn >= unit && bn <= 256 && bn % unit == 0) p.bn = bn;
+      if (bn >= 64 && bn <= 256 && bn % 32 == 0) pair_bn = bn;
     }
     if (const char *q = std::strstr(o, "splits=")) {
       const int f = std::atoi(q + 7);
       if (f >= 1 && f <= 8) p.splits = f > nk ? nk : f;
     }
   }
+  if (p.pair) {
+    p.bn = pair_bn;
+    return p;
+  }
+  // As many stages as there are K blocks, or as leave room for two CTAs per SM
+  // where that makes four; the ring also takes the partial sums of all tokens.
   const int nkb = (nk + p.splits - 1) / p.splits;
-  // The stages hold the partial sums afterwards; two CTAs per SM where that
-  // leaves four stages, and no more than there are K blocks.
-  const uint32_t sb = split_stage_bytes(p.bn);
-  int least = static_cast<int>((uint32_t(p.bn) * 512u + sb - 1) / sb);
-  int most = static_cast<int>((113u * 1024u - split_smem(p.bn, 0)) / sb);
-  if (most < 4) most = static_cast<int>((uint32_t(d.optin) - split_smem(p.bn, 0)) / sb);
-  if (most > 12) most = 12;
+  const uint32_t sb = split_stage_bytes(p.bn), fixed = split_smem(p.bn, p.splits, 0);
+  int most = static_cast<int>((uint32_t(d.optin) / 2 - 1024 - fixed) / sb);
+  if (most < 4) most = static_cast<int>((uint32_t(d.optin) - fixed) / sb);
+  if (most > kSplitMaxStages) most = kSplitMaxStages;
   p.stages = nkb < most ? nkb : most;
-  if (p.stages < least) p.stages = least;
+  const int least = static_cast<int>((uint32_t(p.bn) * 512u + sb - 1) / sb);
+  if (!split_push(p.bn, p.splits) && p.stages < least) p.stages = least;
   return p;
 }
 
@@ -142,13 +150,15 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     int pairs = 0;
     if ((st = resident_pairs(d, fn, &pairs)) != NORM_OK) return st;
     if ((st = map_of(&ta, a, bf16, a_mn ? kLinBK : 128)) != NORM_OK) return st;
-    if ((st = map_of(&tb, b, bf16, b_mn ? kLinBK : 128)) != NORM_OK) return st;
+    if ((st = map_of(&tb, b, bf16, b_mn ? kLinBK : uint32_t(plan.bn / 2))) != NORM_OK) return st;
     PairArgs p = {};
     p.e = e;
     p.m = static_cast<int>(m);
     p.n = static_cast<int>(n);
     p.nk = nk;
-    p.stages = e.r || e.z ? 5 : 6;
+    p.bn = plan.bn;
+    p.bufs = e.r || e.z ? 4 : 2;
+    p.stages = pair_stages(p.bn, b_mn, p.bufs);
     p.sets = e.r && !e.z ? 4 : 2;
     p.ahead = p.sets / 2;
     p.gm = 8;
@@ -163,13 +173,13 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
       if ((st = map_of(maps[i], out[i], bf16, 32)) != NORM_OK) return st;
       *flags[i] = 1;
     }
-    const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
+    const int64_t tiles = ((m + 255) / 256) * ((n + plan.bn - 1) / plan.bn);
     const int64_t grid = 2 * (tiles < pairs ? tiles : pairs);
     void *args[] = {&ta, &tb, &ty, &tz, &tr, &p};
     return launch_serial(fn, dim3(unsigned(grid)), dim3(kPairThreads), pair_smem(), 2, args, s);
   }
   const void *fn = linear_split_kernel_ptr(a_mn, b_mn, bf16);
-  const uint32_t smem = split_smem(plan.bn, plan.stages);
+  const uint32_t smem = split_smem(plan.bn, plan.splits, plan.stages);
   if (d.optin < int(smem)) return NORM_ERR_UNSUPPORTED;
   if ((st = function_ready(d.dev, fn, d.optin)) != NORM_OK) return st;
   if ((st = map_of(&ta, a, bf16, a_mn ? kLinBK : uint32_t(plan.bn))) != NORM_OK) return st;

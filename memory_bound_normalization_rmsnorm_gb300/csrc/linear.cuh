@@ -105,27 +105,38 @@ __device__ __forceinline__ uint32_t lin_pack(float a, float b) {
 }
 
 // ------------------------------------------------------------- kernels
-// Output tiles of 256 x 256 by CTA pairs, persistent (linear_pair.cu).
+// Output tiles of 256 x bn by CTA pairs, persistent (linear_pair.cu).
 constexpr int kPairThreads = 192;
 struct PairArgs {
   LinEpilogue e;
   int m, n, nk;
-  int stages;   // operand stages: 6, or 5 beside four output buffers
+  int bn;       // tile columns: a multiple of 32, up to 256
+  int stages;   // operand stages
+  int bufs;     // 16 KB output buffers: 2 or 4
   int sets;     // output buffers (pairs of them where z is written) used in turn
   int ahead;    // slices that r is loaded ahead
   int tma_y, tma_z, tma_r;  // moved by tensor copies (else by the warps)
   int gm;       // row blocks per group of the tile walk
   unsigned *err;
 };
-__host__ __device__ constexpr uint32_t pair_smem() {
-  return 1024 + 6 * 32768 + 2 * 16384 + 1024 + 512;
+constexpr int kPairMaxStages = 9;
+// Operand ring (A and B tiles of a stage), output buffers, bias row, barriers.
+constexpr uint32_t kPairTiles = 6 * 32768 + 2 * 16384;  // ring and buffers
+__host__ __device__ constexpr uint32_t pair_stage(int bn, bool b_mn) {
+  return 16384u + (b_mn ? 16384u : uint32_t(bn) * 64u);
 }
+__host__ __device__ constexpr int pair_stages(int bn, bool b_mn, int bufs) {
+  const uint32_t n = (kPairTiles - uint32_t(bufs) * 16384u) / pair_stage(bn, b_mn);
+  return n < uint32_t(kPairMaxStages) ? int(n) : kPairMaxStages;
+}
+__host__ __device__ constexpr uint32_t pair_smem() { return 1024 + kPairTiles + 1024 + 512; }
 // (A MN-major, B MN-major, bf16); nullptr for A MN-major with B K-major.
 const void *linear_pair_kernel_ptr(bool a_mn, bool b_mn, bool bf16);
 
 // One 128-feature x bn-token tile per cluster of `splits` CTAs that share its k
 // (linear_split.cu).
 constexpr int kSplitThreads = 192;
+constexpr int kSplitMaxStages = 12;
 struct SplitArgs {
   LinEpilogue e;
   int m, n, nk;    // tokens, features, K blocks
@@ -138,8 +149,14 @@ struct SplitArgs {
   unsigned *err;
 };
 __host__ __device__ constexpr uint32_t split_stage_bytes(int bn) { return 16384u + uint32_t(bn) * 128u; }
-__host__ __device__ constexpr uint32_t split_smem(int bn, int stages) {
-  return 1024u + uint32_t(stages) * split_stage_bytes(bn) + 256u;
+// Each CTA of a cluster owns a share of the tile's tokens.
+__host__ __device__ constexpr int split_share(int bn, int splits) { return (bn + splits - 1) / splits; }
+// Few tokens: the partial sums go straight to their owners, into a region beside
+// the ring.  More: they go through the ring's memory.
+__host__ __device__ constexpr bool split_push(int bn, int splits) { return bn == 16 && splits > 1; }
+__host__ __device__ constexpr uint32_t split_smem(int bn, int splits, int stages) {
+  return 1024u + uint32_t(stages) * split_stage_bytes(bn) + 256u +
+         (split_push(bn, splits) ? uint32_t(splits * split_share(bn, splits)) * 512u : 0u);
 }
 const void *linear_split_kernel_ptr(bool a_mn, bool b_mn, bool bf16);
 

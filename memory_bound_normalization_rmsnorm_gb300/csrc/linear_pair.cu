@@ -1,20 +1,22 @@
 // linear_pair.cu -- large products of norm_linear_fwd / norm_linear_bwd:
-// 256 x 256 output tiles by CTA pairs, with the epilogue of linear.cuh.
+// 256 x bn output tiles by CTA pairs (bn a multiple of 32 up to 256), with the
+// epilogue of linear.cuh.
 //
 // Bound by the tensor cores (one 256 x 256 x 64 block takes a pair about 512
 // clocks; its 64 KB of operands come from L2 mostly).  A persistent grid of
 // 2-CTA clusters walks the tiles; per CTA:
-//   warp 0   TMA loads of 128 A rows and 128 B rows per stage (5 or 6 stages),
-//            counted on rank 0's barrier;
+//   warp 0   TMA loads of 128 A rows and bn / 2 B rows per stage (5 to 9
+//            stages), counted on rank 0's barrier;
 //   warp 1   (rank 0) four cta_group::2 MMAs per K block into one of two
-//            256-column accumulators in tensor memory;
+//            accumulators in tensor memory;
 //   warps 2-5  drain the other accumulator: 64 columns at a time, each warp its
 //            own 32 rows through its own swizzled output buffers and TMA
 //            stores, so that no barrier joins the four.  A residual tile is
 //            loaded into the buffer that its output leaves from, `ahead`
 //            slices earlier.
 // Rows of outputs or residuals that tensor copies cannot address (an odd row
-// length, for example) are moved by the warps, two elements per lane.
+// length, for example), and the last 32 columns of a tile that is no multiple of
+// 64 wide, are moved by the warps, two elements per lane.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -24,9 +26,8 @@ namespace gbn {
 
 namespace {
 
-constexpr uint32_t kTile = 16384;       // 128 x 64 elements
-constexpr uint32_t kStage = 2 * kTile;  // A and B
-constexpr int kMaxStages = 6;
+constexpr uint32_t kTile = 16384;  // 128 x 64 elements
+constexpr int kMaxStages = kPairMaxStages;
 constexpr int kMaxSets = 4;
 constexpr int kSliceCols = 64;
 
@@ -137,9 +138,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t *ring = smem_raw + pad;
-  uint8_t *staging = ring + p.stages * kStage;
-  // 6 stages and two buffers, or 5 and four: the same end
-  float *bias_s = reinterpret_cast<float *>(ring + 6 * kStage + 2 * kTile);
+  uint8_t *staging = ring + kPairTiles - p.bufs * kTile;  // behind the stages
+  float *bias_s = reinterpret_cast<float *>(ring + kPairTiles);
   uint64_t *full = reinterpret_cast<uint64_t *>(bias_s + 256);
   uint64_t *empty = full + kMaxStages;
   uint64_t *acc_full = empty + kMaxStages;  // [2]
@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const int stages = p.stages;
+  const uint32_t kstage = pair_stage(p.bn, BMN);  // A tile, then B tile
   Walk walk;
   walk.m_tiles = (p.m + 255) / 256;
-  walk.n_tiles = (p.n + 255) / 256;
+  walk.n_tiles = (p.n + p.bn - 1) / p.bn;
   walk.gm = p.gm;
   walk.first = blockIdx.x / 2;
   walk.step = gridDim.x / 2;
@@ -194,15 +195,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int mb, nb;
       for (int j = 0; ok && walk.at(j, mb, nb); ++j) {
         const int m0 = mb * 256 + int(rank) * 128;
-        const int n0 = nb * 256 + int(rank) * 128;
+        const int n0 = nb * p.bn + int(rank) * (p.bn / 2);
         for (int kb = 0; kb < p.nk; ++kb) {
           if (issued >= stages && !mbar_wait(&empty[s], ph ^ 1u, p.err, abort)) {
             ok = false;
             break;
           }
           const uint32_t bar = full_rank0 + uint32_t(s * 8);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
-          uint8_t *a = ring + s * kStage, *b = a + kTile;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kstage);
+          uint8_t *a = ring + s * kstage, *b = a + kTile;
           const int k0 = kb * kLinBK;
           if (AMN) {
             tma_load_2d_pair(a, &tm_a, m0, k0, bar);
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = lin_idesc(256, 256, DT == kBF16, AMN, BMN);
+      const uint32_t idesc = lin_idesc(256, p.bn, DT == kBF16, AMN, BMN);
       constexpr uint32_t astep = lin_kstep(AMN), bstep = lin_kstep(BMN);
       const uint64_t adesc0 = lin_desc(smem_addr(ring), AMN);
       const uint64_t bdesc0 = lin_desc(smem_addr(ring + kTile), BMN);
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t ad = adesc0 + uint32_t(s * int(kStage >> 4));
-          const uint64_t bd = bdesc0 + uint32_t(s * int(kStage >> 4));
+          const uint64_t ad = adesc0 + uint32_t(s) * (kstage >> 4);
+          const uint64_t bd = bdesc0 + uint32_t(s) * (kstage >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_bf16_ss_pair(d, ad + k * astep, bd + k * bstep, idesc, (kb | k) != 0);
@@ -281,43 +282,49 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int sets = p.sets, zset = sets * int(kTile);
     const uint32_t acc_empty0 = mapa_shared(acc_empty, 0);
     uint64_t *rbar = rfull + quarter * kMaxSets;
-    int lj = 0, lh = 0, loaded = 0;  // next residual slice to load: tile, slice, count
-    auto load_next = [&]() {         // lane 0
+    // A slice is whole (64 columns, moved by tensor copies) or the last 32 of a
+    // tile.
+    const auto whole = [&](int h) { return (h + 1) * kSliceCols <= p.bn; };
+    int lj = 0, lh = 0, lset = 0;  // next residual slice to load: tile, slice, set
+    auto load_next = [&]() {       // lane 0
       int mb, nb;
       if (!walk.at(lj, mb, nb)) return;
-      uint8_t *buf = staging + (loaded % sets) * kTile + t0 * 128;
-      uint64_t *bar = rbar + loaded % sets;
-      mbar_arrive_expect_tx(bar, 4096);
-      tma_load_2d(buf, &tm_r, nb * 256 + lh * kSliceCols, mb * 256 + int(rank) * 128 + t0, bar);
-      ++loaded;
-      if (++lh == 4 || nb * 256 + lh * kSliceCols >= p.n) {
+      if (whole(lh)) {
+        mbar_arrive_expect_tx(rbar + lset, 4096);
+        tma_load_2d(staging + lset * kTile + t0 * 128, &tm_r, nb * p.bn + lh * kSliceCols,
+                    mb * 256 + int(rank) * 128 + t0, rbar + lset);
+      }
+      lset = lset + 1 == sets ? 0 : lset + 1;
+      if (++lh * kSliceCols >= p.bn || nb * p.bn + lh * kSliceCols >= p.n) {
         lh = 0;
         ++lj;
       }
     };
     if (pre && lane == 0)
       for (int i = 0; i < p.ahead; ++i) load_next();
-    int slice = 0;
+    uint32_t rphase = 0;  // per set: parity of its next load
+    int set = 0;
     int mb, nb;
     for (int j = 0; walk.at(j, mb, nb); ++j) {
       const int b = j & 1;
       const int row0 = mb * 256 + int(rank) * 128 + t0;
-      const int n0 = nb * 256;
+      const int n0 = nb * p.bn;
       mbar_wait(&acc_full[b], (j >> 1) & 1, p.err, abort);
       if (e.bias) {
         named_bar_sync(1, 128);  // the last tile's values have been read
         for (int c = t; c < 256; c += 128)
-          bias_s[c] = n0 + c < p.n ? load_elem<DT>(e.bias, n0 + c) : 0.f;
+          bias_s[c] = c < p.bn && n0 + c < p.n ? load_elem<DT>(e.bias, n0 + c) : 0.f;
         named_bar_sync(1, 128);
       }
       __syncwarp();
       tc_fence_after();
       const uint32_t t_lane = tmem + (uint32_t(t0) << 16) + uint32_t(b * 256);
 #pragma unroll 1
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h * kSliceCols < p.bn; ++h) {
         const int col = n0 + h * kSliceCols;
         if (col >= p.n) break;
-        const int set = slice % sets;
+        const int cols_end = min(p.n, n0 + p.bn);
+        const bool by_tma = whole(h);
         uint8_t *ybuf = staging + set * kTile;
         uint8_t *zbuf = e.z ? ybuf + zset : nullptr;
         if (lane == 0) {
@@ -332,14 +339,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t acc[2][32];
         tmem_ld32(t_lane + h * kSliceCols, acc[0]);
         tmem_ld32(t_lane + h * kSliceCols + 32, acc[1]);
-        if (pre)
-          mbar_wait(&rbar[set], (slice / sets) & 1, p.err, abort);
-        else if (has_r)
-          copy_rows<true>(ybuf, t0, const_cast<void *>(e.r), e.ldr, row0, p.m, col, p.n);
+        if (pre && by_tma) {
+          mbar_wait(&rbar[set], (rphase >> set) & 1, p.err, abort);
+          rphase ^= 1u << set;
+        } else if (has_r) {
+          copy_rows<true>(ybuf, t0, const_cast<void *>(e.r), e.ldr, row0, p.m, col, cols_end);
+        }
         __syncwarp();
         tmem_wait_ld(acc[0]);
         tmem_wait_ld(acc[1]);
-        if (h == 3 || col + kSliceCols >= p.n) {  // this accumulator is read
+        if (col + kSliceCols >= cols_end) {  // this accumulator is read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -361,22 +370,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && row0 < p.m) {
+        if (lane == 0 && row0 < p.m && by_tma) {
           if (p.tma_y) tma_store_2d(&tm_y, col, row0, ybuf + t0 * 128);
           if (zbuf && p.tma_z) tma_store_2d(&tm_z, col, row0, zbuf + t0 * 128);
         }
         if (lane == 0) bulk_commit();
-        if (!p.tma_y) copy_rows<false>(ybuf, t0, e.y, e.ldy, row0, p.m, col, p.n);
-        if (zbuf && !p.tma_z) copy_rows<false>(zbuf, t0, e.z, e.ldz, row0, p.m, col, p.n);
-        ++slice;
+        if (!p.tma_y || !by_tma) copy_rows<false>(ybuf, t0, e.y, e.ldy, row0, p.m, col, cols_end);
+        if (zbuf && !(p.tma_z && by_tma))
+          copy_rows<false>(zbuf, t0, e.z, e.ldz, row0, p.m, col, cols_end);
+        set = set + 1 == sets ? 0 : set + 1;
       }
     }
     if (lane == 0) {
-      // residual tiles that a lost wait left behind, then the stores
-      if (pre) {
-        volatile int never = 0;
-        for (int i = slice; i < loaded; ++i) mbar_wait(&rbar[i % sets], (i / sets) & 1, p.err, &never);
-      }
       bulk_wait_all();
     }
     __syncwarp();

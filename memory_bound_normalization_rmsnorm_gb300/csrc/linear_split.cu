@@ -2,18 +2,21 @@
 // middling rows (tokens): 128 output features x `bn` tokens per cluster, whose
 // CTAs share the contraction.
 //
-// Few tokens: bound by reading the weights once.  The weights are the MMA's
-// 128-row operand and the tokens its columns (16 at least), so a tile of W
+// Few tokens: bound by reading the weights once, and for one layer alone by the
+// way from launch to first byte and from last byte to result.  The weights are the
+// MMA's 128-row operand and the tokens its columns (16 at least), so a tile of W
 // feeds the tensor core whatever the number of tokens, and a layer of 4096
 // features has 32 tiles: the contraction is cut into up to 8 parts to keep
-// every SM's copies in flight.  Each CTA streams its part of W and x by TMA
-// (every stage in flight from the start where they all fit), leaves its fp32
-// partial sums in its own shared memory, frees its tensor memory and meets the
-// cluster; then each CTA adds the partials of its share of the tokens over
-// distributed shared memory in rank order (no atomics) and writes them with
-// the epilogue, whole 256-byte rows per warp.  A CTA holds no tensor memory
-// while it waits for a peer, so clusters of different streams cannot block each
-// other.
+// every SM's copies in flight.  Each CTA streams its part of W and x by TMA (the
+// first stages before anything else is set up).  The tile's tokens are shared out
+// among the CTAs, which add the fp32 partial sums of theirs in rank order (no
+// atomics) and write them with the epilogue, whole 256-byte rows per warp.  Up to
+// 16 tokens go from tensor memory straight to their owners over distributed
+// shared memory, behind one cluster barrier; more go through the CTA's own shared
+// memory (the ring's) and are fetched in 16-byte pieces, behind two (64 tokens by
+// single words: 17 us where this takes 12).  A CTA holds no tensor memory while it
+// waits for a peer that might wait for some, so clusters of different streams
+// cannot block each other.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -23,7 +26,7 @@ namespace gbn {
 
 namespace {
 
-__device__ __forceinline__ float4 ld_peer(uint32_t local, uint32_t rank) {
+__device__ __forceinline__ float4 ld_peer(uint32_t local, int rank) {
   uint32_t remote;
   float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
@@ -32,6 +35,9 @@ __device__ __forceinline__ float4 ld_peer(uint32_t local, uint32_t rank) {
                : "r"(remote)
                : "memory");
   return v;
+}
+__device__ __forceinline__ void st_peer(uint32_t remote, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
 }
 
 // Four consecutive elements (fewer at the end of a row).
@@ -67,15 +73,19 @@ __global__ void __launch_bounds__(kSplitThreads)
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t *ring = smem_raw + pad;
   const uint32_t stage_bytes = split_stage_bytes(p.bn);
+  const int splits = p.splits;
+  const int share = split_share(p.bn, splits);
+  const bool push = split_push(p.bn, splits);
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + p.stages * stage_bytes);
-  uint64_t *empty = full + 12;
-  uint64_t *acc = empty + 12;  // every MMA of the CTA finished
+  // received: [rank][share][128 features]; or this CTA's: [token][128], in the ring
+  float *part = reinterpret_cast<float *>(push ? reinterpret_cast<uint8_t *>(full) + 256 : ring);
+  uint64_t *empty = full + kSplitMaxStages;
+  uint64_t *acc = empty + kSplitMaxStages;  // every MMA of the CTA finished
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  const int splits = p.splits;
   const int rank = splits > 1 ? int(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / splits;
   const int j0 = (tile % p.tiles_j) * p.bn;  // first token
@@ -83,8 +93,29 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int kb0 = int(int64_t(p.nk) * rank / splits), kb1 = int(int64_t(p.nk) * (rank + 1) / splits);
   const int nkb = kb1 - kb0;
   const int stages = p.stages;
+  const int tokens = min(p.bn, p.m - j0);
+
+  // Fetches K block kb0 + n into stage s.
+  const auto fetch = [&](int n, int s) {
+    mbar_arrive_expect_tx(&full[s], stage_bytes);
+    uint8_t *b = ring + s * stage_bytes, *a = b + 16384;
+    const int k0 = (kb0 + n) * kLinBK;
+    if (BMN) {
+      tma_load_2d(b, &tm_b, i0, k0, &full[s]);
+      tma_load_2d(b + 8192, &tm_b, i0 + 64, k0, &full[s]);
+    } else {
+      tma_load_2d(b, &tm_b, k0, i0, &full[s]);
+    }
+    if (AMN) {
+      for (int c = 0; c < p.bn; c += 64) tma_load_2d(a + c * 128, &tm_a, j0 + c, k0, &full[s]);
+    } else {
+      tma_load_2d(a, &tm_a, k0, j0, &full[s]);
+    }
+  };
 
   if (threadIdx.x == 0) {
+    prefetch_tensor_map(&tm_a);
+    prefetch_tensor_map(&tm_b);
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -92,8 +123,13 @@ __global__ void __launch_bounds__(kSplitThreads)
     mbar_init(acc, 1);
     *abort = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
   }
+  __syncwarp();
+  if (splits > 1) cluster_arrive_release();  // this CTA runs: peers may write to it
   grid_dependency_wait();  // before tensor memory is taken: never held while waiting
+  if (threadIdx.x == 0)
+    for (int n = 0; n < stages && n < nkb; ++n) fetch(n, n);
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem);
     tmem_relinquish();
@@ -104,39 +140,31 @@ __global__ void __launch_bounds__(kSplitThreads)
   grid_launch_dependents();
   const uint32_t tmem = *tmem_slot;
 
+  // The epilogue's first operands, fetched while the products run: this CTA owns
+  // tokens ja .. jb - 1 of the tile, a warp per token, four features per lane.
+  const LinEpilogue &e = p.e;
+  const bool vec = p.vec;
+  const int ja = min(tokens, rank * share), jb = min(tokens, ja + share);
+  const int i = i0 + lane * 4;
+  const int count = min(4, p.n - i);
+  float bias[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
+  const auto load_r = [&](int j) {
+    if (e.r && count > 0 && j < jb) load4<DT>(e.r, int64_t(j0 + j) * e.ldr + i, count, vec, r);
+  };
+
   if (warp == 0) {
     if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (issued >= stages && !mbar_wait(&empty[s], ph ^ 1u, p.err, abort)) break;
-        mbar_arrive_expect_tx(&full[s], stage_bytes);
-        uint8_t *b = ring + s * stage_bytes, *a = b + 16384;
-        const int k0 = kb * kLinBK;
-        if (BMN) {
-          tma_load_2d(b, &tm_b, i0, k0, &full[s]);
-          tma_load_2d(b + 8192, &tm_b, i0 + 64, k0, &full[s]);
-        } else {
-          tma_load_2d(b, &tm_b, k0, i0, &full[s]);
-        }
-        if (AMN) {
-          for (int c = 0; c < p.bn; c += 64)
-            tma_load_2d(a + c * 128, &tm_a, j0 + c, k0, &full[s]);
-        } else {
-          tma_load_2d(a, &tm_a, k0, j0, &full[s]);
-        }
-        ++issued;
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1u;
-        }
+      int issued = min(stages, nkb);
+      for (; issued < nkb; ++issued) {
+        const int s = issued % stages;
+        if (!mbar_wait(&empty[s], (issued / stages - 1) & 1, p.err, abort)) break;
+        fetch(issued, s);
       }
-      // every copy has landed before the ring is used for the partial sums
+      // No copy may still be landing when the CTA exits.
       volatile int never = 0;
-      for (int i = 0; i < stages && i < issued; ++i) {
-        const int loads = (issued - i + stages - 1) / stages;
-        mbar_wait(&full[i], (loads - 1) & 1, p.err, &never);
+      for (int s = 0; s < stages && s < issued; ++s) {
+        const int loads = (issued - s + stages - 1) / stages;
+        mbar_wait(&full[s], (loads - 1) & 1, p.err, &never);
       }
     }
     __syncwarp();
@@ -165,61 +193,72 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     __syncwarp();
   }
-  __syncthreads();  // warp 0's copies have landed
-  // Partial sums [token][128 features] into the ring, once all MMAs have read it.
-  float *part = reinterpret_cast<float *>(ring);
+  if (e.bias && count > 0) load4<DT>(e.bias, i, count, vec, bias);
+  load_r(ja + warp);
+  __syncwarp();
+  if (splits > 1) cluster_wait_acquire();  // every CTA of the cluster runs
   if (warp >= 2) {
     mbar_wait(acc, 0, p.err, abort);
     __syncwarp();
     tc_fence_after();
     const int t0 = (warp & 3) * 32;
     const uint32_t t_lane = tmem + (uint32_t(t0) << 16);
-    for (int c = 0; c < p.bn; c += 16) {
+    if (push) {
       uint32_t v[16];
-      tmem_ld_n<16>(t_lane + c, v);
+      tmem_ld_n<16>(t_lane, v);
       tmem_wait_ld_n<16>(v);
+      float *const mine = part + rank * share * 128 + t0 + lane;
+      int owner = 0, at = 0;  // of token q: its CTA, and its row there
+      uint32_t to = mapa_shared(mine, 0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c + i) * 128 + t0 + lane] = __uint_as_float(v[i]);
+      for (int q = 0; q < 16; ++q) {
+        if (q < tokens) {
+          st_peer(to + uint32_t(at) * 512u, v[q]);
+          if (++at == share && ++owner < splits) {
+            at = 0;
+            to = mapa_shared(mine, owner);
+          }
+        }
+      }
+    } else {
+      for (int c = 0; c < tokens; c += 16) {
+        uint32_t v[16];
+        tmem_ld_n<16>(t_lane + c, v);
+        tmem_wait_ld_n<16>(v);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) part[(c + q) * 128 + t0 + lane] = __uint_as_float(v[q]);
+      }
     }
     tc_fence_before();
   }
+  __syncwarp();
+  if (splits > 1) cluster_arrive_release();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 1) {  // every read of it is done; freed before the peers are waited for
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem);
   }
-  if (splits > 1) cluster_sync();
+  if (splits > 1) cluster_wait_acquire();
 
-  // This CTA's share of the tile's tokens, a warp per token, four features per
-  // lane.
-  const LinEpilogue &e = p.e;
-  const int tokens = min(p.bn, p.m - j0);
-  const int ja = tokens * rank / splits, jb = tokens * (rank + 1) / splits;
-  const int i = i0 + lane * 4;
-  const int count = min(4, p.n - i);
   if (count > 0) {
-    const bool vec = p.vec;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (e.bias) load4<DT>(e.bias, i, count, vec, bias);
     for (int j = ja + warp; j < jb; j += kSplitThreads / 32) {
       const int64_t row = j0 + j;
-      float r[4] = {0.f, 0.f, 0.f, 0.f};
-      if (e.r) load4<DT>(e.r, row * e.ldr + i, count, vec, r);
-      const uint32_t at = smem_addr(part + j * 128 + lane * 4);
-      float f[4];
-      if (splits == 1) {
-        const float4 v = *reinterpret_cast<const float4 *>(part + j * 128 + lane * 4);
-        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-      } else {
-        float4 v[8];
+      float4 v[8];
+      if (push || splits == 1) {
+        const float *src = part + (j - ja) * 128 + lane * 4;  // (one CTA owns all: ja = 0)
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-          if (s < splits) v[s] = ld_peer(at, uint32_t(s));
-        f[0] = v[0].x, f[1] = v[0].y, f[2] = v[0].z, f[3] = v[0].w;
+          if (s < splits) v[s] = *reinterpret_cast<const float4 *>(src + s * share * 128);
+      } else {
+        const uint32_t src = smem_addr(part + j * 128 + lane * 4);
 #pragma unroll
-        for (int s = 1; s < 8; ++s)
-          if (s < splits) f[0] += v[s].x, f[1] += v[s].y, f[2] += v[s].z, f[3] += v[s].w;
+        for (int s = 0; s < 8; ++s)
+          if (s < splits) v[s] = ld_peer(src, s);
       }
+      float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int s = 1; s < 8; ++s)
+        if (s < splits) f[0] += v[s].x, f[1] += v[s].y, f[2] += v[s].z, f[3] += v[s].w;
 #pragma unroll
       for (int q = 0; q < 4; ++q) f[q] += bias[q];
       if (e.z) store4<DT>(e.z, row * e.ldz + i, count, vec, f);
@@ -231,10 +270,13 @@ __global__ void __launch_bounds__(kSplitThreads)
                r[q];
       }
       store4<DT>(e.y, row * e.ldy + i, count, vec, f);
+      load_r(j + kSplitThreads / 32);
     }
   }
-  __syncwarp();
-  if (splits > 1) cluster_sync();  // peers may still read this CTA's partials
+  if (splits > 1 && !push) {  // peers may still read this CTA's partials
+    __syncwarp();
+    cluster_sync();
+  }
 }
 
 template <bool AMN, bool BMN>

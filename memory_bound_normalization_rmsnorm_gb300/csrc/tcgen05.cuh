@@ -29,6 +29,11 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int c0,
       : "memory");
 }
 
+// Fetches a tensor map (a kernel parameter) ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensor_map(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // The same load with an L2 eviction-priority policy (createpolicy).
 __device__ __forceinline__ void tma_load_2d_hint(void *dst, const void *tmap, int c0, int c1,
                                                  uint64_t *bar, uint64_t policy) {

@@ -146,9 +146,10 @@ def test_both_directions(dtype, name, shape):
     assert gb.norm_get_device_error() == 0
 
 
-FORMS = ["pair=1"] + [f"pair=0,bn={b},splits={s}" for b, s in
-                      ((16, 1), (16, 8), (32, 3), (48, 2), (64, 5), (64, 1), (128, 2), (128, 7),
-                       (192, 1), (256, 1), (256, 4))]
+FORMS = [f"pair=1,bn={b}" for b in (64, 96, 128, 160, 192, 224, 256)]
+FORMS += [f"pair=0,bn={b},splits={s}" for b, s in
+          ((16, 1), (16, 8), (32, 3), (48, 2), (64, 5), (64, 1), (80, 6), (112, 4), (128, 1),
+           (128, 2), (128, 7), (192, 1), (256, 4))]
 
 
 @pytest.mark.gpu
