@@ -159,8 +159,7 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     p.bn = plan.bn;
     p.bufs = e.r || e.z ? 4 : 2;
     p.stages = pair_stages(p.bn, b_mn, p.bufs);
-    p.sets = e.r && !e.z ? 4 : 2;
-    p.ahead = p.sets / 2;
+    p.sets = p.bufs / 2 / (e.z ? 2 : 1);
     p.gm = 8;
     p.err = d.err;
     CUtensorMap ty = ta, tz = ta, tr = ta;

@@ -106,15 +106,14 @@ __device__ __forceinline__ uint32_t lin_pack(float a, float b) {
 
 // ------------------------------------------------------------- kernels
 // Output tiles of 256 x bn by CTA pairs, persistent (linear_pair.cu).
-constexpr int kPairThreads = 192;
+constexpr int kPairThreads = 320;
 struct PairArgs {
   LinEpilogue e;
   int m, n, nk;
   int bn;       // tile columns: a multiple of 32, up to 256
   int stages;   // operand stages
   int bufs;     // 16 KB output buffers: 2 or 4
-  int sets;     // output buffers (pairs of them where z is written) used in turn
-  int ahead;    // slices that r is loaded ahead
+  int sets;     // of them a warp's slices use in turn (pairs where z is written): 1 or 2
   int tma_y, tma_z, tma_r;  // moved by tensor copies (else by the warps)
   int gm;       // row blocks per group of the tile walk
   unsigned *err;

@@ -9,11 +9,11 @@
 //            stages), counted on rank 0's barrier;
 //   warp 1   (rank 0) four cta_group::2 MMAs per K block into one of two
 //            accumulators in tensor memory;
-//   warps 2-5  drain the other accumulator: 64 columns at a time, each warp its
-//            own 32 rows through its own swizzled output buffers and TMA
-//            stores, so that no barrier joins the four.  A residual tile is
-//            loaded into the buffer that its output leaves from, `ahead`
-//            slices earlier.
+//   warps 2-9  drain the other accumulator: 64 columns at a time, two warps per
+//            32 rows taking them in turn, each through its own swizzled output
+//            buffers and TMA stores, so that no barrier joins the eight.  A
+//            residual tile is loaded into the buffer that its output leaves
+//            from, a slice of the warp earlier where there are two buffers.
 // Rows of outputs or residuals that tensor copies cannot address (an odd row
 // length, for example), and the last 32 columns of a tile that is no multiple of
 // 64 wide, are moved by the warps, two elements per lane.
@@ -28,16 +28,14 @@ namespace {
 
 constexpr uint32_t kTile = 16384;  // 128 x 64 elements
 constexpr int kMaxStages = kPairMaxStages;
-constexpr int kMaxSets = 4;
+constexpr int kMaxSets = 2;  // output buffers (pairs with z) of a warp
 constexpr int kSliceCols = 64;
 
 __device__ __forceinline__ void wait_read(int left) {
   if (left == 0)
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  else if (left == 1)
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    bulk_wait_read_all();
   else
-    asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+    bulk_wait_read_but_one();
 }
 
 // Tiles in groups of gm row blocks, column by column within a group, so that
@@ -145,8 +143,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t *acc_full = empty + kMaxStages;  // [2]
   uint64_t *acc_empty = acc_full + 2;       // [2]
   uint64_t *done = acc_empty + 2;
-  uint64_t *rfull = done + 1;               // [4 warps][kMaxSets]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rfull + 4 * kMaxSets);
+  uint64_t *rfull = done + 1;               // [8 warps][kMaxSets]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rfull + 8 * kMaxSets);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32;
@@ -169,10 +167,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);  // four warps of each CTA
+      mbar_init(&acc_empty[b], 16);  // eight warps of each CTA
     }
     mbar_init(done, 1);
-    for (int i = 0; i < 4 * kMaxSets; ++i) mbar_init(&rfull[i], 1);
+    for (int i = 0; i < 8 * kMaxSets; ++i) mbar_init(&rfull[i], 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -274,34 +272,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     __syncwarp();
   } else {
-    // Warps 2 .. 5 reach tensor-memory lanes 32 (warp % 4) .. + 31.
-    const int quarter = warp & 3;
+    // Warp w reaches tensor-memory lanes 32 (w % 4) .. + 31.
+    const int quarter = warp & 3, half = (warp - 2) / 4;
     const int t0 = quarter * 32, t = t0 + lane;
     const LinEpilogue &e = p.e;
     const bool has_r = e.r != nullptr, pre = has_r && p.tma_r;
-    const int sets = p.sets, zset = sets * int(kTile);
+    const int sets = p.sets, ahead = sets - 1;
+    uint8_t *const bufs = staging + half * (p.bufs / 2) * int(kTile);  // this half's
+    const int zset = sets * int(kTile);
     const uint32_t acc_empty0 = mapa_shared(acc_empty, 0);
-    uint64_t *rbar = rfull + quarter * kMaxSets;
+    uint64_t *rbar = rfull + (warp - 2) * kMaxSets;
     // A slice is whole (64 columns, moved by tensor copies) or the last 32 of a
-    // tile.
+    // tile; the warp takes every other one.
     const auto whole = [&](int h) { return (h + 1) * kSliceCols <= p.bn; };
-    int lj = 0, lh = 0, lset = 0;  // next residual slice to load: tile, slice, set
-    auto load_next = [&]() {       // lane 0
+    const auto in_tile = [&](int h, int nb) {
+      return h * kSliceCols < p.bn && nb * p.bn + h * kSliceCols < p.n;
+    };
+    int lj = 0, lh = half, lset = 0;  // next residual slice to load: tile, slice, set
+    auto load_next = [&]() {          // lane 0
       int mb, nb;
-      if (!walk.at(lj, mb, nb)) return;
+      for (;; ++lj, lh = half) {
+        if (!walk.at(lj, mb, nb)) return;
+        if (in_tile(lh, nb)) break;
+      }
       if (whole(lh)) {
         mbar_arrive_expect_tx(rbar + lset, 4096);
-        tma_load_2d(staging + lset * kTile + t0 * 128, &tm_r, nb * p.bn + lh * kSliceCols,
+        tma_load_2d(bufs + lset * kTile + t0 * 128, &tm_r, nb * p.bn + lh * kSliceCols,
                     mb * 256 + int(rank) * 128 + t0, rbar + lset);
       }
       lset = lset + 1 == sets ? 0 : lset + 1;
-      if (++lh * kSliceCols >= p.bn || nb * p.bn + lh * kSliceCols >= p.n) {
-        lh = 0;
-        ++lj;
-      }
+      lh += 2;
     };
     if (pre && lane == 0)
-      for (int i = 0; i < p.ahead; ++i) load_next();
+      for (int i = 0; i < ahead; ++i) load_next();
     uint32_t rphase = 0;  // per set: parity of its next load
     int set = 0;
     int mb, nb;
@@ -311,25 +314,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int n0 = nb * p.bn;
       mbar_wait(&acc_full[b], (j >> 1) & 1, p.err, abort);
       if (e.bias) {
-        named_bar_sync(1, 128);  // the last tile's values have been read
-        for (int c = t; c < 256; c += 128)
-          bias_s[c] = c < p.bn && n0 + c < p.n ? load_elem<DT>(e.bias, n0 + c) : 0.f;
-        named_bar_sync(1, 128);
+        named_bar_sync(1, 256);  // the last tile's values have been read
+        const int c = threadIdx.x - 64;
+        bias_s[c] = c < p.bn && n0 + c < p.n ? load_elem<DT>(e.bias, n0 + c) : 0.f;
+        named_bar_sync(1, 256);
       }
       __syncwarp();
       tc_fence_after();
       const uint32_t t_lane = tmem + (uint32_t(t0) << 16) + uint32_t(b * 256);
+      const auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0)
+            mbar_arrive(&acc_empty[b]);
+          else
+            mbar_arrive_remote(acc_empty0 + uint32_t(b * 8));
+        }
+      };
+      if (!in_tile(half, nb)) release();
 #pragma unroll 1
-      for (int h = 0; h * kSliceCols < p.bn; ++h) {
+      for (int h = half; in_tile(h, nb); h += 2) {
         const int col = n0 + h * kSliceCols;
-        if (col >= p.n) break;
         const int cols_end = min(p.n, n0 + p.bn);
         const bool by_tma = whole(h);
-        uint8_t *ybuf = staging + set * kTile;
+        uint8_t *ybuf = bufs + set * kTile;
         uint8_t *zbuf = e.z ? ybuf + zset : nullptr;
         if (lane == 0) {
           if (pre) {
-            wait_read(sets - 1 - p.ahead);
+            wait_read(0);
             load_next();
           } else {
             wait_read(sets - 1);
@@ -348,25 +361,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         tmem_wait_ld(acc[0]);
         tmem_wait_ld(acc[1]);
-        if (col + kSliceCols >= cols_end) {  // this accumulator is read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (rank == 0)
-              mbar_arrive(&acc_empty[b]);
-            else
-              mbar_arrive_remote(acc_empty0 + uint32_t(b * 8));
-          }
-        }
+        if (!in_tile(h + 2, nb)) release();  // this warp has read its slices
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float *bs = e.bias ? bias_s + h * kSliceCols + half * 32 : nullptr;
+        for (int q = 0; q < 2; ++q) {
+          const float *bs = e.bias ? bias_s + h * kSliceCols + q * 32 : nullptr;
           if (e.act == kLinNone)
-            finish32<DT, kLinNone>(acc[half], bs, half * 4, t, ybuf, zbuf, has_r);
+            finish32<DT, kLinNone>(acc[q], bs, q * 4, t, ybuf, zbuf, has_r);
           else if (e.act == kLinSilu)
-            finish32<DT, kLinSilu>(acc[half], bs, half * 4, t, ybuf, zbuf, has_r);
+            finish32<DT, kLinSilu>(acc[q], bs, q * 4, t, ybuf, zbuf, has_r);
           else
-            finish32<DT, kLinGelu>(acc[half], bs, half * 4, t, ybuf, zbuf, has_r);
+            finish32<DT, kLinGelu>(acc[q], bs, q * 4, t, ybuf, zbuf, has_r);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -381,9 +385,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         set = set + 1 == sets ? 0 : set + 1;
       }
     }
-    if (lane == 0) {
-      bulk_wait_all();
-    }
+    if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
 
