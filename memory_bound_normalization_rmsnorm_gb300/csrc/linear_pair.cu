@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rfull + 8 * kMaxSets);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32;
+  const int warp = warp_index();
   const int lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const int stages = p.stages;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc = lin_idesc(256, p.bn, DT == kBF16, AMN, BMN);
       constexpr uint32_t astep = lin_kstep(AMN), bstep = lin_kstep(BMN);
       const uint64_t adesc0 = lin_desc(smem_addr(ring), AMN);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       return h * kSliceCols < p.bn && nb * p.bn + h * kSliceCols < p.n;
     };
     int lj = 0, lh = half, lset = 0;  // next residual slice to load: tile, slice, set
-    auto load_next = [&]() {          // lane 0
+    auto load_next = [&]() {          // one lane
       int mb, nb;
       for (;; ++lj, lh = half) {
         if (!walk.at(lj, mb, nb)) return;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       lset = lset + 1 == sets ? 0 : lset + 1;
       lh += 2;
     };
-    if (pre && lane == 0)
+    if (pre && elect_one())
       for (int i = 0; i < ahead; ++i) load_next();
     uint32_t rphase = 0;  // per set: parity of its next load
     int set = 0;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
+        if (elect_one()) {
           if (rank == 0)
             mbar_arrive(&acc_empty[b]);
           else
@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const bool by_tma = whole(h);
         uint8_t *ybuf = bufs + set * kTile;
         uint8_t *zbuf = e.z ? ybuf + zset : nullptr;
-        if (lane == 0) {
+        __syncwarp();
+        if (elect_one()) {
           if (pre) {
             wait_read(0);
             load_next();
@@ -374,18 +375,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && row0 < p.m && by_tma) {
-          if (p.tma_y) tma_store_2d(&tm_y, col, row0, ybuf + t0 * 128);
-          if (zbuf && p.tma_z) tma_store_2d(&tm_z, col, row0, zbuf + t0 * 128);
+        if (elect_one()) {
+          if (row0 < p.m && by_tma) {
+            if (p.tma_y) tma_store_2d(&tm_y, col, row0, ybuf + t0 * 128);
+            if (zbuf && p.tma_z) tma_store_2d(&tm_z, col, row0, zbuf + t0 * 128);
+          }
+          bulk_commit();
         }
-        if (lane == 0) bulk_commit();
         if (!p.tma_y || !by_tma) copy_rows<false>(ybuf, t0, e.y, e.ldy, row0, p.m, col, cols_end);
         if (zbuf && !(p.tma_z && by_tma))
           copy_rows<false>(zbuf, t0, e.z, e.ldz, row0, p.m, col, cols_end);
         set = set + 1 == sets ? 0 : set + 1;
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (elect_one()) bulk_wait_all();
     __syncwarp();
   }
 

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc + 1);
   volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-  const int warp = threadIdx.x / 32;
+  const int warp = warp_index();
   const int lane = threadIdx.x % 32;
   const int rank = splits > 1 ? int(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / splits;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
   };
 
-  if (threadIdx.x == 0) {
+  if (warp == 0 && elect_one()) {
     prefetch_tensor_map(&tm_a);
     prefetch_tensor_map(&tm_b);
     for (int s = 0; s < stages; ++s) {
@@ -128,8 +128,11 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncwarp();
   if (splits > 1) cluster_arrive_release();  // this CTA runs: peers may write to it
   grid_dependency_wait();  // before tensor memory is taken: never held while waiting
-  if (threadIdx.x == 0)
-    for (int n = 0; n < stages && n < nkb; ++n) fetch(n, n);
+  if (warp == 0) {
+    if (elect_one())
+      for (int n = 0; n < stages && n < nkb; ++n) fetch(n, n);
+    __syncwarp();
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem);
     tmem_relinquish();
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int issued = min(stages, nkb);
       for (; issued < nkb; ++issued) {
         const int s = issued % stages;
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // rows of the accumulator: features; columns: tokens
       const uint32_t idesc = lin_idesc(128, p.bn, DT == kBF16, BMN, AMN);
       constexpr uint32_t astep = lin_kstep(AMN), bstep = lin_kstep(BMN);

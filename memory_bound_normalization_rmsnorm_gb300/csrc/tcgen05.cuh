@@ -108,6 +108,23 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp.  Branching on this instead of on the lane's
+// number tells the compiler that the branch is taken by one thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+// This thread's warp, as a value that is the same across the warp for the
+// compiler too.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
+}
+
 // ------------------------------------------------------------- the MMA
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D, both
 // operands K-major, tile M x N (M in {64, 128}, N a multiple of 16 up to
