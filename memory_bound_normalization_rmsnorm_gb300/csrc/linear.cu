@@ -7,6 +7,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 
 #include "../../include/gbnorm.h"
@@ -63,63 +64,43 @@ struct ProductPlan {
 
 int round_up(int64_t v, int to) { return static_cast<int>((v + to - 1) / to * to); }
 
-ProductPlan plan_product(int64_t m, int64_t n, int64_t k, bool a_mn, const Device &d) {
-  const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
-  ProductPlan p;
-  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  p.pair = pair_tiles >= d.sms / 4;
-  const int unit = a_mn ? 64 : 16;
-  int pair_bn = 256;
-  p.bn = m >= 128 ? 128 : round_up(m, unit);
-  const int64_t tiles = ((m + p.bn - 1) / p.bn) * ((n + 127) / 128);
-  int s = static_cast<int>((2 * d.sms) / tiles);
-  s = s < 1 ? 1 : s > 8 ? 8 : s;
-  p.splits = s > nk ? nk : s;
-  // GBNORM_LINEAR="pair=0,bn=64,splits=4" forces fields (for sweeps)
-  if (const char *o = std::getenv("GBNORM_LINEAR")) {
-    if (const char *q = std::strstr(o, "pair=")) p.pair = std::atoi(q + 5) != 0;
-    if (const char *q = std::strstr(o, "bn=")) {
-      const int bn = std::atoi(q + 3);
-      if (bn >= unit && bn <= 256 && bn % unit == 0) p.bn = bn;
-      if (bn >= 64 && bn <= 256 && bn % 32 == 0) pair_bn = bn;
-    }
-    if (const char *q = std::strstr(o, "splits=")) {
-      const int f = std::atoi(q + 7);
-      if (f >= 1 && f <= 8) p.splits = f > nk ? nk : f;
-    }
-  }
-  if (p.pair) {
-    p.bn = pair_bn;
-    return p;
-  }
-  // As many stages as there are K blocks, or as leave room for two CTAs per SM
-  // where that makes four; the ring also takes the partial sums of all tokens.
-  const int nkb = (nk + p.splits - 1) / p.splits;
-  const uint32_t sb = split_stage_bytes(p.bn), fixed = split_smem(p.bn, p.splits, 0);
-  int most = static_cast<int>((uint32_t(d.optin) / 2 - 1024 - fixed) / sb);
-  if (most < 4) most = static_cast<int>((uint32_t(d.optin) - fixed) / sb);
+// As many stages as there are K blocks, or as leave room for two CTAs per SM
+// where that makes four; the ring also takes the partial sums of all tokens.
+int split_stages(int nk, int bn, int splits, int optin) {
+  const int nkb = (nk + splits - 1) / splits;
+  const uint32_t sb = split_stage_bytes(bn), fixed = split_smem(bn, splits, 0);
+  int most = static_cast<int>((uint32_t(optin) / 2 - 1024 - fixed) / sb);
+  if (most < 4) most = static_cast<int>((uint32_t(optin) - fixed) / sb);
   if (most > kSplitMaxStages) most = kSplitMaxStages;
-  p.stages = nkb < most ? nkb : most;
-  const int least = static_cast<int>((uint32_t(p.bn) * 512u + sb - 1) / sb);
-  if (!split_push(p.bn, p.splits) && p.stages < least) p.stages = least;
-  return p;
+  int stages = nkb < most ? nkb : most;
+  const int least = static_cast<int>((uint32_t(bn) * 512u + sb - 1) / sb);
+  if (!split_push(bn, splits) && stages < least) stages = least;
+  return stages;
 }
 
-std::mutex g_pairs_mu;
-std::map<std::pair<int, const void *>, int> g_pairs;  // co-resident CTA pairs
+uint32_t tmem_columns(int bn) {
+  uint32_t c = 32;
+  while (c < uint32_t(bn)) c *= 2;
+  return c;
+}
 
-norm_status_t resident_pairs(const Device &d, const void *fn, int *out) {
-  std::lock_guard<std::mutex> lk(g_pairs_mu);
-  auto it = g_pairs.find({d.dev, fn});
-  if (it == g_pairs.end()) {
+std::mutex g_plan_mu;
+std::map<std::tuple<const void *, int, uint32_t>, int> g_resident;  // per SM (cluster 1) or clusters
+
+// Clusters of `cluster` CTAs of kernel fn that are resident at once.
+norm_status_t resident(const Device &d, const void *fn, int threads, int cluster, uint32_t smem,
+                       int *out) {
+  std::lock_guard<std::mutex> lk(g_plan_mu);
+  auto it = g_resident.find({fn, cluster * 64 + d.dev, smem});
+  if (it == g_resident.end()) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.x = unsigned(cluster);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(d.sms - d.sms % 2));
-    cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = pair_smem();
+    cfg.gridDim = dim3(unsigned(cluster) * 1024u);
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
@@ -127,10 +108,130 @@ norm_status_t resident_pairs(const Device &d, const void *fn, int *out) {
       cudaGetLastError();
       return NORM_ERR_CUDA;
     }
-    if (n < 1) return NORM_ERR_UNSUPPORTED;
-    it = g_pairs.emplace(std::make_pair(d.dev, fn), n).first;
+    it = g_resident.emplace(std::make_tuple(fn, cluster * 64 + d.dev, smem), n).first;
   }
   *out = it->second;
+  return *out < 1 ? NORM_ERR_UNSUPPORTED : NORM_OK;
+}
+
+// Estimated microseconds of the two forms.  The constants were fitted to 830
+// measured (form, size) pairs of 52 sizes (1 to 16384 rows, forward and both
+// gradients, operands not in L2); on these sizes the form of least estimate is
+// 3 % slower than the fastest measured one in the geometric mean, 28 % at worst.
+// No size was held back.
+double pair_time(int64_t m, int64_t n, int nk, int bn, bool b_mn, int pairs) {
+  const int64_t tiles = ((m + 255) / 256) * ((n + bn - 1) / bn);
+  const double waves = double((tiles + pairs - 1) / pairs);
+  double kb = 0.0289 + 0.001076 * bn;         // per K block: the MMAs
+  if (b_mn && kb < 0.2157) kb = 0.2157;       // whole 128-column boxes to load
+  const double epi = 1.2 + 0.0033 * bn;  // per tile, beside the next tile's MMAs
+  const double main = nk * kb;
+  const double mem = 2.0 * (double(m + n) * nk * kLinBK + double(m) * n) / 3.54e6;
+  const double work = waves * (main > epi ? main : epi);
+  return 3.2 + epi + (work > mem ? work : mem);
+}
+
+double split_time(int64_t m, int64_t n, int nk, int bn, int splits, int stages, int clusters,
+                  int sms) {
+  const int64_t tiles = ((m + bn - 1) / bn) * ((n + 127) / 128);
+  const int nkb = (nk + splits - 1) / splits;
+  const double stage = split_stage_bytes(bn);
+  const double rate = stage / 134600.0 > 0.00196 * bn ? stage / 134600.0 : 0.00196 * bn;
+  const auto wave = [&](int64_t c) {  // c clusters side by side
+    if (c == 0) return 0.0;
+    const double per_sm = double(c) * splits > sms ? double(c) * splits / sms : 1.0;
+    double kb = per_sm * rate;              // an SM's bytes or MMAs
+    if (kb < 0.053 / stages) kb = 0.053 / stages;
+    if (kb < 0.2) kb = 0.2;  // one CTA's turn
+    return nkb * kb + 0.0251 * bn / splits * per_sm + 3.51;
+  };
+  const double work = double(tiles / clusters) * wave(clusters) + wave(tiles % clusters);
+  const double mem = 2.0 * (double(m + n) * nk * kLinBK + double(m) * n) / 5.13e6;
+  const double join = splits == 1 ? 0.0 : split_push(bn, splits) ? 0.016 : 2.56;
+  const double odd = splits == 8 ? 0.5 : splits == 6 ? 0.4 : splits == 3 ? 0.2 : 0.1 * (splits == 2);
+  return (work > mem ? work : mem) + join + odd;
+}
+
+// The form of least estimate.
+norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn,
+                        bool bf16, ProductPlan *best) {
+  const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
+  const int unit = a_mn ? 64 : 16;
+  norm_status_t st;
+  double time = 1e30;
+  const void *pair = linear_pair_kernel_ptr(a_mn, b_mn, bf16);
+  const void *split = linear_split_kernel_ptr(a_mn, b_mn, bf16);
+  if ((st = function_ready(d.dev, pair, d.optin)) != NORM_OK) return st;
+  if ((st = function_ready(d.dev, split, d.optin)) != NORM_OK) return st;
+  // GBNORM_LINEAR="pair=0,bn=64,splits=4" forces fields (for sweeps)
+  int want_pair = -1, want_bn = 0, want_splits = 0;
+  if (const char *o = std::getenv("GBNORM_LINEAR")) {
+    if (const char *q = std::strstr(o, "pair=")) want_pair = std::atoi(q + 5) != 0;
+    if (const char *q = std::strstr(o, "bn=")) want_bn = std::atoi(q + 3);
+    if (const char *q = std::strstr(o, "splits=")) want_splits = std::atoi(q + 7);
+  }
+  if (want_pair != 0 && (want_pair == 1 || m > 192)) {
+    int pairs = 0;
+    if ((st = resident(d, pair, kPairThreads, 2, pair_smem(), &pairs)) != NORM_OK) return st;
+    for (int bn : {128, 192, 224, 256}) {
+      if (want_pair == 1 && want_bn >= 64 && want_bn <= 256 && want_bn % 32 == 0) bn = want_bn;
+      const double t = pair_time(m, n, nk, bn, b_mn, pairs);
+      if (t < time) {
+        time = t;
+        *best = ProductPlan{true, bn, 1, 0};
+      }
+    }
+  }
+  // The split form does not pay beyond two waves of tiles or so.
+  if (want_pair != 1 && (want_pair == 0 || m * n <= int64_t(4096) * 4096)) {
+    const int whole = m <= 128 ? round_up(m, unit) : 128;
+    for (int bn : {whole, 64}) {
+      if (want_pair == 0 && want_bn >= unit && want_bn <= 256 && want_bn % unit == 0) bn = want_bn;
+      for (int s : {1, 2, 3, 4, 6, 8}) {
+        if (want_pair == 0 && want_splits >= 1 && want_splits <= 8) s = want_splits;
+        if (s > nk) s = nk;
+        const int stages = split_stages(nk, bn, s, d.optin);
+        int clusters = 0;
+        if ((st = resident(d, split, kSplitThreads, s, split_smem(bn, s, stages), &clusters)) !=
+            NORM_OK)
+          return st;
+        const int tm = d.sms * (512 / int(tmem_columns(bn))) / s;  // tensor memory's limit
+        const double t = split_time(m, n, nk, bn, s, stages, clusters < tm ? clusters : tm, d.sms);
+        if (t < time) {
+          time = t;
+          *best = ProductPlan{false, bn, s, stages};
+        }
+      }
+    }
+  }
+  return NORM_OK;
+}
+
+// Plans of sizes seen before, per device, storage of the operands and type.
+std::map<std::tuple<int, int64_t, int64_t, int64_t>, ProductPlan> g_plans;
+constexpr size_t kMaxPlans = 4096;  // then the cache starts anew
+
+norm_status_t plan_product(const Device &d, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn,
+                           bool bf16, ProductPlan *out) {
+  const bool forced = std::getenv("GBNORM_LINEAR") != nullptr;
+  const auto key = std::make_tuple(d.dev * 8 + a_mn * 4 + b_mn * 2 + bf16, m, n, k);
+  if (!forced) {
+    std::lock_guard<std::mutex> lk(g_plan_mu);
+    auto it = g_plans.find(key);
+    if (it != g_plans.end()) {
+      *out = it->second;
+      return NORM_OK;
+    }
+  }
+  ProductPlan p;
+  const norm_status_t st = best_form(d, m, n, k, a_mn, b_mn, bf16, &p);
+  if (st != NORM_OK) return st;
+  if (!forced) {
+    std::lock_guard<std::mutex> lk(g_plan_mu);
+    if (g_plans.size() >= kMaxPlans) g_plans.clear();
+    g_plans[key] = p;
+  }
+  *out = p;
   return NORM_OK;
 }
 
@@ -139,16 +240,17 @@ norm_status_t resident_pairs(const Device &d, const void *fn, int *out) {
 norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix &b, bool b_mn,
                       int64_t m, int64_t n, int64_t k, const LinEpilogue &e, bool bf16,
                       cudaStream_t s) {
-  const ProductPlan plan = plan_product(m, n, k, a_mn, d);
+  ProductPlan plan;
+  norm_status_t st = plan_product(d, m, n, k, a_mn, b_mn, bf16, &plan);
+  if (st != NORM_OK) return st;
   const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
-  norm_status_t st;
   CUtensorMap ta, tb;
   if (plan.pair) {
     const void *fn = linear_pair_kernel_ptr(a_mn, b_mn, bf16);
     if (d.optin < int(pair_smem())) return NORM_ERR_UNSUPPORTED;
     if ((st = function_ready(d.dev, fn, d.optin)) != NORM_OK) return st;
     int pairs = 0;
-    if ((st = resident_pairs(d, fn, &pairs)) != NORM_OK) return st;
+    if ((st = resident(d, fn, kPairThreads, 2, pair_smem(), &pairs)) != NORM_OK) return st;
     if ((st = map_of(&ta, a, bf16, a_mn ? kLinBK : 128)) != NORM_OK) return st;
     if ((st = map_of(&tb, b, bf16, b_mn ? kLinBK : uint32_t(plan.bn / 2))) != NORM_OK) return st;
     PairArgs p = {};
@@ -192,8 +294,7 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
   p.splits = plan.splits;
   p.stages = plan.stages;
   p.tiles_j = static_cast<int>((m + plan.bn - 1) / plan.bn);
-  p.tmem = 32;
-  while (p.tmem < uint32_t(plan.bn)) p.tmem *= 2;
+  p.tmem = tmem_columns(plan.bn);
   p.err = d.err;
   p.vec = 1;
   const Matrix rows[4] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n},
