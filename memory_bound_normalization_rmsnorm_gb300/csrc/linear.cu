@@ -239,7 +239,7 @@ norm_status_t plan_product(const Device &d, int64_t m, int64_t n, int64_t k, boo
 // copies, stored [m or n, k], or [k, m or n] where a_mn / b_mn.
 norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix &b, bool b_mn,
                       int64_t m, int64_t n, int64_t k, const LinEpilogue &e, bool bf16,
-                      cudaStream_t s) {
+                      bool late, cudaStream_t s) {
   ProductPlan plan;
   norm_status_t st = plan_product(d, m, n, k, a_mn, b_mn, bf16, &plan);
   if (st != NORM_OK) return st;
@@ -259,10 +259,13 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     p.n = static_cast<int>(n);
     p.nk = nk;
     p.bn = plan.bn;
-    p.bufs = e.r || e.z ? 4 : 2;
+    // (with many K blocks a residual tile that is loaded when its slice begins is
+    // in time, and the room goes to the operands)
+    p.bufs = e.z || (e.r && nk < 32) ? 4 : 2;
     p.stages = pair_stages(p.bn, b_mn, p.bufs);
     p.sets = p.bufs / 2 / (e.z ? 2 : 1);
     p.gm = 8;
+    p.late = late;
     p.err = d.err;
     CUtensorMap ty = ta, tz = ta, tr = ta;
     const Matrix out[3] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n}};
@@ -296,6 +299,7 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
   p.tiles_j = static_cast<int>((m + plan.bn - 1) / plan.bn);
   p.tmem = tmem_columns(plan.bn);
   p.err = d.err;
+  p.late = late;
   p.vec = 1;
   const Matrix rows[4] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n},
                           {e.bias, 0, 1, n}};
@@ -312,21 +316,36 @@ size_t packed_bytes(const Matrix &t) {
   return (size_t(t.rows) * size_t(round_up(t.cols, 8)) * 2 + 255) & ~size_t(255);
 }
 
-norm_status_t pack(Matrix *t, char **ws, cudaStream_t s) {
-  if (tma_ready(*t)) return NORM_OK;
-  const uint16_t *src = static_cast<const uint16_t *>(t->p);
-  uint16_t *dst = reinterpret_cast<uint16_t *>(*ws);
-  int64_t ld = t->ld, ldd = round_up(t->cols, 8);
-  int rows = static_cast<int>(t->rows), cols = static_cast<int>(t->cols);
-  const int gy = (rows + 7) / 8 < 65535 ? (rows + 7) / 8 : 65535;
-  void *args[] = {&src, &ld, &rows, &cols, &dst, &ldd};
-  const norm_status_t st = launch_serial(linear_pack_kernel_ptr(),
-                                         dim3(unsigned((cols + 255) / 256), unsigned(gy)),
-                                         dim3(256), 0, 1, args, s);
-  *ws += packed_bytes(*t);
-  t->p = dst;
-  t->ld = ldd;
-  return st;
+// Copies those of the matrices that are not null and not addressable, in one
+// launch, and has them point to the copies.
+norm_status_t pack(Matrix *t0, Matrix *t1, char **ws, cudaStream_t s) {
+  PackArgs a = {};
+  int n = 0, most = 0;
+  bool two = true;
+  for (const Matrix *t : {t0, t1})
+    if (t && !tma_ready(*t) &&
+        (reinterpret_cast<uintptr_t>(t->p) % 4 || t->cols % 2 || (t->rows > 1 && t->ld % 2)))
+      two = false;
+  for (Matrix *t : {t0, t1}) {
+    if (!t || tma_ready(*t)) continue;
+    a.src[n] = static_cast<const uint16_t *>(t->p);
+    a.dst[n] = reinterpret_cast<uint16_t *>(*ws);
+    a.ld[n] = t->ld;
+    a.ldd[n] = round_up(t->cols, 8);
+    a.rows[n] = static_cast<int>(t->rows);
+    a.cols[n] = static_cast<int>(t->cols);
+    a.strips[n] = (a.cols[n] / (two ? 2 : 1) + 255) / 256;
+    if (a.rows[n] > most) most = a.rows[n];
+    *ws += packed_bytes(*t);
+    t->p = a.dst[n];
+    t->ld = a.ldd[n];
+    ++n;
+  }
+  if (n == 0) return NORM_OK;
+  const int gy = (most + 7) / 8 < 65535 ? (most + 7) / 8 : 65535;
+  void *args[] = {&a};
+  return launch_serial(linear_pack_kernel_ptr(two), dim3(unsigned(a.strips[0] + a.strips[1]), unsigned(gy)),
+                       dim3(256), 0, 1, args, s);
 }
 
 norm_status_t check_shape(int64_t M, int64_t K, int64_t N) {
@@ -426,10 +445,9 @@ norm_status_t norm_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t
     if ((st = check_device_memory(p, d.dev)) != NORM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
-  if ((st = pack(&mx, &ws, s)) != NORM_OK) return st;
-  if ((st = pack(&mw, &ws, s)) != NORM_OK) return st;
+  if ((st = pack(&mx, &mw, &ws, s)) != NORM_OK) return st;
   const LinEpilogue e = {bias, r, z, y, ldr, ldz, ldy, int(act)};
-  return product(d, mx, false, mw, false, M, N, K, e, dtype == NORM_BF16, s);
+  return product(d, mx, false, mw, false, M, N, K, e, dtype == NORM_BF16, false, s);
 }
 
 norm_status_t norm_linear_bwd_workspace_bytes(const void *dy, int64_t lddy, const void *x,
@@ -481,6 +499,8 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   Matrix mdz = mdy;
+  const float *part = nullptr;
+  bool first = true;  // of the products
   if (g.need_dz || dbias) {
     GradArgs a = {};
     a.dy = dy;
@@ -499,7 +519,7 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
       mdz.ld = a.lddz;
     }
     if (dbias) {
-      a.part = reinterpret_cast<float *>(ws);
+      part = a.part = reinterpret_cast<float *>(ws);
       ws += g.part;
     }
     void *args[] = {&a};
@@ -507,26 +527,27 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
     st = launch_serial(linear_grad_kernel_ptr(bf16, g.vec), dim3(unsigned(strips), unsigned(g.chunks)),
                        dim3(kGradThreads), 0, 1, args, s);
     if (st != NORM_OK) return st;
-    if (dbias) {
-      const float *part = a.part;
-      int n = a.N, rows = a.chunks;
-      void *fold[] = {&part, &n, &rows, &dbias};
-      st = launch_serial(linear_fold_kernel_ptr(), dim3(unsigned((n + 31) / 32)), dim3(1024), 0, 1,
-                         fold, s);
-      if (st != NORM_OK) return st;
-    }
   }
+  if ((st = pack(dx ? &mw : nullptr, dw ? &mx : nullptr, &ws, s)) != NORM_OK) return st;
+  // The products and the last sum need nothing of one another: all but the first
+  // start where the one before leaves room, and end after it.
   if (dx) {
-    if ((st = pack(&mw, &ws, s)) != NORM_OK) return st;
     const LinEpilogue e = {nullptr, nullptr, nullptr, dx, 0, 0, lddx, kLinNone};
-    if ((st = product(d, mdz, false, mw, true, M, K, N, e, bf16, s)) != NORM_OK) return st;
+    if ((st = product(d, mdz, false, mw, true, M, K, N, e, bf16, !first, s)) != NORM_OK) return st;
+    first = false;
   }
   if (dw) {
-    if ((st = pack(&mx, &ws, s)) != NORM_OK) return st;
     const LinEpilogue e = {nullptr, nullptr, nullptr, dw, 0, 0, lddw, kLinNone};
-    if ((st = product(d, mdz, true, mx, true, N, K, M, e, bf16, s)) != NORM_OK) return st;
+    if ((st = product(d, mdz, true, mx, true, N, K, M, e, bf16, !first, s)) != NORM_OK) return st;
+    first = false;
   }
-  return NORM_OK;
+  if (dbias) {
+    int n = static_cast<int>(N), rows = g.chunks, late = !first;
+    void *fold[] = {&part, &n, &rows, &dbias, &late};
+    st = launch_serial(linear_fold_kernel_ptr(), dim3(unsigned((n + 31) / 32)), dim3(1024), 0, 1,
+                       fold, s);
+  }
+  return st;
 }
 
 }  // extern "C"

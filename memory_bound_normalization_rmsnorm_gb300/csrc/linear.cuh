@@ -116,6 +116,7 @@ struct PairArgs {
   int sets;     // of them a warp's slices use in turn (pairs where z is written): 1 or 2
   int tma_y, tma_z, tma_r;  // moved by tensor copies (else by the warps)
   int gm;       // row blocks per group of the tile walk
+  int late;     // see SplitArgs
   unsigned *err;
 };
 constexpr int kPairMaxStages = 9;
@@ -145,6 +146,9 @@ struct SplitArgs {
   int tiles_j;     // token tiles
   uint32_t tmem;   // tensor-memory columns
   int vec;         // y, z, r and bias take 8-byte accesses
+  // The product reads nothing that the kernel before it writes, and that kernel
+  // waited for those before: it starts beside it and waits for it at its end.
+  int late;
   unsigned *err;
 };
 __host__ __device__ constexpr uint32_t split_stage_bytes(int bn) { return 16384u + uint32_t(bn) * 128u; }
@@ -170,7 +174,15 @@ struct GradArgs {
 };
 // (fp16 / bf16, eight columns per thread or one)
 const void *linear_grad_kernel_ptr(bool bf16, bool vec);
-const void *linear_pack_kernel_ptr();
+// (two elements at a time, where rows are even and start on four bytes)
+const void *linear_pack_kernel_ptr(bool two);
+struct PackArgs {  // up to two matrices
+  const uint16_t *src[2];
+  uint16_t *dst[2];
+  int64_t ld[2], ldd[2];
+  int rows[2], cols[2];
+  int strips[2];  // of 256 columns (pairs of columns)
+};
 const void *linear_fold_kernel_ptr();
 
 }  // namespace gbn

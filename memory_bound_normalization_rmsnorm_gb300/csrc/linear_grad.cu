@@ -90,10 +90,10 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradArg
 
 // Adds the chunks' rows in order: 32 columns per block, 32 rows side by side.
 __global__ void __launch_bounds__(1024)
-    linear_fold_kernel(const float *part, int n, int rows, float *out) {
+    linear_fold_kernel(const float *part, int n, int rows, float *out, int late) {
   __shared__ float sum[32][33];
   grid_launch_dependents();
-  grid_dependency_wait();
+  if (!late) grid_dependency_wait();
   const int lane = threadIdx.x & 31, row = threadIdx.x / 32;
   const int col = blockIdx.x * 32 + lane;
   float v = 0.f;
@@ -107,21 +107,32 @@ __global__ void __launch_bounds__(1024)
     for (int r = 0; r < 32; ++r) v += sum[r][lane];
     out[col] = v;
   }
+  if (late) grid_dependency_wait();  // (SplitArgs::late)
 }
 
-// 16-bit rows to rows whose stride and address tensor copies take.
-__global__ void __launch_bounds__(256)
-    linear_pack_kernel(const uint16_t *src, int64_t ld, int rows, int cols, uint16_t *dst,
-                       int64_t ldd) {
+// 16-bit rows to rows whose stride and address tensor copies take; one or two
+// matrices, one after the other along the grid's x.  T: one element, or two where
+// every row starts on a multiple of four bytes.  A warp takes 256 T of a row.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ PackArgs a) {
+  constexpr int E = sizeof(T) / 2;
   grid_launch_dependents();
   grid_dependency_wait();
+  const bool second = static_cast<int>(blockIdx.x) >= a.strips[0];
+  const T *src = reinterpret_cast<const T *>(second ? a.src[1] : a.src[0]);
+  T *dst = reinterpret_cast<T *>(second ? a.dst[1] : a.dst[0]);
+  const int64_t ld = (second ? a.ld[1] : a.ld[0]) / E, ldd = (second ? a.ldd[1] : a.ldd[0]) / E;
+  const int rows = second ? a.rows[1] : a.rows[0];
+  const int cols = (second ? a.cols[1] : a.cols[0]) / E;
+  const int c0 = (static_cast<int>(blockIdx.x) - (second ? a.strips[0] : 0)) * 256 + (threadIdx.x & 31);
   for (int r = blockIdx.y * 8 + threadIdx.x / 32; r < rows; r += gridDim.y * 8) {
-    const int c0 = blockIdx.x * 256 + (threadIdx.x & 31);
+    T v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int c = c0 + 32 * u;
-      if (c < cols) dst[r * ldd + c] = src[r * ld + c];
-    }
+    for (int u = 0; u < 8; ++u)
+      if (c0 + 32 * u < cols) v[u] = src[r * ld + c0 + 32 * u];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (c0 + 32 * u < cols) dst[r * ldd + c0 + 32 * u] = v[u];
   }
 }
 
@@ -135,6 +146,9 @@ const void *linear_grad_kernel_ptr(bool bf16, bool vec) {
              : reinterpret_cast<const void *>(&linear_grad_kernel<kFP16, 1>);
 }
 const void *linear_fold_kernel_ptr() { return reinterpret_cast<const void *>(&linear_fold_kernel); }
-const void *linear_pack_kernel_ptr() { return reinterpret_cast<const void *>(&linear_pack_kernel); }
+const void *linear_pack_kernel_ptr(bool two) {
+  return two ? reinterpret_cast<const void *>(&linear_pack_kernel<uint32_t>)
+             : reinterpret_cast<const void *>(&linear_pack_kernel<uint16_t>);
+}
 
 }  // namespace gbn

@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   __syncwarp();
   if (splits > 1) cluster_arrive_release();  // this CTA runs: peers may write to it
-  grid_dependency_wait();  // before tensor memory is taken: never held while waiting
+  // before tensor memory is taken: never held while waiting
+  if (!p.late) grid_dependency_wait();
   if (warp == 0) {
     if (elect_one())
       for (int n = 0; n < stages && n < nkb; ++n) fetch(n, n);
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       load_r(j + kSplitThreads / 32);
     }
   }
+  if (p.late) grid_dependency_wait();  // this kernel's end is the end of both
   if (splits > 1 && !push) {  // peers may still read this CTA's partials
     __syncwarp();
     cluster_sync();

@@ -347,6 +347,37 @@ def test_streams_graphs_and_repeats():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2304, 4096, 512), (512, 256, 4096), (40, 2048, 512),
+                                   (300, 640, 4099)])
+def test_backward_between_writers_and_readers(shape):
+    """The backward's kernels overlap one another; what runs before and behind
+    them on the stream does not: every gradient is read by the next kernel, and
+    the operands are written right before."""
+    M, K, N = shape
+    c = _make("bf16", M, K, N)
+    dx, dw = torch.empty_like(c["x"]), torch.empty_like(c["w"])
+    db = torch.empty(N, device="cuda")
+    keep = dict(p=0.0, seed=1)
+    want = {}
+    for i in range(12):
+        f = 1.0 + i % 3  # exact factors: the gradients scale with dy, and dw with x
+        dy, x = c["dy"] * f, gb.norm_dropout(c["x"] * f, **keep)
+        gb.norm_linear_bwd(dy, x, c["w"], dx=dx, dw=dw, dbias=db)
+        got = (gb.norm_dropout(dx, **keep), gb.norm_dropout(dw, **keep), gb.norm_dropout(db, **keep))
+        for t in (dx, dw, db):
+            t.fill_(float("nan"))
+        if i < 3:
+            want[f] = [g.clone() for g in got]
+        else:
+            for g, w in zip(got, want[f]):
+                assert torch.equal(g, w)
+    torch.cuda.synchronize()
+    full = gb.norm_linear_bwd(c["dy"], c["x"], c["w"])
+    for g, w in zip(want[1.0], full):
+        assert torch.equal(g, w)
+
+
+@pytest.mark.gpu
 def test_beside_other_kernels_that_hold_tensor_memory():
     """Split-form clusters on one stream, pair-form and the normalisation-GEMM on
     others, many at once."""
