@@ -407,7 +407,7 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
  *              be NULL)
  *   pos        device int32 or int64 (pos_bits 32 or 64): the position of token
  *              t on axis a at pos[a * pos_stride + t]; any integer
- *   inv_freq   device fp64 [rd / 2]: radians per position, finite
+ *   inv_freq   device fp64 [rd / 2]: radians per position, finite and below 2^53
  *   pair_axis  HOST uint8 [rd / 2], read before the call returns: the axis of
  *              each pair, below `axes`; NULL: all on axis 0 (axes = 1)
  *   gamma_q, gamma_k, beta_q, beta_k   [D] of `dtype`.  gamma_q NULL: no

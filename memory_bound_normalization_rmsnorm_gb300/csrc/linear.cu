@@ -182,8 +182,8 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
       }
     }
   }
-  // The split form does not pay beyond two waves of tiles or so.
-  if (want_pair != 1 && (want_pair == 0 || m * n <= int64_t(4096) * 4096)) {
+  // The split form for few rows, and as long as its tiles are two waves or so.
+  if (want_pair != 1 && (want_pair == 0 || m <= 192 || m * n <= int64_t(4096) * 4096)) {
     const int whole = m <= 128 ? round_up(m, unit) : 128;
     for (int bn : {whole, 64}) {
       if (want_pair == 0 && want_bn >= unit && want_bn <= 256 && want_bn % unit == 0) bn = want_bn;

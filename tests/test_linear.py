@@ -131,7 +131,8 @@ def _bwd_check(c, name, got=None, **kw):
 SHAPES = [(1, 1, 1), (1, 64, 128), (2, 8, 16), (1, 4096, 1024), (3, 520, 264), (16, 1000, 400),
           (17, 136, 72), (48, 2048, 512), (129, 256, 384), (200, 72, 130), (65, 77, 99),
           (33, 130, 7), (7, 9, 300), (500, 640, 1288), (777, 1234, 999), (2100, 200, 1544),
-          (2500, 71, 1541), (1, 16384, 256)]
+          (2500, 71, 1541), (1, 16384, 256), (150, 64, 131072), (192, 40, 90001),
+          (90001, 24, 40), (20000, 8, 192)]
 
 
 @pytest.mark.gpu
@@ -344,6 +345,51 @@ def test_streams_graphs_and_repeats():
             assert torch.equal(x, w)
     assert not torch.equal(want[0], first[0])
     assert gb.norm_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_first_call_of_a_size_inside_a_capture():
+    c = _make("fp16", 37, 192, 336)
+    z = c["r"]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.empty(1, device="cuda")
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        y, _ = gb.norm_linear_fwd(c["x"], c["w"], c["bias"], c["r"], "silu")
+        got = gb.norm_linear_bwd(c["dy"], c["x"], c["w"], z, "silu")
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, gb.norm_linear_fwd(c["x"], c["w"], c["bias"], c["r"], "silu")[0])
+    for a, b in zip(got, gb.norm_linear_bwd(c["dy"], c["x"], c["w"], z, "silu")):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_many_threads_and_sizes():
+    """Calls of new sizes from several threads at once, each on its stream."""
+    import threading
+
+    sizes = [(5 + 7 * i, 40 + 8 * i, 24 + 16 * i) for i in range(12)]
+    cases = [_make("bf16", *s, seed=i) for i, s in enumerate(sizes)]
+    outs = {}
+
+    def work(t):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for i in range(t, 12, 4):
+                outs[i] = gb.norm_linear_fwd(cases[i]["x"], cases[i]["w"], cases[i]["bias"])[0]
+        s.synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i, c in enumerate(cases):
+        (wy, _), (ey, _) = lr.forward(c["x"], c["w"], c["bias"], None, "none")
+        lr.check(outs[i], wy, ey, "y")
 
 
 @pytest.mark.gpu
