@@ -61,12 +61,14 @@
 
 #include "../../include/gbnorm.h"
 #include "common.cuh"
-#include "host_util.h"
 #include "rowops.cuh"
 #include "tcgen05.cuh"
-#include "tensor_map.h"
 
 namespace gbn {
+
+// Device error word and shape of the current device (api.cu).
+norm_status_t device_context(int *dev, int *sms, int *smem_optin, unsigned **err,
+                             unsigned long long *ctx);
 
 namespace {
 
@@ -619,9 +621,7 @@ std::mutex g_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::set<std::pair<unsigned long long, const void *>> g_attr_done;  // (context, kernel)
 
-}  // namespace
-
-norm_status_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out) {
+norm_status_t encoder(PFN_cuTensorMapEncodeTiled_v12000 *out) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (!g_encode) {
     void *fn = nullptr;
@@ -638,14 +638,12 @@ norm_status_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out) {
   return NORM_OK;
 }
 
-namespace {
-
 // Row-major bf16 [rows, cols] with boxes of box_rows x 64 columns, 128-byte
 // swizzle, zero fill outside the tensor.
 norm_status_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
                        uint32_t box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  norm_status_t st = tensor_map_encoder(&enc);
+  norm_status_t st = encoder(&enc);
   if (st != NORM_OK) return st;
   cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
   cuuint64_t strides[1] = {cuuint64_t(cols) * 2};
@@ -658,8 +656,6 @@ norm_status_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t c
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-}  // namespace
 
 // x, W' and out are moved by tiled tensor copies, whose tensor maps take a
 // global address this GPU can reach: device memory of the current device
@@ -674,8 +670,6 @@ norm_status_t check_device_memory(const void *p, int dev) {
   if (a.type == cudaMemoryTypeManaged) return NORM_OK;
   return (a.type == cudaMemoryTypeDevice && a.device == dev) ? NORM_OK : NORM_ERR_MEMORY;
 }
-
-namespace {
 
 // Kernel form: the CTA pair (cta_group::2) by default, GBNORM_GEMM_CTAS=1
 // the single-CTA kernel.  Measured on GB300 at M = 32768, K = Nout from 2048

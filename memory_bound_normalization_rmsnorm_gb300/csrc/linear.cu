@@ -1,6 +1,7 @@
 // linear.cu -- entry points norm_linear_fwd / norm_linear_bwd: which kernels run
 // a product, its tensor maps, workspaces and launches.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdlib>
@@ -14,7 +15,6 @@
 #include "common.cuh"
 #include "host_util.h"
 #include "linear.cuh"
-#include "tensor_map.h"
 
 namespace gbn {
 
@@ -32,10 +32,38 @@ bool tma_ready(const Matrix &t) {
   return aligned_to_16(t.p) && (t.rows == 1 || t.ld % 8 == 0);
 }
 
+using MapEncoder = PFN_cuTensorMapEncodeTiled_v12000;
+
+// The driver's encoder of tensor maps (null where there is none).
+MapEncoder map_encoder() {
+  static const MapEncoder found = [] {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      fn = nullptr;
+    }
+    return reinterpret_cast<MapEncoder>(fn);
+  }();
+  return found;
+}
+
+// Tensor copies reach device memory of the current device, or managed memory.
+norm_status_t check_memory(const void *p, int dev) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();
+    return NORM_ERR_MEMORY;
+  }
+  const bool here = a.type == cudaMemoryTypeDevice && a.device == dev;
+  return here || a.type == cudaMemoryTypeManaged ? NORM_OK : NORM_ERR_MEMORY;
+}
+
 norm_status_t map_of(CUtensorMap *m, const Matrix &t, bool bf16, uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  norm_status_t st = tensor_map_encoder(&enc);
-  if (st != NORM_OK) return st;
+  const MapEncoder enc = map_encoder();
+  if (!enc) return NORM_ERR_CUDA;
   const int64_t ld = t.rows == 1 ? (t.cols + 7) / 8 * 8 : t.ld;
   cuuint64_t dims[2] = {cuuint64_t(t.cols), cuuint64_t(t.rows)};
   cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
@@ -60,6 +88,7 @@ struct ProductPlan {
   int bn = 0;      // tile columns (pair), or tokens per tile (split)
   int splits = 1;  // the split form
   int stages = 0;
+  double time = 1e30;  // estimate, us
 };
 
 int round_up(int64_t v, int to) { return static_cast<int>((v + to - 1) / to * to); }
@@ -152,15 +181,38 @@ double split_time(int64_t m, int64_t n, int nk, int bn, int splits, int stages, 
   return (work > mem ? work : mem) + join + odd;
 }
 
+// The split form with clusters of s CTAs (s <= nk): its tile width and estimate.
+norm_status_t split_form(const Device &d, int64_t m, int64_t n, int nk, bool a_mn, bool bf16, int s,
+                         int want_bn, ProductPlan *best) {
+  const int unit = a_mn ? 64 : 16;
+  const int whole = m <= 128 ? round_up(m, unit) : 128;
+  const void *fn = linear_split_kernel_ptr(bf16);
+  *best = ProductPlan{};
+  for (int bn : {whole, 64}) {
+    if (want_bn >= unit && want_bn <= 256 && want_bn % unit == 0) bn = want_bn;
+    const int stages = split_stages(nk, bn, s, d.optin);
+    int clusters = 0;
+    const norm_status_t st =
+        resident(d, fn, kSplitThreads, s, split_smem(bn, s, stages), &clusters);
+    if (st != NORM_OK) return st;
+    const int tm = d.sms * (512 / int(tmem_columns(bn))) / s;  // tensor memory's limit
+    const double t = split_time(m, n, nk, bn, s, stages, clusters < tm ? clusters : tm, d.sms);
+    if (t < best->time) *best = ProductPlan{false, bn, s, stages, t};
+  }
+  return NORM_OK;
+}
+
+// The split form is for few rows, and as long as its tiles are two waves or so.
+bool split_size(int64_t m, int64_t n) { return m <= 192 || m * n <= int64_t(4096) * 4096; }
+
 // The form of least estimate.
 norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn,
                         bool bf16, ProductPlan *best) {
   const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
-  const int unit = a_mn ? 64 : 16;
   norm_status_t st;
-  double time = 1e30;
+  *best = ProductPlan{};
   const void *pair = linear_pair_kernel_ptr(a_mn, b_mn, bf16);
-  const void *split = linear_split_kernel_ptr(a_mn, b_mn, bf16);
+  const void *split = linear_split_kernel_ptr(bf16);
   if ((st = function_ready(d.dev, pair, d.optin)) != NORM_OK) return st;
   if ((st = function_ready(d.dev, split, d.optin)) != NORM_OK) return st;
   // GBNORM_LINEAR="pair=0,bn=64,splits=4" forces fields (for sweeps)
@@ -176,32 +228,17 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
     for (int bn : {128, 192, 224, 256}) {
       if (want_pair == 1 && want_bn >= 64 && want_bn <= 256 && want_bn % 32 == 0) bn = want_bn;
       const double t = pair_time(m, n, nk, bn, b_mn, pairs);
-      if (t < time) {
-        time = t;
-        *best = ProductPlan{true, bn, 1, 0};
-      }
+      if (t < best->time) *best = ProductPlan{true, bn, 1, 0, t};
     }
   }
-  // The split form for few rows, and as long as its tiles are two waves or so.
-  if (want_pair != 1 && (want_pair == 0 || m <= 192 || m * n <= int64_t(4096) * 4096)) {
-    const int whole = m <= 128 ? round_up(m, unit) : 128;
-    for (int bn : {whole, 64}) {
-      if (want_pair == 0 && want_bn >= unit && want_bn <= 256 && want_bn % unit == 0) bn = want_bn;
-      for (int s : {1, 2, 3, 4, 6, 8}) {
-        if (want_pair == 0 && want_splits >= 1 && want_splits <= 8) s = want_splits;
-        if (s > nk) s = nk;
-        const int stages = split_stages(nk, bn, s, d.optin);
-        int clusters = 0;
-        if ((st = resident(d, split, kSplitThreads, s, split_smem(bn, s, stages), &clusters)) !=
-            NORM_OK)
-          return st;
-        const int tm = d.sms * (512 / int(tmem_columns(bn))) / s;  // tensor memory's limit
-        const double t = split_time(m, n, nk, bn, s, stages, clusters < tm ? clusters : tm, d.sms);
-        if (t < time) {
-          time = t;
-          *best = ProductPlan{false, bn, s, stages};
-        }
-      }
+  if (want_pair != 1 && (want_pair == 0 || split_size(m, n))) {
+    for (int s : {1, 2, 3, 4, 6, 8}) {
+      if (want_pair == 0 && want_splits >= 1 && want_splits <= 8) s = want_splits;
+      if (s > nk) s = nk;
+      ProductPlan p;
+      st = split_form(d, m, n, nk, a_mn, bf16, s, want_pair == 0 ? want_bn : 0, &p);
+      if (st != NORM_OK) return st;
+      if (p.time < best->time) *best = p;
     }
   }
   return NORM_OK;
@@ -235,11 +272,65 @@ norm_status_t plan_product(const Device &d, int64_t m, int64_t n, int64_t k, boo
   return NORM_OK;
 }
 
+// A launch of the split form: one or two products, and a sum of rows behind them.
+struct SplitLaunch {
+  SplitMaps maps = {};
+  SplitArgs args = {};
+  uint32_t smem = 0;
+  int count = 0;
+
+  explicit SplitLaunch(int splits) {
+    args.splits = splits;
+    args.tmem = 32;
+  }
+  norm_status_t add(const Matrix &a, bool a_mn, const Matrix &b, bool b_mn, int64_t m, int64_t n,
+                    int nk, const ProductPlan &plan, const LinEpilogue &e, bool bf16) {
+    norm_status_t st;
+    if ((st = map_of(&maps.a[count], a, bf16, a_mn ? kLinBK : uint32_t(plan.bn))) != NORM_OK)
+      return st;
+    if ((st = map_of(&maps.b[count], b, bf16, b_mn ? kLinBK : 128)) != NORM_OK) return st;
+    SplitProblem &p = args.q[count++];
+    p.e = e;
+    p.m = static_cast<int>(m);
+    p.n = static_cast<int>(n);
+    p.nk = nk;
+    p.bn = plan.bn;
+    p.stages = plan.stages;
+    p.tiles_j = static_cast<int>((m + plan.bn - 1) / plan.bn);
+    const int64_t clusters = int64_t(p.tiles_j) * ((n + 127) / 128);
+    if (clusters * args.splits > 0x3fffffff) return NORM_ERR_UNSUPPORTED;
+    p.clusters = static_cast<int>(clusters);
+    p.a_mn = a_mn;
+    p.b_mn = b_mn;
+    p.vec = 1;
+    const Matrix rows[4] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n},
+                            {e.bias, 0, 1, n}};
+    for (const Matrix &t : rows)
+      if (reinterpret_cast<uintptr_t>(t.p) % 8 || (t.rows > 1 && t.p && t.ld % 4)) p.vec = 0;
+    if (tmem_columns(p.bn) > args.tmem) args.tmem = tmem_columns(p.bn);
+    const uint32_t need = split_smem(p.bn, args.splits, p.stages);
+    if (need > smem) smem = need;
+    return NORM_OK;
+  }
+  norm_status_t go(const Device &d, bool bf16, cudaStream_t s) {
+    const void *fn = linear_split_kernel_ptr(bf16);
+    if (d.optin < int(smem)) return NORM_ERR_UNSUPPORTED;
+    const norm_status_t st = function_ready(d.dev, fn, d.optin);
+    if (st != NORM_OK) return st;
+    int64_t clusters = int64_t(args.q[0].clusters) + args.q[1].clusters;
+    if (args.part)
+      clusters += (args.cols + kSplitThreads * args.splits - 1) / (kSplitThreads * args.splits);
+    void *a[] = {&maps, &args};
+    return launch_serial(fn, dim3(unsigned(clusters * args.splits)), dim3(kSplitThreads), smem,
+                         args.splits, a, s);
+  }
+};
+
 // out[j, i] = epilogue(sum_k A[j, k] B[i, k]); A and B are addressable by tensor
 // copies, stored [m or n, k], or [k, m or n] where a_mn / b_mn.
 norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix &b, bool b_mn,
                       int64_t m, int64_t n, int64_t k, const LinEpilogue &e, bool bf16,
-                      bool late, cudaStream_t s) {
+                      cudaStream_t s) {
   ProductPlan plan;
   norm_status_t st = plan_product(d, m, n, k, a_mn, b_mn, bf16, &plan);
   if (st != NORM_OK) return st;
@@ -265,7 +356,6 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     p.stages = pair_stages(p.bn, b_mn, p.bufs);
     p.sets = p.bufs / 2 / (e.z ? 2 : 1);
     p.gm = 8;
-    p.late = late;
     p.err = d.err;
     CUtensorMap ty = ta, tz = ta, tr = ta;
     const Matrix out[3] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n}};
@@ -273,7 +363,7 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     int *flags[3] = {&p.tma_y, &p.tma_z, &p.tma_r};
     for (int i = 0; i < 3; ++i) {
       if (!out[i].p || !tma_ready(out[i])) continue;
-      if ((st = check_device_memory(out[i].p, d.dev)) != NORM_OK) return st;
+      if ((st = check_memory(out[i].p, d.dev)) != NORM_OK) return st;
       if ((st = map_of(maps[i], out[i], bf16, 32)) != NORM_OK) return st;
       *flags[i] = 1;
     }
@@ -282,33 +372,61 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     void *args[] = {&ta, &tb, &ty, &tz, &tr, &p};
     return launch_serial(fn, dim3(unsigned(grid)), dim3(kPairThreads), pair_smem(), 2, args, s);
   }
-  const void *fn = linear_split_kernel_ptr(a_mn, b_mn, bf16);
-  const uint32_t smem = split_smem(plan.bn, plan.splits, plan.stages);
-  if (d.optin < int(smem)) return NORM_ERR_UNSUPPORTED;
-  if ((st = function_ready(d.dev, fn, d.optin)) != NORM_OK) return st;
-  if ((st = map_of(&ta, a, bf16, a_mn ? kLinBK : uint32_t(plan.bn))) != NORM_OK) return st;
-  if ((st = map_of(&tb, b, bf16, b_mn ? kLinBK : 128)) != NORM_OK) return st;
-  SplitArgs p = {};
-  p.e = e;
-  p.m = static_cast<int>(m);
-  p.n = static_cast<int>(n);
-  p.nk = nk;
-  p.bn = plan.bn;
-  p.splits = plan.splits;
-  p.stages = plan.stages;
-  p.tiles_j = static_cast<int>((m + plan.bn - 1) / plan.bn);
-  p.tmem = tmem_columns(plan.bn);
-  p.err = d.err;
-  p.late = late;
-  p.vec = 1;
-  const Matrix rows[4] = {{e.y, e.ldy, m, n}, {e.z, e.ldz, m, n}, {e.r, e.ldr, m, n},
-                          {e.bias, 0, 1, n}};
-  for (const Matrix &t : rows)
-    if (reinterpret_cast<uintptr_t>(t.p) % 8 || (t.rows > 1 && t.p && t.ld % 4)) p.vec = 0;
-  const int64_t grid = int64_t(p.tiles_j) * ((n + 127) / 128) * plan.splits;
-  if (grid > 0x7fffffff) return NORM_ERR_UNSUPPORTED;
-  void *args[] = {&ta, &tb, &p};
-  return launch_serial(fn, dim3(unsigned(grid)), dim3(kSplitThreads), smem, plan.splits, args, s);
+  SplitLaunch l(plan.splits);
+  if ((st = l.add(a, a_mn, b, b_mn, m, n, nk, plan, e, bf16)) != NORM_OK) return st;
+  return l.go(d, bf16, s);
+}
+
+// Whether both gradients' products of a layer go into one launch of the split
+// form, and their plans there, with clusters of the same size.  Each product
+// alone takes 3 us or so from the launch to the first byte and from the last, and
+// fills part of the GPU: 531 x 648 x 1001 with the bias takes 11 us in one launch
+// where it took 19 in three, 1024 x 1024 x 1024 13 in place of 19.
+struct JointPlan {
+  bool joint = false;
+  ProductPlan dx, dw;
+};
+std::map<std::tuple<int, int64_t, int64_t, int64_t>, JointPlan> g_joint;
+
+norm_status_t plan_joint(const Device &d, int64_t M, int64_t N, int64_t K, bool bf16, JointPlan *out) {
+  const bool forced = std::getenv("GBNORM_LINEAR") != nullptr;
+  const auto key = std::make_tuple(d.dev * 2 + bf16, M, N, K);
+  if (!forced) {
+    std::lock_guard<std::mutex> lk(g_plan_mu);
+    auto it = g_joint.find(key);
+    if (it != g_joint.end()) {
+      *out = it->second;
+      return NORM_OK;
+    }
+  }
+  JointPlan j;
+  norm_status_t st;
+  ProductPlan one[2];
+  if ((st = plan_product(d, M, K, N, false, true, bf16, &one[0])) != NORM_OK) return st;
+  if ((st = plan_product(d, N, K, M, true, true, bf16, &one[1])) != NORM_OK) return st;
+  if (forced ? !one[0].pair : split_size(M, K) && split_size(N, K)) {
+    const int nk = static_cast<int>((N + kLinBK - 1) / kLinBK);
+    const int mk = static_cast<int>((M + kLinBK - 1) / kLinBK);
+    double best = forced ? 1e30 : one[0].time + one[1].time;
+    for (int s : {1, 2, 3, 4, 6, 8}) {
+      if (s > nk || s > mk) break;
+      ProductPlan p[2];
+      if ((st = split_form(d, M, K, nk, false, bf16, s, 0, &p[0])) != NORM_OK) return st;
+      if ((st = split_form(d, N, K, mk, true, bf16, s, 0, &p[1])) != NORM_OK) return st;
+      const double t = p[0].time + p[1].time - 4.0;  // one start for two
+      if (t < best) {
+        best = t;
+        j = JointPlan{true, p[0], p[1]};
+      }
+    }
+  }
+  if (!forced) {
+    std::lock_guard<std::mutex> lk(g_plan_mu);
+    if (g_joint.size() >= kMaxPlans) g_joint.clear();
+    g_joint[key] = j;
+  }
+  *out = j;
+  return NORM_OK;
 }
 
 // Copies of operands in a workspace: whole multiples of 256 bytes.
@@ -442,12 +560,12 @@ norm_status_t norm_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t
   Device d;
   if ((st = device_of(&d)) != NORM_OK) return st;
   for (const void *p : {x, w})
-    if ((st = check_device_memory(p, d.dev)) != NORM_OK) return st;
+    if ((st = check_memory(p, d.dev)) != NORM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   if ((st = pack(&mx, &mw, &ws, s)) != NORM_OK) return st;
   const LinEpilogue e = {bias, r, z, y, ldr, ldz, ldy, int(act)};
-  return product(d, mx, false, mw, false, M, N, K, e, dtype == NORM_BF16, false, s);
+  return product(d, mx, false, mw, false, M, N, K, e, dtype == NORM_BF16, s);
 }
 
 norm_status_t norm_linear_bwd_workspace_bytes(const void *dy, int64_t lddy, const void *x,
@@ -482,7 +600,8 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
   if (!dx && !dw && !dbias) return NORM_ERR_ARG;
   if (act != NORM_ACT_NONE && !z) return NORM_ERR_NULL;
   if (act == NORM_ACT_NONE) z = nullptr;
-  Matrix mdy{dy, lddy, M, N}, mx{x, dw ? ldx : K, M, K}, mw{w, dx ? ldw : K, N, K};
+  Matrix mdy{dy, lddy, M, N};
+  Matrix mx{dw ? x : nullptr, dw ? ldx : K, M, K}, mw{dx ? w : nullptr, dx ? ldw : K, N, K};
   const Matrix mz{z, z ? ldz : N, M, N};
   for (const Matrix &t : {mdy, mx, mw, mz, Matrix{dx, dx ? lddx : K, M, K},
                           Matrix{dw, dw ? lddw : K, N, K}})
@@ -494,13 +613,12 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
   if (g.total() && (!workspace || workspace_bytes < g.total())) return NORM_ERR_WORKSPACE;
   if (g.total() && !aligned_to_16(workspace)) return NORM_ERR_ALIGN;
   for (const void *p : {dy, dw ? x : nullptr, dx ? w : nullptr})
-    if (p && (st = check_device_memory(p, d.dev)) != NORM_OK) return st;
+    if (p && (st = check_memory(p, d.dev)) != NORM_OK) return st;
   const bool bf16 = dtype == NORM_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   Matrix mdz = mdy;
   const float *part = nullptr;
-  bool first = true;  // of the products
   if (g.need_dz || dbias) {
     GradArgs a = {};
     a.dy = dy;
@@ -529,21 +647,29 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
     if (st != NORM_OK) return st;
   }
   if ((st = pack(dx ? &mw : nullptr, dw ? &mx : nullptr, &ws, s)) != NORM_OK) return st;
-  // The products and the last sum need nothing of one another: all but the first
-  // start where the one before leaves room, and end after it.
-  if (dx) {
-    const LinEpilogue e = {nullptr, nullptr, nullptr, dx, 0, 0, lddx, kLinNone};
-    if ((st = product(d, mdz, false, mw, true, M, K, N, e, bf16, !first, s)) != NORM_OK) return st;
-    first = false;
+  const LinEpilogue ex = {nullptr, nullptr, nullptr, dx, 0, 0, lddx, kLinNone};
+  const LinEpilogue ew = {nullptr, nullptr, nullptr, dw, 0, 0, lddw, kLinNone};
+  if (dx && dw) {  // one launch for both, and the sum, where both are small
+    JointPlan plan;
+    if ((st = plan_joint(d, M, N, K, bf16, &plan)) != NORM_OK) return st;
+    if (plan.joint) {
+      SplitLaunch l(plan.dx.splits);
+      const int nk = static_cast<int>((N + kLinBK - 1) / kLinBK);
+      const int mk = static_cast<int>((M + kLinBK - 1) / kLinBK);
+      if ((st = l.add(mdz, false, mw, true, M, K, nk, plan.dx, ex, bf16)) != NORM_OK) return st;
+      if ((st = l.add(mdz, true, mx, true, N, K, mk, plan.dw, ew, bf16)) != NORM_OK) return st;
+      l.args.part = part;
+      l.args.sums = dbias;
+      l.args.rows = g.chunks;
+      l.args.cols = static_cast<int>(N);
+      return l.go(d, bf16, s);
+    }
   }
-  if (dw) {
-    const LinEpilogue e = {nullptr, nullptr, nullptr, dw, 0, 0, lddw, kLinNone};
-    if ((st = product(d, mdz, true, mx, true, N, K, M, e, bf16, !first, s)) != NORM_OK) return st;
-    first = false;
-  }
+  if (dx && (st = product(d, mdz, false, mw, true, M, K, N, ex, bf16, s)) != NORM_OK) return st;
+  if (dw && (st = product(d, mdz, true, mx, true, N, K, M, ew, bf16, s)) != NORM_OK) return st;
   if (dbias) {
-    int n = static_cast<int>(N), rows = g.chunks, late = !first;
-    void *fold[] = {&part, &n, &rows, &dbias, &late};
+    int n = static_cast<int>(N), rows = g.chunks;
+    void *fold[] = {&part, &n, &rows, &dbias};
     st = launch_serial(linear_fold_kernel_ptr(), dim3(unsigned((n + 31) / 32)), dim3(1024), 0, 1,
                        fold, s);
   }

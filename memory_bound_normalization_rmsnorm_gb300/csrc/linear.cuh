@@ -10,6 +10,8 @@
 // An operand stored with k contiguous is K-major, else MN-major; the tensor
 // cores take either from shared memory, so no transpose is ever written.
 #pragma once
+#include <cuda.h>
+
 #include <cstdint>
 
 #include "elem.cuh"
@@ -32,6 +34,30 @@ struct LinEpilogue {
   int64_t ldr, ldz, ldy;
   int act;
 };
+
+// ---------------------------------------------------- single-thread roles
+// One lane of a converged warp.  A branch on this tells the compiler that one
+// thread takes it, and warp_index() that all of a warp do, so that what they form
+// there (descriptors, addresses) is uniform to it, as the tensor instructions'
+// operands have to be: with `lane == 0` in its place a K block of the MMA loop took
+// 440 clocks, twice that of its 256 x 128 x 64 MMAs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
+}
+
+// Fetches a tensor map (a kernel parameter) ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensor_map(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
 
 // --------------------------------------------------------- descriptors
 // kind::f16 with fp32 D: A and B both bf16 or both fp16, K- or MN-major.
@@ -116,7 +142,6 @@ struct PairArgs {
   int sets;     // of them a warp's slices use in turn (pairs where z is written): 1 or 2
   int tma_y, tma_z, tma_r;  // moved by tensor copies (else by the warps)
   int gm;       // row blocks per group of the tile walk
-  int late;     // see SplitArgs
   unsigned *err;
 };
 constexpr int kPairMaxStages = 9;
@@ -137,19 +162,29 @@ const void *linear_pair_kernel_ptr(bool a_mn, bool b_mn, bool bf16);
 // (linear_split.cu).
 constexpr int kSplitThreads = 192;
 constexpr int kSplitMaxStages = 12;
-struct SplitArgs {
+struct SplitProblem {
   LinEpilogue e;
   int m, n, nk;    // tokens, features, K blocks
   int bn;          // tokens per tile: a multiple of 16 (64 where A is MN-major), up to 256
-  int splits;      // CTAs per cluster
   int stages;
   int tiles_j;     // token tiles
-  uint32_t tmem;   // tensor-memory columns
+  int clusters;    // tiles of the problem
+  int a_mn, b_mn;  // storage of the token operand (A) and of the feature operand (B)
   int vec;         // y, z, r and bias take 8-byte accesses
-  // The product reads nothing that the kernel before it writes, and that kernel
-  // waited for those before: it starts beside it and waits for it at its end.
-  int late;
+};
+// One or two products in one launch, clusters of one after those of the other, and
+// behind them CTAs that add rows of partial sums (dbias).
+struct SplitArgs {
+  SplitProblem q[2];
+  const float *part;  // [rows, cols] or null
+  float *sums;        // [cols]
+  int rows, cols;
+  int splits;      // CTAs per cluster
+  uint32_t tmem;   // tensor-memory columns
   unsigned *err;
+};
+struct SplitMaps {
+  CUtensorMap a[2], b[2];
 };
 __host__ __device__ constexpr uint32_t split_stage_bytes(int bn) { return 16384u + uint32_t(bn) * 128u; }
 // Each CTA of a cluster owns a share of the tile's tokens.
@@ -161,7 +196,7 @@ __host__ __device__ constexpr uint32_t split_smem(int bn, int splits, int stages
   return 1024u + uint32_t(stages) * split_stage_bytes(bn) + 256u +
          (split_push(bn, splits) ? uint32_t(splits * split_share(bn, splits)) * 512u : 0u);
 }
-const void *linear_split_kernel_ptr(bool a_mn, bool b_mn, bool bf16);
+const void *linear_split_kernel_ptr(bool bf16);
 
 // linear_grad.cu
 constexpr int kGradThreads = 256;

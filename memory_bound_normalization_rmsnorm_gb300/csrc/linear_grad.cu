@@ -90,10 +90,10 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradArg
 
 // Adds the chunks' rows in order: 32 columns per block, 32 rows side by side.
 __global__ void __launch_bounds__(1024)
-    linear_fold_kernel(const float *part, int n, int rows, float *out, int late) {
+    linear_fold_kernel(const float *part, int n, int rows, float *out) {
   __shared__ float sum[32][33];
   grid_launch_dependents();
-  if (!late) grid_dependency_wait();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, row = threadIdx.x / 32;
   const int col = blockIdx.x * 32 + lane;
   float v = 0.f;
@@ -107,7 +107,6 @@ __global__ void __launch_bounds__(1024)
     for (int r = 0; r < 32; ++r) v += sum[r][lane];
     out[col] = v;
   }
-  if (late) grid_dependency_wait();  // (SplitArgs::late)
 }
 
 // 16-bit rows to rows whose stride and address tensor copies take; one or two

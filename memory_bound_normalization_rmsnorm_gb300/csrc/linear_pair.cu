@@ -159,8 +159,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   walk.first = blockIdx.x / 2;
   walk.step = gridDim.x / 2;
 
-  // before tensor memory is taken: never held while waiting
-  if (!p.late) grid_dependency_wait();
+  grid_dependency_wait();  // before tensor memory is taken: never held while waiting
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -406,7 +405,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
-  if (p.late) grid_dependency_wait();  // this kernel's end is the end of both
   cluster_sync();
 }
 

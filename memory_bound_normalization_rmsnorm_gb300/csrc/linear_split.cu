@@ -64,16 +64,35 @@ __device__ __forceinline__ void store4(void *base, int64_t at, int count, bool v
   }
 }
 
-// AMN, BMN: storage of the token operand (A) and of the feature operand (B).
-template <bool AMN, bool BMN, int DT>
+// sums[c] = part[0][c] + part[1][c] + ..., a column per thread, in order.
+__device__ __forceinline__ void add_rows(const SplitArgs &a, int first) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int c = first + static_cast<int>(threadIdx.x);
+  if (c >= a.cols) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int r = 0; r < a.rows; ++r) v += __ldcg(a.part + int64_t(r) * a.cols + c);
+  a.sums[c] = v;
+}
+
+template <int DT>
 __global__ void __launch_bounds__(kSplitThreads)
-    linear_split_kernel(const __grid_constant__ CUtensorMap tm_a,
-                        const __grid_constant__ CUtensorMap tm_b, const SplitArgs p) {
+    linear_split_kernel(const __grid_constant__ SplitMaps maps, const __grid_constant__ SplitArgs args) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t *ring = smem_raw + pad;
+  const int splits = args.splits;
+  const int cluster = blockIdx.x / splits;
+  const int which = cluster >= args.q[0].clusters;
+  const SplitProblem &p = args.q[which];
+  if (which && cluster >= args.q[0].clusters + p.clusters) {  // whole clusters
+    add_rows(args, (blockIdx.x - (args.q[0].clusters + p.clusters) * splits) * kSplitThreads);
+    return;
+  }
+  const CUtensorMap &tm_a = maps.a[which], &tm_b = maps.b[which];
+  const bool a_mn = p.a_mn, b_mn = p.b_mn;
   const uint32_t stage_bytes = split_stage_bytes(p.bn);
-  const int splits = p.splits;
   const int share = split_share(p.bn, splits);
   const bool push = split_push(p.bn, splits);
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + p.stages * stage_bytes);
@@ -87,7 +106,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int warp = warp_index();
   const int lane = threadIdx.x % 32;
   const int rank = splits > 1 ? int(cluster_ctarank()) : 0;
-  const int tile = blockIdx.x / splits;
+  const int tile = cluster - (which ? args.q[0].clusters : 0);
   const int j0 = (tile % p.tiles_j) * p.bn;  // first token
   const int i0 = (tile / p.tiles_j) * 128;   // first feature
   const int kb0 = int(int64_t(p.nk) * rank / splits), kb1 = int(int64_t(p.nk) * (rank + 1) / splits);
@@ -100,13 +119,13 @@ __global__ void __launch_bounds__(kSplitThreads)
     mbar_arrive_expect_tx(&full[s], stage_bytes);
     uint8_t *b = ring + s * stage_bytes, *a = b + 16384;
     const int k0 = (kb0 + n) * kLinBK;
-    if (BMN) {
+    if (b_mn) {
       tma_load_2d(b, &tm_b, i0, k0, &full[s]);
       tma_load_2d(b + 8192, &tm_b, i0 + 64, k0, &full[s]);
     } else {
       tma_load_2d(b, &tm_b, k0, i0, &full[s]);
     }
-    if (AMN) {
+    if (a_mn) {
       for (int c = 0; c < p.bn; c += 64) tma_load_2d(a + c * 128, &tm_a, j0 + c, k0, &full[s]);
     } else {
       tma_load_2d(a, &tm_a, k0, j0, &full[s]);
@@ -127,15 +146,14 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   __syncwarp();
   if (splits > 1) cluster_arrive_release();  // this CTA runs: peers may write to it
-  // before tensor memory is taken: never held while waiting
-  if (!p.late) grid_dependency_wait();
+  grid_dependency_wait();  // before tensor memory is taken: never held while waiting
   if (warp == 0) {
     if (elect_one())
       for (int n = 0; n < stages && n < nkb; ++n) fetch(n, n);
     __syncwarp();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, p.tmem);
+    tmem_alloc(tmem_slot, args.tmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -161,29 +179,29 @@ __global__ void __launch_bounds__(kSplitThreads)
       int issued = min(stages, nkb);
       for (; issued < nkb; ++issued) {
         const int s = issued % stages;
-        if (!mbar_wait(&empty[s], (issued / stages - 1) & 1, p.err, abort)) break;
+        if (!mbar_wait(&empty[s], (issued / stages - 1) & 1, args.err, abort)) break;
         fetch(issued, s);
       }
       // No copy may still be landing when the CTA exits.
       volatile int never = 0;
       for (int s = 0; s < stages && s < issued; ++s) {
         const int loads = (issued - s + stages - 1) / stages;
-        mbar_wait(&full[s], (loads - 1) & 1, p.err, &never);
+        mbar_wait(&full[s], (loads - 1) & 1, args.err, &never);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (elect_one()) {
       // rows of the accumulator: features; columns: tokens
-      const uint32_t idesc = lin_idesc(128, p.bn, DT == kBF16, BMN, AMN);
-      constexpr uint32_t astep = lin_kstep(AMN), bstep = lin_kstep(BMN);
+      const uint32_t idesc = lin_idesc(128, p.bn, DT == kBF16, b_mn, a_mn);
+      const uint32_t astep = lin_kstep(a_mn), bstep = lin_kstep(b_mn);
       int s = 0;
       uint32_t ph = 0;
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait(&full[s], ph, p.err, abort)) break;
+        if (!mbar_wait(&full[s], ph, args.err, abort)) break;
         tc_fence_after();
         const uint32_t base = smem_addr(ring + s * stage_bytes);
-        const uint64_t bd = lin_desc(base, BMN), ad = lin_desc(base + 16384, AMN);
+        const uint64_t bd = lin_desc(base, b_mn), ad = lin_desc(base + 16384, a_mn);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_bf16_ss(tmem, bd + k * bstep, ad + k * astep, idesc, (kb | k) != 0);
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncwarp();
   if (splits > 1) cluster_wait_acquire();  // every CTA of the cluster runs
   if (warp >= 2) {
-    mbar_wait(acc, 0, p.err, abort);
+    mbar_wait(acc, 0, args.err, abort);
     __syncwarp();
     tc_fence_after();
     const int t0 = (warp & 3) * 32;
@@ -240,7 +258,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncthreads();
   if (warp == 1) {  // every read of it is done; freed before the peers are waited for
     tc_fence_after();
-    tmem_dealloc(tmem, p.tmem);
+    tmem_dealloc(tmem, args.tmem);
   }
   if (splits > 1) cluster_wait_acquire();
 
@@ -277,24 +295,17 @@ __global__ void __launch_bounds__(kSplitThreads)
       load_r(j + kSplitThreads / 32);
     }
   }
-  if (p.late) grid_dependency_wait();  // this kernel's end is the end of both
   if (splits > 1 && !push) {  // peers may still read this CTA's partials
     __syncwarp();
     cluster_sync();
   }
 }
 
-template <bool AMN, bool BMN>
-const void *pick(bool bf16) {
-  return bf16 ? reinterpret_cast<const void *>(&linear_split_kernel<AMN, BMN, kBF16>)
-              : reinterpret_cast<const void *>(&linear_split_kernel<AMN, BMN, kFP16>);
-}
-
 }  // namespace
 
-const void *linear_split_kernel_ptr(bool a_mn, bool b_mn, bool bf16) {
-  if (a_mn) return b_mn ? pick<true, true>(bf16) : nullptr;
-  return b_mn ? pick<false, true>(bf16) : pick<false, false>(bf16);
+const void *linear_split_kernel_ptr(bool bf16) {
+  return bf16 ? reinterpret_cast<const void *>(&linear_split_kernel<kBF16>)
+              : reinterpret_cast<const void *>(&linear_split_kernel<kFP16>);
 }
 
 }  // namespace gbn

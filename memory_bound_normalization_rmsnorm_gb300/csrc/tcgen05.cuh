@@ -29,11 +29,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int c0,
       : "memory");
 }
 
-// Fetches a tensor map (a kernel parameter) ahead of its first copy.
-__device__ __forceinline__ void prefetch_tensor_map(const void *tmap) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
-}
-
 // The same load with an L2 eviction-priority policy (createpolicy).
 __device__ __forceinline__ void tma_load_2d_hint(void *dst, const void *tmap, int c0, int c1,
                                                  uint64_t *bar, uint64_t policy) {
@@ -106,23 +101,6 @@ __device__ __forceinline__ void tc_fence_before() {
 }
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// One lane of a converged warp.  Branching on this instead of on the lane's
-// number tells the compiler that the branch is taken by one thread.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
-// This thread's warp, as a value that is the same across the warp for the
-// compiler too.
-__device__ __forceinline__ int warp_index() {
-  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
 }
 
 // ------------------------------------------------------------- the MMA

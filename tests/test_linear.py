@@ -396,9 +396,8 @@ def test_many_threads_and_sizes():
 @pytest.mark.parametrize("shape", [(2304, 4096, 512), (512, 256, 4096), (40, 2048, 512),
                                    (300, 640, 4099)])
 def test_backward_between_writers_and_readers(shape):
-    """The backward's kernels overlap one another; what runs before and behind
-    them on the stream does not: every gradient is read by the next kernel, and
-    the operands are written right before."""
+    """Every gradient is read by the kernel behind, and the operands are written by
+    the one before, over and over in the same buffers."""
     M, K, N = shape
     c = _make("bf16", M, K, N)
     dx, dw = torch.empty_like(c["x"]), torch.empty_like(c["w"])
