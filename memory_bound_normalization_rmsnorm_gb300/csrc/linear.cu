@@ -182,11 +182,10 @@ double split_time(int64_t m, int64_t n, int nk, int bn, int splits, int stages, 
 }
 
 // The split form with clusters of s CTAs (s <= nk): its tile width and estimate.
-norm_status_t split_form(const Device &d, int64_t m, int64_t n, int nk, bool a_mn, bool bf16, int s,
-                         int want_bn, ProductPlan *best) {
+norm_status_t split_form(const Device &d, const void *fn, int64_t m, int64_t n, int nk, bool a_mn,
+                         int s, int want_bn, ProductPlan *best) {
   const int unit = a_mn ? 64 : 16;
   const int whole = m <= 128 ? round_up(m, unit) : 128;
-  const void *fn = linear_split_kernel_ptr(bf16);
   *best = ProductPlan{};
   for (int bn : {whole, 64}) {
     if (want_bn >= unit && want_bn <= 256 && want_bn % unit == 0) bn = want_bn;
@@ -212,7 +211,7 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
   norm_status_t st;
   *best = ProductPlan{};
   const void *pair = linear_pair_kernel_ptr(a_mn, b_mn, bf16);
-  const void *split = linear_split_kernel_ptr(bf16);
+  const void *split = linear_split_kernel_ptr(!a_mn && !b_mn, bf16);
   if ((st = function_ready(d.dev, pair, d.optin)) != NORM_OK) return st;
   if ((st = function_ready(d.dev, split, d.optin)) != NORM_OK) return st;
   // GBNORM_LINEAR="pair=0,bn=64,splits=4" forces fields (for sweeps)
@@ -236,7 +235,7 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
       if (want_pair == 0 && want_splits >= 1 && want_splits <= 8) s = want_splits;
       if (s > nk) s = nk;
       ProductPlan p;
-      st = split_form(d, m, n, nk, a_mn, bf16, s, want_pair == 0 ? want_bn : 0, &p);
+      st = split_form(d, split, m, n, nk, a_mn, s, want_pair == 0 ? want_bn : 0, &p);
       if (st != NORM_OK) return st;
       if (p.time < best->time) *best = p;
     }
@@ -313,9 +312,10 @@ struct SplitLaunch {
     return NORM_OK;
   }
   norm_status_t go(const Device &d, bool bf16, cudaStream_t s) {
-    const void *fn = linear_split_kernel_ptr(bf16);
+    const bool fwd = count == 1 && !args.part && !args.q[0].a_mn && !args.q[0].b_mn;
+    const void *fn = linear_split_kernel_ptr(fwd, bf16);
     if (d.optin < int(smem)) return NORM_ERR_UNSUPPORTED;
-    const norm_status_t st = function_ready(d.dev, fn, d.optin);
+    norm_status_t st = function_ready(d.dev, fn, d.optin);
     if (st != NORM_OK) return st;
     int64_t clusters = int64_t(args.q[0].clusters) + args.q[1].clusters;
     if (args.part)
@@ -407,12 +407,13 @@ norm_status_t plan_joint(const Device &d, int64_t M, int64_t N, int64_t K, bool 
   if (forced ? !one[0].pair : split_size(M, K) && split_size(N, K)) {
     const int nk = static_cast<int>((N + kLinBK - 1) / kLinBK);
     const int mk = static_cast<int>((M + kLinBK - 1) / kLinBK);
+    const void *fn = linear_split_kernel_ptr(false, bf16);
     double best = forced ? 1e30 : one[0].time + one[1].time;
     for (int s : {1, 2, 3, 4, 6, 8}) {
       if (s > nk || s > mk) break;
       ProductPlan p[2];
-      if ((st = split_form(d, M, K, nk, false, bf16, s, 0, &p[0])) != NORM_OK) return st;
-      if ((st = split_form(d, N, K, mk, true, bf16, s, 0, &p[1])) != NORM_OK) return st;
+      if ((st = split_form(d, fn, M, K, nk, false, s, 0, &p[0])) != NORM_OK) return st;
+      if ((st = split_form(d, fn, N, K, mk, true, s, 0, &p[1])) != NORM_OK) return st;
       const double t = p[0].time + p[1].time - 4.0;  // one start for two
       if (t < best) {
         best = t;

@@ -196,7 +196,8 @@ __host__ __device__ constexpr uint32_t split_smem(int bn, int splits, int stages
   return 1024u + uint32_t(stages) * split_stage_bytes(bn) + 256u +
          (split_push(bn, splits) ? uint32_t(splits * split_share(bn, splits)) * 512u : 0u);
 }
-const void *linear_split_kernel_ptr(bool bf16);
+// fwd: for a single product of K-major operands, without sums behind it.
+const void *linear_split_kernel_ptr(bool fwd, bool bf16);
 
 // linear_grad.cu
 constexpr int kGradThreads = 256;

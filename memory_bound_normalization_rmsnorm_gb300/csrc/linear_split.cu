@@ -76,7 +76,9 @@ __device__ __forceinline__ void add_rows(const SplitArgs &a, int first) {
   a.sums[c] = v;
 }
 
-template <int DT>
+// FWD: one product of two K-major operands (what a decoding step runs; with the
+// choices at run time 48 x 4096 x 16384 takes 28.6 us, compiled in 27.4).
+template <int DT, bool FWD>
 __global__ void __launch_bounds__(kSplitThreads)
     linear_split_kernel(const __grid_constant__ SplitMaps maps, const __grid_constant__ SplitArgs args) {
   extern __shared__ uint8_t smem_raw[];
@@ -84,14 +86,14 @@ __global__ void __launch_bounds__(kSplitThreads)
   uint8_t *ring = smem_raw + pad;
   const int splits = args.splits;
   const int cluster = blockIdx.x / splits;
-  const int which = cluster >= args.q[0].clusters;
+  const int which = FWD ? 0 : cluster >= args.q[0].clusters;
   const SplitProblem &p = args.q[which];
-  if (which && cluster >= args.q[0].clusters + p.clusters) {  // whole clusters
+  if (!FWD && which && cluster >= args.q[0].clusters + p.clusters) {  // whole clusters
     add_rows(args, (blockIdx.x - (args.q[0].clusters + p.clusters) * splits) * kSplitThreads);
     return;
   }
   const CUtensorMap &tm_a = maps.a[which], &tm_b = maps.b[which];
-  const bool a_mn = p.a_mn, b_mn = p.b_mn;
+  const bool a_mn = !FWD && p.a_mn, b_mn = !FWD && p.b_mn;
   const uint32_t stage_bytes = split_stage_bytes(p.bn);
   const int share = split_share(p.bn, splits);
   const bool push = split_push(p.bn, splits);
@@ -303,9 +305,12 @@ __global__ void __launch_bounds__(kSplitThreads)
 
 }  // namespace
 
-const void *linear_split_kernel_ptr(bool bf16) {
-  return bf16 ? reinterpret_cast<const void *>(&linear_split_kernel<kBF16>)
-              : reinterpret_cast<const void *>(&linear_split_kernel<kFP16>);
+const void *linear_split_kernel_ptr(bool fwd, bool bf16) {
+  if (fwd)
+    return bf16 ? reinterpret_cast<const void *>(&linear_split_kernel<kBF16, true>)
+                : reinterpret_cast<const void *>(&linear_split_kernel<kFP16, true>);
+  return bf16 ? reinterpret_cast<const void *>(&linear_split_kernel<kBF16, false>)
+              : reinterpret_cast<const void *>(&linear_split_kernel<kFP16, false>);
 }
 
 }  // namespace gbn

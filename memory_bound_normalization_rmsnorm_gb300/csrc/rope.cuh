@@ -8,7 +8,7 @@
 //
 // Layout.  A unit is two chunks of V elements: the 2V elements of V pairs, or
 // 2V elements behind rd.  The rows are short (D <= 256), so L = 4 to 32 lanes
-// of a warp share one, a unit (or kUnits, for the narrow V of odd sizes) per
+// of a warp share one, a unit (or several, for the narrow V of odd sizes) per
 // lane: both elements of every pair lie in one thread, a row's statistics take
 // log2 L shuffles, and the 32 / L groups of a warp read heads side by side.  V
 // is the widest chunk (up to 16 bytes) that the pair count, the unturned rest,
