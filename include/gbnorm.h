@@ -18,9 +18,10 @@
  *              c = sum(g*xhat)/N, a = sum(g)/N (LayerNorm; 0 for RMSNorm),
  *              dx = rstd*(g - a - xhat*c),
  *              dgamma = column sums of dy*xhat, dbeta = column sums of dy.
- * Beside it: dropout, dropout in front of the residual add, and group
- * normalisation of channels-last tensors (with their own definitions, types
- * and requirements below; the paragraphs here on ownership, execution and
+ * Beside it: dropout, dropout in front of the residual add, group
+ * normalisation of channels-last tensors, the normalisation and rotation of
+ * query and key heads, and the linear layer with bias, activation and residual
+ * (with their own definitions, types and requirements below; the paragraphs here on ownership, execution and
  * reproducibility hold for them too).
  *
  * Data layout.  x, y, dy, dx: bf16 [M, N], row-major, rows contiguous (row

@@ -1,6 +1,8 @@
 """GB300 (sm_103a) RMSNorm / LayerNorm forward and backward, the
 normalisation fused into a tensor-core GEMM, group normalisation with an
-activation, and counter-based dropout, alone and in front of the residual add.
+activation, counter-based dropout, alone and in front of the residual add, the
+linear layer with bias, activation and residual, and the normalisation and
+rotation of query and key heads.
 
 The computation runs in hand-written CUDA kernels behind the C ABI of
 include/gbnorm.h (libgbnorm.so); this package is its thin Python binding plus

@@ -1,8 +1,8 @@
 """ctypes binding of libgbnorm.so (the C ABI of include/gbnorm.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels of the library.  The dropout and group-normalisation functions, whose
-small calls are shorter than ctypes marshalling, marshal in the extension
+kernels of the library.  The dropout, group-normalisation, rotation and linear
+functions, whose small calls are shorter than ctypes marshalling, marshal in the extension
 module gbnorm_torch.so instead (csrc/torch_binding.cpp).  PyTorch supplies device memory (outputs and the
 backward workspace are allocated with torch when the caller passes none) and
 the stream (torch's current stream unless one is given).  There is no

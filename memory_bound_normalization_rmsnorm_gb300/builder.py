@@ -4,12 +4,13 @@ Its translation units (bf16- and E4M3-output forward, forward with staged
 parameters, backward, long-row kernels plain, with the fused residual add and
 with E4M3 output, the streamed rows, the two-pass path for the longest rows,
 host ABI, host-tensor pipeline, the normalisation fused into a tcgen05 GEMM,
-dropout, dropout + residual add + norm, and group normalisation) are
+dropout, dropout + residual add + norm, group normalisation, head rotation, and
+the linear layer) are
 compiled in parallel with nvcc and linked into one shared object with the
 CUDA runtime linked statically, so the library needs no CUDA library path at
 load time.  Beside it a small extension module, gbnorm_torch.so, is compiled
 against PyTorch's headers and linked to the library: the tensor side of the
-dropout and group-normalisation entry points.  It belongs to one PyTorch and one
+dropout, group-normalisation, rotation and linear-layer entry points.  It belongs to one PyTorch and one
 Python, which gbnorm_torch.stamp names: for others it is built again, and not
 loaded before that.  A PyTorch without CUDA has no tensors for it, so there the
 library alone is built.  `python -m memory_bound_normalization_rmsnorm_gb300.builder -v`
