@@ -14,10 +14,10 @@ namespace gbn {
 namespace {
 
 // One pass: read a row, normalise it in registers, turn its pairs, write it.
-template <int DT, int V, int MODE, int MIX>
-__global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
+template <int DT, int V, int NU, int MODE, int MIX>
+__global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V, NU, MIX == kMixed))
     rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP, S = kRopeFwdStages;
+  constexpr int NP = RopeUnit<V>::NP, S = rope_fwd_stages(NU);
   extern __shared__ uint4 smem[];
   RopeShared &sh = *reinterpret_cast<RopeShared *>(smem);
   uint4 *ring_mem = smem + sizeof(RopeShared) / 16;
@@ -25,13 +25,13 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
   grid_dependency_wait();
   const int side = static_cast<int>(blockIdx.x) >= a.ctas[0] ? 1 : 0;
   const RopeSide &s = a.side[side];
-  const RopeLane<DT, V, MIX> l(a);
+  const RopeLane<DT, V, NU, MIX> l(a);
   const int groups = 32 >> a.lanes_log2;
   const int first = threadIdx.x / 32 * groups + l.group, per = kRopeThreads / 32 * groups;
   RopeTiles<V> tile;
   tile.start(a, side, static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0));
-  RopeRing<DT, V, MIX, 1, S> ring;
-  ring.start(a, side, ring_mem, tile.t, first, per);
+  RopeRing<DT, V, NU, MIX, 1, S> ring;
+  ring.start(a, side, l, ring_mem, tile.t, first, per);
   for (int n = 0; n < S - 1; ++n) ring.fetch(a, side, l, first, per);
   RopeUnit<V> g[NU];
   RopeVec<DT, V> b[NU][2];
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
       ring.template wait<S - 2>();
       ring.read(o, 0);
       l.get(f, o);
-      ring.step();
+      if (MIX != kMixed) ring.step();  // else trade needs the round's slots
       ring.fetch(a, side, l, first, per);
       if constexpr (MODE != kNoNorm) {
         const float2 rstd = splat2(rope_stats<MODE>(a, l, f));
@@ -67,12 +67,16 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
           }
       }
       const bool on = first < left;
-      RopeAngles<V> ang;
+      RopeAngles<V, NU> ang;
       ang.get(a, l, sh.cs + (on ? out.tok * 2 * a.pairs : 0));
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         if (l.pair[i] >= 0) ang.turn(i, f[i]);
         f[i].template set<MIX>(o[i], l.mix[i]);
+      }
+      if (MIX == kMixed) {
+        ring.trade(o);
+        ring.step();
       }
       if (on) l.store(o, const_cast<char *>(out.p[0]));
       out.next();
@@ -80,39 +84,39 @@ __global__ void __launch_bounds__(kRopeThreads, rope_fwd_ctas(MODE, V))
   }
 }
 
-template <int DT, int V, int MIX>
+template <int DT, int V, int NU, int MIX>
 const void *pick_mode(int mode) {
   switch (mode) {
-    case kRMS: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kRMS, MIX>);
-    case kLayer: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kLayer, MIX>);
-    default: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, kNoNorm, MIX>);
+    case kRMS: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, NU, kRMS, MIX>);
+    case kLayer: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, NU, kLayer, MIX>);
+    default: return reinterpret_cast<const void *>(&rope_fwd_kernel<DT, V, NU, kNoNorm, MIX>);
   }
 }
 
-template <int DT, int V>
+template <int DT, int V, int NU>
 const void *pick_mix(int mode, bool inter) {
-  return inter ? pick_mode<DT, V, kMixed>(mode) : pick_mode<DT, V, kApart>(mode);
+  return inter ? pick_mode<DT, V, NU, kMixed>(mode) : pick_mode<DT, V, NU, kApart>(mode);
 }
 
 template <int DT>
-const void *pick_width(int V, int mode, bool inter) {
+const void *pick_width(int V, int NU, int mode, bool inter) {
   switch (V) {
     case 8:
-      if constexpr (DT != kFP32) return pick_mix<DT, 8>(mode, inter);
+      if constexpr (DT != kFP32) return pick_mix<DT, 8, 1>(mode, inter);
       return nullptr;
-    case 4: return pick_mix<DT, 4>(mode, inter);
-    case 2: return pick_mode<DT, 2, kEither>(mode);
-    default: return pick_mode<DT, 1, kApart>(mode);
+    case 4: return NU == 3 ? pick_mix<DT, 4, 3>(mode, inter) : pick_mix<DT, 4, 1>(mode, inter);
+    case 2: return pick_mode<DT, 2, rope_units(2), kEither>(mode);
+    default: return pick_mode<DT, 1, rope_units(1), kApart>(mode);
   }
 }
 
 }  // namespace
 
-const void *rope_fwd_kernel_ptr(int dt, int V, int mode, bool inter) {
+const void *rope_fwd_kernel_ptr(int dt, int V, int NU, int mode, bool inter) {
   switch (dt) {
-    case kBF16: return pick_width<kBF16>(V, mode, inter);
-    case kFP16: return pick_width<kFP16>(V, mode, inter);
-    default: return pick_width<kFP32>(V, mode, inter);
+    case kBF16: return pick_width<kBF16>(V, NU, mode, inter);
+    case kFP16: return pick_width<kFP16>(V, NU, mode, inter);
+    default: return pick_width<kFP32>(V, NU, mode, inter);
   }
 }
 
@@ -207,12 +211,32 @@ norm_status_t rope_args(const void *pos, int pos_bits, int64_t pos_stride, const
   return NORM_OK;
 }
 
-// Lanes per row, once the chunk width is known.
-void rope_lanes(RopeArgs *a, int V) {
-  a->units = a->pairs / V + (a->D - a->rd + 2 * V - 1) / (2 * V);
-  const int l = pow2_log(a->units);
-  a->lanes_log2 = l < 5 ? l : 5;
+// Lanes per row, once the chunk width and the units per lane are known.
+void rope_lanes(RopeArgs *a, int V, int NU) {
+  const int units = a->pairs / V + (a->D - a->rd + 2 * V - 1) / (2 * V);
+  a->lanes_log2 = pow2_log((units + NU - 1) / NU);
   a->pairs_log2 = pow2_log(a->pairs);
+}
+
+// Units per lane of the forward kernels, and the lanes: three units of chunks of
+// four where those leave fewer lanes without a unit than one unit each (heads of
+// 48, 72, 80, 96, 112, 144, 160, ... elements).  32768 tokens of 16 + 16 heads,
+// RMSNorm, one unit and three, us: bf16 heads of 72 101 and 64, 80 86 and 64, 160
+// 155 and 114; fp32, whose copies of two lanes are too short, 48 66 and 68, from
+// four lanes on 72 105 and 107, 80 104 and 105, 160 224 and 228, but with
+// LayerNorm 128 and 109, 128 and 106, 243 and 230, and 1500 tokens of 80 9.0 and
+// 7.5.  (The backward kernels would hold too many sums.)
+int rope_fwd_units(RopeArgs *a, int *V, int dtype) {
+  const int one = rope_units(*V);
+  rope_lanes(a, *V, one);
+  if (*V < 4) return one;
+  const int slots = *V << a->lanes_log2;
+  RopeArgs b = *a;
+  rope_lanes(&b, 4, 3);
+  if ((12 << b.lanes_log2) >= slots || (dtype == NORM_FP32 && b.lanes_log2 < 2)) return one;
+  a->lanes_log2 = b.lanes_log2;
+  *V = 4;
+  return 3;
 }
 
 // CTAs of each side: `per_sm` per SM in all, shared in proportion to the sides'
@@ -229,8 +253,10 @@ void rope_ctas(int64_t T, int64_t Hq, int64_t Hk, int sms, int per_sm, int *cq, 
 }
 
 // Tokens per tile: all of a CTA's where shared memory holds their angles (5476
-// tokens of 16 heads: 30 us in one tile, 32 in two), else `rows` rows or so, few
-// enough for the CTAs to end together.
+// tokens of 16 + 16 heads of 80, one unit per lane: 30 us in one tile, 32 in two), else `rows` rows or so (six
+// rounds or more with three units per lane: 32768 tokens of 16 + 16 heads of 80,
+// LayerNorm, fp32 116 us with two rounds, 106 with six, bf16 104, 88 and with
+// twelve 85), few enough for the CTAs to end together.
 void rope_tiles(RopeArgs *a, int rows) {
   for (int i = 0; i < 2; ++i) {
     const int H = a->side[i].H;
@@ -248,18 +274,19 @@ void rope_tiles(RopeArgs *a, int rows) {
 
 norm_status_t rope_launch_fwd(RopeArgs *a, int V, int mode, int dtype, int dev, int sms, int optin,
                               cudaStream_t s) {
-  const void *fn = rope_fwd_kernel_ptr(dtype, V, mode, a->inter);
+  const int NU = rope_fwd_units(a, &V, dtype);
+  const void *fn = rope_fwd_kernel_ptr(dtype, V, NU, mode, a->inter);
   const norm_status_t st = function_ready(dev, fn, optin);
   if (st != NORM_OK) return st;
   // With few tokens per CTA a third CTA per SM costs more to start than it brings
   // (333 tokens: 4.7 us with three, 3.2 with two).
-  const int per_sm = a->T < int64_t(sms) * 16 ? 2 : rope_fwd_ctas(mode, V);
+  const int per_sm = a->T < int64_t(sms) * 16 ? 2 : rope_fwd_ctas(mode, V, NU, a->inter);
   rope_ctas(a->T, a->side[0].H, a->side[1].H, sms, per_sm, &a->ctas[0], &a->ctas[1]);
-  rope_tiles(a, 128);
+  rope_tiles(a, NU == 3 ? 1536 / elem_bytes(dtype) : 128);
   void *args[] = {a};
-  return launch_serial(fn, dim3(unsigned(a->ctas[0] + a->ctas[1])),
-                       dim3(kRopeThreads),
-                       sizeof(RopeShared) + rope_ring_bytes(dtype, V, false), 1, args, s);
+  return launch_serial(fn, dim3(unsigned(a->ctas[0] + a->ctas[1])), dim3(kRopeThreads),
+                       sizeof(RopeShared) + rope_ring_bytes(dtype, V, NU, rope_fwd_stages(NU)), 1,
+                       args, s);
 }
 
 }  // namespace
@@ -313,7 +340,6 @@ norm_status_t norm_rope_fwd(const norm_heads_t *q, const norm_heads_t *k, int64_
   int dev = 0, sms = 0, optin = 0;
   unsigned *err = nullptr;
   if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
-  rope_lanes(&a, w.V);
   return rope_launch_fwd(&a, w.V, norm ? mode : kNoNorm, dtype, dev, sms, optin,
                          reinterpret_cast<cudaStream_t>(stream));
 }
@@ -393,7 +419,6 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk, co
   int dev = 0, sms = 0, optin = 0;
   unsigned *err = nullptr;
   if ((st = device_context(&dev, &sms, &optin, &err, nullptr)) != NORM_OK) return st;
-  rope_lanes(&a, w.V);
   a.sign = -1.f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!norm) return rope_launch_fwd(&a, w.V, kNoNorm, dtype, dev, sms, optin, s);
@@ -402,12 +427,14 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk, co
   if (!workspace || workspace_bytes < need) return NORM_ERR_WORKSPACE;
   if (!aligned_to_16(workspace)) return NORM_ERR_ALIGN;
   a.part = static_cast<float *>(workspace);
+  rope_lanes(&a, w.V, rope_units(w.V));
   rope_ctas(T, Hq, Hk, sms, kRopeBwdCtas, &a.ctas[0], &a.ctas[1]);
   rope_tiles(&a, 256);
   const bool layer = mode == NORM_LAYER;
   const void *fn = rope_bwd_kernel_ptr(dtype, w.V, mode, a.inter);
   if ((st = function_ready(dev, fn, optin)) != NORM_OK) return st;
-  const uint32_t ring = rope_ring_bytes(dtype, w.V, true), fold_bytes = rope_fold_floats(a.D, layer) * 4;
+  const uint32_t ring = rope_ring_bytes(dtype, w.V, rope_units(w.V), 2 * kRopeBwdStages);
+  const uint32_t fold_bytes = rope_fold_floats(a.D, layer) * 4;
   void *args[] = {&a};
   st = launch_serial(fn, dim3(a.ctas[0] + a.ctas[1]), dim3(kRopeThreads),
                      sizeof(RopeShared) + (ring > fold_bytes ? ring : fold_bytes), 1, args, s);

@@ -7,12 +7,13 @@
 // the angle pos[axis(p)][token] * inv_freq[p], the others stay.
 //
 // Layout.  A unit is two chunks of V elements: the 2V elements of V pairs, or
-// 2V elements behind rd.  The rows are short (D <= 256), so L = 4 to 32 lanes
-// of a warp share one, a unit (or several, for the narrow V of odd sizes) per
-// lane: both elements of every pair lie in one thread, a row's statistics take
-// log2 L shuffles, and the 32 / L groups of a warp read heads side by side.  V
-// is the widest chunk (up to 16 bytes) that the pair count, the unturned rest,
-// every stride and every address are whole multiples of.
+// 2V elements behind rd.  The rows are short (D <= 256), so L = 1 to 32 lanes
+// of a warp share one, a unit (or several, for the narrow V of odd sizes and where
+// one each would leave lanes without) per lane: both elements of every pair lie in
+// one thread, a row's statistics take log2 L shuffles, and the 32 / L groups of a
+// warp read heads side by side.  V is the widest chunk (up to 16 bytes) that the
+// pair count, the unturned rest, every stride and every address are whole
+// multiples of.
 #pragma once
 #include <cstdint>
 
@@ -24,10 +25,15 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxD = 256;
 constexpr int kRopeMaxAxes = 4;
 // CTAs per SM, by registers (LayerNorm holds two parameter rows; with eight
-// elements per chunk it spills at 80 registers).
-__host__ __device__ constexpr int rope_fwd_ctas(int mode, int V) { return mode == 1 && V == 8 ? 2 : 3; }
+// elements per chunk it spills at 80 registers, and so does RMSNorm where pairs
+// are neighbours: 16384 tokens of 16 + 16 heads of 128, bf16, 53 us with three
+// CTAs, 47 with two).
+__host__ __device__ constexpr int rope_fwd_ctas(int mode, int V, int NU, bool mixed) {
+  return (V == 8 && (mode == 1 || (mode == 0 && mixed))) || NU == 3 ? 2 : 3;
+}
 constexpr int kRopeBwdCtas = 2;
-constexpr int kRopeFwdStages = 5, kRopeBwdStages = 4;  // of the ring
+__host__ __device__ constexpr int rope_fwd_stages(int NU) { return NU == 3 ? 3 : 5; }  // of the ring
+constexpr int kRopeBwdStages = 4;
 constexpr int kNoNorm = 2;  // mode beside kRMS and kLayer: rotation alone
 
 struct RopeSide {
@@ -66,7 +72,7 @@ struct RopeArgs {
   int ctas[2];          // CTAs of each side
   int tile[2];          // tokens per tile of each side
   RopeDiv by_H[2];      // by the heads of each side
-  int D, rd, pairs, units;
+  int D, rd, pairs;
   int lanes_log2;       // log2 L
   int pairs_log2;       // log2 of the pairs, rounded up
   int axes;
@@ -207,14 +213,23 @@ struct RopeUnit {
 };
 
 // ----------------------------------------------------------------- lanes
-// Where the units of this lane lie in a row.
-template <int DT, int V, int MIX>
+// Where the units of this lane lie in a row, and which chunks it moves between
+// memory and the chip.  A unit of neighbours is 2V elements in a row: with 16-byte
+// chunks a lane that moved its own would touch half of a 32-byte sector at a time,
+// twice the traffic to L2, so its row's lanes move the chunks side by side and
+// trade them in shared memory (16384 tokens of 16 + 16 heads of 128, forward: fp32
+// 120 us where lanes moved their own, 93 now; bf16 61, 47).  The copies land in the
+// lanes' order: permuted in shared memory they were split into three times the
+// requests to L2, and no faster.
+template <int DT, int V, int NU, int MIX>
 struct RopeLane {
-  static constexpr int NU = rope_units(V);
-  int o1[NU], o2[NU];     // bytes from the row to the two chunks
+  int o1[NU], o2[NU];     // bytes from the row to the two chunks of the unit
+  int m1[NU], m2[NU];     // and to those that are moved
   int pair[NU];           // first pair of the unit, or -1: not turned
   bool in1[NU], in2[NU];  // the chunk exists
+  bool on1[NU], on2[NU];  // as in1, in2, of those that are moved
   bool mix[NU];           // kEither
+  bool swap;              // kMixed: o1 is the unit's second chunk and o2 its first
   int group;              // this lane's row among the warp's
 
   __device__ __forceinline__ explicit RopeLane(const RopeArgs &a) {
@@ -222,6 +237,11 @@ struct RopeLane {
     const int L = 1 << a.lanes_log2;
     group = lane >> a.lanes_log2;
     const int punits = a.pairs / V;
+    // The lanes that read shared memory together find their first chunks in half
+    // of the banks: every other group of them begins with the second chunk.
+    constexpr int most = V * elem_bytes(DT) == 16 ? 2 : 3;
+    const int bit = a.lanes_log2 - 1 < most ? a.lanes_log2 - 1 : most;
+    swap = MIX == kMixed && bit >= 0 && (lane >> bit & 1);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int u = (lane & (L - 1)) + i * L;
@@ -235,11 +255,24 @@ struct RopeLane {
         e1 = a.rd + 2 * V * (u - punits);
         e2 = e1 + V;
       }
+      if (swap) {
+        const int e = e1;
+        e1 = e2;
+        e2 = e;
+      }
       in1[i] = e1 < a.D;
       in2[i] = e2 < a.D;
       mix[i] = a.inter && pair[i] >= 0;
       o1[i] = e1 * elem_bytes(DT);
       o2[i] = e2 * elem_bytes(DT);
+      if (MIX == kMixed) {
+        e1 = V * (u + i * L);
+        e2 = e1 + V * L;
+      }
+      on1[i] = e1 < a.D;
+      on2[i] = e2 < a.D;
+      m1[i] = e1 * elem_bytes(DT);
+      m2[i] = e2 * elem_bytes(DT);
     }
   }
 
@@ -253,11 +286,12 @@ struct RopeLane {
       if (row && in2[i]) v[i][1].load(p + o2[i]);
     }
   }
+  // The chunks that the lane moves, to the row at p.
   __device__ __forceinline__ void store(const RopeVec<DT, V> (&v)[NU][2], char *p) const {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      if (in1[i]) v[i][0].store(p + o1[i]);
-      if (in2[i]) v[i][1].store(p + o2[i]);
+      if (on1[i]) v[i][0].store(p + m1[i]);
+      if (on2[i]) v[i][1].store(p + m2[i]);
     }
   }
   __device__ __forceinline__ void get(RopeUnit<V> (&f)[NU], const RopeVec<DT, V> (&v)[NU][2]) const {
@@ -328,8 +362,8 @@ __device__ __forceinline__ void rope_sincos(uint32_t turn, float &c, float &s) {
 // a row needs its V pairs, every head the same ones: computed where they are
 // used they were half of the kernel's instructions), and read from shared
 // memory.  The positions of the next tile are fetched meanwhile.
-constexpr int kRopeMaxTile = 32;      // tokens
-constexpr int kRopeMaxAngles = 1024;  // tokens x pairs
+constexpr int kRopeMaxTile = 64;      // tokens
+constexpr int kRopeMaxAngles = 2048;  // tokens x pairs
 struct RopeShared {
   // [token][V / 2 rows of][unit] (cos, cos, sin, sin) of two pairs, so that the
   // lanes of a row read side by side
@@ -394,15 +428,14 @@ struct RopeTiles {
 };
 
 // cos and sin of this lane's pairs.
-template <int V>
+template <int V, int NU>
 struct RopeAngles {
-  static constexpr int NU = rope_units(V);
   static constexpr int NP = V > 1 ? V / 2 : 1;
   float2 c[NU][NP], s[NU][NP];
 
   // cs: the token's angles
   template <int DT, int MIX>
-  __device__ __forceinline__ void get(const RopeArgs &a, const RopeLane<DT, V, MIX> &l,
+  __device__ __forceinline__ void get(const RopeArgs &a, const RopeLane<DT, V, NU, MIX> &l,
                                       const float *cs) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
@@ -415,7 +448,7 @@ struct RopeAngles {
           s[i][e] = make_float2(v.y, 0.f);
         } else {
           const float4 v = *reinterpret_cast<const float4 *>(
-              cs + (e * (a.pairs / V) + l.pair[i] / V) * 4);
+              cs + ((l.swap ? e ^ (NP / 2) : e) * (a.pairs / V) + l.pair[i] / V) * 4);
           c[i][e] = make_float2(v.x, v.y);
           s[i][e] = make_float2(v.z, v.w);
         }
@@ -484,22 +517,35 @@ struct RopeRow {
 // memory, zeros where there is no row.  No registers hold what is in flight and
 // no barrier joins the threads.  A round is fetched into the slots of the one
 // before the round that is being read, whose values have been used up.
-template <int DT, int V, int MIX, int N, int S>
+// With pairs of neighbours (kMixed) a unit's chunks are read from the slots of the
+// lanes that moved them, and the results go out the same way, through the slots of
+// the round that was read: the warp waits for itself at both.
+template <int DT, int V, int NU, int MIX, int N, int S>
 struct RopeRing {
-  static constexpr int NU = rope_units(V);
   static constexpr int kBytes = RopeVec<DT, V>::kBytes;
   static constexpr uint32_t kStage = kRopeThreads * N * 2 * NU * kBytes;
   static constexpr uint32_t kTotal = S * kStage;
 
   uint32_t slot;       // shared-memory address of this thread's first slot
+  uint32_t unit[2];    // kMixed: of the slots of its first unit's chunks
   RopeRow<N> row;      // the row that is fetched next
   int64_t t;           // its tile
   int left;            // rows of the tile from the round's first on
   uint32_t stage, now; // byte offsets of the stages that are fetched into and read next
 
-  __device__ __forceinline__ void start(const RopeArgs &a, int side, const void *ring,
+  __device__ __forceinline__ void start(const RopeArgs &a, int side,
+                                        const RopeLane<DT, V, NU, MIX> &l, const void *ring,
                                         int64_t first_tile, int first, int per) {
     slot = smem_addr(ring) + threadIdx.x * kBytes;
+    if constexpr (MIX == kMixed) {
+      const int l2 = a.lanes_log2, L = 1 << l2, sub = threadIdx.x & (L - 1);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int chunk = 2 * sub + (c ^ int(l.swap));
+        unit[c] = slot + static_cast<uint32_t>((chunk >> l2) * kRopeThreads - sub +
+                                               (chunk & (L - 1))) * kBytes;
+      }
+    }
     t = first_tile;
     stage = now = 0;
     const RopeSide &s = a.side[side];
@@ -517,6 +563,10 @@ struct RopeRing {
   static __device__ __forceinline__ uint32_t at(int k, int i, int c) {
     return static_cast<uint32_t>(((k * NU + i) * 2 + c) * kRopeThreads * kBytes);
   }
+  // The chunk c of this lane's unit.
+  __device__ __forceinline__ uint32_t own(int k, int i, int c) const {
+    return MIX == kMixed ? unit[c] + at(k, i, 0) : slot + at(k, i, c);
+  }
   static __device__ __forceinline__ void copy(uint32_t dst, const char *src, bool on) {
     if constexpr (kBytes == 16) {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -532,17 +582,16 @@ struct RopeRing {
     }
   }
   // Fetches the next round.
-  __device__ __forceinline__ void fetch(const RopeArgs &a, int side, const RopeLane<DT, V, MIX> &l,
+  __device__ __forceinline__ void fetch(const RopeArgs &a, int side, const RopeLane<DT, V, NU, MIX> &l,
                                         int first, int per) {
     if (left > 0) {
       const bool on = first < left;
-      const uint32_t d = slot + stage;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          copy(d + at(k, i, 0), row.p[k] + l.o1[i], on && l.in1[i]);
-          copy(d + at(k, i, 1), row.p[k] + l.o2[i], on && l.in2[i]);
+          copy(slot + stage + at(k, i, 0), row.p[k] + l.m1[i], on && l.on1[i]);
+          copy(slot + stage + at(k, i, 1), row.p[k] + l.m2[i], on && l.on2[i]);
         }
       }
       left -= per;
@@ -559,31 +608,60 @@ struct RopeRing {
   template <int LEFT>
   __device__ __forceinline__ void wait() const {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+    if constexpr (MIX == kMixed) __syncwarp();
   }
   // On to the next round.
-  __device__ __forceinline__ void step() { now = now + kStage == kTotal ? 0u : now + kStage; }
+  __device__ __forceinline__ void step() {
+    now = now + kStage == kTotal ? 0u : now + kStage;
+  }
   __device__ __forceinline__ void read(RopeVec<DT, V> (&v)[NU][2], int k) const {
 #pragma unroll
     for (int i = 0; i < NU; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t p = slot + now + at(k, i, c);
-        uint32_t *w = v[i][c].w;
-        if constexpr (kBytes == 16) {
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(p)
-                       : "memory");
-        } else if constexpr (kBytes == 8) {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p) : "memory");
-        } else if constexpr (kBytes == 4) {
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p) : "memory");
-        } else {
-          uint16_t h;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(p) : "memory");
-          w[0] = h;
-        }
-      }
+      for (int c = 0; c < 2; ++c) get(v[i][c], own(k, i, c) + now);
+  }
+  // From the units' own chunks to those that the lane moves, through the slots of
+  // the round that was read.
+  __device__ __forceinline__ void trade(RopeVec<DT, V> (&v)[NU][2]) const {
+    if constexpr (MIX == kMixed) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) put(v[i][c], own(0, i, c) + now);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) get(v[i][c], slot + now + at(0, i, c));
+    }
+  }
+
+ private:
+  static __device__ __forceinline__ void get(RopeVec<DT, V> &v, uint32_t p) {
+    uint32_t *w = v.w;
+    if constexpr (kBytes == 16) {
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(p)
+                   : "memory");
+    } else if constexpr (kBytes == 8) {
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p) : "memory");
+    } else if constexpr (kBytes == 4) {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(p) : "memory");
+    } else {
+      uint16_t h;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(p) : "memory");
+      w[0] = h;
+    }
+  }
+  static __device__ __forceinline__ void put(const RopeVec<DT, V> &v, uint32_t p) {
+    const uint32_t *w = v.w;
+    if constexpr (kBytes == 16)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(w[0]), "r"(w[1]),
+                   "r"(w[2]), "r"(w[3])
+                   : "memory");
+    else
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p), "r"(w[0]), "r"(w[1]) : "memory");
   }
 };
 
@@ -596,10 +674,10 @@ __device__ __forceinline__ float rope_sum(float v, int lanes_log2) {
 }
 
 // x - mean (LayerNorm) in f, zero where there is no element; returns rstd.
-template <int MODE, int DT, int V, int MIX>
-__device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT, V, MIX> &l,
-                                            RopeUnit<V> (&f)[rope_units(V)]) {
-  constexpr int NU = rope_units(V), NP = RopeUnit<V>::NP;
+template <int MODE, int DT, int V, int NU, int MIX>
+__device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT, V, NU, MIX> &l,
+                                            RopeUnit<V> (&f)[NU]) {
+  constexpr int NP = RopeUnit<V>::NP;
   if constexpr (MODE == kLayer) {
     float2 m = make_float2(0.f, 0.f);
 #pragma unroll
@@ -631,11 +709,10 @@ __device__ __forceinline__ float rope_stats(const RopeArgs &a, const RopeLane<DT
 
 
 // Kernels, and the shared memory of their rings.
-const void *rope_fwd_kernel_ptr(int dt, int V, int mode, bool inter);
+const void *rope_fwd_kernel_ptr(int dt, int V, int NU, int mode, bool inter);
 const void *rope_bwd_kernel_ptr(int dt, int V, int mode, bool inter);
-__host__ __device__ inline uint32_t rope_ring_bytes(int dt, int V, bool bwd) {
-  return uint32_t(kRopeThreads * 2 * rope_units(V) * V * elem_bytes(dt)) *
-         (bwd ? 2 * kRopeBwdStages : kRopeFwdStages);
+inline uint32_t rope_ring_bytes(int dt, int V, int NU, int rounds) {
+  return uint32_t(kRopeThreads * 2 * NU * V * elem_bytes(dt)) * rounds;
 }
 const void *rope_fold_kernel_ptr();
 // Floats of shared memory that the backward's last fold takes.

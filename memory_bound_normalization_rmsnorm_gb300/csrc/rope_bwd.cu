@@ -30,13 +30,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
   const int warps = kRopeThreads / 32, warp = threadIdx.x / 32;
   const int side = static_cast<int>(blockIdx.x) >= a.ctas[0] ? 1 : 0;
   const RopeSide &s = a.side[side];
-  const RopeLane<DT, V, MIX> l(a);
+  const RopeLane<DT, V, NU, MIX> l(a);
   const int groups = 32 >> a.lanes_log2;
   const int first = warp * groups + l.group, per = warps * groups;
   RopeTiles<V> tile;
   tile.start(a, side, static_cast<int>(blockIdx.x) - (side ? a.ctas[0] : 0));
-  RopeRing<DT, V, MIX, 2, S> ring;
-  ring.start(a, side, ring_mem, tile.t, first, per);
+  RopeRing<DT, V, NU, MIX, 2, S> ring;
+  ring.start(a, side, l, ring_mem, tile.t, first, per);
   for (int n = 0; n < S - 1; ++n) ring.fetch(a, side, l, first, per);
   RopeVec<DT, V> g[NU][2];
   l.load(g, static_cast<const char *>(s.gamma), true);
@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
       l.get(f, v);
       ring.read(v, 1);
       l.get(d, v);
-      ring.step();
+      if (MIX != kMixed) ring.step();  // else trade needs the round's slots
       ring.fetch(a, side, l, first, per);
       {
-        RopeAngles<V> ang;
+        RopeAngles<V, NU> ang;
         ang.get(a, l, sh.cs + (on ? out.tok * 2 * a.pairs : 0));
 #pragma unroll
         for (int i = 0; i < NU; ++i)
@@ -105,6 +105,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
         }
         d[i].template set<MIX>(o[i], l.mix[i]);
       }
+      if (MIX == kMixed) {
+        ring.trade(o);
+        ring.step();
+      }
       if (on) l.store(o, const_cast<char *>(out.p[0]));
       out.next();
     }
@@ -131,10 +135,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
       for (int e = 0; e < V; ++e) {
         const float x = e & 1 ? u[i].u[e / 2].y : u[i].u[e / 2].x;
         const float y = e & 1 ? u[i].w[e / 2].y : u[i].w[e / 2].x;
-        if (V > 1 && rope_mixed(MIX, l.mix[i])) {  // neighbours, the two chunks in a row
+        if (V > 1 && rope_mixed(MIX, l.mix[i])) {  // neighbours
           if (2 * e < V ? l.in1[i] : l.in2[i]) {
-            out[e1 + 2 * e] = x;
-            out[e1 + 2 * e + 1] = y;
+            const int at = 2 * e < V ? e1 + 2 * e : e2 + 2 * e - V;
+            out[at] = x;
+            out[at + 1] = y;
           }
         } else {
           if (l.in1[i]) out[e1 + e] = x;

@@ -218,6 +218,30 @@ def test_both_directions(dtype, mode, shape):
     _check_bwd(c, dys, _bwd(c, *dys))
 
 
+# Heads of one to thirty-two lanes with one to three units each, turned whole and
+# in part, in both pair layouts.
+LANES = [
+    (9, 2, 1, 8, 8, 1), (9, 3, 2, 16, 16, 1), (9, 3, 1, 16, 8, 1), (9, 2, 2, 24, 16, 1),
+    (21, 3, 2, 32, 32, 2), (70, 3, 2, 48, 48, 3), (21, 3, 2, 48, 32, 1), (21, 2, 1, 80, 48, 1),
+    (11, 5, 3, 96, 32, 1), (21, 3, 2, 96, 96, 2), (23, 2, 2, 104, 96, 2), (13, 2, 1, 112, 112, 1),
+    (23, 2, 2, 144, 144, 3), (11, 3, 1, 160, 160, 3), (11, 3, 1, 192, 192, 1), (11, 2, 1, 192, 64, 1),
+    (11, 2, 1, 208, 176, 2), (5, 2, 1, 256, 256, 1), (12000, 2, 1, 80, 80, 2),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("mode", ["none", "rms", "layer"])
+@pytest.mark.parametrize("shape", LANES)
+def test_lanes_and_units(shape, mode, inter):
+    T, Hq, Hk, D, rd, axes = shape
+    for dtype in ("bf16", "fp32"):
+        c = _make(dtype, mode, T, Hq, Hk, D, rd, axes, inter, True)
+        _check_fwd(c, *_fwd(c))
+        dys = [torch.randn_like(c["q"]), torch.randn_like(c["k"])]
+        _check_bwd(c, dys, _bwd(c, *dys))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("pos", [2 ** 31 - 1, -1, -2 ** 31, 2 ** 20 + 12345])
 def test_far_positions(pos):
