@@ -225,7 +225,8 @@ void rope_lanes(RopeArgs *a, int V, int NU) {
 // 155 and 114; fp32, whose copies of two lanes are too short, 48 66 and 68, from
 // four lanes on 72 105 and 107, 80 104 and 105, 160 224 and 228, but with
 // LayerNorm 128 and 109, 128 and 106, 243 and 230, and 1500 tokens of 80 9.0 and
-// 7.5.  (The backward kernels would hold too many sums.)
+// 7.5.  (The backward kernels would spill their sums: bf16, 32768 tokens of 80 128
+// us with one unit, 156 with three.)
 int rope_fwd_units(RopeArgs *a, int *V, int dtype) {
   const int one = rope_units(*V);
   rope_lanes(a, *V, one);
