@@ -147,7 +147,7 @@ norm_status_t resident(const Device &d, const void *fn, int threads, int cluster
 // measured (form, size) pairs of 52 sizes (1 to 16384 rows, forward and both
 // gradients, operands not in L2); on these sizes the form of least estimate is
 // 3 % slower than the fastest measured one in the geometric mean, 28 % at worst.
-// No size was held back.
+// No size was held back; with best_form's limits it is 1.6 % and 10 % on 47 more.
 double pair_time(int64_t m, int64_t n, int nk, int bn, bool b_mn, int pairs) {
   const int64_t tiles = ((m + 255) / 256) * ((n + bn - 1) / bn);
   const double waves = double((tiles + pairs - 1) / pairs);
@@ -221,16 +221,26 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
     if (const char *q = std::strstr(o, "bn=")) want_bn = std::atoi(q + 3);
     if (const char *q = std::strstr(o, "splits=")) want_splits = std::atoi(q + 7);
   }
+  int pairs = 0;
+  if ((st = resident(d, pair, kPairThreads, 2, pair_smem(), &pairs)) != NORM_OK) return st;
+  const int64_t high = (m + 255) / 256;  // tiles of 256 rows
   if (want_pair != 0 && (want_pair == 1 || m > 192)) {
-    int pairs = 0;
-    if ((st = resident(d, pair, kPairThreads, 2, pair_smem(), &pairs)) != NORM_OK) return st;
-    for (int bn : {128, 192, 224, 256}) {
+    // Tiles of 64 for what does not fill the GPU otherwise: operands cross L2 twice
+    // as often as for 128 (256 x 4096 x 4096 14.1 us and 15.5, 2048 x 1024 x 4096
+    // 22.8 and 17.7), and a K block of an MN-major B loads as long.
+    const bool few = !b_mn && high * ((n + 63) / 64) <= pairs;
+    for (int bn : {64, 128, 192, 224, 256}) {
+      if (bn == 64 && !few && want_pair != 1) continue;
       if (want_pair == 1 && want_bn >= 64 && want_bn <= 256 && want_bn % 32 == 0) bn = want_bn;
       const double t = pair_time(m, n, nk, bn, b_mn, pairs);
       if (t < best->time) *best = ProductPlan{true, bn, 1, 0, t};
     }
   }
-  if (want_pair != 1 && (want_pair == 0 || split_size(m, n))) {
+  // With many rows the split form is for products that leave many SMs to it: with
+  // 40 tiles of 256 x 128 (777 x 1232 x 1000) it takes 8.6 us where pairs take 10.0,
+  // with 64 (8192 x 256 x 1024) 11.4 and 9.1.
+  const bool gaps = m <= 192 || high * ((n + 127) / 128) * 3 <= int64_t(pairs) * 2;
+  if (want_pair != 1 && (want_pair == 0 || (split_size(m, n) && gaps))) {
     for (int s : {1, 2, 3, 4, 6, 8}) {
       if (want_pair == 0 && want_splits >= 1 && want_splits <= 8) s = want_splits;
       if (s > nk) s = nk;

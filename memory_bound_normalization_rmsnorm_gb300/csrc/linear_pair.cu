@@ -101,27 +101,36 @@ __device__ __forceinline__ void finish32(const uint32_t (&acc)[32], const float 
 }
 
 // The warp's 32 rows x 64 columns between a swizzled buffer and rows that no
-// tensor copy addresses: lane l takes columns l and l + 32.
+// tensor copy addresses: lane l takes columns l and l + 32, eight rows at a time
+// (777 x 1234 x 999 with r and z, tiles of 64: 15.9 us with four at a time and
+// their loads behind each other's stores, 15.3 now).
 template <bool LOAD>
 __device__ __forceinline__ void copy_rows(uint8_t *buf, int t0, void *base, int64_t ld, int row0,
                                           int m, int col0, int n) {
   const int lane = threadIdx.x & 31;
   uint16_t *g = static_cast<uint16_t *>(base);
-#pragma unroll 4
-  for (int r = 0; r < 32; ++r) {
-    if (row0 + r >= m) break;
+  const auto at = [&](int r, int c) {
     const int t = t0 + r;
+    return reinterpret_cast<uint16_t *>(buf + t * 128 + (((c >> 3) ^ (t & 7)) << 4)) + (c & 7);
+  };
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32 && row0 + r0 < m; r0 += 8) {
+    uint16_t v[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = lane + 32 * h;
-      uint16_t *s = reinterpret_cast<uint16_t *>(buf + t * 128 + (((c >> 3) ^ (t & 7)) << 4)) + (c & 7);
-      if (col0 + c < n) {
-        uint16_t *p = g + static_cast<int64_t>(row0 + r) * ld + col0 + c;
-        if (LOAD)
-          *s = *p;
-        else
-          *p = *s;
-      }
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + i / 2, c = lane + 32 * (i & 1);
+      const bool in = row0 + r < m && col0 + c < n;
+      if (!LOAD)
+        v[i] = *at(r, c);
+      else if (in)
+        v[i] = g[static_cast<int64_t>(row0 + r) * ld + col0 + c];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + i / 2, c = lane + 32 * (i & 1);
+      const bool in = row0 + r < m && col0 + c < n;
+      if (LOAD && in) *at(r, c) = v[i];
+      if (!LOAD && in) g[static_cast<int64_t>(row0 + r) * ld + col0 + c] = v[i];
     }
   }
 }
