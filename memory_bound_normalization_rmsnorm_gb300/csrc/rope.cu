@@ -254,10 +254,16 @@ void rope_ctas(int64_t T, int64_t Hq, int64_t Hk, int sms, int per_sm, int *cq, 
 }
 
 // Tokens per tile: all of a CTA's where shared memory holds their angles (5476
-// tokens of 16 + 16 heads of 80, one unit per lane: 30 us in one tile, 32 in two), else `rows` rows or so (six
-// rounds or more with three units per lane: 32768 tokens of 16 + 16 heads of 80,
-// LayerNorm, fp32 116 us with two rounds, 106 with six, bf16 104, 88 and with
-// twelve 85), few enough for the CTAs to end together.
+// tokens of 16 + 16 heads of 80, one unit per lane: 30 us in one tile, 32 in two),
+// else `rows` rows or so, few enough for the CTAs to end together.  Few rows mean
+// many barriers, many rows CTAs that drift apart and a wider stretch of memory in
+// use.  Forward: 128 rows (32768 tokens of 32 + 8 heads of 128, bf16: 96 rows 113
+// us, 128 108, 192 118; 16384 of 16 + 16: 45, 44 with 192), eight rounds where a
+// round has 64 rows or more (heads of 64 with LayerNorm, 128 rows 31 us, 512 27),
+// six of three units per lane in fp32 (32768 tokens of 80, LayerNorm: two rounds
+// 116 us, six 106), twelve in 16 bits (two rounds 104, six 88, twelve 85).
+// Backward: 512 rows (16384 tokens of 32 + 8 heads of 128: 256 rows 82.4 us, 384
+// 81.1, 512 80.1, 768 81.7), sixteen rounds at least.
 void rope_tiles(RopeArgs *a, int rows) {
   for (int i = 0; i < 2; ++i) {
     const int H = a->side[i].H;
@@ -283,7 +289,8 @@ norm_status_t rope_launch_fwd(RopeArgs *a, int V, int mode, int dtype, int dev, 
   // (333 tokens: 4.7 us with three, 3.2 with two).
   const int per_sm = a->T < int64_t(sms) * 16 ? 2 : rope_fwd_ctas(mode, V, NU, a->inter);
   rope_ctas(a->T, a->side[0].H, a->side[1].H, sms, per_sm, &a->ctas[0], &a->ctas[1]);
-  rope_tiles(a, NU == 3 ? 1536 / elem_bytes(dtype) : 128);
+  const int narrow = a->lanes_log2 <= 2 ? 8 * kRopeThreads >> a->lanes_log2 : 128;
+  rope_tiles(a, NU == 3 ? 1536 / elem_bytes(dtype) : narrow);
   void *args[] = {a};
   return launch_serial(fn, dim3(unsigned(a->ctas[0] + a->ctas[1])), dim3(kRopeThreads),
                        sizeof(RopeShared) + rope_ring_bytes(dtype, V, NU, rope_fwd_stages(NU)), 1,
@@ -430,7 +437,8 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk, co
   a.part = static_cast<float *>(workspace);
   rope_lanes(&a, w.V, rope_units(w.V));
   rope_ctas(T, Hq, Hk, sms, kRopeBwdCtas, &a.ctas[0], &a.ctas[1]);
-  rope_tiles(&a, 256);
+  const int per = kRopeThreads >> a.lanes_log2;  // rows of a round
+  rope_tiles(&a, 16 * per > 512 ? 16 * per : 512);
   const bool layer = mode == NORM_LAYER;
   const void *fn = rope_bwd_kernel_ptr(dtype, w.V, mode, a.inter);
   if ((st = function_ready(dev, fn, optin)) != NORM_OK) return st;
