@@ -288,9 +288,10 @@ struct SplitLaunch {
   uint32_t smem = 0;
   int count = 0;
 
-  explicit SplitLaunch(int splits) {
+  SplitLaunch(const Device &d, int splits) {
     args.splits = splits;
     args.tmem = 32;
+    args.err = d.err;
   }
   norm_status_t add(const Matrix &a, bool a_mn, const Matrix &b, bool b_mn, int64_t m, int64_t n,
                     int nk, const ProductPlan &plan, const LinEpilogue &e, bool bf16) {
@@ -382,7 +383,7 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     void *args[] = {&ta, &tb, &ty, &tz, &tr, &p};
     return launch_serial(fn, dim3(unsigned(grid)), dim3(kPairThreads), pair_smem(), 2, args, s);
   }
-  SplitLaunch l(plan.splits);
+  SplitLaunch l(d, plan.splits);
   if ((st = l.add(a, a_mn, b, b_mn, m, n, nk, plan, e, bf16)) != NORM_OK) return st;
   return l.go(d, bf16, s);
 }
@@ -664,7 +665,7 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
     JointPlan plan;
     if ((st = plan_joint(d, M, N, K, bf16, &plan)) != NORM_OK) return st;
     if (plan.joint) {
-      SplitLaunch l(plan.dx.splits);
+      SplitLaunch l(d, plan.dx.splits);
       const int nk = static_cast<int>((N + kLinBK - 1) / kLinBK);
       const int mk = static_cast<int>((M + kLinBK - 1) / kLinBK);
       if ((st = l.add(mdz, false, mw, true, M, K, nk, plan.dx, ex, bf16)) != NORM_OK) return st;
