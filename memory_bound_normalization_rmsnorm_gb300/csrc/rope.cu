@@ -151,6 +151,12 @@ struct Widest {
   }
 };
 
+// The strides that kernels step by.  A single token's or head's says nothing: lanes
+// beyond the last row form addresses with it, for copies of no bytes that have to
+// be aligned all the same.
+int64_t token_step(const norm_heads_t *h, int64_t T) { return T > 1 ? h->token_stride : 0; }
+int64_t head_step(const norm_heads_t *h, int64_t H) { return H > 1 ? h->head_stride : 0; }
+
 bool strides_ok(const norm_heads_t *h) {
   const int64_t most = int64_t(1) << 40;
   return h->token_stride >= 0 && h->token_stride <= most && h->head_stride >= 0 &&
@@ -337,11 +343,11 @@ norm_status_t norm_rope_fwd(const norm_heads_t *q, const norm_heads_t *k, int64_
       w.address(p);
     }
     s.x = x[i]->data;
-    s.xt = x[i]->token_stride;
-    s.xh = x[i]->head_stride;
+    s.xt = token_step(x[i], T);
+    s.xh = head_step(x[i], s.H);
     s.out = y[i]->data;
-    s.ot = y[i]->token_stride;
-    s.oh = y[i]->head_stride;
+    s.ot = token_step(y[i], T);
+    s.oh = head_step(y[i], s.H);
     s.gamma = gamma[i];
     s.beta = beta[i];
   }
@@ -408,16 +414,16 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk, co
     for (const float *p : {dgamma[i], dbeta[i]})
       if (reinterpret_cast<uintptr_t>(p) % 4) return NORM_ERR_ALIGN;
     s.out = out[i]->data;
-    s.ot = out[i]->token_stride;
-    s.oh = out[i]->head_stride;
+    s.ot = token_step(out[i], T);
+    s.oh = head_step(out[i], s.H);
     s.dy = dy[i]->data;
-    s.dt = dy[i]->token_stride;
-    s.dh = dy[i]->head_stride;
+    s.dt = token_step(dy[i], T);
+    s.dh = head_step(dy[i], s.H);
     s.gamma = gamma[i];
     if (norm) {
       s.x = x[i]->data;
-      s.xt = x[i]->token_stride;
-      s.xh = x[i]->head_stride;
+      s.xt = token_step(x[i], T);
+      s.xh = head_step(x[i], s.H);
     } else {  // the gradient turns back: the forward kernel with the other sign
       s.x = s.dy;
       s.xt = s.dt;
