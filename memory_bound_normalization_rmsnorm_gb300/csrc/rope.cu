@@ -170,7 +170,8 @@ bool rows_apart(const norm_heads_t *h, int64_t T, int64_t H, int64_t D) {
   if (H > 1 && hs < D) return false;
   if (T > 1 && ts < D) return false;
   if (H == 1 || T == 1) return true;
-  return ts >= (H - 1) * hs + D || hs >= (T - 1) * ts + D;
+  // (the products pass 64 bits: the second as a quotient, ts >= D >= 2)
+  return ts >= (H - 1) * hs + D || (hs >= D && (hs - D) / ts >= T - 1);
 }
 
 int pow2_log(int n) {

@@ -40,6 +40,25 @@ def _call(T, H, D, odd, dtype, inter, backward, seed=0):
     return out, dgamma
 
 
+def test_rows_that_overlap_far_apart_are_refused():
+    """Token and head strides of 2^40: token 1 of head 0 is token 0 of head 1,
+    though (T - 1) * stride is 2^64."""
+    def call(T, H, ts, hs):
+        far, near = gb._binding.Heads(256, ts, hs), gb._binding.Heads(256, 16 * H, 16)
+        return gb.lib().norm_rope_fwd(ctypes.byref(near), None, T, H, 0, 16, 16, 256, 64, 0, 256,
+                                      None, 1, 0, None, None, None, None, 1e-6, 0, 0,
+                                      ctypes.byref(far), None, None)
+
+    wide = 1 << 40
+    assert call((1 << 24) + 1, 3, wide, wide) == 2
+    assert call(1 << 31, 3, wide, wide) == 2
+    assert call(4, 3, 20, 75) == 2             # tokens 20 apart reach to 76
+    if not torch.cuda.is_available():          # (on a GPU these would run)
+        assert call(4, 3, 20, 76) == 7
+        assert call(1 << 31, 2, 16, 16 << 31) == 7
+        assert call(1 << 31, 65536, wide, 16) == 7
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("backward", [False, True])
 @pytest.mark.parametrize("inter", [0, 1])
