@@ -512,8 +512,28 @@ struct GradPlan {
   size_t total() const { return dz + part + x + w; }
 };
 
-GradPlan grad_plan(const Matrix &dy, const Matrix &x, const Matrix &w, const Matrix &z, int act,
-                   bool dx, bool dw, bool dbias, int sms) {
+// What a backward call reads: x, w and z as null matrices where they are not needed.
+struct GradIn {
+  Matrix dy, x, w, z;
+};
+
+norm_status_t grad_in(GradIn *in, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                      const void *w, int64_t ldw, const void *z, int64_t ldz, int64_t M, int64_t K,
+                      int64_t N, int act, bool dx, bool dw) {
+  if (act == NORM_ACT_NONE) z = nullptr;
+  *in = {{dy, lddy, M, N},
+         {dw ? x : nullptr, dw ? ldx : K, M, K},
+         {dx ? w : nullptr, dx ? ldw : K, N, K},
+         {z, z ? ldz : N, M, N}};
+  for (const Matrix &t : {in->dy, in->x, in->w, in->z}) {
+    const norm_status_t st = check_matrix(t);
+    if (st != NORM_OK) return st;
+  }
+  return NORM_OK;
+}
+
+GradPlan grad_plan(const GradIn &in, int act, bool dx, bool dw, bool dbias, int sms) {
+  const Matrix &dy = in.dy, &x = in.x, &w = in.w, &z = in.z;
   GradPlan g = {};
   const bool products = dx || dw;
   g.need_dz = products && (act != NORM_ACT_NONE || !tma_ready(dy));
@@ -591,11 +611,13 @@ norm_status_t norm_linear_bwd_workspace_bytes(const void *dy, int64_t lddy, cons
   if (st != NORM_OK) return st;
   if (!known_act(act)) return NORM_ERR_ARG;
   if (act != NORM_ACT_NONE && !z) return NORM_ERR_NULL;
+  GradIn in;
+  if ((st = grad_in(&in, dy, lddy, x, ldx, w, ldw, z, ldz, M, K, N, act, want_dx, want_dw)) !=
+      NORM_OK)
+    return st;
   Device d;
   if ((st = device_of(&d)) != NORM_OK) return st;
-  *bytes = grad_plan({dy, lddy, M, N}, {x, ldx, M, K}, {w, ldw, N, K}, {z, ldz, M, N}, act,
-                     want_dx, want_dw, want_dbias, d.sms)
-               .total();
+  *bytes = grad_plan(in, act, want_dx, want_dw, want_dbias, d.sms).total();
   return NORM_OK;
 }
 
@@ -611,30 +633,28 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
   if (!known_act(act) || (dtype != NORM_BF16 && dtype != NORM_FP16)) return NORM_ERR_ARG;
   if (!dx && !dw && !dbias) return NORM_ERR_ARG;
   if (act != NORM_ACT_NONE && !z) return NORM_ERR_NULL;
-  if (act == NORM_ACT_NONE) z = nullptr;
-  Matrix mdy{dy, lddy, M, N};
-  Matrix mx{dw ? x : nullptr, dw ? ldx : K, M, K}, mw{dx ? w : nullptr, dx ? ldw : K, N, K};
-  const Matrix mz{z, z ? ldz : N, M, N};
-  for (const Matrix &t : {mdy, mx, mw, mz, Matrix{dx, dx ? lddx : K, M, K},
-                          Matrix{dw, dw ? lddw : K, N, K}})
+  GradIn in;
+  if ((st = grad_in(&in, dy, lddy, x, ldx, w, ldw, z, ldz, M, K, N, act, dx, dw)) != NORM_OK)
+    return st;
+  for (const Matrix &t : {Matrix{dx, dx ? lddx : K, M, K}, Matrix{dw, dw ? lddw : K, N, K}})
     if ((st = check_matrix(t)) != NORM_OK) return st;
   if (reinterpret_cast<uintptr_t>(dbias) % 4) return NORM_ERR_ALIGN;
   Device d;
   if ((st = device_of(&d)) != NORM_OK) return st;
-  const GradPlan g = grad_plan(mdy, mx, mw, mz, act, dx, dw, dbias, d.sms);
+  const GradPlan g = grad_plan(in, act, dx, dw, dbias, d.sms);
   if (g.total() && (!workspace || workspace_bytes < g.total())) return NORM_ERR_WORKSPACE;
   if (g.total() && !aligned_to_16(workspace)) return NORM_ERR_ALIGN;
-  for (const void *p : {dy, dw ? x : nullptr, dx ? w : nullptr})
+  for (const void *p : {dy, in.x.p, in.w.p})
     if (p && (st = check_memory(p, d.dev)) != NORM_OK) return st;
   const bool bf16 = dtype == NORM_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
-  Matrix mdz = mdy;
+  Matrix mdz = in.dy, mx = in.x, mw = in.w;
   const float *part = nullptr;
   if (g.need_dz || dbias) {
     GradArgs a = {};
     a.dy = dy;
-    a.z = z;
+    a.z = in.z.p;
     a.lddy = lddy;
     a.ldz = ldz;
     a.M = static_cast<int>(M);
