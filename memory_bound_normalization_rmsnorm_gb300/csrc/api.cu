@@ -138,7 +138,10 @@ norm_status_t prepare_function(int dev, const void *fn, int smem_optin) {
     cudaGetLastError();
     return NORM_ERR_CUDA;
   }
-  g_attr_done.insert({dev, fn});
+  try {
+    g_attr_done.insert({dev, fn});
+  } catch (...) {  // out of host memory: they are set again next time
+  }
   return NORM_OK;
 }
 

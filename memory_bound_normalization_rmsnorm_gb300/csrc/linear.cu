@@ -6,8 +6,6 @@
 
 #include <cstdlib>
 #include <cstring>
-#include <map>
-#include <mutex>
 #include <tuple>
 #include <utility>
 
@@ -15,6 +13,7 @@
 #include "common.cuh"
 #include "host_util.h"
 #include "linear.cuh"
+#include "plan_cache.h"
 
 namespace gbn {
 
@@ -113,15 +112,16 @@ uint32_t tmem_columns(int bn) {
   return c;
 }
 
-std::mutex g_plan_mu;
-std::map<std::tuple<const void *, int, uint32_t>, int> g_resident;  // per SM (cluster 1) or clusters
+constexpr size_t kMaxPlans = 4096;
+
+// clusters resident at once, by kernel, cluster size and device, shared memory
+PlanCache<std::tuple<const void *, int, uint32_t>, int> g_resident(kMaxPlans);
 
 // Clusters of `cluster` CTAs of kernel fn that are resident at once.
 norm_status_t resident(const Device &d, const void *fn, int threads, int cluster, uint32_t smem,
                        int *out) {
-  std::lock_guard<std::mutex> lk(g_plan_mu);
-  auto it = g_resident.find({fn, cluster * 64 + d.dev, smem});
-  if (it == g_resident.end()) {
+  const auto key = std::make_tuple(fn, cluster * 64 + d.dev, smem);
+  if (!g_resident.find(key, out)) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -137,9 +137,9 @@ norm_status_t resident(const Device &d, const void *fn, int threads, int cluster
       cudaGetLastError();
       return NORM_ERR_CUDA;
     }
-    it = g_resident.emplace(std::make_tuple(fn, cluster * 64 + d.dev, smem), n).first;
+    g_resident.keep(key, n);
+    *out = n;
   }
-  *out = it->second;
   return *out < 1 ? NORM_ERR_UNSUPPORTED : NORM_OK;
 }
 
@@ -254,29 +254,17 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
 }
 
 // Plans of sizes seen before, per device, storage of the operands and type.
-std::map<std::tuple<int, int64_t, int64_t, int64_t>, ProductPlan> g_plans;
-constexpr size_t kMaxPlans = 4096;  // then the cache starts anew
+PlanCache<std::tuple<int, int64_t, int64_t, int64_t>, ProductPlan> g_plans(kMaxPlans);
 
 norm_status_t plan_product(const Device &d, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn,
                            bool bf16, ProductPlan *out) {
   const bool forced = std::getenv("GBNORM_LINEAR") != nullptr;
   const auto key = std::make_tuple(d.dev * 8 + a_mn * 4 + b_mn * 2 + bf16, m, n, k);
-  if (!forced) {
-    std::lock_guard<std::mutex> lk(g_plan_mu);
-    auto it = g_plans.find(key);
-    if (it != g_plans.end()) {
-      *out = it->second;
-      return NORM_OK;
-    }
-  }
+  if (!forced && g_plans.find(key, out)) return NORM_OK;
   ProductPlan p;
   const norm_status_t st = best_form(d, m, n, k, a_mn, b_mn, bf16, &p);
   if (st != NORM_OK) return st;
-  if (!forced) {
-    std::lock_guard<std::mutex> lk(g_plan_mu);
-    if (g_plans.size() >= kMaxPlans) g_plans.clear();
-    g_plans[key] = p;
-  }
+  if (!forced) g_plans.keep(key, p);
   *out = p;
   return NORM_OK;
 }
@@ -397,19 +385,12 @@ struct JointPlan {
   bool joint = false;
   ProductPlan dx, dw;
 };
-std::map<std::tuple<int, int64_t, int64_t, int64_t>, JointPlan> g_joint;
+PlanCache<std::tuple<int, int64_t, int64_t, int64_t>, JointPlan> g_joint(kMaxPlans);
 
 norm_status_t plan_joint(const Device &d, int64_t M, int64_t N, int64_t K, bool bf16, JointPlan *out) {
   const bool forced = std::getenv("GBNORM_LINEAR") != nullptr;
   const auto key = std::make_tuple(d.dev * 2 + bf16, M, N, K);
-  if (!forced) {
-    std::lock_guard<std::mutex> lk(g_plan_mu);
-    auto it = g_joint.find(key);
-    if (it != g_joint.end()) {
-      *out = it->second;
-      return NORM_OK;
-    }
-  }
+  if (!forced && g_joint.find(key, out)) return NORM_OK;
   JointPlan j;
   norm_status_t st;
   ProductPlan one[2];
@@ -432,11 +413,7 @@ norm_status_t plan_joint(const Device &d, int64_t M, int64_t N, int64_t K, bool 
       }
     }
   }
-  if (!forced) {
-    std::lock_guard<std::mutex> lk(g_plan_mu);
-    if (g_joint.size() >= kMaxPlans) g_joint.clear();
-    g_joint[key] = j;
-  }
+  if (!forced) g_joint.keep(key, j);
   *out = j;
   return NORM_OK;
 }
