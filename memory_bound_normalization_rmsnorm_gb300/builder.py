@@ -38,7 +38,7 @@ SOURCES = ["fwd.cu", "fwd_fp8.cu", "fwd_gsm.cu", "bwd.cu", "long.cu", "long_resi
            "long_fp8.cu", "split.cu", "stream.cu", "api.cu", "host.cu", "gemm.cu", "dropout.cu",
            "drop_add.cu", "group_fwd.cu", "group_bwd.cu", "group_ring.cu",
            "group.cu", "rope.cu", "rope_bwd.cu", "linear.cu",
-           "linear_pair.cu", "linear_split.cu", "linear_grad.cu"]
+           "linear_pair.cu", "linear_split.cu", "linear_grad.cu", "tensor_map.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -47,7 +47,6 @@
 // CTA still waits (bounded) for its own copies and MMAs in flight, frees its
 // tensor memory and exits.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -63,6 +62,7 @@
 #include "common.cuh"
 #include "rowops.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace gbn {
 
@@ -618,32 +618,14 @@ __global__ void __launch_bounds__(256)
 }
 
 std::mutex g_mu;
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::set<std::pair<unsigned long long, const void *>> g_attr_done;  // (context, kernel)
-
-norm_status_t encoder(PFN_cuTensorMapEncodeTiled_v12000 *out) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_encode) {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                         cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn) {
-      cudaGetLastError();
-      return NORM_ERR_CUDA;
-    }
-    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  *out = g_encode;
-  return NORM_OK;
-}
 
 // Row-major bf16 [rows, cols] with boxes of box_rows x 64 columns, 128-byte
 // swizzle, zero fill outside the tensor.
 norm_status_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
                        uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
-  norm_status_t st = encoder(&enc);
+  MapEncoder enc = nullptr;
+  norm_status_t st = map_encoder(&enc);
   if (st != NORM_OK) return st;
   cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
   cuuint64_t strides[1] = {cuuint64_t(cols) * 2};
@@ -656,20 +638,6 @@ norm_status_t make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t c
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// x, W' and out are moved by tiled tensor copies, whose tensor maps take a
-// global address this GPU can reach: device memory of the current device
-// (or managed memory).  Host memory, another device's memory and addresses
-// unknown to CUDA are refused before a map is built.
-norm_status_t check_device_memory(const void *p, int dev) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return NORM_ERR_MEMORY;
-  }
-  if (a.type == cudaMemoryTypeManaged) return NORM_OK;
-  return (a.type == cudaMemoryTypeDevice && a.device == dev) ? NORM_OK : NORM_ERR_MEMORY;
-}
 
 // Kernel form: the CTA pair (cta_group::2) by default, GBNORM_GEMM_CTAS=1
 // the single-CTA kernel.  Measured on GB300 at M = 32768, K = Nout from 2048

@@ -1,7 +1,6 @@
 // linear.cu -- entry points norm_linear_fwd / norm_linear_bwd: which kernels run
 // a product, its tensor maps, workspaces and launches.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdlib>
@@ -14,6 +13,7 @@
 #include "host_util.h"
 #include "linear.cuh"
 #include "plan_cache.h"
+#include "tensor_map.h"
 
 namespace gbn {
 
@@ -31,38 +31,10 @@ bool tma_ready(const Matrix &t) {
   return aligned_to_16(t.p) && (t.rows == 1 || t.ld % 8 == 0);
 }
 
-using MapEncoder = PFN_cuTensorMapEncodeTiled_v12000;
-
-// The driver's encoder of tensor maps (null where there is none).
-MapEncoder map_encoder() {
-  static const MapEncoder found = [] {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      fn = nullptr;
-    }
-    return reinterpret_cast<MapEncoder>(fn);
-  }();
-  return found;
-}
-
-// Tensor copies reach device memory of the current device, or managed memory.
-norm_status_t check_memory(const void *p, int dev) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return NORM_ERR_MEMORY;
-  }
-  const bool here = a.type == cudaMemoryTypeDevice && a.device == dev;
-  return here || a.type == cudaMemoryTypeManaged ? NORM_OK : NORM_ERR_MEMORY;
-}
-
 norm_status_t map_of(CUtensorMap *m, const Matrix &t, bool bf16, uint32_t box_rows) {
-  const MapEncoder enc = map_encoder();
-  if (!enc) return NORM_ERR_CUDA;
+  MapEncoder enc = nullptr;
+  const norm_status_t st = map_encoder(&enc);
+  if (st != NORM_OK) return st;
   const int64_t ld = t.rows == 1 ? (t.cols + 7) / 8 * 8 : t.ld;
   cuuint64_t dims[2] = {cuuint64_t(t.cols), cuuint64_t(t.rows)};
   cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
@@ -362,7 +334,7 @@ norm_status_t product(const Device &d, const Matrix &a, bool a_mn, const Matrix 
     int *flags[3] = {&p.tma_y, &p.tma_z, &p.tma_r};
     for (int i = 0; i < 3; ++i) {
       if (!out[i].p || !tma_ready(out[i])) continue;
-      if ((st = check_memory(out[i].p, d.dev)) != NORM_OK) return st;
+      if ((st = check_device_memory(out[i].p, d.dev)) != NORM_OK) return st;
       if ((st = map_of(maps[i], out[i], bf16, 32)) != NORM_OK) return st;
       *flags[i] = 1;
     }
@@ -569,7 +541,7 @@ norm_status_t norm_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t
   Device d;
   if ((st = device_of(&d)) != NORM_OK) return st;
   for (const void *p : {x, w})
-    if ((st = check_memory(p, d.dev)) != NORM_OK) return st;
+    if ((st = check_device_memory(p, d.dev)) != NORM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
   if ((st = pack(&mx, &mw, &ws, s)) != NORM_OK) return st;
@@ -622,7 +594,7 @@ norm_status_t norm_linear_bwd(const void *dy, int64_t lddy, const void *x, int64
   if (g.total() && (!workspace || workspace_bytes < g.total())) return NORM_ERR_WORKSPACE;
   if (g.total() && !aligned_to_16(workspace)) return NORM_ERR_ALIGN;
   for (const void *p : {dy, in.x.p, in.w.p})
-    if (p && (st = check_memory(p, d.dev)) != NORM_OK) return st;
+    if (p && (st = check_device_memory(p, d.dev)) != NORM_OK) return st;
   const bool bf16 = dtype == NORM_BF16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
