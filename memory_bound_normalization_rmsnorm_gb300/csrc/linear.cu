@@ -176,9 +176,30 @@ norm_status_t split_form(const Device &d, const void *fn, int64_t m, int64_t n, 
 // The split form is for few rows, and as long as its tiles are two waves or so.
 bool split_size(int64_t m, int64_t n) { return m <= 192 || m * n <= int64_t(4096) * 4096; }
 
+// GBNORM_LINEAR="pair=0,bn=64,splits=4,joint=0" forces fields (for sweeps): the form,
+// tile width and cluster size, where a product can have them, and whether both
+// gradients' products go into one launch.
+struct LinForce {
+  bool any = false;
+  int pair = -1, joint = -1, bn = 0, splits = 0;
+};
+
+LinForce read_force() {
+  LinForce f;
+  if (const char *o = std::getenv("GBNORM_LINEAR")) {
+    f.any = true;
+    if (const char *q = std::strstr(o, "pair=")) f.pair = std::atoi(q + 5) != 0;
+    if (const char *q = std::strstr(o, "joint=")) f.joint = std::atoi(q + 6) != 0;
+    if (const char *q = std::strstr(o, "bn=")) f.bn = std::atoi(q + 3);
+    if (const char *q = std::strstr(o, "splits=")) f.splits = std::atoi(q + 7);
+    if (f.splits < 1 || f.splits > 8) f.splits = 0;
+  }
+  return f;
+}
+
 // The form of least estimate.
 norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn,
-                        bool bf16, ProductPlan *best) {
+                        bool bf16, const LinForce &f, ProductPlan *best) {
   const int nk = static_cast<int>((k + kLinBK - 1) / kLinBK);
   norm_status_t st;
   *best = ProductPlan{};
@@ -186,24 +207,17 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
   const void *split = linear_split_kernel_ptr(!a_mn && !b_mn, bf16);
   if ((st = function_ready(d.dev, pair, d.optin)) != NORM_OK) return st;
   if ((st = function_ready(d.dev, split, d.optin)) != NORM_OK) return st;
-  // GBNORM_LINEAR="pair=0,bn=64,splits=4" forces fields (for sweeps)
-  int want_pair = -1, want_bn = 0, want_splits = 0;
-  if (const char *o = std::getenv("GBNORM_LINEAR")) {
-    if (const char *q = std::strstr(o, "pair=")) want_pair = std::atoi(q + 5) != 0;
-    if (const char *q = std::strstr(o, "bn=")) want_bn = std::atoi(q + 3);
-    if (const char *q = std::strstr(o, "splits=")) want_splits = std::atoi(q + 7);
-  }
   int pairs = 0;
   if ((st = resident(d, pair, kPairThreads, 2, pair_smem(), &pairs)) != NORM_OK) return st;
   const int64_t high = (m + 255) / 256;  // tiles of 256 rows
-  if (want_pair != 0 && (want_pair == 1 || m > 192)) {
+  if (f.pair != 0 && (f.pair == 1 || m > 192)) {
     // Tiles of 64 for what does not fill the GPU otherwise: operands cross L2 twice
     // as often as for 128 (256 x 4096 x 4096 14.1 us and 15.5, 2048 x 1024 x 4096
     // 22.8 and 17.7), and a K block of an MN-major B loads as long.
     const bool few = !b_mn && high * ((n + 63) / 64) <= pairs;
     for (int bn : {64, 128, 192, 224, 256}) {
-      if (bn == 64 && !few && want_pair != 1) continue;
-      if (want_pair == 1 && want_bn >= 64 && want_bn <= 256 && want_bn % 32 == 0) bn = want_bn;
+      if (bn == 64 && !few && f.pair != 1) continue;
+      if (f.pair == 1 && f.bn >= 64 && f.bn <= 256 && f.bn % 32 == 0) bn = f.bn;
       const double t = pair_time(m, n, nk, bn, b_mn, pairs);
       if (t < best->time) *best = ProductPlan{true, bn, 1, 0, t};
     }
@@ -212,12 +226,12 @@ norm_status_t best_form(const Device &d, int64_t m, int64_t n, int64_t k, bool a
   // 40 tiles of 256 x 128 (777 x 1232 x 1000) it takes 8.6 us where pairs take 10.0,
   // with 64 (8192 x 256 x 1024) 11.4 and 9.1.
   const bool gaps = m <= 192 || high * ((n + 127) / 128) * 3 <= int64_t(pairs) * 2;
-  if (want_pair != 1 && (want_pair == 0 || (split_size(m, n) && gaps))) {
+  if (f.pair != 1 && (f.pair == 0 || (split_size(m, n) && gaps))) {
     for (int s : {1, 2, 3, 4, 6, 8}) {
-      if (want_pair == 0 && want_splits >= 1 && want_splits <= 8) s = want_splits;
+      if (f.pair == 0 && f.splits) s = f.splits;
       if (s > nk) s = nk;
       ProductPlan p;
-      st = split_form(d, split, m, n, nk, a_mn, s, want_pair == 0 ? want_bn : 0, &p);
+      st = split_form(d, split, m, n, nk, a_mn, s, f.pair == 0 ? f.bn : 0, &p);
       if (st != NORM_OK) return st;
       if (p.time < best->time) *best = p;
     }
@@ -230,13 +244,13 @@ PlanCache<std::tuple<int, int64_t, int64_t, int64_t>, ProductPlan> g_plans(kMaxP
 
 norm_status_t plan_product(const Device &d, int64_t m, int64_t n, int64_t k, bool a_mn, bool b_mn,
                            bool bf16, ProductPlan *out) {
-  const bool forced = std::getenv("GBNORM_LINEAR") != nullptr;
+  const LinForce force = read_force();
   const auto key = std::make_tuple(d.dev * 8 + a_mn * 4 + b_mn * 2 + bf16, m, n, k);
-  if (!forced && g_plans.find(key, out)) return NORM_OK;
+  if (!force.any && g_plans.find(key, out)) return NORM_OK;
   ProductPlan p;
-  const norm_status_t st = best_form(d, m, n, k, a_mn, b_mn, bf16, &p);
+  const norm_status_t st = best_form(d, m, n, k, a_mn, b_mn, bf16, force, &p);
   if (st != NORM_OK) return st;
-  if (!forced) g_plans.keep(key, p);
+  if (!force.any) g_plans.keep(key, p);
   *out = p;
   return NORM_OK;
 }
@@ -360,24 +374,27 @@ struct JointPlan {
 PlanCache<std::tuple<int, int64_t, int64_t, int64_t>, JointPlan> g_joint(kMaxPlans);
 
 norm_status_t plan_joint(const Device &d, int64_t M, int64_t N, int64_t K, bool bf16, JointPlan *out) {
-  const bool forced = std::getenv("GBNORM_LINEAR") != nullptr;
+  const LinForce force = read_force();
   const auto key = std::make_tuple(d.dev * 2 + bf16, M, N, K);
-  if (!forced && g_joint.find(key, out)) return NORM_OK;
+  if (!force.any && g_joint.find(key, out)) return NORM_OK;
   JointPlan j;
   norm_status_t st;
   ProductPlan one[2];
   if ((st = plan_product(d, M, K, N, false, true, bf16, &one[0])) != NORM_OK) return st;
   if ((st = plan_product(d, N, K, M, true, true, bf16, &one[1])) != NORM_OK) return st;
-  if (forced ? !one[0].pair : split_size(M, K) && split_size(N, K)) {
+  const bool open = force.joint >= 0 ? force.joint == 1
+                                     : force.any ? !one[0].pair : split_size(M, K) && split_size(N, K);
+  if (open) {
     const int nk = static_cast<int>((N + kLinBK - 1) / kLinBK);
     const int mk = static_cast<int>((M + kLinBK - 1) / kLinBK);
     const void *fn = linear_split_kernel_ptr(false, bf16);
-    double best = forced ? 1e30 : one[0].time + one[1].time;
+    double best = force.any ? 1e30 : one[0].time + one[1].time;
     for (int s : {1, 2, 3, 4, 6, 8}) {
+      if (force.splits) s = force.splits < nk && force.splits < mk ? force.splits : nk < mk ? nk : mk;
       if (s > nk || s > mk) break;
       ProductPlan p[2];
-      if ((st = split_form(d, fn, M, K, nk, false, s, 0, &p[0])) != NORM_OK) return st;
-      if ((st = split_form(d, fn, N, K, mk, true, s, 0, &p[1])) != NORM_OK) return st;
+      if ((st = split_form(d, fn, M, K, nk, false, s, force.bn, &p[0])) != NORM_OK) return st;
+      if ((st = split_form(d, fn, N, K, mk, true, s, force.bn, &p[1])) != NORM_OK) return st;
       const double t = p[0].time + p[1].time - 4.0;  // one start for two
       if (t < best) {
         best = t;
@@ -385,7 +402,7 @@ norm_status_t plan_joint(const Device &d, int64_t M, int64_t N, int64_t K, bool 
       }
     }
   }
-  if (!forced) g_joint.keep(key, j);
+  if (!force.any) g_joint.keep(key, j);
   *out = j;
   return NORM_OK;
 }
