@@ -387,9 +387,11 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
  *       `interleaved`; elements rd .. D - 1 are not turned
  * rounded once.  Rotary positions of one axis are axes = 1; images and video
  * have one axis for each of (time,) height and width, and every pair belongs to
- * one of them.  The angle is reduced exactly (positions are integers: the
- * product is taken in 64-bit fractions of a turn), so far positions are as
- * exact as near ones.
+ * one of them.  The angle is an integer product (positions are integers, and
+ * inv_freq is taken as a 64-bit fraction of a turn), reduced without rounding; it
+ * is off by at most |pos| (2^-64 + |inv_freq| 2^-72) + 2^-32 turns: below 2^-25
+ * radians, half a step of fp32 below 1, for |pos| <= 2^35 with |inv_freq| <= 256,
+ * all int32 positions among them, and in proportion to |pos| beyond.
  * Backward, from the gradients dyq, dyk and the forward's inputs (the
  * statistics are taken again):  dn = dy turned back, g = dn gamma,
  *   xhat = (v - mean) rstd,  dv = rstd (g - mean(g) - xhat mean(g xhat))
@@ -407,8 +409,10 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
  *              Hk = 0: no keys (k, yk, ... are not read, gamma_k and beta_k must
  *              be NULL)
  *   pos        device int32 or int64 (pos_bits 32 or 64): the position of token
- *              t on axis a at pos[a * pos_stride + t]; any integer
- *   inv_freq   device fp64 [rd / 2]: radians per position, finite and below 2^53
+ *              t on axis a at pos[a * pos_stride + t]; any integer (see above for
+ *              how exact far ones are)
+ *   inv_freq   device fp64 [rd / 2]: radians per position, finite, magnitudes below
+ *              2^53
  *   pair_axis  HOST uint8 [rd / 2], read before the call returns: the axis of
  *              each pair, below `axes`; NULL: all on axis 0 (axes = 1)
  *   gamma_q, gamma_k, beta_q, beta_k   [D] of `dtype`.  gamma_q NULL: no
@@ -418,7 +422,7 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
  *              device, 16-byte aligned; may be NULL without normalisation.  Two
  *              calls that overlap in time must not share it.
  * Requirements: 1 <= T <= 2^31, 1 <= Hq <= 65536, 0 <= Hk <= 65536, 2 <= D <=
- * 256, rd even, 2 <= rd <= D, strides below 2^40 (else NORM_ERR_SHAPE); axes 1
+ * 256, rd even, 2 <= rd <= D, strides up to 2^40 (else NORM_ERR_SHAPE); axes 1
  * to 4 (NORM_ERR_ARG); pointers aligned to their elements (NORM_ERR_ALIGN):
  * any stride and address works, 16-byte multiples are fastest.
  * One kernel; with normalisation the backward adds a fixed-order sum of the

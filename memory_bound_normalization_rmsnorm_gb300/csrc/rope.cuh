@@ -309,11 +309,13 @@ struct RopeLane {
 // ---------------------------------------------------------------- angles
 // An angle is a fraction of a turn: with f = inv_freq / (2 pi) as a 64-bit
 // binary fraction of a turn, pos * f modulo 2^64 is the angle modulo a whole
-// turn exactly, however far the position: an integer product in place of a
-// range reduction.  (A product in 32 bits is off by 0.06 radians at position
-// 2^20.)  f is formed from the bits of inv_freq in integers too, truncated to
-// 2^-64 of a turn (float64 products, at 1/64 of the fp32 rate, made 333 tokens
-// take 5.1 us instead of 4.7).
+// turn: an integer product in place of a range reduction, which adds no error of
+// its own.  (A product in 32 bits is off by 0.06 radians at position 2^20.)  f is
+// formed from the bits of inv_freq in integers too (float64 products, at 1/64 of
+// the fp32 rate, made 333 tokens take 5.1 us instead of 4.7).  It is truncated to
+// 2^-64 of a turn, and 2^66 / (2 pi) to 64 bits is off by 0.0151: together at most
+// 2^-64 + inv_freq 2^-72 turns per position, which for positions up to 2^35 and
+// frequencies up to 256 is 2^-25 radians.
 __device__ __forceinline__ uint64_t rope_turns(double inv_freq) {
   const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(inv_freq));
   const int e = static_cast<int>(bits >> 52) & 2047;

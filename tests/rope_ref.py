@@ -3,14 +3,18 @@ definitions, with the magnitudes that the CUDA path's tolerances multiply.
 
 Tolerances.  An output of type t is rounded once, at most u_t = finfo(t).eps / 2
 of its value.  In front of that stands float32 arithmetic on magnitudes bounded
-by the terms that enter (`*_mag` below): a row's sums take at most 16 values in
-a lane, then 5 levels of shuffles, each rounding 2^-24 of the sum of magnitudes,
-21 x 2^-24 for the mean and again for the squares (half of it in rstd, and 2
-ulp of the root); cos and sin are off by at most pi 2^-25 (the angle in half
-turns, below 1, rounded to fp32) plus 2 ulp; five products and sums per element
-follow.  Together below 64 x 2^-24 = 2^-18 for y.  dx chains two such sums more
-and the products of two such factors: 2^-16.  dgamma and dbeta add up to 64
-rows in a thread (the tests' shapes) and up to 45 partial sums: 2^-16.
+by the terms that enter (`*_mag` below): a row's sums take at most 24 values in
+a lane (three units of two chunks of four), two side by side, so 12 additions one
+behind the other and one more, then 5 levels of shuffles and the product with 1 / D,
+each rounding 2^-24 of the sum of magnitudes: 19 x 2^-24 for the mean, and one more
+for the squares (half of it in rstd, and 2 ulp of the root): 12 x 2^-24.  The angle
+is a 32-bit fraction of a turn, off by 2^-32 turns (and by 2^-25 radians at far
+positions, tests/test_rope_far.py), rounded to 24 bits as turns and as radians, below
+an eighth of a turn: 2 x 2^-24 radians; the polynomials add 2^-28 and two roundings:
+cos and sin are off by at most 5 x 2^-24.  Six products and sums per element follow.  Together below
+64 x 2^-24 = 2^-18 for y.  dx chains two such sums more and the products of two such
+factors: 2^-16.  dgamma and dbeta add up to 64 rows in a thread (the tests' shapes)
+and the rows of the CTAs, 32 side by side: 2^-16.
 """
 import torch
 
