@@ -397,7 +397,9 @@ norm_status_t norm_group_plan(int64_t B, int64_t S, int64_t C, int64_t groups,
  *   xhat = (v - mean) rstd,  dv = rstd (g - mean(g) - xhat mean(g xhat))
  *   (mean(g) for LAYER only),  dgamma = sum of dn xhat and dbeta = sum of dn
  *   over all tokens and heads.
- * Results are bitwise reproducible for a given shape, type and device.
+ * Results are bitwise reproducible for a given shape, type, device and alignment
+ * of addresses and strides (which choose how many lanes share a row, and so the
+ * order of its sums).
  *
  * Arguments:
  *   q, k, yq, yk, dyq, dyk, dq, dk   head tensors: element (t, h, d) at
@@ -474,7 +476,9 @@ norm_status_t norm_rope_bwd(const norm_heads_t *dyq, const norm_heads_t *dyk,
  *   dbias = column sums of dz (fp32, from the unrounded dz)
  *   dx = dz W,  dw = dz^T x   (fp32 accumulation, rounded once)
  * and the gradient of r is dy.  Results are bitwise reproducible for a given
- * shape, type and device.
+ * shape, type, device and choice of outputs (dx and dw together may be cut in
+ * other parts than one alone); dbias also depends on whether addresses and strides
+ * of dy and z are multiples of 16 bytes, which chooses the order of its sums.
  *
  * Arguments:
  *   x, w, bias, r, y, z, dy, dx, dw   of `dtype`, NORM_BF16 or NORM_FP16;
