@@ -4,8 +4,8 @@ Its translation units (bf16- and E4M3-output forward, forward with staged
 parameters, backward, long-row kernels plain, with the fused residual add and
 with E4M3 output, the streamed rows, the two-pass path for the longest rows,
 host ABI, host-tensor pipeline, the normalisation fused into a tcgen05 GEMM,
-dropout, dropout + residual add + norm, group normalisation, head rotation, and
-the linear layer) are
+dropout, dropout + residual add + norm, group normalisation, head rotation, the
+linear layer, and the driver's tensor-map encoder) are
 compiled in parallel with nvcc and linked into one shared object with the
 CUDA runtime linked statically, so the library needs no CUDA library path at
 load time.  Beside it a small extension module, gbnorm_torch.so, is compiled

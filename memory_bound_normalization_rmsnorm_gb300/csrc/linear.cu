@@ -119,7 +119,8 @@ norm_status_t resident(const Device &d, const void *fn, int threads, int cluster
 // measured (form, size) pairs of 52 sizes (1 to 16384 rows, forward and both
 // gradients, operands not in L2); on these sizes the form of least estimate is
 // 3 % slower than the fastest measured one in the geometric mean, 28 % at worst.
-// No size was held back; with best_form's limits it is 1.6 % and 10 % on 47 more.
+// No size was held back; with best_form's limits it is 1.6 % and 10 % on 47 more,
+// and 13 % for 512 x 4096 x 16384 (50.0 us, with tiles of 256 44.4).
 double pair_time(int64_t m, int64_t n, int nk, int bn, bool b_mn, int pairs) {
   const int64_t tiles = ((m + 255) / 256) * ((n + bn - 1) / bn);
   const double waves = double((tiles + pairs - 1) / pairs);

@@ -14,7 +14,10 @@ constexpr int kGradRows = 4;  // rows in flight per thread
 // Bound by HBM: one read of dy and z, one write of dz.  A warp takes rows of 256
 // columns (32 with V = 1), the CTA's 8 warps every 8th row of a chunk; a
 // thread's sums are those of its V columns, joined over the warps in order into
-// one row of partials per chunk.  Sums are of the unrounded dz.
+// one row of partials per chunk.  Sums are of the unrounded dz.  dz itself is
+// rounded to the operands' 16-bit type, since kind::f16 takes no wider one: the
+// errors of dx and dW are those of two roundings in place of one (1.41 times), where
+// dz as the sum of two 16-bit values would double their products.
 template <int DT, int V>
 __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradArgs a) {
   constexpr int W = kGradThreads / 32;
