@@ -3,6 +3,7 @@
 // tensor copies cannot address.
 #include <cuda_runtime.h>
 
+#include "fold.cuh"
 #include "linear.cuh"
 
 namespace gbn {
@@ -91,25 +92,12 @@ __global__ void __launch_bounds__(kGradThreads) linear_grad_kernel(const GradArg
   }
 }
 
-// Adds the chunks' rows in order: 32 columns per block, 32 rows side by side.
+// Adds the chunks' rows in order.
 __global__ void __launch_bounds__(1024)
     linear_fold_kernel(const float *part, int n, int rows, float *out) {
-  __shared__ float sum[32][33];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, row = threadIdx.x / 32;
-  const int col = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (col < n)
-    for (int r = row; r < rows; r += 32) v += __ldcg(part + int64_t(r) * n + col);
-  sum[row][lane] = v;
-  __syncthreads();
-  if (row == 0 && col < n) {
-    v = 0.f;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) v += sum[r][lane];
-    out[col] = v;
-  }
+  fold_columns(part, rows, n, out);
 }
 
 // 16-bit rows to rows whose stride and address tensor copies take; one or two

@@ -10,6 +10,7 @@
 // the CTA in a fixed order, and rope_fold_kernel adds the CTAs' rows in order.
 #include <cuda_runtime.h>
 
+#include "fold.cuh"
 #include "rope.cuh"
 
 namespace gbn {
@@ -160,32 +161,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
   }
 }
 
-// Adds the CTAs' rows: block y = 0 dgamma of q, 1 of k, 2 and 3 dbeta of them;
-// 32 columns per block, 32 rows side by side, joined in order.
+// Adds the CTAs' rows: block y = 0 dgamma of q, 1 of k, 2 and 3 dbeta of them.
 __global__ void __launch_bounds__(1024)
     rope_fold_kernel(const float *part, int n, int cq, int ck, float *dgq, float *dgk, float *dbq,
                      float *dbk) {
-  __shared__ float sum[32][33];
   grid_launch_dependents();
   grid_dependency_wait();
   const int which = blockIdx.y >> 1, side = blockIdx.y & 1;
   float *out = which ? (side ? dbk : dbq) : (side ? dgk : dgq);
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x / 32;
-  const int rows = side ? ck : cq;
   const float *src = part + (static_cast<int64_t>(which) * (cq + ck) + (side ? cq : 0)) * n;
-  float v = 0.f;
-  if (out && col < n) {
-#pragma unroll 4
-    for (int r = row; r < rows; r += 32) v += __ldcg(src + static_cast<int64_t>(r) * n + col);
-  }
-  sum[row][threadIdx.x & 31] = v;
-  __syncthreads();
-  if (row == 0 && out && col < n) {
-    v = 0.f;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) v += sum[r][threadIdx.x & 31];
-    out[col] = v;
-  }
+  fold_columns(src, side ? ck : cq, n, out);
 }
 
 template <int DT, int V, int MIX>
